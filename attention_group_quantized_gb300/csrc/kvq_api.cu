@@ -211,9 +211,10 @@ static bool table_ok(const kvq_block_table* t, const kvq_cache& pool) {
 static kvq_status decode_impl(const void* q, const kvq_cache* k, const kvq_cache* v, const kvq_block_table* table,
                               const int32_t* seq_lens, int32_t Hq, float softmax_scale, void* out, int32_t out_dtype,
                               void* workspace, size_t workspace_bytes, int32_t* dev_status, void* stream,
-                              const kvq_policy* policy = nullptr) {
+                              const kvq_policy* policy = nullptr, int32_t window = 0, int32_t sinks = 0) {
   if (q == nullptr || k == nullptr || v == nullptr || seq_lens == nullptr || out == nullptr)
     return KVQ_ERR_INVALID_ARG;
+  if (window < 0 || sinks < 0) return KVQ_ERR_INVALID_ARG;
   if (k->codes == nullptr || k->sz == nullptr || v->codes == nullptr || v->sz == nullptr) return KVQ_ERR_INVALID_ARG;
   if (k->D > 0 && k->D != 64 && k->D != 128) return KVQ_ERR_UNSUPPORTED;
   DecodeArgs a;
@@ -239,6 +240,8 @@ static kvq_status decode_impl(const void* q, const kvq_cache* k, const kvq_cache
   a.ws = workspace;
   a.ws_bytes = workspace_bytes;
   a.status = dev_status;
+  a.window = window;
+  a.sinks = sinks;
   if (!resolve_policy(policy, &a.pol)) return KVQ_ERR_INVALID_ARG;
   if (table != nullptr) {
     a.bt = table->pages;
@@ -674,6 +677,184 @@ kvq_status kvq_prefill_attention_ex(const void* q, const void* k, const void* v,
                                     const kvq_policy* policy, int32_t* dev_status, void* stream) {
   return prefill_impl(q, k, v, B, Hq, Hkv, S, D, seq_lens, causal, softmax_scale, tile_mask, tile, k_cache, v_cache,
                       out, out_dtype, dev_status, stream, policy);
+}
+
+}  // extern "C"
+
+// ---- chunks: several new tokens per sequence, packed ----
+
+// The checks that every chunk call makes: the description, its storage and
+// the sizes that the kernels index in 32 bits.
+static kvq_status chunk_desc(const kvq_chunk* c, const kvq_cache& storage, const kvq_block_table* table,
+                             ChunkDesc* out) {
+  if (c == nullptr || c->start == nullptr || c->seq_lens == nullptr ||
+      (reinterpret_cast<uintptr_t>(c->start) & 3u) || (reinterpret_cast<uintptr_t>(c->seq_lens) & 3u))
+    return KVQ_ERR_INVALID_ARG;
+  if (c->B <= 0 || c->rows < 0 || c->max_chunk < 0) return KVQ_ERR_INVALID_ARG;
+  if (table != nullptr && !table_ok(table, storage)) return KVQ_ERR_INVALID_ARG;
+  if (c->B != (table != nullptr ? table->B : storage.B)) return KVQ_ERR_INVALID_ARG;
+  if (c->B > 4096 || static_cast<int64_t>(c->rows) * storage.Hkv >= (int64_t(1) << 31)) return KVQ_ERR_UNSUPPORTED;
+  out->start = c->start;
+  out->seq_lens = c->seq_lens;
+  out->B = c->B;
+  out->rows = c->rows;
+  out->max_chunk = c->max_chunk == 0 ? c->rows : c->max_chunk;
+  out->bt = table != nullptr ? table->pages : nullptr;
+  out->bt_max_pages = table != nullptr ? table->max_pages : 0;
+  out->cap = table != nullptr ? table->max_pages * KVQ_TILE_TOKENS : storage.Tcap;
+  return KVQ_OK;
+}
+
+static bool buffers_ok(const kvq_cache& c) {
+  return c.codes != nullptr && c.sz != nullptr && aligned16(c.codes) && aligned16(c.sz);
+}
+
+static kvq_status append_chunk_impl(const void* k_new, const void* v_new, int64_t s_row, int64_t s_head,
+                                    const kvq_chunk* chunk, const kvq_cache* k, const kvq_cache* v,
+                                    const kvq_block_table* table, int32_t* dev_status, void* stream) {
+  if (k_new == nullptr || v_new == nullptr || k == nullptr || v == nullptr || !buffers_ok(*k) || !buffers_ok(*v))
+    return KVQ_ERR_INVALID_ARG;
+  if (k->D > 0 && k->D != 64 && k->D != 128) return KVQ_ERR_UNSUPPORTED;
+  AppendChunkArgs a;
+  if (!resolve_layout(*k, &a.layout) || !same_cache_shape(*k, *v)) return KVQ_ERR_INVALID_ARG;
+  if (!aligned16(k_new) || !aligned16(v_new) || s_row < 0 || s_head < 0 || s_row % 8 || s_head % 8)
+    return KVQ_ERR_INVALID_ARG;
+  const kvq_status s = chunk_desc(chunk, *k, table, &a.chunk);
+  if (s != KVQ_OK) return s;
+  if (chunk->rows == 0) return KVQ_OK;
+  a.k_new = static_cast<const uint16_t*>(k_new);
+  a.v_new = static_cast<const uint16_t*>(v_new);
+  a.s_row = s_row;
+  a.s_head = s_head;
+  a.k = k;
+  a.v = v;
+  a.status = dev_status;
+  return launch_append_chunk(a, static_cast<cudaStream_t>(stream)) == cudaSuccess ? KVQ_OK : KVQ_ERR_CUDA;
+}
+
+static kvq_status dequantize_impl(const kvq_cache* src, const kvq_chunk* chunk, const kvq_block_table* table,
+                                  void* out, int32_t out_dtype, int32_t* dev_status, void* stream) {
+  if (src == nullptr || out == nullptr || !buffers_ok(*src)) return KVQ_ERR_INVALID_ARG;
+  if (src->D > 0 && src->D != 64 && src->D != 128) return KVQ_ERR_UNSUPPORTED;
+  DequantizeArgs a;
+  if (!resolve_layout(*src, &a.layout)) return KVQ_ERR_INVALID_ARG;
+  if (!aligned16(out) || (out_dtype != KVQ_OUT_F32 && out_dtype != KVQ_OUT_BF16)) return KVQ_ERR_INVALID_ARG;
+  const kvq_status s = chunk_desc(chunk, *src, table, &a.chunk);
+  if (s != KVQ_OK) return s;
+  if (chunk->rows == 0) return KVQ_OK;
+  a.src = src;
+  a.out = out;
+  a.out_dtype = out_dtype;
+  a.status = dev_status;
+  return launch_dequantize(a, static_cast<cudaStream_t>(stream)) == cudaSuccess ? KVQ_OK : KVQ_ERR_CUDA;
+}
+
+static kvq_status chunk_attention_impl(const void* q, int64_t sq_row, int64_t sq_head, const kvq_chunk* chunk,
+                                       const kvq_cache* k, const kvq_cache* v, const kvq_block_table* table,
+                                       int32_t Hq, float softmax_scale, int32_t window, int32_t sinks, void* out,
+                                       int32_t out_dtype, void* workspace, size_t workspace_bytes,
+                                       int32_t* dev_status, void* stream) {
+  if (q == nullptr || k == nullptr || v == nullptr || out == nullptr || !buffers_ok(*k) || !buffers_ok(*v))
+    return KVQ_ERR_INVALID_ARG;
+  if (k->D > 0 && k->D != 64 && k->D != 128) return KVQ_ERR_UNSUPPORTED;
+  ChunkAttnArgs a;
+  if (!resolve_layout(*k, &a.layout) || !same_cache_shape(*k, *v)) return KVQ_ERR_INVALID_ARG;
+  if (Hq <= 0 || Hq % k->Hkv || window < 0 || sinks < 0) return KVQ_ERR_INVALID_ARG;
+  if (Hq / k->Hkv > 128) return KVQ_ERR_UNSUPPORTED;
+  if (out_dtype != KVQ_OUT_F32 && out_dtype != KVQ_OUT_BF16) return KVQ_ERR_INVALID_ARG;
+  if (!aligned16(q) || !aligned16(out) || sq_row < 0 || sq_head < 0 || sq_row % 8 || sq_head % 8)
+    return KVQ_ERR_INVALID_ARG;
+  const kvq_status s = chunk_desc(chunk, *k, table, &a.chunk);
+  if (s != KVQ_OK) return s;
+  if (static_cast<int64_t>(chunk->rows) * Hq >= (int64_t(1) << 31)) return KVQ_ERR_UNSUPPORTED;
+  if (workspace == nullptr || !aligned16(workspace) ||
+      workspace_bytes < chunk_workspace_bytes(chunk->rows, chunk->B, Hq, k->Hkv, k->D))
+    return KVQ_ERR_WORKSPACE;
+  if (chunk->rows == 0) return KVQ_OK;
+  a.q = static_cast<const uint16_t*>(q);
+  a.sq_row = sq_row;
+  a.sq_head = sq_head;
+  a.k = k;
+  a.v = v;
+  a.Hq = Hq;
+  a.softmax_scale = softmax_scale;
+  a.window = window;
+  a.sinks = sinks;
+  a.out = out;
+  a.out_dtype = out_dtype;
+  a.ws = workspace;
+  a.ws_bytes = workspace_bytes;
+  a.status = dev_status;
+  return launch_chunk_attention(a, static_cast<cudaStream_t>(stream));
+}
+
+extern "C" {
+
+kvq_status kvq_append_chunk(const void* k_new, const void* v_new, int64_t s_row, int64_t s_head,
+                            const kvq_chunk* chunk, const kvq_cache* k, const kvq_cache* v, int32_t* dev_status,
+                            void* stream) {
+  return append_chunk_impl(k_new, v_new, s_row, s_head, chunk, k, v, nullptr, dev_status, stream);
+}
+
+kvq_status kvq_append_chunk_paged(const void* k_new, const void* v_new, int64_t s_row, int64_t s_head,
+                                  const kvq_chunk* chunk, const kvq_cache* k_pool, const kvq_cache* v_pool,
+                                  const kvq_block_table* table, int32_t* dev_status, void* stream) {
+  if (table == nullptr) return KVQ_ERR_INVALID_ARG;
+  return append_chunk_impl(k_new, v_new, s_row, s_head, chunk, k_pool, v_pool, table, dev_status, stream);
+}
+
+kvq_status kvq_dequantize(const kvq_cache* src, const kvq_chunk* chunk, void* out, int32_t out_dtype,
+                          int32_t* dev_status, void* stream) {
+  return dequantize_impl(src, chunk, nullptr, out, out_dtype, dev_status, stream);
+}
+
+kvq_status kvq_dequantize_paged(const kvq_cache* pool, const kvq_chunk* chunk, const kvq_block_table* table,
+                                void* out, int32_t out_dtype, int32_t* dev_status, void* stream) {
+  if (table == nullptr) return KVQ_ERR_INVALID_ARG;
+  return dequantize_impl(pool, chunk, table, out, out_dtype, dev_status, stream);
+}
+
+size_t kvq_chunk_workspace_bytes(int32_t rows, int32_t B, int32_t Hq, int32_t Hkv, int32_t D) {
+  if (rows < 0 || B <= 0 || B > 4096 || Hkv <= 0 || Hkv > KVQ_MAX_HKV || Hq <= 0 || Hq % Hkv || Hq / Hkv > 128 ||
+      (D != 64 && D != 128) || static_cast<int64_t>(rows) * Hq >= (int64_t(1) << 31))
+    return 0;
+  return chunk_workspace_bytes(rows, B, Hq, Hkv, D);
+}
+
+kvq_status kvq_chunk_attention(const void* q, int64_t sq_row, int64_t sq_head, const kvq_chunk* chunk,
+                               const kvq_cache* k, const kvq_cache* v, int32_t Hq, float softmax_scale,
+                               int32_t window, int32_t sinks, void* out, int32_t out_dtype, void* workspace,
+                               size_t workspace_bytes, int32_t* dev_status, void* stream) {
+  return chunk_attention_impl(q, sq_row, sq_head, chunk, k, v, nullptr, Hq, softmax_scale, window, sinks, out,
+                              out_dtype, workspace, workspace_bytes, dev_status, stream);
+}
+
+kvq_status kvq_chunk_attention_paged(const void* q, int64_t sq_row, int64_t sq_head, const kvq_chunk* chunk,
+                                     const kvq_cache* k_pool, const kvq_cache* v_pool, const kvq_block_table* table,
+                                     int32_t Hq, float softmax_scale, int32_t window, int32_t sinks, void* out,
+                                     int32_t out_dtype, void* workspace, size_t workspace_bytes, int32_t* dev_status,
+                                     void* stream) {
+  if (table == nullptr) return KVQ_ERR_INVALID_ARG;
+  return chunk_attention_impl(q, sq_row, sq_head, chunk, k_pool, v_pool, table, Hq, softmax_scale, window, sinks, out,
+                              out_dtype, workspace, workspace_bytes, dev_status, stream);
+}
+
+kvq_status kvq_decode_attention_window(const void* q, const kvq_cache* k, const kvq_cache* v,
+                                       const int32_t* seq_lens, int32_t Hq, float softmax_scale, int32_t window,
+                                       int32_t sinks, void* out, int32_t out_dtype, void* workspace,
+                                       size_t workspace_bytes, int32_t* dev_status, void* stream) {
+  return decode_impl(q, k, v, nullptr, seq_lens, Hq, softmax_scale, out, out_dtype, workspace, workspace_bytes,
+                     dev_status, stream, nullptr, window, sinks);
+}
+
+kvq_status kvq_decode_attention_window_paged(const void* q, const kvq_cache* k_pool, const kvq_cache* v_pool,
+                                             const kvq_block_table* table, const int32_t* seq_lens, int32_t Hq,
+                                             float softmax_scale, int32_t window, int32_t sinks, void* out,
+                                             int32_t out_dtype, void* workspace, size_t workspace_bytes,
+                                             int32_t* dev_status, void* stream) {
+  if (table == nullptr) return KVQ_ERR_INVALID_ARG;
+  return decode_impl(q, k_pool, v_pool, table, seq_lens, Hq, softmax_scale, out, out_dtype, workspace,
+                     workspace_bytes, dev_status, stream, nullptr, window, sinks);
 }
 
 }  // extern "C"

@@ -105,6 +105,9 @@ struct DParams {
   // one, it is page bt[b * bt_stride + i] of a pool of pB pages of pT = 64
   const int32_t* bt;
   int32_t bt_stride, pB, pT;
+  // sliding window (WIN instantiations): a sequence's query sees its last
+  // `window` tokens and its first `sinks`
+  int32_t window, sinks;
   float scale_log2;
   // per-call policy: tiles per CTA prefetched into L2 before the dependency
   // wait (0 .. kMaxL2Tiles), the bounded-wait limit, and the test-only issue
@@ -190,6 +193,32 @@ __device__ __forceinline__ void ffma2_b(float& d0, float& d1, float a, float b0,
       "mov.b64 {%0, %1}, rd;\n\t}"
       : "+f"(d0), "+f"(d1)
       : "f"(a), "f"(b0), "f"(b1));
+}
+
+// The 64-token tiles of a sequence that its query sees, in order: without a
+// window all of them; with one, the sinks' tiles and then those from the
+// window's first token on.  Index i of that list is tile visible_tile(i); the
+// work list, the split and the merge only ever see the indices.
+template <bool WIN>
+struct Visible {
+  int n;               // tiles
+  int ns, skip;        // (WIN) index ns and later: tile i + skip
+  __device__ __forceinline__ Visible(const DParams& p, int len) : ns(0), skip(0) {
+    n = (len + kTile - 1) / kTile;
+    if constexpr (WIN) {
+      const int fw = max(len - p.window, 0) / kTile;   // tile of the window's first token
+      ns = min((min(p.sinks, len) + kTile - 1) / kTile, fw);
+      skip = fw - ns;
+      n -= skip;
+    }
+  }
+  __device__ __forceinline__ int tile(int i) const { return WIN && i >= ns ? i + skip : i; }
+};
+
+// Whether the query of a sequence of length len does not see token j < len.
+template <bool WIN>
+__device__ __forceinline__ bool window_hides(const DParams& p, int len, int j) {
+  return WIN && j < len - p.window && j >= p.sinks;
 }
 
 using split::Cursor;
@@ -555,9 +584,10 @@ __device__ __forceinline__ void segment_end(const DParams& p, const EpiBuf<D>* e
 // the P.V products.  lim[u] = tokens of tile u inside the sequence.  The
 // running max m_run and the per-lane partial sums l_run are those of heads
 // 2t, 2t+1 -- the same heads as the lane's output accumulator columns.
-template <int D, int BITS, int NT>
+// WIN: rows from sk[u] to lo[u] - 1 of tile u lie before the window and are no sinks.
+template <int D, int BITS, int NT, bool WIN>
 __device__ __forceinline__ void consume_tiles(const uint32_t (&st_s)[NT], const uint8_t* const (&st)[NT],
-                                              const int (&lim)[NT], const uint32_t (&qa)[D / 16][2],
+                                              const int (&lim)[NT], const int (&lo)[NT], const int (&sk)[NT], const uint32_t (&qa)[D / 16][2],
                                               const float (&qs)[D / 32][2], float (&O)[D / 16][4],
                                               float (&Z)[2][4], float (&m_run)[2], float (&l_run)[2],
                                               const LaneAddr& la, int w, int g, int t) {
@@ -570,6 +600,10 @@ __device__ __forceinline__ void consume_tiles(const uint32_t (&st_s)[NT], const 
   for (int u = 0; u < NT; ++u) {
     if (r0 >= lim[u]) S[u][0] = S[u][1] = -INFINITY;
     if (r0 + 8 >= lim[u]) S[u][2] = S[u][3] = -INFINITY;
+    if constexpr (WIN) {
+      if (r0 < lo[u] && r0 >= sk[u]) S[u][0] = S[u][1] = -INFINITY;
+      if (r0 + 8 < lo[u] && r0 + 8 >= sk[u]) S[u][2] = S[u][3] = -INFINITY;
+    }
   }
   // online softmax for heads 2t, 2t+1: the max over the warp's tokens (rows g).
   // While no score exceeds the running max the max is unchanged and so is
@@ -634,13 +668,13 @@ __device__ __forceinline__ void consume_tiles(const uint32_t (&st_s)[NT], const 
 // but they only choose which lines to prefetch (clamped into the cache), and
 // an L2 prefetch returns nothing to the program, so no result depends on
 // them.  Batches of more than 32 sequences skip the warm-up.
-template <int D, bool PAGED>
+template <int D, bool PAGED, bool WIN>
 __device__ __forceinline__ void warm_l2(const DParams& p, int lane) {
   constexpr int G = D / 32;
   if (p.l2_warm <= 0 || p.B > 32) return;
   int len = lane < p.B ? p.seq_lens[lane] : 0;
   len = min(max(len, 0), p.Tcap);
-  const int n = (len + kTile - 1) / kTile;
+  const int n = Visible<WIN>(p, len).n;
   int incl = n;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
@@ -659,9 +693,11 @@ __device__ __forceinline__ void warm_l2(const DParams& p, int lane) {
   const int bs = min(b, p.B - 1);
   const int nb = __shfl_sync(0xffffffffu, n, bs);
   const int eb = __shfl_sync(0xffffffffu, incl, bs) - nb;
+  const int lb = __shfl_sync(0xffffffffu, len, bs);
   if (lane >= p.l2_warm || f >= f1 || b >= p.B || nb == 0) return;
   const int64_t off = f - static_cast<int64_t>(p.Hkv) * eb;
-  const int kvh = static_cast<int>(off / nb), i = static_cast<int>(off % nb);
+  const int kvh = static_cast<int>(off / nb);
+  const int i = Visible<WIN>(p, lb).tile(static_cast<int>(off % nb));
   const int bits = p.bits[kvh];
   int pb = bs, pt = i * kTile;
   if constexpr (PAGED) {   // (a stale or bad page id only misdirects this prefetch)
@@ -681,7 +717,9 @@ __device__ __forceinline__ void warm_l2(const DParams& p, int lane) {
 // PAGED: the tiles are pages of a pool found through p.bt (a separate
 // instantiation, so the contiguous kernel carries none of it).  RING: tiles
 // kept in flight into shared memory (the policy's ring depth, 2 or kStages).
-template <int D, bool PAGED, int RING>
+// WIN: only the tiles that a sliding window and its sinks leave visible (again
+// its own instantiation).
+template <int D, bool PAGED, int RING, bool WIN>
 __global__ void __launch_bounds__(kThreads, KVQ_DECODE_MIN_BLOCKS) decode_split_kernel(const __grid_constant__ DParams p) {
   using L = Smem<D>;
   constexpr int G = D / 32;
@@ -718,7 +756,7 @@ __global__ void __launch_bounds__(kThreads, KVQ_DECODE_MIN_BLOCKS) decode_split_
     prefetch_tmap(&p.tm_k4);
     prefetch_tmap(&p.tm_v4);
   }
-  if (w == kWarps) warm_l2<D, PAGED>(p, lane);
+  if (w == kWarps) warm_l2<D, PAGED, WIN>(p, lane);
   // With programmatic dependent launch this kernel may start while the
   // previous kernel in the stream is finishing: wait for it (and its memory)
   // before the first global access whose data is used, then let the next one
@@ -750,7 +788,7 @@ __global__ void __launch_bounds__(kThreads, KVQ_DECODE_MIN_BLOCKS) decode_split_
         len = small_b ? load_len(b) : lens[b];
         if (small_b) lens[b] = len;
       }
-      int n = (len + kTile - 1) / kTile;
+      int n = Visible<WIN>(p, len).n;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
         const int v = __shfl_up_sync(0xffffffffu, n, o);
@@ -797,13 +835,17 @@ __global__ void __launch_bounds__(kThreads, KVQ_DECODE_MIN_BLOCKS) decode_split_
       // paged caches: the page ids are loaded kStages tiles ahead of their
       // copies (a ring of registers), so the lookups overlap the stage waits
       Cursor pa = pc;
+      auto page_id = [&](const Cursor& c) -> int {
+        const int i = Visible<WIN>(p, lens[c.b]).tile(c.i);
+        return KVQ_IN_RANGE(c.b < p.B && i < p.bt_stride, p.status)
+                   ? p.bt[static_cast<int64_t>(c.b) * p.bt_stride + i] : 0;
+      };
       int pg[kStages];
 #pragma unroll
       for (int j = 0; j < kStages; ++j) {
         pg[j] = 0;
         if (PAGED && j < ntiles) {
-          pg[j] = KVQ_IN_RANGE(pa.b < p.B && pa.i < p.bt_stride, p.status)
-                      ? p.bt[static_cast<int64_t>(pa.b) * p.bt_stride + pa.i] : 0;
+          pg[j] = page_id(pa);
           advance(pa, pre, B, Hkv);
         }
       }
@@ -818,15 +860,14 @@ __global__ void __launch_bounds__(kThreads, KVQ_DECODE_MIN_BLOCKS) decode_split_
         uint8_t* st = smem + slot * L::kStageBytes;
         const int bits = p.bits[pc.kvh];
         const int Rb = D * bits / 8;
-        int pb = pc.b, pt = pc.i * kTile;
+        int pb = pc.b, pt = Visible<WIN>(p, lens[pc.b]).tile(pc.i) * kTile;
         if constexpr (PAGED) {
           pb = pg[0];
 #pragma unroll
           for (int j = 0; j + 1 < kStages; ++j) pg[j] = pg[j + 1];
           pg[kStages - 1] = 0;
           if (k + kStages < ntiles) {
-            pg[kStages - 1] = KVQ_IN_RANGE(pa.b < p.B && pa.i < p.bt_stride, p.status)
-                                  ? p.bt[static_cast<int64_t>(pa.b) * p.bt_stride + pa.i] : 0;
+            pg[kStages - 1] = page_id(pa);
             advance(pa, pre, B, Hkv);
           }
           if (pb < 0 || pb >= p.pB) {   // a page outside the pool: report, read page 0 instead
@@ -875,6 +916,7 @@ __global__ void __launch_bounds__(kThreads, KVQ_DECODE_MIN_BLOCKS) decode_split_
         const uint32_t* ksz = reinterpret_cast<const uint32_t*>(st + L::kOffKsz);
         const uint32_t* vsz = reinterpret_cast<const uint32_t*>(st + L::kOffVsz);
         const int len = lens[tc.b];
+        const int ti = Visible<WIN>(p, len).tile(tc.i);
         // Lane l takes tokens 2l and 2l+1 (all G groups of each: the raw words
         // are [token][group]) and writes their entries in the consumers'
         // fragment order: warp l/8; K table rows 2(l%4) and 2(l%4)+1, slot
@@ -891,7 +933,7 @@ __global__ void __launch_bounds__(kThreads, KVQ_DECODE_MIN_BLOCKS) decode_split_
         load_words<G>(vw[1], vsz + (t0 + 1) * G);
 #pragma unroll
         for (int u = 0; u < 2; ++u)
-          if (tc.i * kTile + t0 + u >= len) {   // past the sequence end: zero scales
+          if (ti * kTile + t0 + u >= len || window_hides<WIN>(p, len, ti * kTile + t0 + u)) {   // not seen: zero scales
 #pragma unroll
             for (int grp = 0; grp < G; ++grp) kw[u][grp] = vw[u][grp] = 0u;
           }
@@ -911,9 +953,9 @@ __global__ void __launch_bounds__(kThreads, KVQ_DECODE_MIN_BLOCKS) decode_split_
         fence_proxy_async_smem();
         if (lane == 0) {
           const int n_b = pre[tc.b + 1] - pre[tc.b];
-          int flags = tc.i;
+          int flags = ti;
           if (p.bits[tc.kvh] == 4) flags |= kFlag4;
-          if ((tc.i + 1) * kTile <= len) flags |= kFlagFull;
+          if ((ti + 1) * kTile <= len) flags |= kFlagFull;
           if (tc.i == 0 || kk == 0) flags |= kFlagStart;
           if (tc.i == n_b - 1 || kk == ntiles - 1) flags |= kFlagEnd;
           *reinterpret_cast<int4*>(st + L::kOffMeta) = make_int4(tc.b, tc.kvh, flags, len);
@@ -979,6 +1021,8 @@ __global__ void __launch_bounds__(kThreads, KVQ_DECODE_MIN_BLOCKS) decode_split_
     }
     // tokens of a tile inside the sequence
     auto tile_lim = [len](int f) { return (f & kFlagFull) ? kTile : len - (f & 0xFFFFFF) * kTile; };
+    auto tile_lo = [&](int f) { return len - p.window - (f & 0xFFFFFF) * kTile; };   // (WIN)
+    auto tile_sk = [&](int f) { return p.sinks - (f & 0xFFFFFF) * kTile; };
     int fend, nt;
     if (!(meta.z & kFlagEnd)) {
       // the next tile belongs to the same piece: take both in one step
@@ -991,16 +1035,17 @@ __global__ void __launch_bounds__(kThreads, KVQ_DECODE_MIN_BLOCKS) decode_split_
       const uint32_t ss[2] = {smem_u32(st0), smem_u32(st1)};
       const uint8_t* const sp[2] = {st0, st1};
       const int lim[2] = {tile_lim(meta.z), tile_lim(f1)};
-      if (!four) consume_tiles<D, 8, 2>(ss, sp, lim, qa, qs, O, Z, m_run, l_run, la, w, g, t);
-      else consume_tiles<D, 4, 2>(ss, sp, lim, qa, qs, O, Z, m_run, l_run, la, w, g, t);
+      const int lo[2] = {tile_lo(meta.z), tile_lo(f1)}, sk[2] = {tile_sk(meta.z), tile_sk(f1)};
+      if (!four) consume_tiles<D, 8, 2, WIN>(ss, sp, lim, lo, sk, qa, qs, O, Z, m_run, l_run, la, w, g, t);
+      else consume_tiles<D, 4, 2, WIN>(ss, sp, lim, lo, sk, qa, qs, O, Z, m_run, l_run, la, w, g, t);
       fend = f1;
       nt = 2;
     } else {
       const uint32_t ss[1] = {smem_u32(st0)};
       const uint8_t* const sp[1] = {st0};
-      const int lim[1] = {tile_lim(meta.z)};
-      if (!four) consume_tiles<D, 8, 1>(ss, sp, lim, qa, qs, O, Z, m_run, l_run, la, w, g, t);
-      else consume_tiles<D, 4, 1>(ss, sp, lim, qa, qs, O, Z, m_run, l_run, la, w, g, t);
+      const int lim[1] = {tile_lim(meta.z)}, lo[1] = {tile_lo(meta.z)}, sk[1] = {tile_sk(meta.z)};
+      if (!four) consume_tiles<D, 8, 1, WIN>(ss, sp, lim, lo, sk, qa, qs, O, Z, m_run, l_run, la, w, g, t);
+      else consume_tiles<D, 4, 1, WIN>(ss, sp, lim, lo, sk, qa, qs, O, Z, m_run, l_run, la, w, g, t);
       fend = meta.z;
       nt = 1;
     }
@@ -1069,8 +1114,8 @@ __global__ void __launch_bounds__(kThreads, KVQ_DECODE_MIN_BLOCKS) decode_split_
 }
 
 // CTAs per SM of the decode kernel on the current device (the same for both
-// ring depths: their resources are the same); sets the shared-memory limit
-// of both instantiations once per device.
+// ring depths and with a window: their resources are the same); sets the
+// shared-memory limit of these instantiations once per device.
 template <int D, bool PAGED>
 int ctas_per_sm() {
   static int cached[64] = {0};
@@ -1080,9 +1125,13 @@ int ctas_per_sm() {
     int n = 0;
     const size_t sm = Smem<D>::bytes(64);
     const int lim = static_cast<int>(Smem<D>::bytes(4096));
-    cudaFuncSetAttribute(decode_split_kernel<D, PAGED, 2>, cudaFuncAttributeMaxDynamicSharedMemorySize, lim);
-    cudaFuncSetAttribute(decode_split_kernel<D, PAGED, kStages>, cudaFuncAttributeMaxDynamicSharedMemorySize, lim);
-    if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, decode_split_kernel<D, PAGED, kStages>, kThreads, sm) !=
+    cudaFuncSetAttribute(decode_split_kernel<D, PAGED, 2, false>, cudaFuncAttributeMaxDynamicSharedMemorySize, lim);
+    cudaFuncSetAttribute(decode_split_kernel<D, PAGED, kStages, false>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                         lim);
+    cudaFuncSetAttribute(decode_split_kernel<D, PAGED, kStages, true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                         lim);
+    if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, decode_split_kernel<D, PAGED, kStages, false>, kThreads,
+                                                      sm) !=
             cudaSuccess ||
         n < 1)
       n = 1;
@@ -1097,9 +1146,12 @@ template <int D, bool PAGED>
 bool regs_ok() {
   static int cached = -1;
   if (cached < 0) {
-    cudaFuncAttributes fa, fb;
-    cached = (cudaFuncGetAttributes(&fa, decode_split_kernel<D, PAGED, 2>) == cudaSuccess && fa.numRegs == 128 &&
-              cudaFuncGetAttributes(&fb, decode_split_kernel<D, PAGED, kStages>) == cudaSuccess && fb.numRegs == 128)
+    auto has128 = [](auto* kernel) {
+      cudaFuncAttributes fa;
+      return cudaFuncGetAttributes(&fa, kernel) == cudaSuccess && fa.numRegs == 128;
+    };
+    cached = (has128(decode_split_kernel<D, PAGED, 2, false>) && has128(decode_split_kernel<D, PAGED, kStages, false>) &&
+              has128(decode_split_kernel<D, PAGED, kStages, true>))
                  ? 1
                  : 0;
   }
@@ -1121,8 +1173,10 @@ cudaError_t launch_split(const DParams& p, int C, int B, int ring, cudaStream_t 
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return ring == 2 ? cudaLaunchKernelEx(&cfg, decode_split_kernel<D, PAGED, 2>, p)
-                   : cudaLaunchKernelEx(&cfg, decode_split_kernel<D, PAGED, kStages>, p);
+  // (a windowed call takes the default ring depth: it has no policy argument)
+  if (p.window > 0) return cudaLaunchKernelEx(&cfg, decode_split_kernel<D, PAGED, kStages, true>, p);
+  return ring == 2 ? cudaLaunchKernelEx(&cfg, decode_split_kernel<D, PAGED, 2, false>, p)
+                   : cudaLaunchKernelEx(&cfg, decode_split_kernel<D, PAGED, kStages, false>, p);
 }
 
 }  // namespace
@@ -1197,6 +1251,8 @@ kvq_status launch_decode(const DecodeArgs& a, cudaStream_t stream) {
   p.bt_stride = a.bt_max_pages;
   p.pB = K.B;
   p.pT = K.Tcap;
+  p.window = a.window;
+  p.sinks = a.sinks;
   const float scale = a.softmax_scale > 0.0f ? a.softmax_scale : 1.0f / sqrtf(static_cast<float>(D));
   p.scale_log2 = scale * 1.4426950408889634f;
   for (int h = 0; h < KVQ_MAX_HKV; ++h) {

@@ -1,0 +1,151 @@
+// kvq_dequantize.cu -- the group-quantised cache read back as values
+// (《分块稀疏注意力与KV Cache量化：长文本推理显存优化实践》 §2.4: x_hat = (c - z) s).
+//
+// HBM-bound: each code and scale/zero word is read once, each value written
+// once; the output (256 bytes a row in bf16 at D = 128) is the larger side.  A
+// lane takes 8 channels: 8 bytes of codes (4 of a 4-bit head) in, one 16-byte
+// bf16 store out, so that a warp's loads cover whole consecutive cache rows of
+// one head and its stores whole output rows.  c - z is exact in fp32 and so is
+// its product with the fp16 scale (9 + 11 significant bits), so the only
+// rounding is the one to bf16.
+#include <algorithm>
+
+#include "kvq_chunk.cuh"
+#include "kvq_internal.h"
+
+namespace kvq {
+namespace {
+
+constexpr int kWarps = 8;
+
+struct DqParams {
+  chunk::View c;
+  const uint8_t* codes;
+  const uint32_t* sz;
+  void* out;
+  int32_t* status;
+  int32_t Hkv, tiles;       // tiles: runs of kRows rows
+  int64_t codes_bytes;      // size of the code buffer (the debug build's index checks)
+  int64_t plane_off[KVQ_MAX_HKV];
+  int8_t bits[KVQ_MAX_HKV];
+};
+
+// 2^23 + c as an fp32 has c in its low byte
+__device__ __forceinline__ float biased(uint32_t c) { return __uint_as_float(0x4B000000u | c); }
+
+// The 8 values of a lane's codes: (c - z) s.
+__device__ __forceinline__ void values8(float (&x)[8], uint2 c, int bits, uint32_t word) {
+  const float zb = 8388608.0f + half_hi(word), s = half_lo(word);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const uint32_t code = bits == 8 ? ((i < 4 ? c.x : c.y) >> (8 * (i & 3))) & 0xFFu : (c.x >> (4 * i)) & 0xFu;
+    x[i] = (biased(code) - zb) * s;
+  }
+}
+
+template <int D, bool F32>
+__global__ void __launch_bounds__(kWarps * 32) dequantize_kernel(const __grid_constant__ DqParams p) {
+  constexpr int G = D / 32;
+  constexpr int LPR = D / 8;          // lanes per row
+  constexpr int RPP = 32 / LPR;       // rows per pass
+  constexpr int NP = 4;               // passes whose loads are in flight together
+  constexpr int R = RPP * NP;         // rows per warp
+  // launched as a programmatic dependent: the rows may have been written by
+  // the kernel before it
+  grid_dependency_wait();
+  grid_launch_dependents();
+  const int lane = threadIdx.x & 31;
+  if (blockIdx.x == 0) chunk::check_sequences(p.c, threadIdx.x, blockDim.x, p.status);
+  const int64_t nw = static_cast<int64_t>(p.tiles) * p.Hkv;
+  const int64_t storage = static_cast<int64_t>(p.c.pB) * p.c.pT;
+  const int col = lane % LPR;
+  for (int64_t u = static_cast<int64_t>(blockIdx.x) * kWarps + (threadIdx.x >> 5); u < nw;
+       u += static_cast<int64_t>(gridDim.x) * kWarps) {
+    const int tile = static_cast<int>(static_cast<uint32_t>(u) / static_cast<uint32_t>(p.Hkv));
+    const int h = static_cast<int>(static_cast<uint32_t>(u) - static_cast<uint32_t>(tile) * p.Hkv);
+    const int r0 = tile * R;
+    const int64_t mine = chunk::locate_rows(p.c, r0, lane, R, h == 0, p.status);
+    const int bits = p.bits[h];
+    int64_t pos[NP];
+    uint2 c[NP];
+    uint32_t word[NP];
+#pragma unroll
+    for (int k = 0; k < NP; ++k) {
+      pos[k] = __shfl_sync(0xffffffffu, mine, k * RPP + lane / LPR);
+      c[k] = make_uint2(0u, 0u);
+      word[k] = 0u;                   // a page outside the pool reads as zeros
+      if (pos[k] < 0) continue;
+      const int64_t off = p.plane_off[h] + pos[k] * (D * bits / 8) + col * bits;
+      const int64_t si = (static_cast<int64_t>(h) * storage + pos[k]) * G + col / 4;
+      if (!KVQ_IN_RANGE(off >= 0 && off + bits <= p.codes_bytes && si < static_cast<int64_t>(p.Hkv) * storage * G,
+                        p.status))
+        continue;
+      if (bits == 8) c[k] = *reinterpret_cast<const uint2*>(p.codes + off);
+      else c[k].x = *reinterpret_cast<const uint32_t*>(p.codes + off);
+      word[k] = p.sz[si];
+    }
+#pragma unroll
+    for (int k = 0; k < NP; ++k) {
+      if (pos[k] == chunk::kNoRow) continue;
+      float x[8];
+      values8(x, c[k], bits, word[k]);
+      const int64_t o = (static_cast<int64_t>(r0 + k * RPP + lane / LPR) * p.Hkv + h) * D + col * 8;
+      if constexpr (F32) {
+        float4* dst = reinterpret_cast<float4*>(static_cast<float*>(p.out) + o);
+        dst[0] = make_float4(x[0], x[1], x[2], x[3]);
+        dst[1] = make_float4(x[4], x[5], x[6], x[7]);
+      } else {
+        uint32_t v[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const __nv_bfloat162 b = __floats2bfloat162_rn(x[2 * i], x[2 * i + 1]);
+          v[i] = *reinterpret_cast<const uint32_t*>(&b);
+        }
+        *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.out) + o) = make_uint4(v[0], v[1], v[2], v[3]);
+      }
+    }
+  }
+}
+
+}  // namespace
+
+cudaError_t launch_dequantize(const DequantizeArgs& a, cudaStream_t stream) {
+  DqParams p;
+  const kvq_cache& s = *a.src;
+  p.c.start = a.chunk.start; p.c.seq_lens = a.chunk.seq_lens; p.c.bt = a.chunk.bt;
+  p.c.B = a.chunk.B; p.c.rows = a.chunk.rows; p.c.max_chunk = a.chunk.max_chunk;
+  p.c.bt_stride = a.chunk.bt_max_pages;
+  p.c.cap = a.chunk.cap;
+  p.c.pB = s.B; p.c.pT = s.Tcap;
+  p.codes = s.codes;
+  p.sz = s.sz;
+  p.out = a.out;
+  p.status = a.status;
+  p.Hkv = s.Hkv;
+  p.codes_bytes = a.layout.off4 + static_cast<int64_t>(a.layout.n4) * s.B * s.Tcap * (s.D / 2);
+  for (int h = 0; h < KVQ_MAX_HKV; ++h) {
+    p.plane_off[h] = a.layout.plane_off[h];
+    p.bits[h] = a.layout.bits[h];
+  }
+  const int R = 4 * 256 / s.D;
+  p.tiles = (a.chunk.rows + R - 1) / R;
+  const int64_t warps = static_cast<int64_t>(p.tiles) * p.Hkv;
+  const int64_t blocks = std::min<int64_t>((warps + kWarps - 1) / kWarps, int64_t(1) << 30);
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(blocks));
+  cfg.blockDim = dim3(kWarps * 32);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  const bool f32 = a.out_dtype == KVQ_OUT_F32;
+  if (s.D == 128)
+    return f32 ? cudaLaunchKernelEx(&cfg, dequantize_kernel<128, true>, p)
+               : cudaLaunchKernelEx(&cfg, dequantize_kernel<128, false>, p);
+  return f32 ? cudaLaunchKernelEx(&cfg, dequantize_kernel<64, true>, p)
+             : cudaLaunchKernelEx(&cfg, dequantize_kernel<64, false>, p);
+}
+
+}  // namespace kvq

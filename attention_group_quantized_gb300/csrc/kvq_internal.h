@@ -69,6 +69,60 @@ struct AppendArgs {
 };
 cudaError_t launch_append(const AppendArgs& a, cudaStream_t stream);
 
+// A ragged chunk over a cache's storage (chunk::View of kvq_chunk.cuh).
+struct ChunkDesc {
+  const int32_t* start;
+  const int32_t* seq_lens;
+  const int32_t* bt = nullptr;      // optional block table
+  int32_t B, rows, max_chunk;
+  int32_t bt_max_pages = 0;
+  int32_t cap;                      // tokens a sequence may have
+};
+
+// The chunk's rows of K and V, quantised to their positions (one launch).
+struct AppendChunkArgs {
+  const uint16_t* k_new;
+  const uint16_t* v_new;
+  int64_t s_row, s_head;
+  ChunkDesc chunk;
+  const kvq_cache* k;
+  const kvq_cache* v;
+  HeadLayout layout;                // shared by K and V
+  int32_t* status;
+};
+cudaError_t launch_append_chunk(const AppendChunkArgs& a, cudaStream_t stream);
+
+// The chunk's positions of one cache as values.
+struct DequantizeArgs {
+  const kvq_cache* src;
+  HeadLayout layout;
+  ChunkDesc chunk;
+  void* out;
+  int32_t out_dtype;
+  int32_t* status;
+};
+cudaError_t launch_dequantize(const DequantizeArgs& a, cudaStream_t stream);
+
+// Attention of the chunk's queries.
+struct ChunkAttnArgs {
+  const uint16_t* q;
+  int64_t sq_row, sq_head;
+  ChunkDesc chunk;
+  const kvq_cache* k;
+  const kvq_cache* v;
+  HeadLayout layout;
+  int32_t Hq;
+  float softmax_scale;
+  int32_t window, sinks;
+  void* out;
+  int32_t out_dtype;
+  void* ws;
+  size_t ws_bytes;
+  int32_t* status;
+};
+size_t chunk_workspace_bytes(int rows, int B, int Hq, int Hkv, int D);
+kvq_status launch_chunk_attention(const ChunkAttnArgs& a, cudaStream_t stream);
+
 struct DecodeArgs {
   const uint16_t* q;
   const kvq_cache* k;
@@ -85,6 +139,8 @@ struct DecodeArgs {
   // optional block table: the caches are page pools (B = pages, Tcap = 64)
   const int32_t* bt = nullptr;
   int32_t bt_B = 0, bt_max_pages = 0;
+  // sliding window (0: none) and leading tokens that stay visible with it
+  int32_t window = 0, sinks = 0;
   Policy pol;
 };
 // Number of persistent split CTAs on the current device for head dim D.

@@ -13,6 +13,9 @@
 // be are redone value by value.  One 32-byte (INT8) or 16-byte (INT4) store
 // of codes per group; a warp's stores cover whole contiguous rows.  The result
 // is bit-identical to the specification's IEEE fp32 arithmetic.
+#include <algorithm>
+
+#include "kvq_chunk.cuh"
 #include "kvq_device.cuh"
 #include "kvq_internal.h"
 
@@ -480,6 +483,56 @@ __global__ void __launch_bounds__(256) append_kernel(const __grid_constant__ APa
   }
 }
 
+// Append of a chunk: packed rows of K and V ([row][head], strided) written at
+// their sequences' positions.  One thread per group of 32 channels, as in
+// quantize_kernel; a warp takes one KV head and 32 / G consecutive rows, so
+// that its code stores cover whole consecutive cache rows and its scale/zero
+// stores one contiguous run, while its loads are whole 128- or 256-byte rows.
+// The rows' positions are looked up once per warp, a lane per row.
+struct ACParams {
+  chunk::View c;
+  const uint16_t* x[2];     // k_new, v_new
+  int64_t s_row, s_head;
+  uint8_t* codes[2];
+  uint32_t* sz[2];
+  int32_t* status;
+  int32_t Hkv;
+  int32_t tiles;            // runs of 32 / G rows
+  int64_t codes_bytes;      // size of each code buffer (the debug build's index checks)
+  int64_t plane_off[KVQ_MAX_HKV];
+  int8_t bits[KVQ_MAX_HKV];
+};
+
+template <int D>
+__global__ void __launch_bounds__(256, KVQ_QUANT_MIN_BLOCKS) append_chunk_kernel(const __grid_constant__ ACParams p) {
+  constexpr int G = D / 32;
+  constexpr int R = 32 / G;                   // rows per warp
+  grid_launch_dependents();
+  const int lane = threadIdx.x & 31;
+  if (blockIdx.x == 0) chunk::check_sequences(p.c, threadIdx.x, blockDim.x, p.status);
+  const int64_t nw = static_cast<int64_t>(p.tiles) * p.Hkv * 2;
+  const int64_t storage = static_cast<int64_t>(p.c.pB) * p.c.pT;
+  for (int64_t u = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5); u < nw;
+       u += static_cast<int64_t>(gridDim.x) * 8) {
+    const int job = static_cast<int>(u & 1);  // K and V of the same rows side by side: they share the look-up's lines
+    const uint32_t th = static_cast<uint32_t>(u >> 1);
+    const int tile = static_cast<int>(th / static_cast<uint32_t>(p.Hkv));
+    const int h = static_cast<int>(th - static_cast<uint32_t>(tile) * p.Hkv);
+    const int r0 = tile * R;
+    const int64_t mine = chunk::locate_rows(p.c, r0, lane, R, h == 0 && job == 0, p.status);
+    const int64_t pos = __shfl_sync(0xffffffffu, mine, lane / G);
+    if (pos < 0) continue;
+    const int g = lane % G, bits = p.bits[h];
+    const int64_t off = p.plane_off[h] + pos * (D * bits / 8) + g * (32 * bits / 8);
+    const int64_t si = (static_cast<int64_t>(h) * storage + pos) * G + g;
+    if (!group_dst_ok(off, 4 * bits, si, p.codes_bytes, static_cast<int64_t>(p.Hkv) * storage * G, p.status)) continue;
+    uint32_t w[16];
+    const uint16_t* src = p.x[job] + (r0 + lane / G) * p.s_row + h * p.s_head + g * 32;
+    load_group(w, src);
+    quantize_group(w, src, bits, p.codes[job] + off, p.sz[job] + si, p.status);
+  }
+}
+
 // Per-head error statistics: grid (chunks, H); block (c, h) takes groups
 // c * 256 + tid, then every chunks * 256, of head h's B * T * G groups
 // (row r = b * T + t, group g), and writes its (error, norm) sums in fp64 to
@@ -684,6 +737,41 @@ cudaError_t launch_append(const AppendArgs& a, cudaStream_t stream) {
     if (p.bt != nullptr) append_kernel<64, true><<<g, 256, 0, stream>>>(p);
     else append_kernel<64, false><<<g, 256, 0, stream>>>(p);
   }
+  return cudaGetLastError();
+}
+
+static chunk::View chunk_view(const ChunkDesc& c, const kvq_cache& storage) {
+  chunk::View v;
+  v.start = c.start; v.seq_lens = c.seq_lens; v.bt = c.bt;
+  v.B = c.B; v.rows = c.rows; v.max_chunk = c.max_chunk;
+  v.bt_stride = c.bt_max_pages;
+  v.cap = c.cap;
+  v.pB = storage.B; v.pT = storage.Tcap;
+  return v;
+}
+
+cudaError_t launch_append_chunk(const AppendChunkArgs& a, cudaStream_t stream) {
+  ACParams p;
+  p.c = chunk_view(a.chunk, *a.k);
+  p.x[0] = a.k_new; p.x[1] = a.v_new;
+  p.s_row = a.s_row; p.s_head = a.s_head;
+  p.codes[0] = a.k->codes; p.codes[1] = a.v->codes;
+  p.sz[0] = a.k->sz; p.sz[1] = a.v->sz;
+  p.status = a.status;
+  p.Hkv = a.k->Hkv;
+  const int R = 32 / (a.k->D / 32);
+  p.tiles = (a.chunk.rows + R - 1) / R;
+  p.codes_bytes = a.layout.off4 + static_cast<int64_t>(a.layout.n4) * a.k->B * a.k->Tcap * (a.k->D / 2);
+  for (int h = 0; h < KVQ_MAX_HKV; ++h) {
+    p.plane_off[h] = a.layout.plane_off[h];
+    p.bits[h] = a.layout.bits[h];
+  }
+  // one warp per (run of rows, head, K or V); grid-stride beyond 2^30 blocks
+  const int64_t warps = static_cast<int64_t>(p.tiles) * p.Hkv * 2;
+  const int64_t blocks = std::min<int64_t>((warps + 7) / 8, int64_t(1) << 30);
+  const unsigned g = static_cast<unsigned>(blocks);
+  if (a.k->D == 128) append_chunk_kernel<128><<<g, 256, 0, stream>>>(p);
+  else append_chunk_kernel<64><<<g, 256, 0, stream>>>(p);
   return cudaGetLastError();
 }
 

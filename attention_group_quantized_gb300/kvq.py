@@ -33,11 +33,18 @@ EXPORTS = ("kvq_cache_codes_bytes", "kvq_cache_sz_bytes", "kvq_cache_head_offset
            "kvq_decode_step_host", "kvq_quantize_paged", "kvq_decode_attention_paged", "kvq_decode_step_paged",
            "kvq_build_tile_mask", "kvq_prefill_attention_varlen", "kvq_head_error_stats_workspace_bytes", "kvq_head_error_stats",
            "kvq_allocate_head_bits", "kvq_status_str", "kvq_policy_default", "kvq_decode_attention_ex",
-           "kvq_prefill_attention_ex")
+           "kvq_prefill_attention_ex", "kvq_append_chunk", "kvq_append_chunk_paged", "kvq_dequantize",
+           "kvq_dequantize_paged", "kvq_chunk_workspace_bytes", "kvq_chunk_attention", "kvq_chunk_attention_paged",
+           "kvq_decode_attention_window", "kvq_decode_attention_window_paged")
 
 
 class CBlockTable(ctypes.Structure):
     _fields_ = [("pages", ctypes.c_void_p), ("B", ctypes.c_int32), ("max_pages", ctypes.c_int32)]
+
+
+class CChunk(ctypes.Structure):
+    _fields_ = [("start", ctypes.c_void_p), ("seq_lens", ctypes.c_void_p), ("B", ctypes.c_int32),
+                ("rows", ctypes.c_int32), ("max_chunk", ctypes.c_int32)]
 
 
 class KvqError(RuntimeError):
@@ -114,6 +121,25 @@ def lib() -> ctypes.CDLL:
         L.kvq_prefill_attention_ex.argtypes = [P, P, P, I32, I32, I32, I32, I32, P, I32, F32, P, I32, CP, CP, P,
                                                I32, PP, P, P]
         L.kvq_prefill_attention_ex.restype = I32
+        CH = ctypes.POINTER(CChunk)
+        L.kvq_append_chunk.argtypes = [P, P, I64, I64, CH, CP, CP, P, P]
+        L.kvq_append_chunk.restype = I32
+        L.kvq_append_chunk_paged.argtypes = [P, P, I64, I64, CH, CP, CP, BT, P, P]
+        L.kvq_append_chunk_paged.restype = I32
+        L.kvq_dequantize.argtypes = [CP, CH, P, I32, P, P]
+        L.kvq_dequantize.restype = I32
+        L.kvq_dequantize_paged.argtypes = [CP, CH, BT, P, I32, P, P]
+        L.kvq_dequantize_paged.restype = I32
+        L.kvq_chunk_workspace_bytes.argtypes = [I32, I32, I32, I32, I32]
+        L.kvq_chunk_workspace_bytes.restype = SZ
+        L.kvq_chunk_attention.argtypes = [P, I64, I64, CH, CP, CP, I32, F32, I32, I32, P, I32, P, SZ, P, P]
+        L.kvq_chunk_attention.restype = I32
+        L.kvq_chunk_attention_paged.argtypes = [P, I64, I64, CH, CP, CP, BT, I32, F32, I32, I32, P, I32, P, SZ, P, P]
+        L.kvq_chunk_attention_paged.restype = I32
+        L.kvq_decode_attention_window.argtypes = [P, CP, CP, P, I32, F32, I32, I32, P, I32, P, SZ, P, P]
+        L.kvq_decode_attention_window.restype = I32
+        L.kvq_decode_attention_window_paged.argtypes = [P, CP, CP, BT, P, I32, F32, I32, I32, P, I32, P, SZ, P, P]
+        L.kvq_decode_attention_window_paged.restype = I32
         _LIB = L
     return _LIB
 
@@ -515,3 +541,206 @@ def prefill_attention(q, k, v, k_cache: QuantCache, v_cache: QuantCache, softmax
                                                 out_dtype, status_p, _stream_ptr(stream))
         _check(st, "kvq_prefill_attention_varlen")
     return out
+
+
+# ---------------------------------------------------------------------------
+# chunks: several new tokens per sequence, packed
+# ---------------------------------------------------------------------------
+
+def _require(ok: bool, what: str):
+    if not ok:
+        raise KvqError(1, what)
+
+
+def _on_current_device(x, *others):
+    """The kernels launch on the current device: every tensor must live there."""
+    import torch
+    dev = x.device
+    if dev.type != "cuda" or dev.index != torch.cuda.current_device():
+        raise KvqError(1, f"tensors on {dev}, not on the current CUDA device")
+    for o in others:
+        if o.device != dev:
+            raise KvqError(1, f"tensors on {dev} and {o.device}")
+
+
+def _chunk(start, seq_lens, rows: int, max_chunk: Optional[int]) -> CChunk:
+    """start: device int32 [B + 1], seq_lens: device int32 [B]."""
+    import torch
+    B = seq_lens.shape[0]
+    _require(start.dtype == torch.int32 and seq_lens.dtype == torch.int32 and start.dim() == 1 and seq_lens.dim() == 1
+             and start.shape[0] == B + 1 and start.is_contiguous() and seq_lens.is_contiguous(),
+             "chunk: start int32 [B + 1] and seq_lens int32 [B], contiguous")
+    return CChunk(start.data_ptr(), seq_lens.data_ptr(), B, rows, 0 if max_chunk is None else max_chunk)
+
+
+def _packed(x, heads: int, D: int, what: str):
+    import torch
+    _require(x.dtype == torch.bfloat16 and x.dim() == 3 and x.shape[1] == heads and x.shape[2] == D
+             and x.stride(2) == 1, f"{what}: bf16 [rows][{heads}][{D}], channels contiguous")
+
+
+def _status_ptr(status):
+    return status.data_ptr() if status is not None else None
+
+
+def _out(out, shape, out_dtype: int, device, what: str):
+    import torch
+    _require(out_dtype in (OUT_F32, OUT_BF16), f"{what}: out_dtype")
+    dt = torch.float32 if out_dtype == OUT_F32 else torch.bfloat16
+    if out is None:
+        return torch.empty(shape, dtype=dt, device=device)
+    _require(tuple(out.shape) == tuple(shape) and out.dtype == dt and out.is_contiguous() and out.device == device,
+             f"{what}: out must be a contiguous {dt} {tuple(shape)} on {device}")
+    return out
+
+
+def _append_chunk(k_new, v_new, k: QuantCache, v: QuantCache, block_table, start, seq_lens, status, stream):
+    _packed(k_new, k.Hkv, k.D, "k_new")
+    _packed(v_new, k.Hkv, k.D, "v_new")
+    _on_current_device(k_new, v_new, k.codes, v.codes, start, seq_lens)
+    _require(k_new.shape[0] == v_new.shape[0] and k_new.stride() == v_new.stride(),
+             "k_new and v_new: the same rows and strides")
+    ch = _chunk(start, seq_lens, int(k_new.shape[0]), None)
+    kc, vc = k.c_struct(), v.c_struct()
+    args = [k_new.data_ptr(), v_new.data_ptr(), k_new.stride(0), k_new.stride(1), ctypes.byref(ch), ctypes.byref(kc),
+            ctypes.byref(vc)]
+    if block_table is None:
+        _check(lib().kvq_append_chunk(*args, _status_ptr(status), _stream_ptr(stream)), "kvq_append_chunk")
+    else:
+        bt = _table(block_table)
+        _check(lib().kvq_append_chunk_paged(*args, ctypes.byref(bt), _status_ptr(status), _stream_ptr(stream)),
+               "kvq_append_chunk_paged")
+
+
+def append_chunk(k_new, v_new, k: QuantCache, v: QuantCache, start, seq_lens, status=None, stream=None):
+    """Quantise packed new rows k_new/v_new bf16 [rows][Hkv][D] (row and head strides free) into the caches:
+    sequence b's rows start[b] .. start[b + 1] - 1 go to its positions seq_lens[b] - n_b .. seq_lens[b] - 1."""
+    _append_chunk(k_new, v_new, k, v, None, start, seq_lens, status, stream)
+
+
+def append_chunk_paged(k_new, v_new, k_pool: QuantCache, v_pool: QuantCache, block_table, start, seq_lens,
+                       status=None, stream=None):
+    """append_chunk into page pools through a block table."""
+    _append_chunk(k_new, v_new, k_pool, v_pool, block_table, start, seq_lens, status, stream)
+
+
+def _dequantize(cache: QuantCache, block_table, start, seq_lens, rows: int, out, out_dtype, status, stream):
+    _on_current_device(cache.codes, start, seq_lens)
+    out = _out(out, (rows, cache.Hkv, cache.D), out_dtype, cache.codes.device, "dequantize")
+    ch = _chunk(start, seq_lens, rows, None)
+    cs = cache.c_struct()
+    if block_table is None:
+        _check(lib().kvq_dequantize(ctypes.byref(cs), ctypes.byref(ch), out.data_ptr(), out_dtype,
+                                    _status_ptr(status), _stream_ptr(stream)), "kvq_dequantize")
+    else:
+        bt = _table(block_table)
+        _check(lib().kvq_dequantize_paged(ctypes.byref(cs), ctypes.byref(ch), ctypes.byref(bt), out.data_ptr(),
+                                          out_dtype, _status_ptr(status), _stream_ptr(stream)),
+               "kvq_dequantize_paged")
+    return out
+
+
+def dequantize(cache: QuantCache, start, seq_lens, rows: int, out=None, out_dtype: int = OUT_BF16, status=None,
+               stream=None):
+    """The stored values of ragged position ranges, [rows][Hkv][D]: row start[b] + i is sequence b's position
+    seq_lens[b] - n_b + i.  start = running sum of seq_lens reads whole sequences."""
+    return _dequantize(cache, None, start, seq_lens, rows, out, out_dtype, status, stream)
+
+
+def dequantize_paged(pool: QuantCache, block_table, start, seq_lens, rows: int, out=None, out_dtype: int = OUT_BF16,
+                     status=None, stream=None):
+    """dequantize from a page pool through a block table."""
+    return _dequantize(pool, block_table, start, seq_lens, rows, out, out_dtype, status, stream)
+
+
+def chunk_workspace_bytes(rows: int, B: int, Hq: int, Hkv: int, D: int) -> int:
+    return int(lib().kvq_chunk_workspace_bytes(rows, B, Hq, Hkv, D))
+
+
+def chunk_workspace(rows: int, B: int, Hq: int, Hkv: int, D: int, device="cuda"):
+    """A zero-filled workspace for chunk_attention over up to `rows` packed rows of B sequences."""
+    import torch
+    return torch.zeros(max(chunk_workspace_bytes(rows, B, Hq, Hkv, D), 16), dtype=torch.uint8, device=device)
+
+
+def _chunk_attention(q, k: QuantCache, v: QuantCache, block_table, start, seq_lens, softmax_scale, window, sinks, out,
+                     out_dtype, workspace, max_chunk, status, stream):
+    _require(q.dim() == 3, "q: bf16 [rows][Hq][D]")
+    rows, Hq, D = q.shape
+    _packed(q, Hq, k.D, "q")
+    _on_current_device(q, k.codes, v.codes, start, seq_lens)
+    out = _out(out, (rows, Hq, D), out_dtype, q.device, "chunk_attention")
+    if workspace is None:
+        workspace = chunk_workspace(rows, int(seq_lens.shape[0]), Hq, k.Hkv, D, q.device)
+    ch = _chunk(start, seq_lens, rows, max_chunk)
+    kc, vc = k.c_struct(), v.c_struct()
+    head = [q.data_ptr(), q.stride(0), q.stride(1), ctypes.byref(ch), ctypes.byref(kc), ctypes.byref(vc)]
+    tail = [Hq, float(softmax_scale), window, sinks, out.data_ptr(), out_dtype, workspace.data_ptr(),
+            workspace.numel() * workspace.element_size(), _status_ptr(status), _stream_ptr(stream)]
+    if block_table is None:
+        _check(lib().kvq_chunk_attention(*head, *tail), "kvq_chunk_attention")
+    else:
+        bt = _table(block_table)
+        _check(lib().kvq_chunk_attention_paged(*head, ctypes.byref(bt), *tail), "kvq_chunk_attention_paged")
+    return out
+
+
+def chunk_attention(q, k: QuantCache, v: QuantCache, start, seq_lens, softmax_scale: float = 0.0, window: int = 0,
+                    sinks: int = 0, out=None, out_dtype: int = OUT_F32, workspace=None,
+                    max_chunk: Optional[int] = None, status=None, stream=None):
+    """Attention of packed new tokens q bf16 [rows][Hq][D] over caches that already hold them (append_chunk first);
+    causal by cache position, optionally with a window of `window` tokens and the first `sinks` ones.
+    max_chunk: most rows of one sequence, if the caller knows it (chooses the kernel); returns [rows][Hq][D]."""
+    return _chunk_attention(q, k, v, None, start, seq_lens, softmax_scale, window, sinks, out, out_dtype, workspace,
+                            max_chunk, status, stream)
+
+
+def chunk_attention_paged(q, k_pool: QuantCache, v_pool: QuantCache, block_table, start, seq_lens,
+                          softmax_scale: float = 0.0, window: int = 0, sinks: int = 0, out=None,
+                          out_dtype: int = OUT_F32, workspace=None, max_chunk: Optional[int] = None, status=None,
+                          stream=None):
+    """chunk_attention over page pools through a block table."""
+    return _chunk_attention(q, k_pool, v_pool, block_table, start, seq_lens, softmax_scale, window, sinks, out,
+                            out_dtype, workspace, max_chunk, status, stream)
+
+
+def _decode_window(q, k: QuantCache, v: QuantCache, block_table, seq_lens, window, sinks, softmax_scale, out,
+                   out_dtype, workspace, status, stream):
+    import torch
+    _require(q.dim() == 3 and q.dtype == torch.bfloat16 and q.is_contiguous() and q.shape[2] == k.D,
+             "q: contiguous bf16 [B][Hq][D]")
+    B, Hq, D = q.shape
+    _require(seq_lens.dtype == torch.int32 and seq_lens.is_contiguous() and tuple(seq_lens.shape) == (B,)
+             and B == (k.B if block_table is None else block_table.shape[0]), "seq_lens: int32 [B]")
+    _on_current_device(q, k.codes, v.codes, seq_lens)
+    out = _out(out, (B, Hq, D), out_dtype, q.device, "decode_attention_window")
+    if workspace is None:
+        workspace = decode_workspace(B, Hq, k.Hkv, D, q.device)
+    kc, vc = k.c_struct(), v.c_struct()
+    head = [q.data_ptr(), ctypes.byref(kc), ctypes.byref(vc)]
+    tail = [seq_lens.data_ptr(), Hq, float(softmax_scale), window, sinks, out.data_ptr(), out_dtype,
+            workspace.data_ptr(), workspace.numel() * workspace.element_size(), _status_ptr(status),
+            _stream_ptr(stream)]
+    if block_table is None:
+        _check(lib().kvq_decode_attention_window(*head, *tail), "kvq_decode_attention_window")
+    else:
+        bt = _table(block_table)
+        _check(lib().kvq_decode_attention_window_paged(*head, ctypes.byref(bt), *tail),
+               "kvq_decode_attention_window_paged")
+    return out
+
+
+def decode_attention_window(q, k: QuantCache, v: QuantCache, seq_lens, window: int, sinks: int = 0,
+                            softmax_scale: float = 0.0, out=None, out_dtype: int = OUT_F32, workspace=None,
+                            status=None, stream=None):
+    """decode_attention over the last `window` tokens of each sequence and its first `sinks` ones (window 0: all)."""
+    return _decode_window(q, k, v, None, seq_lens, window, sinks, softmax_scale, out, out_dtype, workspace, status,
+                          stream)
+
+
+def decode_attention_window_paged(q, k_pool: QuantCache, v_pool: QuantCache, block_table, seq_lens, window: int,
+                                  sinks: int = 0, softmax_scale: float = 0.0, out=None, out_dtype: int = OUT_F32,
+                                  workspace=None, status=None, stream=None):
+    """decode_attention_window over page pools through a block table."""
+    return _decode_window(q, k_pool, v_pool, block_table, seq_lens, window, sinks, softmax_scale, out, out_dtype,
+                          workspace, status, stream)

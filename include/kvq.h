@@ -474,6 +474,120 @@ KVQ_API kvq_status kvq_prefill_attention_ex(const void* q, const void* k, const 
                                             void* out, int32_t out_dtype, const kvq_policy* policy,
                                             int32_t* dev_status, void* stream);
 
+/*
+ * kvq_chunk -- a ragged batch of new tokens, packed: sequence b's n_b =
+ * start[b + 1] - start[b] new tokens are rows start[b] .. start[b + 1] - 1 of
+ * the caller's row buffers and cache positions seq_lens[b] - n_b ..
+ * seq_lens[b] - 1, in order (as in kvq_decode_step, a length INCLUDES the new
+ * tokens).  start[0] .. start[B] ascend from 0 to at most `rows`; a sequence
+ * may have no new token.  The calls that take a chunk read both arrays on the
+ * device.  A sequence with start[b] < 0, start[b + 1] < start[b],
+ * start[b + 1] > rows, n_b > max_chunk, seq_lens[b] < n_b or seq_lens[b]
+ * beyond the cache's capacity reports KVQ_ERR_INVALID_ARG in dev_status and is
+ * left out: nothing of it is read or written.
+ * Rows that belong to no sequence (from start[B] on) are left as they are.
+ */
+typedef struct kvq_chunk {
+  const int32_t* start;      /* device int32 [B + 1], 4-byte aligned */
+  const int32_t* seq_lens;   /* device int32 [B], 4-byte aligned */
+  int32_t B;                 /* sequences, 1 .. 4096; the cache's B, or the block table's */
+  int32_t rows;              /* rows of the caller's packed buffers */
+  int32_t max_chunk;         /* most new tokens of one sequence; 0 = rows.  Chunk attention chooses its kernel by it. */
+} kvq_chunk;
+
+/*
+ * kvq_append_chunk -- quantise-on-write of a chunk (several new tokens per
+ * sequence, each sequence at its own position), K and V in one launch; each
+ * row is quantised exactly as kvq_quantize does it.
+ *
+ * k_new, v_new: device bf16, channel d of (row r, KV head h) at
+ *   x[r * s_row + h * s_head + d] (element strides, multiples of 8; channels
+ *   contiguous; 16-byte aligned base), the same strides for both -- rows of a
+ *   fused projection's output can be passed in place.
+ * k, v: caches with identical B, Hkv, Tcap, D and head_bits.
+ * Positions other than the chunk's keep their contents.  Non-finite input as
+ * in kvq_quantize.
+ */
+KVQ_API kvq_status kvq_append_chunk(const void* k_new, const void* v_new, int64_t s_row, int64_t s_head,
+                                    const kvq_chunk* chunk, const kvq_cache* k, const kvq_cache* v,
+                                    int32_t* dev_status, void* stream);
+/* The same into page pools; a row whose page id lies outside the pool reports
+ * KVQ_ERR_INVALID_ARG and is not written. */
+KVQ_API kvq_status kvq_append_chunk_paged(const void* k_new, const void* v_new, int64_t s_row, int64_t s_head,
+                                          const kvq_chunk* chunk, const kvq_cache* k_pool, const kvq_cache* v_pool,
+                                          const kvq_block_table* table, int32_t* dev_status, void* stream);
+
+/*
+ * kvq_dequantize -- the cache read back: row r of the chunk description gets
+ * the stored values (c - z) * s of its cache position (the difference is
+ * exact; one rounding, to out's type), for every KV head.  With start the
+ * running sum of seq_lens it reads whole sequences.
+ * out: device [rows][Hkv][D], contiguous, 16-byte aligned, fp32 or bf16.
+ */
+KVQ_API kvq_status kvq_dequantize(const kvq_cache* src, const kvq_chunk* chunk, void* out, int32_t out_dtype,
+                                  int32_t* dev_status, void* stream);
+/* The same from a page pool; a row whose page id lies outside the pool reports
+ * KVQ_ERR_INVALID_ARG and is written as zeros. */
+KVQ_API kvq_status kvq_dequantize_paged(const kvq_cache* pool, const kvq_chunk* chunk, const kvq_block_table* table,
+                                        void* out, int32_t out_dtype, int32_t* dev_status, void* stream);
+
+/*
+ * kvq_chunk_attention -- attention of a chunk of new tokens over caches that
+ * already hold them (kvq_append_chunk or kvq_quantize before it on the same
+ * stream): prompt chunks, verification of several drafted tokens, or a batch
+ * that mixes both with single tokens.  The query of row r, at cache position
+ * p, attends its sequence's tokens j <= p; with window > 0 only those with
+ * j > p - window or j < sinks (the last `window` tokens, itself among them,
+ * and the first `sinks` ones).
+ *
+ * q: device bf16, channel d of (row r, query head h) at
+ *   q[r * sq_row + h * sq_head + d] (element strides, multiples of 8; channels
+ *   contiguous; 16-byte aligned base; |q| < 65504, as kvq_decode_attention).
+ * Hq % Hkv == 0, Hq / Hkv <= 128.  window >= 0 (0: none), sinks >= 0.
+ * out: device [rows][Hq][D], contiguous, 16-byte aligned, fp32 or bf16.
+ * workspace: device scratch of >= kvq_chunk_workspace_bytes(rows, B, Hq, Hkv,
+ *   D) bytes, with kvq_decode_attention's rules (16-byte aligned, zero-filled
+ *   once before its first use, calls that share it ordered on the GPU).
+ * Cache tokens that no query of the call sees are not read into the result
+ * (they may hold anything).  Errors and other arguments as
+ * kvq_decode_attention.
+ */
+KVQ_API size_t kvq_chunk_workspace_bytes(int32_t rows, int32_t B, int32_t Hq, int32_t Hkv, int32_t D);
+KVQ_API kvq_status kvq_chunk_attention(const void* q, int64_t sq_row, int64_t sq_head, const kvq_chunk* chunk,
+                                       const kvq_cache* k, const kvq_cache* v, int32_t Hq, float softmax_scale,
+                                       int32_t window, int32_t sinks, void* out, int32_t out_dtype,
+                                       void* workspace, size_t workspace_bytes, int32_t* dev_status, void* stream);
+/* The same over page pools.  Pages that hold no visible token may be anything;
+ * a visible one outside the pool reports KVQ_ERR_INVALID_ARG and page 0 is
+ * read instead. */
+KVQ_API kvq_status kvq_chunk_attention_paged(const void* q, int64_t sq_row, int64_t sq_head, const kvq_chunk* chunk,
+                                             const kvq_cache* k_pool, const kvq_cache* v_pool,
+                                             const kvq_block_table* table, int32_t Hq, float softmax_scale,
+                                             int32_t window, int32_t sinks, void* out, int32_t out_dtype,
+                                             void* workspace, size_t workspace_bytes, int32_t* dev_status,
+                                             void* stream);
+
+/*
+ * kvq_decode_attention_window -- kvq_decode_attention with a sliding window:
+ * sequence b's query, at position len_b - 1, attends tokens j >= len_b -
+ * window and j < min(sinks, len_b).  Only the 64-token tiles that hold such
+ * tokens are read; tokens outside them may hold anything.  window == 0: every
+ * token (kvq_decode_attention).  window, sinks >= 0.  Other arguments, the
+ * workspace and errors as kvq_decode_attention.
+ */
+KVQ_API kvq_status kvq_decode_attention_window(const void* q, const kvq_cache* k, const kvq_cache* v,
+                                               const int32_t* seq_lens, int32_t Hq, float softmax_scale,
+                                               int32_t window, int32_t sinks, void* out, int32_t out_dtype,
+                                               void* workspace, size_t workspace_bytes, int32_t* dev_status,
+                                               void* stream);
+/* The same over page pools (kvq_decode_attention_paged); block-table entries
+ * of tiles without a visible token are not used. */
+KVQ_API kvq_status kvq_decode_attention_window_paged(const void* q, const kvq_cache* k_pool, const kvq_cache* v_pool,
+                                                     const kvq_block_table* table, const int32_t* seq_lens,
+                                                     int32_t Hq, float softmax_scale, int32_t window, int32_t sinks,
+                                                     void* out, int32_t out_dtype, void* workspace,
+                                                     size_t workspace_bytes, int32_t* dev_status, void* stream);
+
 /* Static, human-readable name of a status code. */
 KVQ_API const char* kvq_status_str(kvq_status status);
 
