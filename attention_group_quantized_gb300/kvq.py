@@ -149,10 +149,25 @@ def _check(status: int, what: str):
         raise KvqError(status, what)
 
 
+_TORCH = None
+
+
+def _torch():
+    """torch, imported on first use (an import statement in every call costs more than this)."""
+    global _TORCH
+    if _TORCH is None:
+        import torch
+        _TORCH = torch
+    return _TORCH
+
+
 def _stream_ptr(stream) -> Optional[int]:
-    import torch
-    s = stream if stream is not None else torch.cuda.current_stream()
-    return s.cuda_stream
+    if stream is not None:
+        return stream.cuda_stream
+    torch = _torch()
+    # the current stream's handle without building a Stream object (0.1 us instead of 3 us of host time)
+    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+    return raw(torch.cuda.current_device()) if raw is not None else torch.cuda.current_stream().cuda_stream
 
 
 @dataclass
@@ -546,70 +561,80 @@ def prefill_attention(q, k, v, k_cache: QuantCache, v_cache: QuantCache, softmax
 # ---------------------------------------------------------------------------
 # chunks: several new tokens per sequence, packed
 # ---------------------------------------------------------------------------
+# (These calls run every few microseconds in a serving loop: the checks below
+# format nothing unless they fail.)
 
-def _require(ok: bool, what: str):
-    if not ok:
-        raise KvqError(1, what)
+def _bad(what: str):
+    raise KvqError(1, what)
 
 
 def _on_current_device(x, *others):
     """The kernels launch on the current device: every tensor must live there."""
-    import torch
-    dev = x.device
-    if dev.type != "cuda" or dev.index != torch.cuda.current_device():
-        raise KvqError(1, f"tensors on {dev}, not on the current CUDA device")
+    i = x.get_device()
+    if i < 0 or i != _torch().cuda.current_device():
+        _bad("tensors that are not on the current CUDA device")
     for o in others:
-        if o.device != dev:
-            raise KvqError(1, f"tensors on {dev} and {o.device}")
+        if o.get_device() != i:
+            _bad("tensors on different devices")
 
 
 def _chunk(start, seq_lens, rows: int, max_chunk: Optional[int]) -> CChunk:
     """start: device int32 [B + 1], seq_lens: device int32 [B]."""
-    import torch
-    B = seq_lens.shape[0]
-    _require(start.dtype == torch.int32 and seq_lens.dtype == torch.int32 and start.dim() == 1 and seq_lens.dim() == 1
-             and start.shape[0] == B + 1 and start.is_contiguous() and seq_lens.is_contiguous(),
-             "chunk: start int32 [B + 1] and seq_lens int32 [B], contiguous")
-    return CChunk(start.data_ptr(), seq_lens.data_ptr(), B, rows, 0 if max_chunk is None else max_chunk)
+    i32 = _torch().int32
+    if (start.dtype != i32 or seq_lens.dtype != i32 or start.dim() != 1 or seq_lens.dim() != 1
+            or start.shape[0] != seq_lens.shape[0] + 1 or not start.is_contiguous() or not seq_lens.is_contiguous()):
+        _bad("chunk: start int32 [B + 1] and seq_lens int32 [B], contiguous")
+    return CChunk(start.data_ptr(), seq_lens.data_ptr(), seq_lens.shape[0], rows, 0 if max_chunk is None else max_chunk)
+
+
+def _block_table(block_table):
+    """The C view of a block table (device int32 [B][max_pages], contiguous), None for None."""
+    if block_table is None:
+        return None
+    if block_table.dtype != _torch().int32 or block_table.dim() != 2 or not block_table.is_contiguous():
+        _bad("block_table: int32 [B][max_pages], contiguous")
+    return CBlockTable(block_table.data_ptr(), block_table.shape[0], block_table.shape[1])
 
 
 def _packed(x, heads: int, D: int, what: str):
-    import torch
-    _require(x.dtype == torch.bfloat16 and x.dim() == 3 and x.shape[1] == heads and x.shape[2] == D
-             and x.stride(2) == 1, f"{what}: bf16 [rows][{heads}][{D}], channels contiguous")
+    if x.dtype != _torch().bfloat16 or x.dim() != 3 or x.shape[1] != heads or x.shape[2] != D or x.stride(2) != 1:
+        _bad(f"{what}: bf16 [rows][{heads}][{D}], channels contiguous")
 
 
 def _status_ptr(status):
-    return status.data_ptr() if status is not None else None
+    return None if status is None else status.data_ptr()
 
 
-def _out(out, shape, out_dtype: int, device, what: str):
-    import torch
-    _require(out_dtype in (OUT_F32, OUT_BF16), f"{what}: out_dtype")
+def _out(out, shape, out_dtype: int, like, what: str):
+    torch = _torch()
+    if out_dtype != OUT_F32 and out_dtype != OUT_BF16:
+        _bad(f"{what}: out_dtype")
     dt = torch.float32 if out_dtype == OUT_F32 else torch.bfloat16
     if out is None:
-        return torch.empty(shape, dtype=dt, device=device)
-    _require(tuple(out.shape) == tuple(shape) and out.dtype == dt and out.is_contiguous() and out.device == device,
-             f"{what}: out must be a contiguous {dt} {tuple(shape)} on {device}")
+        return torch.empty(shape, dtype=dt, device=like.device)
+    if tuple(out.shape) != shape or out.dtype != dt or not out.is_contiguous() or out.get_device() != like.get_device():
+        _bad(f"{what}: out must be contiguous {dt} {shape} on the inputs' device")
     return out
 
 
 def _append_chunk(k_new, v_new, k: QuantCache, v: QuantCache, block_table, start, seq_lens, status, stream):
     _packed(k_new, k.Hkv, k.D, "k_new")
     _packed(v_new, k.Hkv, k.D, "v_new")
+    if k_new.shape[0] != v_new.shape[0] or k_new.stride() != v_new.stride():
+        _bad("k_new and v_new: the same rows and strides")
+    bt = _block_table(block_table)
     _on_current_device(k_new, v_new, k.codes, v.codes, start, seq_lens)
-    _require(k_new.shape[0] == v_new.shape[0] and k_new.stride() == v_new.stride(),
-             "k_new and v_new: the same rows and strides")
-    ch = _chunk(start, seq_lens, int(k_new.shape[0]), None)
-    kc, vc = k.c_struct(), v.c_struct()
-    args = [k_new.data_ptr(), v_new.data_ptr(), k_new.stride(0), k_new.stride(1), ctypes.byref(ch), ctypes.byref(kc),
-            ctypes.byref(vc)]
-    if block_table is None:
-        _check(lib().kvq_append_chunk(*args, _status_ptr(status), _stream_ptr(stream)), "kvq_append_chunk")
+    ch = _chunk(start, seq_lens, k_new.shape[0], None)
+    s_row, s_head, _ = k_new.stride()
+    if bt is None:
+        st = lib().kvq_append_chunk(k_new.data_ptr(), v_new.data_ptr(), s_row, s_head, ch, k.c_struct(), v.c_struct(),
+                                    _status_ptr(status), _stream_ptr(stream))
+        _check(st, "kvq_append_chunk")
     else:
-        bt = _table(block_table)
-        _check(lib().kvq_append_chunk_paged(*args, ctypes.byref(bt), _status_ptr(status), _stream_ptr(stream)),
-               "kvq_append_chunk_paged")
+        _on_current_device(block_table)
+        st = lib().kvq_append_chunk_paged(k_new.data_ptr(), v_new.data_ptr(), s_row, s_head, ch, k.c_struct(),
+                                          v.c_struct(), bt, _status_ptr(status), _stream_ptr(stream))
+        _check(st, "kvq_append_chunk_paged")
 
 
 def append_chunk(k_new, v_new, k: QuantCache, v: QuantCache, start, seq_lens, status=None, stream=None):
@@ -625,18 +650,19 @@ def append_chunk_paged(k_new, v_new, k_pool: QuantCache, v_pool: QuantCache, blo
 
 
 def _dequantize(cache: QuantCache, block_table, start, seq_lens, rows: int, out, out_dtype, status, stream):
+    bt = _block_table(block_table)
     _on_current_device(cache.codes, start, seq_lens)
-    out = _out(out, (rows, cache.Hkv, cache.D), out_dtype, cache.codes.device, "dequantize")
+    out = _out(out, (rows, cache.Hkv, cache.D), out_dtype, cache.codes, "dequantize")
     ch = _chunk(start, seq_lens, rows, None)
-    cs = cache.c_struct()
-    if block_table is None:
-        _check(lib().kvq_dequantize(ctypes.byref(cs), ctypes.byref(ch), out.data_ptr(), out_dtype,
-                                    _status_ptr(status), _stream_ptr(stream)), "kvq_dequantize")
+    if bt is None:
+        st = lib().kvq_dequantize(cache.c_struct(), ch, out.data_ptr(), out_dtype, _status_ptr(status),
+                                  _stream_ptr(stream))
+        _check(st, "kvq_dequantize")
     else:
-        bt = _table(block_table)
-        _check(lib().kvq_dequantize_paged(ctypes.byref(cs), ctypes.byref(ch), ctypes.byref(bt), out.data_ptr(),
-                                          out_dtype, _status_ptr(status), _stream_ptr(stream)),
-               "kvq_dequantize_paged")
+        _on_current_device(block_table)
+        st = lib().kvq_dequantize_paged(cache.c_struct(), ch, bt, out.data_ptr(), out_dtype, _status_ptr(status),
+                                        _stream_ptr(stream))
+        _check(st, "kvq_dequantize_paged")
     return out
 
 
@@ -665,23 +691,29 @@ def chunk_workspace(rows: int, B: int, Hq: int, Hkv: int, D: int, device="cuda")
 
 def _chunk_attention(q, k: QuantCache, v: QuantCache, block_table, start, seq_lens, softmax_scale, window, sinks, out,
                      out_dtype, workspace, max_chunk, status, stream):
-    _require(q.dim() == 3, "q: bf16 [rows][Hq][D]")
+    if q.dim() != 3:
+        _bad("q: bf16 [rows][Hq][D]")
     rows, Hq, D = q.shape
     _packed(q, Hq, k.D, "q")
+    bt = _block_table(block_table)
     _on_current_device(q, k.codes, v.codes, start, seq_lens)
-    out = _out(out, (rows, Hq, D), out_dtype, q.device, "chunk_attention")
+    out = _out(out, (rows, Hq, D), out_dtype, q, "chunk_attention")
     if workspace is None:
         workspace = chunk_workspace(rows, int(seq_lens.shape[0]), Hq, k.Hkv, D, q.device)
     ch = _chunk(start, seq_lens, rows, max_chunk)
-    kc, vc = k.c_struct(), v.c_struct()
-    head = [q.data_ptr(), q.stride(0), q.stride(1), ctypes.byref(ch), ctypes.byref(kc), ctypes.byref(vc)]
-    tail = [Hq, float(softmax_scale), window, sinks, out.data_ptr(), out_dtype, workspace.data_ptr(),
-            workspace.numel() * workspace.element_size(), _status_ptr(status), _stream_ptr(stream)]
-    if block_table is None:
-        _check(lib().kvq_chunk_attention(*head, *tail), "kvq_chunk_attention")
+    s_row, s_head, _ = q.stride()
+    ws_n = workspace.numel() * workspace.element_size()
+    if bt is None:
+        st = lib().kvq_chunk_attention(q.data_ptr(), s_row, s_head, ch, k.c_struct(), v.c_struct(), Hq, softmax_scale,
+                                       window, sinks, out.data_ptr(), out_dtype, workspace.data_ptr(), ws_n,
+                                       _status_ptr(status), _stream_ptr(stream))
+        _check(st, "kvq_chunk_attention")
     else:
-        bt = _table(block_table)
-        _check(lib().kvq_chunk_attention_paged(*head, ctypes.byref(bt), *tail), "kvq_chunk_attention_paged")
+        _on_current_device(block_table)
+        st = lib().kvq_chunk_attention_paged(q.data_ptr(), s_row, s_head, ch, k.c_struct(), v.c_struct(), bt, Hq,
+                                             softmax_scale, window, sinks, out.data_ptr(), out_dtype,
+                                             workspace.data_ptr(), ws_n, _status_ptr(status), _stream_ptr(stream))
+        _check(st, "kvq_chunk_attention_paged")
     return out
 
 
@@ -706,27 +738,31 @@ def chunk_attention_paged(q, k_pool: QuantCache, v_pool: QuantCache, block_table
 
 def _decode_window(q, k: QuantCache, v: QuantCache, block_table, seq_lens, window, sinks, softmax_scale, out,
                    out_dtype, workspace, status, stream):
-    import torch
-    _require(q.dim() == 3 and q.dtype == torch.bfloat16 and q.is_contiguous() and q.shape[2] == k.D,
-             "q: contiguous bf16 [B][Hq][D]")
+    torch = _torch()
+    if q.dim() != 3 or q.dtype != torch.bfloat16 or not q.is_contiguous() or q.shape[2] != k.D:
+        _bad("q: contiguous bf16 [B][Hq][D]")
     B, Hq, D = q.shape
-    _require(seq_lens.dtype == torch.int32 and seq_lens.is_contiguous() and tuple(seq_lens.shape) == (B,)
-             and B == (k.B if block_table is None else block_table.shape[0]), "seq_lens: int32 [B]")
+    bt = _block_table(block_table)
+    if (seq_lens.dtype != torch.int32 or seq_lens.dim() != 1 or seq_lens.shape[0] != B or not seq_lens.is_contiguous()
+            or B != (k.B if bt is None else bt.B)):
+        _bad("seq_lens: int32 [B]")
     _on_current_device(q, k.codes, v.codes, seq_lens)
-    out = _out(out, (B, Hq, D), out_dtype, q.device, "decode_attention_window")
+    out = _out(out, (B, Hq, D), out_dtype, q, "decode_attention_window")
     if workspace is None:
         workspace = decode_workspace(B, Hq, k.Hkv, D, q.device)
-    kc, vc = k.c_struct(), v.c_struct()
-    head = [q.data_ptr(), ctypes.byref(kc), ctypes.byref(vc)]
-    tail = [seq_lens.data_ptr(), Hq, float(softmax_scale), window, sinks, out.data_ptr(), out_dtype,
-            workspace.data_ptr(), workspace.numel() * workspace.element_size(), _status_ptr(status),
-            _stream_ptr(stream)]
-    if block_table is None:
-        _check(lib().kvq_decode_attention_window(*head, *tail), "kvq_decode_attention_window")
+    ws_n = workspace.numel() * workspace.element_size()
+    if bt is None:
+        st = lib().kvq_decode_attention_window(q.data_ptr(), k.c_struct(), v.c_struct(), seq_lens.data_ptr(), Hq,
+                                               softmax_scale, window, sinks, out.data_ptr(), out_dtype,
+                                               workspace.data_ptr(), ws_n, _status_ptr(status), _stream_ptr(stream))
+        _check(st, "kvq_decode_attention_window")
     else:
-        bt = _table(block_table)
-        _check(lib().kvq_decode_attention_window_paged(*head, ctypes.byref(bt), *tail),
-               "kvq_decode_attention_window_paged")
+        _on_current_device(block_table)
+        st = lib().kvq_decode_attention_window_paged(q.data_ptr(), k.c_struct(), v.c_struct(), bt,
+                                                     seq_lens.data_ptr(), Hq, softmax_scale, window, sinks,
+                                                     out.data_ptr(), out_dtype, workspace.data_ptr(), ws_n,
+                                                     _status_ptr(status), _stream_ptr(stream))
+        _check(st, "kvq_decode_attention_window_paged")
     return out
 
 
