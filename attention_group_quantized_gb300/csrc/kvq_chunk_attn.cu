@@ -1,108 +1,963 @@
 // kvq_chunk_attn.cu -- attention of a chunk of new tokens over the
-// group-quantised cache: the query of packed row r, at cache position p,
-// attends tokens j <= p of its sequence, with a window only j > p - window or
-// j < sinks.
+// group-quantised cache, on the 5th-generation tensor cores.
 //
-// One warp per (packed row, query head): the lanes hold the query's channels
-// and walk the visible keys with an online softmax.
+// Method: the query of packed row r, at cache position p, attends tokens
+// j <= p of its sequence, with a window only j > p - window or j < sinks; the
+// cache holds integer codes with a scale and a zero point per 32 channels
+// (《分块稀疏注意力与KV Cache量化：长文本推理显存优化实践》 §2.4), dequantised inside
+// the attention read (§1.3); the keys are visited in 128-token tiles with an
+// online softmax (§2.2).
+//
+// Work: the query heads that share a KV head are packed with the chunk's
+// tokens into one list of rows (row = token * rep + head), so every
+// dequantised K/V tile serves them all; 256 rows (two slots of 128, one
+// tcgen05 tile each) are a segment's rows, and the key tiles that any of them
+// sees its tiles.  The list of all (sequence, KV head, row block, key tile) is
+// cut into equal ranges, one per persistent CTA ("stream-K"): ragged lengths
+// and few rows over a long cache load every SM alike.  A segment that is cut
+// leaves one partial (o, lse) per piece in the workspace, and the CTA that
+// completes it merges them in a fixed order.
+//
+// One CTA (512 threads, one per SM):
+//   warp 0      allocates TMEM and frees it once every other role is done;
+//   warps 1, 2  issue slot h = warp - 1's tcgen05.mma (S_h = Q_h K^T from
+//               shared memory, O_h += P_h V with P from TMEM), taking turns so
+//               that one slot's softmax runs under the other's products;
+//   warps 4-7   per piece, its query rows to fp16; per key tile, K and V codes
+//               to fp16 operand tiles (two stages), the next part's codes in
+//               flight in registers meanwhile;
+//   warps 8-15  softmax of slot 0 and slot 1, one thread per row; at a piece's
+//               end O / sum to the output or the workspace.
+// TMEM (512 columns): S_0 [0,128) O_0 [128,128+D) S_1 [256,384) O_1 [384,384+D).
+// The running max only moves (and O is rescaled) when it grows by more than
+// 2^8; P is rounded to fp16, sums and O stay in fp32.
 #include <cmath>
+#include <cstring>
+#include <mutex>
 
 #include "kvq_chunk.cuh"
 #include "kvq_internal.h"
+#include "kvq_tc.cuh"
+#include "kvq_tile.cuh"
 
 namespace kvq {
 namespace {
+
+using namespace tile;
+
+constexpr int kThreads = 512;
+constexpr int kRows = 2 * kT;          // packed rows per segment
+constexpr uint32_t kTmemCols = 512;
+constexpr float kRescaleThreshold = 8.0f;  // log2 units
+constexpr uint64_t kWaitNs = kDefaultWaitLimitNs;
 
 struct CParams {
   chunk::View c;
   const uint16_t* q;
   int64_t sq_row, sq_head;
-  const uint8_t* codes[2];
+  const uint8_t* codes[2];          // K, V code buffers
   const uint32_t* sz[2];
+  int32_t* cnt;                     // [CTAs][2] arrivals at a cut segment, by its first CTA and slot
+  float* ws_lse;                    // [2 * CTAs][slot_rows], log2 domain
+  float* ws_o;                      // [2 * CTAs][slot_rows][D]
   void* out;
   int32_t* status;
-  int32_t out_dtype, Hq, Hkv, window, sinks;
+  int32_t out_dtype, Hq, Hkv, rep, window, sinks, num_ctas, slot_rows;
   float scale_log2;
+  int64_t codes_bytes;              // size of each code buffer (the debug build's index checks)
   int64_t plane_off[KVQ_MAX_HKV];
   int8_t bits[KVQ_MAX_HKV];
 };
 
-// CPL consecutive channels (a lane's share) of one stored row
+enum {
+  B_QREADY = 0, B_QEMPTY, B_KFULL0, B_KFULL1, B_VFULL0, B_VFULL1, B_KVEMPTY0, B_KVEMPTY1, B_SFULL0, B_SFULL1,
+  B_PFIRST0, B_PFIRST1, B_PFULL0, B_PFULL1, B_ORDY0, B_ORDY1, B_OFREE0, B_OFREE1, B_TURN0, B_TURN1, B_GROUP0, B_GROUP1,
+  B_MMADONE, B_EXIT, B_COUNT
+};
+// Every warp but warp 0 arrives once on B_EXIT when it is done with shared
+// memory, TMEM and its asynchronous operations, on the normal path and after
+// a timed-out wait alike; warp 0 frees TMEM only after that.
+constexpr int kExitArrivals = kThreads / 32 - 1;
+
 template <int D>
-__device__ __forceinline__ void lane_values(float (&x)[D / 32], const CParams& p, int which, int h, int64_t row,
-                                            int lane) {
-  constexpr int N = D / 32;
-  const int bits = p.bits[h];
-  const int64_t storage = static_cast<int64_t>(p.c.pB) * p.c.pT;
-  const uint32_t word = p.sz[which][(h * storage + row) * N + lane * N / 32];
-  const uint8_t* c = p.codes[which] + p.plane_off[h] + row * (D * bits / 8) + lane * N * bits / 8;
+struct CLayout {
+  static constexpr int kQBytes = kT * D * 2;            // one slot's fp16 rows / one K or V tile
+  static constexpr int kOffQ = 0;                       // 2 slots
+  static constexpr int kOffK = kOffQ + 2 * kQBytes;     // 2 stages
+  static constexpr int kOffV = kOffK + 2 * kQBytes;     // 2 stages
+  static constexpr int kOffBar = kOffV + 2 * kQBytes;
+  static constexpr int kOffMisc = kOffBar + B_COUNT * 8;  // TMEM address, merge flags
+  static constexpr int kOffPre = kOffMisc + 16;           // int64 [B + 1]
+  static size_t bytes(int B) { return 1024 + kOffPre + static_cast<size_t>(B + 1) * 8; }
+};
+
+// A segment's key tiles: those that some row of the block sees, in order.
+// Index i of the list is tile (i < ns ? i : i + skip).
+struct Tiles {
+  int n, ns, skip;
+  int pos_lo, pos_hi;    // positions of the block's first and last row
+  int rows;              // its rows
+  __device__ __forceinline__ int tile(int i) const { return i < ns ? i : i + skip; }
+};
+__device__ __forceinline__ Tiles segment_tiles(const CParams& p, const chunk::Seq& s, int rt) {
+  Tiles t;
+  t.rows = min(kRows, s.n * p.rep - rt * kRows);
+  t.pos_lo = s.len - s.n + rt * kRows / p.rep;
+  t.pos_hi = s.len - s.n + (rt * kRows + t.rows - 1) / p.rep;
+  t.n = t.pos_hi / kT + 1;
+  t.ns = t.skip = 0;
+  if (p.window > 0) {
+    const int fw = max(t.pos_lo - p.window + 1, 0) / kT;
+    t.ns = min((min(p.sinks, t.pos_hi + 1) + kT - 1) / kT, fw);
+    t.skip = fw - t.ns;
+    t.n -= t.skip;
+  }
+  return t;
+}
+__device__ __forceinline__ int row_blocks(const CParams& p, const chunk::Seq& s) {
+  return (s.n * p.rep + kRows - 1) / kRows;
+}
+
+// A CTA's walk through its range of the work list, piece by piece.
+struct Walk {
+  int64_t f;             // flat index of the piece's first tile
+  int64_t left;          // tiles of the range from there on
+  int b, kvh, rt, i;     // the piece starts at tile index i of this segment
+  chunk::Seq s;
+  Tiles t;
+  int n;                 // tiles of the piece
+};
+
+__device__ __forceinline__ void open_piece(const CParams& p, Walk& w) {
+  w.t = segment_tiles(p, w.s, w.rt);
+  w.n = static_cast<int>(min(static_cast<int64_t>(w.t.n - w.i), w.left));
+}
+// To the next piece; false at the range's end.
+__device__ __forceinline__ bool next_piece(const CParams& p, Walk& w) {
+  w.left -= w.n;
+  w.f += w.n;
+  if (w.left <= 0) return false;
+  w.i = 0;
+  if (++w.rt >= row_blocks(p, w.s)) {
+    w.rt = 0;
+    if (++w.kvh >= p.Hkv) {
+      w.kvh = 0;
+      do {
+        ++w.b;
+        w.s = chunk::sequence(p.c, w.b);
+      } while (w.s.n == 0);
+    }
+  }
+  open_piece(p, w);
+  return true;
+}
+
+// Tile parts of one key tile as its dequant threads read them: the storage
+// rows of its two 64-token halves (a half that nothing sees stands in for the
+// other: its rows are masked), and the rows whose scale/zero words count.
+struct TileRows {
+  int64_t half[2];       // storage rows of the halves' first tokens
+  int hi, lo, sk;        // row r counts when r < hi and (r >= lo or r < sk)
+};
+__device__ __forceinline__ TileRows tile_rows(const CParams& p, const Walk& w, int kt) {
+  TileRows r;
+  const int t0 = kt * kT, end = w.t.pos_hi + 1;
+  const int lo = p.window > 0 ? w.t.pos_lo - p.window + 1 : 0;
+  r.hi = end - t0;
+  r.lo = lo - t0;
+  r.sk = p.sinks - t0;
+  bool seen[2];
 #pragma unroll
-  for (int i = 0; i < N; ++i) {
-    const int code = bits == 8 ? c[i] : (c[i / 2] >> (4 * (i & 1))) & 15;
-    x[i] = (static_cast<float>(code) - half_hi(word)) * half_lo(word);
+  for (int h = 0; h < 2; ++h) {
+    const int a = t0 + h * 64;
+    seen[h] = a < end && (a + 64 > lo || a < p.sinks);
+    r.half[h] = 0;
+    if (seen[h] && KVQ_IN_RANGE(p.c.bt == nullptr || a / 64 < p.c.bt_stride, p.status)) {
+      r.half[h] = chunk::storage_row(p.c, w.b, a);
+      if (r.half[h] < 0) {   // a page outside the pool: report, read page 0 instead
+        report(p.status, KVQ_ERR_INVALID_ARG);
+        r.half[h] = 0;
+      }
+    }
+  }
+  if (!seen[0]) r.half[0] = r.half[1];
+  if (!seen[1]) r.half[1] = r.half[0];
+  return r;
+}
+
+// Cache loads: each byte is used once per CTA, so it takes no L1 line.
+__device__ __forceinline__ uint4 load_codes(const uint8_t* src) {
+  uint4 v;
+  asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "l"(src));
+  return v;
+}
+__device__ __forceinline__ uint32_t load_word(const uint32_t* src) {
+  uint32_t v;
+  asm volatile("ld.global.L1::no_allocate.u32 %0, [%1];" : "=r"(v) : "l"(src));
+  return v;
+}
+
+template <int D, int BITS>
+struct PartRegs {
+  uint4 c[DqFmt<D, BITS>::NI];
+  uint32_t w[DqFmt<D, BITS>::NI];
+};
+
+// One part (K or V) of a key tile into a dequant thread's registers.
+template <int D, int BITS>
+__device__ __forceinline__ void load_part(PartRegs<D, BITS>& r, const CParams& p, int which, int kvh,
+                                          const TileRows& tr, int row, int c) {
+  using F = DqFmt<D, BITS>;
+  constexpr int G = D / 32;
+  const int64_t storage = static_cast<int64_t>(p.c.pB) * p.c.pT;
+  const uint8_t* codes = p.codes[which] + p.plane_off[kvh] + c * 16;
+  const uint32_t* sz = p.sz[which] + kvh * storage * G + c * F::VPC / 32;
+#pragma unroll
+  for (int it = 0; it < F::NI; ++it) {
+    const int64_t at = tr.half[it >= F::NI / 2] + (it % (F::NI / 2)) * F::RPI + row;
+    const uint8_t* cp = codes + at * F::R;
+    const uint32_t* sp = sz + at * G;
+    if (KVQ_IN_RANGE(at >= 0 && at < storage && cp + 16 <= p.codes[which] + p.codes_bytes, p.status)) {
+      r.c[it] = load_codes(cp);
+      r.w[it] = load_word(sp);
+    } else {
+      r.c[it] = make_uint4(0u, 0u, 0u, 0u);
+      r.w[it] = 0u;
+    }
+  }
+  // rows that nothing sees read as zeros, whatever is stored there
+  if (tr.hi < kT || tr.lo > 0) {
+#pragma unroll
+    for (int it = 0; it < F::NI; ++it) {
+      const int k = F::RPI * it + row;
+      if (k >= tr.hi || (k < tr.lo && k >= tr.sk)) r.w[it] = 0u;
+    }
+  }
+}
+
+template <int D, int BITS>
+__device__ __forceinline__ void store_part(uint32_t dst, const PartRegs<D, BITS>& r, int row, int c) {
+  using F = DqFmt<D, BITS>;
+#pragma unroll
+  for (int it = 0; it < F::NI; ++it) dequant_chunk<BITS>(dst, F::RPI * it + row, c * F::VPC, r.c[it], r.w[it]);
+}
+
+// The piece's query rows to fp16 in the swizzled layout (rows past the
+// segment's end zero); for a 4-bit head in the channel order of its K tiles.
+template <int D>
+__device__ __forceinline__ bool load_queries(const CParams& p, uint8_t* smem, uint64_t* bar, const Walk& w, int t,
+                                             uint32_t qempty_parity, bool wait) {
+  using L = CLayout<D>;
+  constexpr int CPR = D / 8;              // 16-byte chunks per row
+  constexpr int RPP = 128 / CPR;          // rows per pass
+  constexpr int NB = 8;                   // passes in flight
+  const int slots = w.t.rows > kT ? 2 : 1;
+  const int ch = t % CPR;
+  const bool four = p.bits[w.kvh] == 4;
+  const uint16_t* base = p.q + w.kvh * p.rep * p.sq_head + ch * 8;
+  const uint32_t dst = smem_u32(smem + L::kOffQ);
+  bool finite = true;
+  for (int r0 = 0; r0 < slots * kT; r0 += RPP * NB) {
+    uint4 v[NB];
+#pragma unroll
+    for (int k = 0; k < NB; ++k) {
+      const int r = r0 + k * RPP + t / CPR;
+      v[k] = make_uint4(0u, 0u, 0u, 0u);
+      if (r < w.t.rows) {
+        const int R = w.rt * kRows + r, tok = R / p.rep, hh = R - tok * p.rep;
+        v[k] = *reinterpret_cast<const uint4*>(base + (w.s.row0 + tok) * p.sq_row + hh * p.sq_head);
+      }
+    }
+    if (r0 == 0 && wait &&
+        !__all_sync(0xffffffffu, mbar_wait(&bar[B_QEMPTY], qempty_parity, p.status, kWaitNs)))
+      return false;
+#pragma unroll
+    for (int k = 0; k < NB; ++k) {
+      const int r = r0 + k * RPP + t / CPR;
+      uint32_t x[4] = {v[k].x, v[k].y, v[k].z, v[k].w};
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const float lo = __uint_as_float(x[e] << 16), hi = __uint_as_float(x[e] & 0xFFFF0000u);
+        finite &= fabsf(lo) < 65504.0f && fabsf(hi) < 65504.0f;
+        x[e] = pack_half2(lo, hi);
+      }
+      if (four) {   // channels 0,4,1,5,2,6,3,7
+        const uint32_t a = prmt(x[0], x[2], 0x5410u), b = prmt(x[0], x[2], 0x7632u);
+        const uint32_t c = prmt(x[1], x[3], 0x5410u), d = prmt(x[1], x[3], 0x7632u);
+        x[0] = a; x[1] = b; x[2] = c; x[3] = d;
+      }
+      const uint32_t rowp = dst + (r / kT) * L::kQBytes + (ch >> 3) * (kT * 128) + (r % kT) * 128;
+      sts128(rowp + (((ch & 7) ^ (r & 7)) << 4), x[0], x[1], x[2], x[3]);
+    }
+  }
+  if (!finite) report(p.status, KVQ_ERR_NONFINITE);
+  return true;
+}
+
+// The key tiles of one piece: codes to fp16 operand tiles.  jj counts the
+// CTA's tiles (stage jj & 1).  False after a wait that ran out.
+template <int D, int BITS>
+__device__ __forceinline__ bool dequant_piece(const CParams& p, uint8_t* smem, uint64_t* bar, const Walk& w,
+                                              uint32_t& jj, uint32_t piece, int t, int lane) {
+  using L = CLayout<D>;
+  using F = DqFmt<D, BITS>;
+  static_assert(F::NI % 2 == 0, "whole iterations per half tile");
+  int row, c;
+  dq_lane<D, BITS>(t, row, c);
+  const uint32_t kdst = smem_u32(smem + L::kOffK);
+  const uint32_t vdst = smem_u32(smem + L::kOffV);
+  PartRegs<D, BITS> ra, rb;
+  TileRows tr = tile_rows(p, w, w.t.tile(w.i));
+  load_part<D, BITS>(ra, p, 0, w.kvh, tr, row, c);
+  if (!load_queries<D>(p, smem, bar, w, t, (piece - 1) & 1, piece > 0)) return false;
+  fence_proxy_async_smem();
+  __syncwarp();
+  if (lane == 0) mbar_arrive(&bar[B_QREADY]);
+  for (int j = 0; j < w.n; ++j, ++jj) {
+    const int st = jj & 1;
+    load_part<D, BITS>(rb, p, 1, w.kvh, tr, row, c);
+    const bool more = j + 1 < w.n;
+    if (more) tr = tile_rows(p, w, w.t.tile(w.i + j + 1));
+    if (jj >= 2 && !__all_sync(0xffffffffu, mbar_wait(&bar[B_KVEMPTY0 + st], ((jj >> 1) - 1) & 1, p.status, kWaitNs)))
+      return false;
+    store_part<D, BITS>(kdst + st * L::kQBytes, ra, row, c);
+    fence_proxy_async_smem();
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&bar[B_KFULL0 + st]);
+    if (more) load_part<D, BITS>(ra, p, 0, w.kvh, tr, row, c);
+    store_part<D, BITS>(vdst + st * L::kQBytes, rb, row, c);
+    fence_proxy_async_smem();
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&bar[B_VFULL0 + st]);
+  }
+  return true;
+}
+
+// 32 output values of one row, from channel offset `off` of the output.
+__device__ __forceinline__ void store_row32(const CParams& p, int D, int64_t off, const float (&o)[32]) {
+  if (!KVQ_IN_RANGE(off >= 0 && off + 32 <= static_cast<int64_t>(p.c.rows) * p.Hq * D, p.status)) return;
+  if (p.out_dtype == KVQ_OUT_F32) {
+    float4* dst = reinterpret_cast<float4*>(static_cast<float*>(p.out) + off);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) dst[i] = make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+  } else {
+    uint4* dst = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.out) + off);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      uint32_t v[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const __nv_bfloat162 b = __floats2bfloat162_rn(o[8 * i + 2 * e], o[8 * i + 2 * e + 1]);
+        v[e] = *reinterpret_cast<const uint32_t*>(&b);
+      }
+      dst[i] = make_uint4(v[0], v[1], v[2], v[3]);
+    }
+  }
+}
+
+// Output offset of packed row R of a sequence and KV head.
+__device__ __forceinline__ int64_t out_offset(const CParams& p, const Walk& w, int R, int D) {
+  const int tok = R / p.rep, hh = R - tok * p.rep;
+  return ((static_cast<int64_t>(w.s.row0) + tok) * p.Hq + w.kvh * p.rep + hh) * D;
+}
+
+// The pieces of slot h of a segment held by CTAs c0 .. c1, merged by
+// log-sum-exp in CTA order: one warp per row, a lane per D / 32 channels.
+template <int D>
+__device__ __forceinline__ void merge_rows(const CParams& p, const Walk& w, int h, int c0, int c1, int slot0, int warp4,
+                                           int lane) {
+  constexpr int N = D / 32;
+  const int nr = min(kT, w.t.rows - h * kT);
+  for (int r = warp4; r < nr; r += 4) {
+    float M = -INFINITY, L = 0.0f, acc[N];
+#pragma unroll
+    for (int e = 0; e < N; ++e) acc[e] = 0.0f;
+    for (int c = c0; c <= c1; ++c) {
+      const int64_t at = static_cast<int64_t>(2 * c + (c == c0 ? slot0 : 0)) * p.slot_rows + h * kT + r;
+      const float lse = __ldcg(p.ws_lse + at);
+      if (lse == -INFINITY) continue;
+      float v[N];
+#pragma unroll
+      for (int e = 0; e < N; ++e) v[e] = __ldcg(p.ws_o + at * D + lane + 32 * e);
+      const float mn = fmaxf(M, lse), a = fast_exp2(M - mn), b = fast_exp2(lse - mn);
+      L = L * a + b;
+#pragma unroll
+      for (int e = 0; e < N; ++e) acc[e] = acc[e] * a + b * v[e];
+      M = mn;
+    }
+    const float inv = L > 0.0f ? 1.0f / L : 0.0f;
+    const int64_t off = out_offset(p, w, w.rt * kRows + h * kT + r, D) + lane;
+    if (!KVQ_IN_RANGE(off >= 0 && off + 32 * (N - 1) < static_cast<int64_t>(p.c.rows) * p.Hq * D, p.status)) continue;
+#pragma unroll
+    for (int e = 0; e < N; ++e) {
+      if (p.out_dtype == KVQ_OUT_F32) static_cast<float*>(p.out)[off + 32 * e] = acc[e] * inv;
+      else static_cast<__nv_bfloat16*>(p.out)[off + 32 * e] = __float2bfloat16_rn(acc[e] * inv);
+    }
   }
 }
 
 template <int D>
-__global__ void __launch_bounds__(256) chunk_attention_kernel(const __grid_constant__ CParams p) {
-  constexpr int N = D / 32;
+__global__ void __launch_bounds__(kThreads, 1) chunk_attention_kernel(const __grid_constant__ CParams p) {
+  using L = CLayout<D>;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint64_t* bar = reinterpret_cast<uint64_t*>(smem + L::kOffBar);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::kOffMisc);
+  int32_t* flag = reinterpret_cast<int32_t*>(smem + L::kOffMisc) + 1;   // merge flags of the two slots
+  int64_t* pre = reinterpret_cast<int64_t*>(smem + L::kOffPre);          // tiles of sequences 0 .. b-1, per KV head
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+  if (threadIdx.x == 0) {
+    mbar_init(&bar[B_QREADY], 4);
+    mbar_init(&bar[B_QEMPTY], 2);
+    for (int s = 0; s < 2; ++s) {
+      mbar_init(&bar[B_KFULL0 + s], 4);
+      mbar_init(&bar[B_VFULL0 + s], 4);
+      mbar_init(&bar[B_KVEMPTY0 + s], 2);
+      mbar_init(&bar[B_SFULL0 + s], 1);
+      mbar_init(&bar[B_PFIRST0 + s], 4);
+      mbar_init(&bar[B_PFULL0 + s], 4);
+      mbar_init(&bar[B_ORDY0 + s], 1);
+      mbar_init(&bar[B_OFREE0 + s], 4);
+      mbar_init(&bar[B_TURN0 + s], 1);
+      mbar_init(&bar[B_GROUP0 + s], 4);
+    }
+    mbar_init(&bar[B_MMADONE], 2);
+    mbar_init(&bar[B_EXIT], kExitArrivals);
+    fence_barrier_init();
+  }
+  // the caches, queries and lengths may come from the kernel before this one
   grid_dependency_wait();
   grid_launch_dependents();
-  const int lane = threadIdx.x & 31;
-  if (blockIdx.x == 0) chunk::check_sequences(p.c, threadIdx.x, blockDim.x, p.status);
-  const int64_t u = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5);
-  const int r = static_cast<int>(u / p.Hq), h = static_cast<int>(u % p.Hq);
-  if (r >= p.c.rows) return;
-  int b = chunk::find_sequence(p.c.start, p.c.B, r, lane);
-  const chunk::Seq s = chunk::sequence(p.c, b);
-  if (r < s.row0 || r >= s.row0 + s.n) return;
-  const int pos = s.len - s.n + (r - s.row0);
-  const int kvh = h / (p.Hq / p.Hkv);
-  float q[N], o[N], m = -INFINITY, l = 0.0f;
-  bool ok = true;
+  if (blockIdx.x == 0) chunk::check_sequences(p.c, threadIdx.x, kThreads, p.status);
+  // tiles per sequence (one KV head): a warp per sequence, a lane per row block
+  for (int b = warp; b < p.c.B; b += kThreads / 32) {
+    const chunk::Seq s = chunk::sequence(p.c, b);
+    const int nrt = row_blocks(p, s);
+    int64_t n = 0;
+    for (int rt = lane; rt < nrt; rt += 32) n += segment_tiles(p, s, rt).n;
 #pragma unroll
-  for (int i = 0; i < N; ++i) {
-    q[i] = __uint_as_float(static_cast<uint32_t>(p.q[r * p.sq_row + h * p.sq_head + lane * N + i]) << 16);
-    ok &= fabsf(q[i]) < 65504.0f;
-    o[i] = 0.0f;
+    for (int o = 16; o > 0; o >>= 1) n += __shfl_xor_sync(0xffffffffu, n, o);
+    if (lane == 0) pre[b + 1] = n;
   }
-  if (!ok) report(p.status, KVQ_ERR_NONFINITE);
-  const int first = p.window > 0 && pos >= p.window ? pos - p.window + 1 : 0;
-  for (int j = first > 0 && p.sinks > 0 ? 0 : first; j <= pos; ++j) {
-    if (j < first && j >= p.sinks) j = first;
-    int64_t row = chunk::storage_row(p.c, b, j);
-    if (row < 0) {
-      report(p.status, KVQ_ERR_INVALID_ARG);
-      row = j % KVQ_TILE_TOKENS;
+  __syncthreads();
+  if (warp == 0) {
+    int64_t carry = 0;
+    for (int b0 = 0; b0 < p.c.B; b0 += 32) {
+      int64_t n = b0 + lane < p.c.B ? pre[b0 + lane + 1] : 0;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int64_t v = __shfl_up_sync(0xffffffffu, n, o);
+        if (lane >= o) n += v;
+      }
+      if (b0 + lane < p.c.B) pre[b0 + lane + 1] = carry + n;
+      carry += __shfl_sync(0xffffffffu, n, 31);
     }
-    float x[N], dot = 0.0f;
-    lane_values<D>(x, p, 0, kvh, row, lane);
-#pragma unroll
-    for (int i = 0; i < N; ++i) dot = fmaf(q[i], x[i], dot);
-#pragma unroll
-    for (int k = 16; k > 0; k >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, k);
-    dot *= p.scale_log2;
-    const float mn = fmaxf(m, dot), a = fast_exp2(m - mn), w = fast_exp2(dot - mn);
-    lane_values<D>(x, p, 1, kvh, row, lane);
-#pragma unroll
-    for (int i = 0; i < N; ++i) o[i] = fmaf(w, x[i], o[i] * a);
-    l = l * a + w;
-    m = mn;
+    if (lane == 0) pre[0] = 0;
+    tc::tmem_alloc(tmem_slot, kTmemCols);
+    tc::tmem_relinquish();
   }
-  const int64_t at = (static_cast<int64_t>(r) * p.Hq + h) * D + lane * N;
-#pragma unroll
-  for (int i = 0; i < N; ++i) {
-    if (p.out_dtype == KVQ_OUT_F32) static_cast<float*>(p.out)[at + i] = o[i] / l;
-    else static_cast<__nv_bfloat16*>(p.out)[at + i] = __float2bfloat16_rn(o[i] / l);
+  tc::fence_before_sync();
+  __syncthreads();
+  tc::fence_after_sync();
+  const uint32_t tmem = *tmem_slot;
+
+  // this CTA's range [f0, f1) of the N tiles; never more CTAs in the split than tiles
+  const int64_t N = p.Hkv * pre[p.c.B];
+  const int C = N < p.num_ctas ? static_cast<int>(N) : p.num_ctas;
+  const bool in_split = static_cast<int>(blockIdx.x) < C;
+  Walk w;
+  w.f = in_split ? N * blockIdx.x / C : 0;
+  w.left = in_split ? N * (blockIdx.x + 1) / C - w.f : 0;
+  if (w.left <= 0) {   // the whole CTA: nothing was started
+    if (warp == 0) tc::tmem_dealloc(tmem, kTmemCols);
+    return;
   }
+  {
+    int lo = 0, hi = p.c.B - 1;   // the last b with Hkv * pre[b] <= f: a sequence with tiles
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) >> 1;
+      if (p.Hkv * pre[mid] <= w.f) lo = mid; else hi = mid - 1;
+    }
+    w.b = lo;
+    w.s = chunk::sequence(p.c, w.b);
+    const int64_t per = pre[lo + 1] - pre[lo], off = w.f - p.Hkv * pre[lo];
+    w.kvh = static_cast<int>(off / per);
+    int64_t rem = off - w.kvh * per;
+    // the row block: prefix sums over 32 blocks at a time
+    const int nrt = row_blocks(p, w.s);
+    w.rt = 0;
+    w.i = 0;
+    for (int r0 = 0; r0 < nrt; r0 += 32) {
+      const int64_t mine = r0 + lane < nrt ? segment_tiles(p, w.s, r0 + lane).n : 0;
+      int64_t incl = mine;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int64_t v = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += v;
+      }
+      const unsigned past = __ballot_sync(0xffffffffu, r0 + lane < nrt && incl > rem);
+      if (past != 0u) {
+        const int k = __ffs(past) - 1;
+        w.rt = r0 + k;
+        w.i = static_cast<int>(rem - (__shfl_sync(0xffffffffu, incl, k) - __shfl_sync(0xffffffffu, mine, k)));
+        break;
+      }
+      rem -= __shfl_sync(0xffffffffu, incl, 31);
+    }
+  }
+  open_piece(p, w);
+  const int64_t total = w.left;
+
+  // Registers: launched with 128 per thread (checked on the host); per
+  // warpgroup 80 + 192 + 120 + 120 = 4 x 128.
+  if (warp < 4) {
+    tc::reg_dealloc<80>();
+    if (warp == 0) {
+      // The other roles finish in bounded time: each stops at its first wait
+      // that runs out, and a role waits at most a few times per tile.
+      const uint64_t deadline = kWaitNs * static_cast<uint64_t>(8 * total + 16);
+      const uint64_t t0 = global_ns();
+      uint32_t n = 0;
+      while (!mbar_try_wait(&bar[B_EXIT], 0)) {
+        if ((++n & 255u) == 0 && global_ns() - t0 > deadline) {
+          report(p.status, KVQ_ERR_TIMEOUT);
+          break;
+        }
+      }
+      __syncwarp();
+      tc::fence_after_sync();
+      tc::tmem_dealloc(tmem, kTmemCols);
+      return;
+    }
+    if (warp == 3) {
+      if (lane == 0) mbar_arrive(&bar[B_EXIT]);
+      return;
+    }
+    // ---------------- MMA issuers, one warp per slot ----------------
+    const int h = warp - 1;
+    const uint32_t id_qk = tc::idesc_f16_f32(kT, kT, false);
+    const uint32_t id_pv = tc::idesc_f16_f32(kT, D, true);
+    const uint32_t qh = smem_u32(smem + L::kOffQ) + h * L::kQBytes;
+    const uint32_t k_base = smem_u32(smem + L::kOffK);
+    const uint32_t v_base = smem_u32(smem + L::kOffV);
+    const uint32_t d_s = tmem + h * 256, d_o = d_s + 128;
+    auto wait_all = [&](int which, uint32_t parity) -> bool {
+      return __all_sync(0xffffffffu, mbar_wait(&bar[which], parity & 1, p.status, kWaitNs));
+    };
+    auto issue_qk = [&](int st) {
+      const uint32_t kh = k_base + st * L::kQBytes;
+      tc::mma_ss<false>(d_s, tc::smem_desc_sw128(qh, 16, 1024), tc::smem_desc_sw128(kh, 16, 1024), id_qk);
+#pragma unroll
+      for (int s = 1; s < D / 16; ++s) {
+        const uint32_t off = (s >> 2) * (kT * 128) + (s & 3) * 32;
+        tc::mma_ss<true>(d_s, tc::smem_desc_sw128(qh + off, 16, 1024), tc::smem_desc_sw128(kh + off, 16, 1024), id_qk);
+      }
+      tc::commit(&bar[B_SFULL0 + h]);
+    };
+    auto issue_pv = [&](int st, bool first, int hf) {
+      const uint32_t vs = v_base + st * L::kQBytes;
+      if (hf == 0) {
+        const uint64_t v0 = tc::smem_desc_sw128(vs, kT * 128, 1024);
+        if (first) tc::mma_ts<false>(d_o, d_s, v0, id_pv);
+        else tc::mma_ts<true>(d_o, d_s, v0, id_pv);
+      }
+#pragma unroll
+      for (int s = hf == 0 ? 1 : 2; s < (hf == 0 ? 2 : kT / 16); ++s)
+        tc::mma_ts<true>(d_o, d_s + s * 8, tc::smem_desc_sw128(vs + s * 2048, kT * 128, 1024), id_pv);
+    };
+    // Turns (pieces with both slots): in block g a slot issues P.V of one tile
+    // and Q.K^T of the next.  Slot 0 goes after slot 1's block g - 1, slot 1
+    // after slot 0's block g; g runs on from piece to piece.
+    uint32_t g = 0, jj = 0, sj = 0, mine = 0, piece = 0;
+    bool ok = true;
+    do {
+      const int nh = w.t.rows > kT ? 2 : 1;
+      if (h >= nh) {
+        // a piece without slot 1: its issuer only frees what the piece's
+        // barriers expect of it (and so meets every phase of them in order)
+        ok = wait_all(B_QREADY, piece);
+        if (ok && lane == 0) mbar_arrive(&bar[B_QEMPTY]);
+        for (int j = 0; j < w.n && ok; ++j, ++jj) {
+          ok = wait_all(B_KFULL0 + (jj & 1), jj >> 1) && wait_all(B_VFULL0 + (jj & 1), jj >> 1);
+          if (ok && lane == 0) mbar_arrive(&bar[B_KVEMPTY0 + (jj & 1)]);
+        }
+        if (!ok) break;
+        ++piece;
+        continue;
+      }
+      const bool turns = nh == 2;
+      auto take_turn = [&]() -> bool {
+        if (!turns || (h == 0 && g == 0)) return true;
+        return h == 0 ? wait_all(B_TURN0, g - 1) : wait_all(B_TURN1, g);
+      };
+      auto pass_turn = [&]() {
+        if (turns) mbar_arrive(&bar[h == 0 ? B_TURN1 : B_TURN0]);
+      };
+      // the query rows are free once the piece's last Q.K^T is done
+      auto free_queries = [&]() { tc::commit(&bar[B_QEMPTY]); };
+      ok = wait_all(B_QREADY, piece) && wait_all(B_KFULL0 + (jj & 1), jj >> 1) && take_turn();
+      if (!ok) break;
+      tc::fence_after_sync();
+      if (tc::elect_one()) {
+        issue_qk(jj & 1);
+        if (w.n == 1) free_queries();
+        pass_turn();
+      }
+      __syncwarp();
+      if (turns) ++g;
+      for (int j = 0; j < w.n && ok; ++j, ++jj, ++sj) {
+        const int st = jj & 1;
+        ok = wait_all(B_VFULL0 + st, jj >> 1) && wait_all(B_PFIRST0 + h, sj) && take_turn();
+        // the first P.V overwrites O: the previous piece's has been read
+        if (ok && j == 0 && mine > 0) ok = wait_all(B_OFREE0 + h, mine - 1);
+        if (!ok) break;
+        tc::fence_after_sync();
+        if (tc::elect_one()) issue_pv(st, j == 0, 0);
+        __syncwarp();
+        ok = wait_all(B_PFULL0 + h, sj);
+        if (!ok) break;
+        tc::fence_after_sync();
+        if (tc::elect_one()) {
+          issue_pv(st, false, 1);
+          tc::commit(&bar[B_ORDY0 + h]);
+          tc::commit(&bar[B_KVEMPTY0 + st]);
+        }
+        __syncwarp();
+        if (j + 1 < w.n) {
+          ok = wait_all(B_KFULL0 + ((jj + 1) & 1), (jj + 1) >> 1);
+          if (!ok) break;
+          tc::fence_after_sync();
+        }
+        if (tc::elect_one()) {
+          if (j + 1 < w.n) {
+            issue_qk((jj + 1) & 1);
+            if (j + 2 == w.n) free_queries();
+          }
+          pass_turn();
+        }
+        __syncwarp();
+        if (turns) ++g;
+      }
+      if (!ok) break;
+      ++piece;
+      ++mine;
+    } while (next_piece(p, w));
+    // every product this warp issued has completed (a commit with none
+    // pending arrives at once) before the warp reports that it is done
+    if (tc::elect_one()) tc::commit(&bar[B_MMADONE]);
+    __syncwarp();
+    wait_all(B_MMADONE, 0);
+    tc::fence_before_sync();
+    if (lane == 0) mbar_arrive(&bar[B_EXIT]);
+    return;
+  }
+
+  if (warp < 8) {
+    tc::reg_alloc<192>();
+    // ---------------- dequant warpgroup ----------------
+    const int t = threadIdx.x - 128;
+    uint32_t jj = 0, piece = 0;
+    bool ok;
+    do {
+      ok = p.bits[w.kvh] == 4 ? dequant_piece<D, 4>(p, smem, bar, w, jj, piece, t, lane)
+                              : dequant_piece<D, 8>(p, smem, bar, w, jj, piece, t, lane);
+      ++piece;
+    } while (ok && next_piece(p, w));
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&bar[B_EXIT]);
+    return;
+  }
+
+  // ---------------- softmax warpgroups ----------------
+  tc::reg_dealloc<120>();
+  const int h = (warp - 8) >> 2;            // slot 0 or 1
+  const int q4 = warp & 3;                  // TMEM lane quarter
+  const int r = q4 * 32 + lane;             // row within the slot
+  const uint32_t lane_off = static_cast<uint32_t>(q4 * 32) << 16;
+  const uint32_t s_addr = tmem + lane_off + h * 256;
+  const uint32_t o_addr = s_addr + 128;
+  const float sl2 = p.scale_log2;
+  uint32_t sj = 0, group = 0;
+  bool ok = true;
+  // the slot's four warps, without a wait that could last for ever
+  auto group_sync = [&]() {
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&bar[B_GROUP0 + h]);
+    ok = __all_sync(0xffffffffu, mbar_wait(&bar[B_GROUP0 + h], group & 1, p.status, kWaitNs)) && ok;
+    ++group;
+  };
+  do {
+    if (h * kT >= w.t.rows) continue;       // a piece without this slot
+    const bool four = p.bits[w.kvh] == 4;
+    const int R = w.rt * kRows + h * kT + r;
+    const bool live = h * kT + r < w.t.rows;
+    // positions: this row's, and the slot's first and last (tile-wide tests)
+    const int pos0 = w.s.len - w.s.n;
+    const int pos = live ? pos0 + R / p.rep : w.t.pos_hi;
+    const int slot_lo = pos0 + (w.rt * kRows + h * kT) / p.rep;
+    const int slot_hi = pos0 + (w.rt * kRows + min(h * kT + kT, w.t.rows) - 1) / p.rep;
+    float m_run = -INFINITY, l_run = 0.0f;
+    for (int j = 0; j < w.n; ++j, ++sj) {
+      const int t0 = w.t.tile(w.i + j) * kT;
+      // columns past `lim`, and those from `sk` to `lo` - 1, are not seen by this row
+      const int lim = pos - t0;
+      const int lo = p.window > 0 ? pos - p.window + 1 - t0 : 0, sk = p.sinks - t0;
+      const bool masked = t0 + kT - 1 > slot_lo || (p.window > 0 && t0 < slot_hi - p.window + 1 && sk < kT);
+      ok = __all_sync(0xffffffffu, mbar_wait(&bar[B_SFULL0 + h], sj & 1, p.status, kWaitNs));
+      if (!ok) break;
+      tc::fence_after_sync();
+      auto hidden = [&](int col) { return col > lim || (col < lo && col >= sk); };
+      float mxa = -INFINITY, mxb = -INFINITY;
+      if (!masked) {
+        uint32_t va[32], vb[32];
+        auto mx_chunk = [&](const uint32_t (&v)[32]) {
+#pragma unroll
+          for (int i = 0; i < 32; i += 4) {
+            mxa = fmax3(mxa, __uint_as_float(v[i]), __uint_as_float(v[i + 1]));
+            mxb = fmax3(mxb, __uint_as_float(v[i + 2]), __uint_as_float(v[i + 3]));
+          }
+        };
+        tc::ld_32x32b_x32(s_addr, va);
+        tc::wait_ld(va);
+        tc::ld_32x32b_x32(s_addr + 32, vb);
+        mx_chunk(va);
+        tc::wait_ld(vb);
+        tc::ld_32x32b_x32(s_addr + 64, va);
+        mx_chunk(vb);
+        tc::wait_ld(va);
+        tc::ld_32x32b_x32(s_addr + 96, vb);
+        mx_chunk(va);
+        tc::wait_ld(vb);
+        mx_chunk(vb);
+      } else {
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          uint32_t v[32];
+          tc::ld_32x32b_x32(s_addr + c * 32, v);
+          tc::wait_ld(v);
+#pragma unroll
+          for (int i = 0; i < 32; ++i) mxa = hidden(c * 32 + i) ? mxa : fmaxf(mxa, __uint_as_float(v[i]));
+        }
+      }
+      const float m_tile = fmaxf(mxa, mxb) * sl2;
+      float m_use = m_run, alpha = 1.0f;
+      if (m_run == -INFINITY || m_tile > m_run + kRescaleThreshold) {
+        m_use = fmaxf(m_run, m_tile);
+        alpha = (m_run == -INFINITY) ? 0.0f : fast_exp2(m_run - m_use);
+        m_run = m_use;
+      }
+      // rescale O (rare) before any P.V of this tile is issued
+      if (__any_sync(0xffffffffu, alpha != 1.0f) && j > 0) {
+        ok = __all_sync(0xffffffffu, mbar_wait(&bar[B_ORDY0 + h], (sj - 1) & 1, p.status, kWaitNs));
+        if (!ok) break;
+        tc::fence_after_sync();
+#pragma unroll
+        for (int c = 0; c < D / 32; ++c) {
+          uint32_t v[32];
+          tc::ld_32x32b_x32(o_addr + c * 32, v);
+          tc::wait_ld();
+#pragma unroll
+          for (int i = 0; i < 32; ++i) v[i] = __float_as_uint(__uint_as_float(v[i]) * alpha);
+          tc::st_32x32b_x32(o_addr + c * 32, v);
+        }
+      }
+      auto p_first = [&]() {
+        tc::wait_st();
+        tc::fence_before_sync();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bar[B_PFIRST0 + h]);
+      };
+      float s0 = 0.0f, s1 = 0.0f, s2 = 0.0f, s3 = 0.0f;
+      const float neg_m = m_use == -INFINITY ? 0.0f : -m_use;   // (a row that sees nothing yet: every weight is 0)
+      if (!masked) {
+        uint32_t va[32], vb[32];
+        auto p_chunk = [&](const uint32_t (&v)[32], int c) {
+          uint32_t pk[16];
+#pragma unroll
+          for (int i = 0; i < 32; i += 4) {
+            float x0, x1, x2, x3;
+            ffma2(x0, x1, __uint_as_float(v[i]), __uint_as_float(v[i + 1]), sl2, neg_m);
+            ffma2(x2, x3, __uint_as_float(v[i + 2]), __uint_as_float(v[i + 3]), sl2, neg_m);
+            const float p0 = fast_exp2(x0), p1 = fast_exp2(x1), p2 = fast_exp2(x2), p3 = fast_exp2(x3);
+            fadd2(s0, s1, p0, p1);
+            fadd2(s2, s3, p2, p3);
+            pk[i / 2] = pack_half2(p0, p1);
+            pk[i / 2 + 1] = pack_half2(p2, p3);
+          }
+          tc::st_32x32b_x16(s_addr + c * 16, pk);
+        };
+        tc::ld_32x32b_x32(s_addr, va);
+        tc::wait_ld(va);
+        tc::ld_32x32b_x32(s_addr + 32, vb);
+        p_chunk(va, 0);
+        p_first();
+        tc::wait_ld(vb);
+        tc::ld_32x32b_x32(s_addr + 64, va);
+        p_chunk(vb, 1);
+        tc::wait_ld(va);
+        tc::ld_32x32b_x32(s_addr + 96, vb);
+        p_chunk(va, 2);
+        tc::wait_ld(vb);
+        p_chunk(vb, 3);
+      } else {
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          uint32_t v[32];
+          uint32_t pk[16];
+          tc::ld_32x32b_x32(s_addr + c * 32, v);
+          tc::wait_ld(v);
+#pragma unroll
+          for (int i = 0; i < 32; i += 2) {
+            const float p0 = hidden(c * 32 + i) ? 0.0f : fast_exp2(fmaf(__uint_as_float(v[i]), sl2, neg_m));
+            const float p1 = hidden(c * 32 + i + 1) ? 0.0f : fast_exp2(fmaf(__uint_as_float(v[i + 1]), sl2, neg_m));
+            fadd2(s0, s1, p0, p1);
+            pk[i / 2] = pack_half2(p0, p1);
+          }
+          tc::st_32x32b_x16(s_addr + c * 16, pk);
+          if (c == 0) p_first();
+        }
+      }
+      l_run = l_run * alpha + ((s0 + s1) + (s2 + s3));
+      tc::wait_st();
+      tc::fence_before_sync();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bar[B_PFULL0 + h]);
+    }
+    if (!ok) break;
+    // ---- end of the piece ----
+    ok = __all_sync(0xffffffffu, mbar_wait(&bar[B_ORDY0 + h], (sj - 1) & 1, p.status, kWaitNs));
+    if (!ok) break;
+    tc::fence_after_sync();
+    const float inv = l_run > 0.0f ? 1.0f / l_run : 0.0f;
+    const bool whole = w.n == w.t.n;
+    // CTAs c0 .. c1 hold the segment; a CTA's piece of it is partial 0 of its
+    // workspace when the segment began before the CTA's range (or with it), else 1
+    const int64_t seg0 = w.f - w.i;
+    const int c0 = static_cast<int>(((seg0 + 1) * C - 1) / N), c1 = static_cast<int>(((seg0 + w.t.n) * C - 1) / N);
+    const int slot0 = seg0 <= N * c0 / C ? 0 : 1;
+    const int64_t part = static_cast<int64_t>(2 * blockIdx.x + (static_cast<int>(blockIdx.x) == c0 ? slot0 : 0)) *
+                             p.slot_rows + h * kT + r;
+    const int64_t orow = out_offset(p, w, R, D);
+#pragma unroll
+    for (int c = 0; c < D / 32; ++c) {
+      uint32_t v[32];
+      tc::ld_32x32b_x32(o_addr + c * 32, v);
+      tc::wait_ld();
+      float o[32];
+      if (four) {   // column 8m + 2k holds channel 8m + k, column 8m + 2k + 1 channel 8m + 4 + k
+#pragma unroll
+        for (int i = 0; i < 32; ++i) o[i] = __uint_as_float(v[(i & ~7) | ((i & 3) << 1) | ((i >> 2) & 1)]) * inv;
+      } else {
+#pragma unroll
+        for (int i = 0; i < 32; ++i) o[i] = __uint_as_float(v[i]) * inv;
+      }
+      if (!live) continue;
+      if (whole) {
+        store_row32(p, D, orow + c * 32, o);
+      } else {
+        float4* dst = reinterpret_cast<float4*>(p.ws_o + part * D + c * 32);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) dst[i] = make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+        if (c == 0) p.ws_lse[part] = l_run > 0.0f ? m_run + __log2f(l_run) : -INFINITY;
+      }
+    }
+    tc::fence_before_sync();
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&bar[B_OFREE0 + h]);
+    if (!whole) {
+      group_sync();   // every thread's partial is stored
+      if (!ok) break;
+      // one acquire-release atomic after the group's barrier: its release
+      // covers the group's stores, its acquire the other pieces' (released by
+      // their own arrivals) for the last arriver
+      if (threadIdx.x == 256 + h * kT)
+        flag[h] = atom_add_acq_rel_gpu(p.cnt + 2 * c0 + h, 1) + 1 == c1 - c0 + 1 ? 1 : 0;
+      group_sync();
+      if (!ok) break;
+      if (flag[h] == 1) {
+        merge_rows<D>(p, w, h, c0, c1, slot0, q4, lane);
+        if (threadIdx.x == 256 + h * kT) p.cnt[2 * c0 + h] = 0;   // ready for the next call
+      }
+      group_sync();   // the flag has been read
+      if (!ok) break;
+    }
+  } while (next_piece(p, w));
+  tc::wait_st();   // P and rescaled O stores of a loop left early have landed
+  tc::fence_before_sync();
+  __syncwarp();
+  if (lane == 0) mbar_arrive(&bar[B_EXIT]);
+}
+
+// Per device and head dim, set once under a lock: the kernel's dynamic
+// shared-memory limit, and whether it was built with the 128 registers per
+// thread that the register split above assumes.  1 = ready, -2 = not usable.
+std::mutex g_prep_mu;
+int g_prep[64][2] = {};
+
+template <int D>
+int prepare_on_current_device() {
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return -1;
+  std::lock_guard<std::mutex> lock(g_prep_mu);
+  int& st = g_prep[dev][D == 128 ? 1 : 0];
+  if (st == 0) {
+    cudaFuncAttributes fa;
+    if (cudaFuncGetAttributes(&fa, chunk_attention_kernel<D>) != cudaSuccess || fa.numRegs != 128) {
+      st = -2;
+    } else if (cudaFuncSetAttribute(chunk_attention_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                    static_cast<int>(CLayout<D>::bytes(4096))) != cudaSuccess) {
+      return -1;   // a CUDA error; try again on the next call
+    } else {
+      st = 1;
+    }
+  }
+  return st;
+}
+static_assert(CLayout<128>::kOffPre + 1024 + 4097 * 8 <= 232448, "shared memory of the D = 128 kernel");
+
+size_t align16(size_t x) { return (x + 15) & ~size_t(15); }
+
+// Workspace: [cnt: 2 per CTA][lse: 2 partials per CTA][o: the same rows of D]
+int slot_rows(int rows, int rep) {
+  const int64_t all = static_cast<int64_t>(rows) * rep;
+  return all < kRows ? static_cast<int>(all < 1 ? 1 : all) : kRows;
+}
+size_t counter_bytes(int ctas) { return align16(static_cast<size_t>(ctas) * 2 * 4); }
+size_t lse_bytes(int ctas, int sr) { return align16(static_cast<size_t>(ctas) * 2 * sr * 4); }
+
+template <int D>
+kvq_status launch_d(const CParams& p, cudaStream_t stream) {
+  const int prep = prepare_on_current_device<D>();
+  if (prep == -2) return KVQ_ERR_UNSUPPORTED;
+  if (prep != 1) return KVQ_ERR_CUDA;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(p.num_ctas));
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = CLayout<D>::bytes(p.c.B);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, chunk_attention_kernel<D>, p) == cudaSuccess ? KVQ_OK : KVQ_ERR_CUDA;
 }
 
 }  // namespace
 
-size_t chunk_workspace_bytes(int, int, int, int, int) { return 16; }
+size_t chunk_workspace_bytes(int rows, int B, int Hq, int Hkv, int D) {
+  (void)B;
+  const int ctas = device_sm_count(), sr = slot_rows(rows, Hq / Hkv);
+  return counter_bytes(ctas) + lse_bytes(ctas, sr) + static_cast<size_t>(ctas) * 2 * sr * D * 4;
+}
 
 kvq_status launch_chunk_attention(const ChunkAttnArgs& a, cudaStream_t stream) {
   CParams p;
+  memset(&p, 0, sizeof(p));
+  const int D = a.k->D;
   p.c.start = a.chunk.start; p.c.seq_lens = a.chunk.seq_lens; p.c.bt = a.chunk.bt;
   p.c.B = a.chunk.B; p.c.rows = a.chunk.rows; p.c.max_chunk = a.chunk.max_chunk;
   p.c.bt_stride = a.chunk.bt_max_pages;
@@ -114,26 +969,22 @@ kvq_status launch_chunk_attention(const ChunkAttnArgs& a, cudaStream_t stream) {
   p.sz[0] = a.k->sz; p.sz[1] = a.v->sz;
   p.out = a.out;
   p.status = a.status;
-  p.out_dtype = a.out_dtype; p.Hq = a.Hq; p.Hkv = a.k->Hkv; p.window = a.window; p.sinks = a.sinks;
-  const float scale = a.softmax_scale > 0.0f ? a.softmax_scale : 1.0f / sqrtf(static_cast<float>(a.k->D));
+  p.out_dtype = a.out_dtype; p.Hq = a.Hq; p.Hkv = a.k->Hkv; p.rep = a.Hq / a.k->Hkv;
+  p.window = a.window; p.sinks = a.sinks;
+  p.num_ctas = device_sm_count();
+  p.slot_rows = slot_rows(a.chunk.rows, p.rep);
+  uint8_t* ws = static_cast<uint8_t*>(a.ws);
+  p.cnt = reinterpret_cast<int32_t*>(ws);
+  p.ws_lse = reinterpret_cast<float*>(ws + counter_bytes(p.num_ctas));
+  p.ws_o = reinterpret_cast<float*>(ws + counter_bytes(p.num_ctas) + lse_bytes(p.num_ctas, p.slot_rows));
+  const float scale = a.softmax_scale > 0.0f ? a.softmax_scale : 1.0f / sqrtf(static_cast<float>(D));
   p.scale_log2 = scale * 1.4426950408889634f;
+  p.codes_bytes = kvq_cache_codes_bytes(a.k);
   for (int h = 0; h < KVQ_MAX_HKV; ++h) {
     p.plane_off[h] = a.layout.plane_off[h];
     p.bits[h] = a.layout.bits[h];
   }
-  const int64_t blocks = (static_cast<int64_t>(a.chunk.rows) * a.Hq + 7) / 8;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(blocks));
-  cfg.blockDim = dim3(256);
-  cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  const cudaError_t e = a.k->D == 128 ? cudaLaunchKernelEx(&cfg, chunk_attention_kernel<128>, p)
-                                      : cudaLaunchKernelEx(&cfg, chunk_attention_kernel<64>, p);
-  return e == cudaSuccess ? KVQ_OK : KVQ_ERR_CUDA;
+  return D == 128 ? launch_d<128>(p, stream) : launch_d<64>(p, stream);
 }
 
 }  // namespace kvq
