@@ -68,6 +68,18 @@ __device__ __forceinline__ int64_t storage_row(const View& c, int b, int pos) {
   return static_cast<int64_t>(page) * KVQ_TILE_TOKENS + pos % KVQ_TILE_TOKENS;
 }
 
+// The 64-token storage block (a page, or that much of a sequence) of tokens
+// 64 i .. 64 i + 63 of sequence b; a page id outside the pool is reported and
+// block 0 returned.  (int: the host refuses storage of 2^31 blocks.)
+__device__ __forceinline__ int storage_block(const View& c, int b, int i, int32_t* status) {
+  if (c.bt == nullptr) return b * (c.pT / KVQ_TILE_TOKENS) + i;
+  if (!KVQ_IN_RANGE(i < c.bt_stride, status)) return 0;
+  const int page = c.bt[static_cast<int64_t>(b) * c.bt_stride + i];
+  if (page >= 0 && page < c.pB) return page;
+  report(status, KVQ_ERR_INVALID_ARG);
+  return 0;
+}
+
 constexpr int64_t kNoRow = -1;     // belongs to no usable sequence
 constexpr int64_t kBadPage = -2;   // its page lies outside the pool
 

@@ -59,7 +59,7 @@ struct CParams {
   const uint32_t* sz[2];
   int32_t* cnt;                     // [CTAs][2] arrivals at a cut segment, by its first CTA and slot
   float* ws_lse;                    // [2 * CTAs][slot_rows], log2 domain
-  float* ws_o;                      // [2 * CTAs][slot_rows][D]
+  float* ws_o;                      // [2 * CTAs][D / 4][slot_rows][4]
   void* out;
   int32_t* status;
   int32_t out_dtype, Hq, Hkv, rep, window, sinks, num_ctas, slot_rows;
@@ -87,7 +87,8 @@ struct CLayout {
   static constexpr int kOffV = kOffK + 2 * kQBytes;     // 2 stages
   static constexpr int kOffBar = kOffV + 2 * kQBytes;
   static constexpr int kOffMisc = kOffBar + B_COUNT * 8;  // TMEM address, merge flags
-  static constexpr int kOffPre = kOffMisc + 16;           // int64 [B + 1]
+  static constexpr int kOffWalk = kOffMisc + 16;          // Walk of each warp
+  static constexpr int kOffPre = kOffWalk + kThreads / 32 * 112;   // int64 [B + 1]
   static size_t bytes(int B) { return 1024 + kOffPre + static_cast<size_t>(B + 1) * 8; }
 };
 
@@ -118,7 +119,8 @@ __device__ __forceinline__ int row_blocks(const CParams& p, const chunk::Seq& s)
   return (s.n * p.rep + kRows - 1) / kRows;
 }
 
-// A CTA's walk through its range of the work list, piece by piece.
+// A warp's walk through its CTA's range of the work list, piece by piece.  It
+// lives in shared memory: the roles' loops need their registers.
 struct Walk {
   int64_t f;             // flat index of the piece's first tile
   int64_t left;          // tiles of the range from there on
@@ -127,76 +129,67 @@ struct Walk {
   Tiles t;
   int n;                 // tiles of the piece
 };
+static_assert(sizeof(Walk) <= 112, "room for a Walk per warp");
 
 __device__ __forceinline__ void open_piece(const CParams& p, Walk& w) {
   w.t = segment_tiles(p, w.s, w.rt);
   w.n = static_cast<int>(min(static_cast<int64_t>(w.t.n - w.i), w.left));
 }
-// To the next piece; false at the range's end.
-__device__ __forceinline__ bool next_piece(const CParams& p, Walk& w) {
-  w.left -= w.n;
-  w.f += w.n;
-  if (w.left <= 0) return false;
-  w.i = 0;
-  if (++w.rt >= row_blocks(p, w.s)) {
-    w.rt = 0;
-    if (++w.kvh >= p.Hkv) {
-      w.kvh = 0;
-      do {
-        ++w.b;
-        w.s = chunk::sequence(p.c, w.b);
-      } while (w.s.n == 0);
+// To the next piece (the whole warp; lane 0 does it); false at the range's end.
+__device__ __forceinline__ bool next_piece(const CParams& p, Walk& w, int lane) {
+  __syncwarp();
+  if (lane == 0) {
+    w.left -= w.n;
+    w.f += w.n;
+    if (w.left > 0) {
+      w.i = 0;
+      if (++w.rt >= row_blocks(p, w.s)) {
+        w.rt = 0;
+        if (++w.kvh >= p.Hkv) {
+          w.kvh = 0;
+          do {
+            ++w.b;
+            w.s = chunk::sequence(p.c, w.b);
+          } while (w.s.n == 0);
+        }
+      }
+      open_piece(p, w);
     }
   }
-  open_piece(p, w);
-  return true;
+  __syncwarp();
+  return w.left > 0;
 }
 
-// Tile parts of one key tile as its dequant threads read them: the storage
-// rows of its two 64-token halves (a half that nothing sees stands in for the
-// other: its rows are masked), and the rows whose scale/zero words count.
+// One key tile as its dequant threads read it: the storage blocks (64 tokens:
+// a page, or that much of a sequence) of its two halves -- a half that nothing
+// sees stands in for the other, its rows are masked -- and, in `edge`, whether
+// some of its rows are seen by no query of the segment.
 struct TileRows {
-  int64_t half[2];       // storage rows of the halves' first tokens
-  int hi, lo, sk;        // row r counts when r < hi and (r >= lo or r < sk)
+  int t0;                // the tile's first token
+  int half[2];
+  bool edge;
 };
-__device__ __forceinline__ TileRows tile_rows(const CParams& p, const Walk& w, int kt) {
+// What a segment sees, as the dequant threads keep it in registers.
+struct Seen {
+  int b, i, ns, skip;    // tile indices from i on (Tiles::tile)
+  int end, lo;           // tokens below end, from lo on or below the sinks
+};
+__device__ __forceinline__ TileRows tile_rows(const CParams& p, const Seen& w, int j) {
   TileRows r;
-  const int t0 = kt * kT, end = w.t.pos_hi + 1;
-  const int lo = p.window > 0 ? w.t.pos_lo - p.window + 1 : 0;
-  r.hi = end - t0;
-  r.lo = lo - t0;
-  r.sk = p.sinks - t0;
+  const int k = w.i + j;
+  r.t0 = (k < w.ns ? k : k + w.skip) * kT;
+  r.edge = r.t0 + kT > w.end || (r.t0 < w.lo && r.t0 + kT > p.sinks);
   bool seen[2];
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
-    const int a = t0 + h * 64;
-    seen[h] = a < end && (a + 64 > lo || a < p.sinks);
+    const int a = r.t0 + h * 64;
+    seen[h] = a < w.end && (a + 64 > w.lo || a < p.sinks);
     r.half[h] = 0;
-    if (seen[h] && KVQ_IN_RANGE(p.c.bt == nullptr || a / 64 < p.c.bt_stride, p.status)) {
-      r.half[h] = chunk::storage_row(p.c, w.b, a);
-      if (r.half[h] < 0) {   // a page outside the pool: report, read page 0 instead
-        report(p.status, KVQ_ERR_INVALID_ARG);
-        r.half[h] = 0;
-      }
-    }
+    if (seen[h]) r.half[h] = chunk::storage_block(p.c, w.b, a / 64, p.status);
   }
   if (!seen[0]) r.half[0] = r.half[1];
   if (!seen[1]) r.half[1] = r.half[0];
   return r;
-}
-
-// Cache loads: each byte is used once per CTA, so it takes no L1 line.
-__device__ __forceinline__ uint4 load_codes(const uint8_t* src) {
-  uint4 v;
-  asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
-               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-               : "l"(src));
-  return v;
-}
-__device__ __forceinline__ uint32_t load_word(const uint32_t* src) {
-  uint32_t v;
-  asm volatile("ld.global.L1::no_allocate.u32 %0, [%1];" : "=r"(v) : "l"(src));
-  return v;
 }
 
 template <int D, int BITS>
@@ -205,34 +198,24 @@ struct PartRegs {
   uint32_t w[DqFmt<D, BITS>::NI];
 };
 
-// One part (K or V) of a key tile into a dequant thread's registers.
+// One part of a key tile into a dequant thread's registers, from the thread's
+// place (row, chunk) in block 0 of the head's codes and words.
 template <int D, int BITS>
-__device__ __forceinline__ void load_part(PartRegs<D, BITS>& r, const CParams& p, int which, int kvh,
-                                          const TileRows& tr, int row, int c) {
+__device__ __forceinline__ void load_part(PartRegs<D, BITS>& r, const CParams& p, const uint8_t* codes,
+                                          const uint32_t* sz, const TileRows& tr) {
   using F = DqFmt<D, BITS>;
   constexpr int G = D / 32;
-  const int64_t storage = static_cast<int64_t>(p.c.pB) * p.c.pT;
-  const uint8_t* codes = p.codes[which] + p.plane_off[kvh] + c * 16;
-  const uint32_t* sz = p.sz[which] + kvh * storage * G + c * F::VPC / 32;
+  constexpr int H = F::NI / 2;      // iterations per half
+  const int64_t blocks = static_cast<int64_t>(p.c.pB) * (p.c.pT / 64);
 #pragma unroll
-  for (int it = 0; it < F::NI; ++it) {
-    const int64_t at = tr.half[it >= F::NI / 2] + (it % (F::NI / 2)) * F::RPI + row;
-    const uint8_t* cp = codes + at * F::R;
-    const uint32_t* sp = sz + at * G;
-    if (KVQ_IN_RANGE(at >= 0 && at < storage && cp + 16 <= p.codes[which] + p.codes_bytes, p.status)) {
-      r.c[it] = load_codes(cp);
-      r.w[it] = load_word(sp);
-    } else {
-      r.c[it] = make_uint4(0u, 0u, 0u, 0u);
-      r.w[it] = 0u;
-    }
-  }
-  // rows that nothing sees read as zeros, whatever is stored there
-  if (tr.hi < kT || tr.lo > 0) {
+  for (int h = 0; h < 2; ++h) {
+    const int blk = KVQ_IN_RANGE(tr.half[h] >= 0 && tr.half[h] < blocks, p.status) ? tr.half[h] : 0;
+    const uint8_t* cp = codes + blk * int64_t(64 * F::R);
+    const uint32_t* sp = sz + blk * int64_t(64 * G);
 #pragma unroll
-    for (int it = 0; it < F::NI; ++it) {
-      const int k = F::RPI * it + row;
-      if (k >= tr.hi || (k < tr.lo && k >= tr.sk)) r.w[it] = 0u;
+    for (int it = 0; it < H; ++it) {   // (each byte is used once per CTA: no L1 line)
+      r.c[h * H + it] = __ldcg(reinterpret_cast<const uint4*>(cp + it * F::RPI * F::R));
+      r.w[h * H + it] = __ldcg(sp + it * F::RPI * G);
     }
   }
 }
@@ -244,6 +227,24 @@ __device__ __forceinline__ void store_part(uint32_t dst, const PartRegs<D, BITS>
   for (int it = 0; it < F::NI; ++it) dequant_chunk<BITS>(dst, F::RPI * it + row, c * F::VPC, r.c[it], r.w[it]);
 }
 
+// Rows of the tile at token t0 that no query of the segment sees become zeros
+// in the operand tile, whatever is stored there (a masked weight of 0 must not
+// meet an infinity or a NaN).  Run after store_part by the threads that wrote
+// them: a test on the registers themselves, before or after their loads, cost
+// 15 % of the whole kernel, because the branch waits for loads in flight.
+template <int D, int BITS>
+__device__ __forceinline__ void clear_unseen(uint32_t dst, const Seen& w, int sinks, int t0, int row, int c) {
+  using F = DqFmt<D, BITS>;
+#pragma unroll 1
+  for (int it = 0; it < F::NI; ++it) {
+    const int r = F::RPI * it + row, j = t0 + r;
+    if (j < w.end && (j >= w.lo || j < sinks)) continue;
+    const int ch0 = c * F::VPC;
+    const uint32_t rowp = dst + (ch0 >> 6) * (kT * 128) + r * 128;
+    for (int i = 0; i < F::VPC / 8; ++i) sts128(rowp + (((((ch0 & 63) >> 3) + i) ^ (r & 7)) << 4), 0u, 0u, 0u, 0u);
+  }
+}
+
 // The piece's query rows to fp16 in the swizzled layout (rows past the
 // segment's end zero); for a 4-bit head in the channel order of its K tiles.
 template <int D>
@@ -252,7 +253,7 @@ __device__ __forceinline__ bool load_queries(const CParams& p, uint8_t* smem, ui
   using L = CLayout<D>;
   constexpr int CPR = D / 8;              // 16-byte chunks per row
   constexpr int RPP = 128 / CPR;          // rows per pass
-  constexpr int NB = 8;                   // passes in flight
+  constexpr int NB = 16;                  // passes in flight
   const int slots = w.t.rows > kT ? 2 : 1;
   const int ch = t % CPR;
   const bool four = p.bits[w.kvh] == 4;
@@ -303,31 +304,43 @@ __device__ __forceinline__ bool dequant_piece(const CParams& p, uint8_t* smem, u
                                               uint32_t& jj, uint32_t piece, int t, int lane) {
   using L = CLayout<D>;
   using F = DqFmt<D, BITS>;
+  constexpr int G = D / 32;
   static_assert(F::NI % 2 == 0, "whole iterations per half tile");
   int row, c;
   dq_lane<D, BITS>(t, row, c);
-  const uint32_t kdst = smem_u32(smem + L::kOffK);
-  const uint32_t vdst = smem_u32(smem + L::kOffV);
+  const uint32_t dst = smem_u32(smem + L::kOffK);
+  const int64_t blocks = static_cast<int64_t>(p.c.pB) * (p.c.pT / 64);
+  const int64_t coff = p.plane_off[w.kvh] + row * F::R + c * 16;
+  const int64_t soff = w.kvh * blocks * (64 * G) + row * G + c * F::VPC / 32;
+  const uint8_t* kcodes = p.codes[0] + coff;
+  const uint8_t* vcodes = p.codes[1] + coff;
+  const uint32_t* ksz = p.sz[0] + soff;
+  const uint32_t* vsz = p.sz[1] + soff;
+  const Seen seen{w.b, w.i, w.t.ns, w.t.skip, w.t.pos_hi + 1, p.window > 0 ? w.t.pos_lo - p.window + 1 : 0};
+  const int n = w.n;
   PartRegs<D, BITS> ra, rb;
-  TileRows tr = tile_rows(p, w, w.t.tile(w.i));
-  load_part<D, BITS>(ra, p, 0, w.kvh, tr, row, c);
+  TileRows tr = tile_rows(p, seen, 0);
+  load_part<D, BITS>(ra, p, kcodes, ksz, tr);
   if (!load_queries<D>(p, smem, bar, w, t, (piece - 1) & 1, piece > 0)) return false;
   fence_proxy_async_smem();
   __syncwarp();
   if (lane == 0) mbar_arrive(&bar[B_QREADY]);
-  for (int j = 0; j < w.n; ++j, ++jj) {
+  for (int j = 0; j < n; ++j, ++jj) {
     const int st = jj & 1;
-    load_part<D, BITS>(rb, p, 1, w.kvh, tr, row, c);
-    const bool more = j + 1 < w.n;
-    if (more) tr = tile_rows(p, w, w.t.tile(w.i + j + 1));
+    load_part<D, BITS>(rb, p, vcodes, vsz, tr);
+    const bool more = j + 1 < n, edge = tr.edge;
+    const int t0 = tr.t0;
+    if (more) tr = tile_rows(p, seen, j + 1);
     if (jj >= 2 && !__all_sync(0xffffffffu, mbar_wait(&bar[B_KVEMPTY0 + st], ((jj >> 1) - 1) & 1, p.status, kWaitNs)))
       return false;
-    store_part<D, BITS>(kdst + st * L::kQBytes, ra, row, c);
+    store_part<D, BITS>(dst + st * L::kQBytes, ra, row, c);
+    if (edge) clear_unseen<D, BITS>(dst + st * L::kQBytes, seen, p.sinks, t0, row, c);
     fence_proxy_async_smem();
     __syncwarp();
     if (lane == 0) mbar_arrive(&bar[B_KFULL0 + st]);
-    if (more) load_part<D, BITS>(ra, p, 0, w.kvh, tr, row, c);
-    store_part<D, BITS>(vdst + st * L::kQBytes, rb, row, c);
+    if (more) load_part<D, BITS>(ra, p, kcodes, ksz, tr);
+    store_part<D, BITS>(dst + (L::kOffV - L::kOffK) + st * L::kQBytes, rb, row, c);
+    if (edge) clear_unseen<D, BITS>(dst + (L::kOffV - L::kOffK) + st * L::kQBytes, seen, p.sinks, t0, row, c);
     fence_proxy_async_smem();
     __syncwarp();
     if (lane == 0) mbar_arrive(&bar[B_VFULL0 + st]);
@@ -363,38 +376,49 @@ __device__ __forceinline__ int64_t out_offset(const CParams& p, const Walk& w, i
   return ((static_cast<int64_t>(w.s.row0) + tok) * p.Hq + w.kvh * p.rep + hh) * D;
 }
 
-// The pieces of slot h of a segment held by CTAs c0 .. c1, merged by
-// log-sum-exp in CTA order: one warp per row, a lane per D / 32 channels.
+// Partial sums in the workspace: partial k's value 4 i + e of row r at
+// ws_o[((k * D / 4 + i) * slot_rows + r) * 4 + e], so that the threads of a
+// slot, one row each, write and read whole lines.
 template <int D>
-__device__ __forceinline__ void merge_rows(const CParams& p, const Walk& w, int h, int c0, int c1, int slot0, int warp4,
-                                           int lane) {
-  constexpr int N = D / 32;
-  const int nr = min(kT, w.t.rows - h * kT);
-  for (int r = warp4; r < nr; r += 4) {
-    float M = -INFINITY, L = 0.0f, acc[N];
+__device__ __forceinline__ float4* partial_o(const CParams& p, int k, int r) {
+  return reinterpret_cast<float4*>(p.ws_o) + static_cast<int64_t>(k) * (D / 4) * p.slot_rows + r;
+}
+
+// This row's pieces in CTAs c0 .. c1 merged by log-sum-exp in CTA order; the
+// normalised row goes to offset orow of the output.
+template <int D>
+__device__ __forceinline__ void merge_row(const CParams& p, int c0, int c1, int slot0, int r, int64_t orow) {
+  auto index = [&](int c) { return 2 * c + (c == c0 ? slot0 : 0); };
+  float M = -INFINITY, L = 0.0f;
+  for (int c = c0; c <= c1; ++c) {
+    const float lse = __ldcg(p.ws_lse + static_cast<int64_t>(index(c)) * p.slot_rows + r);
+    const float mn = fmaxf(M, lse);
+    if (mn == -INFINITY) continue;   // no piece with weight yet
+    L = L * fast_exp2(M - mn) + fast_exp2(lse - mn);
+    M = mn;
+  }
+  const float inv = L > 0.0f ? 1.0f / L : 0.0f;
+#pragma unroll 1
+  for (int i0 = 0; i0 < D / 4; i0 += 8) {
+    float o[32];
 #pragma unroll
-    for (int e = 0; e < N; ++e) acc[e] = 0.0f;
+    for (int i = 0; i < 32; ++i) o[i] = 0.0f;
     for (int c = c0; c <= c1; ++c) {
-      const int64_t at = static_cast<int64_t>(2 * c + (c == c0 ? slot0 : 0)) * p.slot_rows + h * kT + r;
-      const float lse = __ldcg(p.ws_lse + at);
-      if (lse == -INFINITY) continue;
-      float v[N];
+      const float lse = __ldcg(p.ws_lse + static_cast<int64_t>(index(c)) * p.slot_rows + r);
+      const float4* src = partial_o<D>(p, index(c), r) + static_cast<int64_t>(i0) * p.slot_rows;
+      float4 v[8];
 #pragma unroll
-      for (int e = 0; e < N; ++e) v[e] = __ldcg(p.ws_o + at * D + lane + 32 * e);
-      const float mn = fmaxf(M, lse), a = fast_exp2(M - mn), b = fast_exp2(lse - mn);
-      L = L * a + b;
+      for (int i = 0; i < 8; ++i) v[i] = __ldcg(src + static_cast<int64_t>(i) * p.slot_rows);
+      const float b = lse == -INFINITY ? 0.0f : fast_exp2(lse - M) * inv;
 #pragma unroll
-      for (int e = 0; e < N; ++e) acc[e] = acc[e] * a + b * v[e];
-      M = mn;
+      for (int i = 0; i < 8; ++i) {
+        o[4 * i] = fmaf(b, v[i].x, o[4 * i]);
+        o[4 * i + 1] = fmaf(b, v[i].y, o[4 * i + 1]);
+        o[4 * i + 2] = fmaf(b, v[i].z, o[4 * i + 2]);
+        o[4 * i + 3] = fmaf(b, v[i].w, o[4 * i + 3]);
+      }
     }
-    const float inv = L > 0.0f ? 1.0f / L : 0.0f;
-    const int64_t off = out_offset(p, w, w.rt * kRows + h * kT + r, D) + lane;
-    if (!KVQ_IN_RANGE(off >= 0 && off + 32 * (N - 1) < static_cast<int64_t>(p.c.rows) * p.Hq * D, p.status)) continue;
-#pragma unroll
-    for (int e = 0; e < N; ++e) {
-      if (p.out_dtype == KVQ_OUT_F32) static_cast<float*>(p.out)[off + 32 * e] = acc[e] * inv;
-      else static_cast<__nv_bfloat16*>(p.out)[off + 32 * e] = __float2bfloat16_rn(acc[e] * inv);
-    }
+    store_row32(p, D, orow + 4 * i0, o);
   }
 }
 
@@ -468,30 +492,28 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_attention_kernel(const __gr
   const int64_t N = p.Hkv * pre[p.c.B];
   const int C = N < p.num_ctas ? static_cast<int>(N) : p.num_ctas;
   const bool in_split = static_cast<int>(blockIdx.x) < C;
-  Walk w;
-  w.f = in_split ? N * blockIdx.x / C : 0;
-  w.left = in_split ? N * (blockIdx.x + 1) / C - w.f : 0;
-  if (w.left <= 0) {   // the whole CTA: nothing was started
+  const int64_t f0 = in_split ? N * blockIdx.x / C : 0;
+  const int64_t total = in_split ? N * (blockIdx.x + 1) / C - f0 : 0;
+  if (total <= 0) {   // the whole CTA: nothing was started
     if (warp == 0) tc::tmem_dealloc(tmem, kTmemCols);
     return;
   }
+  Walk& w = reinterpret_cast<Walk*>(smem + L::kOffWalk)[warp];
   {
-    int lo = 0, hi = p.c.B - 1;   // the last b with Hkv * pre[b] <= f: a sequence with tiles
+    int lo = 0, hi = p.c.B - 1;   // the last b with Hkv * pre[b] <= f0: a sequence with tiles
     while (lo < hi) {
       const int mid = (lo + hi + 1) >> 1;
-      if (p.Hkv * pre[mid] <= w.f) lo = mid; else hi = mid - 1;
+      if (p.Hkv * pre[mid] <= f0) lo = mid; else hi = mid - 1;
     }
-    w.b = lo;
-    w.s = chunk::sequence(p.c, w.b);
-    const int64_t per = pre[lo + 1] - pre[lo], off = w.f - p.Hkv * pre[lo];
-    w.kvh = static_cast<int>(off / per);
-    int64_t rem = off - w.kvh * per;
+    const chunk::Seq s = chunk::sequence(p.c, lo);
+    const int64_t per = pre[lo + 1] - pre[lo], off = f0 - p.Hkv * pre[lo];
+    const int kvh = static_cast<int>(off / per);
+    int64_t rem = off - kvh * per;
     // the row block: prefix sums over 32 blocks at a time
-    const int nrt = row_blocks(p, w.s);
-    w.rt = 0;
-    w.i = 0;
+    const int nrt = row_blocks(p, s);
+    int rt = 0;
     for (int r0 = 0; r0 < nrt; r0 += 32) {
-      const int64_t mine = r0 + lane < nrt ? segment_tiles(p, w.s, r0 + lane).n : 0;
+      const int64_t mine = r0 + lane < nrt ? segment_tiles(p, s, r0 + lane).n : 0;
       int64_t incl = mine;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
@@ -501,15 +523,24 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_attention_kernel(const __gr
       const unsigned past = __ballot_sync(0xffffffffu, r0 + lane < nrt && incl > rem);
       if (past != 0u) {
         const int k = __ffs(past) - 1;
-        w.rt = r0 + k;
-        w.i = static_cast<int>(rem - (__shfl_sync(0xffffffffu, incl, k) - __shfl_sync(0xffffffffu, mine, k)));
+        rt = r0 + k;
+        rem -= __shfl_sync(0xffffffffu, incl, k) - __shfl_sync(0xffffffffu, mine, k);
         break;
       }
       rem -= __shfl_sync(0xffffffffu, incl, 31);
     }
+    if (lane == 0) {
+      w.f = f0;
+      w.left = total;
+      w.b = lo;
+      w.kvh = kvh;
+      w.rt = rt;
+      w.i = static_cast<int>(rem);
+      w.s = s;
+      open_piece(p, w);
+    }
+    __syncwarp();
   }
-  open_piece(p, w);
-  const int64_t total = w.left;
 
   // Registers: launched with 128 per thread (checked on the host); per
   // warpgroup 80 + 192 + 120 + 120 = 4 x 128.
@@ -533,6 +564,17 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_attention_kernel(const __gr
       return;
     }
     if (warp == 3) {
+      // ---------------- the next piece's queries and first tile into L2 ----------------
+      bool ok = true;
+      for (uint32_t piece = 0; ok && next_piece(p, w, lane); ++piece) {
+        for (int r = lane; r < w.t.rows; r += 32) {
+          const int R = w.rt * kRows + r, tok = R / p.rep, hh = R - tok * p.rep;
+          const uint16_t* src = p.q + (w.s.row0 + tok) * p.sq_row + (w.kvh * p.rep + hh) * p.sq_head;
+          prefetch_l2_bulk(src, D * 2);
+        }
+        // (piece's queries are in shared memory: one piece ahead, no further)
+        ok = __all_sync(0xffffffffu, mbar_wait(&bar[B_QREADY], piece & 1, p.status, kWaitNs));
+      }
       if (lane == 0) mbar_arrive(&bar[B_EXIT]);
       return;
     }
@@ -644,7 +686,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_attention_kernel(const __gr
       if (!ok) break;
       ++piece;
       ++mine;
-    } while (next_piece(p, w));
+    } while (next_piece(p, w, lane));
     // every product this warp issued has completed (a commit with none
     // pending arrives at once) before the warp reports that it is done
     if (tc::elect_one()) tc::commit(&bar[B_MMADONE]);
@@ -665,7 +707,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_attention_kernel(const __gr
       ok = p.bits[w.kvh] == 4 ? dequant_piece<D, 4>(p, smem, bar, w, jj, piece, t, lane)
                               : dequant_piece<D, 8>(p, smem, bar, w, jj, piece, t, lane);
       ++piece;
-    } while (ok && next_piece(p, w));
+    } while (ok && next_piece(p, w, lane));
     __syncwarp();
     if (lane == 0) mbar_arrive(&bar[B_EXIT]);
     return;
@@ -709,7 +751,11 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_attention_kernel(const __gr
       ok = __all_sync(0xffffffffu, mbar_wait(&bar[B_SFULL0 + h], sj & 1, p.status, kWaitNs));
       if (!ok) break;
       tc::fence_after_sync();
-      auto hidden = [&](int col) { return col > lim || (col < lo && col >= sk); };
+      // the columns of 32-column chunk c that this row sees, one bit each
+      auto seen_bits = [&](int c) -> uint32_t {
+        auto below = [](int x) -> uint32_t { return x <= 0 ? 0u : x >= 32 ? 0xFFFFFFFFu : (1u << x) - 1u; };
+        return below(lim + 1 - 32 * c) & (~below(lo - 32 * c) | below(sk - 32 * c));
+      };
       float mxa = -INFINITY, mxb = -INFINITY;
       if (!masked) {
         uint32_t va[32], vb[32];
@@ -735,12 +781,20 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_attention_kernel(const __gr
       } else {
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
+          // a score that is not seen becomes -infinity, here and in TMEM: the
+          // second pass is the same for every tile (2^-infinity = 0)
           uint32_t v[32];
           tc::ld_32x32b_x32(s_addr + c * 32, v);
+          const uint32_t m = seen_bits(c);
           tc::wait_ld(v);
 #pragma unroll
-          for (int i = 0; i < 32; ++i) mxa = hidden(c * 32 + i) ? mxa : fmaxf(mxa, __uint_as_float(v[i]));
+          for (int i = 0; i < 32; ++i) {
+            if (!(m & (1u << i))) v[i] = 0xFF800000u;
+            if (i & 1) mxa = fmax3(mxa, __uint_as_float(v[i - 1]), __uint_as_float(v[i]));
+          }
+          tc::st_32x32b_x32(s_addr + c * 32, v);
         }
+        tc::wait_st();
       }
       const float m_tile = fmaxf(mxa, mxb) * sl2;
       float m_use = m_run, alpha = 1.0f;
@@ -772,54 +826,35 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_attention_kernel(const __gr
       };
       float s0 = 0.0f, s1 = 0.0f, s2 = 0.0f, s3 = 0.0f;
       const float neg_m = m_use == -INFINITY ? 0.0f : -m_use;   // (a row that sees nothing yet: every weight is 0)
-      if (!masked) {
-        uint32_t va[32], vb[32];
-        auto p_chunk = [&](const uint32_t (&v)[32], int c) {
-          uint32_t pk[16];
+      uint32_t va[32], vb[32];
+      auto p_chunk = [&](const uint32_t (&v)[32], int c) {
+        uint32_t pk[16];
 #pragma unroll
-          for (int i = 0; i < 32; i += 4) {
-            float x0, x1, x2, x3;
-            ffma2(x0, x1, __uint_as_float(v[i]), __uint_as_float(v[i + 1]), sl2, neg_m);
-            ffma2(x2, x3, __uint_as_float(v[i + 2]), __uint_as_float(v[i + 3]), sl2, neg_m);
-            const float p0 = fast_exp2(x0), p1 = fast_exp2(x1), p2 = fast_exp2(x2), p3 = fast_exp2(x3);
-            fadd2(s0, s1, p0, p1);
-            fadd2(s2, s3, p2, p3);
-            pk[i / 2] = pack_half2(p0, p1);
-            pk[i / 2 + 1] = pack_half2(p2, p3);
-          }
-          tc::st_32x32b_x16(s_addr + c * 16, pk);
-        };
-        tc::ld_32x32b_x32(s_addr, va);
-        tc::wait_ld(va);
-        tc::ld_32x32b_x32(s_addr + 32, vb);
-        p_chunk(va, 0);
-        p_first();
-        tc::wait_ld(vb);
-        tc::ld_32x32b_x32(s_addr + 64, va);
-        p_chunk(vb, 1);
-        tc::wait_ld(va);
-        tc::ld_32x32b_x32(s_addr + 96, vb);
-        p_chunk(va, 2);
-        tc::wait_ld(vb);
-        p_chunk(vb, 3);
-      } else {
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          uint32_t v[32];
-          uint32_t pk[16];
-          tc::ld_32x32b_x32(s_addr + c * 32, v);
-          tc::wait_ld(v);
-#pragma unroll
-          for (int i = 0; i < 32; i += 2) {
-            const float p0 = hidden(c * 32 + i) ? 0.0f : fast_exp2(fmaf(__uint_as_float(v[i]), sl2, neg_m));
-            const float p1 = hidden(c * 32 + i + 1) ? 0.0f : fast_exp2(fmaf(__uint_as_float(v[i + 1]), sl2, neg_m));
-            fadd2(s0, s1, p0, p1);
-            pk[i / 2] = pack_half2(p0, p1);
-          }
-          tc::st_32x32b_x16(s_addr + c * 16, pk);
-          if (c == 0) p_first();
+        for (int i = 0; i < 32; i += 4) {
+          float x0, x1, x2, x3;
+          ffma2(x0, x1, __uint_as_float(v[i]), __uint_as_float(v[i + 1]), sl2, neg_m);
+          ffma2(x2, x3, __uint_as_float(v[i + 2]), __uint_as_float(v[i + 3]), sl2, neg_m);
+          const float p0 = fast_exp2(x0), p1 = fast_exp2(x1), p2 = fast_exp2(x2), p3 = fast_exp2(x3);
+          fadd2(s0, s1, p0, p1);
+          fadd2(s2, s3, p2, p3);
+          pk[i / 2] = pack_half2(p0, p1);
+          pk[i / 2 + 1] = pack_half2(p2, p3);
         }
-      }
+        tc::st_32x32b_x16(s_addr + c * 16, pk);
+      };
+      tc::ld_32x32b_x32(s_addr, va);
+      tc::wait_ld(va);
+      tc::ld_32x32b_x32(s_addr + 32, vb);
+      p_chunk(va, 0);
+      p_first();
+      tc::wait_ld(vb);
+      tc::ld_32x32b_x32(s_addr + 64, va);
+      p_chunk(vb, 1);
+      tc::wait_ld(va);
+      tc::ld_32x32b_x32(s_addr + 96, vb);
+      p_chunk(va, 2);
+      tc::wait_ld(vb);
+      p_chunk(vb, 3);
       l_run = l_run * alpha + ((s0 + s1) + (s2 + s3));
       tc::wait_st();
       tc::fence_before_sync();
@@ -838,8 +873,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_attention_kernel(const __gr
     const int64_t seg0 = w.f - w.i;
     const int c0 = static_cast<int>(((seg0 + 1) * C - 1) / N), c1 = static_cast<int>(((seg0 + w.t.n) * C - 1) / N);
     const int slot0 = seg0 <= N * c0 / C ? 0 : 1;
-    const int64_t part = static_cast<int64_t>(2 * blockIdx.x + (static_cast<int>(blockIdx.x) == c0 ? slot0 : 0)) *
-                             p.slot_rows + h * kT + r;
+    const int part = 2 * blockIdx.x + (static_cast<int>(blockIdx.x) == c0 ? slot0 : 0);
     const int64_t orow = out_offset(p, w, R, D);
 #pragma unroll
     for (int c = 0; c < D / 32; ++c) {
@@ -858,10 +892,13 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_attention_kernel(const __gr
       if (whole) {
         store_row32(p, D, orow + c * 32, o);
       } else {
-        float4* dst = reinterpret_cast<float4*>(p.ws_o + part * D + c * 32);
+        float4* dst = partial_o<D>(p, part, h * kT + r) + static_cast<int64_t>(8 * c) * p.slot_rows;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) dst[i] = make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
-        if (c == 0) p.ws_lse[part] = l_run > 0.0f ? m_run + __log2f(l_run) : -INFINITY;
+        for (int i = 0; i < 8; ++i)
+          dst[static_cast<int64_t>(i) * p.slot_rows] = make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+        if (c == 0)
+          p.ws_lse[static_cast<int64_t>(part) * p.slot_rows + h * kT + r] =
+              l_run > 0.0f ? m_run + __log2f(l_run) : -INFINITY;
       }
     }
     tc::fence_before_sync();
@@ -878,13 +915,13 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_attention_kernel(const __gr
       group_sync();
       if (!ok) break;
       if (flag[h] == 1) {
-        merge_rows<D>(p, w, h, c0, c1, slot0, q4, lane);
+        if (live) merge_row<D>(p, c0, c1, slot0, h * kT + r, orow);
         if (threadIdx.x == 256 + h * kT) p.cnt[2 * c0 + h] = 0;   // ready for the next call
       }
       group_sync();   // the flag has been read
       if (!ok) break;
     }
-  } while (next_piece(p, w));
+  } while (next_piece(p, w, lane));
   tc::wait_st();   // P and rescaled O stores of a loop left early have landed
   tc::fence_before_sync();
   __syncwarp();
@@ -920,7 +957,7 @@ static_assert(CLayout<128>::kOffPre + 1024 + 4097 * 8 <= 232448, "shared memory 
 
 size_t align16(size_t x) { return (x + 15) & ~size_t(15); }
 
-// Workspace: [cnt: 2 per CTA][lse: 2 partials per CTA][o: the same rows of D]
+// Workspace: [cnt: 2 per CTA][lse: 2 partials per CTA][o: the same, D values a row]
 int slot_rows(int rows, int rep) {
   const int64_t all = static_cast<int64_t>(rows) * rep;
   return all < kRows ? static_cast<int>(all < 1 ? 1 : all) : kRows;
