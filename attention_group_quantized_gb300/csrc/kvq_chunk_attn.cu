@@ -23,6 +23,7 @@
 //   warps 1, 2  issue slot h = warp - 1's tcgen05.mma (S_h = Q_h K^T from
 //               shared memory, O_h += P_h V with P from TMEM), taking turns so
 //               that one slot's softmax runs under the other's products;
+//   warp 3      fetches the next piece's queries into L2;
 //   warps 4-7   per piece, its query rows to fp16; per key tile, K and V codes
 //               to fp16 operand tiles (two stages), the next part's codes in
 //               flight in registers meanwhile;
@@ -88,8 +89,8 @@ struct CLayout {
   static constexpr int kOffBar = kOffV + 2 * kQBytes;
   static constexpr int kOffMisc = kOffBar + B_COUNT * 8;  // TMEM address, merge flags
   static constexpr int kOffWalk = kOffMisc + 16;          // Walk of each warp
-  static constexpr int kOffPre = kOffWalk + kThreads / 32 * 112;   // int64 [B + 1]
-  static size_t bytes(int B) { return 1024 + kOffPre + static_cast<size_t>(B + 1) * 8; }
+  static constexpr int kOffPre = kOffWalk + kThreads / 32 * 128;   // int32 [B + 1]
+  static size_t bytes(int B) { return 1024 + kOffPre + static_cast<size_t>(B + 1) * 4; }
 };
 
 // A segment's key tiles: those that some row of the block sees, in order.
@@ -128,8 +129,10 @@ struct Walk {
   chunk::Seq s;
   Tiles t;
   int n;                 // tiles of the piece
+  int C;                 // CTAs that share the N tiles of the work list
+  int64_t N;
 };
-static_assert(sizeof(Walk) <= 112, "room for a Walk per warp");
+static_assert(sizeof(Walk) <= 128, "room for a Walk per warp");
 
 __device__ __forceinline__ void open_piece(const CParams& p, Walk& w) {
   w.t = segment_tiles(p, w.s, w.rt);
@@ -160,37 +163,52 @@ __device__ __forceinline__ bool next_piece(const CParams& p, Walk& w, int lane) 
   return w.left > 0;
 }
 
+// Tokens that a segment's queries see: below `end`, from `lo` on or below the sinks.
+struct Seen {
+  int end, lo;
+  __device__ __forceinline__ Seen(const CParams& p, const Walk& w)
+      : end(w.t.pos_hi + 1), lo(p.window > 0 ? w.t.pos_lo - p.window + 1 : 0) {}
+};
+
 // One key tile as its dequant threads read it: the storage blocks (64 tokens:
 // a page, or that much of a sequence) of its two halves -- a half that nothing
-// sees stands in for the other, its rows are masked -- and, in `edge`, whether
-// some of its rows are seen by no query of the segment.
+// sees stands in for the other, its rows are masked.  Looked up one tile ahead
+// of the loads that use it and free of branches: a branch between a load and
+// its use waits for every load in flight.
+template <bool PAGED>
 struct TileRows {
   int t0;                // the tile's first token
-  int half[2];
-  bool edge;
-};
-// What a segment sees, as the dequant threads keep it in registers.
-struct Seen {
-  int b, i, ns, skip;    // tile indices from i on (Tiles::tile)
-  int end, lo;           // tokens below end, from lo on or below the sinks
-};
-__device__ __forceinline__ TileRows tile_rows(const CParams& p, const Seen& w, int j) {
-  TileRows r;
-  const int k = w.i + j;
-  r.t0 = (k < w.ns ? k : k + w.skip) * kT;
-  r.edge = r.t0 + kT > w.end || (r.t0 < w.lo && r.t0 + kT > p.sinks);
-  bool seen[2];
-#pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    const int a = r.t0 + h * 64;
-    seen[h] = a < w.end && (a + 64 > w.lo || a < p.sinks);
-    r.half[h] = 0;
-    if (seen[h]) r.half[h] = chunk::storage_block(p.c, w.b, a / 64, p.status);
+  int half[2];           // page ids as they stand in the table, or blocks
+  __device__ __forceinline__ void look_up(const CParams& p, const Walk& w, int j) {
+    const Seen s(p, w);
+    t0 = w.t.tile(w.i + j) * kT;
+    int i0 = t0 / 64, i1 = i0 + 1;
+    const bool seen0 = t0 + 64 > s.lo || t0 < p.sinks;
+    const bool seen1 = t0 + 64 < s.end && (t0 + kT > s.lo || t0 + 64 < p.sinks);
+    i0 = seen0 ? i0 : i1;
+    i1 = seen1 ? i1 : i0;
+    if constexpr (PAGED) {
+      const int32_t* pages = p.c.bt + static_cast<int64_t>(w.b) * p.c.bt_stride;
+      const bool ok = KVQ_IN_RANGE(i0 >= 0 && i0 < p.c.bt_stride && i1 >= 0 && i1 < p.c.bt_stride, p.status);
+      half[0] = ok ? pages[i0] : 0;
+      half[1] = ok ? pages[i1] : 0;
+    } else {
+      half[0] = w.b * (p.c.pT / 64) + i0;
+      half[1] = w.b * (p.c.pT / 64) + i1;
+    }
   }
-  if (!seen[0]) r.half[0] = r.half[1];
-  if (!seen[1]) r.half[1] = r.half[0];
-  return r;
-}
+  // A page outside the pool reads as page 0 (and is reported at the piece's end).
+  __device__ __forceinline__ void check(const CParams& p, bool& bad) {
+    if constexpr (PAGED) {
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const bool out = static_cast<uint32_t>(half[h]) >= static_cast<uint32_t>(p.c.pB);
+        bad |= out;
+        half[h] = out ? 0 : half[h];
+      }
+    }
+  }
+};
 
 template <int D, int BITS>
 struct PartRegs {
@@ -198,26 +216,37 @@ struct PartRegs {
   uint32_t w[DqFmt<D, BITS>::NI];
 };
 
-// One part of a key tile into a dequant thread's registers, from the thread's
-// place (row, chunk) in block 0 of the head's codes and words.
+// A thread's place (row, chunk) in the two halves of one part of a key tile.
 template <int D, int BITS>
-__device__ __forceinline__ void load_part(PartRegs<D, BITS>& r, const CParams& p, const uint8_t* codes,
-                                          const uint32_t* sz, const TileRows& tr) {
-  using F = DqFmt<D, BITS>;
-  constexpr int G = D / 32;
-  constexpr int H = F::NI / 2;      // iterations per half
-  const int64_t blocks = static_cast<int64_t>(p.c.pB) * (p.c.pT / 64);
+struct PartPtr {
+  const uint8_t* c[2];
+  const uint32_t* w[2];
+  // codes, sz: the thread's place in block 0 of the head's codes and words
+  __device__ __forceinline__ PartPtr(const CParams& p, const uint8_t* codes, const uint32_t* sz, int half0, int half1) {
+    const int64_t blocks = static_cast<int64_t>(p.c.pB) * (p.c.pT / 64);
 #pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    const int blk = KVQ_IN_RANGE(tr.half[h] >= 0 && tr.half[h] < blocks, p.status) ? tr.half[h] : 0;
-    const uint8_t* cp = codes + blk * int64_t(64 * F::R);
-    const uint32_t* sp = sz + blk * int64_t(64 * G);
-#pragma unroll
-    for (int it = 0; it < H; ++it) {   // (each byte is used once per CTA: no L1 line)
-      r.c[h * H + it] = __ldcg(reinterpret_cast<const uint4*>(cp + it * F::RPI * F::R));
-      r.w[h * H + it] = __ldcg(sp + it * F::RPI * G);
+    for (int h = 0; h < 2; ++h) {
+      const int half = h == 0 ? half0 : half1;
+      const int blk = KVQ_IN_RANGE(half >= 0 && half < blocks, p.status) ? half : 0;
+      c[h] = codes + blk * int64_t(64 * DqFmt<D, BITS>::R);
+      w[h] = sz + blk * int64_t(64 * (D / 32));
     }
   }
+};
+
+// Iteration it of a part (each byte is used once per CTA: no L1 line).
+template <int D, int BITS>
+__device__ __forceinline__ void load_iter(PartRegs<D, BITS>& r, const PartPtr<D, BITS>& s, int it) {
+  using F = DqFmt<D, BITS>;
+  constexpr int H = F::NI / 2;      // iterations per half
+  r.c[it] = __ldcg(reinterpret_cast<const uint4*>(s.c[it / H] + (it % H) * F::RPI * F::R));
+  r.w[it] = __ldcg(s.w[it / H] + (it % H) * F::RPI * (D / 32));
+}
+
+template <int D, int BITS>
+__device__ __forceinline__ void load_part(PartRegs<D, BITS>& r, const PartPtr<D, BITS>& s) {
+#pragma unroll
+  for (int it = 0; it < DqFmt<D, BITS>::NI; ++it) load_iter<D, BITS>(r, s, it);
 }
 
 template <int D, int BITS>
@@ -227,18 +256,20 @@ __device__ __forceinline__ void store_part(uint32_t dst, const PartRegs<D, BITS>
   for (int it = 0; it < F::NI; ++it) dequant_chunk<BITS>(dst, F::RPI * it + row, c * F::VPC, r.c[it], r.w[it]);
 }
 
-// Rows of the tile at token t0 that no query of the segment sees become zeros
-// in the operand tile, whatever is stored there (a masked weight of 0 must not
-// meet an infinity or a NaN).  Run after store_part by the threads that wrote
+// Rows of the V tile at token t0 that no query of the segment sees become zeros
+// in the operand tile, whatever is stored there: a masked weight of 0 must not
+// meet an infinity or a NaN (K needs none of it, its scores are replaced).  Run after store_part by the threads that wrote
 // them: a test on the registers themselves, before or after their loads, cost
 // 15 % of the whole kernel, because the branch waits for loads in flight.
 template <int D, int BITS>
-__device__ __forceinline__ void clear_unseen(uint32_t dst, const Seen& w, int sinks, int t0, int row, int c) {
+__device__ __forceinline__ void clear_unseen(uint32_t dst, const CParams& p, const Walk& w, int t0, int row, int c) {
   using F = DqFmt<D, BITS>;
+  const Seen s(p, w);
+  if (t0 + kT <= s.end && (t0 >= s.lo || t0 + kT <= p.sinks)) return;   // the whole tile is seen by someone
 #pragma unroll 1
   for (int it = 0; it < F::NI; ++it) {
     const int r = F::RPI * it + row, j = t0 + r;
-    if (j < w.end && (j >= w.lo || j < sinks)) continue;
+    if (j < s.end && (j >= s.lo || j < p.sinks)) continue;
     const int ch0 = c * F::VPC;
     const uint32_t rowp = dst + (ch0 >> 6) * (kT * 128) + r * 128;
     for (int i = 0; i < F::VPC / 8; ++i) sts128(rowp + (((((ch0 & 63) >> 3) + i) ^ (r & 7)) << 4), 0u, 0u, 0u, 0u);
@@ -253,13 +284,13 @@ __device__ __forceinline__ bool load_queries(const CParams& p, uint8_t* smem, ui
   using L = CLayout<D>;
   constexpr int CPR = D / 8;              // 16-byte chunks per row
   constexpr int RPP = 128 / CPR;          // rows per pass
-  constexpr int NB = 16;                  // passes in flight
-  const int slots = w.t.rows > kT ? 2 : 1;
+  constexpr int NB = 8;                   // passes in flight
   const int ch = t % CPR;
   const bool four = p.bits[w.kvh] == 4;
   const uint16_t* base = p.q + w.kvh * p.rep * p.sq_head + ch * 8;
   const uint32_t dst = smem_u32(smem + L::kOffQ);
   bool finite = true;
+  const int slots = w.t.rows > kT ? 2 : 1;
   for (int r0 = 0; r0 < slots * kT; r0 += RPP * NB) {
     uint4 v[NB];
 #pragma unroll
@@ -299,51 +330,50 @@ __device__ __forceinline__ bool load_queries(const CParams& p, uint8_t* smem, ui
 
 // The key tiles of one piece: codes to fp16 operand tiles.  jj counts the
 // CTA's tiles (stage jj & 1).  False after a wait that ran out.
-template <int D, int BITS>
+template <int D, int BITS, bool PAGED>
 __device__ __forceinline__ bool dequant_piece(const CParams& p, uint8_t* smem, uint64_t* bar, const Walk& w,
-                                              uint32_t& jj, uint32_t piece, int t, int lane) {
+                                              uint32_t& jj, uint32_t piece, bool& bad, int t, int lane) {
   using L = CLayout<D>;
   using F = DqFmt<D, BITS>;
   constexpr int G = D / 32;
   static_assert(F::NI % 2 == 0, "whole iterations per half tile");
   int row, c;
   dq_lane<D, BITS>(t, row, c);
-  const uint32_t dst = smem_u32(smem + L::kOffK);
+  const uint32_t kdst = smem_u32(smem + L::kOffK);
+  constexpr uint32_t kToV = L::kOffV - L::kOffK;
   const int64_t blocks = static_cast<int64_t>(p.c.pB) * (p.c.pT / 64);
   const int64_t coff = p.plane_off[w.kvh] + row * F::R + c * 16;
   const int64_t soff = w.kvh * blocks * (64 * G) + row * G + c * F::VPC / 32;
-  const uint8_t* kcodes = p.codes[0] + coff;
-  const uint8_t* vcodes = p.codes[1] + coff;
-  const uint32_t* ksz = p.sz[0] + soff;
-  const uint32_t* vsz = p.sz[1] + soff;
-  const Seen seen{w.b, w.i, w.t.ns, w.t.skip, w.t.pos_hi + 1, p.window > 0 ? w.t.pos_lo - p.window + 1 : 0};
-  const int n = w.n;
+  TileRows<PAGED> cur, next;
+  auto k_ptr = [&](const TileRows<PAGED>& r) { return PartPtr<D, BITS>(p, p.codes[0] + coff, p.sz[0] + soff, r.half[0], r.half[1]); };
+  auto v_ptr = [&](const TileRows<PAGED>& r) { return PartPtr<D, BITS>(p, p.codes[1] + coff, p.sz[1] + soff, r.half[0], r.half[1]); };
+  auto done = [&](int which) {
+    fence_proxy_async_smem();
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&bar[which]);
+  };
   PartRegs<D, BITS> ra, rb;
-  TileRows tr = tile_rows(p, seen, 0);
-  load_part<D, BITS>(ra, p, kcodes, ksz, tr);
+  cur.look_up(p, w, 0);
+  next.look_up(p, w, min(1, w.n - 1));
+  cur.check(p, bad);
+  load_part<D, BITS>(ra, k_ptr(cur));
   if (!load_queries<D>(p, smem, bar, w, t, (piece - 1) & 1, piece > 0)) return false;
-  fence_proxy_async_smem();
-  __syncwarp();
-  if (lane == 0) mbar_arrive(&bar[B_QREADY]);
-  for (int j = 0; j < n; ++j, ++jj) {
-    const int st = jj & 1;
-    load_part<D, BITS>(rb, p, vcodes, vsz, tr);
-    const bool more = j + 1 < n, edge = tr.edge;
-    const int t0 = tr.t0;
-    if (more) tr = tile_rows(p, seen, j + 1);
+  done(B_QREADY);
+  for (int j = 0; j < w.n; ++j, ++jj) {
+    const uint32_t st = jj & 1;
+    load_part<D, BITS>(rb, v_ptr(cur));
+    const int t0 = cur.t0;
+    next.check(p, bad);
+    cur = next;
+    next.look_up(p, w, min(j + 2, w.n - 1));
     if (jj >= 2 && !__all_sync(0xffffffffu, mbar_wait(&bar[B_KVEMPTY0 + st], ((jj >> 1) - 1) & 1, p.status, kWaitNs)))
       return false;
-    store_part<D, BITS>(dst + st * L::kQBytes, ra, row, c);
-    if (edge) clear_unseen<D, BITS>(dst + st * L::kQBytes, seen, p.sinks, t0, row, c);
-    fence_proxy_async_smem();
-    __syncwarp();
-    if (lane == 0) mbar_arrive(&bar[B_KFULL0 + st]);
-    if (more) load_part<D, BITS>(ra, p, kcodes, ksz, tr);
-    store_part<D, BITS>(dst + (L::kOffV - L::kOffK) + st * L::kQBytes, rb, row, c);
-    if (edge) clear_unseen<D, BITS>(dst + (L::kOffV - L::kOffK) + st * L::kQBytes, seen, p.sinks, t0, row, c);
-    fence_proxy_async_smem();
-    __syncwarp();
-    if (lane == 0) mbar_arrive(&bar[B_VFULL0 + st]);
+    store_part<D, BITS>(kdst + st * L::kQBytes, ra, row, c);
+    done(B_KFULL0 + st);
+    if (j + 1 < w.n) load_part<D, BITS>(ra, k_ptr(cur));
+    store_part<D, BITS>(kdst + kToV + st * L::kQBytes, rb, row, c);
+    clear_unseen<D, BITS>(kdst + kToV + st * L::kQBytes, p, w, t0, row, c);
+    done(B_VFULL0 + st);
   }
   return true;
 }
@@ -422,15 +452,17 @@ __device__ __forceinline__ void merge_row(const CParams& p, int c0, int c1, int 
   }
 }
 
-template <int D>
+template <int D, bool PAGED>
 __global__ void __launch_bounds__(kThreads, 1) chunk_attention_kernel(const __grid_constant__ CParams p) {
   using L = CLayout<D>;
   extern __shared__ uint8_t smem_raw[];
-  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  // (by an offset: a pointer rounded up as an integer would lose its address
+  // space, and every access would carry a 64-bit generic address)
+  uint8_t* smem = smem_raw + (-smem_u32(smem_raw) & 1023u);
   uint64_t* bar = reinterpret_cast<uint64_t*>(smem + L::kOffBar);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::kOffMisc);
   int32_t* flag = reinterpret_cast<int32_t*>(smem + L::kOffMisc) + 1;   // merge flags of the two slots
-  int64_t* pre = reinterpret_cast<int64_t*>(smem + L::kOffPre);          // tiles of sequences 0 .. b-1, per KV head
+  int32_t* pre = reinterpret_cast<int32_t*>(smem + L::kOffPre);         // tiles of sequences 0 .. b-1, per KV head
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
   if (threadIdx.x == 0) {
@@ -460,7 +492,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_attention_kernel(const __gr
   for (int b = warp; b < p.c.B; b += kThreads / 32) {
     const chunk::Seq s = chunk::sequence(p.c, b);
     const int nrt = row_blocks(p, s);
-    int64_t n = 0;
+    int32_t n = 0;
     for (int rt = lane; rt < nrt; rt += 32) n += segment_tiles(p, s, rt).n;
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) n += __shfl_xor_sync(0xffffffffu, n, o);
@@ -468,12 +500,12 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_attention_kernel(const __gr
   }
   __syncthreads();
   if (warp == 0) {
-    int64_t carry = 0;
+    int32_t carry = 0;
     for (int b0 = 0; b0 < p.c.B; b0 += 32) {
-      int64_t n = b0 + lane < p.c.B ? pre[b0 + lane + 1] : 0;
+      int32_t n = b0 + lane < p.c.B ? pre[b0 + lane + 1] : 0;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
-        const int64_t v = __shfl_up_sync(0xffffffffu, n, o);
+        const int32_t v = __shfl_up_sync(0xffffffffu, n, o);
         if (lane >= o) n += v;
       }
       if (b0 + lane < p.c.B) pre[b0 + lane + 1] = carry + n;
@@ -489,7 +521,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_attention_kernel(const __gr
   const uint32_t tmem = *tmem_slot;
 
   // this CTA's range [f0, f1) of the N tiles; never more CTAs in the split than tiles
-  const int64_t N = p.Hkv * pre[p.c.B];
+  const int64_t N = static_cast<int64_t>(p.Hkv) * pre[p.c.B];
   const int C = N < p.num_ctas ? static_cast<int>(N) : p.num_ctas;
   const bool in_split = static_cast<int>(blockIdx.x) < C;
   const int64_t f0 = in_split ? N * blockIdx.x / C : 0;
@@ -503,10 +535,10 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_attention_kernel(const __gr
     int lo = 0, hi = p.c.B - 1;   // the last b with Hkv * pre[b] <= f0: a sequence with tiles
     while (lo < hi) {
       const int mid = (lo + hi + 1) >> 1;
-      if (p.Hkv * pre[mid] <= f0) lo = mid; else hi = mid - 1;
+      if (static_cast<int64_t>(p.Hkv) * pre[mid] <= f0) lo = mid; else hi = mid - 1;
     }
     const chunk::Seq s = chunk::sequence(p.c, lo);
-    const int64_t per = pre[lo + 1] - pre[lo], off = f0 - p.Hkv * pre[lo];
+    const int64_t per = pre[lo + 1] - pre[lo], off = f0 - static_cast<int64_t>(p.Hkv) * pre[lo];
     const int kvh = static_cast<int>(off / per);
     int64_t rem = off - kvh * per;
     // the row block: prefix sums over 32 blocks at a time
@@ -530,6 +562,8 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_attention_kernel(const __gr
       rem -= __shfl_sync(0xffffffffu, incl, 31);
     }
     if (lane == 0) {
+      w.C = C;
+      w.N = N;
       w.f = f0;
       w.left = total;
       w.b = lo;
@@ -543,9 +577,11 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_attention_kernel(const __gr
   }
 
   // Registers: launched with 128 per thread (checked on the host); per
-  // warpgroup 80 + 192 + 120 + 120 = 4 x 128.
+  // warpgroup 112 + 160 + 120 + 120 = 4 x 128 (of eight such splits the
+  // fastest: 861 us for 2048 tokens on 32K, 80 + 192 + 2 x 120 takes 910 us,
+  // 80 + 176 + 2 x 128 1064 us).
   if (warp < 4) {
-    tc::reg_dealloc<80>();
+    tc::reg_dealloc<112>();
     if (warp == 0) {
       // The other roles finish in bounded time: each stops at its first wait
       // that runs out, and a role waits at most a few times per tile.
@@ -564,15 +600,14 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_attention_kernel(const __gr
       return;
     }
     if (warp == 3) {
-      // ---------------- the next piece's queries and first tile into L2 ----------------
+      // ---------------- the next piece's queries into L2 ----------------
       bool ok = true;
       for (uint32_t piece = 0; ok && next_piece(p, w, lane); ++piece) {
         for (int r = lane; r < w.t.rows; r += 32) {
           const int R = w.rt * kRows + r, tok = R / p.rep, hh = R - tok * p.rep;
-          const uint16_t* src = p.q + (w.s.row0 + tok) * p.sq_row + (w.kvh * p.rep + hh) * p.sq_head;
-          prefetch_l2_bulk(src, D * 2);
+          prefetch_l2_bulk(p.q + (w.s.row0 + tok) * p.sq_row + (w.kvh * p.rep + hh) * p.sq_head, D * 2);
         }
-        // (piece's queries are in shared memory: one piece ahead, no further)
+        // (one piece ahead, no further)
         ok = __all_sync(0xffffffffu, mbar_wait(&bar[B_QREADY], piece & 1, p.status, kWaitNs));
       }
       if (lane == 0) mbar_arrive(&bar[B_EXIT]);
@@ -616,13 +651,13 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_attention_kernel(const __gr
     uint32_t g = 0, jj = 0, sj = 0, mine = 0, piece = 0;
     bool ok = true;
     do {
-      const int nh = w.t.rows > kT ? 2 : 1;
+      const int nh = w.t.rows > kT ? 2 : 1, n = w.n;
       if (h >= nh) {
         // a piece without slot 1: its issuer only frees what the piece's
         // barriers expect of it (and so meets every phase of them in order)
         ok = wait_all(B_QREADY, piece);
         if (ok && lane == 0) mbar_arrive(&bar[B_QEMPTY]);
-        for (int j = 0; j < w.n && ok; ++j, ++jj) {
+        for (int j = 0; j < n && ok; ++j, ++jj) {
           ok = wait_all(B_KFULL0 + (jj & 1), jj >> 1) && wait_all(B_VFULL0 + (jj & 1), jj >> 1);
           if (ok && lane == 0) mbar_arrive(&bar[B_KVEMPTY0 + (jj & 1)]);
         }
@@ -645,12 +680,12 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_attention_kernel(const __gr
       tc::fence_after_sync();
       if (tc::elect_one()) {
         issue_qk(jj & 1);
-        if (w.n == 1) free_queries();
+        if (n == 1) free_queries();
         pass_turn();
       }
       __syncwarp();
       if (turns) ++g;
-      for (int j = 0; j < w.n && ok; ++j, ++jj, ++sj) {
+      for (int j = 0; j < n && ok; ++j, ++jj, ++sj) {
         const int st = jj & 1;
         ok = wait_all(B_VFULL0 + st, jj >> 1) && wait_all(B_PFIRST0 + h, sj) && take_turn();
         // the first P.V overwrites O: the previous piece's has been read
@@ -668,15 +703,15 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_attention_kernel(const __gr
           tc::commit(&bar[B_KVEMPTY0 + st]);
         }
         __syncwarp();
-        if (j + 1 < w.n) {
+        if (j + 1 < n) {
           ok = wait_all(B_KFULL0 + ((jj + 1) & 1), (jj + 1) >> 1);
           if (!ok) break;
           tc::fence_after_sync();
         }
         if (tc::elect_one()) {
-          if (j + 1 < w.n) {
+          if (j + 1 < n) {
             issue_qk((jj + 1) & 1);
-            if (j + 2 == w.n) free_queries();
+            if (j + 2 == n) free_queries();
           }
           pass_turn();
         }
@@ -698,16 +733,17 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_attention_kernel(const __gr
   }
 
   if (warp < 8) {
-    tc::reg_alloc<192>();
+    tc::reg_alloc<160>();
     // ---------------- dequant warpgroup ----------------
     const int t = threadIdx.x - 128;
     uint32_t jj = 0, piece = 0;
-    bool ok;
+    bool ok, bad = false;
     do {
-      ok = p.bits[w.kvh] == 4 ? dequant_piece<D, 4>(p, smem, bar, w, jj, piece, t, lane)
-                              : dequant_piece<D, 8>(p, smem, bar, w, jj, piece, t, lane);
+      ok = p.bits[w.kvh] == 4 ? dequant_piece<D, 4, PAGED>(p, smem, bar, w, jj, piece, bad, t, lane)
+                              : dequant_piece<D, 8, PAGED>(p, smem, bar, w, jj, piece, bad, t, lane);
       ++piece;
     } while (ok && next_piece(p, w, lane));
+    if (bad) report(p.status, KVQ_ERR_INVALID_ARG);
     __syncwarp();
     if (lane == 0) mbar_arrive(&bar[B_EXIT]);
     return;
@@ -736,23 +772,24 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_attention_kernel(const __gr
     const bool four = p.bits[w.kvh] == 4;
     const int R = w.rt * kRows + h * kT + r;
     const bool live = h * kT + r < w.t.rows;
-    // positions: this row's, and the slot's first and last (tile-wide tests)
     const int pos0 = w.s.len - w.s.n;
     const int pos = live ? pos0 + R / p.rep : w.t.pos_hi;
-    const int slot_lo = pos0 + (w.rt * kRows + h * kT) / p.rep;
-    const int slot_hi = pos0 + (w.rt * kRows + min(h * kT + kT, w.t.rows) - 1) / p.rep;
+    // tiles with columns that some row of the slot does not see: those that
+    // begin after mask_from or before mask_below
+    const int mask_from = pos0 + (w.rt * kRows + h * kT) / p.rep - (kT - 1);
+    const int mask_below =
+        p.window > 0 ? pos0 + (w.rt * kRows + min(h * kT + kT, w.t.rows) - 1) / p.rep - p.window + 1 : 0;
     float m_run = -INFINITY, l_run = 0.0f;
     for (int j = 0; j < w.n; ++j, ++sj) {
       const int t0 = w.t.tile(w.i + j) * kT;
-      // columns past `lim`, and those from `sk` to `lo` - 1, are not seen by this row
-      const int lim = pos - t0;
-      const int lo = p.window > 0 ? pos - p.window + 1 - t0 : 0, sk = p.sinks - t0;
-      const bool masked = t0 + kT - 1 > slot_lo || (p.window > 0 && t0 < slot_hi - p.window + 1 && sk < kT);
+      const bool masked = t0 > mask_from || (t0 < mask_below && t0 + kT > p.sinks);
       ok = __all_sync(0xffffffffu, mbar_wait(&bar[B_SFULL0 + h], sj & 1, p.status, kWaitNs));
       if (!ok) break;
       tc::fence_after_sync();
-      // the columns of 32-column chunk c that this row sees, one bit each
+      // the columns of 32-column chunk c that this row sees, one bit each:
+      // up to `lim`, but for those from `sk` to `lo` - 1
       auto seen_bits = [&](int c) -> uint32_t {
+        const int lim = pos - t0, lo = p.window > 0 ? pos - p.window + 1 - t0 : 0, sk = p.sinks - t0;
         auto below = [](int x) -> uint32_t { return x <= 0 ? 0u : x >= 32 ? 0xFFFFFFFFu : (1u << x) - 1u; };
         return below(lim + 1 - 32 * c) & (~below(lo - 32 * c) | below(sk - 32 * c));
       };
@@ -871,8 +908,9 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_attention_kernel(const __gr
     // CTAs c0 .. c1 hold the segment; a CTA's piece of it is partial 0 of its
     // workspace when the segment began before the CTA's range (or with it), else 1
     const int64_t seg0 = w.f - w.i;
-    const int c0 = static_cast<int>(((seg0 + 1) * C - 1) / N), c1 = static_cast<int>(((seg0 + w.t.n) * C - 1) / N);
-    const int slot0 = seg0 <= N * c0 / C ? 0 : 1;
+    const int c0 = static_cast<int>(((seg0 + 1) * w.C - 1) / w.N);
+    const int c1 = static_cast<int>(((seg0 + w.t.n) * w.C - 1) / w.N);
+    const int slot0 = seg0 <= w.N * c0 / w.C ? 0 : 1;
     const int part = 2 * blockIdx.x + (static_cast<int>(blockIdx.x) == c0 ? slot0 : 0);
     const int64_t orow = out_offset(p, w, R, D);
 #pragma unroll
@@ -928,23 +966,23 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_attention_kernel(const __gr
   if (lane == 0) mbar_arrive(&bar[B_EXIT]);
 }
 
-// Per device and head dim, set once under a lock: the kernel's dynamic
+// Per device and instantiation, set once under a lock: the kernel's dynamic
 // shared-memory limit, and whether it was built with the 128 registers per
 // thread that the register split above assumes.  1 = ready, -2 = not usable.
 std::mutex g_prep_mu;
-int g_prep[64][2] = {};
+int g_prep[64][4] = {};
 
-template <int D>
+template <int D, bool PAGED>
 int prepare_on_current_device() {
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return -1;
   std::lock_guard<std::mutex> lock(g_prep_mu);
-  int& st = g_prep[dev][D == 128 ? 1 : 0];
+  int& st = g_prep[dev][(D == 128 ? 1 : 0) + (PAGED ? 2 : 0)];
   if (st == 0) {
     cudaFuncAttributes fa;
-    if (cudaFuncGetAttributes(&fa, chunk_attention_kernel<D>) != cudaSuccess || fa.numRegs != 128) {
+    if (cudaFuncGetAttributes(&fa, chunk_attention_kernel<D, PAGED>) != cudaSuccess || fa.numRegs != 128) {
       st = -2;
-    } else if (cudaFuncSetAttribute(chunk_attention_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    } else if (cudaFuncSetAttribute(chunk_attention_kernel<D, PAGED>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                     static_cast<int>(CLayout<D>::bytes(4096))) != cudaSuccess) {
       return -1;   // a CUDA error; try again on the next call
     } else {
@@ -953,7 +991,7 @@ int prepare_on_current_device() {
   }
   return st;
 }
-static_assert(CLayout<128>::kOffPre + 1024 + 4097 * 8 <= 232448, "shared memory of the D = 128 kernel");
+static_assert(CLayout<128>::kOffPre + 1024 + 4097 * 4 <= 232448, "shared memory of the D = 128 kernel");
 
 size_t align16(size_t x) { return (x + 15) & ~size_t(15); }
 
@@ -965,9 +1003,9 @@ int slot_rows(int rows, int rep) {
 size_t counter_bytes(int ctas) { return align16(static_cast<size_t>(ctas) * 2 * 4); }
 size_t lse_bytes(int ctas, int sr) { return align16(static_cast<size_t>(ctas) * 2 * sr * 4); }
 
-template <int D>
+template <int D, bool PAGED>
 kvq_status launch_d(const CParams& p, cudaStream_t stream) {
-  const int prep = prepare_on_current_device<D>();
+  const int prep = prepare_on_current_device<D, PAGED>();
   if (prep == -2) return KVQ_ERR_UNSUPPORTED;
   if (prep != 1) return KVQ_ERR_CUDA;
   cudaLaunchConfig_t cfg = {};
@@ -980,7 +1018,7 @@ kvq_status launch_d(const CParams& p, cudaStream_t stream) {
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, chunk_attention_kernel<D>, p) == cudaSuccess ? KVQ_OK : KVQ_ERR_CUDA;
+  return cudaLaunchKernelEx(&cfg, chunk_attention_kernel<D, PAGED>, p) == cudaSuccess ? KVQ_OK : KVQ_ERR_CUDA;
 }
 
 }  // namespace
@@ -1010,6 +1048,9 @@ kvq_status launch_chunk_attention(const ChunkAttnArgs& a, cudaStream_t stream) {
   p.window = a.window; p.sinks = a.sinks;
   p.num_ctas = device_sm_count();
   p.slot_rows = slot_rows(a.chunk.rows, p.rep);
+  // tiles of all sequences (one KV head) are counted in 32 bits
+  const int64_t blocks = static_cast<int64_t>(a.chunk.rows) * p.rep / kRows + a.chunk.B;
+  if (blocks * (a.chunk.cap / kT + 1) >= (int64_t(1) << 31)) return KVQ_ERR_UNSUPPORTED;
   uint8_t* ws = static_cast<uint8_t*>(a.ws);
   p.cnt = reinterpret_cast<int32_t*>(ws);
   p.ws_lse = reinterpret_cast<float*>(ws + counter_bytes(p.num_ctas));
@@ -1021,7 +1062,8 @@ kvq_status launch_chunk_attention(const ChunkAttnArgs& a, cudaStream_t stream) {
     p.plane_off[h] = a.layout.plane_off[h];
     p.bits[h] = a.layout.bits[h];
   }
-  return D == 128 ? launch_d<128>(p, stream) : launch_d<64>(p, stream);
+  if (p.c.bt != nullptr) return D == 128 ? launch_d<128, true>(p, stream) : launch_d<64, true>(p, stream);
+  return D == 128 ? launch_d<128, false>(p, stream) : launch_d<64, false>(p, stream);
 }
 
 }  // namespace kvq

@@ -569,3 +569,83 @@ def test_non_finite_queries_are_reported():
     b.attend(q)
     torch.cuda.synchronize()
     assert int(b.status.item()) == 6
+
+
+# ---------------------------------------------------------------- long walks: many tiles and pieces per CTA
+
+WALKS = [
+    # name, Hq, Hkv, D, bits, B, new range, ctx range, paged, window, sinks
+    ("many_pieces", 16, 8, 64, "84848484", 24, (1, 230), (900, 2000), False, 0, 0),
+    ("many_pieces_pages", 32, 8, 128, "88448844", 16, (1, 300), (500, 3000), True, 0, 0),
+    ("windows_pages", 16, 4, 128, "4", 12, (100, 600), (2000, 9000), True, 900, 70),
+    ("one_long_prompt", 8, 2, 128, "8", 1, (1500, 1500), (9000, 9000), False, 0, 0),
+    ("few_rows_long", 8, 2, 128, "84", 3, (3, 9), (20000, 40000), True, 0, 0),
+]
+
+
+@pytest.mark.parametrize("case", WALKS, ids=[c[0] for c in WALKS])
+def test_long_walks_against_the_definition_on_the_device(case):
+    """Shapes whose CTAs walk tens of tiles over several segments; the reference is the definition in fp64 on the
+    values that dequantize reads back (tested bit for bit above)."""
+    kvq = _kvq()
+    name, Hq, Hkv, D, bits, B, nr, cr, paged, window, sinks = case
+    rng = np.random.default_rng(61)
+    new = rng.integers(nr[0], nr[1] + 1, B)
+    lens = new + rng.integers(cr[0], cr[1] + 1, B)
+    cap = -(-int(lens.max()) // 64) * 64
+    hb = np.array([int(b) for b in (bits if len(bits) == Hkv else bits * (Hkv // len(bits)))], np.int8)
+    bt = None
+    if paged:
+        pages = cap // 64
+        bt = torch.from_numpy(rng.permutation(B * pages + 3)[:B * pages].reshape(B, pages).astype(np.int32)).cuda()
+        kc, vc = (kvq.empty_page_pool(hb, B * pages + 3, D) for _ in "kv")
+    else:
+        kc, vc = (kvq.empty_cache(hb, B, cap, D) for _ in "kv")
+    for c in (kc, vc):
+        c.codes.fill_(SENT_CODE)
+        c.sz.fill_(SENT_WORD)
+    gen = torch.Generator(device="cuda").manual_seed(62)
+    dev = lambda a: torch.tensor(np.asarray(a), dtype=torch.int32, device="cuda")
+    whole, d_lens = dev(np.concatenate([[0], np.cumsum(lens)])), dev(lens)
+    start, rows = np.concatenate([[0], np.cumsum(new)]), int(new.sum())
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    total = int(lens.sum())
+    k, v = (torch.randn((total, Hkv, D), generator=gen, device="cuda").bfloat16() for _ in "kv")
+    q = torch.randn((rows, Hq, D), generator=gen, device="cuda").bfloat16()
+    tab = () if bt is None else (bt,)
+    sfx = "" if bt is None else "_paged"
+    getattr(kvq, "append_chunk" + sfx)(k, v, kc, vc, *tab, whole, d_lens, status=status)
+    read = getattr(kvq, "dequantize" + sfx)
+    kd, vd = (read(c, *tab, whole, d_lens, total, out_dtype=kvq.OUT_F32, status=status) for c in (kc, vc))
+    ws = kvq.chunk_workspace(rows, B, Hq, Hkv, D)
+    attend = getattr(kvq, "chunk_attention" + sfx)
+    out = None
+    for _ in range(3):
+        prev, out = out, attend(q, kc, vc, *tab, dev(start), d_lens, window=window, sinks=sinks, workspace=ws,
+                                max_chunk=int(new.max()), status=status)
+        torch.cuda.synchronize()
+        assert int(status.item()) == 0
+        assert prev is None or torch.equal(prev, out)
+    off = np.concatenate([[0], np.cumsum(lens)])
+    rep = Hq // Hkv
+    worst = 0.0
+    for b in range(B):
+        n, L = int(new[b]), int(lens[b])
+        pos = torch.arange(L - n, L, device="cuda")[:, None]
+        j = torch.arange(L, device="cuda")[None]
+        see = j <= pos
+        if window:
+            see &= (j > pos - window) | (j < sinks)
+        for h in range(Hq):
+            kk = kd[off[b]:off[b] + L, h // rep].double()
+            vv = vd[off[b]:off[b] + L, h // rep].double()
+            qq = q[start[b]:start[b] + n, h].double()
+            s = (qq @ kk.T * D ** -0.5).masked_fill_(~see, float("-inf"))
+            p = torch.softmax(s, 1)
+            A = p @ vv.abs()
+            E = D ** -0.5 * 2.0 ** -11 * (qq.abs() @ kk.abs().T).masked_fill_(~see, 0.0).amax(1, keepdim=True)
+            bound = A * (2.0 ** -10 + torch.expm1(2 * E) + 2.0 ** -13) + 1e-7      # as attention_and_bound
+            err = (out[start[b]:start[b] + n, h].double() - p @ vv).abs()
+            worst = max(worst, float((err / bound).max()))
+            assert torch.isfinite(err).all()
+    assert worst <= 1.0, worst
