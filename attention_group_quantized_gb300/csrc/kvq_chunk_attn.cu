@@ -36,7 +36,7 @@
 #include <cstring>
 #include <mutex>
 
-#include "kvq_chunk.cuh"
+#include "kvq_chunk_walk.cuh"
 #include "kvq_internal.h"
 #include "kvq_tc.cuh"
 #include "kvq_tile.cuh"
@@ -45,30 +45,11 @@ namespace kvq {
 namespace {
 
 using namespace tile;
+using namespace chunk_walk;
 
 constexpr int kThreads = 512;
 constexpr int kRows = 2 * kT;          // packed rows per segment
 constexpr uint32_t kTmemCols = 512;
-constexpr float kRescaleThreshold = 8.0f;  // log2 units
-constexpr uint64_t kWaitNs = kDefaultWaitLimitNs;
-
-struct CParams {
-  chunk::View c;
-  const uint16_t* q;
-  int64_t sq_row, sq_head;
-  const uint8_t* codes[2];          // K, V code buffers
-  const uint32_t* sz[2];
-  int32_t* cnt;                     // [CTAs][2] arrivals at a cut segment, by its first CTA and slot
-  float* ws_lse;                    // [2 * CTAs][slot_rows], log2 domain
-  float* ws_o;                      // [2 * CTAs][D / 4][slot_rows][4]
-  void* out;
-  int32_t* status;
-  int32_t out_dtype, Hq, Hkv, rep, window, sinks, num_ctas, slot_rows;
-  float scale_log2;
-  int64_t codes_bytes;              // size of each code buffer (the debug build's index checks)
-  int64_t plane_off[KVQ_MAX_HKV];
-  int8_t bits[KVQ_MAX_HKV];
-};
 
 enum {
   B_QREADY = 0, B_QEMPTY, B_KFULL0, B_KFULL1, B_VFULL0, B_VFULL1, B_KVEMPTY0, B_KVEMPTY1, B_SFULL0, B_SFULL1,
@@ -91,83 +72,6 @@ struct CLayout {
   static constexpr int kOffWalk = kOffMisc + 16;          // Walk of each warp
   static constexpr int kOffPre = kOffWalk + kThreads / 32 * 128;   // int32 [B + 1]
   static size_t bytes(int B) { return 1024 + kOffPre + static_cast<size_t>(B + 1) * 4; }
-};
-
-// A segment's key tiles: those that some row of the block sees, in order.
-// Index i of the list is tile (i < ns ? i : i + skip).
-struct Tiles {
-  int n, ns, skip;
-  int pos_lo, pos_hi;    // positions of the block's first and last row
-  int rows;              // its rows
-  __device__ __forceinline__ int tile(int i) const { return i < ns ? i : i + skip; }
-};
-__device__ __forceinline__ Tiles segment_tiles(const CParams& p, const chunk::Seq& s, int rt) {
-  Tiles t;
-  t.rows = min(kRows, s.n * p.rep - rt * kRows);
-  t.pos_lo = s.len - s.n + rt * kRows / p.rep;
-  t.pos_hi = s.len - s.n + (rt * kRows + t.rows - 1) / p.rep;
-  t.n = t.pos_hi / kT + 1;
-  t.ns = t.skip = 0;
-  if (p.window > 0) {
-    const int fw = max(t.pos_lo - p.window + 1, 0) / kT;
-    t.ns = min((min(p.sinks, t.pos_hi + 1) + kT - 1) / kT, fw);
-    t.skip = fw - t.ns;
-    t.n -= t.skip;
-  }
-  return t;
-}
-__device__ __forceinline__ int row_blocks(const CParams& p, const chunk::Seq& s) {
-  return (s.n * p.rep + kRows - 1) / kRows;
-}
-
-// A warp's walk through its CTA's range of the work list, piece by piece.  It
-// lives in shared memory: the roles' loops need their registers.
-struct Walk {
-  int64_t f;             // flat index of the piece's first tile
-  int64_t left;          // tiles of the range from there on
-  int b, kvh, rt, i;     // the piece starts at tile index i of this segment
-  chunk::Seq s;
-  Tiles t;
-  int n;                 // tiles of the piece
-  int C;                 // CTAs that share the N tiles of the work list
-  int64_t N;
-};
-static_assert(sizeof(Walk) <= 128, "room for a Walk per warp");
-
-__device__ __forceinline__ void open_piece(const CParams& p, Walk& w) {
-  w.t = segment_tiles(p, w.s, w.rt);
-  w.n = static_cast<int>(min(static_cast<int64_t>(w.t.n - w.i), w.left));
-}
-// To the next piece (the whole warp; lane 0 does it); false at the range's end.
-__device__ __forceinline__ bool next_piece(const CParams& p, Walk& w, int lane) {
-  __syncwarp();
-  if (lane == 0) {
-    w.left -= w.n;
-    w.f += w.n;
-    if (w.left > 0) {
-      w.i = 0;
-      if (++w.rt >= row_blocks(p, w.s)) {
-        w.rt = 0;
-        if (++w.kvh >= p.Hkv) {
-          w.kvh = 0;
-          do {
-            ++w.b;
-            w.s = chunk::sequence(p.c, w.b);
-          } while (w.s.n == 0);
-        }
-      }
-      open_piece(p, w);
-    }
-  }
-  __syncwarp();
-  return w.left > 0;
-}
-
-// Tokens that a segment's queries see: below `end`, from `lo` on or below the sinks.
-struct Seen {
-  int end, lo;
-  __device__ __forceinline__ Seen(const CParams& p, const Walk& w)
-      : end(w.t.pos_hi + 1), lo(p.window > 0 ? w.t.pos_lo - p.window + 1 : 0) {}
 };
 
 // One key tile as its dequant threads read it: the storage blocks (64 tokens:
@@ -256,78 +160,6 @@ __device__ __forceinline__ void store_part(uint32_t dst, const PartRegs<D, BITS>
   for (int it = 0; it < F::NI; ++it) dequant_chunk<BITS>(dst, F::RPI * it + row, c * F::VPC, r.c[it], r.w[it]);
 }
 
-// Rows of the V tile at token t0 that no query of the segment sees become zeros
-// in the operand tile, whatever is stored there: a masked weight of 0 must not
-// meet an infinity or a NaN (K needs none of it, its scores are replaced).  Run after store_part by the threads that wrote
-// them: a test on the registers themselves, before or after their loads, cost
-// 15 % of the whole kernel, because the branch waits for loads in flight.
-template <int D, int BITS>
-__device__ __forceinline__ void clear_unseen(uint32_t dst, const CParams& p, const Walk& w, int t0, int row, int c) {
-  using F = DqFmt<D, BITS>;
-  const Seen s(p, w);
-  if (t0 + kT <= s.end && (t0 >= s.lo || t0 + kT <= p.sinks)) return;   // the whole tile is seen by someone
-#pragma unroll 1
-  for (int it = 0; it < F::NI; ++it) {
-    const int r = F::RPI * it + row, j = t0 + r;
-    if (j < s.end && (j >= s.lo || j < p.sinks)) continue;
-    const int ch0 = c * F::VPC;
-    const uint32_t rowp = dst + (ch0 >> 6) * (kT * 128) + r * 128;
-    for (int i = 0; i < F::VPC / 8; ++i) sts128(rowp + (((((ch0 & 63) >> 3) + i) ^ (r & 7)) << 4), 0u, 0u, 0u, 0u);
-  }
-}
-
-// The piece's query rows to fp16 in the swizzled layout (rows past the
-// segment's end zero); for a 4-bit head in the channel order of its K tiles.
-template <int D>
-__device__ __forceinline__ bool load_queries(const CParams& p, uint8_t* smem, uint64_t* bar, const Walk& w, int t,
-                                             uint32_t qempty_parity, bool wait) {
-  using L = CLayout<D>;
-  constexpr int CPR = D / 8;              // 16-byte chunks per row
-  constexpr int RPP = 128 / CPR;          // rows per pass
-  constexpr int NB = 8;                   // passes in flight
-  const int ch = t % CPR;
-  const bool four = p.bits[w.kvh] == 4;
-  const uint16_t* base = p.q + w.kvh * p.rep * p.sq_head + ch * 8;
-  const uint32_t dst = smem_u32(smem + L::kOffQ);
-  bool finite = true;
-  const int slots = w.t.rows > kT ? 2 : 1;
-  for (int r0 = 0; r0 < slots * kT; r0 += RPP * NB) {
-    uint4 v[NB];
-#pragma unroll
-    for (int k = 0; k < NB; ++k) {
-      const int r = r0 + k * RPP + t / CPR;
-      v[k] = make_uint4(0u, 0u, 0u, 0u);
-      if (r < w.t.rows) {
-        const int R = w.rt * kRows + r, tok = R / p.rep, hh = R - tok * p.rep;
-        v[k] = *reinterpret_cast<const uint4*>(base + (w.s.row0 + tok) * p.sq_row + hh * p.sq_head);
-      }
-    }
-    if (r0 == 0 && wait &&
-        !__all_sync(0xffffffffu, mbar_wait(&bar[B_QEMPTY], qempty_parity, p.status, kWaitNs)))
-      return false;
-#pragma unroll
-    for (int k = 0; k < NB; ++k) {
-      const int r = r0 + k * RPP + t / CPR;
-      uint32_t x[4] = {v[k].x, v[k].y, v[k].z, v[k].w};
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const float lo = __uint_as_float(x[e] << 16), hi = __uint_as_float(x[e] & 0xFFFF0000u);
-        finite &= fabsf(lo) < 65504.0f && fabsf(hi) < 65504.0f;
-        x[e] = pack_half2(lo, hi);
-      }
-      if (four) {   // channels 0,4,1,5,2,6,3,7
-        const uint32_t a = prmt(x[0], x[2], 0x5410u), b = prmt(x[0], x[2], 0x7632u);
-        const uint32_t c = prmt(x[1], x[3], 0x5410u), d = prmt(x[1], x[3], 0x7632u);
-        x[0] = a; x[1] = b; x[2] = c; x[3] = d;
-      }
-      const uint32_t rowp = dst + (r / kT) * L::kQBytes + (ch >> 3) * (kT * 128) + (r % kT) * 128;
-      sts128(rowp + (((ch & 7) ^ (r & 7)) << 4), x[0], x[1], x[2], x[3]);
-    }
-  }
-  if (!finite) report(p.status, KVQ_ERR_NONFINITE);
-  return true;
-}
-
 // The key tiles of one piece: codes to fp16 operand tiles.  jj counts the
 // CTA's tiles (stage jj & 1).  False after a wait that ran out.
 template <int D, int BITS, bool PAGED>
@@ -357,7 +189,7 @@ __device__ __forceinline__ bool dequant_piece(const CParams& p, uint8_t* smem, u
   next.look_up(p, w, min(1, w.n - 1));
   cur.check(p, bad);
   load_part<D, BITS>(ra, k_ptr(cur));
-  if (!load_queries<D>(p, smem, bar, w, t, (piece - 1) & 1, piece > 0)) return false;
+  if (!load_queries<D, kT, kRows>(p, smem_u32(smem + L::kOffQ), &bar[B_QEMPTY], w, t, (piece - 1) & 1, piece > 0)) return false;
   done(B_QREADY);
   for (int j = 0; j < w.n; ++j, ++jj) {
     const uint32_t st = jj & 1;
@@ -400,13 +232,7 @@ __device__ __forceinline__ void store_row32(const CParams& p, int D, int64_t off
   }
 }
 
-// Output offset of packed row R of a sequence and KV head.
-__device__ __forceinline__ int64_t out_offset(const CParams& p, const Walk& w, int R, int D) {
-  const int tok = R / p.rep, hh = R - tok * p.rep;
-  return ((static_cast<int64_t>(w.s.row0) + tok) * p.Hq + w.kvh * p.rep + hh) * D;
-}
-
-// Partial sums in the workspace: partial k's value 4 i + e of row r at
+// Partial sums in the workspace, [2 * CTAs][D / 4][slot_rows][4]: partial k's value 4 i + e of row r at
 // ws_o[((k * D / 4 + i) * slot_rows + r) * 4 + e], so that the threads of a
 // slot, one row each, write and read whole lines.
 template <int D>
@@ -417,11 +243,10 @@ __device__ __forceinline__ float4* partial_o(const CParams& p, int k, int r) {
 // This row's pieces in CTAs c0 .. c1 merged by log-sum-exp in CTA order; the
 // normalised row goes to offset orow of the output.
 template <int D>
-__device__ __forceinline__ void merge_row(const CParams& p, int c0, int c1, int slot0, int r, int64_t orow) {
-  auto index = [&](int c) { return 2 * c + (c == c0 ? slot0 : 0); };
+__device__ __forceinline__ void merge_row(const CParams& p, const Cut& cut, int r, int64_t orow) {
   float M = -INFINITY, L = 0.0f;
-  for (int c = c0; c <= c1; ++c) {
-    const float lse = __ldcg(p.ws_lse + static_cast<int64_t>(index(c)) * p.slot_rows + r);
+  for (int c = cut.c0; c <= cut.c1; ++c) {
+    const float lse = __ldcg(p.ws_lse + static_cast<int64_t>(cut.partial(c)) * p.slot_rows + r);
     const float mn = fmaxf(M, lse);
     if (mn == -INFINITY) continue;   // no piece with weight yet
     L = L * fast_exp2(M - mn) + fast_exp2(lse - mn);
@@ -433,9 +258,9 @@ __device__ __forceinline__ void merge_row(const CParams& p, int c0, int c1, int 
     float o[32];
 #pragma unroll
     for (int i = 0; i < 32; ++i) o[i] = 0.0f;
-    for (int c = c0; c <= c1; ++c) {
-      const float lse = __ldcg(p.ws_lse + static_cast<int64_t>(index(c)) * p.slot_rows + r);
-      const float4* src = partial_o<D>(p, index(c), r) + static_cast<int64_t>(i0) * p.slot_rows;
+    for (int c = cut.c0; c <= cut.c1; ++c) {
+      const float lse = __ldcg(p.ws_lse + static_cast<int64_t>(cut.partial(c)) * p.slot_rows + r);
+      const float4* src = partial_o<D>(p, cut.partial(c), r) + static_cast<int64_t>(i0) * p.slot_rows;
       float4 v[8];
 #pragma unroll
       for (int i = 0; i < 8; ++i) v[i] = __ldcg(src + static_cast<int64_t>(i) * p.slot_rows);
@@ -488,30 +313,10 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_attention_kernel(const __gr
   grid_dependency_wait();
   grid_launch_dependents();
   if (blockIdx.x == 0) chunk::check_sequences(p.c, threadIdx.x, kThreads, p.status);
-  // tiles per sequence (one KV head): a warp per sequence, a lane per row block
-  for (int b = warp; b < p.c.B; b += kThreads / 32) {
-    const chunk::Seq s = chunk::sequence(p.c, b);
-    const int nrt = row_blocks(p, s);
-    int32_t n = 0;
-    for (int rt = lane; rt < nrt; rt += 32) n += segment_tiles(p, s, rt).n;
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) n += __shfl_xor_sync(0xffffffffu, n, o);
-    if (lane == 0) pre[b + 1] = n;
-  }
+  count_tiles<kRows>(p, pre, warp, lane, kThreads / 32);
   __syncthreads();
   if (warp == 0) {
-    int32_t carry = 0;
-    for (int b0 = 0; b0 < p.c.B; b0 += 32) {
-      int32_t n = b0 + lane < p.c.B ? pre[b0 + lane + 1] : 0;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int32_t v = __shfl_up_sync(0xffffffffu, n, o);
-        if (lane >= o) n += v;
-      }
-      if (b0 + lane < p.c.B) pre[b0 + lane + 1] = carry + n;
-      carry += __shfl_sync(0xffffffffu, n, 31);
-    }
-    if (lane == 0) pre[0] = 0;
+    sum_tiles(p, pre, lane);
     tc::tmem_alloc(tmem_slot, kTmemCols);
     tc::tmem_relinquish();
   }
@@ -520,60 +325,11 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_attention_kernel(const __gr
   tc::fence_after_sync();
   const uint32_t tmem = *tmem_slot;
 
-  // this CTA's range [f0, f1) of the N tiles; never more CTAs in the split than tiles
-  const int64_t N = static_cast<int64_t>(p.Hkv) * pre[p.c.B];
-  const int C = N < p.num_ctas ? static_cast<int>(N) : p.num_ctas;
-  const bool in_split = static_cast<int>(blockIdx.x) < C;
-  const int64_t f0 = in_split ? N * blockIdx.x / C : 0;
-  const int64_t total = in_split ? N * (blockIdx.x + 1) / C - f0 : 0;
+  Walk& w = reinterpret_cast<Walk*>(smem + L::kOffWalk)[warp];
+  const int64_t total = start_walk<kRows>(p, pre, w, lane);
   if (total <= 0) {   // the whole CTA: nothing was started
     if (warp == 0) tc::tmem_dealloc(tmem, kTmemCols);
     return;
-  }
-  Walk& w = reinterpret_cast<Walk*>(smem + L::kOffWalk)[warp];
-  {
-    int lo = 0, hi = p.c.B - 1;   // the last b with Hkv * pre[b] <= f0: a sequence with tiles
-    while (lo < hi) {
-      const int mid = (lo + hi + 1) >> 1;
-      if (static_cast<int64_t>(p.Hkv) * pre[mid] <= f0) lo = mid; else hi = mid - 1;
-    }
-    const chunk::Seq s = chunk::sequence(p.c, lo);
-    const int64_t per = pre[lo + 1] - pre[lo], off = f0 - static_cast<int64_t>(p.Hkv) * pre[lo];
-    const int kvh = static_cast<int>(off / per);
-    int64_t rem = off - kvh * per;
-    // the row block: prefix sums over 32 blocks at a time
-    const int nrt = row_blocks(p, s);
-    int rt = 0;
-    for (int r0 = 0; r0 < nrt; r0 += 32) {
-      const int64_t mine = r0 + lane < nrt ? segment_tiles(p, s, r0 + lane).n : 0;
-      int64_t incl = mine;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int64_t v = __shfl_up_sync(0xffffffffu, incl, o);
-        if (lane >= o) incl += v;
-      }
-      const unsigned past = __ballot_sync(0xffffffffu, r0 + lane < nrt && incl > rem);
-      if (past != 0u) {
-        const int k = __ffs(past) - 1;
-        rt = r0 + k;
-        rem -= __shfl_sync(0xffffffffu, incl, k) - __shfl_sync(0xffffffffu, mine, k);
-        break;
-      }
-      rem -= __shfl_sync(0xffffffffu, incl, 31);
-    }
-    if (lane == 0) {
-      w.C = C;
-      w.N = N;
-      w.f = f0;
-      w.left = total;
-      w.b = lo;
-      w.kvh = kvh;
-      w.rt = rt;
-      w.i = static_cast<int>(rem);
-      w.s = s;
-      open_piece(p, w);
-    }
-    __syncwarp();
   }
 
   // Registers: launched with 128 per thread (checked on the host); per
@@ -602,7 +358,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_attention_kernel(const __gr
     if (warp == 3) {
       // ---------------- the next piece's queries into L2 ----------------
       bool ok = true;
-      for (uint32_t piece = 0; ok && next_piece(p, w, lane); ++piece) {
+      for (uint32_t piece = 0; ok && next_piece<kRows>(p, w, lane); ++piece) {
         for (int r = lane; r < w.t.rows; r += 32) {
           const int R = w.rt * kRows + r, tok = R / p.rep, hh = R - tok * p.rep;
           prefetch_l2_bulk(p.q + (w.s.row0 + tok) * p.sq_row + (w.kvh * p.rep + hh) * p.sq_head, D * 2);
@@ -721,7 +477,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_attention_kernel(const __gr
       if (!ok) break;
       ++piece;
       ++mine;
-    } while (next_piece(p, w, lane));
+    } while (next_piece<kRows>(p, w, lane));
     // every product this warp issued has completed (a commit with none
     // pending arrives at once) before the warp reports that it is done
     if (tc::elect_one()) tc::commit(&bar[B_MMADONE]);
@@ -742,7 +498,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_attention_kernel(const __gr
       ok = p.bits[w.kvh] == 4 ? dequant_piece<D, 4, PAGED>(p, smem, bar, w, jj, piece, bad, t, lane)
                               : dequant_piece<D, 8, PAGED>(p, smem, bar, w, jj, piece, bad, t, lane);
       ++piece;
-    } while (ok && next_piece(p, w, lane));
+    } while (ok && next_piece<kRows>(p, w, lane));
     if (bad) report(p.status, KVQ_ERR_INVALID_ARG);
     __syncwarp();
     if (lane == 0) mbar_arrive(&bar[B_EXIT]);
@@ -905,13 +661,8 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_attention_kernel(const __gr
     tc::fence_after_sync();
     const float inv = l_run > 0.0f ? 1.0f / l_run : 0.0f;
     const bool whole = w.n == w.t.n;
-    // CTAs c0 .. c1 hold the segment; a CTA's piece of it is partial 0 of its
-    // workspace when the segment began before the CTA's range (or with it), else 1
-    const int64_t seg0 = w.f - w.i;
-    const int c0 = static_cast<int>(((seg0 + 1) * w.C - 1) / w.N);
-    const int c1 = static_cast<int>(((seg0 + w.t.n) * w.C - 1) / w.N);
-    const int slot0 = seg0 <= w.N * c0 / w.C ? 0 : 1;
-    const int part = 2 * blockIdx.x + (static_cast<int>(blockIdx.x) == c0 ? slot0 : 0);
+    const Cut cut(w);
+    const int part = cut.partial(blockIdx.x);
     const int64_t orow = out_offset(p, w, R, D);
 #pragma unroll
     for (int c = 0; c < D / 32; ++c) {
@@ -949,17 +700,17 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_attention_kernel(const __gr
       // covers the group's stores, its acquire the other pieces' (released by
       // their own arrivals) for the last arriver
       if (threadIdx.x == 256 + h * kT)
-        flag[h] = atom_add_acq_rel_gpu(p.cnt + 2 * c0 + h, 1) + 1 == c1 - c0 + 1 ? 1 : 0;
+        flag[h] = atom_add_acq_rel_gpu(p.cnt + 2 * cut.c0 + h, 1) + 1 == cut.c1 - cut.c0 + 1 ? 1 : 0;
       group_sync();
       if (!ok) break;
       if (flag[h] == 1) {
-        if (live) merge_row<D>(p, c0, c1, slot0, h * kT + r, orow);
-        if (threadIdx.x == 256 + h * kT) p.cnt[2 * c0 + h] = 0;   // ready for the next call
+        if (live) merge_row<D>(p, cut, h * kT + r, orow);
+        if (threadIdx.x == 256 + h * kT) p.cnt[2 * cut.c0 + h] = 0;   // ready for the next call
       }
       group_sync();   // the flag has been read
       if (!ok) break;
     }
-  } while (next_piece(p, w, lane));
+  } while (next_piece<kRows>(p, w, lane));
   tc::wait_st();   // P and rescaled O stores of a loop left early have landed
   tc::fence_before_sync();
   __syncwarp();
@@ -1062,6 +813,10 @@ kvq_status launch_chunk_attention(const ChunkAttnArgs& a, cudaStream_t stream) {
     p.plane_off[h] = a.layout.plane_off[h];
     p.bits[h] = a.layout.bits[h];
   }
+  // At most 64 rows of a (sequence, KV head): the kernel that puts the keys on
+  // the rows' side (a 128-row query tile would be half empty).
+  const int64_t max_rows = static_cast<int64_t>(p.c.max_chunk) * p.rep;
+  if (chunk_narrow_takes(p.c.B, max_rows)) return launch_chunk_narrow(p, D, max_rows, stream);
   if (p.c.bt != nullptr) return D == 128 ? launch_d<128, true>(p, stream) : launch_d<64, true>(p, stream);
   return D == 128 ? launch_d<128, false>(p, stream) : launch_d<64, false>(p, stream);
 }

@@ -1,0 +1,682 @@
+// kvq_chunk_narrow.cu -- chunk attention of few rows per KV head (drafted
+// tokens, short chunks, single tokens next to them): the same work as
+// kvq_chunk_attn.cu, with the keys on the tensor cores' row side.
+//
+// With at most 64 packed rows (token * rep + head) a 128-row query tile is
+// mostly empty, and what bounds the call is the cache read.  So a key tile is
+// the M side of both products,
+//   S^T [128 keys x NR rows]      = K [keys x D]      Q^T [D x rows]
+//   O^T [D channels x NR rows]   += V^T [channels x keys] P^T [keys x rows]
+// and the softmax works on NR = 16, 32 or 64 columns: a thread has one key's
+// scores, a row's running max lives in shared memory and moves only when a
+// score exceeds it by more than 2^8 (a vote of the four warps a tile), and the
+// sums are per thread until the piece ends.
+//
+// One CTA (512 threads, one per SM) walks its range of the work list
+// (kvq_chunk_walk.cuh):
+//   warp 0       TMEM; warp 1 issues the products; warp 2 keeps rings of raw
+//                code slots full by bulk copies (about 50 KB in flight an SM,
+//                which is what the latency of HBM asks for);
+//   warps 4-7    K codes (and the piece's queries) to fp16 operand tiles;
+//   warps 8-11   V codes likewise;
+//   warps 12-15  softmax, rescaling, the piece's output or partial, the merge.
+// TMEM: S^T twice NR columns, O^T NR columns.
+#include <cmath>
+#include <mutex>
+
+#include "kvq_chunk_walk.cuh"
+#include "kvq_internal.h"
+#include "kvq_tc.cuh"
+#include "kvq_tile.cuh"
+
+namespace kvq {
+namespace {
+
+using namespace tile;
+using namespace chunk_walk;
+
+constexpr int kThreads = 512;
+constexpr int kRing = 6;               // raw slots of K, and as many of V
+
+enum {
+  B_QREADY = 0, B_QEMPTY, B_FULL0, B_EMPTY0 = B_FULL0 + 4, B_SFULL0 = B_EMPTY0 + 4, B_PFULL = B_SFULL0 + 2, B_PDONE,
+  B_OFREE, B_MMADONE, B_EXIT, B_RAW0, B_RFREE0 = B_RAW0 + 2 * kRing, B_COUNT = B_RFREE0 + 2 * kRing
+};   // FULL and EMPTY: K stages 0, 1, V stages 0, 1; RAW and RFREE: K slots, V slots
+// Every warp but warp 0 arrives once on B_EXIT when it is done with shared
+// memory, TMEM and its asynchronous operations; warp 0 frees TMEM after that.
+constexpr int kExitArrivals = kThreads / 32 - 1;
+
+template <int D, int NR>
+struct NLayout {
+  static constexpr int kTile = kT * D * 2;              // one K or V operand tile
+  static constexpr int kOffK = 0;                       // 2 stages
+  static constexpr int kOffV = kOffK + 2 * kTile;       // 2 stages; with D = 64 the products read 16 KB past each
+  static constexpr int kOffP = kOffV + 2 * kTile;       // P^T: [128 keys][64 rows] fp16, rows of 128 B
+  static constexpr int kOffQ = kOffP + kT * 128;        // [D / 64][NR][128 B]
+  // raw slots: kST tokens' codes (8-bit heads fill the room), then their words
+  static constexpr int kST = D == 128 ? 32 : 64;
+  static constexpr int kRawWords = kST * D;
+  static constexpr int kRawBytes = kRawWords + kST * (D / 32) * 4;
+  static constexpr int kOffRaw = kOffQ + NR * D * 2;
+  static constexpr int kOffBar = kOffRaw + 2 * kRing * kRawBytes;
+  static constexpr int kOffMisc = kOffBar + B_COUNT * 8;     // TMEM address
+  static constexpr int kOffRow = (kOffMisc + 16 + 15) / 16 * 16;   // per row: max, factor, position, four warps' values
+  static constexpr int kOffWalk = kOffRow + NR * 7 * 4;
+  static constexpr int kOffPre = kOffWalk + kThreads / 32 * 128;
+  static constexpr size_t bytes(int B) { return 1024 + kOffPre + static_cast<size_t>(B + 1) * 4; }
+};
+constexpr int kMaxB = 1024;            // sequences (their tile counts lie in shared memory)
+static_assert(NLayout<128, 64>::bytes(kMaxB) <= 232448, "shared memory");
+
+// Whether any of the softmax warpgroup's 128 threads says so (all take part).
+__device__ __forceinline__ bool group_or(bool x) {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.u32 p, %1, 0;\n\t"
+      "barrier.cta.red.or.pred q, 1, 128, p;\n\t"
+      "selp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(r)
+      : "r"(x ? 1u : 0u)
+      : "memory");
+  return r != 0;
+}
+__device__ __forceinline__ void group_sync() { asm volatile("barrier.cta.sync 1, 128;" ::: "memory"); }
+
+// Floats as integers of the same order (for the integer warp maximum).
+__device__ __forceinline__ int to_ordered(float x) {
+  const int i = __float_as_int(x);
+  return i ^ ((i >> 31) & 0x7FFFFFFF);
+}
+__device__ __forceinline__ float from_ordered(int i) { return __int_as_float(i ^ ((i >> 31) & 0x7FFFFFFF)); }
+
+// One dequant warpgroup's part (0: K, 1: V) of a piece's tiles.
+template <int D, int NR, int BITS>
+__device__ __forceinline__ bool dequant_piece(const CParams& p, uint8_t* smem, uint64_t* bar, const Walk& w, int which,
+                                              uint32_t& jj, uint32_t& slot, uint32_t& round, int t, int lane) {
+  using L = NLayout<D, NR>;
+  using F = DqFmt<D, BITS>;
+  constexpr int IPS = L::kST / F::RPI;      // iterations per slot
+  static_assert(IPS * F::RPI == L::kST, "whole iterations per slot");
+  int row, c;
+  dq_lane<D, BITS>(t, row, c);
+  for (int j = 0; j < w.n; ++j, ++jj) {
+    const uint32_t st = jj & 1;
+    if (jj >= 2 && !__all_sync(0xffffffffu, mbar_wait(&bar[B_EMPTY0 + 2 * which + st], ((jj >> 1) - 1) & 1, p.status,
+                                                      kWaitNs)))
+      return false;
+    const uint32_t dst = smem_u32(smem + (which ? L::kOffV : L::kOffK) + st * L::kTile);
+#pragma unroll
+    for (int s = 0; s < kT / L::kST; ++s) {
+      const int k = which * kRing + slot;
+      if (!__all_sync(0xffffffffu, mbar_wait(&bar[B_RAW0 + k], round & 1, p.status, kWaitNs))) return false;
+      const uint8_t* raw = smem + L::kOffRaw + k * L::kRawBytes;
+      const uint4* codes = reinterpret_cast<const uint4*>(raw + row * F::R + c * 16);
+      const uint32_t* words = reinterpret_cast<const uint32_t*>(raw + L::kRawWords) + row * (D / 32) + c * F::VPC / 32;
+      uint4 v[IPS];
+      uint32_t word[IPS];
+#pragma unroll
+      for (int it = 0; it < IPS; ++it) {
+        v[it] = codes[it * F::RPI * F::R / 16];
+        word[it] = words[it * F::RPI * (D / 32)];
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bar[B_RFREE0 + k]);
+#pragma unroll
+      for (int it = 0; it < IPS; ++it)
+        dequant_chunk<BITS>(dst, F::RPI * (s * IPS + it) + row, c * F::VPC, v[it], word[it]);
+      if (++slot == kRing) {
+        slot = 0;
+        ++round;
+      }
+    }
+    if (which) clear_unseen<D, BITS>(dst, p, w, w.t.tile(w.i + j) * kT, row, c);
+    fence_proxy_async_smem();
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&bar[B_FULL0 + 2 * which + st]);
+  }
+  return true;
+}
+
+// One row of a cut segment: its pieces merged by log-sum-exp in CTA order, by
+// one warp, a lane per D / 32 channels.
+template <int D>
+__device__ __forceinline__ void merge_row(const CParams& p, const Walk& w, const Cut& cut, int rows_per_block, int r,
+                                          int lane) {
+  constexpr int N = D / 32;
+  const int np = cut.c1 - cut.c0 + 1;
+  auto lse_of = [&](int k) {
+    return k < np ? __ldcg(p.ws_lse + static_cast<int64_t>(cut.partial(cut.c0 + k)) * p.slot_rows + r) : -INFINITY;
+  };
+  float M = -INFINITY;
+  for (int k0 = 0; k0 < np; k0 += 32) M = fmaxf(M, lse_of(k0 + lane));
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+  float acc[N], L = 0.0f;
+#pragma unroll
+  for (int e = 0; e < N; ++e) acc[e] = 0.0f;
+  for (int k0 = 0; k0 < np; k0 += 32) {
+    const float lse = lse_of(k0 + lane);
+    const float mine = lse == -INFINITY ? 0.0f : fast_exp2(lse - M);
+    const int cnt = min(32, np - k0);
+    for (int k = 0; k < cnt; k += 4) {
+      float v[4][N];
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        const int c = cut.c0 + k0 + min(k + u, cnt - 1);
+        const float* src = p.ws_o + (static_cast<int64_t>(cut.partial(c)) * p.slot_rows + r) * D + lane * N;
+        if constexpr (N == 4) {
+          const float4 x = __ldcg(reinterpret_cast<const float4*>(src));
+          v[u][0] = x.x; v[u][1] = x.y; v[u][2] = x.z; v[u][3] = x.w;
+        } else {
+          const float2 x = __ldcg(reinterpret_cast<const float2*>(src));
+          v[u][0] = x.x; v[u][1] = x.y;
+        }
+      }
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        const float b = k + u < cnt ? __shfl_sync(0xffffffffu, mine, min(k + u, 31)) : 0.0f;
+        L += b;
+#pragma unroll
+        for (int e = 0; e < N; ++e) acc[e] = fmaf(b, v[u][e], acc[e]);
+      }
+    }
+  }
+  const float inv = L > 0.0f ? 1.0f / L : 0.0f;
+  const int64_t off = out_offset(p, w, w.rt * rows_per_block + r, D) + lane * N;
+  if (!KVQ_IN_RANGE(off >= 0 && off + N <= static_cast<int64_t>(p.c.rows) * p.Hq * D, p.status)) return;
+  if (p.out_dtype == KVQ_OUT_F32) {
+    float* dst = static_cast<float*>(p.out) + off;
+    if constexpr (N == 4)
+      *reinterpret_cast<float4*>(dst) = make_float4(acc[0] * inv, acc[1] * inv, acc[2] * inv, acc[3] * inv);
+    else *reinterpret_cast<float2*>(dst) = make_float2(acc[0] * inv, acc[1] * inv);
+  } else {
+    __nv_bfloat162* dst = reinterpret_cast<__nv_bfloat162*>(static_cast<__nv_bfloat16*>(p.out) + off);
+#pragma unroll
+    for (int e = 0; e < N; e += 2) dst[e / 2] = __floats2bfloat162_rn(acc[e] * inv, acc[e + 1] * inv);
+  }
+}
+
+template <int D, int NR>
+__global__ void __launch_bounds__(kThreads, 1) chunk_narrow_kernel(const __grid_constant__ CParams p) {
+  using L = NLayout<D, NR>;
+  constexpr uint32_t kCols = NR == 16 ? 64 : NR == 32 ? 128 : 256;   // TMEM columns (a power of two)
+  constexpr int CH = NR < 32 ? NR : 32;                              // columns handled at a time
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = smem_raw + (-smem_u32(smem_raw) & 1023u);
+  uint64_t* bar = reinterpret_cast<uint64_t*>(smem + L::kOffBar);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::kOffMisc);
+  float* row_m = reinterpret_cast<float*>(smem + L::kOffRow);        // running max, log2 domain
+  float* row_a = row_m + NR;                                         // factor of the last move of the max
+  int32_t* row_pos = reinterpret_cast<int32_t*>(row_a + NR);         // position in the cache
+  int32_t* row_w = row_pos + NR;                                     // [4 warps][NR]: maxima, sums
+  int32_t* pre = reinterpret_cast<int32_t*>(smem + L::kOffPre);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+  if (threadIdx.x == 0) {
+    mbar_init(&bar[B_QREADY], 4);
+    mbar_init(&bar[B_QEMPTY], 1);
+    for (int k = 0; k < 4; ++k) {
+      mbar_init(&bar[B_FULL0 + k], 4);
+      mbar_init(&bar[B_EMPTY0 + k], 1);
+    }
+    mbar_init(&bar[B_SFULL0], 1);
+    mbar_init(&bar[B_SFULL0 + 1], 1);
+    mbar_init(&bar[B_PFULL], 4);
+    mbar_init(&bar[B_PDONE], 1);
+    mbar_init(&bar[B_OFREE], 4);
+    mbar_init(&bar[B_MMADONE], 1);
+    mbar_init(&bar[B_EXIT], kExitArrivals);
+    for (int k = 0; k < 2 * kRing; ++k) {
+      mbar_init(&bar[B_RAW0 + k], 1);
+      mbar_init(&bar[B_RFREE0 + k], 4);
+    }
+    fence_barrier_init();
+  }
+  // the caches, queries and lengths may come from the kernel before this one
+  grid_dependency_wait();
+  grid_launch_dependents();
+  if (blockIdx.x == 0) chunk::check_sequences(p.c, threadIdx.x, kThreads, p.status);
+  count_tiles<NR>(p, pre, warp, lane, kThreads / 32);
+  __syncthreads();
+  if (warp == 0) {
+    sum_tiles(p, pre, lane);
+    tc::tmem_alloc(tmem_slot, kCols);
+    tc::tmem_relinquish();
+  }
+  tc::fence_before_sync();
+  __syncthreads();
+  tc::fence_after_sync();
+  const uint32_t tmem = *tmem_slot;
+  Walk& w = reinterpret_cast<Walk*>(smem + L::kOffWalk)[warp];
+  const int64_t total = start_walk<NR>(p, pre, w, lane);
+  if (total <= 0) {   // the whole CTA: nothing was started
+    if (warp == 0) tc::tmem_dealloc(tmem, kCols);
+    return;
+  }
+  auto wait_all = [&](int which, uint32_t parity) -> bool {
+    return __all_sync(0xffffffffu, mbar_wait(&bar[which], parity & 1, p.status, kWaitNs));
+  };
+
+  if (warp == 0) {
+    // The other roles finish in bounded time: each stops at its first wait
+    // that runs out, and a role waits at most a few times per tile.
+    const uint64_t deadline = kWaitNs * static_cast<uint64_t>(16 * total + 16);
+    const uint64_t t0 = global_ns();
+    uint32_t n = 0;
+    while (!mbar_try_wait(&bar[B_EXIT], 0)) {
+      if ((++n & 255u) == 0 && global_ns() - t0 > deadline) {
+        report(p.status, KVQ_ERR_TIMEOUT);
+        break;
+      }
+    }
+    __syncwarp();
+    tc::fence_after_sync();
+    tc::tmem_dealloc(tmem, kCols);
+    return;
+  }
+
+  if (warp == 1) {
+    // ---------------- MMA issuer ----------------
+    constexpr uint32_t id_qk = tc::idesc_f16_f32(kT, NR, false);
+    constexpr uint32_t id_pv = tc::idesc_f16_f32(kT, NR, true, true);
+    const uint32_t q = smem_u32(smem + L::kOffQ), pt = smem_u32(smem + L::kOffP);
+    const uint32_t kb = smem_u32(smem + L::kOffK), vb = smem_u32(smem + L::kOffV);
+    const uint32_t d_o = tmem + 2 * NR;
+    uint32_t jj = 0, piece = 0;
+    bool ok = true;
+    // O^T (+)= V^T P^T of tile k; `first`: of its piece
+    auto pv = [&](uint32_t k, bool first) -> bool {
+      bool good = wait_all(B_FULL0 + 2 + (k & 1), k >> 1) && wait_all(B_PFULL, k);
+      if (good && first && piece > 0) good = wait_all(B_OFREE, piece - 1);   // the previous piece's O has been read
+      if (!good) return false;
+      tc::fence_after_sync();
+      if (tc::elect_one()) {
+        const uint32_t vs = vb + (k & 1) * L::kTile;
+        // (D = 64: channels 64-127 of the A operand are whatever follows the
+        // tile; their rows of O^T are never read)
+        if (first) tc::mma_ss<false>(d_o, tc::smem_desc_sw128(vs, kT * 128, 1024), tc::smem_desc_sw128(pt, kT * 128, 1024), id_pv);
+        else tc::mma_ss<true>(d_o, tc::smem_desc_sw128(vs, kT * 128, 1024), tc::smem_desc_sw128(pt, kT * 128, 1024), id_pv);
+#pragma unroll
+        for (int s = 1; s < kT / 16; ++s)
+          tc::mma_ss<true>(d_o, tc::smem_desc_sw128(vs + s * 2048, kT * 128, 1024),
+                           tc::smem_desc_sw128(pt + s * 2048, kT * 128, 1024), id_pv);
+        tc::commit(&bar[B_EMPTY0 + 2 + (k & 1)]);
+        tc::commit(&bar[B_PDONE]);
+      }
+      __syncwarp();
+      return true;
+    };
+    do {
+      const int n = w.n;
+      ok = wait_all(B_QREADY, piece);
+      for (int j = 0; j < n && ok; ++j, ++jj) {
+        ok = wait_all(B_FULL0 + (jj & 1), jj >> 1);
+        if (!ok) break;
+        tc::fence_after_sync();
+        if (tc::elect_one()) {
+          // S^T = K Q^T (its buffer was read before tile jj - 2's P was complete)
+          const uint32_t ks = kb + (jj & 1) * L::kTile, d_s = tmem + (jj & 1) * NR;
+          tc::mma_ss<false>(d_s, tc::smem_desc_sw128(ks, 16, 1024), tc::smem_desc_sw128(q, 16, 1024), id_qk);
+#pragma unroll
+          for (int s = 1; s < D / 16; ++s)
+            tc::mma_ss<true>(d_s, tc::smem_desc_sw128(ks + (s >> 2) * (kT * 128) + (s & 3) * 32, 16, 1024),
+                             tc::smem_desc_sw128(q + (s >> 2) * (NR * 128) + (s & 3) * 32, 16, 1024), id_qk);
+          tc::commit(&bar[B_SFULL0 + (jj & 1)]);
+          tc::commit(&bar[B_EMPTY0 + (jj & 1)]);
+          if (j + 1 == n) tc::commit(&bar[B_QEMPTY]);
+        }
+        __syncwarp();
+        if (j > 0) ok = pv(jj - 1, j == 1);
+      }
+      if (ok) ok = pv(jj - 1, n == 1);
+      ++piece;
+    } while (ok && next_piece<NR>(p, w, lane));
+    if (tc::elect_one()) tc::commit(&bar[B_MMADONE]);
+    __syncwarp();
+    wait_all(B_MMADONE, 0);
+    tc::fence_before_sync();
+    if (lane == 0) mbar_arrive(&bar[B_EXIT]);
+    return;
+  }
+
+  if (warp == 2) {
+    // ---------------- copies: raw slots of K and V ----------------
+    const int64_t blocks = static_cast<int64_t>(p.c.pB) * (p.c.pT / 64);
+    const uint64_t pol = l2_evict_first_policy();
+    uint32_t slot = 0, round = 0;      // the same for both rings
+    bool ok = true;
+    do {
+      const Seen seen(p, w);
+      const int rb = D * p.bits[w.kvh] / 8;                        // code bytes of a token
+      const uint32_t cb = L::kST * rb, wb = L::kST * (D / 32) * 4;
+      const int lo64 = seen.lo;
+      int half[2] = {0, 0};
+      for (int j = 0; j < w.n && ok; ++j) {
+        if ((j & 31) == 0 && j + lane < w.n) {                     // 32 tiles' pages at a time, a lane each
+          const int t0 = w.t.tile(w.i + j + lane) * kT;
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const int a = t0 + 64 * h;
+            const bool is_seen = a < seen.end && (a + 64 > lo64 || a < p.sinks);
+            // (a half that nothing sees stands for the other: its rows are masked)
+            const int b = is_seen ? a : (h == 0 ? a + 64 : a - 64);
+            half[h] = chunk::storage_block(p.c, w.b, b / 64, p.status);
+          }
+        }
+        int blk[2];
+        blk[0] = __shfl_sync(0xffffffffu, half[0], j & 31);
+        blk[1] = __shfl_sync(0xffffffffu, half[1], j & 31);
+        uint32_t s2 = slot, r2 = round;
+#pragma unroll
+        for (int x = 0; x < 2 && ok; ++x) {                        // K, V
+          s2 = slot;
+          r2 = round;
+          for (int s = 0; s < kT / L::kST && ok; ++s) {
+            const int k = x * kRing + s2;
+            if (r2 > 0) ok = wait_all(B_RFREE0 + k, r2 - 1);
+            if (!ok) break;
+            if (lane == 0) {
+              uint8_t* raw = smem + L::kOffRaw + k * L::kRawBytes;
+              const int tok = s * L::kST;                          // within the tile
+              int64_t at = static_cast<int64_t>(blk[tok / 64]) * 64 + tok % 64;
+              if (!KVQ_IN_RANGE(at >= 0 && at + L::kST <= blocks * 64 &&
+                                    p.plane_off[w.kvh] + (at + L::kST) * rb <= p.codes_bytes, p.status))
+                at = 0;
+              mbar_arrive_expect_tx(&bar[B_RAW0 + k], cb + wb);
+              bulk_g2s_hint(raw, p.codes[x] + p.plane_off[w.kvh] + at * rb, cb, &bar[B_RAW0 + k], pol);
+              bulk_g2s_hint(raw + L::kRawWords, p.sz[x] + (w.kvh * blocks * 64 + at) * (D / 32), wb, &bar[B_RAW0 + k],
+                            pol);
+            }
+            if (++s2 == kRing) {
+              s2 = 0;
+              ++r2;
+            }
+          }
+          __syncwarp();
+        }
+        if (ok) {
+          slot = s2;
+          round = r2;
+        }
+      }
+    } while (ok && next_piece<NR>(p, w, lane));
+    // Every copy has landed before the CTA can exit: on the normal path the
+    // dequant warps have read them all, after a wait that ran out the copies
+    // in flight get one more limit each.
+    if (!ok) {
+      const uint64_t t0 = global_ns();
+      while (global_ns() - t0 < 1000000ull) {
+      }
+    }
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&bar[B_EXIT]);
+    return;
+  }
+
+  if (warp == 3) {
+    if (lane == 0) mbar_arrive(&bar[B_EXIT]);
+    return;
+  }
+
+  if (warp < 12) {
+    // ---------------- dequant warpgroups: K (and the queries), V ----------------
+    const int which = warp < 8 ? 0 : 1;
+    const int t = threadIdx.x - 128 - 128 * which;
+    uint32_t jj = 0, slot = 0, round = 0, piece = 0;
+    bool ok = true;
+    do {
+      if (which == 0) {
+        ok = load_queries<D, NR, NR>(p, smem_u32(smem + L::kOffQ), &bar[B_QEMPTY], w, t, (piece - 1) & 1, piece > 0);
+        if (!ok) break;
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bar[B_QREADY]);
+      }
+      ok = p.bits[w.kvh] == 4 ? dequant_piece<D, NR, 4>(p, smem, bar, w, which, jj, slot, round, t, lane)
+                              : dequant_piece<D, NR, 8>(p, smem, bar, w, which, jj, slot, round, t, lane);
+      ++piece;
+    } while (ok && next_piece<NR>(p, w, lane));
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&bar[B_EXIT]);
+    return;
+  }
+
+  // ---------------- softmax warpgroup: thread = key of the tile, then channel of O^T ----------------
+  // (its four warps take every decision together, so that its barriers are
+  // always met by all: a wait that ran out is a vote)
+  const int q4 = warp & 3, key = q4 * 32 + lane;
+  const uint32_t lanes = static_cast<uint32_t>(q4 * 32) << 16;
+  const uint32_t o_addr = tmem + lanes + 2 * NR;
+  const uint32_t p_row = smem_u32(smem + L::kOffP) + key * 128;
+  const float sl2 = p.scale_log2;
+  uint32_t jj = 0;
+  bool ok = true, stop = false;
+  do {
+    // the piece's rows: positions (a row past the segment's end as the last one), no maximum yet
+    if (key < NR) {
+      const int R = w.rt * NR + key;
+      row_pos[key] = key < w.t.rows ? w.s.len - w.s.n + R / p.rep : w.t.pos_hi;
+      row_m[key] = -INFINITY;
+    }
+    group_sync();
+    float l[NR];
+#pragma unroll
+    for (int i = 0; i < NR; ++i) l[i] = 0.0f;
+    const bool four = p.bits[w.kvh] == 4;
+    for (int j = 0; j < w.n; ++j, ++jj) {
+      const int t0 = w.t.tile(w.i + j) * kT, tok = t0 + key;
+      // some row of the block does not see some key of the tile
+      const bool masked = t0 + kT - 1 > w.t.pos_lo ||
+                          (p.window > 0 && t0 < w.t.pos_hi - p.window + 1 && t0 + kT > p.sinks);
+      const bool always = tok < p.sinks || p.window == 0;          // no window for this key
+      ok = wait_all(B_SFULL0 + (jj & 1), jj >> 1) && ok;
+      tc::fence_after_sync();
+      const uint32_t s_addr = tmem + lanes + (jj & 1) * NR;
+      float s[NR];
+#pragma unroll
+      for (int c0 = 0; c0 < NR; c0 += CH) {
+        uint32_t v[CH];
+        if constexpr (CH == 16) tc::ld_32x32b_x16(s_addr + c0, v);
+        else tc::ld_32x32b_x32(s_addr + c0, v);
+        tc::wait_ld(v);
+#pragma unroll
+        for (int i = 0; i < CH; ++i) s[c0 + i] = __uint_as_float(v[i]) * sl2;
+      }
+      if (masked) {
+#pragma unroll
+        for (int i = 0; i < NR; i += 4) {
+          const int4 pos = *reinterpret_cast<const int4*>(row_pos + i);
+          const int ps[4] = {pos.x, pos.y, pos.z, pos.w};
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            if (!(ps[e] >= tok && (always || ps[e] - p.window < tok))) s[i + e] = -INFINITY;
+        }
+      }
+      bool move = !ok;
+#pragma unroll
+      for (int i = 0; i < NR; i += 4) {
+        const float4 m4 = *reinterpret_cast<const float4*>(row_m + i);
+        move |= s[i] > m4.x + kRescaleThreshold || s[i + 1] > m4.y + kRescaleThreshold ||
+                s[i + 2] > m4.z + kRescaleThreshold || s[i + 3] > m4.w + kRescaleThreshold;
+      }
+      if (group_or(move)) {
+        if (group_or(!ok)) {
+          stop = true;
+          break;
+        }
+        // new maxima of the rows that need one, the sums and O^T rescaled
+#pragma unroll
+        for (int i = 0; i < NR; ++i) {
+          const int mx = __reduce_max_sync(0xffffffffu, to_ordered(s[i]));
+          if (lane == (i & 31)) row_w[q4 * NR + i] = mx;
+        }
+        group_sync();
+        if (key < NR) {
+          const float M = fmaxf(fmaxf(from_ordered(row_w[key]), from_ordered(row_w[NR + key])),
+                                fmaxf(from_ordered(row_w[2 * NR + key]), from_ordered(row_w[3 * NR + key])));
+          const float mo = row_m[key];
+          const float mn = M > mo + kRescaleThreshold ? M : mo;   // (mo -infinity: any M)
+          row_a[key] = mo == -INFINITY ? 1.0f : fast_exp2(mo - mn);
+          row_m[key] = mn;
+        }
+        group_sync();
+#pragma unroll
+        for (int i = 0; i < NR; ++i) l[i] *= row_a[i];
+        if (j > 0) {
+          ok = wait_all(B_PDONE, jj - 1) && ok;
+          tc::fence_after_sync();
+#pragma unroll
+          for (int c0 = 0; c0 < NR; c0 += CH) {
+            uint32_t v[CH];
+            if constexpr (CH == 16) tc::ld_32x32b_x16(o_addr + c0, v);
+            else tc::ld_32x32b_x32(o_addr + c0, v);
+            tc::wait_ld(v);
+#pragma unroll
+            for (int i = 0; i < CH; ++i) v[i] = __float_as_uint(__uint_as_float(v[i]) * row_a[c0 + i]);
+            if constexpr (CH == 16) tc::st_32x32b_x16(o_addr + c0, v);
+            else tc::st_32x32b_x32(o_addr + c0, v);
+          }
+          tc::wait_st();
+        }
+      }
+      // P^T = 2^(S - m): this key's row of the operand tile, once the previous tile's product has read it
+      uint32_t pk[NR / 2];
+#pragma unroll
+      for (int i = 0; i < NR; i += 4) {
+        const float4 m4 = *reinterpret_cast<const float4*>(row_m + i);
+        const float mm[4] = {m4.x, m4.y, m4.z, m4.w};
+        float e[4];
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          // (a row that sees nothing yet has no maximum: its weights are 2^-infinity = 0)
+          e[u] = fast_exp2(s[i + u] - (mm[u] == -INFINITY ? 0.0f : mm[u]));
+          l[i + u] += e[u];
+        }
+        pk[i / 2] = pack_half2(e[0], e[1]);
+        pk[i / 2 + 1] = pack_half2(e[2], e[3]);
+      }
+      if (jj > 0) ok = wait_all(B_PDONE, jj - 1) && ok;
+#pragma unroll
+      for (int i = 0; i < NR / 8; ++i)
+        sts128(p_row + ((i ^ (key & 7)) << 4), pk[4 * i], pk[4 * i + 1], pk[4 * i + 2], pk[4 * i + 3]);
+      fence_proxy_async_smem();
+      tc::fence_before_sync();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bar[B_PFULL]);
+    }
+    if (stop) break;
+    // ---- end of the piece: sums over the keys, then O^T / sum ----
+    ok = wait_all(B_PDONE, jj - 1) && ok;
+    if (group_or(!ok)) break;
+    tc::fence_after_sync();
+#pragma unroll
+    for (int i = 0; i < NR; ++i) {
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) l[i] += __shfl_xor_sync(0xffffffffu, l[i], o);
+      if (lane == (i & 31)) row_w[q4 * NR + i] = __float_as_int(l[i]);
+    }
+    group_sync();
+    const int rows = w.t.rows;
+    const bool whole = w.n == w.t.n;
+    const Cut cut(w);
+    const int part = cut.partial(blockIdx.x);
+    if (key < NR) {
+      const float sum = (__int_as_float(row_w[key]) + __int_as_float(row_w[NR + key])) +
+                        (__int_as_float(row_w[2 * NR + key]) + __int_as_float(row_w[3 * NR + key]));
+      row_a[key] = sum > 0.0f ? 1.0f / sum : 0.0f;
+      if (!whole && key < rows)
+        p.ws_lse[static_cast<int64_t>(part) * p.slot_rows + key] = sum > 0.0f ? row_m[key] + __log2f(sum) : -INFINITY;
+    }
+    group_sync();
+    {
+      // operand column `key` holds this channel (4-bit heads: order 0,4,1,5,2,6,3,7 within eight)
+      const int ch = four ? (key & ~7) | ((key & 1) << 2) | ((key & 7) >> 1) : key;
+#pragma unroll
+      for (int c0 = 0; c0 < NR; c0 += CH) {
+        uint32_t v[CH];
+        if constexpr (CH == 16) tc::ld_32x32b_x16(o_addr + c0, v);
+        else tc::ld_32x32b_x32(o_addr + c0, v);
+        tc::wait_ld(v);
+        if (key >= D) continue;
+#pragma unroll
+        for (int i = 0; i < CH; ++i) {
+          const int r = c0 + i;
+          if (r >= rows) continue;
+          const float o = __uint_as_float(v[i]) * row_a[r];
+          if (whole) {
+            const int64_t off = out_offset(p, w, w.rt * NR + r, D) + ch;
+            if (!KVQ_IN_RANGE(off >= 0 && off < static_cast<int64_t>(p.c.rows) * p.Hq * D, p.status)) continue;
+            if (p.out_dtype == KVQ_OUT_F32) static_cast<float*>(p.out)[off] = o;
+            else static_cast<__nv_bfloat16*>(p.out)[off] = __float2bfloat16_rn(o);
+          } else {
+            p.ws_o[(static_cast<int64_t>(part) * p.slot_rows + r) * D + ch] = o;
+          }
+        }
+      }
+    }
+    tc::fence_before_sync();
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&bar[B_OFREE]);
+    group_sync();   // the rows' values have been read; every partial is stored
+    if (!whole) {
+      // one acquire-release atomic after the group's barrier, and a vote that
+      // hands its outcome (and what it acquired) to the group
+      bool last = false;
+      if (key == 0) last = atom_add_acq_rel_gpu(p.cnt + 2 * cut.c0, 1) + 1 == cut.c1 - cut.c0 + 1;
+      if (group_or(last)) {
+        for (int r = q4; r < rows; r += 4) merge_row<D>(p, w, cut, NR, r, lane);
+        if (key == 0) p.cnt[2 * cut.c0] = 0;   // ready for the next call
+      }
+    }
+  } while (next_piece<NR>(p, w, lane));
+  tc::wait_st();
+  tc::fence_before_sync();
+  __syncwarp();
+  if (lane == 0) mbar_arrive(&bar[B_EXIT]);
+}
+
+// Per device and instantiation, set once under a lock: the kernel's dynamic
+// shared-memory limit.
+std::mutex g_prep_mu;
+bool g_prep[64][6] = {};
+
+template <int D, int NR>
+kvq_status launch_n(const CParams& p, cudaStream_t stream) {
+  using L = NLayout<D, NR>;
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return KVQ_ERR_CUDA;
+  {
+    std::lock_guard<std::mutex> lock(g_prep_mu);
+    bool& ready = g_prep[dev][(D == 128 ? 3 : 0) + (NR == 16 ? 0 : NR == 32 ? 1 : 2)];
+    if (!ready && cudaFuncSetAttribute(chunk_narrow_kernel<D, NR>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                       static_cast<int>(L::bytes(kMaxB))) != cudaSuccess)
+      return KVQ_ERR_CUDA;
+    ready = true;
+  }
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(p.num_ctas));
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = L::bytes(p.c.B);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, chunk_narrow_kernel<D, NR>, p) == cudaSuccess ? KVQ_OK : KVQ_ERR_CUDA;
+}
+
+}  // namespace
+
+bool chunk_narrow_takes(int B, int64_t max_rows) { return B <= kMaxB && max_rows <= 64; }
+
+kvq_status launch_chunk_narrow(const CParams& p, int D, int64_t max_rows, cudaStream_t stream) {
+  if (D == 128)
+    return max_rows <= 16 ? launch_n<128, 16>(p, stream)
+                          : max_rows <= 32 ? launch_n<128, 32>(p, stream) : launch_n<128, 64>(p, stream);
+  return max_rows <= 16 ? launch_n<64, 16>(p, stream)
+                        : max_rows <= 32 ? launch_n<64, 32>(p, stream) : launch_n<64, 64>(p, stream);
+}
+
+}  // namespace kvq

@@ -1,0 +1,310 @@
+// kvq_chunk_walk.cuh -- the work list of the chunk attention kernels: every
+// (sequence, KV head, row block, 128-token key tile) in order, cut into equal
+// contiguous ranges, one per CTA ("stream-K"), so that ragged lengths and few
+// rows over a long cache load every SM alike.  A segment is a row block (ROWS
+// packed rows, token * rep + head) of one (sequence, KV head); the run of a
+// segment's tiles inside one CTA's range is a piece.
+#pragma once
+
+#include <cstdint>
+
+#include "kvq_chunk.cuh"
+#include "kvq_tile.cuh"
+
+namespace kvq {
+namespace chunk_walk {
+
+using tile::kT;
+
+constexpr float kRescaleThreshold = 8.0f;  // log2 units: the running max moves (and O is rescaled) beyond it
+constexpr uint64_t kWaitNs = kDefaultWaitLimitNs;
+
+struct CParams {
+  chunk::View c;
+  const uint16_t* q;
+  int64_t sq_row, sq_head;
+  const uint8_t* codes[2];          // K, V code buffers
+  const uint32_t* sz[2];
+  int32_t* cnt;                     // [CTAs][2] arrivals at a cut segment, by its first CTA and slot
+  float* ws_lse;                    // [2 * CTAs][slot_rows], log2 domain
+  float* ws_o;                      // [2 * CTAs][slot_rows * D], in the kernel's own order
+  void* out;
+  int32_t* status;
+  int32_t out_dtype, Hq, Hkv, rep, window, sinks, num_ctas, slot_rows;
+  float scale_log2;
+  int64_t codes_bytes;              // size of each code buffer (the debug build's index checks)
+  int64_t plane_off[KVQ_MAX_HKV];
+  int8_t bits[KVQ_MAX_HKV];
+};
+
+// A segment's key tiles: those that some row of the block sees, in order.
+// Index i of the list is tile (i < ns ? i : i + skip).
+struct Tiles {
+  int n, ns, skip;
+  int pos_lo, pos_hi;    // positions of the block's first and last row
+  int rows;              // its rows
+  __device__ __forceinline__ int tile(int i) const { return i < ns ? i : i + skip; }
+};
+template <int ROWS>
+__device__ __forceinline__ Tiles segment_tiles(const CParams& p, const chunk::Seq& s, int rt) {
+  Tiles t;
+  t.rows = min(ROWS, s.n * p.rep - rt * ROWS);
+  t.pos_lo = s.len - s.n + rt * ROWS / p.rep;
+  t.pos_hi = s.len - s.n + (rt * ROWS + t.rows - 1) / p.rep;
+  t.n = t.pos_hi / kT + 1;
+  t.ns = t.skip = 0;
+  if (p.window > 0) {
+    const int fw = max(t.pos_lo - p.window + 1, 0) / kT;
+    t.ns = min((min(p.sinks, t.pos_hi + 1) + kT - 1) / kT, fw);
+    t.skip = fw - t.ns;
+    t.n -= t.skip;
+  }
+  return t;
+}
+template <int ROWS>
+__device__ __forceinline__ int row_blocks(const CParams& p, const chunk::Seq& s) {
+  return (s.n * p.rep + ROWS - 1) / ROWS;
+}
+
+// A warp's walk through its CTA's range of the work list, piece by piece.  It
+// lives in shared memory: the roles' loops need their registers.
+struct Walk {
+  int64_t f;             // flat index of the piece's first tile
+  int64_t left;          // tiles of the range from there on
+  int b, kvh, rt, i;     // the piece starts at tile index i of this segment
+  chunk::Seq s;
+  Tiles t;
+  int n;                 // tiles of the piece
+  int C;                 // CTAs that share the N tiles of the work list
+  int64_t N;
+};
+static_assert(sizeof(Walk) <= 128, "room for a Walk per warp");
+
+template <int ROWS>
+__device__ __forceinline__ void open_piece(const CParams& p, Walk& w) {
+  w.t = segment_tiles<ROWS>(p, w.s, w.rt);
+  w.n = static_cast<int>(min(static_cast<int64_t>(w.t.n - w.i), w.left));
+}
+// To the next piece (the whole warp; lane 0 does it); false at the range's end.
+template <int ROWS>
+__device__ __forceinline__ bool next_piece(const CParams& p, Walk& w, int lane) {
+  __syncwarp();
+  if (lane == 0) {
+    w.left -= w.n;
+    w.f += w.n;
+    if (w.left > 0) {
+      w.i = 0;
+      if (++w.rt >= row_blocks<ROWS>(p, w.s)) {
+        w.rt = 0;
+        if (++w.kvh >= p.Hkv) {
+          w.kvh = 0;
+          do {
+            ++w.b;
+            w.s = chunk::sequence(p.c, w.b);
+          } while (w.s.n == 0);
+        }
+      }
+      open_piece<ROWS>(p, w);
+    }
+  }
+  __syncwarp();
+  return w.left > 0;
+}
+
+// Tokens that a segment's queries see: below `end`, from `lo` on or below the sinks.
+struct Seen {
+  int end, lo;
+  __device__ __forceinline__ Seen(const CParams& p, const Walk& w)
+      : end(w.t.pos_hi + 1), lo(p.window > 0 ? w.t.pos_lo - p.window + 1 : 0) {}
+};
+
+// Output offset of packed row R of a sequence and KV head.
+__device__ __forceinline__ int64_t out_offset(const CParams& p, const Walk& w, int R, int D) {
+  const int tok = R / p.rep, hh = R - tok * p.rep;
+  return ((static_cast<int64_t>(w.s.row0) + tok) * p.Hq + w.kvh * p.rep + hh) * D;
+}
+
+// Tiles of a sequence for one KV head (the whole warp, a lane per row block).
+template <int ROWS>
+__device__ __forceinline__ int32_t sequence_tiles(const CParams& p, const chunk::Seq& s, int lane) {
+  const int nrt = row_blocks<ROWS>(p, s);
+  int32_t n = 0;
+  for (int rt = lane; rt < nrt; rt += 32) n += segment_tiles<ROWS>(p, s, rt).n;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) n += __shfl_xor_sync(0xffffffffu, n, o);
+  return n;
+}
+
+// pre[b + 1] = tiles of sequence b for one KV head: a warp per sequence.
+template <int ROWS>
+__device__ __forceinline__ void count_tiles(const CParams& p, int32_t* pre, int warp, int lane, int warps) {
+  for (int b = warp; b < p.c.B; b += warps) {
+    const int32_t n = sequence_tiles<ROWS>(p, chunk::sequence(p.c, b), lane);
+    if (lane == 0) pre[b + 1] = n;
+  }
+}
+
+// The counts' prefix sums in place: pre[b] = tiles of sequences 0 .. b - 1 (one warp).
+__device__ __forceinline__ void sum_tiles(const CParams& p, int32_t* pre, int lane) {
+  int32_t carry = 0;
+  for (int b0 = 0; b0 < p.c.B; b0 += 32) {
+    int32_t n = b0 + lane < p.c.B ? pre[b0 + lane + 1] : 0;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int32_t v = __shfl_up_sync(0xffffffffu, n, o);
+      if (lane >= o) n += v;
+    }
+    if (b0 + lane < p.c.B) pre[b0 + lane + 1] = carry + n;
+    carry += __shfl_sync(0xffffffffu, n, 31);
+  }
+  if (lane == 0) pre[0] = 0;
+}
+
+// Opens the first piece of this CTA's range [N c / C, N (c + 1) / C) of the N
+// tiles (the whole warp; never more CTAs than tiles in the split); returns the
+// range's length, 0 for a CTA outside the split.
+template <int ROWS>
+__device__ __forceinline__ int64_t start_walk(const CParams& p, const int32_t* pre, Walk& w, int lane) {
+  const int64_t N = static_cast<int64_t>(p.Hkv) * pre[p.c.B];
+  const int C = N < p.num_ctas ? static_cast<int>(N) : p.num_ctas;
+  if (static_cast<int>(blockIdx.x) >= C) return 0;
+  const int64_t f0 = N * blockIdx.x / C, total = N * (blockIdx.x + 1) / C - f0;
+  int lo = 0, hi = p.c.B - 1;   // the last b with Hkv * pre[b] <= f0: a sequence with tiles
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (static_cast<int64_t>(p.Hkv) * pre[mid] <= f0) lo = mid; else hi = mid - 1;
+  }
+  const chunk::Seq s = chunk::sequence(p.c, lo);
+  const int64_t per = pre[lo + 1] - pre[lo], off = f0 - static_cast<int64_t>(p.Hkv) * pre[lo];
+  const int kvh = static_cast<int>(off / per);
+  int64_t rem = off - kvh * per;
+  // the row block: prefix sums over 32 blocks at a time
+  const int nrt = row_blocks<ROWS>(p, s);
+  int rt = 0;
+  for (int r0 = 0; r0 < nrt; r0 += 32) {
+    const int64_t mine = r0 + lane < nrt ? segment_tiles<ROWS>(p, s, r0 + lane).n : 0;
+    int64_t incl = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int64_t v = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += v;
+    }
+    const unsigned past = __ballot_sync(0xffffffffu, r0 + lane < nrt && incl > rem);
+    if (past != 0u) {
+      const int k = __ffs(past) - 1;
+      rt = r0 + k;
+      rem -= __shfl_sync(0xffffffffu, incl, k) - __shfl_sync(0xffffffffu, mine, k);
+      break;
+    }
+    rem -= __shfl_sync(0xffffffffu, incl, 31);
+  }
+  if (lane == 0) {
+    w.C = C;
+    w.N = N;
+    w.f = f0;
+    w.left = total;
+    w.b = lo;
+    w.kvh = kvh;
+    w.rt = rt;
+    w.i = static_cast<int>(rem);
+    w.s = s;
+    open_piece<ROWS>(p, w);
+  }
+  __syncwarp();
+  return total;
+}
+
+// A cut segment: CTAs c0 .. c1 hold it.  A CTA's piece of it is partial 0 of
+// the CTA's two when the segment began before the CTA's range (or with it),
+// else 1.
+struct Cut {
+  int c0, c1, slot0;
+  __device__ __forceinline__ explicit Cut(const Walk& w) {
+    const int64_t seg0 = w.f - w.i;
+    c0 = static_cast<int>(((seg0 + 1) * w.C - 1) / w.N);
+    c1 = static_cast<int>(((seg0 + w.t.n) * w.C - 1) / w.N);
+    slot0 = seg0 <= w.N * c0 / w.C ? 0 : 1;
+  }
+  __device__ __forceinline__ int partial(int c) const { return 2 * c + (c == c0 ? slot0 : 0); }
+};
+
+// Rows of the V tile at token t0 that no query of the segment sees become zeros
+// in the operand tile, whatever is stored there: a masked weight of 0 must not
+// meet an infinity or a NaN (K needs none of it, its scores are replaced).  Run
+// by the threads that wrote the rows, after they did: a test on the registers
+// themselves cost 15 % of the 256-row kernel, because a branch there waits for
+// every load in flight.
+template <int D, int BITS>
+__device__ __forceinline__ void clear_unseen(uint32_t dst, const CParams& p, const Walk& w, int t0, int row, int c) {
+  using F = tile::DqFmt<D, BITS>;
+  const Seen s(p, w);
+  if (t0 + kT <= s.end && (t0 >= s.lo || t0 + kT <= p.sinks)) return;   // the whole tile is seen by someone
+#pragma unroll 1
+  for (int it = 0; it < F::NI; ++it) {
+    const int r = F::RPI * it + row, j = t0 + r;
+    if (j < s.end && (j >= s.lo || j < p.sinks)) continue;
+    const int ch0 = c * F::VPC;
+    const uint32_t rowp = dst + (ch0 >> 6) * (kT * 128) + r * 128;
+    for (int i = 0; i < F::VPC / 8; ++i) tile::sts128(rowp + (((((ch0 & 63) >> 3) + i) ^ (r & 7)) << 4), 0u, 0u, 0u, 0u);
+  }
+}
+
+// The piece's query rows to fp16 in the swizzled layout (rows past the
+// segment's end zero); for a 4-bit head in the channel order of its K tiles.
+// dst: tiles of TILE rows ([D / 64 blocks][TILE rows][128 B] each), ROWS rows
+// a segment; empty: the barrier that says that the buffer is free.
+template <int D, int TILE, int ROWS>
+__device__ __forceinline__ bool load_queries(const CParams& p, uint32_t dst, uint64_t* empty, const Walk& w, int t,
+                                             uint32_t parity, bool wait) {
+  constexpr int CPR = D / 8;              // 16-byte chunks per row
+  constexpr int RPP = 128 / CPR;          // rows per pass
+  constexpr int NB = TILE / RPP < 8 ? TILE / RPP : 8;   // passes in flight
+  const int ch = t % CPR;
+  const bool four = p.bits[w.kvh] == 4;
+  const uint16_t* base = p.q + w.kvh * p.rep * p.sq_head + ch * 8;
+  bool finite = true;
+  const int end = (w.t.rows + TILE - 1) / TILE * TILE;
+  for (int r0 = 0; r0 < end; r0 += RPP * NB) {
+    uint4 v[NB];
+#pragma unroll
+    for (int k = 0; k < NB; ++k) {
+      const int r = r0 + k * RPP + t / CPR;
+      v[k] = make_uint4(0u, 0u, 0u, 0u);
+      if (r < w.t.rows) {
+        const int R = w.rt * ROWS + r, tok = R / p.rep, hh = R - tok * p.rep;
+        v[k] = *reinterpret_cast<const uint4*>(base + (w.s.row0 + tok) * p.sq_row + hh * p.sq_head);
+      }
+    }
+    if (r0 == 0 && wait &&
+        !__all_sync(0xffffffffu, mbar_wait(empty, parity, p.status, kWaitNs)))
+      return false;
+#pragma unroll
+    for (int k = 0; k < NB; ++k) {
+      const int r = r0 + k * RPP + t / CPR;
+      uint32_t x[4] = {v[k].x, v[k].y, v[k].z, v[k].w};
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const float lo = __uint_as_float(x[e] << 16), hi = __uint_as_float(x[e] & 0xFFFF0000u);
+        finite &= fabsf(lo) < 65504.0f && fabsf(hi) < 65504.0f;
+        x[e] = pack_half2(lo, hi);
+      }
+      if (four) {   // channels 0,4,1,5,2,6,3,7
+        const uint32_t a = prmt(x[0], x[2], 0x5410u), b = prmt(x[0], x[2], 0x7632u);
+        const uint32_t c = prmt(x[1], x[3], 0x5410u), d = prmt(x[1], x[3], 0x7632u);
+        x[0] = a; x[1] = b; x[2] = c; x[3] = d;
+      }
+      const uint32_t rowp = dst + (r / TILE) * (TILE * D * 2) + (ch >> 3) * (TILE * 128) + (r % TILE) * 128;
+      tile::sts128(rowp + (((ch & 7) ^ (r & 7)) << 4), x[0], x[1], x[2], x[3]);
+    }
+  }
+  if (!finite) report(p.status, KVQ_ERR_NONFINITE);
+  return true;
+}
+
+}  // namespace chunk_walk
+
+// The kernel for at most 64 rows per (sequence, KV head), where it applies.
+bool chunk_narrow_takes(int B, int64_t max_rows);
+kvq_status launch_chunk_narrow(const chunk_walk::CParams& p, int D, int64_t max_rows, cudaStream_t stream);
+
+}  // namespace kvq
