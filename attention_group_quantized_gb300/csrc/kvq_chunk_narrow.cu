@@ -14,9 +14,10 @@
 //
 // One CTA (512 threads, one per SM) walks its range of the work list
 // (kvq_chunk_walk.cuh):
-//   warp 0       TMEM; warp 1 issues the products; warp 2 keeps rings of raw
-//                code slots full by bulk copies (about 50 KB in flight an SM,
-//                which is what the latency of HBM asks for);
+//   warp 0       TMEM, and the issue of V^T P^T; warp 1 issues K Q^T (a warp
+//                each: neither waits for what only the other needs); warps 2 and 3 keep rings of
+//                raw code slots of K and V full by bulk copies (about 50 KB in
+//                flight an SM, which is what the latency of HBM asks for);
 //   warps 4-7    K codes (and the piece's queries) to fp16 operand tiles;
 //   warps 8-11   V codes likewise;
 //   warps 12-15  softmax, rescaling, the piece's output or partial, the merge.
@@ -36,11 +37,11 @@ using namespace tile;
 using namespace chunk_walk;
 
 constexpr int kThreads = 512;
-constexpr int kRing = 6;               // raw slots of K, and as many of V
+constexpr int kRing = 3;               // raw slots of K, and as many of V
 
 enum {
-  B_QREADY = 0, B_QEMPTY, B_FULL0, B_EMPTY0 = B_FULL0 + 4, B_SFULL0 = B_EMPTY0 + 4, B_PFULL = B_SFULL0 + 2, B_PDONE,
-  B_OFREE, B_MMADONE, B_EXIT, B_RAW0, B_RFREE0 = B_RAW0 + 2 * kRing, B_COUNT = B_RFREE0 + 2 * kRing
+  B_QREADY = 0, B_QEMPTY, B_FULL0, B_EMPTY0 = B_FULL0 + 4, B_SFULL0 = B_EMPTY0 + 4, B_PFULL0 = B_SFULL0 + 2,
+  B_PDONE0 = B_PFULL0 + 2,  B_OFREE = B_PDONE0 + 2, B_MMADONE0, B_EXIT = B_MMADONE0 + 2, B_RAW0, B_RFREE0 = B_RAW0 + 2 * kRing, B_COUNT = B_RFREE0 + 2 * kRing
 };   // FULL and EMPTY: K stages 0, 1, V stages 0, 1; RAW and RFREE: K slots, V slots
 // Every warp but warp 0 arrives once on B_EXIT when it is done with shared
 // memory, TMEM and its asynchronous operations; warp 0 frees TMEM after that.
@@ -51,10 +52,13 @@ struct NLayout {
   static constexpr int kTile = kT * D * 2;              // one K or V operand tile
   static constexpr int kOffK = 0;                       // 2 stages
   static constexpr int kOffV = kOffK + 2 * kTile;       // 2 stages; with D = 64 the products read 16 KB past each
-  static constexpr int kOffP = kOffV + 2 * kTile;       // P^T: [128 keys][64 rows] fp16, rows of 128 B
+  // P^T: [128 keys][64 rows] fp16, rows of 128 B; up to 32 rows two of them,
+  // side by side, so that a tile's P is written while the previous one is read
+  static constexpr int kOffP = kOffV + 2 * kTile;
+  static constexpr int kPBufs = NR <= 32 ? 2 : 1;
   static constexpr int kOffQ = kOffP + kT * 128;        // [D / 64][NR][128 B]
   // raw slots: kST tokens' codes (8-bit heads fill the room), then their words
-  static constexpr int kST = D == 128 ? 32 : 64;
+  static constexpr int kST = 64;
   static constexpr int kRawWords = kST * D;
   static constexpr int kRawBytes = kRawWords + kST * (D / 32) * 4;
   static constexpr int kOffRaw = kOffQ + NR * D * 2;
@@ -222,10 +226,13 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_narrow_kernel(const __grid_
     }
     mbar_init(&bar[B_SFULL0], 1);
     mbar_init(&bar[B_SFULL0 + 1], 1);
-    mbar_init(&bar[B_PFULL], 4);
-    mbar_init(&bar[B_PDONE], 1);
+    mbar_init(&bar[B_PFULL0], 4);
+    mbar_init(&bar[B_PFULL0 + 1], 4);
+    mbar_init(&bar[B_PDONE0], 1);
+    mbar_init(&bar[B_PDONE0 + 1], 1);
     mbar_init(&bar[B_OFREE], 4);
-    mbar_init(&bar[B_MMADONE], 1);
+    mbar_init(&bar[B_MMADONE0], 1);
+    mbar_init(&bar[B_MMADONE0 + 1], 1);
     mbar_init(&bar[B_EXIT], kExitArrivals);
     for (int k = 0; k < 2 * kRing; ++k) {
       mbar_init(&bar[B_RAW0 + k], 1);
@@ -259,6 +266,39 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_narrow_kernel(const __grid_
   };
 
   if (warp == 0) {
+    // ---------------- issuer of O^T (+)= V^T P^T, then the end of the CTA ----------------
+    constexpr uint32_t id_pv = tc::idesc_f16_f32(kT, NR, true, true);
+    const uint32_t pt = smem_u32(smem + L::kOffP), vb = smem_u32(smem + L::kOffV);
+    const uint32_t d_o = tmem + 2 * NR;
+    uint32_t k = 0, piece = 0;
+    bool ok = true;
+    do {
+      const int n = w.n;
+      for (int j = 0; j < n && ok; ++j, ++k) {
+        ok = wait_all(B_FULL0 + 2 + (k & 1), k >> 1) && wait_all(B_PFULL0 + (k & 1), k >> 1);
+        if (ok && j == 0 && piece > 0) ok = wait_all(B_OFREE, piece - 1);   // the previous piece's O has been read
+        if (!ok) break;
+        tc::fence_after_sync();
+        if (tc::elect_one()) {
+          // (D = 64: channels 64-127 of the A operand are whatever follows the
+          // tile; their rows of O^T are never read)
+          const uint32_t vs = vb + (k & 1) * L::kTile, pk = pt + (k % L::kPBufs) * 64;
+          const uint64_t da = tc::smem_desc_sw128(vs, kT * 128, 1024), db = tc::smem_desc_sw128(pk, kT * 128, 1024);
+          if (j == 0) tc::mma_ss<false>(d_o, da, db, id_pv);
+          else tc::mma_ss<true>(d_o, da, db, id_pv);
+#pragma unroll
+          for (int s = 1; s < kT / 16; ++s)   // 16 keys on: 2 KB, 128 in the descriptors' address field
+            tc::mma_ss<true>(d_o, da + s * 128, db + s * 128, id_pv);
+          tc::commit(&bar[B_EMPTY0 + 2 + (k & 1)]);
+          tc::commit(&bar[B_PDONE0 + (k & 1)]);
+        }
+        __syncwarp();
+      }
+      ++piece;
+    } while (ok && next_piece<NR>(p, w, lane));
+    if (tc::elect_one()) tc::commit(&bar[B_MMADONE0 + 1]);
+    __syncwarp();
+    wait_all(B_MMADONE0 + 1, 0);
     // The other roles finish in bounded time: each stops at its first wait
     // that runs out, and a role waits at most a few times per tile.
     const uint64_t deadline = kWaitNs * static_cast<uint64_t>(16 * total + 16);
@@ -277,80 +317,59 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_narrow_kernel(const __grid_
   }
 
   if (warp == 1) {
-    // ---------------- MMA issuer ----------------
+    // ---------------- issuer of S^T = K Q^T ----------------
     constexpr uint32_t id_qk = tc::idesc_f16_f32(kT, NR, false);
-    constexpr uint32_t id_pv = tc::idesc_f16_f32(kT, NR, true, true);
-    const uint32_t q = smem_u32(smem + L::kOffQ), pt = smem_u32(smem + L::kOffP);
-    const uint32_t kb = smem_u32(smem + L::kOffK), vb = smem_u32(smem + L::kOffV);
-    const uint32_t d_o = tmem + 2 * NR;
+    const uint32_t q = smem_u32(smem + L::kOffQ), kb = smem_u32(smem + L::kOffK);
     uint32_t jj = 0, piece = 0;
     bool ok = true;
-    // O^T (+)= V^T P^T of tile k; `first`: of its piece
-    auto pv = [&](uint32_t k, bool first) -> bool {
-      bool good = wait_all(B_FULL0 + 2 + (k & 1), k >> 1) && wait_all(B_PFULL, k);
-      if (good && first && piece > 0) good = wait_all(B_OFREE, piece - 1);   // the previous piece's O has been read
-      if (!good) return false;
-      tc::fence_after_sync();
-      if (tc::elect_one()) {
-        const uint32_t vs = vb + (k & 1) * L::kTile;
-        // (D = 64: channels 64-127 of the A operand are whatever follows the
-        // tile; their rows of O^T are never read)
-        if (first) tc::mma_ss<false>(d_o, tc::smem_desc_sw128(vs, kT * 128, 1024), tc::smem_desc_sw128(pt, kT * 128, 1024), id_pv);
-        else tc::mma_ss<true>(d_o, tc::smem_desc_sw128(vs, kT * 128, 1024), tc::smem_desc_sw128(pt, kT * 128, 1024), id_pv);
-#pragma unroll
-        for (int s = 1; s < kT / 16; ++s)
-          tc::mma_ss<true>(d_o, tc::smem_desc_sw128(vs + s * 2048, kT * 128, 1024),
-                           tc::smem_desc_sw128(pt + s * 2048, kT * 128, 1024), id_pv);
-        tc::commit(&bar[B_EMPTY0 + 2 + (k & 1)]);
-        tc::commit(&bar[B_PDONE]);
-      }
-      __syncwarp();
-      return true;
-    };
     do {
       const int n = w.n;
       ok = wait_all(B_QREADY, piece);
       for (int j = 0; j < n && ok; ++j, ++jj) {
         ok = wait_all(B_FULL0 + (jj & 1), jj >> 1);
+        if (ok && jj >= 2) ok = wait_all(B_PFULL0 + (jj & 1), (jj >> 1) - 1);   // the S buffer has been read
         if (!ok) break;
         tc::fence_after_sync();
         if (tc::elect_one()) {
-          // S^T = K Q^T (its buffer was read before tile jj - 2's P was complete)
-          const uint32_t ks = kb + (jj & 1) * L::kTile, d_s = tmem + (jj & 1) * NR;
-          tc::mma_ss<false>(d_s, tc::smem_desc_sw128(ks, 16, 1024), tc::smem_desc_sw128(q, 16, 1024), id_qk);
+          const uint32_t d_s = tmem + (jj & 1) * NR;
+          const uint64_t da = tc::smem_desc_sw128(kb + (jj & 1) * L::kTile, 16, 1024);
+          const uint64_t db = tc::smem_desc_sw128(q, 16, 1024);
+          tc::mma_ss<false>(d_s, da, db, id_qk);
 #pragma unroll
-          for (int s = 1; s < D / 16; ++s)
-            tc::mma_ss<true>(d_s, tc::smem_desc_sw128(ks + (s >> 2) * (kT * 128) + (s & 3) * 32, 16, 1024),
-                             tc::smem_desc_sw128(q + (s >> 2) * (NR * 128) + (s & 3) * 32, 16, 1024), id_qk);
+          for (int s = 1; s < D / 16; ++s)    // 16 channels on: 32 B, or the next 64-channel block
+            tc::mma_ss<true>(d_s, da + (s >> 2) * (kT * 8) + (s & 3) * 2, db + (s >> 2) * (NR * 8) + (s & 3) * 2, id_qk);
           tc::commit(&bar[B_SFULL0 + (jj & 1)]);
           tc::commit(&bar[B_EMPTY0 + (jj & 1)]);
           if (j + 1 == n) tc::commit(&bar[B_QEMPTY]);
         }
         __syncwarp();
-        if (j > 0) ok = pv(jj - 1, j == 1);
       }
-      if (ok) ok = pv(jj - 1, n == 1);
       ++piece;
     } while (ok && next_piece<NR>(p, w, lane));
-    if (tc::elect_one()) tc::commit(&bar[B_MMADONE]);
+    // every product this warp issued has completed (a commit with none
+    // pending arrives at once) before the warp reports that it is done
+    if (tc::elect_one()) tc::commit(&bar[B_MMADONE0]);
     __syncwarp();
-    wait_all(B_MMADONE, 0);
+    wait_all(B_MMADONE0, 0);
     tc::fence_before_sync();
     if (lane == 0) mbar_arrive(&bar[B_EXIT]);
     return;
   }
 
-  if (warp == 2) {
-    // ---------------- copies: raw slots of K and V ----------------
+  if (warp < 4) {
+    // ---------------- copies: raw slots of K (warp 2) and of V (warp 3) ----------------
+    // (a warp each: one warp for both held K's copies back while V's ring was full)
+    const int x = warp - 2;
     const int64_t blocks = static_cast<int64_t>(p.c.pB) * (p.c.pT / 64);
     const uint64_t pol = l2_evict_first_policy();
-    uint32_t slot = 0, round = 0;      // the same for both rings
+    uint32_t slot = 0, round = 0;
     bool ok = true;
     do {
       const Seen seen(p, w);
       const int rb = D * p.bits[w.kvh] / 8;                        // code bytes of a token
       const uint32_t cb = L::kST * rb, wb = L::kST * (D / 32) * 4;
-      const int lo64 = seen.lo;
+      const uint8_t* codes = p.codes[x] + p.plane_off[w.kvh];
+      const uint32_t* words = p.sz[x] + w.kvh * blocks * (64 * (D / 32));
       int half[2] = {0, 0};
       for (int j = 0; j < w.n && ok; ++j) {
         if ((j & 31) == 0 && j + lane < w.n) {                     // 32 tiles' pages at a time, a lane each
@@ -358,63 +377,45 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_narrow_kernel(const __grid_
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
             const int a = t0 + 64 * h;
-            const bool is_seen = a < seen.end && (a + 64 > lo64 || a < p.sinks);
+            const bool is_seen = a < seen.end && (a + 64 > seen.lo || a < p.sinks);
             // (a half that nothing sees stands for the other: its rows are masked)
             const int b = is_seen ? a : (h == 0 ? a + 64 : a - 64);
             half[h] = chunk::storage_block(p.c, w.b, b / 64, p.status);
           }
         }
-        int blk[2];
-        blk[0] = __shfl_sync(0xffffffffu, half[0], j & 31);
-        blk[1] = __shfl_sync(0xffffffffu, half[1], j & 31);
-        uint32_t s2 = slot, r2 = round;
 #pragma unroll
-        for (int x = 0; x < 2 && ok; ++x) {                        // K, V
-          s2 = slot;
-          r2 = round;
-          for (int s = 0; s < kT / L::kST && ok; ++s) {
-            const int k = x * kRing + s2;
-            if (r2 > 0) ok = wait_all(B_RFREE0 + k, r2 - 1);
-            if (!ok) break;
-            if (lane == 0) {
-              uint8_t* raw = smem + L::kOffRaw + k * L::kRawBytes;
-              const int tok = s * L::kST;                          // within the tile
-              int64_t at = static_cast<int64_t>(blk[tok / 64]) * 64 + tok % 64;
-              if (!KVQ_IN_RANGE(at >= 0 && at + L::kST <= blocks * 64 &&
-                                    p.plane_off[w.kvh] + (at + L::kST) * rb <= p.codes_bytes, p.status))
-                at = 0;
-              mbar_arrive_expect_tx(&bar[B_RAW0 + k], cb + wb);
-              bulk_g2s_hint(raw, p.codes[x] + p.plane_off[w.kvh] + at * rb, cb, &bar[B_RAW0 + k], pol);
-              bulk_g2s_hint(raw + L::kRawWords, p.sz[x] + (w.kvh * blocks * 64 + at) * (D / 32), wb, &bar[B_RAW0 + k],
-                            pol);
-            }
-            if (++s2 == kRing) {
-              s2 = 0;
-              ++r2;
-            }
+        for (int s = 0; s < kT / L::kST; ++s) {
+          int64_t blk = __shfl_sync(0xffffffffu, half[s * L::kST / 64], j & 31);
+          const int k = x * kRing + slot;
+          if (round > 0) ok = wait_all(B_RFREE0 + k, round - 1);
+          if (!ok) break;
+          if (lane == 0) {
+            uint8_t* raw = smem + L::kOffRaw + k * L::kRawBytes;
+            if (!KVQ_IN_RANGE(blk >= 0 && blk < blocks && p.plane_off[w.kvh] + (blk + 1) * 64 * rb <= p.codes_bytes,
+                              p.status))
+              blk = 0;
+            const int64_t at = blk * 64 + s * L::kST % 64;
+            mbar_arrive_expect_tx(&bar[B_RAW0 + k], cb + wb);
+            bulk_g2s_hint(raw, codes + at * rb, cb, &bar[B_RAW0 + k], pol);
+            bulk_g2s_hint(raw + L::kRawWords, words + at * (D / 32), wb, &bar[B_RAW0 + k], pol);
+          }
+          if (++slot == kRing) {
+            slot = 0;
+            ++round;
           }
           __syncwarp();
-        }
-        if (ok) {
-          slot = s2;
-          round = r2;
         }
       }
     } while (ok && next_piece<NR>(p, w, lane));
     // Every copy has landed before the CTA can exit: on the normal path the
-    // dequant warps have read them all, after a wait that ran out the copies
-    // in flight get one more limit each.
+    // dequant warps have read them all; after a wait that ran out those in
+    // flight get a millisecond.
     if (!ok) {
       const uint64_t t0 = global_ns();
       while (global_ns() - t0 < 1000000ull) {
       }
     }
     __syncwarp();
-    if (lane == 0) mbar_arrive(&bar[B_EXIT]);
-    return;
-  }
-
-  if (warp == 3) {
     if (lane == 0) mbar_arrive(&bar[B_EXIT]);
     return;
   }
@@ -450,6 +451,9 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_narrow_kernel(const __grid_
   const uint32_t o_addr = tmem + lanes + 2 * NR;
   const uint32_t p_row = smem_u32(smem + L::kOffP) + key * 128;
   const float sl2 = p.scale_log2;
+  // P.V of tile k is complete (one barrier for even tiles, one for odd: a
+  // single one could be two phases ahead of a wait)
+  auto product_done = [&](uint32_t k) -> bool { return wait_all(B_PDONE0 + (k & 1), k >> 1); };
   uint32_t jj = 0;
   bool ok = true, stop = false;
   do {
@@ -524,7 +528,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_narrow_kernel(const __grid_
 #pragma unroll
         for (int i = 0; i < NR; ++i) l[i] *= row_a[i];
         if (j > 0) {
-          ok = wait_all(B_PDONE, jj - 1) && ok;
+          ok = product_done(jj - 1) && ok;
           tc::fence_after_sync();
 #pragma unroll
           for (int c0 = 0; c0 < NR; c0 += CH) {
@@ -540,7 +544,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_narrow_kernel(const __grid_
           tc::wait_st();
         }
       }
-      // P^T = 2^(S - m): this key's row of the operand tile, once the previous tile's product has read it
+      // P^T = 2^(S - m): this key's row of the operand tile, once the product that used the buffer has read it
       uint32_t pk[NR / 2];
 #pragma unroll
       for (int i = 0; i < NR; i += 4) {
@@ -556,18 +560,18 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_narrow_kernel(const __grid_
         pk[i / 2] = pack_half2(e[0], e[1]);
         pk[i / 2 + 1] = pack_half2(e[2], e[3]);
       }
-      if (jj > 0) ok = wait_all(B_PDONE, jj - 1) && ok;
+      if (jj >= L::kPBufs) ok = product_done(jj - L::kPBufs) && ok;
 #pragma unroll
       for (int i = 0; i < NR / 8; ++i)
-        sts128(p_row + ((i ^ (key & 7)) << 4), pk[4 * i], pk[4 * i + 1], pk[4 * i + 2], pk[4 * i + 3]);
+        sts128(p_row + (((i + (jj % L::kPBufs) * 4) ^ (key & 7)) << 4), pk[4 * i], pk[4 * i + 1], pk[4 * i + 2], pk[4 * i + 3]);
       fence_proxy_async_smem();
       tc::fence_before_sync();
       __syncwarp();
-      if (lane == 0) mbar_arrive(&bar[B_PFULL]);
+      if (lane == 0) mbar_arrive(&bar[B_PFULL0 + (jj & 1)]);
     }
     if (stop) break;
     // ---- end of the piece: sums over the keys, then O^T / sum ----
-    ok = wait_all(B_PDONE, jj - 1) && ok;
+    ok = product_done(jj - 1) && ok;
     if (group_or(!ok)) break;
     tc::fence_after_sync();
 #pragma unroll
