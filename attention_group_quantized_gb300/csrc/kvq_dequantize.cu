@@ -16,7 +16,7 @@
 namespace kvq {
 namespace {
 
-constexpr int kWarps = 8;
+constexpr int kWarps = 4;
 
 struct DqParams {
   chunk::View c;
@@ -24,7 +24,7 @@ struct DqParams {
   const uint32_t* sz;
   void* out;
   int32_t* status;
-  int32_t Hkv, tiles;       // tiles: runs of kRows rows
+  int32_t Hkv, tiles;       // tiles: runs of a warp's rows
   int64_t codes_bytes;      // size of the code buffer (the debug build's index checks)
   int64_t plane_off[KVQ_MAX_HKV];
   int8_t bits[KVQ_MAX_HKV];
@@ -43,12 +43,15 @@ __device__ __forceinline__ void values8(float (&x)[8], uint2 c, int bits, uint32
   }
 }
 
-template <int D, bool F32>
+// NP: passes of 32 lanes whose loads are in flight together (NP x 256 / D rows
+// a warp).  Eight amortise the rows' look-up best when there are warps enough
+// (79 MB: 17.3 us, four 19.1); two spread a short call over more of them (5 MB:
+// 3.4 us, eight 3.8).
+template <int D, bool F32, int NP>
 __global__ void __launch_bounds__(kWarps * 32) dequantize_kernel(const __grid_constant__ DqParams p) {
   constexpr int G = D / 32;
   constexpr int LPR = D / 8;          // lanes per row
   constexpr int RPP = 32 / LPR;       // rows per pass
-  constexpr int NP = 4;               // passes whose loads are in flight together
   constexpr int R = RPP * NP;         // rows per warp
   // launched as a programmatic dependent: the rows may have been written by
   // the kernel before it
@@ -127,8 +130,9 @@ cudaError_t launch_dequantize(const DequantizeArgs& a, cudaStream_t stream) {
     p.plane_off[h] = a.layout.plane_off[h];
     p.bits[h] = a.layout.bits[h];
   }
-  const int R = 4 * 256 / s.D;
-  p.tiles = (a.chunk.rows + R - 1) / R;
+  auto tiles_of = [&](int np) { return (a.chunk.rows + np * (256 / s.D) - 1) / (np * (256 / s.D)); };
+  const bool many = static_cast<int64_t>(tiles_of(8)) * p.Hkv >= 16 * device_sm_count();
+  p.tiles = tiles_of(many ? 8 : 2);
   const int64_t warps = static_cast<int64_t>(p.tiles) * p.Hkv;
   const int64_t blocks = std::min<int64_t>((warps + kWarps - 1) / kWarps, int64_t(1) << 30);
   cudaLaunchConfig_t cfg = {};
@@ -141,11 +145,14 @@ cudaError_t launch_dequantize(const DequantizeArgs& a, cudaStream_t stream) {
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   const bool f32 = a.out_dtype == KVQ_OUT_F32;
+  auto launch = [&](auto kernel2, auto kernel8) {
+    return many ? cudaLaunchKernelEx(&cfg, kernel8, p) : cudaLaunchKernelEx(&cfg, kernel2, p);
+  };
   if (s.D == 128)
-    return f32 ? cudaLaunchKernelEx(&cfg, dequantize_kernel<128, true>, p)
-               : cudaLaunchKernelEx(&cfg, dequantize_kernel<128, false>, p);
-  return f32 ? cudaLaunchKernelEx(&cfg, dequantize_kernel<64, true>, p)
-             : cudaLaunchKernelEx(&cfg, dequantize_kernel<64, false>, p);
+    return f32 ? launch(dequantize_kernel<128, true, 2>, dequantize_kernel<128, true, 8>)
+               : launch(dequantize_kernel<128, false, 2>, dequantize_kernel<128, false, 8>);
+  return f32 ? launch(dequantize_kernel<64, true, 2>, dequantize_kernel<64, true, 8>)
+             : launch(dequantize_kernel<64, false, 2>, dequantize_kernel<64, false, 8>);
 }
 
 }  // namespace kvq

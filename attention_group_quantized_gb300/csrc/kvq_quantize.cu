@@ -503,8 +503,10 @@ struct ACParams {
   int8_t bits[KVQ_MAX_HKV];
 };
 
+constexpr int kAppendWarps = 4;   // per block (eight: 53.4 us for 176 MB against 51.6)
+
 template <int D>
-__global__ void __launch_bounds__(256, KVQ_QUANT_MIN_BLOCKS) append_chunk_kernel(const __grid_constant__ ACParams p) {
+__global__ void __launch_bounds__(kAppendWarps * 32, 2 * KVQ_QUANT_MIN_BLOCKS) append_chunk_kernel(const __grid_constant__ ACParams p) {
   constexpr int G = D / 32;
   constexpr int R = 32 / G;                   // rows per warp
   grid_launch_dependents();
@@ -512,8 +514,8 @@ __global__ void __launch_bounds__(256, KVQ_QUANT_MIN_BLOCKS) append_chunk_kernel
   if (blockIdx.x == 0) chunk::check_sequences(p.c, threadIdx.x, blockDim.x, p.status);
   const int64_t nw = static_cast<int64_t>(p.tiles) * p.Hkv * 2;
   const int64_t storage = static_cast<int64_t>(p.c.pB) * p.c.pT;
-  for (int64_t u = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5); u < nw;
-       u += static_cast<int64_t>(gridDim.x) * 8) {
+  for (int64_t u = static_cast<int64_t>(blockIdx.x) * kAppendWarps + (threadIdx.x >> 5); u < nw;
+       u += static_cast<int64_t>(gridDim.x) * kAppendWarps) {
     const int job = static_cast<int>(u & 1);  // K and V of the same rows side by side: they share the look-up's lines
     const uint32_t th = static_cast<uint32_t>(u >> 1);
     const int tile = static_cast<int>(th / static_cast<uint32_t>(p.Hkv));
@@ -768,10 +770,10 @@ cudaError_t launch_append_chunk(const AppendChunkArgs& a, cudaStream_t stream) {
   }
   // one warp per (run of rows, head, K or V); grid-stride beyond 2^30 blocks
   const int64_t warps = static_cast<int64_t>(p.tiles) * p.Hkv * 2;
-  const int64_t blocks = std::min<int64_t>((warps + 7) / 8, int64_t(1) << 30);
+  const int64_t blocks = std::min<int64_t>((warps + kAppendWarps - 1) / kAppendWarps, int64_t(1) << 30);
   const unsigned g = static_cast<unsigned>(blocks);
-  if (a.k->D == 128) append_chunk_kernel<128><<<g, 256, 0, stream>>>(p);
-  else append_chunk_kernel<64><<<g, 256, 0, stream>>>(p);
+  if (a.k->D == 128) append_chunk_kernel<128><<<g, kAppendWarps * 32, 0, stream>>>(p);
+  else append_chunk_kernel<64><<<g, kAppendWarps * 32, 0, stream>>>(p);
   return cudaGetLastError();
 }
 
