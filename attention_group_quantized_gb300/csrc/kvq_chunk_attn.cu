@@ -288,6 +288,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_attention_kernel(const __gr
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::kOffMisc);
   int32_t* flag = reinterpret_cast<int32_t*>(smem + L::kOffMisc) + 1;   // merge flags of the two slots
   int32_t* pre = reinterpret_cast<int32_t*>(smem + L::kOffPre);         // tiles of sequences 0 .. b-1, per KV head
+  Walk* walks = reinterpret_cast<Walk*>(smem + L::kOffWalk);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
   if (threadIdx.x == 0) {
@@ -316,21 +317,25 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_attention_kernel(const __gr
   count_tiles<kRows>(p, pre, warp, lane, kThreads / 32);
   __syncthreads();
   if (warp == 0) {
-    sum_tiles(p, pre, lane);
     tc::tmem_alloc(tmem_slot, kTmemCols);
     tc::tmem_relinquish();
+  } else if (warp == 1) {
+    sum_tiles(p, pre, lane);
+    start_walk<kRows>(p, pre, walks[1], lane);
   }
   tc::fence_before_sync();
   __syncthreads();
   tc::fence_after_sync();
   const uint32_t tmem = *tmem_slot;
 
-  Walk& w = reinterpret_cast<Walk*>(smem + L::kOffWalk)[warp];
-  const int64_t total = start_walk<kRows>(p, pre, w, lane);
+  Walk& w = walks[warp];
+  const int64_t total = walks[1].left;
   if (total <= 0) {   // the whole CTA: nothing was started
     if (warp == 0) tc::tmem_dealloc(tmem, kTmemCols);
     return;
   }
+  if (warp != 1) copy_walk(w, walks[1], lane);
+  __syncthreads();   // (warp 1's walk goes on from here)
 
   // Registers: launched with 128 per thread (checked on the host); per
   // warpgroup 112 + 160 + 120 + 120 = 4 x 128 (of eight such splits the

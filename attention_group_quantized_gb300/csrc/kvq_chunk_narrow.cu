@@ -12,16 +12,17 @@
 // score exceeds it by more than 2^8 (a vote of the four warps a tile), and the
 // sums are per thread until the piece ends.
 //
-// One CTA (512 threads, one per SM) walks its range of the work list
+// One CTA (896 threads, one per SM) walks its range of the work list
 // (kvq_chunk_walk.cuh):
 //   warp 0       TMEM, and the issue of V^T P^T; warp 1 issues K Q^T (a warp
 //                each: neither waits for what only the other needs); warps 2 and 3 keep rings of
 //                raw code slots of K and V full by bulk copies (about 50 KB in
 //                flight an SM, which is what the latency of HBM asks for);
-//   warps 4-7    K codes (and the piece's queries) to fp16 operand tiles;
-//   warps 8-11   V codes likewise;
-//   warps 12-15  softmax, rescaling, the piece's output or partial, the merge.
-// TMEM: S^T twice NR columns, O^T NR columns.
+//   warps 4-11   K codes (and the piece's queries) to fp16 operand tiles;
+//                warps 12-19 V codes likewise (two warps a scheduler for each
+//                part: one alone took 1.2 us a tile, most of it latency);
+//   warps 20-27  softmax (two states, of even and of odd tiles), rescaling, the piece's output or partial, the merge.
+// TMEM: S^T and O^T of each state, NR columns each.
 #include <cmath>
 #include <mutex>
 
@@ -36,13 +37,14 @@ namespace {
 using namespace tile;
 using namespace chunk_walk;
 
-constexpr int kThreads = 512;
-constexpr int kRing = 3;               // raw slots of K, and as many of V
+constexpr int kThreads = 896;
+constexpr int kMaxRing = 3;            // most raw slots of K, and as many of V
 
 enum {
   B_QREADY = 0, B_QEMPTY, B_FULL0, B_EMPTY0 = B_FULL0 + 4, B_SFULL0 = B_EMPTY0 + 4, B_PFULL0 = B_SFULL0 + 2,
-  B_PDONE0 = B_PFULL0 + 2,  B_OFREE = B_PDONE0 + 2, B_MMADONE0, B_EXIT = B_MMADONE0 + 2, B_RAW0, B_RFREE0 = B_RAW0 + 2 * kRing, B_COUNT = B_RFREE0 + 2 * kRing
-};   // FULL and EMPTY: K stages 0, 1, V stages 0, 1; RAW and RFREE: K slots, V slots
+  B_PDONE0 = B_PFULL0 + 2, B_OFREE = B_PDONE0 + 2, B_STATE, B_MMADONE0, B_EXIT = B_MMADONE0 + 2, B_RAW0,
+  B_RFREE0 = B_RAW0 + 2 * kMaxRing, B_COUNT = B_RFREE0 + 2 * kMaxRing
+};   // FULL and EMPTY: K stages 0, 1, V stages 0, 1; SFULL, PFULL, PDONE: states; RAW and RFREE: K slots, V slots
 // Every warp but warp 0 arrives once on B_EXIT when it is done with shared
 // memory, TMEM and its asynchronous operations; warp 0 frees TMEM after that.
 constexpr int kExitArrivals = kThreads / 32 - 1;
@@ -52,11 +54,12 @@ struct NLayout {
   static constexpr int kTile = kT * D * 2;              // one K or V operand tile
   static constexpr int kOffK = 0;                       // 2 stages
   static constexpr int kOffV = kOffK + 2 * kTile;       // 2 stages; with D = 64 the products read 16 KB past each
-  // P^T: [128 keys][64 rows] fp16, rows of 128 B; up to 32 rows two of them,
-  // side by side, so that a tile's P is written while the previous one is read
+  // P^T of each state: [128 keys][64 rows] fp16, rows of 128 B; up to 32 rows
+  // the two share the lines
   static constexpr int kOffP = kOffV + 2 * kTile;
-  static constexpr int kPBufs = NR <= 32 ? 2 : 1;
-  static constexpr int kOffQ = kOffP + kT * 128;        // [D / 64][NR][128 B]
+  static constexpr int kPStep = NR <= 32 ? 64 : kT * 128;
+  static constexpr int kOffQ = kOffP + (NR <= 32 ? 1 : 2) * kT * 128;   // [D / 64][NR][128 B]
+  static constexpr int kRing = NR <= 32 ? kMaxRing : 2;    // what shared memory has room for
   // raw slots: kST tokens' codes (8-bit heads fill the room), then their words
   static constexpr int kST = 64;
   static constexpr int kRawWords = kST * D;
@@ -64,28 +67,31 @@ struct NLayout {
   static constexpr int kOffRaw = kOffQ + NR * D * 2;
   static constexpr int kOffBar = kOffRaw + 2 * kRing * kRawBytes;
   static constexpr int kOffMisc = kOffBar + B_COUNT * 8;     // TMEM address
-  static constexpr int kOffRow = (kOffMisc + 16 + 15) / 16 * 16;   // per row: max, factor, position, four warps' values
-  static constexpr int kOffWalk = kOffRow + NR * 7 * 4;
+  static constexpr int kOffRow = (kOffMisc + 16 + 15) / 16 * 16;   // per state and row: position, max, factor, four warps' values
+  static constexpr int kOffWalk = kOffRow + NR * 2 * 7 * 4;
   static constexpr int kOffPre = kOffWalk + kThreads / 32 * 128;
   static constexpr size_t bytes(int B) { return 1024 + kOffPre + static_cast<size_t>(B + 1) * 4; }
 };
 constexpr int kMaxB = 1024;            // sequences (their tile counts lie in shared memory)
 static_assert(NLayout<128, 64>::bytes(kMaxB) <= 232448, "shared memory");
+static_assert(16 * 128 * 4 <= kT * 128 && 32 * 128 * 4 <= kT * 128 && 64 * 128 * 4 <= 2 * kT * 128,
+              "the output rows fit the P buffers");
 
-// Whether any of the softmax warpgroup's 128 threads says so (all take part).
-__device__ __forceinline__ bool group_or(bool x) {
+// Whether any of a softmax warpgroup's 128 threads says so (all take part);
+// id: the warpgroup's barrier.
+__device__ __forceinline__ bool group_or(bool x, int id) {
   uint32_t r;
   asm volatile(
       "{\n\t.reg .pred p, q;\n\t"
       "setp.ne.u32 p, %1, 0;\n\t"
-      "barrier.cta.red.or.pred q, 1, 128, p;\n\t"
+      "barrier.cta.red.or.pred q, %2, 128, p;\n\t"
       "selp.u32 %0, 1, 0, q;\n\t}"
       : "=r"(r)
-      : "r"(x ? 1u : 0u)
+      : "r"(x ? 1u : 0u), "r"(id)
       : "memory");
   return r != 0;
 }
-__device__ __forceinline__ void group_sync() { asm volatile("barrier.cta.sync 1, 128;" ::: "memory"); }
+__device__ __forceinline__ void group_sync(int id) { asm volatile("barrier.cta.sync %0, 128;" ::"r"(id) : "memory"); }
 
 // Floats as integers of the same order (for the integer warp maximum).
 __device__ __forceinline__ int to_ordered(float x) {
@@ -94,14 +100,45 @@ __device__ __forceinline__ int to_ordered(float x) {
 }
 __device__ __forceinline__ float from_ordered(int i) { return __int_as_float(i ^ ((i >> 31) & 0x7FFFFFFF)); }
 
-// One dequant warpgroup's part (0: K, 1: V) of a piece's tiles.
+// The warp's sums of NR rows' values, one per lane and row, to dst[NR]: halves
+// of the rows change sides at each step, so a row's value is added up in
+// 31 shuffles a warp and 32 rows instead of five for each.
+template <int NR>
+__device__ __forceinline__ void sum_rows(float (&l)[NR], int lane, int32_t* dst) {
+#pragma unroll
+  for (int r0 = 0; r0 < NR; r0 += 32) {
+    constexpr int W = NR < 32 ? NR : 32;
+    int row = 0;
+#pragma unroll
+    for (int o = 16, n = W / 2; o > 0; o >>= 1, n >>= 1) {
+      if (n > 0) {
+        const bool up = lane & o;         // keeps rows n .. 2n - 1 of those it has
+#pragma unroll
+        for (int i = 0; i < n; ++i) {
+          const float give = up ? l[r0 + i] : l[r0 + n + i];
+          const float keep = up ? l[r0 + n + i] : l[r0 + i];
+          l[r0 + i] = keep + __shfl_xor_sync(0xffffffffu, give, o);
+        }
+        row += up ? n : 0;
+      } else {
+        l[r0] += __shfl_xor_sync(0xffffffffu, l[r0], o);   // (16 rows: both lanes of a pair have the row)
+      }
+    }
+    dst[r0 + row] = __float_as_int(l[r0]);
+  }
+}
+
+// One part (0: K, 1: V) of a piece's tiles by its two warpgroups: raw slots (64
+// tokens) to rows of the operand tile, warpgroup `sub` taking every second
+// iteration.
 template <int D, int NR, int BITS>
 __device__ __forceinline__ bool dequant_piece(const CParams& p, uint8_t* smem, uint64_t* bar, const Walk& w, int which,
-                                              uint32_t& jj, uint32_t& slot, uint32_t& round, int t, int lane) {
+                                              int sub, uint32_t& jj, uint32_t& slot, uint32_t& round, int t, int lane) {
   using L = NLayout<D, NR>;
   using F = DqFmt<D, BITS>;
-  constexpr int IPS = L::kST / F::RPI;      // iterations per slot
-  static_assert(IPS * F::RPI == L::kST, "whole iterations per slot");
+  constexpr int H = F::NI / 2;              // iterations per slot, both warpgroups'
+  static_assert(H * F::RPI == 64, "whole iterations per slot");
+  constexpr int N = H > 1 ? H / 2 : 1;      // this warpgroup's (of a slot with one: every second slot)
   int row, c;
   dq_lane<D, BITS>(t, row, c);
   for (int j = 0; j < w.n; ++j, ++jj) {
@@ -111,30 +148,38 @@ __device__ __forceinline__ bool dequant_piece(const CParams& p, uint8_t* smem, u
       return false;
     const uint32_t dst = smem_u32(smem + (which ? L::kOffV : L::kOffK) + st * L::kTile);
 #pragma unroll
-    for (int s = 0; s < kT / L::kST; ++s) {
-      const int k = which * kRing + slot;
+    for (int s = 0; s < 2; ++s) {
+      const int k = which * L::kRing + static_cast<int>(slot);
       if (!__all_sync(0xffffffffu, mbar_wait(&bar[B_RAW0 + k], round & 1, p.status, kWaitNs))) return false;
+      const bool mine = H > 1 || s == sub;
       const uint8_t* raw = smem + L::kOffRaw + k * L::kRawBytes;
       const uint4* codes = reinterpret_cast<const uint4*>(raw + row * F::R + c * 16);
       const uint32_t* words = reinterpret_cast<const uint32_t*>(raw + L::kRawWords) + row * (D / 32) + c * F::VPC / 32;
-      uint4 v[IPS];
-      uint32_t word[IPS];
+      uint4 v[N];
+      uint32_t word[N];
+      if (mine) {
 #pragma unroll
-      for (int it = 0; it < IPS; ++it) {
-        v[it] = codes[it * F::RPI * F::R / 16];
-        word[it] = words[it * F::RPI * (D / 32)];
+        for (int i = 0; i < N; ++i) {
+          const int it = H > 1 ? 2 * i + sub : 0;
+          v[i] = codes[it * F::RPI * F::R / 16];
+          word[i] = words[it * F::RPI * (D / 32)];
+        }
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(&bar[B_RFREE0 + k]);
+      if (mine) {
 #pragma unroll
-      for (int it = 0; it < IPS; ++it)
-        dequant_chunk<BITS>(dst, F::RPI * (s * IPS + it) + row, c * F::VPC, v[it], word[it]);
-      if (++slot == kRing) {
+        for (int i = 0; i < N; ++i) {
+          const int it = s * H + (H > 1 ? 2 * i + sub : 0);
+          dequant_chunk<BITS>(dst, F::RPI * it + row, c * F::VPC, v[i], word[i]);
+        }
+      }
+      if (++slot == L::kRing) {
         slot = 0;
         ++round;
       }
     }
-    if (which) clear_unseen<D, BITS>(dst, p, w, w.t.tile(w.i + j) * kT, row, c);
+    if (which) clear_unseen<D, BITS>(dst, p, w, w.t.tile(w.i + j) * kT, row, c, sub, F::NI, 2);
     fence_proxy_async_smem();
     __syncwarp();
     if (lane == 0) mbar_arrive(&bar[B_FULL0 + 2 * which + st]);
@@ -204,24 +249,21 @@ __device__ __forceinline__ void merge_row(const CParams& p, const Walk& w, const
 template <int D, int NR>
 __global__ void __launch_bounds__(kThreads, 1) chunk_narrow_kernel(const __grid_constant__ CParams p) {
   using L = NLayout<D, NR>;
-  constexpr uint32_t kCols = NR == 16 ? 64 : NR == 32 ? 128 : 256;   // TMEM columns (a power of two)
+  constexpr uint32_t kCols = 4 * NR;                                 // TMEM: S^T and O^T of both states
   constexpr int CH = NR < 32 ? NR : 32;                              // columns handled at a time
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = smem_raw + (-smem_u32(smem_raw) & 1023u);
   uint64_t* bar = reinterpret_cast<uint64_t*>(smem + L::kOffBar);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::kOffMisc);
-  float* row_m = reinterpret_cast<float*>(smem + L::kOffRow);        // running max, log2 domain
-  float* row_a = row_m + NR;                                         // factor of the last move of the max
-  int32_t* row_pos = reinterpret_cast<int32_t*>(row_a + NR);         // position in the cache
-  int32_t* row_w = row_pos + NR;                                     // [4 warps][NR]: maxima, sums
   int32_t* pre = reinterpret_cast<int32_t*>(smem + L::kOffPre);
+  Walk* walks = reinterpret_cast<Walk*>(smem + L::kOffWalk);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
   if (threadIdx.x == 0) {
     mbar_init(&bar[B_QREADY], 4);
     mbar_init(&bar[B_QEMPTY], 1);
     for (int k = 0; k < 4; ++k) {
-      mbar_init(&bar[B_FULL0 + k], 4);
+      mbar_init(&bar[B_FULL0 + k], 8);
       mbar_init(&bar[B_EMPTY0 + k], 1);
     }
     mbar_init(&bar[B_SFULL0], 1);
@@ -231,12 +273,13 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_narrow_kernel(const __grid_
     mbar_init(&bar[B_PDONE0], 1);
     mbar_init(&bar[B_PDONE0 + 1], 1);
     mbar_init(&bar[B_OFREE], 4);
+    mbar_init(&bar[B_STATE], 4);
     mbar_init(&bar[B_MMADONE0], 1);
     mbar_init(&bar[B_MMADONE0 + 1], 1);
     mbar_init(&bar[B_EXIT], kExitArrivals);
-    for (int k = 0; k < 2 * kRing; ++k) {
+    for (int k = 0; k < 2 * L::kRing; ++k) {
       mbar_init(&bar[B_RAW0 + k], 1);
-      mbar_init(&bar[B_RFREE0 + k], 4);
+      mbar_init(&bar[B_RFREE0 + k], 8);
     }
     fence_barrier_init();
   }
@@ -247,50 +290,59 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_narrow_kernel(const __grid_
   count_tiles<NR>(p, pre, warp, lane, kThreads / 32);
   __syncthreads();
   if (warp == 0) {
-    sum_tiles(p, pre, lane);
     tc::tmem_alloc(tmem_slot, kCols);
     tc::tmem_relinquish();
+  } else if (warp == 1) {
+    sum_tiles(p, pre, lane);
+    start_walk<NR>(p, pre, walks[1], lane);
   }
   tc::fence_before_sync();
   __syncthreads();
   tc::fence_after_sync();
   const uint32_t tmem = *tmem_slot;
-  Walk& w = reinterpret_cast<Walk*>(smem + L::kOffWalk)[warp];
-  const int64_t total = start_walk<NR>(p, pre, w, lane);
+  Walk& w = walks[warp];
+  const int64_t total = walks[1].left;
   if (total <= 0) {   // the whole CTA: nothing was started
     if (warp == 0) tc::tmem_dealloc(tmem, kCols);
     return;
   }
+  if (warp != 1) copy_walk(w, walks[1], lane);
+  __syncthreads();   // (warp 1's walk goes on from here)
   auto wait_all = [&](int which, uint32_t parity) -> bool {
     return __all_sync(0xffffffffu, mbar_wait(&bar[which], parity & 1, p.status, kWaitNs));
   };
 
+  // Registers: launched with 72 per thread (checked on the host); per
+  // warpgroup 56 + 4 x 56 + 2 x 112 = 7 x 72.
+  if (warp < 4) tc::reg_dealloc<56>();
   if (warp == 0) {
     // ---------------- issuer of O^T (+)= V^T P^T, then the end of the CTA ----------------
     constexpr uint32_t id_pv = tc::idesc_f16_f32(kT, NR, true, true);
     const uint32_t pt = smem_u32(smem + L::kOffP), vb = smem_u32(smem + L::kOffV);
-    const uint32_t d_o = tmem + 2 * NR;
-    uint32_t k = 0, piece = 0;
+    uint32_t k = 0, piece = 0, cnt[2] = {0, 0};   // tiles, and each state's
     bool ok = true;
     do {
       const int n = w.n;
       for (int j = 0; j < n && ok; ++j, ++k) {
-        ok = wait_all(B_FULL0 + 2 + (k & 1), k >> 1) && wait_all(B_PFULL0 + (k & 1), k >> 1);
+        const int x = j & 1;                        // the tile's state
+        ok = wait_all(B_FULL0 + 2 + (k & 1), k >> 1) && wait_all(B_PFULL0 + x, cnt[x]);
         if (ok && j == 0 && piece > 0) ok = wait_all(B_OFREE, piece - 1);   // the previous piece's O has been read
         if (!ok) break;
+        ++cnt[x];
         tc::fence_after_sync();
         if (tc::elect_one()) {
           // (D = 64: channels 64-127 of the A operand are whatever follows the
           // tile; their rows of O^T are never read)
-          const uint32_t vs = vb + (k & 1) * L::kTile, pk = pt + (k % L::kPBufs) * 64;
-          const uint64_t da = tc::smem_desc_sw128(vs, kT * 128, 1024), db = tc::smem_desc_sw128(pk, kT * 128, 1024);
-          if (j == 0) tc::mma_ss<false>(d_o, da, db, id_pv);
+          const uint32_t vs = vb + (k & 1) * L::kTile, d_o = tmem + 2 * NR + x * NR;
+          const uint64_t da = tc::smem_desc_sw128(vs, kT * 128, 1024);
+          const uint64_t db = tc::smem_desc_sw128(pt + x * L::kPStep, kT * 128, 1024);
+          if (j < 2) tc::mma_ss<false>(d_o, da, db, id_pv);
           else tc::mma_ss<true>(d_o, da, db, id_pv);
 #pragma unroll
           for (int s = 1; s < kT / 16; ++s)   // 16 keys on: 2 KB, 128 in the descriptors' address field
             tc::mma_ss<true>(d_o, da + s * 128, db + s * 128, id_pv);
           tc::commit(&bar[B_EMPTY0 + 2 + (k & 1)]);
-          tc::commit(&bar[B_PDONE0 + (k & 1)]);
+          tc::commit(&bar[B_PDONE0 + x]);
         }
         __syncwarp();
       }
@@ -320,25 +372,27 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_narrow_kernel(const __grid_
     // ---------------- issuer of S^T = K Q^T ----------------
     constexpr uint32_t id_qk = tc::idesc_f16_f32(kT, NR, false);
     const uint32_t q = smem_u32(smem + L::kOffQ), kb = smem_u32(smem + L::kOffK);
-    uint32_t jj = 0, piece = 0;
+    uint32_t jj = 0, piece = 0, cnt[2] = {0, 0};
     bool ok = true;
     do {
       const int n = w.n;
       ok = wait_all(B_QREADY, piece);
       for (int j = 0; j < n && ok; ++j, ++jj) {
+        const int x = j & 1;
         ok = wait_all(B_FULL0 + (jj & 1), jj >> 1);
-        if (ok && jj >= 2) ok = wait_all(B_PFULL0 + (jj & 1), (jj >> 1) - 1);   // the S buffer has been read
+        if (ok && cnt[x] > 0) ok = wait_all(B_PFULL0 + x, cnt[x] - 1);   // the state's S has been read
         if (!ok) break;
+        ++cnt[x];
         tc::fence_after_sync();
         if (tc::elect_one()) {
-          const uint32_t d_s = tmem + (jj & 1) * NR;
+          const uint32_t d_s = tmem + x * NR;
           const uint64_t da = tc::smem_desc_sw128(kb + (jj & 1) * L::kTile, 16, 1024);
           const uint64_t db = tc::smem_desc_sw128(q, 16, 1024);
           tc::mma_ss<false>(d_s, da, db, id_qk);
 #pragma unroll
           for (int s = 1; s < D / 16; ++s)    // 16 channels on: 32 B, or the next 64-channel block
             tc::mma_ss<true>(d_s, da + (s >> 2) * (kT * 8) + (s & 3) * 2, db + (s >> 2) * (NR * 8) + (s & 3) * 2, id_qk);
-          tc::commit(&bar[B_SFULL0 + (jj & 1)]);
+          tc::commit(&bar[B_SFULL0 + x]);
           tc::commit(&bar[B_EMPTY0 + (jj & 1)]);
           if (j + 1 == n) tc::commit(&bar[B_QEMPTY]);
         }
@@ -384,9 +438,9 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_narrow_kernel(const __grid_
           }
         }
 #pragma unroll
-        for (int s = 0; s < kT / L::kST; ++s) {
-          int64_t blk = __shfl_sync(0xffffffffu, half[s * L::kST / 64], j & 31);
-          const int k = x * kRing + slot;
+        for (int s = 0; s < 2; ++s) {
+          int64_t blk = __shfl_sync(0xffffffffu, half[s], j & 31);
+          const int k = x * L::kRing + static_cast<int>(slot);
           if (round > 0) ok = wait_all(B_RFREE0 + k, round - 1);
           if (!ok) break;
           if (lane == 0) {
@@ -394,12 +448,12 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_narrow_kernel(const __grid_
             if (!KVQ_IN_RANGE(blk >= 0 && blk < blocks && p.plane_off[w.kvh] + (blk + 1) * 64 * rb <= p.codes_bytes,
                               p.status))
               blk = 0;
-            const int64_t at = blk * 64 + s * L::kST % 64;
+            const int64_t at = blk * 64;
             mbar_arrive_expect_tx(&bar[B_RAW0 + k], cb + wb);
             bulk_g2s_hint(raw, codes + at * rb, cb, &bar[B_RAW0 + k], pol);
             bulk_g2s_hint(raw + L::kRawWords, words + at * (D / 32), wb, &bar[B_RAW0 + k], pol);
           }
-          if (++slot == kRing) {
+          if (++slot == L::kRing) {
             slot = 0;
             ++round;
           }
@@ -420,22 +474,23 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_narrow_kernel(const __grid_
     return;
   }
 
-  if (warp < 12) {
-    // ---------------- dequant warpgroups: K (and the queries), V ----------------
-    const int which = warp < 8 ? 0 : 1;
-    const int t = threadIdx.x - 128 - 128 * which;
+  if (warp < 20) {
+    tc::reg_dealloc<56>();
+    // ---------------- dequant warpgroups: two for K (the first also the queries), two for V ----------------
+    const int wg = (warp - 4) >> 2, which = wg >> 1, sub = wg & 1;
+    const int t = threadIdx.x & 127;
     uint32_t jj = 0, slot = 0, round = 0, piece = 0;
     bool ok = true;
     do {
-      if (which == 0) {
+      if (wg == 0) {
         ok = load_queries<D, NR, NR>(p, smem_u32(smem + L::kOffQ), &bar[B_QEMPTY], w, t, (piece - 1) & 1, piece > 0);
         if (!ok) break;
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(&bar[B_QREADY]);
       }
-      ok = p.bits[w.kvh] == 4 ? dequant_piece<D, NR, 4>(p, smem, bar, w, which, jj, slot, round, t, lane)
-                              : dequant_piece<D, NR, 8>(p, smem, bar, w, which, jj, slot, round, t, lane);
+      ok = p.bits[w.kvh] == 4 ? dequant_piece<D, NR, 4>(p, smem, bar, w, which, sub, jj, slot, round, t, lane)
+                              : dequant_piece<D, NR, 8>(p, smem, bar, w, which, sub, jj, slot, round, t, lane);
       ++piece;
     } while (ok && next_piece<NR>(p, w, lane));
     __syncwarp();
@@ -443,40 +498,53 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_narrow_kernel(const __grid_
     return;
   }
 
-  // ---------------- softmax warpgroup: thread = key of the tile, then channel of O^T ----------------
-  // (its four warps take every decision together, so that its barriers are
-  // always met by all: a wait that ran out is a vote)
+  tc::reg_alloc<112>();
+  // ---------------- softmax warpgroups: thread = key of the tile, then channel of O^T ----------------
+  // Two states of the online softmax, each with its own maxima, sums and O^T:
+  // warpgroup x takes the piece's tiles j with j % 2 == x, so that a tile's
+  // chain of waits (scores, vote, weights, products) runs under the other's;
+  // at the piece's end warpgroup 0 joins the two.  (A warpgroup's four warps
+  // take every decision together, so that its barriers are always met by all:
+  // a wait that ran out is a vote.)
+  const int x = (warp - 20) >> 2, id = 1 + x;
   const int q4 = warp & 3, key = q4 * 32 + lane;
+  // positions of the rows (each warpgroup has its own copy), the running
+  // maxima (log2 domain), the factors of their last move, four warps' values
+  constexpr int kState = 7 * NR;
+  int32_t* row_pos = reinterpret_cast<int32_t*>(smem + L::kOffRow) + x * kState;
+  float* row_m = reinterpret_cast<float*>(row_pos + NR);
+  float* row_a = row_m + NR;
+  int32_t* row_w = reinterpret_cast<int32_t*>(row_a + NR);
   const uint32_t lanes = static_cast<uint32_t>(q4 * 32) << 16;
-  const uint32_t o_addr = tmem + lanes + 2 * NR;
-  const uint32_t p_row = smem_u32(smem + L::kOffP) + key * 128;
+  const uint32_t s_addr = tmem + lanes + x * NR;
+  const uint32_t o_addr = tmem + lanes + 2 * NR + x * NR;
+  const uint32_t p_row = smem_u32(smem + L::kOffP) + key * 128 + (NR > 32 ? x * L::kPStep : 0);
+  constexpr int kPChunk = NR <= 32 ? L::kPStep / 16 : 0;   // 16-byte chunks to state 1's columns
   const float sl2 = p.scale_log2;
-  // P.V of tile k is complete (one barrier for even tiles, one for odd: a
-  // single one could be two phases ahead of a wait)
-  auto product_done = [&](uint32_t k) -> bool { return wait_all(B_PDONE0 + (k & 1), k >> 1); };
-  uint32_t jj = 0;
+  uint32_t cnt = 0, piece = 0;                             // this state's tiles; pieces
   bool ok = true, stop = false;
   do {
-    // the piece's rows: positions (a row past the segment's end as the last one), no maximum yet
+    // the piece's rows: positions (a row past the segment's end as the last
+    // one), no maximum yet -- once warpgroup 0 has read the previous piece's
+    if (x == 1 && piece > 0) ok = wait_all(B_OFREE, piece - 1) && ok;
     if (key < NR) {
       const int R = w.rt * NR + key;
       row_pos[key] = key < w.t.rows ? w.s.len - w.s.n + R / p.rep : w.t.pos_hi;
       row_m[key] = -INFINITY;
     }
-    group_sync();
+    if (group_or(!ok, id)) break;
     float l[NR];
 #pragma unroll
     for (int i = 0; i < NR; ++i) l[i] = 0.0f;
-    const bool four = p.bits[w.kvh] == 4;
-    for (int j = 0; j < w.n; ++j, ++jj) {
+    const int n = w.n;
+    for (int j = x; j < n; j += 2, ++cnt) {
       const int t0 = w.t.tile(w.i + j) * kT, tok = t0 + key;
       // some row of the block does not see some key of the tile
       const bool masked = t0 + kT - 1 > w.t.pos_lo ||
                           (p.window > 0 && t0 < w.t.pos_hi - p.window + 1 && t0 + kT > p.sinks);
-      const bool always = tok < p.sinks || p.window == 0;          // no window for this key
-      ok = wait_all(B_SFULL0 + (jj & 1), jj >> 1) && ok;
+      const bool always = tok < p.sinks || p.window == 0;  // no window for this key
+      ok = wait_all(B_SFULL0 + x, cnt) && ok;
       tc::fence_after_sync();
-      const uint32_t s_addr = tmem + lanes + (jj & 1) * NR;
       float s[NR];
 #pragma unroll
       for (int c0 = 0; c0 < NR; c0 += CH) {
@@ -504,8 +572,8 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_narrow_kernel(const __grid_
         move |= s[i] > m4.x + kRescaleThreshold || s[i + 1] > m4.y + kRescaleThreshold ||
                 s[i + 2] > m4.z + kRescaleThreshold || s[i + 3] > m4.w + kRescaleThreshold;
       }
-      if (group_or(move)) {
-        if (group_or(!ok)) {
+      if (group_or(move, id)) {
+        if (group_or(!ok, id)) {
           stop = true;
           break;
         }
@@ -515,7 +583,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_narrow_kernel(const __grid_
           const int mx = __reduce_max_sync(0xffffffffu, to_ordered(s[i]));
           if (lane == (i & 31)) row_w[q4 * NR + i] = mx;
         }
-        group_sync();
+        group_sync(id);
         if (key < NR) {
           const float M = fmaxf(fmaxf(from_ordered(row_w[key]), from_ordered(row_w[NR + key])),
                                 fmaxf(from_ordered(row_w[2 * NR + key]), from_ordered(row_w[3 * NR + key])));
@@ -524,27 +592,28 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_narrow_kernel(const __grid_
           row_a[key] = mo == -INFINITY ? 1.0f : fast_exp2(mo - mn);
           row_m[key] = mn;
         }
-        group_sync();
+        group_sync(id);
 #pragma unroll
-        for (int i = 0; i < NR; ++i) l[i] *= row_a[i];
-        if (j > 0) {
-          ok = product_done(jj - 1) && ok;
+        for (int i = 0; i < NR; i += 4) {
+          const float4 a4 = *reinterpret_cast<const float4*>(row_a + i);
+          l[i] *= a4.x; l[i + 1] *= a4.y; l[i + 2] *= a4.z; l[i + 3] *= a4.w;
+        }
+        if (j > x) {
+          ok = wait_all(B_PDONE0 + x, cnt - 1) && ok;
           tc::fence_after_sync();
 #pragma unroll
-          for (int c0 = 0; c0 < NR; c0 += CH) {
-            uint32_t v[CH];
-            if constexpr (CH == 16) tc::ld_32x32b_x16(o_addr + c0, v);
-            else tc::ld_32x32b_x32(o_addr + c0, v);
+          for (int c0 = 0; c0 < NR; c0 += 16) {
+            uint32_t v[16];
+            tc::ld_32x32b_x16(o_addr + c0, v);
             tc::wait_ld(v);
 #pragma unroll
-            for (int i = 0; i < CH; ++i) v[i] = __float_as_uint(__uint_as_float(v[i]) * row_a[c0 + i]);
-            if constexpr (CH == 16) tc::st_32x32b_x16(o_addr + c0, v);
-            else tc::st_32x32b_x32(o_addr + c0, v);
+            for (int i = 0; i < 16; ++i) v[i] = __float_as_uint(__uint_as_float(v[i]) * row_a[c0 + i]);
+            tc::st_32x32b_x16(o_addr + c0, v);
           }
           tc::wait_st();
         }
       }
-      // P^T = 2^(S - m): this key's row of the operand tile, once the product that used the buffer has read it
+      // P^T = 2^(S - m): this key's row of the operand tile, once the state's previous product has read it
       uint32_t pk[NR / 2];
 #pragma unroll
       for (int i = 0; i < NR; i += 4) {
@@ -560,79 +629,111 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_narrow_kernel(const __grid_
         pk[i / 2] = pack_half2(e[0], e[1]);
         pk[i / 2 + 1] = pack_half2(e[2], e[3]);
       }
-      if (jj >= L::kPBufs) ok = product_done(jj - L::kPBufs) && ok;
+      if (cnt > 0) ok = wait_all(B_PDONE0 + x, cnt - 1) && ok;
 #pragma unroll
       for (int i = 0; i < NR / 8; ++i)
-        sts128(p_row + (((i + (jj % L::kPBufs) * 4) ^ (key & 7)) << 4), pk[4 * i], pk[4 * i + 1], pk[4 * i + 2], pk[4 * i + 3]);
+        sts128(p_row + (((i + x * kPChunk) ^ (key & 7)) << 4), pk[4 * i], pk[4 * i + 1], pk[4 * i + 2], pk[4 * i + 3]);
       fence_proxy_async_smem();
       tc::fence_before_sync();
       __syncwarp();
-      if (lane == 0) mbar_arrive(&bar[B_PFULL0 + (jj & 1)]);
+      if (lane == 0) mbar_arrive(&bar[B_PFULL0 + x]);
     }
     if (stop) break;
-    // ---- end of the piece: sums over the keys, then O^T / sum ----
-    ok = product_done(jj - 1) && ok;
-    if (group_or(!ok)) break;
+    // ---- end of the piece: sums over the keys; the two states joined; O^T / sum ----
+    if (n > x) ok = wait_all(B_PDONE0 + x, cnt - 1) && ok;
+    if (group_or(!ok, id)) break;
     tc::fence_after_sync();
-#pragma unroll
-    for (int i = 0; i < NR; ++i) {
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) l[i] += __shfl_xor_sync(0xffffffffu, l[i], o);
-      if (lane == (i & 31)) row_w[q4 * NR + i] = __float_as_int(l[i]);
+    sum_rows<NR>(l, lane, row_w + q4 * NR);
+    if (x == 1) {   // maxima and sums are in shared memory, O^T in TMEM: warpgroup 0's from here
+      tc::fence_before_sync();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bar[B_STATE]);
+      ++piece;
+      continue;
     }
-    group_sync();
+    ok = wait_all(B_STATE, piece) && ok;
+    if (group_or(!ok, id)) break;
+    tc::fence_after_sync();
     const int rows = w.t.rows;
-    const bool whole = w.n == w.t.n;
+    const bool whole = n == w.t.n, four = p.bits[w.kvh] == 4;
     const Cut cut(w);
     const int part = cut.partial(blockIdx.x);
+    // a row's factors of the two O^T, each in its state's row_a
     if (key < NR) {
-      const float sum = (__int_as_float(row_w[key]) + __int_as_float(row_w[NR + key])) +
-                        (__int_as_float(row_w[2 * NR + key]) + __int_as_float(row_w[3 * NR + key]));
-      row_a[key] = sum > 0.0f ? 1.0f / sum : 0.0f;
+      float sum0 = 0.0f, sum1 = 0.0f;
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        sum0 += __int_as_float(row_w[q * NR + key]);
+        sum1 += __int_as_float(row_w[kState + q * NR + key]);
+      }
+      const float m0 = row_m[key], m1 = row_m[kState + key], M = fmaxf(m0, m1);
+      const float f0 = m0 == -INFINITY ? 0.0f : fast_exp2(m0 - M);
+      const float f1 = m1 == -INFINITY ? 0.0f : fast_exp2(m1 - M);
+      const float sum = f0 * sum0 + f1 * sum1, inv = sum > 0.0f ? 1.0f / sum : 0.0f;
+      row_a[key] = f0 * inv;
+      row_a[kState + key] = f1 * inv;
       if (!whole && key < rows)
-        p.ws_lse[static_cast<int64_t>(part) * p.slot_rows + key] = sum > 0.0f ? row_m[key] + __log2f(sum) : -INFINITY;
+        p.ws_lse[static_cast<int64_t>(part) * p.slot_rows + key] = sum > 0.0f ? M + __log2f(sum) : -INFINITY;
     }
-    group_sync();
+    group_sync(id);
+    // The rows' outputs to shared memory ([row][channel] over the P buffers,
+    // which no product reads any more), then to global memory in a rolled loop:
+    // a piece's end runs once, and straight-line code for every row took 2.6 us
+    // of it to fetch.
+    float* stage = reinterpret_cast<float*>(smem + L::kOffP);
     {
       // operand column `key` holds this channel (4-bit heads: order 0,4,1,5,2,6,3,7 within eight)
       const int ch = four ? (key & ~7) | ((key & 1) << 2) | ((key & 7) >> 1) : key;
+#pragma unroll 1
+      for (int c0 = 0; c0 < rows; c0 += 16) {
+        uint32_t v0[16], v1[16];
+        tc::ld_32x32b_x16(o_addr + c0, v0);
+        if (n > 1) tc::ld_32x32b_x16(o_addr + NR + c0, v1);   // (a piece of one tile has no second state)
+        tc::wait_ld(v0);
+        if (n > 1) tc::wait_ld(v1);
+        if (key < D) {
 #pragma unroll
-      for (int c0 = 0; c0 < NR; c0 += CH) {
-        uint32_t v[CH];
-        if constexpr (CH == 16) tc::ld_32x32b_x16(o_addr + c0, v);
-        else tc::ld_32x32b_x32(o_addr + c0, v);
-        tc::wait_ld(v);
-        if (key >= D) continue;
-#pragma unroll
-        for (int i = 0; i < CH; ++i) {
-          const int r = c0 + i;
-          if (r >= rows) continue;
-          const float o = __uint_as_float(v[i]) * row_a[r];
-          if (whole) {
-            const int64_t off = out_offset(p, w, w.rt * NR + r, D) + ch;
-            if (!KVQ_IN_RANGE(off >= 0 && off < static_cast<int64_t>(p.c.rows) * p.Hq * D, p.status)) continue;
-            if (p.out_dtype == KVQ_OUT_F32) static_cast<float*>(p.out)[off] = o;
-            else static_cast<__nv_bfloat16*>(p.out)[off] = __float2bfloat16_rn(o);
-          } else {
-            p.ws_o[(static_cast<int64_t>(part) * p.slot_rows + r) * D + ch] = o;
+          for (int i = 0; i < 16; ++i) {
+            float o = __uint_as_float(v0[i]) * row_a[c0 + i];
+            if (n > 1) o = fmaf(__uint_as_float(v1[i]), row_a[kState + c0 + i], o);
+            stage[(c0 + i) * D + ch] = o;
           }
         }
       }
     }
+    group_sync(id);
+#pragma unroll 1
+    for (int i = key; i < rows * (D / 4); i += 128) {
+      const int r = i / (D / 4), c = i % (D / 4) * 4;
+      const float4 o = reinterpret_cast<const float4*>(stage)[i];
+      if (!whole) {
+        *reinterpret_cast<float4*>(p.ws_o + (static_cast<int64_t>(part) * p.slot_rows + r) * D + c) = o;
+        continue;
+      }
+      const int64_t off = out_offset(p, w, w.rt * NR + r, D) + c;
+      if (!KVQ_IN_RANGE(off >= 0 && off + 4 <= static_cast<int64_t>(p.c.rows) * p.Hq * D, p.status)) continue;
+      if (p.out_dtype == KVQ_OUT_F32) {
+        *reinterpret_cast<float4*>(static_cast<float*>(p.out) + off) = o;
+      } else {
+        const __nv_bfloat162 a = __floats2bfloat162_rn(o.x, o.y), b = __floats2bfloat162_rn(o.z, o.w);
+        *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.out) + off) =
+            make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
+      }
+    }
     tc::fence_before_sync();
-    __syncwarp();
+    group_sync(id);   // the rows' values have been read; every partial is stored
     if (lane == 0) mbar_arrive(&bar[B_OFREE]);
-    group_sync();   // the rows' values have been read; every partial is stored
     if (!whole) {
       // one acquire-release atomic after the group's barrier, and a vote that
       // hands its outcome (and what it acquired) to the group
       bool last = false;
       if (key == 0) last = atom_add_acq_rel_gpu(p.cnt + 2 * cut.c0, 1) + 1 == cut.c1 - cut.c0 + 1;
-      if (group_or(last)) {
+      if (group_or(last, id)) {
         for (int r = q4; r < rows; r += 4) merge_row<D>(p, w, cut, NR, r, lane);
         if (key == 0) p.cnt[2 * cut.c0] = 0;   // ready for the next call
       }
     }
+    ++piece;
   } while (next_piece<NR>(p, w, lane));
   tc::wait_st();
   tc::fence_before_sync();
@@ -641,7 +742,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_narrow_kernel(const __grid_
 }
 
 // Per device and instantiation, set once under a lock: the kernel's dynamic
-// shared-memory limit.
+// shared-memory limit, and its registers checked.
 std::mutex g_prep_mu;
 bool g_prep[64][6] = {};
 
@@ -653,10 +754,16 @@ kvq_status launch_n(const CParams& p, cudaStream_t stream) {
   {
     std::lock_guard<std::mutex> lock(g_prep_mu);
     bool& ready = g_prep[dev][(D == 128 ? 3 : 0) + (NR == 16 ? 0 : NR == 32 ? 1 : 2)];
-    if (!ready && cudaFuncSetAttribute(chunk_narrow_kernel<D, NR>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       static_cast<int>(L::bytes(kMaxB))) != cudaSuccess)
-      return KVQ_ERR_CUDA;
-    ready = true;
+    if (!ready) {
+      // the register split inside the kernel assumes 72 per thread at launch
+      cudaFuncAttributes fa;
+      if (cudaFuncGetAttributes(&fa, chunk_narrow_kernel<D, NR>) != cudaSuccess) return KVQ_ERR_CUDA;
+      if (fa.numRegs != 72) return KVQ_ERR_UNSUPPORTED;
+      if (cudaFuncSetAttribute(chunk_narrow_kernel<D, NR>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                               static_cast<int>(L::bytes(kMaxB))) != cudaSuccess)
+        return KVQ_ERR_CUDA;
+      ready = true;
+    }
   }
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(p.num_ctas));

@@ -160,33 +160,48 @@ __device__ __forceinline__ void sum_tiles(const CParams& p, int32_t* pre, int la
   if (lane == 0) pre[0] = 0;
 }
 
+// a b / c for a, b, c >= 0: in 32 bits when the product fits (a 64-bit division
+// is a long software sequence, and a CTA's start and every piece's end wait
+// for a few of them).
+__device__ __forceinline__ int64_t mul_div(int64_t a, int64_t b, int64_t c) {
+  const int64_t ab = a * b;
+  if (((ab | c) >> 32) == 0) return static_cast<uint32_t>(ab) / static_cast<uint32_t>(c);
+  return ab / c;
+}
+
 // Opens the first piece of this CTA's range [N c / C, N (c + 1) / C) of the N
-// tiles (the whole warp; never more CTAs than tiles in the split); returns the
-// range's length, 0 for a CTA outside the split.
+// tiles (one warp; never more CTAs than tiles in the split).  w.left is the
+// range's length, 0 for a CTA outside the split.  The other warps copy w
+// (copy_walk): computed by all of them it took 1.8 us of a CTA's start.
 template <int ROWS>
-__device__ __forceinline__ int64_t start_walk(const CParams& p, const int32_t* pre, Walk& w, int lane) {
+__device__ __forceinline__ void start_walk(const CParams& p, const int32_t* pre, Walk& w, int lane) {
   const int64_t N = static_cast<int64_t>(p.Hkv) * pre[p.c.B];
   const int C = N < p.num_ctas ? static_cast<int>(N) : p.num_ctas;
-  if (static_cast<int>(blockIdx.x) >= C) return 0;
-  const int64_t f0 = N * blockIdx.x / C, total = N * (blockIdx.x + 1) / C - f0;
+  if (static_cast<int>(blockIdx.x) >= C) {
+    if (lane == 0) w.left = 0;
+    __syncwarp();
+    return;
+  }
+  const int64_t f0 = mul_div(N, blockIdx.x, C), total = mul_div(N, blockIdx.x + 1, C) - f0;
   int lo = 0, hi = p.c.B - 1;   // the last b with Hkv * pre[b] <= f0: a sequence with tiles
   while (lo < hi) {
     const int mid = (lo + hi + 1) >> 1;
     if (static_cast<int64_t>(p.Hkv) * pre[mid] <= f0) lo = mid; else hi = mid - 1;
   }
   const chunk::Seq s = chunk::sequence(p.c, lo);
-  const int64_t per = pre[lo + 1] - pre[lo], off = f0 - static_cast<int64_t>(p.Hkv) * pre[lo];
-  const int kvh = static_cast<int>(off / per);
-  int64_t rem = off - kvh * per;
+  const int per = pre[lo + 1] - pre[lo];
+  const int64_t off = f0 - static_cast<int64_t>(p.Hkv) * pre[lo];
+  const int kvh = static_cast<int>(mul_div(off, 1, per));
+  int rem = static_cast<int>(off - static_cast<int64_t>(kvh) * per);
   // the row block: prefix sums over 32 blocks at a time
   const int nrt = row_blocks<ROWS>(p, s);
   int rt = 0;
-  for (int r0 = 0; r0 < nrt; r0 += 32) {
-    const int64_t mine = r0 + lane < nrt ? segment_tiles<ROWS>(p, s, r0 + lane).n : 0;
-    int64_t incl = mine;
+  for (int r0 = 0; nrt > 1 && r0 < nrt; r0 += 32) {
+    const int mine = r0 + lane < nrt ? segment_tiles<ROWS>(p, s, r0 + lane).n : 0;
+    int incl = mine;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-      const int64_t v = __shfl_up_sync(0xffffffffu, incl, o);
+      const int v = __shfl_up_sync(0xffffffffu, incl, o);
       if (lane >= o) incl += v;
     }
     const unsigned past = __ballot_sync(0xffffffffu, r0 + lane < nrt && incl > rem);
@@ -206,12 +221,18 @@ __device__ __forceinline__ int64_t start_walk(const CParams& p, const int32_t* p
     w.b = lo;
     w.kvh = kvh;
     w.rt = rt;
-    w.i = static_cast<int>(rem);
+    w.i = rem;
     w.s = s;
     open_piece<ROWS>(p, w);
   }
   __syncwarp();
-  return total;
+}
+
+__device__ __forceinline__ void copy_walk(Walk& to, const Walk& from, int lane) {
+  static_assert(sizeof(Walk) % 4 == 0 && sizeof(Walk) <= 128, "a word per lane");
+  if (lane < static_cast<int>(sizeof(Walk) / 4))
+    reinterpret_cast<uint32_t*>(&to)[lane] = reinterpret_cast<const uint32_t*>(&from)[lane];
+  __syncwarp();
 }
 
 // A cut segment: CTAs c0 .. c1 hold it.  A CTA's piece of it is partial 0 of
@@ -219,11 +240,16 @@ __device__ __forceinline__ int64_t start_walk(const CParams& p, const int32_t* p
 // else 1.
 struct Cut {
   int c0, c1, slot0;
+  __device__ __forceinline__ static int owner(const Walk& w, int64_t f) {
+    const int64_t x = f * w.C + w.C - 1;
+    return static_cast<int>(mul_div(x, 1, w.N));
+  }
   __device__ __forceinline__ explicit Cut(const Walk& w) {
     const int64_t seg0 = w.f - w.i;
-    c0 = static_cast<int>(((seg0 + 1) * w.C - 1) / w.N);
-    c1 = static_cast<int>(((seg0 + w.t.n) * w.C - 1) / w.N);
-    slot0 = seg0 <= w.N * c0 / w.C ? 0 : 1;
+    // the CTA of tile f: floor(((f + 1) C - 1) / N) = floor((f C + C - 1) / N)
+    c0 = owner(w, seg0);
+    c1 = owner(w, seg0 + w.t.n - 1);
+    slot0 = seg0 <= mul_div(w.N, c0, w.C) ? 0 : 1;
   }
   __device__ __forceinline__ int partial(int c) const { return 2 * c + (c == c0 ? slot0 : 0); }
 };
@@ -234,13 +260,15 @@ struct Cut {
 // by the threads that wrote the rows, after they did: a test on the registers
 // themselves cost 15 % of the 256-row kernel, because a branch there waits for
 // every load in flight.
+// (iterations it0, it0 + step, .. below it1 of the part)
 template <int D, int BITS>
-__device__ __forceinline__ void clear_unseen(uint32_t dst, const CParams& p, const Walk& w, int t0, int row, int c) {
+__device__ __forceinline__ void clear_unseen(uint32_t dst, const CParams& p, const Walk& w, int t0, int row, int c,
+                                             int it0 = 0, int it1 = tile::DqFmt<D, BITS>::NI, int step = 1) {
   using F = tile::DqFmt<D, BITS>;
   const Seen s(p, w);
   if (t0 + kT <= s.end && (t0 >= s.lo || t0 + kT <= p.sinks)) return;   // the whole tile is seen by someone
 #pragma unroll 1
-  for (int it = 0; it < F::NI; ++it) {
+  for (int it = it0; it < it1; it += step) {
     const int r = F::RPI * it + row, j = t0 + r;
     if (j < s.end && (j >= s.lo || j < p.sinks)) continue;
     const int ch0 = c * F::VPC;
