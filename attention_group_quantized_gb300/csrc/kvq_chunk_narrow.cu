@@ -187,62 +187,80 @@ __device__ __forceinline__ bool dequant_piece(const CParams& p, uint8_t* smem, u
   return true;
 }
 
-// One row of a cut segment: its pieces merged by log-sum-exp in CTA order, by
-// one warp, a lane per D / 32 channels.
+// Four channels of an output row to global memory.
 template <int D>
-__device__ __forceinline__ void merge_row(const CParams& p, const Walk& w, const Cut& cut, int rows_per_block, int r,
-                                          int lane) {
-  constexpr int N = D / 32;
+__device__ __forceinline__ void store_out4(const CParams& p, int64_t off, float4 o) {
+  if (!KVQ_IN_RANGE(off >= 0 && off + 4 <= static_cast<int64_t>(p.c.rows) * p.Hq * D, p.status)) return;
+  if (p.out_dtype == KVQ_OUT_F32) {
+    *reinterpret_cast<float4*>(static_cast<float*>(p.out) + off) = o;
+  } else {
+    const __nv_bfloat162 a = __floats2bfloat162_rn(o.x, o.y), b = __floats2bfloat162_rn(o.z, o.w);
+    *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.out) + off) =
+        make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
+  }
+}
+
+// The rows of a cut segment merged by log-sum-exp over its pieces, in CTA
+// order: a thread takes four channels of a row, two such at a time and four
+// pieces' loads of each in flight (row by row, a warp each, it took 4.7 us).
+template <int D>
+__device__ __forceinline__ void merge_rows(const CParams& p, const Walk& w, const Cut& cut, int rows_per_block, int rows,
+                                           int t) {
+  constexpr int Q = D / 4, U = 2, P = 4;
   const int np = cut.c1 - cut.c0 + 1;
-  auto lse_of = [&](int k) {
-    return k < np ? __ldcg(p.ws_lse + static_cast<int64_t>(cut.partial(cut.c0 + k)) * p.slot_rows + r) : -INFINITY;
-  };
-  float M = -INFINITY;
-  for (int k0 = 0; k0 < np; k0 += 32) M = fmaxf(M, lse_of(k0 + lane));
+#pragma unroll 1
+  for (int i0 = t; i0 < rows * Q; i0 += U * 128) {
+    float M[U], L[U];
+    float4 acc[U];
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-  float acc[N], L = 0.0f;
+    for (int u = 0; u < U; ++u) {
+      M[u] = -INFINITY;
+      L[u] = 0.0f;
+      acc[u] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    }
+#pragma unroll 1
+    for (int k0 = 0; k0 < np; k0 += P) {
+      float lse[U][P];
+      float4 v[U][P];
 #pragma unroll
-  for (int e = 0; e < N; ++e) acc[e] = 0.0f;
-  for (int k0 = 0; k0 < np; k0 += 32) {
-    const float lse = lse_of(k0 + lane);
-    const float mine = lse == -INFINITY ? 0.0f : fast_exp2(lse - M);
-    const int cnt = min(32, np - k0);
-    for (int k = 0; k < cnt; k += 4) {
-      float v[4][N];
+      for (int k = 0; k < P; ++k) {
+        const int64_t part = static_cast<int64_t>(cut.partial(cut.c0 + min(k0 + k, np - 1))) * p.slot_rows;
 #pragma unroll
-      for (int u = 0; u < 4; ++u) {
-        const int c = cut.c0 + k0 + min(k + u, cnt - 1);
-        const float* src = p.ws_o + (static_cast<int64_t>(cut.partial(c)) * p.slot_rows + r) * D + lane * N;
-        if constexpr (N == 4) {
-          const float4 x = __ldcg(reinterpret_cast<const float4*>(src));
-          v[u][0] = x.x; v[u][1] = x.y; v[u][2] = x.z; v[u][3] = x.w;
-        } else {
-          const float2 x = __ldcg(reinterpret_cast<const float2*>(src));
-          v[u][0] = x.x; v[u][1] = x.y;
+        for (int u = 0; u < U; ++u) {
+          const int i = min(i0 + u * 128, rows * Q - 1), r = i / Q;
+          lse[u][k] = k0 + k < np ? __ldcg(p.ws_lse + part + r) : -INFINITY;
+          v[u][k] = __ldcg(reinterpret_cast<const float4*>(p.ws_o + (part + r) * D) + i % Q);
         }
       }
 #pragma unroll
-      for (int u = 0; u < 4; ++u) {
-        const float b = k + u < cnt ? __shfl_sync(0xffffffffu, mine, min(k + u, 31)) : 0.0f;
-        L += b;
+      for (int u = 0; u < U; ++u) {
+        float m = M[u];
 #pragma unroll
-        for (int e = 0; e < N; ++e) acc[e] = fmaf(b, v[u][e], acc[e]);
+        for (int k = 0; k < P; ++k) m = fmaxf(m, lse[u][k]);
+        if (m == -INFINITY) continue;   // no piece with weight yet
+        const float a = fast_exp2(M[u] - m);
+        acc[u].x *= a; acc[u].y *= a; acc[u].z *= a; acc[u].w *= a;
+        L[u] *= a;
+#pragma unroll
+        for (int k = 0; k < P; ++k) {
+          const float b = fast_exp2(lse[u][k] - m);
+          acc[u].x = fmaf(b, v[u][k].x, acc[u].x);
+          acc[u].y = fmaf(b, v[u][k].y, acc[u].y);
+          acc[u].z = fmaf(b, v[u][k].z, acc[u].z);
+          acc[u].w = fmaf(b, v[u][k].w, acc[u].w);
+          L[u] += b;
+        }
+        M[u] = m;
       }
     }
-  }
-  const float inv = L > 0.0f ? 1.0f / L : 0.0f;
-  const int64_t off = out_offset(p, w, w.rt * rows_per_block + r, D) + lane * N;
-  if (!KVQ_IN_RANGE(off >= 0 && off + N <= static_cast<int64_t>(p.c.rows) * p.Hq * D, p.status)) return;
-  if (p.out_dtype == KVQ_OUT_F32) {
-    float* dst = static_cast<float*>(p.out) + off;
-    if constexpr (N == 4)
-      *reinterpret_cast<float4*>(dst) = make_float4(acc[0] * inv, acc[1] * inv, acc[2] * inv, acc[3] * inv);
-    else *reinterpret_cast<float2*>(dst) = make_float2(acc[0] * inv, acc[1] * inv);
-  } else {
-    __nv_bfloat162* dst = reinterpret_cast<__nv_bfloat162*>(static_cast<__nv_bfloat16*>(p.out) + off);
 #pragma unroll
-    for (int e = 0; e < N; e += 2) dst[e / 2] = __floats2bfloat162_rn(acc[e] * inv, acc[e + 1] * inv);
+    for (int u = 0; u < U; ++u) {
+      const int i = i0 + u * 128;
+      if (i >= rows * Q) break;
+      const float inv = L[u] > 0.0f ? 1.0f / L[u] : 0.0f;
+      store_out4<D>(p, out_offset(p, w, w.rt * rows_per_block + i / Q, D) + i % Q * 4,
+                    make_float4(acc[u].x * inv, acc[u].y * inv, acc[u].z * inv, acc[u].w * inv));
+    }
   }
 }
 
@@ -710,15 +728,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_narrow_kernel(const __grid_
         *reinterpret_cast<float4*>(p.ws_o + (static_cast<int64_t>(part) * p.slot_rows + r) * D + c) = o;
         continue;
       }
-      const int64_t off = out_offset(p, w, w.rt * NR + r, D) + c;
-      if (!KVQ_IN_RANGE(off >= 0 && off + 4 <= static_cast<int64_t>(p.c.rows) * p.Hq * D, p.status)) continue;
-      if (p.out_dtype == KVQ_OUT_F32) {
-        *reinterpret_cast<float4*>(static_cast<float*>(p.out) + off) = o;
-      } else {
-        const __nv_bfloat162 a = __floats2bfloat162_rn(o.x, o.y), b = __floats2bfloat162_rn(o.z, o.w);
-        *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.out) + off) =
-            make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
-      }
+      store_out4<D>(p, out_offset(p, w, w.rt * NR + r, D) + c, o);
     }
     tc::fence_before_sync();
     group_sync(id);   // the rows' values have been read; every partial is stored
@@ -729,7 +739,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_narrow_kernel(const __grid_
       bool last = false;
       if (key == 0) last = atom_add_acq_rel_gpu(p.cnt + 2 * cut.c0, 1) + 1 == cut.c1 - cut.c0 + 1;
       if (group_or(last, id)) {
-        for (int r = q4; r < rows; r += 4) merge_row<D>(p, w, cut, NR, r, lane);
+        merge_rows<D>(p, w, cut, NR, rows, key);
         if (key == 0) p.cnt[2 * cut.c0] = 0;   // ready for the next call
       }
     }
