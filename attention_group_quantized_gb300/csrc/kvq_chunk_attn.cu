@@ -240,16 +240,25 @@ __device__ __forceinline__ float4* partial_o(const CParams& p, int k, int r) {
   return reinterpret_cast<float4*>(p.ws_o) + static_cast<int64_t>(k) * (D / 4) * p.slot_rows + r;
 }
 
-// This row's pieces in CTAs c0 .. c1 merged by log-sum-exp in CTA order; the
-// normalised row goes to offset orow of the output.
+// This row's pieces merged by log-sum-exp in CTA order; the normalised row
+// goes to offset orow of the output.  Two pieces' loads are in flight together
+// (one at a time took 9.9 us a merge).
 template <int D>
 __device__ __forceinline__ void merge_row(const CParams& p, const Cut& cut, int r, int64_t orow) {
+  auto lse_of = [&](int c) {
+    return c <= cut.c1 ? __ldcg(p.ws_lse + static_cast<int64_t>(cut.partial(c)) * p.slot_rows + r) : -INFINITY;
+  };
   float M = -INFINITY, L = 0.0f;
-  for (int c = cut.c0; c <= cut.c1; ++c) {
-    const float lse = __ldcg(p.ws_lse + static_cast<int64_t>(cut.partial(c)) * p.slot_rows + r);
-    const float mn = fmaxf(M, lse);
+#pragma unroll 1
+  for (int c = cut.c0; c <= cut.c1; c += 4) {
+    float lse[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) lse[k] = lse_of(c + k);
+    const float mn = fmaxf(M, fmaxf(fmaxf(lse[0], lse[1]), fmaxf(lse[2], lse[3])));
     if (mn == -INFINITY) continue;   // no piece with weight yet
-    L = L * fast_exp2(M - mn) + fast_exp2(lse - mn);
+    L *= fast_exp2(M - mn);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) L += fast_exp2(lse[k] - mn);
     M = mn;
   }
   const float inv = L > 0.0f ? 1.0f / L : 0.0f;
@@ -258,19 +267,25 @@ __device__ __forceinline__ void merge_row(const CParams& p, const Cut& cut, int 
     float o[32];
 #pragma unroll
     for (int i = 0; i < 32; ++i) o[i] = 0.0f;
-    for (int c = cut.c0; c <= cut.c1; ++c) {
-      const float lse = __ldcg(p.ws_lse + static_cast<int64_t>(cut.partial(c)) * p.slot_rows + r);
-      const float4* src = partial_o<D>(p, cut.partial(c), r) + static_cast<int64_t>(i0) * p.slot_rows;
-      float4 v[8];
+#pragma unroll 1
+    for (int c = cut.c0; c <= cut.c1; c += 2) {
+      const float la = lse_of(c), lb = lse_of(c + 1);
+      const int64_t at = static_cast<int64_t>(i0) * p.slot_rows;
+      const float4* sa = partial_o<D>(p, cut.partial(c), r) + at;
+      const float4* sb = partial_o<D>(p, cut.partial(min(c + 1, cut.c1)), r) + at;
+      float4 va[8], vb[8];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) v[i] = __ldcg(src + static_cast<int64_t>(i) * p.slot_rows);
-      const float b = lse == -INFINITY ? 0.0f : fast_exp2(lse - M) * inv;
+      for (int i = 0; i < 8; ++i) va[i] = __ldcg(sa + i * p.slot_rows);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) vb[i] = __ldcg(sb + i * p.slot_rows);
+      const float wa = la == -INFINITY ? 0.0f : fast_exp2(la - M) * inv;
+      const float wb = lb == -INFINITY ? 0.0f : fast_exp2(lb - M) * inv;
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        o[4 * i] = fmaf(b, v[i].x, o[4 * i]);
-        o[4 * i + 1] = fmaf(b, v[i].y, o[4 * i + 1]);
-        o[4 * i + 2] = fmaf(b, v[i].z, o[4 * i + 2]);
-        o[4 * i + 3] = fmaf(b, v[i].w, o[4 * i + 3]);
+        o[4 * i] = fmaf(wb, vb[i].x, fmaf(wa, va[i].x, o[4 * i]));
+        o[4 * i + 1] = fmaf(wb, vb[i].y, fmaf(wa, va[i].y, o[4 * i + 1]));
+        o[4 * i + 2] = fmaf(wb, vb[i].z, fmaf(wa, va[i].z, o[4 * i + 2]));
+        o[4 * i + 3] = fmaf(wb, vb[i].w, fmaf(wa, va[i].w, o[4 * i + 3]));
       }
     }
     store_row32(p, D, orow + 4 * i0, o);
@@ -293,7 +308,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_attention_kernel(const __gr
 
   if (threadIdx.x == 0) {
     mbar_init(&bar[B_QREADY], 4);
-    mbar_init(&bar[B_QEMPTY], 2);
+    mbar_init(&bar[B_QEMPTY], 3);   // both issuers, and warp 3
     for (int s = 0; s < 2; ++s) {
       mbar_init(&bar[B_KFULL0 + s], 4);
       mbar_init(&bar[B_VFULL0 + s], 4);
@@ -362,15 +377,22 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_attention_kernel(const __gr
     }
     if (warp == 3) {
       // ---------------- the next piece's queries into L2 ----------------
-      bool ok = true;
-      for (uint32_t piece = 0; ok && next_piece<kRows>(p, w, lane); ++piece) {
-        for (int r = lane; r < w.t.rows; r += 32) {
+      // One piece ahead of the dequant warps: this warp waits for each piece's
+      // queries to be in shared memory and counts among those that free them,
+      // so it meets every phase of that barrier in order (a waiter that the
+      // others do not wait for can miss two phases and take a later one for its own).
+      bool ok = true, more;
+      uint32_t piece = 0;
+      do {
+        more = next_piece<kRows>(p, w, lane);
+        for (int r = lane; more && r < w.t.rows; r += 32) {
           const int R = w.rt * kRows + r, tok = R / p.rep, hh = R - tok * p.rep;
           prefetch_l2_bulk(p.q + (w.s.row0 + tok) * p.sq_row + (w.kvh * p.rep + hh) * p.sq_head, D * 2);
         }
-        // (one piece ahead, no further)
         ok = __all_sync(0xffffffffu, mbar_wait(&bar[B_QREADY], piece & 1, p.status, kWaitNs));
-      }
+        if (ok && lane == 0) mbar_arrive(&bar[B_QEMPTY]);
+        ++piece;
+      } while (ok && more);
       if (lane == 0) mbar_arrive(&bar[B_EXIT]);
       return;
     }

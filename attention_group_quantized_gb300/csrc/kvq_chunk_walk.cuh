@@ -289,32 +289,36 @@ __device__ __forceinline__ bool load_queries(const CParams& p, uint32_t dst, uin
   constexpr int NB = TILE / RPP < 8 ? TILE / RPP : 8;   // passes in flight
   const int ch = t % CPR;
   const bool four = p.bits[w.kvh] == 4;
-  const uint16_t* base = p.q + w.kvh * p.rep * p.sq_head + ch * 8;
-  bool finite = true;
-  const int end = (w.t.rows + TILE - 1) / TILE * TILE;
+  const uint16_t* base = p.q + static_cast<int64_t>(w.s.row0) * p.sq_row + w.kvh * p.rep * p.sq_head + ch * 8;
+  const int end = (w.t.rows + TILE - 1) / TILE * TILE, rows = w.t.rows;
+  // token and head of this thread's row, stepped from pass to pass
+  const int R0 = w.rt * ROWS + t / CPR;
+  int tok = R0 / p.rep, hh = R0 - tok * p.rep;
+  const int dtok = RPP / p.rep, dhh = RPP - dtok * p.rep;
+  uint32_t big = 0;                       // the largest magnitude seen, as two bf16 bit patterns
   for (int r0 = 0; r0 < end; r0 += RPP * NB) {
     uint4 v[NB];
 #pragma unroll
     for (int k = 0; k < NB; ++k) {
       const int r = r0 + k * RPP + t / CPR;
       v[k] = make_uint4(0u, 0u, 0u, 0u);
-      if (r < w.t.rows) {
-        const int R = w.rt * ROWS + r, tok = R / p.rep, hh = R - tok * p.rep;
-        v[k] = *reinterpret_cast<const uint4*>(base + (w.s.row0 + tok) * p.sq_row + hh * p.sq_head);
+      if (r < rows) v[k] = *reinterpret_cast<const uint4*>(base + tok * p.sq_row + hh * p.sq_head);
+      tok += dtok;
+      hh += dhh;
+      if (hh >= p.rep) {
+        hh -= p.rep;
+        ++tok;
       }
     }
-    if (r0 == 0 && wait &&
-        !__all_sync(0xffffffffu, mbar_wait(empty, parity, p.status, kWaitNs)))
-      return false;
+    if (r0 == 0 && wait && !__all_sync(0xffffffffu, mbar_wait(empty, parity, p.status, kWaitNs))) return false;
 #pragma unroll
     for (int k = 0; k < NB; ++k) {
       const int r = r0 + k * RPP + t / CPR;
       uint32_t x[4] = {v[k].x, v[k].y, v[k].z, v[k].w};
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        const float lo = __uint_as_float(x[e] << 16), hi = __uint_as_float(x[e] & 0xFFFF0000u);
-        finite &= fabsf(lo) < 65504.0f && fabsf(hi) < 65504.0f;
-        x[e] = pack_half2(lo, hi);
+        big = __vmaxu2(big, x[e] & 0x7FFF7FFFu);
+        x[e] = pack_half2(__uint_as_float(x[e] << 16), __uint_as_float(x[e] & 0xFFFF0000u));
       }
       if (four) {   // channels 0,4,1,5,2,6,3,7
         const uint32_t a = prmt(x[0], x[2], 0x5410u), b = prmt(x[0], x[2], 0x7632u);
@@ -325,7 +329,8 @@ __device__ __forceinline__ bool load_queries(const CParams& p, uint32_t dst, uin
       tile::sts128(rowp + (((ch & 7) ^ (r & 7)) << 4), x[0], x[1], x[2], x[3]);
     }
   }
-  if (!finite) report(p.status, KVQ_ERR_NONFINITE);
+  // 0x4780 is 65536, the first bf16 beyond fp16's range (infinities and NaN lie above it)
+  if ((big & 0xFFFFu) >= 0x4780u || (big >> 16) >= 0x4780u) report(p.status, KVQ_ERR_NONFINITE);
   return true;
 }
 
