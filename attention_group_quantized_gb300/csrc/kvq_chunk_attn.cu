@@ -840,8 +840,8 @@ kvq_status launch_chunk_attention(const ChunkAttnArgs& a, cudaStream_t stream) {
     p.plane_off[h] = a.layout.plane_off[h];
     p.bits[h] = a.layout.bits[h];
   }
-  // At most 64 rows of a (sequence, KV head): the kernel that puts the keys on
-  // the rows' side (a 128-row query tile would be half empty).
+  // Few rows of a (sequence, KV head): the kernel that puts the keys on the
+  // rows' side (a 128-row query tile would be mostly empty).
   const int64_t max_rows = static_cast<int64_t>(p.c.max_chunk) * p.rep;
   if (chunk_narrow_takes(p.c.B, max_rows)) return launch_chunk_narrow(p, D, max_rows, stream);
   if (p.c.bt != nullptr) return D == 128 ? launch_d<128, true>(p, stream) : launch_d<64, true>(p, stream);

@@ -2,27 +2,35 @@
 // tokens, short chunks, single tokens next to them): the same work as
 // kvq_chunk_attn.cu, with the keys on the tensor cores' row side.
 //
-// With at most 64 packed rows (token * rep + head) a 128-row query tile is
+// With at most 32 packed rows (token * rep + head) a 128-row query tile is
 // mostly empty, and what bounds the call is the cache read.  So a key tile is
 // the M side of both products,
 //   S^T [128 keys x NR rows]      = K [keys x D]      Q^T [D x rows]
 //   O^T [D channels x NR rows]   += V^T [channels x keys] P^T [keys x rows]
-// and the softmax works on NR = 16, 32 or 64 columns: a thread has one key's
+// and the softmax works on NR = 16 or 32 columns: a thread has one key's
 // scores, a row's running max lives in shared memory and moves only when a
 // score exceeds it by more than 2^8 (a vote of the four warps a tile), and the
 // sums are per thread until the piece ends.
 //
 // One CTA (896 threads, one per SM) walks its range of the work list
 // (kvq_chunk_walk.cuh):
-//   warp 0       TMEM, and the issue of V^T P^T; warp 1 issues K Q^T (a warp
-//                each: neither waits for what only the other needs); warps 2 and 3 keep rings of
-//                raw code slots of K and V full by bulk copies (about 50 KB in
-//                flight an SM, which is what the latency of HBM asks for);
-//   warps 4-11   K codes (and the piece's queries) to fp16 operand tiles;
-//                warps 12-19 V codes likewise (two warps a scheduler for each
-//                part: one alone took 1.2 us a tile, most of it latency);
-//   warps 20-27  softmax (two states, of even and of odd tiles), rescaling, the piece's output or partial, the merge.
+//   warps 0, 1   issue V^T P^T and K Q^T (a warp each: neither waits for what
+//                only the other needs); warp 0 also allocates and frees TMEM;
+//   warps 2, 3   keep rings of raw slots (64 tokens: codes and words) of K and
+//                V full by bulk copies, about 50 KB in flight an SM;
+//   warps 4-11   K codes (and the piece's queries) to fp16 operand tiles, warps
+//   12-19        V codes likewise (two warps a scheduler for each part: one
+//                alone took 1.2 us a tile, most of it latency);
+//   warps 20-27  softmax in two states, of even and of odd tiles, each with its
+//                own maxima, sums and O^T, so that one's waits run under the
+//                other's; rescaling, the piece's output or partial, the merge.
 // TMEM: S^T and O^T of each state, NR columns each.
+//
+// Measured: long contexts run at the rate of HBM's reads (eight sequences of
+// 32K, 16 rows: 0.96 us per 36 KB tile an SM, 4.7 TB/s over the call); a call
+// costs 10 us before its first tile and about 9 us for a segment's cut.
+// Fetching the codes into L2 further ahead was slower (54 us against 49 for
+// eight sequences of 8K), and so were slots of 32 tokens (more copies).
 #include <cmath>
 #include <mutex>
 
@@ -38,12 +46,12 @@ using namespace tile;
 using namespace chunk_walk;
 
 constexpr int kThreads = 896;
-constexpr int kMaxRing = 3;            // most raw slots of K, and as many of V
+constexpr int kRing = 3;               // raw slots of K, and as many of V
 
 enum {
   B_QREADY = 0, B_QEMPTY, B_FULL0, B_EMPTY0 = B_FULL0 + 4, B_SFULL0 = B_EMPTY0 + 4, B_PFULL0 = B_SFULL0 + 2,
   B_PDONE0 = B_PFULL0 + 2, B_OFREE = B_PDONE0 + 2, B_STATE, B_MMADONE0, B_EXIT = B_MMADONE0 + 2, B_RAW0,
-  B_RFREE0 = B_RAW0 + 2 * kMaxRing, B_COUNT = B_RFREE0 + 2 * kMaxRing
+  B_RFREE0 = B_RAW0 + 2 * kRing, B_COUNT = B_RFREE0 + 2 * kRing
 };   // FULL and EMPTY: K stages 0, 1, V stages 0, 1; SFULL, PFULL, PDONE: states; RAW and RFREE: K slots, V slots
 // Every warp but warp 0 arrives once on B_EXIT when it is done with shared
 // memory, TMEM and its asynchronous operations; warp 0 frees TMEM after that.
@@ -54,12 +62,10 @@ struct NLayout {
   static constexpr int kTile = kT * D * 2;              // one K or V operand tile
   static constexpr int kOffK = 0;                       // 2 stages
   static constexpr int kOffV = kOffK + 2 * kTile;       // 2 stages; with D = 64 the products read 16 KB past each
-  // P^T of each state: [128 keys][64 rows] fp16, rows of 128 B; up to 32 rows
-  // the two share the lines
+  // P^T of both states: [128 keys][64 rows] fp16, the second state's rows 32 on
   static constexpr int kOffP = kOffV + 2 * kTile;
-  static constexpr int kPStep = NR <= 32 ? 64 : kT * 128;
-  static constexpr int kOffQ = kOffP + (NR <= 32 ? 1 : 2) * kT * 128;   // [D / 64][NR][128 B]
-  static constexpr int kRing = NR <= 32 ? kMaxRing : 2;    // what shared memory has room for
+  static constexpr int kPStep = 64;                     // bytes
+  static constexpr int kOffQ = kOffP + kT * 128;        // [D / 64][NR][128 B]
   // raw slots: kST tokens' codes (8-bit heads fill the room), then their words
   static constexpr int kST = 64;
   static constexpr int kRawWords = kST * D;
@@ -72,10 +78,9 @@ struct NLayout {
   static constexpr int kOffPre = kOffWalk + kThreads / 32 * 128;
   static constexpr size_t bytes(int B) { return 1024 + kOffPre + static_cast<size_t>(B + 1) * 4; }
 };
-constexpr int kMaxB = 1024;            // sequences (their tile counts lie in shared memory)
-static_assert(NLayout<128, 64>::bytes(kMaxB) <= 232448, "shared memory");
-static_assert(16 * 128 * 4 <= kT * 128 && 32 * 128 * 4 <= kT * 128 && 64 * 128 * 4 <= 2 * kT * 128,
-              "the output rows fit the P buffers");
+constexpr int kMaxB = 2048;            // sequences (their tile counts lie in shared memory)
+static_assert(NLayout<128, 32>::bytes(kMaxB) <= 232448, "shared memory");
+static_assert(32 * 128 * 4 <= kT * 128, "a piece's output rows fit the P tile");
 
 // Whether any of a softmax warpgroup's 128 threads says so (all take part);
 // id: the warpgroup's barrier.
@@ -100,32 +105,29 @@ __device__ __forceinline__ int to_ordered(float x) {
 }
 __device__ __forceinline__ float from_ordered(int i) { return __int_as_float(i ^ ((i >> 31) & 0x7FFFFFFF)); }
 
-// The warp's sums of NR rows' values, one per lane and row, to dst[NR]: halves
-// of the rows change sides at each step, so a row's value is added up in
-// 31 shuffles a warp and 32 rows instead of five for each.
+// The warp's sums of NR rows' values to dst[NR]: at each step a lane keeps half
+// of the rows that it has and gives away the others (31 shuffles for 32 rows;
+// 80 for 16 rows one by one).
 template <int NR>
 __device__ __forceinline__ void sum_rows(float (&l)[NR], int lane, int32_t* dst) {
+  static_assert(NR == 16 || NR == 32, "at most a row a lane");
+  int row = 0;
 #pragma unroll
-  for (int r0 = 0; r0 < NR; r0 += 32) {
-    constexpr int W = NR < 32 ? NR : 32;
-    int row = 0;
+  for (int o = 16, n = NR / 2; o > 0; o >>= 1, n >>= 1) {
+    if (n > 0) {
+      const bool up = lane & o;           // keeps rows n .. 2n - 1 of those it has
 #pragma unroll
-    for (int o = 16, n = W / 2; o > 0; o >>= 1, n >>= 1) {
-      if (n > 0) {
-        const bool up = lane & o;         // keeps rows n .. 2n - 1 of those it has
-#pragma unroll
-        for (int i = 0; i < n; ++i) {
-          const float give = up ? l[r0 + i] : l[r0 + n + i];
-          const float keep = up ? l[r0 + n + i] : l[r0 + i];
-          l[r0 + i] = keep + __shfl_xor_sync(0xffffffffu, give, o);
-        }
-        row += up ? n : 0;
-      } else {
-        l[r0] += __shfl_xor_sync(0xffffffffu, l[r0], o);   // (16 rows: both lanes of a pair have the row)
+      for (int i = 0; i < n; ++i) {
+        const float give = up ? l[i] : l[n + i];
+        const float keep = up ? l[n + i] : l[i];
+        l[i] = keep + __shfl_xor_sync(0xffffffffu, give, o);
       }
+      row += up ? n : 0;
+    } else {
+      l[0] += __shfl_xor_sync(0xffffffffu, l[0], o);   // (16 rows: both lanes of a pair have the row)
     }
-    dst[r0 + row] = __float_as_int(l[r0]);
   }
+  dst[row] = __float_as_int(l[0]);
 }
 
 // One part (0: K, 1: V) of a piece's tiles by its two warpgroups: raw slots (64
@@ -149,7 +151,7 @@ __device__ __forceinline__ bool dequant_piece(const CParams& p, uint8_t* smem, u
     const uint32_t dst = smem_u32(smem + (which ? L::kOffV : L::kOffK) + st * L::kTile);
 #pragma unroll
     for (int s = 0; s < 2; ++s) {
-      const int k = which * L::kRing + static_cast<int>(slot);
+      const int k = which * kRing + static_cast<int>(slot);
       if (!__all_sync(0xffffffffu, mbar_wait(&bar[B_RAW0 + k], round & 1, p.status, kWaitNs))) return false;
       const bool mine = H > 1 || s == sub;
       const uint8_t* raw = smem + L::kOffRaw + k * L::kRawBytes;
@@ -174,7 +176,7 @@ __device__ __forceinline__ bool dequant_piece(const CParams& p, uint8_t* smem, u
           dequant_chunk<BITS>(dst, F::RPI * it + row, c * F::VPC, v[i], word[i]);
         }
       }
-      if (++slot == L::kRing) {
+      if (++slot == kRing) {
         slot = 0;
         ++round;
       }
@@ -268,7 +270,6 @@ template <int D, int NR>
 __global__ void __launch_bounds__(kThreads, 1) chunk_narrow_kernel(const __grid_constant__ CParams p) {
   using L = NLayout<D, NR>;
   constexpr uint32_t kCols = 4 * NR;                                 // TMEM: S^T and O^T of both states
-  constexpr int CH = NR < 32 ? NR : 32;                              // columns handled at a time
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = smem_raw + (-smem_u32(smem_raw) & 1023u);
   uint64_t* bar = reinterpret_cast<uint64_t*>(smem + L::kOffBar);
@@ -295,7 +296,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_narrow_kernel(const __grid_
     mbar_init(&bar[B_MMADONE0], 1);
     mbar_init(&bar[B_MMADONE0 + 1], 1);
     mbar_init(&bar[B_EXIT], kExitArrivals);
-    for (int k = 0; k < 2 * L::kRing; ++k) {
+    for (int k = 0; k < 2 * kRing; ++k) {
       mbar_init(&bar[B_RAW0 + k], 1);
       mbar_init(&bar[B_RFREE0 + k], 8);
     }
@@ -458,7 +459,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_narrow_kernel(const __grid_
 #pragma unroll
         for (int s = 0; s < 2; ++s) {
           int64_t blk = __shfl_sync(0xffffffffu, half[s], j & 31);
-          const int k = x * L::kRing + static_cast<int>(slot);
+          const int k = x * kRing + static_cast<int>(slot);
           if (round > 0) ok = wait_all(B_RFREE0 + k, round - 1);
           if (!ok) break;
           if (lane == 0) {
@@ -471,7 +472,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_narrow_kernel(const __grid_
             bulk_g2s_hint(raw, codes + at * rb, cb, &bar[B_RAW0 + k], pol);
             bulk_g2s_hint(raw + L::kRawWords, words + at * (D / 32), wb, &bar[B_RAW0 + k], pol);
           }
-          if (++slot == L::kRing) {
+          if (++slot == kRing) {
             slot = 0;
             ++round;
           }
@@ -536,8 +537,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_narrow_kernel(const __grid_
   const uint32_t lanes = static_cast<uint32_t>(q4 * 32) << 16;
   const uint32_t s_addr = tmem + lanes + x * NR;
   const uint32_t o_addr = tmem + lanes + 2 * NR + x * NR;
-  const uint32_t p_row = smem_u32(smem + L::kOffP) + key * 128 + (NR > 32 ? x * L::kPStep : 0);
-  constexpr int kPChunk = NR <= 32 ? L::kPStep / 16 : 0;   // 16-byte chunks to state 1's columns
+  const uint32_t p_row = smem_u32(smem + L::kOffP) + key * 128;
   const float sl2 = p.scale_log2;
   uint32_t cnt = 0, piece = 0;                             // this state's tiles; pieces
   bool ok = true, stop = false;
@@ -564,14 +564,13 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_narrow_kernel(const __grid_
       ok = wait_all(B_SFULL0 + x, cnt) && ok;
       tc::fence_after_sync();
       float s[NR];
-#pragma unroll
-      for (int c0 = 0; c0 < NR; c0 += CH) {
-        uint32_t v[CH];
-        if constexpr (CH == 16) tc::ld_32x32b_x16(s_addr + c0, v);
-        else tc::ld_32x32b_x32(s_addr + c0, v);
+      {
+        uint32_t v[NR];
+        if constexpr (NR == 16) tc::ld_32x32b_x16(s_addr, v);
+        else tc::ld_32x32b_x32(s_addr, v);
         tc::wait_ld(v);
 #pragma unroll
-        for (int i = 0; i < CH; ++i) s[c0 + i] = __uint_as_float(v[i]) * sl2;
+        for (int i = 0; i < NR; ++i) s[i] = __uint_as_float(v[i]) * sl2;
       }
       if (masked) {
 #pragma unroll
@@ -599,7 +598,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_narrow_kernel(const __grid_
 #pragma unroll
         for (int i = 0; i < NR; ++i) {
           const int mx = __reduce_max_sync(0xffffffffu, to_ordered(s[i]));
-          if (lane == (i & 31)) row_w[q4 * NR + i] = mx;
+          if (lane == i) row_w[q4 * NR + i] = mx;
         }
         group_sync(id);
         if (key < NR) {
@@ -650,7 +649,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_narrow_kernel(const __grid_
       if (cnt > 0) ok = wait_all(B_PDONE0 + x, cnt - 1) && ok;
 #pragma unroll
       for (int i = 0; i < NR / 8; ++i)
-        sts128(p_row + (((i + x * kPChunk) ^ (key & 7)) << 4), pk[4 * i], pk[4 * i + 1], pk[4 * i + 2], pk[4 * i + 3]);
+        sts128(p_row + (((i + x * (L::kPStep / 16)) ^ (key & 7)) << 4), pk[4 * i], pk[4 * i + 1], pk[4 * i + 2], pk[4 * i + 3]);
       fence_proxy_async_smem();
       tc::fence_before_sync();
       __syncwarp();
@@ -754,7 +753,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_narrow_kernel(const __grid_
 // Per device and instantiation, set once under a lock: the kernel's dynamic
 // shared-memory limit, and its registers checked.
 std::mutex g_prep_mu;
-bool g_prep[64][6] = {};
+bool g_prep[64][4] = {};
 
 template <int D, int NR>
 kvq_status launch_n(const CParams& p, cudaStream_t stream) {
@@ -763,7 +762,7 @@ kvq_status launch_n(const CParams& p, cudaStream_t stream) {
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return KVQ_ERR_CUDA;
   {
     std::lock_guard<std::mutex> lock(g_prep_mu);
-    bool& ready = g_prep[dev][(D == 128 ? 3 : 0) + (NR == 16 ? 0 : NR == 32 ? 1 : 2)];
+    bool& ready = g_prep[dev][(D == 128 ? 2 : 0) + (NR == 16 ? 0 : 1)];
     if (!ready) {
       // the register split inside the kernel assumes 72 per thread at launch
       cudaFuncAttributes fa;
@@ -790,14 +789,15 @@ kvq_status launch_n(const CParams& p, cudaStream_t stream) {
 
 }  // namespace
 
-bool chunk_narrow_takes(int B, int64_t max_rows) { return B <= kMaxB && max_rows <= 64; }
+// At most 32 rows: with 64 columns a softmax thread's scores and sums do not fit
+// its registers, and the 256-row kernel is faster (eight sequences of 8000
+// tokens, 16 rows: 44 us here, 82 there; 32 rows: 60 and 78 with 4-bit heads;
+// 64 rows: 108 and 79).
+bool chunk_narrow_takes(int B, int64_t max_rows) { return B <= kMaxB && max_rows <= 32; }
 
 kvq_status launch_chunk_narrow(const CParams& p, int D, int64_t max_rows, cudaStream_t stream) {
-  if (D == 128)
-    return max_rows <= 16 ? launch_n<128, 16>(p, stream)
-                          : max_rows <= 32 ? launch_n<128, 32>(p, stream) : launch_n<128, 64>(p, stream);
-  return max_rows <= 16 ? launch_n<64, 16>(p, stream)
-                        : max_rows <= 32 ? launch_n<64, 32>(p, stream) : launch_n<64, 64>(p, stream);
+  if (D == 128) return max_rows <= 16 ? launch_n<128, 16>(p, stream) : launch_n<128, 32>(p, stream);
+  return max_rows <= 16 ? launch_n<64, 16>(p, stream) : launch_n<64, 32>(p, stream);
 }
 
 }  // namespace kvq

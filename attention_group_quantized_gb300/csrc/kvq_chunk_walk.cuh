@@ -336,7 +336,7 @@ __device__ __forceinline__ bool load_queries(const CParams& p, uint32_t dst, uin
 
 }  // namespace chunk_walk
 
-// The kernel for at most 64 rows per (sequence, KV head), where it applies.
+// The kernel for few rows per (sequence, KV head), where it applies.
 bool chunk_narrow_takes(int B, int64_t max_rows);
 kvq_status launch_chunk_narrow(const chunk_walk::CParams& p, int D, int64_t max_rows, cudaStream_t stream);
 
