@@ -649,3 +649,149 @@ def test_long_walks_against_the_definition_on_the_device(case):
             worst = max(worst, float((err / bound).max()))
             assert torch.isfinite(err).all()
     assert worst <= 1.0, worst
+
+
+# ---------------------------------------------------------------- limits, concurrency, the debug library
+
+def test_positions_past_32_bits_of_a_long_cache():
+    """One sequence of five million tokens (codes of over 5 GB per cache): its first tokens and its last ones, far
+    beyond 2^32 bytes, written, read back and attended through a window with sinks."""
+    kvq = _kvq()
+    Hq, Hkv, D, L, n, window, sinks, keep = 16, 8, 128, 5_000_000, 5, 150, 4, 300
+    cap = -(-L // 64) * 64
+    kc, vc = (kvq.empty_cache([8] * Hkv, 1, cap, D) for _ in "kv")
+    assert kc.codes.numel() > 2 ** 32
+    rng = np.random.default_rng(71)
+    k, v = (W._draw_bf16(rng, (1, Hkv, sinks + keep, D)) for _ in "kv")
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    dev = lambda *a: torch.tensor(a, dtype=torch.int32, device="cuda")
+    rows = [U.to_dev_bf16(np.ascontiguousarray(x[0].transpose(1, 0, 2))) for x in (k, v)]
+    kvq.append_chunk(rows[0][:sinks], rows[1][:sinks], kc, vc, dev(0, sinks), dev(sinks), status=status)
+    kvq.append_chunk(rows[0][sinks:], rows[1][sinks:], kc, vc, dev(0, keep), dev(L), status=status)
+    kd, vd = (U.oracle_quantize(x, [8] * Hkv)[3][0] for x in (k, v))
+    got = kvq.dequantize(vc, dev(0, keep), dev(L), keep, out_dtype=kvq.OUT_F32, status=status)
+    torch.cuda.synchronize()
+    assert torch.equal(got.cpu(), torch.from_numpy(vd[:, sinks:].transpose(1, 0, 2).copy()).float())
+    q = W._draw_bf16(rng, (n, Hq, D))
+    pos = np.arange(L - n, L)[:, None]
+    tok = np.concatenate([np.arange(sinks), np.arange(L - keep, L)])[None]
+    see = (tok <= pos) & ((tok > pos - window) | (tok < sinks))
+    ref, bound = np.zeros((n, Hq, D)), np.zeros((n, Hq, D))
+    for h in range(Hq):
+        ref[:, h], bound[:, h] = attention_and_bound(O.bf16_to_f32(q[:, h]).astype(np.float64), kd[h // 2], vd[h // 2],
+                                                     D ** -0.5, see)
+    for max_chunk in (n, None if n * Hq // Hkv > 32 else 4000):          # both kernels
+        out = kvq.chunk_attention(U.to_dev_bf16(q), kc, vc, dev(0, n), dev(L), window=window, sinks=sinks,
+                                  max_chunk=max_chunk, status=status)
+        torch.cuda.synchronize()
+        assert int(status.item()) == 0
+        check(out, ref, bound, False, str(max_chunk))
+    one = kvq.decode_attention_window(U.to_dev_bf16(q[-1:]), kc, vc, dev(L), window, sinks, status=status)
+    torch.cuda.synchronize()
+    assert int(status.item()) == 0
+    check(one, ref[-1:], bound[-1:], False, "decode")
+
+
+@pytest.mark.parametrize("B", [2049, 4096])
+def test_thousands_of_sequences(B):
+    """More sequences than the kernel for few rows has room for, and as many as the calls take; every seventh has no
+    new token."""
+    kvq = _kvq()
+    new = [0 if i % 7 == 3 else 1 + i % 2 for i in range(B)]
+    b = Batch(72, 2, 1, 64, "8", new, [(5 * i) % 70 for i in range(B)], True)
+    b.fill()
+    b.append_new()
+    ref, bound = b.reference(window=9, sinks=2)
+    check(b.attend(U.to_dev_bf16(b.q), window=9, sinks=2, max_chunk=2), ref, bound, False)
+    b.ok()
+
+
+def test_two_calls_at_once_on_two_streams():
+    """Independent calls with workspaces of their own, overlapping: the bits of each call alone."""
+    kvq = _kvq()
+    bs = [Batch(80 + i, 8, 2, 128, "84", n, c, bool(i)) for i, (n, c) in
+          enumerate([([150, 9, 60], [700, 1000, 300]), ([3, 4, 2], [1500, 40, 900])])]
+    qs, wss, alone = [], [], []
+    for b in bs:
+        b.fill()
+        b.append_new()
+        qs.append(U.to_dev_bf16(b.q))
+        wss.append(kvq.chunk_workspace(b.rows, b.B, 8, 2, 128))
+        alone.append(b.attend(qs[-1], workspace=wss[-1], max_chunk=max(b.new)))
+        b.ok()
+    streams = [torch.cuda.Stream() for _ in bs]
+    outs = [[torch.empty_like(a) for _ in range(6)] for a in alone]
+    torch.cuda.synchronize()
+    for r in range(6):
+        for b, q, ws, s, o in zip(bs, qs, wss, streams, outs):
+            b.attend(q, workspace=ws, max_chunk=max(b.new), stream=s, out=o[r])
+    for b, a, o in zip(bs, alone, outs):
+        b.ok()
+        assert all(torch.equal(a, x) for x in o)
+
+
+def test_one_workspace_for_calls_of_different_shapes():
+    """Calls of different rows, heads and widths, ordered on a stream, share one workspace (it stays zeroed where it
+    has to be)."""
+    kvq = _kvq()
+    shapes = [(8, 2, 128, [200, 30], [400, 90]), (4, 4, 64, [3, 1], [900, 700]), (16, 2, 128, [4, 2], [1300, 64])]
+    bs = [Batch(90 + i, Hq, Hkv, D, "8", n, c, False) for i, (Hq, Hkv, D, n, c) in enumerate(shapes)]
+    ws = torch.zeros(max(kvq.chunk_workspace_bytes(b.rows, b.B, b.Hq, b.Hkv, b.D) for b in bs), dtype=torch.uint8,
+                     device="cuda")
+    for b in bs:
+        b.fill()
+        b.append_new()
+        b.ref = b.reference()
+    for _ in range(3):
+        for b in bs:
+            check(b.attend(U.to_dev_bf16(b.q), workspace=ws, max_chunk=max(b.new)), *b.ref, False)
+            b.ok()
+
+
+@pytest.mark.parametrize("case", [a for a in ATTN if a[0] in ("ragged_mixed", "rep3", "window_edges", "long",
+                                                              "sinks_past_the_window", "shared_by_all")],
+                         ids=lambda c: c[0])
+def test_debug_library_finds_no_index_out_of_range(case):
+    """The same calls on the library built with index checks: no failed check, the same bytes."""
+    import os
+    kvq = _kvq()
+    if not os.path.exists(kvq.DEBUG_LIB_PATH):
+        from attention_group_quantized_gb300 import build
+        build.build(debug=True)
+    name, Hq, Hkv, D, bits, new, ctx, paged, window, sinks = case
+    results = []
+    old = kvq.LIB_PATH, kvq._LIB
+    try:
+        for path in (kvq.LIB_PATH, kvq.DEBUG_LIB_PATH):
+            kvq.LIB_PATH, kvq._LIB = path, None
+            b = Batch(95, Hq, Hkv, D, bits, new, ctx, paged)
+            b.fill()
+            b.append_new()
+            q = U.to_dev_bf16(b.q)
+            got = [b.attend(q, window=window, sinks=sinks, max_chunk=m) for m in (None, max(new))]
+            got += [b.read(x, b.d_start, b.d_lens, b.rows) for x in "kv"]
+            b.ok()
+            results.append([x.cpu() for x in got])
+    finally:
+        kvq.LIB_PATH, kvq._LIB = old
+    for x, y in zip(*results):
+        assert torch.equal(x.view(torch.uint8), y.view(torch.uint8))
+
+
+def test_guard_bytes_around_outputs_and_workspace():
+    """Nothing is written outside the output and the workspace."""
+    kvq = _kvq()
+    for new, max_chunk in (([3, 2], 3), ([90, 5], None)):
+        b = Batch(96, 8, 2, 128, "84", new, [700, 100], True)
+        b.fill()
+        b.append_new()
+        n_out, n_ws = b.rows * 8 * 128 * 4, kvq.chunk_workspace_bytes(b.rows, b.B, 8, 2, 128)
+        bufs = [torch.full((512 + n,), 0x5A, dtype=torch.uint8, device="cuda") for n in (n_out, n_ws)]
+        out = bufs[0][256:256 + n_out].view(torch.float32).view(b.rows, 8, 128)
+        ws = bufs[1][256:256 + n_ws]
+        ws.zero_()
+        b.attend(U.to_dev_bf16(b.q), out=out, workspace=ws, max_chunk=max_chunk)
+        b.ok()
+        check(out, *b.reference(), False)
+        for buf, n in zip(bufs, (n_out, n_ws)):
+            assert (buf[:256] == 0x5A).all() and (buf[256 + n:] == 0x5A).all()
