@@ -8,6 +8,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 from dataclasses import dataclass
 from typing import Optional, Sequence
 
@@ -121,24 +122,24 @@ def lib() -> ctypes.CDLL:
         L.kvq_prefill_attention_ex.argtypes = [P, P, P, I32, I32, I32, I32, I32, P, I32, F32, P, I32, CP, CP, P,
                                                I32, PP, P, P]
         L.kvq_prefill_attention_ex.restype = I32
-        CH = ctypes.POINTER(CChunk)
-        L.kvq_append_chunk.argtypes = [P, P, I64, I64, CH, CP, CP, P, P]
+        # (kvq_chunk and kvq_block_table arguments: byref of a CChunk or CBlockTable, or their bytes)
+        L.kvq_append_chunk.argtypes = [P, P, I64, I64, P, CP, CP, P, P]
         L.kvq_append_chunk.restype = I32
-        L.kvq_append_chunk_paged.argtypes = [P, P, I64, I64, CH, CP, CP, BT, P, P]
+        L.kvq_append_chunk_paged.argtypes = [P, P, I64, I64, P, CP, CP, P, P, P]
         L.kvq_append_chunk_paged.restype = I32
-        L.kvq_dequantize.argtypes = [CP, CH, P, I32, P, P]
+        L.kvq_dequantize.argtypes = [CP, P, P, I32, P, P]
         L.kvq_dequantize.restype = I32
-        L.kvq_dequantize_paged.argtypes = [CP, CH, BT, P, I32, P, P]
+        L.kvq_dequantize_paged.argtypes = [CP, P, P, P, I32, P, P]
         L.kvq_dequantize_paged.restype = I32
         L.kvq_chunk_workspace_bytes.argtypes = [I32, I32, I32, I32, I32]
         L.kvq_chunk_workspace_bytes.restype = SZ
-        L.kvq_chunk_attention.argtypes = [P, I64, I64, CH, CP, CP, I32, F32, I32, I32, P, I32, P, SZ, P, P]
+        L.kvq_chunk_attention.argtypes = [P, I64, I64, P, CP, CP, I32, F32, I32, I32, P, I32, P, SZ, P, P]
         L.kvq_chunk_attention.restype = I32
-        L.kvq_chunk_attention_paged.argtypes = [P, I64, I64, CH, CP, CP, BT, I32, F32, I32, I32, P, I32, P, SZ, P, P]
+        L.kvq_chunk_attention_paged.argtypes = [P, I64, I64, P, CP, CP, P, I32, F32, I32, I32, P, I32, P, SZ, P, P]
         L.kvq_chunk_attention_paged.restype = I32
         L.kvq_decode_attention_window.argtypes = [P, CP, CP, P, I32, F32, I32, I32, P, I32, P, SZ, P, P]
         L.kvq_decode_attention_window.restype = I32
-        L.kvq_decode_attention_window_paged.argtypes = [P, CP, CP, BT, P, I32, F32, I32, I32, P, I32, P, SZ, P, P]
+        L.kvq_decode_attention_window_paged.argtypes = [P, CP, CP, P, P, I32, F32, I32, I32, P, I32, P, SZ, P, P]
         L.kvq_decode_attention_window_paged.restype = I32
         _LIB = L
     return _LIB
@@ -562,29 +563,43 @@ def prefill_attention(q, k, v, k_cache: QuantCache, v_cache: QuantCache, softmax
 # chunks: several new tokens per sequence, packed
 # ---------------------------------------------------------------------------
 # (These calls run every few microseconds in a serving loop: the checks below
-# format nothing unless they fail.)
+# format nothing unless they fail, and the small structs are packed as bytes,
+# which costs half of a ctypes structure.)
+
+_pack_chunk = struct.Struct("@PPiii4x").pack   # kvq_chunk
+_pack_table = struct.Struct("@Pii").pack       # kvq_block_table
 
 def _bad(what: str):
     raise KvqError(1, what)
 
 
-def _on_current_device(x, *others):
-    """The kernels launch on the current device: every tensor must live there."""
+def _on_current_device(x, *others) -> int:
+    """The kernels launch on the current device: every tensor must live there.  Returns its index."""
     i = x.get_device()
     if i < 0 or i != _torch().cuda.current_device():
         _bad("tensors that are not on the current CUDA device")
     for o in others:
         if o.get_device() != i:
             _bad("tensors on different devices")
+    return i
 
 
-def _chunk(start, seq_lens, rows: int, max_chunk: Optional[int]) -> CChunk:
+def _stream_on(stream, device: int) -> int:
+    """The stream to launch on: the caller's, or the device's current one."""
+    if stream is not None:
+        return stream.cuda_stream
+    raw = getattr(_TORCH._C, "_cuda_getCurrentRawStream", None)
+    return raw(device) if raw is not None else _TORCH.cuda.current_stream().cuda_stream
+
+
+def _chunk(start, seq_lens, rows: int, max_chunk: Optional[int]) -> bytes:
     """start: device int32 [B + 1], seq_lens: device int32 [B]."""
     i32 = _torch().int32
     if (start.dtype != i32 or seq_lens.dtype != i32 or start.dim() != 1 or seq_lens.dim() != 1
             or start.shape[0] != seq_lens.shape[0] + 1 or not start.is_contiguous() or not seq_lens.is_contiguous()):
         _bad("chunk: start int32 [B + 1] and seq_lens int32 [B], contiguous")
-    return CChunk(start.data_ptr(), seq_lens.data_ptr(), seq_lens.shape[0], rows, 0 if max_chunk is None else max_chunk)
+    return _pack_chunk(start.data_ptr(), seq_lens.data_ptr(), seq_lens.shape[0], rows,
+                       0 if max_chunk is None else max_chunk)
 
 
 def _block_table(block_table):
@@ -593,7 +608,7 @@ def _block_table(block_table):
         return None
     if block_table.dtype != _torch().int32 or block_table.dim() != 2 or not block_table.is_contiguous():
         _bad("block_table: int32 [B][max_pages], contiguous")
-    return CBlockTable(block_table.data_ptr(), block_table.shape[0], block_table.shape[1])
+    return _pack_table(block_table.data_ptr(), block_table.shape[0], block_table.shape[1])
 
 
 def _packed(x, heads: int, D: int, what: str):
@@ -623,17 +638,17 @@ def _append_chunk(k_new, v_new, k: QuantCache, v: QuantCache, block_table, start
     if k_new.shape[0] != v_new.shape[0] or k_new.stride() != v_new.stride():
         _bad("k_new and v_new: the same rows and strides")
     bt = _block_table(block_table)
-    _on_current_device(k_new, v_new, k.codes, v.codes, start, seq_lens)
+    dev = _on_current_device(k_new, v_new, k.codes, v.codes, start, seq_lens)
     ch = _chunk(start, seq_lens, k_new.shape[0], None)
     s_row, s_head, _ = k_new.stride()
     if bt is None:
         st = lib().kvq_append_chunk(k_new.data_ptr(), v_new.data_ptr(), s_row, s_head, ch, k.c_struct(), v.c_struct(),
-                                    _status_ptr(status), _stream_ptr(stream))
+                                    _status_ptr(status), _stream_on(stream, dev))
         _check(st, "kvq_append_chunk")
     else:
         _on_current_device(block_table)
         st = lib().kvq_append_chunk_paged(k_new.data_ptr(), v_new.data_ptr(), s_row, s_head, ch, k.c_struct(),
-                                          v.c_struct(), bt, _status_ptr(status), _stream_ptr(stream))
+                                          v.c_struct(), bt, _status_ptr(status), _stream_on(stream, dev))
         _check(st, "kvq_append_chunk_paged")
 
 
@@ -651,17 +666,17 @@ def append_chunk_paged(k_new, v_new, k_pool: QuantCache, v_pool: QuantCache, blo
 
 def _dequantize(cache: QuantCache, block_table, start, seq_lens, rows: int, out, out_dtype, status, stream):
     bt = _block_table(block_table)
-    _on_current_device(cache.codes, start, seq_lens)
+    dev = _on_current_device(cache.codes, start, seq_lens)
     out = _out(out, (rows, cache.Hkv, cache.D), out_dtype, cache.codes, "dequantize")
     ch = _chunk(start, seq_lens, rows, None)
     if bt is None:
         st = lib().kvq_dequantize(cache.c_struct(), ch, out.data_ptr(), out_dtype, _status_ptr(status),
-                                  _stream_ptr(stream))
+                                  _stream_on(stream, dev))
         _check(st, "kvq_dequantize")
     else:
         _on_current_device(block_table)
         st = lib().kvq_dequantize_paged(cache.c_struct(), ch, bt, out.data_ptr(), out_dtype, _status_ptr(status),
-                                        _stream_ptr(stream))
+                                        _stream_on(stream, dev))
         _check(st, "kvq_dequantize_paged")
     return out
 
@@ -696,7 +711,7 @@ def _chunk_attention(q, k: QuantCache, v: QuantCache, block_table, start, seq_le
     rows, Hq, D = q.shape
     _packed(q, Hq, k.D, "q")
     bt = _block_table(block_table)
-    _on_current_device(q, k.codes, v.codes, start, seq_lens)
+    dev = _on_current_device(q, k.codes, v.codes, start, seq_lens)
     out = _out(out, (rows, Hq, D), out_dtype, q, "chunk_attention")
     if workspace is None:
         workspace = chunk_workspace(rows, int(seq_lens.shape[0]), Hq, k.Hkv, D, q.device)
@@ -706,13 +721,13 @@ def _chunk_attention(q, k: QuantCache, v: QuantCache, block_table, start, seq_le
     if bt is None:
         st = lib().kvq_chunk_attention(q.data_ptr(), s_row, s_head, ch, k.c_struct(), v.c_struct(), Hq, softmax_scale,
                                        window, sinks, out.data_ptr(), out_dtype, workspace.data_ptr(), ws_n,
-                                       _status_ptr(status), _stream_ptr(stream))
+                                       _status_ptr(status), _stream_on(stream, dev))
         _check(st, "kvq_chunk_attention")
     else:
         _on_current_device(block_table)
         st = lib().kvq_chunk_attention_paged(q.data_ptr(), s_row, s_head, ch, k.c_struct(), v.c_struct(), bt, Hq,
                                              softmax_scale, window, sinks, out.data_ptr(), out_dtype,
-                                             workspace.data_ptr(), ws_n, _status_ptr(status), _stream_ptr(stream))
+                                             workspace.data_ptr(), ws_n, _status_ptr(status), _stream_on(stream, dev))
         _check(st, "kvq_chunk_attention_paged")
     return out
 
@@ -744,9 +759,9 @@ def _decode_window(q, k: QuantCache, v: QuantCache, block_table, seq_lens, windo
     B, Hq, D = q.shape
     bt = _block_table(block_table)
     if (seq_lens.dtype != torch.int32 or seq_lens.dim() != 1 or seq_lens.shape[0] != B or not seq_lens.is_contiguous()
-            or B != (k.B if bt is None else bt.B)):
+            or B != (k.B if bt is None else block_table.shape[0])):
         _bad("seq_lens: int32 [B]")
-    _on_current_device(q, k.codes, v.codes, seq_lens)
+    dev = _on_current_device(q, k.codes, v.codes, seq_lens)
     out = _out(out, (B, Hq, D), out_dtype, q, "decode_attention_window")
     if workspace is None:
         workspace = decode_workspace(B, Hq, k.Hkv, D, q.device)
@@ -754,14 +769,14 @@ def _decode_window(q, k: QuantCache, v: QuantCache, block_table, seq_lens, windo
     if bt is None:
         st = lib().kvq_decode_attention_window(q.data_ptr(), k.c_struct(), v.c_struct(), seq_lens.data_ptr(), Hq,
                                                softmax_scale, window, sinks, out.data_ptr(), out_dtype,
-                                               workspace.data_ptr(), ws_n, _status_ptr(status), _stream_ptr(stream))
+                                               workspace.data_ptr(), ws_n, _status_ptr(status), _stream_on(stream, dev))
         _check(st, "kvq_decode_attention_window")
     else:
         _on_current_device(block_table)
         st = lib().kvq_decode_attention_window_paged(q.data_ptr(), k.c_struct(), v.c_struct(), bt,
                                                      seq_lens.data_ptr(), Hq, softmax_scale, window, sinks,
                                                      out.data_ptr(), out_dtype, workspace.data_ptr(), ws_n,
-                                                     _status_ptr(status), _stream_ptr(stream))
+                                                     _status_ptr(status), _stream_on(stream, dev))
         _check(st, "kvq_decode_attention_window_paged")
     return out
 
