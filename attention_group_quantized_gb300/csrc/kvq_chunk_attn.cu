@@ -160,6 +160,56 @@ __device__ __forceinline__ void store_part(uint32_t dst, const PartRegs<D, BITS>
   for (int it = 0; it < F::NI; ++it) dequant_chunk<BITS>(dst, F::RPI * it + row, c * F::VPC, r.c[it], r.w[it]);
 }
 
+// 16 bytes from global to shared memory without a register, zeros for n = 0.
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, uint32_t n) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
+}
+__device__ __forceinline__ uint4 lds128(uint32_t saddr) {
+  uint4 v;
+  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(saddr) : "memory");
+  return v;
+}
+
+// The piece's query rows (rows past the segment's end zero) into the swizzled
+// tiles and there, each thread its own 16-byte chunks, to fp16.  All of a
+// piece's loads are in flight together: through registers, in batches of
+// eight, the next piece's first product waited 2 us longer.
+template <int D>
+__device__ __forceinline__ bool fetch_queries(const CParams& p, uint32_t dst, uint64_t* empty, const Walk& w, int t,
+                                              uint32_t piece) {
+  constexpr int CPR = D / 8;              // 16-byte chunks per row
+  constexpr int RPP = 128 / CPR;          // rows per pass
+  const int ch = t % CPR, row = t / CPR;
+  const int rows = w.t.rows, end = rows > kT ? kRows : kT;
+  if (piece > 0 && !__all_sync(0xffffffffu, mbar_wait(empty, (piece - 1) & 1, p.status, kWaitNs))) return false;
+  const uint16_t* base = p.q + static_cast<int64_t>(w.s.row0) * p.sq_row + w.kvh * p.rep * p.sq_head + ch * 8;
+  const int R0 = w.rt * kRows + row;      // token and head of this thread's row, stepped from pass to pass
+  int tok = R0 / p.rep, hh = R0 - tok * p.rep;
+  const int dtok = RPP / p.rep, dhh = RPP - dtok * p.rep;
+  auto at = [&](int r) { return dst + (r / kT) * (kT * D * 2) + (ch >> 3) * (kT * 128) + (r % kT) * 128 + (((ch & 7) ^ (r & 7)) << 4); };
+#pragma unroll 4
+  for (int r = row; r < end; r += RPP) {
+    const bool live = r < rows;
+    cp_async16(at(r), live ? base + tok * p.sq_row + hh * p.sq_head : base, live ? 16u : 0u);
+    tok += dtok;
+    hh += dhh;
+    if (hh >= p.rep) {
+      hh -= p.rep;
+      ++tok;
+    }
+  }
+  asm volatile("cp.async.wait_all;" ::: "memory");
+  const bool four = p.bits[w.kvh] == 4;
+  uint32_t big = 0;
+#pragma unroll 4
+  for (int r = row; r < end; r += RPP) {
+    const uint4 x = query_chunk(lds128(at(r)), four, big);
+    sts128(at(r), x.x, x.y, x.z, x.w);
+  }
+  check_queries(p, big);
+  return true;
+}
+
 // The key tiles of one piece: codes to fp16 operand tiles.  jj counts the
 // CTA's tiles (stage jj & 1).  False after a wait that ran out.
 template <int D, int BITS, bool PAGED>
@@ -189,7 +239,7 @@ __device__ __forceinline__ bool dequant_piece(const CParams& p, uint8_t* smem, u
   next.look_up(p, w, min(1, w.n - 1));
   cur.check(p, bad);
   load_part<D, BITS>(ra, k_ptr(cur));
-  if (!load_queries<D, kT, kRows>(p, smem_u32(smem + L::kOffQ), &bar[B_QEMPTY], w, t, (piece - 1) & 1, piece > 0)) return false;
+  if (!fetch_queries<D>(p, smem_u32(smem + L::kOffQ), &bar[B_QEMPTY], w, t, piece)) return false;
   done(B_QREADY);
   for (int j = 0; j < w.n; ++j, ++jj) {
     const uint32_t st = jj & 1;

@@ -277,6 +277,25 @@ __device__ __forceinline__ void clear_unseen(uint32_t dst, const CParams& p, con
   }
 }
 
+// Eight query channels, bf16 to fp16 (for a 4-bit head in the channel order of
+// its K tiles, 0,4,1,5,2,6,3,7); big: the largest magnitude seen, as two bf16
+// bit patterns.
+__device__ __forceinline__ uint4 query_chunk(uint4 v, bool four, uint32_t& big) {
+  uint32_t x[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    big = __vmaxu2(big, x[e] & 0x7FFF7FFFu);
+    x[e] = pack_half2(__uint_as_float(x[e] << 16), __uint_as_float(x[e] & 0xFFFF0000u));
+  }
+  if (!four) return make_uint4(x[0], x[1], x[2], x[3]);
+  return make_uint4(prmt(x[0], x[2], 0x5410u), prmt(x[0], x[2], 0x7632u), prmt(x[1], x[3], 0x5410u),
+                    prmt(x[1], x[3], 0x7632u));
+}
+__device__ __forceinline__ void check_queries(const CParams& p, uint32_t big) {
+  // 0x4780 is 65536, the first bf16 beyond fp16's range (infinities and NaN lie above it)
+  if ((big & 0xFFFFu) >= 0x4780u || (big >> 16) >= 0x4780u) report(p.status, KVQ_ERR_NONFINITE);
+}
+
 // The piece's query rows to fp16 in the swizzled layout (rows past the
 // segment's end zero); for a 4-bit head in the channel order of its K tiles.
 // dst: tiles of TILE rows ([D / 64 blocks][TILE rows][128 B] each), ROWS rows
@@ -295,7 +314,7 @@ __device__ __forceinline__ bool load_queries(const CParams& p, uint32_t dst, uin
   const int R0 = w.rt * ROWS + t / CPR;
   int tok = R0 / p.rep, hh = R0 - tok * p.rep;
   const int dtok = RPP / p.rep, dhh = RPP - dtok * p.rep;
-  uint32_t big = 0;                       // the largest magnitude seen, as two bf16 bit patterns
+  uint32_t big = 0;
   for (int r0 = 0; r0 < end; r0 += RPP * NB) {
     uint4 v[NB];
 #pragma unroll
@@ -314,23 +333,12 @@ __device__ __forceinline__ bool load_queries(const CParams& p, uint32_t dst, uin
 #pragma unroll
     for (int k = 0; k < NB; ++k) {
       const int r = r0 + k * RPP + t / CPR;
-      uint32_t x[4] = {v[k].x, v[k].y, v[k].z, v[k].w};
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        big = __vmaxu2(big, x[e] & 0x7FFF7FFFu);
-        x[e] = pack_half2(__uint_as_float(x[e] << 16), __uint_as_float(x[e] & 0xFFFF0000u));
-      }
-      if (four) {   // channels 0,4,1,5,2,6,3,7
-        const uint32_t a = prmt(x[0], x[2], 0x5410u), b = prmt(x[0], x[2], 0x7632u);
-        const uint32_t c = prmt(x[1], x[3], 0x5410u), d = prmt(x[1], x[3], 0x7632u);
-        x[0] = a; x[1] = b; x[2] = c; x[3] = d;
-      }
+      const uint4 x = query_chunk(v[k], four, big);
       const uint32_t rowp = dst + (r / TILE) * (TILE * D * 2) + (ch >> 3) * (TILE * 128) + (r % TILE) * 128;
-      tile::sts128(rowp + (((ch & 7) ^ (r & 7)) << 4), x[0], x[1], x[2], x[3]);
+      tile::sts128(rowp + (((ch & 7) ^ (r & 7)) << 4), x.x, x.y, x.z, x.w);
     }
   }
-  // 0x4780 is 65536, the first bf16 beyond fp16's range (infinities and NaN lie above it)
-  if ((big & 0xFFFFu) >= 0x4780u || (big >> 16) >= 0x4780u) report(p.status, KVQ_ERR_NONFINITE);
+  check_queries(p, big);
   return true;
 }
 
