@@ -18,20 +18,31 @@
 // leaves one partial (o, lse) per piece in the workspace, and the CTA that
 // completes it merges them in a fixed order.
 //
-// One CTA (512 threads, one per SM):
+// One CTA (640 threads, one per SM):
 //   warp 0      allocates TMEM and frees it once every other role is done;
 //   warps 1, 2  issue slot h = warp - 1's tcgen05.mma (S_h = Q_h K^T from
 //               shared memory, O_h += P_h V with P from TMEM), taking turns so
 //               that one slot's softmax runs under the other's products;
 //   warp 3      fetches the next piece's queries into L2;
-//   warps 4-7   per piece, its query rows to fp16; per key tile, K and V codes
-//               to fp16 operand tiles (two stages), the next part's codes in
-//               flight in registers meanwhile;
-//   warps 8-15  softmax of slot 0 and slot 1, one thread per row; at a piece's
+//   warps 4-11  per piece, its query rows to fp16 (a warpgroup per slot); per
+//               key tile, K and V codes to fp16 operand tiles (two stages, a
+//               warpgroup per 64-token half), the next part's codes in flight
+//               in registers meanwhile;
+//   warps 12-19 softmax of slot 0 and slot 1, one thread per row; at a piece's
 //               end O / sum to the output or the workspace.
 // TMEM (512 columns): S_0 [0,128) O_0 [128,128+D) S_1 [256,384) O_1 [384,384+D).
 // The running max only moves (and O is rescaled) when it grows by more than
 // 2^8; P is rounded to fp16, sums and O stay in fp32.
+//
+// Measured (32 query heads on 8, D = 128): 2048 tokens on 32K cached, INT8,
+// 844 us = 1344 TFLOP/s, 72 % of a bf16 GEMM's burst rate -- 1.85 us a tile of
+// 256 rows, of which the products take 1.37 at that rate and the softmax's 2^x
+// 1.1, next to them; what is left is the chain between them.  Shorter pieces
+// add about 12 us each (first queries and codes, partials, merge): 16 sequences
+// of 1 to 286 new tokens on 1K to 8K, from pages, 187 us; 3500 tokens with a
+// window of 4096 on 55K to 84K, INT4, 236 us.  One dequant warpgroup for whole
+// tiles took 246 and 257 us (K's and V's loads of one thread wait for each
+// other), as did an L2 prefetch of the codes.
 #include <cmath>
 #include <cstring>
 #include <mutex>
@@ -47,7 +58,7 @@ namespace {
 using namespace tile;
 using namespace chunk_walk;
 
-constexpr int kThreads = 512;
+constexpr int kThreads = 640;
 constexpr int kRows = 2 * kT;          // packed rows per segment
 constexpr uint32_t kTmemCols = 512;
 
@@ -74,90 +85,70 @@ struct CLayout {
   static size_t bytes(int B) { return 1024 + kOffPre + static_cast<size_t>(B + 1) * 4; }
 };
 
-// One key tile as its dequant threads read it: the storage blocks (64 tokens:
-// a page, or that much of a sequence) of its two halves -- a half that nothing
-// sees stands in for the other, its rows are masked.  Looked up one tile ahead
-// of the loads that use it and free of branches: a branch between a load and
-// its use waits for every load in flight.
+// Half a key tile (64 tokens: a page, or that much of a sequence) as its dequant
+// warpgroup reads it; a half that nothing sees stands in for the other, its
+// rows are masked.  Looked up one tile ahead of the loads that use it and free
+// of branches: a branch between a load and its use waits for every load in
+// flight.
 template <bool PAGED>
-struct TileRows {
+struct HalfTile {
   int t0;                // the tile's first token
-  int half[2];           // page ids as they stand in the table, or blocks
-  __device__ __forceinline__ void look_up(const CParams& p, const Walk& w, int j) {
+  int block;             // a page id as it stands in the table, or a block
+  __device__ __forceinline__ void look_up(const CParams& p, const Walk& w, int j, int x) {
     const Seen s(p, w);
     t0 = w.t.tile(w.i + j) * kT;
-    int i0 = t0 / 64, i1 = i0 + 1;
+    const int i0 = t0 / 64, i1 = i0 + 1;
     const bool seen0 = t0 + 64 > s.lo || t0 < p.sinks;
     const bool seen1 = t0 + 64 < s.end && (t0 + kT > s.lo || t0 + 64 < p.sinks);
-    i0 = seen0 ? i0 : i1;
-    i1 = seen1 ? i1 : i0;
+    const int i = (x == 0 ? seen0 : !seen1) ? i0 : i1;
     if constexpr (PAGED) {
-      const int32_t* pages = p.c.bt + static_cast<int64_t>(w.b) * p.c.bt_stride;
-      const bool ok = KVQ_IN_RANGE(i0 >= 0 && i0 < p.c.bt_stride && i1 >= 0 && i1 < p.c.bt_stride, p.status);
-      half[0] = ok ? pages[i0] : 0;
-      half[1] = ok ? pages[i1] : 0;
+      const bool ok = KVQ_IN_RANGE(i >= 0 && i < p.c.bt_stride, p.status);
+      block = ok ? p.c.bt[static_cast<int64_t>(w.b) * p.c.bt_stride + i] : 0;
     } else {
-      half[0] = w.b * (p.c.pT / 64) + i0;
-      half[1] = w.b * (p.c.pT / 64) + i1;
+      block = w.b * (p.c.pT / 64) + i;
     }
   }
   // A page outside the pool reads as page 0 (and is reported at the piece's end).
   __device__ __forceinline__ void check(const CParams& p, bool& bad) {
     if constexpr (PAGED) {
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const bool out = static_cast<uint32_t>(half[h]) >= static_cast<uint32_t>(p.c.pB);
-        bad |= out;
-        half[h] = out ? 0 : half[h];
-      }
+      const bool out = static_cast<uint32_t>(block) >= static_cast<uint32_t>(p.c.pB);
+      bad |= out;
+      block = out ? 0 : block;
     }
   }
 };
 
+// Half of a part (64 tokens' codes and words of K or V) in registers.
 template <int D, int BITS>
-struct PartRegs {
-  uint4 c[DqFmt<D, BITS>::NI];
-  uint32_t w[DqFmt<D, BITS>::NI];
+struct HalfRegs {
+  static constexpr int N = DqFmt<D, BITS>::NI / 2;
+  static_assert(2 * N == DqFmt<D, BITS>::NI, "whole iterations per half tile");
+  uint4 c[N];
+  uint32_t w[N];
 };
 
-// A thread's place (row, chunk) in the two halves of one part of a key tile.
+// codes, sz: the thread's place in block 0 of the head's codes and words (each
+// byte is used once per CTA: no L1 line).
 template <int D, int BITS>
-struct PartPtr {
-  const uint8_t* c[2];
-  const uint32_t* w[2];
-  // codes, sz: the thread's place in block 0 of the head's codes and words
-  __device__ __forceinline__ PartPtr(const CParams& p, const uint8_t* codes, const uint32_t* sz, int half0, int half1) {
-    const int64_t blocks = static_cast<int64_t>(p.c.pB) * (p.c.pT / 64);
+__device__ __forceinline__ void load_half(const CParams& p, HalfRegs<D, BITS>& r, const uint8_t* codes,
+                                          const uint32_t* sz, int block) {
+  using F = DqFmt<D, BITS>;
+  const int blk = KVQ_IN_RANGE(block >= 0 && block < static_cast<int64_t>(p.c.pB) * (p.c.pT / 64), p.status) ? block : 0;
+  codes += blk * int64_t(64 * F::R);
+  sz += blk * int64_t(64 * (D / 32));
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const int half = h == 0 ? half0 : half1;
-      const int blk = KVQ_IN_RANGE(half >= 0 && half < blocks, p.status) ? half : 0;
-      c[h] = codes + blk * int64_t(64 * DqFmt<D, BITS>::R);
-      w[h] = sz + blk * int64_t(64 * (D / 32));
-    }
+  for (int it = 0; it < r.N; ++it) {
+    r.c[it] = __ldcg(reinterpret_cast<const uint4*>(codes + it * F::RPI * F::R));
+    r.w[it] = __ldcg(sz + it * F::RPI * (D / 32));
   }
-};
-
-// Iteration it of a part (each byte is used once per CTA: no L1 line).
-template <int D, int BITS>
-__device__ __forceinline__ void load_iter(PartRegs<D, BITS>& r, const PartPtr<D, BITS>& s, int it) {
-  using F = DqFmt<D, BITS>;
-  constexpr int H = F::NI / 2;      // iterations per half
-  r.c[it] = __ldcg(reinterpret_cast<const uint4*>(s.c[it / H] + (it % H) * F::RPI * F::R));
-  r.w[it] = __ldcg(s.w[it / H] + (it % H) * F::RPI * (D / 32));
 }
 
 template <int D, int BITS>
-__device__ __forceinline__ void load_part(PartRegs<D, BITS>& r, const PartPtr<D, BITS>& s) {
-#pragma unroll
-  for (int it = 0; it < DqFmt<D, BITS>::NI; ++it) load_iter<D, BITS>(r, s, it);
-}
-
-template <int D, int BITS>
-__device__ __forceinline__ void store_part(uint32_t dst, const PartRegs<D, BITS>& r, int row, int c) {
+__device__ __forceinline__ void store_half(uint32_t dst, const HalfRegs<D, BITS>& r, int x, int row, int c) {
   using F = DqFmt<D, BITS>;
 #pragma unroll
-  for (int it = 0; it < F::NI; ++it) dequant_chunk<BITS>(dst, F::RPI * it + row, c * F::VPC, r.c[it], r.w[it]);
+  for (int it = 0; it < r.N; ++it)
+    dequant_chunk<BITS>(dst, F::RPI * (x * r.N + it) + row, c * F::VPC, r.c[it], r.w[it]);
 }
 
 // 16 bytes from global to shared memory without a register, zeros for n = 0.
@@ -170,23 +161,23 @@ __device__ __forceinline__ uint4 lds128(uint32_t saddr) {
   return v;
 }
 
-// The piece's query rows (rows past the segment's end zero) into the swizzled
-// tiles and there, each thread its own 16-byte chunks, to fp16.  All of a
+// The piece's query rows of slot x (rows past the segment's end zero) into its swizzled
+// tile and there, each thread its own 16-byte chunks, to fp16.  All of a
 // piece's loads are in flight together: through registers, in batches of
 // eight, the next piece's first product waited 2 us longer.
 template <int D>
-__device__ __forceinline__ bool fetch_queries(const CParams& p, uint32_t dst, uint64_t* empty, const Walk& w, int t,
-                                              uint32_t piece) {
+__device__ __forceinline__ bool fetch_queries(const CParams& p, uint32_t dst, uint64_t* empty, const Walk& w, int x,
+                                              int t, uint32_t piece) {
   constexpr int CPR = D / 8;              // 16-byte chunks per row
   constexpr int RPP = 128 / CPR;          // rows per pass
   const int ch = t % CPR, row = t / CPR;
-  const int rows = w.t.rows, end = rows > kT ? kRows : kT;
+  const int rows = w.t.rows - x * kT, end = rows > 0 ? kT : 0;   // the slot's
   if (piece > 0 && !__all_sync(0xffffffffu, mbar_wait(empty, (piece - 1) & 1, p.status, kWaitNs))) return false;
   const uint16_t* base = p.q + static_cast<int64_t>(w.s.row0) * p.sq_row + w.kvh * p.rep * p.sq_head + ch * 8;
-  const int R0 = w.rt * kRows + row;      // token and head of this thread's row, stepped from pass to pass
+  const int R0 = w.rt * kRows + x * kT + row;   // token and head of this thread's row, stepped from pass to pass
   int tok = R0 / p.rep, hh = R0 - tok * p.rep;
   const int dtok = RPP / p.rep, dhh = RPP - dtok * p.rep;
-  auto at = [&](int r) { return dst + (r / kT) * (kT * D * 2) + (ch >> 3) * (kT * 128) + (r % kT) * 128 + (((ch & 7) ^ (r & 7)) << 4); };
+  auto at = [&](int r) { return dst + x * (kT * D * 2) + (ch >> 3) * (kT * 128) + r * 128 + (((ch & 7) ^ (r & 7)) << 4); };
 #pragma unroll 4
   for (int r = row; r < end; r += RPP) {
     const bool live = r < rows;
@@ -210,15 +201,14 @@ __device__ __forceinline__ bool fetch_queries(const CParams& p, uint32_t dst, ui
   return true;
 }
 
-// The key tiles of one piece: codes to fp16 operand tiles.  jj counts the
-// CTA's tiles (stage jj & 1).  False after a wait that ran out.
+// Half x of the key tiles of one piece: codes to fp16 operand tiles.  jj counts
+// the CTA's tiles (stage jj & 1).  False after a wait that ran out.
 template <int D, int BITS, bool PAGED>
-__device__ __forceinline__ bool dequant_piece(const CParams& p, uint8_t* smem, uint64_t* bar, const Walk& w,
+__device__ __forceinline__ bool dequant_piece(const CParams& p, uint8_t* smem, uint64_t* bar, const Walk& w, int x,
                                               uint32_t& jj, uint32_t piece, bool& bad, int t, int lane) {
   using L = CLayout<D>;
   using F = DqFmt<D, BITS>;
-  constexpr int G = D / 32;
-  static_assert(F::NI % 2 == 0, "whole iterations per half tile");
+  constexpr int G = D / 32, N = HalfRegs<D, BITS>::N;
   int row, c;
   dq_lane<D, BITS>(t, row, c);
   const uint32_t kdst = smem_u32(smem + L::kOffK);
@@ -226,35 +216,35 @@ __device__ __forceinline__ bool dequant_piece(const CParams& p, uint8_t* smem, u
   const int64_t blocks = static_cast<int64_t>(p.c.pB) * (p.c.pT / 64);
   const int64_t coff = p.plane_off[w.kvh] + row * F::R + c * 16;
   const int64_t soff = w.kvh * blocks * (64 * G) + row * G + c * F::VPC / 32;
-  TileRows<PAGED> cur, next;
-  auto k_ptr = [&](const TileRows<PAGED>& r) { return PartPtr<D, BITS>(p, p.codes[0] + coff, p.sz[0] + soff, r.half[0], r.half[1]); };
-  auto v_ptr = [&](const TileRows<PAGED>& r) { return PartPtr<D, BITS>(p, p.codes[1] + coff, p.sz[1] + soff, r.half[0], r.half[1]); };
+  HalfTile<PAGED> cur, next;
+  HalfRegs<D, BITS> k, v;
+  auto load_k = [&]() { load_half<D, BITS>(p, k, p.codes[0] + coff, p.sz[0] + soff, cur.block); };
+  auto load_v = [&]() { load_half<D, BITS>(p, v, p.codes[1] + coff, p.sz[1] + soff, cur.block); };
   auto done = [&](int which) {
     fence_proxy_async_smem();
     __syncwarp();
     if (lane == 0) mbar_arrive(&bar[which]);
   };
-  PartRegs<D, BITS> ra, rb;
-  cur.look_up(p, w, 0);
-  next.look_up(p, w, min(1, w.n - 1));
+  cur.look_up(p, w, 0, x);
+  next.look_up(p, w, min(1, w.n - 1), x);
   cur.check(p, bad);
-  load_part<D, BITS>(ra, k_ptr(cur));
-  if (!fetch_queries<D>(p, smem_u32(smem + L::kOffQ), &bar[B_QEMPTY], w, t, piece)) return false;
+  load_k();
+  if (!fetch_queries<D>(p, smem_u32(smem + L::kOffQ), &bar[B_QEMPTY], w, x, t, piece)) return false;
   done(B_QREADY);
   for (int j = 0; j < w.n; ++j, ++jj) {
-    const uint32_t st = jj & 1;
-    load_part<D, BITS>(rb, v_ptr(cur));
+    const uint32_t st = jj & 1, dst = kdst + st * L::kQBytes;
+    load_v();
     const int t0 = cur.t0;
     next.check(p, bad);
     cur = next;
-    next.look_up(p, w, min(j + 2, w.n - 1));
+    next.look_up(p, w, min(j + 2, w.n - 1), x);
     if (jj >= 2 && !__all_sync(0xffffffffu, mbar_wait(&bar[B_KVEMPTY0 + st], ((jj >> 1) - 1) & 1, p.status, kWaitNs)))
       return false;
-    store_part<D, BITS>(kdst + st * L::kQBytes, ra, row, c);
+    store_half<D, BITS>(dst, k, x, row, c);
     done(B_KFULL0 + st);
-    if (j + 1 < w.n) load_part<D, BITS>(ra, k_ptr(cur));
-    store_part<D, BITS>(kdst + kToV + st * L::kQBytes, rb, row, c);
-    clear_unseen<D, BITS>(kdst + kToV + st * L::kQBytes, p, w, t0, row, c);
+    if (j + 1 < w.n) load_k();
+    store_half<D, BITS>(dst + kToV, v, x, row, c);
+    clear_unseen<D, BITS>(dst + kToV, p, w, t0, row, c, x * N, (x + 1) * N);
     done(B_VFULL0 + st);
   }
   return true;
@@ -357,11 +347,11 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_attention_kernel(const __gr
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
   if (threadIdx.x == 0) {
-    mbar_init(&bar[B_QREADY], 4);
+    mbar_init(&bar[B_QREADY], 8);
     mbar_init(&bar[B_QEMPTY], 3);   // both issuers, and warp 3
     for (int s = 0; s < 2; ++s) {
-      mbar_init(&bar[B_KFULL0 + s], 4);
-      mbar_init(&bar[B_VFULL0 + s], 4);
+      mbar_init(&bar[B_KFULL0 + s], 8);
+      mbar_init(&bar[B_VFULL0 + s], 8);
       mbar_init(&bar[B_KVEMPTY0 + s], 2);
       mbar_init(&bar[B_SFULL0 + s], 1);
       mbar_init(&bar[B_PFIRST0 + s], 4);
@@ -402,12 +392,12 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_attention_kernel(const __gr
   if (warp != 1) copy_walk(w, walks[1], lane);
   __syncthreads();   // (warp 1's walk goes on from here)
 
-  // Registers: launched with 128 per thread (checked on the host); per
-  // warpgroup 112 + 160 + 120 + 120 = 4 x 128 (of eight such splits the
-  // fastest: 861 us for 2048 tokens on 32K, 80 + 192 + 2 x 120 takes 910 us,
-  // 80 + 176 + 2 x 128 1064 us).
+  // Registers: launched with 96 per thread (checked on the host); per
+  // warpgroup 64 + 2 x 88 + 2 x 120 = 5 x 96 (of six such splits the fastest:
+  // 48 + 2 x 96 + 2 x 120 takes 1015 us for 2048 tokens on 32K, 72 + 2 x 80 +
+  // 2 x 120 911 us).
   if (warp < 4) {
-    tc::reg_dealloc<112>();
+    tc::reg_dealloc<64>();
     if (warp == 0) {
       // The other roles finish in bounded time: each stops at its first wait
       // that runs out, and a role waits at most a few times per tile.
@@ -565,15 +555,15 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_attention_kernel(const __gr
     return;
   }
 
-  if (warp < 8) {
-    tc::reg_alloc<160>();
-    // ---------------- dequant warpgroup ----------------
-    const int t = threadIdx.x - 128;
+  if (warp < 12) {
+    tc::reg_dealloc<88>();
+    // ---------------- dequant warpgroups: half x of the tiles, slot x's queries ----------------
+    const int x = (warp - 4) >> 2, t = threadIdx.x & 127;
     uint32_t jj = 0, piece = 0;
     bool ok, bad = false;
     do {
-      ok = p.bits[w.kvh] == 4 ? dequant_piece<D, 4, PAGED>(p, smem, bar, w, jj, piece, bad, t, lane)
-                              : dequant_piece<D, 8, PAGED>(p, smem, bar, w, jj, piece, bad, t, lane);
+      ok = p.bits[w.kvh] == 4 ? dequant_piece<D, 4, PAGED>(p, smem, bar, w, x, jj, piece, bad, t, lane)
+                              : dequant_piece<D, 8, PAGED>(p, smem, bar, w, x, jj, piece, bad, t, lane);
       ++piece;
     } while (ok && next_piece<kRows>(p, w, lane));
     if (bad) report(p.status, KVQ_ERR_INVALID_ARG);
@@ -583,8 +573,8 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_attention_kernel(const __gr
   }
 
   // ---------------- softmax warpgroups ----------------
-  tc::reg_dealloc<120>();
-  const int h = (warp - 8) >> 2;            // slot 0 or 1
+  tc::reg_alloc<120>();
+  const int h = (warp - 12) >> 2;           // slot 0 or 1
   const int q4 = warp & 3;                  // TMEM lane quarter
   const int r = q4 * 32 + lane;             // row within the slot
   const uint32_t lane_off = static_cast<uint32_t>(q4 * 32) << 16;
@@ -776,13 +766,13 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_attention_kernel(const __gr
       // one acquire-release atomic after the group's barrier: its release
       // covers the group's stores, its acquire the other pieces' (released by
       // their own arrivals) for the last arriver
-      if (threadIdx.x == 256 + h * kT)
+      if (threadIdx.x == 384 + h * kT)
         flag[h] = atom_add_acq_rel_gpu(p.cnt + 2 * cut.c0 + h, 1) + 1 == cut.c1 - cut.c0 + 1 ? 1 : 0;
       group_sync();
       if (!ok) break;
       if (flag[h] == 1) {
         if (live) merge_row<D>(p, cut, h * kT + r, orow);
-        if (threadIdx.x == 256 + h * kT) p.cnt[2 * cut.c0 + h] = 0;   // ready for the next call
+        if (threadIdx.x == 384 + h * kT) p.cnt[2 * cut.c0 + h] = 0;   // ready for the next call
       }
       group_sync();   // the flag has been read
       if (!ok) break;
@@ -795,7 +785,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_attention_kernel(const __gr
 }
 
 // Per device and instantiation, set once under a lock: the kernel's dynamic
-// shared-memory limit, and whether it was built with the 128 registers per
+// shared-memory limit, and whether it was built with the 96 registers per
 // thread that the register split above assumes.  1 = ready, -2 = not usable.
 std::mutex g_prep_mu;
 int g_prep[64][4] = {};
@@ -808,7 +798,7 @@ int prepare_on_current_device() {
   int& st = g_prep[dev][(D == 128 ? 1 : 0) + (PAGED ? 2 : 0)];
   if (st == 0) {
     cudaFuncAttributes fa;
-    if (cudaFuncGetAttributes(&fa, chunk_attention_kernel<D, PAGED>) != cudaSuccess || fa.numRegs != 128) {
+    if (cudaFuncGetAttributes(&fa, chunk_attention_kernel<D, PAGED>) != cudaSuccess || fa.numRegs != 96) {
       st = -2;
     } else if (cudaFuncSetAttribute(chunk_attention_kernel<D, PAGED>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                     static_cast<int>(CLayout<D>::bytes(4096))) != cudaSuccess) {
