@@ -38,11 +38,12 @@
 // 844 us = 1344 TFLOP/s, 72 % of a bf16 GEMM's burst rate -- 1.85 us a tile of
 // 256 rows, of which the products take 1.37 at that rate and the softmax's 2^x
 // 1.1, next to them; what is left is the chain between them.  Shorter pieces
-// add about 12 us each (first queries and codes, partials, merge): 16 sequences
-// of 1 to 286 new tokens on 1K to 8K, from pages, 187 us; 3500 tokens with a
-// window of 4096 on 55K to 84K, INT4, 236 us.  One dequant warpgroup for whole
-// tiles took 246 and 257 us (K's and V's loads of one thread wait for each
-// other), as did an L2 prefetch of the codes.
+// add about 10 us each (first queries and codes, partials, merge): 16 sequences
+// of 1 to 286 new tokens on 1K to 8K, from pages, 170 us; 3500 tokens with a
+// window of 4096 on 55K to 84K, INT4, 234 us.  One dequant warpgroup for whole
+// tiles took 246 and 257 us (a thread's loads of K and V wait for each other);
+// an L2 prefetch of the codes was slower, too.
+#include <algorithm>
 #include <cmath>
 #include <cstring>
 #include <mutex>
@@ -342,7 +343,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_attention_kernel(const __gr
   uint64_t* bar = reinterpret_cast<uint64_t*>(smem + L::kOffBar);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::kOffMisc);
   int32_t* flag = reinterpret_cast<int32_t*>(smem + L::kOffMisc) + 1;   // merge flags of the two slots
-  int32_t* pre = reinterpret_cast<int32_t*>(smem + L::kOffPre);         // tiles of sequences 0 .. b-1, per KV head
+  int32_t* pre = reinterpret_cast<int32_t*>(smem + L::kOffPre);         // units of sequences 0 .. b-1, per KV head
   Walk* walks = reinterpret_cast<Walk*>(smem + L::kOffWalk);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
@@ -369,13 +370,13 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_attention_kernel(const __gr
   grid_dependency_wait();
   grid_launch_dependents();
   if (blockIdx.x == 0) chunk::check_sequences(p.c, threadIdx.x, kThreads, p.status);
-  count_tiles<kRows>(p, pre, warp, lane, kThreads / 32);
+  count_units<kRows>(p, pre, warp, lane, kThreads / 32);
   __syncthreads();
   if (warp == 0) {
     tc::tmem_alloc(tmem_slot, kTmemCols);
     tc::tmem_relinquish();
   } else if (warp == 1) {
-    sum_tiles(p, pre, lane);
+    sum_units(p, pre, lane);
     start_walk<kRows>(p, pre, walks[1], lane);
   }
   tc::fence_before_sync();
@@ -728,7 +729,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_attention_kernel(const __gr
     tc::fence_after_sync();
     const float inv = l_run > 0.0f ? 1.0f / l_run : 0.0f;
     const bool whole = w.n == w.t.n;
-    const Cut cut(w);
+    const Cut cut(w, kLead<kRows>);
     const int part = cut.partial(blockIdx.x);
     const int64_t orow = out_offset(p, w, R, D);
 #pragma unroll
@@ -866,9 +867,9 @@ kvq_status launch_chunk_attention(const ChunkAttnArgs& a, cudaStream_t stream) {
   p.window = a.window; p.sinks = a.sinks;
   p.num_ctas = device_sm_count();
   p.slot_rows = slot_rows(a.chunk.rows, p.rep);
-  // tiles of all sequences (one KV head) are counted in 32 bits
+  // units of all sequences (one KV head) are counted in 32 bits
   const int64_t blocks = static_cast<int64_t>(a.chunk.rows) * p.rep / kRows + a.chunk.B;
-  if (blocks * (a.chunk.cap / kT + 1) >= (int64_t(1) << 31)) return KVQ_ERR_UNSUPPORTED;
+  if (blocks * (a.chunk.cap / kT + 1 + std::max(kLead<kRows>, kLead<16>)) >= (int64_t(1) << 31)) return KVQ_ERR_UNSUPPORTED;
   uint8_t* ws = static_cast<uint8_t*>(a.ws);
   p.cnt = reinterpret_cast<int32_t*>(ws);
   p.ws_lse = reinterpret_cast<float*>(ws + counter_bytes(p.num_ctas));

@@ -78,7 +78,7 @@ struct NLayout {
   static constexpr int kOffPre = kOffWalk + kThreads / 32 * 128;
   static constexpr size_t bytes(int B) { return 1024 + kOffPre + static_cast<size_t>(B + 1) * 4; }
 };
-constexpr int kMaxB = 2048;            // sequences (their tile counts lie in shared memory)
+constexpr int kMaxB = 2048;            // sequences (their unit counts lie in shared memory)
 static_assert(NLayout<128, 32>::bytes(kMaxB) <= 232448, "shared memory");
 static_assert(32 * 128 * 4 <= kT * 128, "a piece's output rows fit the P tile");
 
@@ -306,13 +306,13 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_narrow_kernel(const __grid_
   grid_dependency_wait();
   grid_launch_dependents();
   if (blockIdx.x == 0) chunk::check_sequences(p.c, threadIdx.x, kThreads, p.status);
-  count_tiles<NR>(p, pre, warp, lane, kThreads / 32);
+  count_units<NR>(p, pre, warp, lane, kThreads / 32);
   __syncthreads();
   if (warp == 0) {
     tc::tmem_alloc(tmem_slot, kCols);
     tc::tmem_relinquish();
   } else if (warp == 1) {
-    sum_tiles(p, pre, lane);
+    sum_units(p, pre, lane);
     start_walk<NR>(p, pre, walks[1], lane);
   }
   tc::fence_before_sync();
@@ -673,7 +673,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_narrow_kernel(const __grid_
     tc::fence_after_sync();
     const int rows = w.t.rows;
     const bool whole = n == w.t.n, four = p.bits[w.kvh] == 4;
-    const Cut cut(w);
+    const Cut cut(w, kLead<NR>);
     const int part = cut.partial(blockIdx.x);
     // a row's factors of the two O^T, each in its state's row_a
     if (key < NR) {
@@ -790,9 +790,11 @@ kvq_status launch_n(const CParams& p, cudaStream_t stream) {
 }  // namespace
 
 // At most 32 rows: with 64 columns a softmax thread's scores and sums do not fit
-// its registers, and the 256-row kernel is faster (eight sequences of 8000
-// tokens, 16 rows: 44 us here, 82 there; 32 rows: 60 and 78 with 4-bit heads;
-// 64 rows: 108 and 79).
+// its registers.  Against the 256-row kernel (eight sequences, 8 KV heads, INT8):
+// 16 rows on 200, 2000, 8000, 32000 tokens 14, 27, 44, 122 us to its 15, 36, 67,
+// 187; 32 rows 19, 40, 59, 150 us to its 15, 35, 66, 186 (shorter than about 4K
+// it would be the faster one; the host does not know the lengths); 64 rows on
+// 8000 tokens 108 us to its 66.
 bool chunk_narrow_takes(int B, int64_t max_rows) { return B <= kMaxB && max_rows <= 32; }
 
 kvq_status launch_chunk_narrow(const CParams& p, int D, int64_t max_rows, cudaStream_t stream) {

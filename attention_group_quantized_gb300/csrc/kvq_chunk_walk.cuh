@@ -3,7 +3,10 @@
 // contiguous ranges, one per CTA ("stream-K"), so that ragged lengths and few
 // rows over a long cache load every SM alike.  A segment is a row block (ROWS
 // packed rows, token * rep + head) of one (sequence, KV head); the run of a
-// segment's tiles inside one CTA's range is a piece.
+// segment's tiles inside one CTA's range is a piece.  The ranges are equal in
+// units: a unit per tile, and kLead<ROWS> before each segment's first for what
+// a segment costs whatever its length (queries, first codes, output) -- with
+// equal tiles alone, CTAs of many short segments finished last.
 #pragma once
 
 #include <cstdint>
@@ -37,6 +40,12 @@ struct CParams {
   int8_t bits[KVQ_MAX_HKV];
 };
 
+// (0, 2, 3, 4, 6 measured in the 256-row kernel for 16 sequences of 1 to 286 new
+// tokens: 189, 172, 170, 170, 171 us; 0, 2, 4, 6, 8 in the narrow one for 32
+// sequences of 1 to 4 new tokens on 100 to 6000: 84, 64, 59, 59, 59 us)
+template <int ROWS>
+constexpr int kLead = ROWS == 256 ? 4 : 6;
+
 // A segment's key tiles: those that some row of the block sees, in order.
 // Index i of the list is tile (i < ns ? i : i + skip).
 struct Tiles {
@@ -69,31 +78,35 @@ __device__ __forceinline__ int row_blocks(const CParams& p, const chunk::Seq& s)
 // A warp's walk through its CTA's range of the work list, piece by piece.  It
 // lives in shared memory: the roles' loops need their registers.
 struct Walk {
-  int64_t f;             // flat index of the piece's first tile
-  int64_t left;          // tiles of the range from there on
+  int64_t left;          // units of the range from the piece's first on
+  int64_t seg;           // the first unit of the piece's segment
   int b, kvh, rt, i;     // the piece starts at tile index i of this segment
   chunk::Seq s;
   Tiles t;
-  int n;                 // tiles of the piece
-  int C;                 // CTAs that share the N tiles of the work list
+  int n, units;          // tiles and units of the piece
+  int C;                 // CTAs that share the N units of the work list
   int64_t N;
 };
 static_assert(sizeof(Walk) <= 128, "room for a Walk per warp");
 
+// u: the piece's first unit within its segment.  A range that ends in a
+// segment's lead has no piece there.
 template <int ROWS>
-__device__ __forceinline__ void open_piece(const CParams& p, Walk& w) {
+__device__ __forceinline__ void open_piece(const CParams& p, Walk& w, int u) {
   w.t = segment_tiles<ROWS>(p, w.s, w.rt);
-  w.n = static_cast<int>(min(static_cast<int64_t>(w.t.n - w.i), w.left));
+  w.units = static_cast<int>(min(static_cast<int64_t>(w.t.n + kLead<ROWS> - u), w.left));
+  w.i = max(u - kLead<ROWS>, 0);
+  w.n = u + w.units - kLead<ROWS> - w.i;
+  if (w.n <= 0) w.left = 0;
 }
 // To the next piece (the whole warp; lane 0 does it); false at the range's end.
 template <int ROWS>
 __device__ __forceinline__ bool next_piece(const CParams& p, Walk& w, int lane) {
   __syncwarp();
   if (lane == 0) {
-    w.left -= w.n;
-    w.f += w.n;
+    w.left -= w.units;
+    w.seg += w.t.n + kLead<ROWS>;   // (a piece with another after it ends its segment)
     if (w.left > 0) {
-      w.i = 0;
       if (++w.rt >= row_blocks<ROWS>(p, w.s)) {
         w.rt = 0;
         if (++w.kvh >= p.Hkv) {
@@ -104,7 +117,7 @@ __device__ __forceinline__ bool next_piece(const CParams& p, Walk& w, int lane) 
           } while (w.s.n == 0);
         }
       }
-      open_piece<ROWS>(p, w);
+      open_piece<ROWS>(p, w, 0);
     }
   }
   __syncwarp();
@@ -124,28 +137,28 @@ __device__ __forceinline__ int64_t out_offset(const CParams& p, const Walk& w, i
   return ((static_cast<int64_t>(w.s.row0) + tok) * p.Hq + w.kvh * p.rep + hh) * D;
 }
 
-// Tiles of a sequence for one KV head (the whole warp, a lane per row block).
+// Units of a sequence for one KV head (the whole warp, a lane per row block).
 template <int ROWS>
-__device__ __forceinline__ int32_t sequence_tiles(const CParams& p, const chunk::Seq& s, int lane) {
+__device__ __forceinline__ int32_t sequence_units(const CParams& p, const chunk::Seq& s, int lane) {
   const int nrt = row_blocks<ROWS>(p, s);
   int32_t n = 0;
-  for (int rt = lane; rt < nrt; rt += 32) n += segment_tiles<ROWS>(p, s, rt).n;
+  for (int rt = lane; rt < nrt; rt += 32) n += segment_tiles<ROWS>(p, s, rt).n + kLead<ROWS>;
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) n += __shfl_xor_sync(0xffffffffu, n, o);
   return n;
 }
 
-// pre[b + 1] = tiles of sequence b for one KV head: a warp per sequence.
+// pre[b + 1] = units of sequence b for one KV head: a warp per sequence.
 template <int ROWS>
-__device__ __forceinline__ void count_tiles(const CParams& p, int32_t* pre, int warp, int lane, int warps) {
+__device__ __forceinline__ void count_units(const CParams& p, int32_t* pre, int warp, int lane, int warps) {
   for (int b = warp; b < p.c.B; b += warps) {
-    const int32_t n = sequence_tiles<ROWS>(p, chunk::sequence(p.c, b), lane);
+    const int32_t n = sequence_units<ROWS>(p, chunk::sequence(p.c, b), lane);
     if (lane == 0) pre[b + 1] = n;
   }
 }
 
-// The counts' prefix sums in place: pre[b] = tiles of sequences 0 .. b - 1 (one warp).
-__device__ __forceinline__ void sum_tiles(const CParams& p, int32_t* pre, int lane) {
+// The counts' prefix sums in place: pre[b] = units of sequences 0 .. b - 1 (one warp).
+__device__ __forceinline__ void sum_units(const CParams& p, int32_t* pre, int lane) {
   int32_t carry = 0;
   for (int b0 = 0; b0 < p.c.B; b0 += 32) {
     int32_t n = b0 + lane < p.c.B ? pre[b0 + lane + 1] : 0;
@@ -170,8 +183,8 @@ __device__ __forceinline__ int64_t mul_div(int64_t a, int64_t b, int64_t c) {
 }
 
 // Opens the first piece of this CTA's range [N c / C, N (c + 1) / C) of the N
-// tiles (one warp; never more CTAs than tiles in the split).  w.left is the
-// range's length, 0 for a CTA outside the split.  The other warps copy w
+// units (one warp; never more CTAs than units in the split).  w.left is the
+// range's length, 0 for a CTA without a piece.  The other warps copy w
 // (copy_walk): computed by all of them it took 1.8 us of a CTA's start.
 template <int ROWS>
 __device__ __forceinline__ void start_walk(const CParams& p, const int32_t* pre, Walk& w, int lane) {
@@ -183,7 +196,7 @@ __device__ __forceinline__ void start_walk(const CParams& p, const int32_t* pre,
     return;
   }
   const int64_t f0 = mul_div(N, blockIdx.x, C), total = mul_div(N, blockIdx.x + 1, C) - f0;
-  int lo = 0, hi = p.c.B - 1;   // the last b with Hkv * pre[b] <= f0: a sequence with tiles
+  int lo = 0, hi = p.c.B - 1;   // the last b with Hkv * pre[b] <= f0: a sequence with units
   while (lo < hi) {
     const int mid = (lo + hi + 1) >> 1;
     if (static_cast<int64_t>(p.Hkv) * pre[mid] <= f0) lo = mid; else hi = mid - 1;
@@ -197,7 +210,7 @@ __device__ __forceinline__ void start_walk(const CParams& p, const int32_t* pre,
   const int nrt = row_blocks<ROWS>(p, s);
   int rt = 0;
   for (int r0 = 0; nrt > 1 && r0 < nrt; r0 += 32) {
-    const int mine = r0 + lane < nrt ? segment_tiles<ROWS>(p, s, r0 + lane).n : 0;
+    const int mine = r0 + lane < nrt ? segment_tiles<ROWS>(p, s, r0 + lane).n + kLead<ROWS> : 0;
     int incl = mine;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -216,14 +229,13 @@ __device__ __forceinline__ void start_walk(const CParams& p, const int32_t* pre,
   if (lane == 0) {
     w.C = C;
     w.N = N;
-    w.f = f0;
+    w.seg = f0 - rem;
     w.left = total;
     w.b = lo;
     w.kvh = kvh;
     w.rt = rt;
-    w.i = rem;
     w.s = s;
-    open_piece<ROWS>(p, w);
+    open_piece<ROWS>(p, w, rem);
   }
   __syncwarp();
 }
@@ -235,21 +247,19 @@ __device__ __forceinline__ void copy_walk(Walk& to, const Walk& from, int lane) 
   __syncwarp();
 }
 
-// A cut segment: CTAs c0 .. c1 hold it.  A CTA's piece of it is partial 0 of
-// the CTA's two when the segment began before the CTA's range (or with it),
-// else 1.
+// A cut segment: CTAs c0 .. c1 hold its tiles.  A CTA's piece of it is partial
+// 0 of the CTA's two when it is the first of the CTA's range (which then began
+// in the segment, its lead at the earliest), else 1.
 struct Cut {
   int c0, c1, slot0;
   __device__ __forceinline__ static int owner(const Walk& w, int64_t f) {
-    const int64_t x = f * w.C + w.C - 1;
+    const int64_t x = f * w.C + w.C - 1;   // the CTA of unit f: floor(((f + 1) C - 1) / N)
     return static_cast<int>(mul_div(x, 1, w.N));
   }
-  __device__ __forceinline__ explicit Cut(const Walk& w) {
-    const int64_t seg0 = w.f - w.i;
-    // the CTA of tile f: floor(((f + 1) C - 1) / N) = floor((f C + C - 1) / N)
-    c0 = owner(w, seg0);
-    c1 = owner(w, seg0 + w.t.n - 1);
-    slot0 = seg0 <= mul_div(w.N, c0, w.C) ? 0 : 1;
+  __device__ __forceinline__ Cut(const Walk& w, int lead) {
+    c0 = owner(w, w.seg + lead);
+    c1 = owner(w, w.seg + lead + w.t.n - 1);
+    slot0 = w.seg <= mul_div(w.N, c0, w.C) ? 0 : 1;
   }
   __device__ __forceinline__ int partial(int c) const { return 2 * c + (c == c0 ? slot0 : 0); }
 };

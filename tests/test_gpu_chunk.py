@@ -706,6 +706,21 @@ def test_thousands_of_sequences(B):
     b.ok()
 
 
+@pytest.mark.parametrize("new", [(0, 3), (17, 40), (90, 150)], ids=["narrow", "one_slot", "two_slots"])
+@pytest.mark.parametrize("B", [1, 2, 9, 19, 38, 77])
+def test_batches_of_short_segments(B, new):
+    """Segments of one to four key tiles, from fewer than CTAs to several per CTA: ranges of the work list that begin
+    or end anywhere in a segment, or hold no tile at all."""
+    rng = np.random.default_rng(1000 * B + new[1])
+    b = Batch(73, 4, 2, 64, "84", [int(x) for x in rng.integers(new[0], new[1] + 1, B)],
+              [int(x) for x in rng.integers(0, 400, B)], B % 2 == 1)
+    b.fill()
+    b.append_new()
+    ref, bound = b.reference(window=0, sinks=0)
+    check(b.attend(U.to_dev_bf16(b.q), max_chunk=new[1]), ref, bound, False)
+    b.ok()
+
+
 def test_two_calls_at_once_on_two_streams():
     """Independent calls with workspaces of their own, overlapping: the bits of each call alone."""
     kvq = _kvq()
