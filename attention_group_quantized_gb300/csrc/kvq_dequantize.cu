@@ -9,6 +9,7 @@
 // its product with the fp16 scale (9 + 11 significant bits), so the only
 // rounding is the one to bf16.
 #include <algorithm>
+#include <type_traits>
 
 #include "kvq_chunk.cuh"
 #include "kvq_internal.h"
@@ -30,16 +31,17 @@ struct DqParams {
   int8_t bits[KVQ_MAX_HKV];
 };
 
-// 2^23 + c as an fp32 has c in its low byte
-__device__ __forceinline__ float biased(uint32_t c) { return __uint_as_float(0x4B000000u | c); }
-
-// The 8 values of a lane's codes: (c - z) s.
-__device__ __forceinline__ void values8(float (&x)[8], uint2 c, int bits, uint32_t word) {
+// The 8 values of a lane's codes: (c - z) s.  The fp32 with the bits
+// 0x4B0000cc is 2^23 + c, put together by one byte permute a value.
+template <int BITS>
+__device__ __forceinline__ void values8(float (&x)[8], uint2 c, uint32_t word) {
   const float zb = 8388608.0f + half_hi(word), s = half_lo(word);
+  const uint32_t lo = c.x & 0x0F0F0F0Fu, hi = (c.x >> 4) & 0x0F0F0F0Fu;   // (4-bit: even and odd channels)
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
-    const uint32_t code = bits == 8 ? ((i < 4 ? c.x : c.y) >> (8 * (i & 3))) & 0xFFu : (c.x >> (4 * i)) & 0xFu;
-    x[i] = (biased(code) - zb) * s;
+    const uint32_t w = BITS == 8 ? (i < 4 ? c.x : c.y) : (i & 1) ? hi : lo;
+    const int byte = BITS == 8 ? i & 3 : i >> 1;
+    x[i] = (__uint_as_float(prmt(w, 0x4B000000u, 0x7440u + byte)) - zb) * s;
   }
 }
 
@@ -87,26 +89,31 @@ __global__ void __launch_bounds__(kWarps * 32) dequantize_kernel(const __grid_co
       else c[k].x = *reinterpret_cast<const uint32_t*>(p.codes + off);
       word[k] = p.sz[si];
     }
+    auto finish = [&](auto bits_of) {
+      constexpr int BITS = decltype(bits_of)::value;
 #pragma unroll
-    for (int k = 0; k < NP; ++k) {
-      if (pos[k] == chunk::kNoRow) continue;
-      float x[8];
-      values8(x, c[k], bits, word[k]);
-      const int64_t o = (static_cast<int64_t>(r0 + k * RPP + lane / LPR) * p.Hkv + h) * D + col * 8;
-      if constexpr (F32) {
-        float4* dst = reinterpret_cast<float4*>(static_cast<float*>(p.out) + o);
-        dst[0] = make_float4(x[0], x[1], x[2], x[3]);
-        dst[1] = make_float4(x[4], x[5], x[6], x[7]);
-      } else {
-        uint32_t v[4];
+      for (int k = 0; k < NP; ++k) {
+        if (pos[k] == chunk::kNoRow) continue;
+        float x[8];
+        values8<BITS>(x, c[k], word[k]);
+        const int64_t o = (static_cast<int64_t>(r0 + k * RPP + lane / LPR) * p.Hkv + h) * D + col * 8;
+        if constexpr (F32) {
+          float4* dst = reinterpret_cast<float4*>(static_cast<float*>(p.out) + o);
+          dst[0] = make_float4(x[0], x[1], x[2], x[3]);
+          dst[1] = make_float4(x[4], x[5], x[6], x[7]);
+        } else {
+          uint32_t v[4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const __nv_bfloat162 b = __floats2bfloat162_rn(x[2 * i], x[2 * i + 1]);
-          v[i] = *reinterpret_cast<const uint32_t*>(&b);
+          for (int i = 0; i < 4; ++i) {
+            const __nv_bfloat162 b = __floats2bfloat162_rn(x[2 * i], x[2 * i + 1]);
+            v[i] = *reinterpret_cast<const uint32_t*>(&b);
+          }
+          *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.out) + o) = make_uint4(v[0], v[1], v[2], v[3]);
         }
-        *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.out) + o) = make_uint4(v[0], v[1], v[2], v[3]);
       }
-    }
+    };
+    if (bits == 8) finish(std::integral_constant<int, 8>{});
+    else finish(std::integral_constant<int, 4>{});
   }
 }
 
