@@ -70,27 +70,26 @@ __global__ void __launch_bounds__(kWarps * 32) dequantize_kernel(const __grid_co
     const int h = static_cast<int>(static_cast<uint32_t>(u) - static_cast<uint32_t>(tile) * p.Hkv);
     const int r0 = tile * R;
     const int64_t mine = chunk::locate_rows(p.c, r0, lane, R, h == 0, p.status);
-    const int bits = p.bits[h];
-    int64_t pos[NP];
-    uint2 c[NP];
-    uint32_t word[NP];
-#pragma unroll
-    for (int k = 0; k < NP; ++k) {
-      pos[k] = __shfl_sync(0xffffffffu, mine, k * RPP + lane / LPR);
-      c[k] = make_uint2(0u, 0u);
-      word[k] = 0u;                   // a page outside the pool reads as zeros
-      if (pos[k] < 0) continue;
-      const int64_t off = p.plane_off[h] + pos[k] * (D * bits / 8) + col * bits;
-      const int64_t si = (static_cast<int64_t>(h) * storage + pos[k]) * G + col / 4;
-      if (!KVQ_IN_RANGE(off >= 0 && off + bits <= p.codes_bytes && si < static_cast<int64_t>(p.Hkv) * storage * G,
-                        p.status))
-        continue;
-      if (bits == 8) c[k] = *reinterpret_cast<const uint2*>(p.codes + off);
-      else c[k].x = *reinterpret_cast<const uint32_t*>(p.codes + off);
-      word[k] = p.sz[si];
-    }
-    auto finish = [&](auto bits_of) {
+    auto rows = [&](auto bits_of) {
       constexpr int BITS = decltype(bits_of)::value;
+      int64_t pos[NP];
+      uint2 c[NP];
+      uint32_t word[NP];
+#pragma unroll
+      for (int k = 0; k < NP; ++k) {
+        pos[k] = __shfl_sync(0xffffffffu, mine, k * RPP + lane / LPR);
+        c[k] = make_uint2(0u, 0u);
+        word[k] = 0u;                   // a page outside the pool reads as zeros
+        if (pos[k] < 0) continue;
+        const int64_t off = p.plane_off[h] + pos[k] * (D * BITS / 8) + col * BITS;
+        const int64_t si = (static_cast<int64_t>(h) * storage + pos[k]) * G + col / 4;
+        if (!KVQ_IN_RANGE(off >= 0 && off + BITS <= p.codes_bytes && si < static_cast<int64_t>(p.Hkv) * storage * G,
+                          p.status))
+          continue;
+        if constexpr (BITS == 8) c[k] = *reinterpret_cast<const uint2*>(p.codes + off);
+        else c[k].x = *reinterpret_cast<const uint32_t*>(p.codes + off);
+        word[k] = p.sz[si];
+      }
 #pragma unroll
       for (int k = 0; k < NP; ++k) {
         if (pos[k] == chunk::kNoRow) continue;
@@ -112,8 +111,8 @@ __global__ void __launch_bounds__(kWarps * 32) dequantize_kernel(const __grid_co
         }
       }
     };
-    if (bits == 8) finish(std::integral_constant<int, 8>{});
-    else finish(std::integral_constant<int, 4>{});
+    if (p.bits[h] == 8) rows(std::integral_constant<int, 8>{});
+    else rows(std::integral_constant<int, 4>{});
   }
 }
 
