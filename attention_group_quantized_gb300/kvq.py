@@ -616,17 +616,38 @@ def _packed(x, heads: int, D: int, what: str):
         _bad(f"{what}: bf16 [rows][{heads}][{D}], channels contiguous")
 
 
-def _status_ptr(status):
-    return None if status is None else status.data_ptr()
+def _status_on(status, device: int):
+    if status is None:
+        return None
+    if status.dtype != _TORCH.int32 or status.get_device() != device:
+        _bad("status: int32 on the inputs' device")
+    return status.data_ptr()
 
 
-def _out(out, shape, out_dtype: int, like, what: str):
+def _made_on(stream, make, *args):
+    """make(*args) with `stream` current: what a call makes for itself is filled, and once freed used again, in the
+    order of the stream that the call runs on."""
+    if stream is None:
+        return make(*args)
+    with _torch().cuda.stream(stream):
+        return make(*args)
+
+
+def _workspace(workspace, device: int, stream, make, *args):
+    if workspace is None:
+        return _made_on(stream, make, *args)
+    if workspace.get_device() != device or not workspace.is_contiguous():
+        _bad("workspace: contiguous, on the inputs' device")
+    return workspace
+
+
+def _out(out, shape, out_dtype: int, like, what: str, stream):
     torch = _torch()
     if out_dtype != OUT_F32 and out_dtype != OUT_BF16:
         _bad(f"{what}: out_dtype")
     dt = torch.float32 if out_dtype == OUT_F32 else torch.bfloat16
     if out is None:
-        return torch.empty(shape, dtype=dt, device=like.device)
+        return _made_on(stream, lambda: torch.empty(shape, dtype=dt, device=like.device))
     if tuple(out.shape) != shape or out.dtype != dt or not out.is_contiguous() or out.get_device() != like.get_device():
         _bad(f"{what}: out must be contiguous {dt} {shape} on the inputs' device")
     return out
@@ -643,12 +664,12 @@ def _append_chunk(k_new, v_new, k: QuantCache, v: QuantCache, block_table, start
     s_row, s_head, _ = k_new.stride()
     if bt is None:
         st = lib().kvq_append_chunk(k_new.data_ptr(), v_new.data_ptr(), s_row, s_head, ch, k.c_struct(), v.c_struct(),
-                                    _status_ptr(status), _stream_on(stream, dev))
+                                    _status_on(status, dev), _stream_on(stream, dev))
         _check(st, "kvq_append_chunk")
     else:
         _on_current_device(block_table)
         st = lib().kvq_append_chunk_paged(k_new.data_ptr(), v_new.data_ptr(), s_row, s_head, ch, k.c_struct(),
-                                          v.c_struct(), bt, _status_ptr(status), _stream_on(stream, dev))
+                                          v.c_struct(), bt, _status_on(status, dev), _stream_on(stream, dev))
         _check(st, "kvq_append_chunk_paged")
 
 
@@ -667,15 +688,15 @@ def append_chunk_paged(k_new, v_new, k_pool: QuantCache, v_pool: QuantCache, blo
 def _dequantize(cache: QuantCache, block_table, start, seq_lens, rows: int, out, out_dtype, status, stream):
     bt = _block_table(block_table)
     dev = _on_current_device(cache.codes, start, seq_lens)
-    out = _out(out, (rows, cache.Hkv, cache.D), out_dtype, cache.codes, "dequantize")
+    out = _out(out, (rows, cache.Hkv, cache.D), out_dtype, cache.codes, "dequantize", stream)
     ch = _chunk(start, seq_lens, rows, None)
     if bt is None:
-        st = lib().kvq_dequantize(cache.c_struct(), ch, out.data_ptr(), out_dtype, _status_ptr(status),
+        st = lib().kvq_dequantize(cache.c_struct(), ch, out.data_ptr(), out_dtype, _status_on(status, dev),
                                   _stream_on(stream, dev))
         _check(st, "kvq_dequantize")
     else:
         _on_current_device(block_table)
-        st = lib().kvq_dequantize_paged(cache.c_struct(), ch, bt, out.data_ptr(), out_dtype, _status_ptr(status),
+        st = lib().kvq_dequantize_paged(cache.c_struct(), ch, bt, out.data_ptr(), out_dtype, _status_on(status, dev),
                                         _stream_on(stream, dev))
         _check(st, "kvq_dequantize_paged")
     return out
@@ -712,22 +733,23 @@ def _chunk_attention(q, k: QuantCache, v: QuantCache, block_table, start, seq_le
     _packed(q, Hq, k.D, "q")
     bt = _block_table(block_table)
     dev = _on_current_device(q, k.codes, v.codes, start, seq_lens)
-    out = _out(out, (rows, Hq, D), out_dtype, q, "chunk_attention")
-    if workspace is None:
-        workspace = chunk_workspace(rows, int(seq_lens.shape[0]), Hq, k.Hkv, D, q.device)
+    out = _out(out, (rows, Hq, D), out_dtype, q, "chunk_attention", stream)
+    workspace = _workspace(workspace, dev, stream, chunk_workspace, rows, int(seq_lens.shape[0]), Hq, k.Hkv, D,
+                           q.device)
     ch = _chunk(start, seq_lens, rows, max_chunk)
     s_row, s_head, _ = q.stride()
     ws_n = workspace.numel() * workspace.element_size()
     if bt is None:
         st = lib().kvq_chunk_attention(q.data_ptr(), s_row, s_head, ch, k.c_struct(), v.c_struct(), Hq, softmax_scale,
                                        window, sinks, out.data_ptr(), out_dtype, workspace.data_ptr(), ws_n,
-                                       _status_ptr(status), _stream_on(stream, dev))
+                                       _status_on(status, dev), _stream_on(stream, dev))
         _check(st, "kvq_chunk_attention")
     else:
         _on_current_device(block_table)
         st = lib().kvq_chunk_attention_paged(q.data_ptr(), s_row, s_head, ch, k.c_struct(), v.c_struct(), bt, Hq,
                                              softmax_scale, window, sinks, out.data_ptr(), out_dtype,
-                                             workspace.data_ptr(), ws_n, _status_ptr(status), _stream_on(stream, dev))
+                                             workspace.data_ptr(), ws_n, _status_on(status, dev),
+                                             _stream_on(stream, dev))
         _check(st, "kvq_chunk_attention_paged")
     return out
 
@@ -762,21 +784,21 @@ def _decode_window(q, k: QuantCache, v: QuantCache, block_table, seq_lens, windo
             or B != (k.B if bt is None else block_table.shape[0])):
         _bad("seq_lens: int32 [B]")
     dev = _on_current_device(q, k.codes, v.codes, seq_lens)
-    out = _out(out, (B, Hq, D), out_dtype, q, "decode_attention_window")
-    if workspace is None:
-        workspace = decode_workspace(B, Hq, k.Hkv, D, q.device)
+    out = _out(out, (B, Hq, D), out_dtype, q, "decode_attention_window", stream)
+    workspace = _workspace(workspace, dev, stream, decode_workspace, B, Hq, k.Hkv, D, q.device)
     ws_n = workspace.numel() * workspace.element_size()
     if bt is None:
         st = lib().kvq_decode_attention_window(q.data_ptr(), k.c_struct(), v.c_struct(), seq_lens.data_ptr(), Hq,
                                                softmax_scale, window, sinks, out.data_ptr(), out_dtype,
-                                               workspace.data_ptr(), ws_n, _status_ptr(status), _stream_on(stream, dev))
+                                               workspace.data_ptr(), ws_n, _status_on(status, dev),
+                                               _stream_on(stream, dev))
         _check(st, "kvq_decode_attention_window")
     else:
         _on_current_device(block_table)
         st = lib().kvq_decode_attention_window_paged(q.data_ptr(), k.c_struct(), v.c_struct(), bt,
                                                      seq_lens.data_ptr(), Hq, softmax_scale, window, sinks,
                                                      out.data_ptr(), out_dtype, workspace.data_ptr(), ws_n,
-                                                     _status_ptr(status), _stream_on(stream, dev))
+                                                     _status_on(status, dev), _stream_on(stream, dev))
         _check(st, "kvq_decode_attention_window_paged")
     return out
 

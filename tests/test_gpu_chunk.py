@@ -745,6 +745,56 @@ def test_two_calls_at_once_on_two_streams():
         assert all(torch.equal(a, x) for x in o)
 
 
+@pytest.mark.parametrize("op", ["narrow", "wide", "decode"])
+def test_what_a_call_makes_for_itself_belongs_to_its_stream(op):
+    """Without a workspace of the caller's, on another stream than the current one, which is busy: the workspace that
+    the call makes is zeroed in the order of the call's stream, over memory that held something else before."""
+    n = {"narrow": 4, "wide": 70, "decode": 1}[op]
+    b = Batch(90, 8, 2, 128, "84", [n, n], [900, 3000], False)
+    b.fill()
+    b.append_new()
+    q = U.to_dev_bf16(b.q if op != "decode" else b.q.reshape(2, 8, 128))
+    call = (lambda **kw: b.decode(q, 0, 0, **kw)) if op == "decode" else (lambda **kw: b.attend(q, max_chunk=n, **kw))
+    want = call()
+    b.ok()
+    side, busy = torch.cuda.Stream(), torch.randn((8192, 8192), device="cuda").bfloat16()
+    for s in (torch.cuda.current_stream(), side):       # freed blocks full of ones, of both streams
+        with torch.cuda.stream(s):
+            junk = [torch.full((m,), 255, dtype=torch.uint8, device="cuda") for m in (1 << 27, 1 << 20, 1 << 16)]
+            del junk
+    torch.cuda.synchronize()
+    for _ in range(20):
+        busy @ busy
+    got = call(stream=side)
+    side.synchronize()
+    assert torch.equal(got, want)
+    b.ok()
+
+
+def test_workspaces_and_status_words_elsewhere_are_refused():
+    kvq = _kvq()
+    b = Batch(91, 8, 2, 128, "84", [4, 1], [10, 20], True)
+    b.fill()
+    b.append_new()
+    q = U.to_dev_bf16(b.q)
+    ws = kvq.chunk_workspace(b.rows, b.B, 8, 2, 128)
+    cpu = torch.zeros(1, dtype=torch.int32)
+    one = U.to_dev_bf16(b.q[:2])
+    for bad in (dict(workspace=ws.cpu()), dict(workspace=ws[::2]), dict(status=cpu), dict(status=b.status.float())):
+        with pytest.raises(kvq.KvqError):
+            b.attend(q, **bad)
+    for bad in (dict(workspace=ws.cpu()), dict(workspace=ws[::2])):
+        with pytest.raises(kvq.KvqError):
+            b.decode(one, 5, 1, **bad)
+    with pytest.raises(kvq.KvqError):
+        kvq.decode_attention_window_paged(one, b.kc, b.vc, b.bt, b.d_lens, 5, 1, status=cpu)
+    with pytest.raises(kvq.KvqError):
+        kvq.dequantize_paged(b.kc, b.bt, b.d_start, b.d_lens, b.rows, status=cpu)
+    with pytest.raises(kvq.KvqError):
+        kvq.append_chunk_paged(one[:, :2], one[:, :2], b.kc, b.vc, b.bt, b.d_start, b.d_lens, status=cpu)
+    b.ok()
+
+
 def test_one_workspace_for_calls_of_different_shapes():
     """Calls of different rows, heads and widths, ordered on a stream, share one workspace (it stays zeroed where it
     has to be)."""
