@@ -35,14 +35,14 @@
 // 2^8; P is rounded to fp16, sums and O stay in fp32.
 //
 // Measured (32 query heads on 8, D = 128): 2048 tokens on 32K cached, INT8,
-// 844 us = 1344 TFLOP/s, 72 % of a bf16 GEMM's burst rate -- 1.85 us a tile of
+// 864 us = 1312 TFLOP/s, 70 % of a bf16 GEMM's burst rate -- 1.87 us a tile of
 // 256 rows, of which the products take 1.37 at that rate and the softmax's 2^x
 // 1.1, next to them; what is left is the chain between them.  Shorter pieces
 // add about 10 us each (first queries and codes, partials, merge): 16 sequences
 // of 1 to 286 new tokens on 1K to 8K, from pages, 170 us; 3500 tokens with a
 // window of 4096 on 55K to 84K, INT4, 234 us.  One dequant warpgroup for whole
-// tiles took 246 and 257 us (a thread's loads of K and V wait for each other);
-// an L2 prefetch of the codes was slower, too.
+// tiles took 246 and 257 us where the two took 187 and 236 (the loads of one
+// thread's K and V wait for each other); an L2 prefetch of the codes was slower.
 #include <algorithm>
 #include <cmath>
 #include <cstring>

@@ -26,10 +26,10 @@
 //                other's; rescaling, the piece's output or partial, the merge.
 // TMEM: S^T and O^T of each state, NR columns each.
 //
-// Measured: long contexts run at the rate of HBM's reads (eight sequences of
-// 32K, 16 rows: 0.96 us per 36 KB tile an SM, 4.7 TB/s over the call); a call
-// costs 10 us before its first tile and about 9 us for a segment's cut.
-// Fetching the codes into L2 further ahead was slower (54 us against 49 for
+// Measured: long contexts are bound by HBM's reads (eight sequences of 32K, 16
+// rows, INT8: 604 MB in 122 us, 4.8 TB/s over the call, 0.96 us per 36 KB tile an
+// SM); a call of one tile takes 10 us, and a segment's cut about 9 us (eight
+// sequences of 8K: 41 us).  Fetching the codes into L2 further ahead was slower (54 us against 49 for
 // eight sequences of 8K), and so were slots of 32 tokens (more copies).
 #include <cmath>
 #include <mutex>

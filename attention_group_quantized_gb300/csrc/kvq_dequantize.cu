@@ -47,8 +47,11 @@ __device__ __forceinline__ void values8(float (&x)[8], uint2 c, uint32_t word) {
 
 // NP: passes of 32 lanes whose loads are in flight together (NP x 256 / D rows
 // a warp).  Eight amortise the rows' look-up best when there are warps enough
-// (79 MB: 17.3 us, four 19.1); two spread a short call over more of them (5 MB:
-// 3.4 us, eight 3.8).
+// (eight against four: 17.3 and 19.1 us for 79 MB); two spread a short call over
+// more of them (two against eight: 3.4 and 3.8 us for 5 MB).  Since 8-bit and
+// 4-bit heads have paths of their own (one path took both widths' shifts for
+// every value) it is 14.9 us for the 79 MB of mixed heads, 5.3 TB/s, 16.4 us for
+// 88 MB of 4-bit ones, 5.4 TB/s, and 3.2 us for the 5 MB.
 template <int D, bool F32, int NP>
 __global__ void __launch_bounds__(kWarps * 32) dequantize_kernel(const __grid_constant__ DqParams p) {
   constexpr int G = D / 32;

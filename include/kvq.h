@@ -506,7 +506,8 @@ typedef struct kvq_chunk {
  *   fused projection's output can be passed in place.
  * k, v: caches with identical B, Hkv, Tcap, D and head_bits.
  * Positions other than the chunk's keep their contents.  Non-finite input as
- * in kvq_quantize.
+ * in kvq_quantize.  No two rows of a call may share a position (through pages
+ * that two sequences share).
  */
 KVQ_API kvq_status kvq_append_chunk(const void* k_new, const void* v_new, int64_t s_row, int64_t s_head,
                                     const kvq_chunk* chunk, const kvq_cache* k, const kvq_cache* v,
@@ -547,9 +548,17 @@ KVQ_API kvq_status kvq_dequantize_paged(const kvq_cache* pool, const kvq_chunk* 
  * out: device [rows][Hq][D], contiguous, 16-byte aligned, fp32 or bf16.
  * workspace: device scratch of >= kvq_chunk_workspace_bytes(rows, B, Hq, Hkv,
  *   D) bytes, with kvq_decode_attention's rules (16-byte aligned, zero-filled
- *   once before its first use, calls that share it ordered on the GPU).
+ *   once before its first use, calls that share it ordered on the GPU).  One
+ *   workspace serves chunk calls of every shape that fits it; it is not shared
+ *   with other kinds of calls.
  * Cache tokens that no query of the call sees are not read into the result
- * (they may hold anything).  Errors and other arguments as
+ * (they may hold anything).  Of those that only some rows of a sequence see,
+ * the values have to be finite in fp16, as the operands are (K_hat, V_hat and
+ * the weights are rounded to fp16 as in kvq_prefill_attention; scores, sums and
+ * outputs are fp32).  A call whose work list of 128-token tiles could reach
+ * 2^31 entries per KV head is KVQ_ERR_UNSUPPORTED.  The result depends on
+ * neither the order of the CTAs nor the call's place in a program: equal calls
+ * on equal devices give equal bits.  Errors and other arguments as
  * kvq_decode_attention.
  */
 KVQ_API size_t kvq_chunk_workspace_bytes(int32_t rows, int32_t B, int32_t Hq, int32_t Hkv, int32_t D);
