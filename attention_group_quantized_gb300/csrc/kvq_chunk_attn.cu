@@ -39,8 +39,8 @@
 // 256 rows, of which the products take 1.37 at that rate and the softmax's 2^x
 // 1.1, next to them; what is left is the chain between them.  Shorter pieces
 // add about 10 us each (first queries and codes, partials, merge): 16 sequences
-// of 1 to 286 new tokens on 1K to 8K, from pages, 170 us; 3500 tokens with a
-// window of 4096 on 55K to 84K, INT4, 234 us.  One dequant warpgroup for whole
+// of 1 to 286 new tokens on 1K to 8K, from pages, 172 us; 3500 tokens with a
+// window of 4096 on 55K to 84K, INT4, 237 us.  One dequant warpgroup for whole
 // tiles took 246 and 257 us where the two took 187 and 236 (the loads of one
 // thread's K and V wait for each other); an L2 prefetch of the codes was slower.
 #include <algorithm>
@@ -80,8 +80,9 @@ struct CLayout {
   static constexpr int kOffK = kOffQ + 2 * kQBytes;     // 2 stages
   static constexpr int kOffV = kOffK + 2 * kQBytes;     // 2 stages
   static constexpr int kOffBar = kOffV + 2 * kQBytes;
-  static constexpr int kOffMisc = kOffBar + B_COUNT * 8;  // TMEM address, merge flags
-  static constexpr int kOffWalk = kOffMisc + 16;          // Walk of each warp
+  static constexpr int kOffMisc = kOffBar + (B_COUNT + 1) / 2 * 16;  // TMEM address, merge flags
+  static constexpr int kOffSplit = kOffMisc + 16;         // Split
+  static constexpr int kOffWalk = kOffSplit + 16;          // Walk of each warp
   static constexpr int kOffPre = kOffWalk + kThreads / 32 * 128;   // int32 [B + 1]
   static size_t bytes(int B) { return 1024 + kOffPre + static_cast<size_t>(B + 1) * 4; }
 };
@@ -345,6 +346,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_attention_kernel(const __gr
   int32_t* flag = reinterpret_cast<int32_t*>(smem + L::kOffMisc) + 1;   // merge flags of the two slots
   int32_t* pre = reinterpret_cast<int32_t*>(smem + L::kOffPre);         // units of sequences 0 .. b-1, per KV head
   Walk* walks = reinterpret_cast<Walk*>(smem + L::kOffWalk);
+  Split& split = *reinterpret_cast<Split*>(smem + L::kOffSplit);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
   if (threadIdx.x == 0) {
@@ -366,18 +368,24 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_attention_kernel(const __gr
     mbar_init(&bar[B_EXIT], kExitArrivals);
     fence_barrier_init();
   }
+  // (before the dependency wait: the registers of two CTAs with TMEM do not fit
+  // an SM, so this never waits for a CTA that could wait for this kernel)
+  if (warp == 0) {
+    tc::tmem_alloc(tmem_slot, kTmemCols);
+    tc::tmem_relinquish();
+  }
   // the caches, queries and lengths may come from the kernel before this one
   grid_dependency_wait();
   grid_launch_dependents();
   if (blockIdx.x == 0) chunk::check_sequences(p.c, threadIdx.x, kThreads, p.status);
   count_units<kRows>(p, pre, warp, lane, kThreads / 32);
   __syncthreads();
-  if (warp == 0) {
-    tc::tmem_alloc(tmem_slot, kTmemCols);
-    tc::tmem_relinquish();
-  } else if (warp == 1) {
+  if (warp == 1) {
     sum_units(p, pre, lane);
-    start_walk<kRows>(p, pre, walks[1], lane);
+    start_walk<kRows>(p, pre, walks[1], split.N, lane);
+  } else if (warp == 2) {
+    const int longest = start_whole<kRows>(p, walks[2], lane);
+    if (lane == 0) split.longest = longest;
   }
   tc::fence_before_sync();
   __syncthreads();
@@ -385,13 +393,14 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_attention_kernel(const __gr
   const uint32_t tmem = *tmem_slot;
 
   Walk& w = walks[warp];
-  const int64_t total = walks[1].left;
+  const int from = split.whole<kRows>(p) ? 2 : 1;   // the warp whose split it is
+  const int64_t total = walks[from].left;
   if (total <= 0) {   // the whole CTA: nothing was started
     if (warp == 0) tc::tmem_dealloc(tmem, kTmemCols);
     return;
   }
-  if (warp != 1) copy_walk(w, walks[1], lane);
-  __syncthreads();   // (warp 1's walk goes on from here)
+  if (warp != from) copy_walk(w, walks[from], lane);
+  __syncthreads();   // (that warp's own walk goes on from here)
 
   // Registers: launched with 96 per thread (checked on the host); per
   // warpgroup 64 + 2 x 88 + 2 x 120 = 5 x 96 (of six such splits the fastest:

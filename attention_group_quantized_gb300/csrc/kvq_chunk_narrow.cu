@@ -74,7 +74,8 @@ struct NLayout {
   static constexpr int kOffBar = kOffRaw + 2 * kRing * kRawBytes;
   static constexpr int kOffMisc = kOffBar + B_COUNT * 8;     // TMEM address
   static constexpr int kOffRow = (kOffMisc + 16 + 15) / 16 * 16;   // per state and row: position, max, factor, four warps' values
-  static constexpr int kOffWalk = kOffRow + NR * 2 * 7 * 4;
+  static constexpr int kOffSplit = kOffRow + NR * 2 * 7 * 4;   // Split
+  static constexpr int kOffWalk = kOffSplit + 16;
   static constexpr int kOffPre = kOffWalk + kThreads / 32 * 128;
   static constexpr size_t bytes(int B) { return 1024 + kOffPre + static_cast<size_t>(B + 1) * 4; }
 };
@@ -276,6 +277,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_narrow_kernel(const __grid_
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::kOffMisc);
   int32_t* pre = reinterpret_cast<int32_t*>(smem + L::kOffPre);
   Walk* walks = reinterpret_cast<Walk*>(smem + L::kOffWalk);
+  Split& split = *reinterpret_cast<Split*>(smem + L::kOffSplit);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
   if (threadIdx.x == 0) {
@@ -302,31 +304,38 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_narrow_kernel(const __grid_
     }
     fence_barrier_init();
   }
+  // (before the dependency wait: the registers of two CTAs with TMEM do not fit
+  // an SM, so this never waits for a CTA that could wait for this kernel)
+  if (warp == 0) {
+    tc::tmem_alloc(tmem_slot, kCols);
+    tc::tmem_relinquish();
+  }
   // the caches, queries and lengths may come from the kernel before this one
   grid_dependency_wait();
   grid_launch_dependents();
   if (blockIdx.x == 0) chunk::check_sequences(p.c, threadIdx.x, kThreads, p.status);
   count_units<NR>(p, pre, warp, lane, kThreads / 32);
   __syncthreads();
-  if (warp == 0) {
-    tc::tmem_alloc(tmem_slot, kCols);
-    tc::tmem_relinquish();
-  } else if (warp == 1) {
+  if (warp == 1) {
     sum_units(p, pre, lane);
-    start_walk<NR>(p, pre, walks[1], lane);
+    start_walk<NR>(p, pre, walks[1], split.N, lane);
+  } else if (warp == 2) {
+    const int longest = start_whole<NR>(p, walks[2], lane);
+    if (lane == 0) split.longest = longest;
   }
   tc::fence_before_sync();
   __syncthreads();
   tc::fence_after_sync();
   const uint32_t tmem = *tmem_slot;
   Walk& w = walks[warp];
-  const int64_t total = walks[1].left;
+  const int from = split.whole<NR>(p) ? 2 : 1;   // the warp whose split it is
+  const int64_t total = walks[from].left;
   if (total <= 0) {   // the whole CTA: nothing was started
     if (warp == 0) tc::tmem_dealloc(tmem, kCols);
     return;
   }
-  if (warp != 1) copy_walk(w, walks[1], lane);
-  __syncthreads();   // (warp 1's walk goes on from here)
+  if (warp != from) copy_walk(w, walks[from], lane);
+  __syncthreads();   // (that warp's own walk goes on from here)
   auto wait_all = [&](int which, uint32_t parity) -> bool {
     return __all_sync(0xffffffffu, mbar_wait(&bar[which], parity & 1, p.status, kWaitNs));
   };

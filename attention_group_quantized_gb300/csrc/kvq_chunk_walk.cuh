@@ -182,13 +182,78 @@ __device__ __forceinline__ int64_t mul_div(int64_t a, int64_t b, int64_t c) {
   return ab / c;
 }
 
+// What cutting costs, in units of a CTA's share (partials, arrival, merge).
+// Measured with 64 segments of 16 rows on 100, 500, 1000, 2000, 3000 tokens: cut
+// 10.8, 15.3, 18.8, 23.0, 25.7 us, whole 10.2, 12.5, 16.3, 23.7, 31.3; of 120
+// rows on 100, 1000, 2000, 3000: cut 17.3, 29.3, 34.1, 39.8, whole 12.7, 23.8,
+// 34.8, 47.2.  With 14 the choice is the faster one, or within 3 % of it.
+constexpr int kCutCost = 14;
+
+// How the work was split (one per CTA, in shared memory).
+struct Split {
+  int64_t N;       // units of the work list
+  int longest;     // tiles of the longest segment when there is a CTA for each, else -1
+  template <int ROWS>
+  __device__ __forceinline__ bool whole(const CParams& p) const {
+    return longest >= 0 && static_cast<int64_t>(longest + kLead<ROWS> - kCutCost) * p.num_ctas <= N;
+  }
+};
+
+// Few short segments: a CTA each and none cut.  Opens this CTA's segment, if it
+// has one; the number of tiles of the longest, or -1 for more segments than CTAs
+// (one warp, while another one runs start_walk).
+template <int ROWS>
+__device__ __forceinline__ int start_whole(const CParams& p, Walk& w, int lane) {
+  if (p.c.B > p.num_ctas) return -1;
+  int segs = 0, longest = 0, my_b = -1, my_off = 0, my_nrt = 1;
+  for (int b0 = 0; b0 < p.c.B; b0 += 32) {
+    const int b = b0 + lane;
+    chunk::Seq s;
+    s.n = 0;
+    if (b < p.c.B) s = chunk::sequence(p.c, b);
+    const int nrt = row_blocks<ROWS>(p, s);
+    int incl = nrt;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int v = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += v;
+    }
+    const int off = static_cast<int>(blockIdx.x) - p.Hkv * (segs + incl - nrt);   // of this CTA in the sequence
+    if (off >= 0 && off < p.Hkv * nrt) {
+      my_b = b;
+      my_off = off;
+      my_nrt = nrt;
+    }
+    segs += __shfl_sync(0xffffffffu, incl, 31);
+    if (static_cast<int64_t>(segs) * p.Hkv > p.num_ctas) return -1;
+    for (int rt = 0; rt < nrt; ++rt) longest = max(longest, segment_tiles<ROWS>(p, s, rt).n);
+  }
+  if (lane == 0) w.left = 0;
+  __syncwarp();
+  if (my_b >= 0) {
+    w.C = 1;
+    w.N = 1;
+    w.seg = 0;
+    w.b = my_b;
+    w.kvh = my_off / my_nrt;
+    w.rt = my_off - w.kvh * my_nrt;
+    w.s = chunk::sequence(p.c, my_b);
+    w.left = int64_t(1) << 40;
+    open_piece<ROWS>(p, w, kLead<ROWS>);
+    w.left = w.units;
+  }
+  __syncwarp();
+  return __reduce_max_sync(0xffffffffu, longest);
+}
+
 // Opens the first piece of this CTA's range [N c / C, N (c + 1) / C) of the N
 // units (one warp; never more CTAs than units in the split).  w.left is the
 // range's length, 0 for a CTA without a piece.  The other warps copy w
 // (copy_walk): computed by all of them it took 1.8 us of a CTA's start.
 template <int ROWS>
-__device__ __forceinline__ void start_walk(const CParams& p, const int32_t* pre, Walk& w, int lane) {
+__device__ __forceinline__ void start_walk(const CParams& p, const int32_t* pre, Walk& w, int64_t& units, int lane) {
   const int64_t N = static_cast<int64_t>(p.Hkv) * pre[p.c.B];
+  if (lane == 0) units = N;
   const int C = N < p.num_ctas ? static_cast<int>(N) : p.num_ctas;
   if (static_cast<int>(blockIdx.x) >= C) {
     if (lane == 0) w.left = 0;
