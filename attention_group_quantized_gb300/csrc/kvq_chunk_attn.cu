@@ -384,8 +384,8 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_attention_kernel(const __gr
     sum_units(p, pre, lane);
     start_walk<kRows>(p, pre, walks[1], split.N, lane);
   } else if (warp == 2) {
-    const int longest = start_whole<kRows>(p, walks[2], lane);
-    if (lane == 0) split.longest = longest;
+    const int most = start_parts<kRows>(p, walks[2], lane);
+    if (lane == 0) split.most = most;
   }
   tc::fence_before_sync();
   __syncthreads();
@@ -393,7 +393,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_attention_kernel(const __gr
   const uint32_t tmem = *tmem_slot;
 
   Walk& w = walks[warp];
-  const int from = split.whole<kRows>(p) ? 2 : 1;   // the warp whose split it is
+  const int from = split.parts<kRows>(p) ? 2 : 1;   // the warp whose split it is
   const int64_t total = walks[from].left;
   if (total <= 0) {   // the whole CTA: nothing was started
     if (warp == 0) tc::tmem_dealloc(tmem, kTmemCols);

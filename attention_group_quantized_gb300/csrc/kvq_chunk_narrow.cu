@@ -320,15 +320,15 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_narrow_kernel(const __grid_
     sum_units(p, pre, lane);
     start_walk<NR>(p, pre, walks[1], split.N, lane);
   } else if (warp == 2) {
-    const int longest = start_whole<NR>(p, walks[2], lane);
-    if (lane == 0) split.longest = longest;
+    const int most = start_parts<NR>(p, walks[2], lane);
+    if (lane == 0) split.most = most;
   }
   tc::fence_before_sync();
   __syncthreads();
   tc::fence_after_sync();
   const uint32_t tmem = *tmem_slot;
   Walk& w = walks[warp];
-  const int from = split.whole<NR>(p) ? 2 : 1;   // the warp whose split it is
+  const int from = split.parts<NR>(p) ? 2 : 1;   // the warp whose split it is
   const int64_t total = walks[from].left;
   if (total <= 0) {   // the whole CTA: nothing was started
     if (warp == 0) tc::tmem_dealloc(tmem, kCols);

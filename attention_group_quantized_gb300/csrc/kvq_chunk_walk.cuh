@@ -84,7 +84,7 @@ struct Walk {
   chunk::Seq s;
   Tiles t;
   int n, units;          // tiles and units of the piece
-  int C;                 // CTAs that share the N units of the work list
+  int C;                 // CTAs that share the N units of the work list (N = 0: parts of the segment, start_parts)
   int64_t N;
 };
 static_assert(sizeof(Walk) <= 128, "room for a Walk per warp");
@@ -182,68 +182,91 @@ __device__ __forceinline__ int64_t mul_div(int64_t a, int64_t b, int64_t c) {
   return ab / c;
 }
 
-// What cutting costs, in units of a CTA's share (partials, arrival, merge).
-// Measured with 64 segments of 16 rows on 100, 500, 1000, 2000, 3000 tokens: cut
-// 10.8, 15.3, 18.8, 23.0, 25.7 us, whole 10.2, 12.5, 16.3, 23.7, 31.3; of 120
-// rows on 100, 1000, 2000, 3000: cut 17.3, 29.3, 34.1, 39.8, whole 12.7, 23.8,
-// 34.8, 47.2.  With 14 the choice is the faster one, or within 3 % of it.
-constexpr int kCutCost = 14;
+// Costs in units (about one tile's time).  kCutCost: what ranges that ignore the
+// segments' ends cost a CTA over one piece each (second pieces, partials,
+// merges); kJoinCost: what parts of a segment cost over all of it, kPartsSlack
+// more than that before they are preferred to such ranges; kMaxParts: with more
+// parts the ranges were as fast or faster.  Measured (us; ranges, whole
+// segments, parts), 64 segments of 16 rows on 500, 1000, 2000, 3000, 4000, 8000
+// tokens: 15.3 18.8 23.0 25.7 28.4 41.4, 12.5 16.3 23.7 31.3 38.8 69.7, - - 20.2
+// 23.9 27.7 43.0; of 120 rows on 100, 1000, 2000, 3000: 17.3 29.3 34.1 39.8, 12.7
+// 23.8 34.8 47.2, - 25.3 29.9 35.9; 8 segments of 256 rows on 2000 in 17 parts:
+// 50 against 53.
+constexpr int kCutCost = 14, kJoinCost = 4, kPartsSlack = 3, kMaxParts = 3;
 
 // How the work was split (one per CTA, in shared memory).
 struct Split {
   int64_t N;       // units of the work list
-  int longest;     // tiles of the longest segment when there is a CTA for each, else -1
+  int most;        // start_parts' tiles of a CTA, or -1
   template <int ROWS>
-  __device__ __forceinline__ bool whole(const CParams& p) const {
-    return longest >= 0 && static_cast<int64_t>(longest + kLead<ROWS> - kCutCost) * p.num_ctas <= N;
+  __device__ __forceinline__ bool parts(const CParams& p) const {
+    return most >= 0 && static_cast<int64_t>(most + kLead<ROWS> - kCutCost) * p.num_ctas <= N;
   }
 };
 
-// Few short segments: a CTA each and none cut.  Opens this CTA's segment, if it
-// has one; the number of tiles of the longest, or -1 for more segments than CTAs
-// (one warp, while another one runs start_walk).
+// No more segments than CTAs: an equal number m of CTAs for each, which take
+// equal parts of its tiles (m = 1 cuts none), so that every CTA has one piece at
+// most.  Opens this CTA's, if it has one; the tiles that a CTA has at most (with
+// m > 1 and what the parts cost), or -1 for more segments than CTAs (one warp,
+// while another one runs start_walk).
 template <int ROWS>
-__device__ __forceinline__ int start_whole(const CParams& p, Walk& w, int lane) {
+__device__ __forceinline__ int start_parts(const CParams& p, Walk& w, int lane) {
   if (p.c.B > p.num_ctas) return -1;
-  int segs = 0, longest = 0, my_b = -1, my_off = 0, my_nrt = 1;
-  for (int b0 = 0; b0 < p.c.B; b0 += 32) {
-    const int b = b0 + lane;
-    chunk::Seq s;
+  int segs = 0, longest = 0, nrt = 0;
+  chunk::Seq s;
+  auto look = [&](int b0) {
     s.n = 0;
-    if (b < p.c.B) s = chunk::sequence(p.c, b);
-    const int nrt = row_blocks<ROWS>(p, s);
+    if (b0 + lane < p.c.B) s = chunk::sequence(p.c, b0 + lane);
+    nrt = row_blocks<ROWS>(p, s);
+  };
+  for (int b0 = 0; b0 < p.c.B; b0 += 32) {
+    look(b0);
+    segs += __reduce_add_sync(0xffffffffu, nrt);
+    if (static_cast<int64_t>(segs) * p.Hkv > p.num_ctas) return -1;
+    for (int rt = 0; rt < nrt; ++rt) longest = max(longest, segment_tiles<ROWS>(p, s, rt).n);
+  }
+  if (lane == 0) w.left = 0;
+  __syncwarp();
+  if (segs == 0) return 0;
+  longest = __reduce_max_sync(0xffffffffu, longest);
+  int m = p.num_ctas / (segs * p.Hkv), most = (longest + m - 1) / m + kJoinCost;
+  if (m == 1 || m > kMaxParts || longest <= most) {
+    m = 1;
+    most = longest;
+  } else {
+    most += kPartsSlack;
+  }
+  // this CTA's segment, counted by sequence, KV head, row block
+  const int mine = blockIdx.x / m, part = blockIdx.x - mine * m;
+  for (int b0 = 0, before = 0; b0 < p.c.B; b0 += 32) {
+    if (p.c.B > 32) look(b0);
     int incl = nrt;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
       const int v = __shfl_up_sync(0xffffffffu, incl, o);
       if (lane >= o) incl += v;
     }
-    const int off = static_cast<int>(blockIdx.x) - p.Hkv * (segs + incl - nrt);   // of this CTA in the sequence
+    const int off = mine - p.Hkv * (before + incl - nrt);
     if (off >= 0 && off < p.Hkv * nrt) {
-      my_b = b;
-      my_off = off;
-      my_nrt = nrt;
+      w.b = b0 + lane;
+      w.s = s;
+      w.kvh = off / nrt;
+      w.rt = off - w.kvh * nrt;
+      w.t = segment_tiles<ROWS>(p, s, w.rt);
+      const int parts = min(m, w.t.n);
+      w.N = 0;                        // (see Cut)
+      w.C = parts;
+      w.seg = mine * m;
+      if (part < parts) {
+        w.i = static_cast<int>(mul_div(w.t.n, part, parts));
+        w.n = static_cast<int>(mul_div(w.t.n, part + 1, parts)) - w.i;
+        w.left = w.units = w.n;
+      }
     }
-    segs += __shfl_sync(0xffffffffu, incl, 31);
-    if (static_cast<int64_t>(segs) * p.Hkv > p.num_ctas) return -1;
-    for (int rt = 0; rt < nrt; ++rt) longest = max(longest, segment_tiles<ROWS>(p, s, rt).n);
-  }
-  if (lane == 0) w.left = 0;
-  __syncwarp();
-  if (my_b >= 0) {
-    w.C = 1;
-    w.N = 1;
-    w.seg = 0;
-    w.b = my_b;
-    w.kvh = my_off / my_nrt;
-    w.rt = my_off - w.kvh * my_nrt;
-    w.s = chunk::sequence(p.c, my_b);
-    w.left = int64_t(1) << 40;
-    open_piece<ROWS>(p, w, kLead<ROWS>);
-    w.left = w.units;
+    before += __shfl_sync(0xffffffffu, incl, 31);
   }
   __syncwarp();
-  return __reduce_max_sync(0xffffffffu, longest);
+  return most;
 }
 
 // Opens the first piece of this CTA's range [N c / C, N (c + 1) / C) of the N
@@ -322,6 +345,12 @@ struct Cut {
     return static_cast<int>(mul_div(x, 1, w.N));
   }
   __device__ __forceinline__ Cut(const Walk& w, int lead) {
+    if (w.N == 0) {   // start_parts: the CTAs from w.seg on have a part each
+      c0 = static_cast<int>(w.seg);
+      c1 = c0 + w.C - 1;
+      slot0 = 0;
+      return;
+    }
     c0 = owner(w, w.seg + lead);
     c1 = owner(w, w.seg + lead + w.t.n - 1);
     slot0 = w.seg <= mul_div(w.N, c0, w.C) ? 0 : 1;

@@ -692,6 +692,24 @@ def test_positions_past_32_bits_of_a_long_cache():
     check(one, ref[-1:], bound[-1:], False, "decode")
 
 
+@pytest.mark.parametrize("new,ctx,window", [(4, 2000, 0), (4, 4000, 0), (30, 2000, 0), (30, 3000, 1700), (70, 2500, 0)])
+def test_segments_in_equal_parts(new, ctx, window):
+    """Enough CTAs for two or three parts of each segment: ragged lengths, some sequences shorter than their parts,
+    single-tile parts, windows; equal calls give equal bits."""
+    kvq = _kvq()
+    B, Hq, Hkv, D = 6, 16, 8, 64
+    ctxs = [ctx, ctx - 300, 0, 100, ctx // 2, ctx - 1]
+    b = Batch(74, Hq, Hkv, D, "84848484", [new, new - 1, new, 1, new, new], ctxs, True)
+    b.fill()
+    b.append_new()
+    ref, bound = b.reference(window=window, sinks=3)
+    q, ws = U.to_dev_bf16(b.q), kvq.chunk_workspace(b.rows, B, Hq, Hkv, D)
+    outs = [b.attend(q, window=window, sinks=3, max_chunk=new, workspace=ws) for _ in range(3)]
+    check(outs[0], ref, bound, False)
+    assert torch.equal(outs[0], outs[1]) and torch.equal(outs[0], outs[2])
+    b.ok()
+
+
 @pytest.mark.parametrize("B", [2049, 4096])
 def test_thousands_of_sequences(B):
     """More sequences than the kernel for few rows has room for, and as many as the calls take; every seventh has no
