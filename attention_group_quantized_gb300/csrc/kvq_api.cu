@@ -707,6 +707,10 @@ static kvq_status chunk_desc(const kvq_chunk* c, const kvq_cache& storage, const
   return KVQ_OK;
 }
 
+// Whether a row buffer is there: a call of no rows needs none (an empty tensor
+// has no address).
+static bool rows_ok(const void* x, const kvq_chunk* c) { return x != nullptr || (c != nullptr && c->rows == 0); }
+
 static bool buffers_ok(const kvq_cache& c) {
   return c.codes != nullptr && c.sz != nullptr && aligned16(c.codes) && aligned16(c.sz);
 }
@@ -714,7 +718,7 @@ static bool buffers_ok(const kvq_cache& c) {
 static kvq_status append_chunk_impl(const void* k_new, const void* v_new, int64_t s_row, int64_t s_head,
                                     const kvq_chunk* chunk, const kvq_cache* k, const kvq_cache* v,
                                     const kvq_block_table* table, int32_t* dev_status, void* stream) {
-  if (k_new == nullptr || v_new == nullptr || k == nullptr || v == nullptr || !buffers_ok(*k) || !buffers_ok(*v))
+  if (!rows_ok(k_new, chunk) || !rows_ok(v_new, chunk) || k == nullptr || v == nullptr || !buffers_ok(*k) || !buffers_ok(*v))
     return KVQ_ERR_INVALID_ARG;
   if (k->D > 0 && k->D != 64 && k->D != 128) return KVQ_ERR_UNSUPPORTED;
   AppendChunkArgs a;
@@ -736,7 +740,7 @@ static kvq_status append_chunk_impl(const void* k_new, const void* v_new, int64_
 
 static kvq_status dequantize_impl(const kvq_cache* src, const kvq_chunk* chunk, const kvq_block_table* table,
                                   void* out, int32_t out_dtype, int32_t* dev_status, void* stream) {
-  if (src == nullptr || out == nullptr || !buffers_ok(*src)) return KVQ_ERR_INVALID_ARG;
+  if (src == nullptr || !rows_ok(out, chunk) || !buffers_ok(*src)) return KVQ_ERR_INVALID_ARG;
   if (src->D > 0 && src->D != 64 && src->D != 128) return KVQ_ERR_UNSUPPORTED;
   DequantizeArgs a;
   if (!resolve_layout(*src, &a.layout)) return KVQ_ERR_INVALID_ARG;
@@ -756,7 +760,8 @@ static kvq_status chunk_attention_impl(const void* q, int64_t sq_row, int64_t sq
                                        int32_t Hq, float softmax_scale, int32_t window, int32_t sinks, void* out,
                                        int32_t out_dtype, void* workspace, size_t workspace_bytes,
                                        int32_t* dev_status, void* stream) {
-  if (q == nullptr || k == nullptr || v == nullptr || out == nullptr || !buffers_ok(*k) || !buffers_ok(*v))
+  if (!rows_ok(q, chunk) || k == nullptr || v == nullptr || !rows_ok(out, chunk) || !buffers_ok(*k) ||
+      !buffers_ok(*v))
     return KVQ_ERR_INVALID_ARG;
   if (k->D > 0 && k->D != 64 && k->D != 128) return KVQ_ERR_UNSUPPORTED;
   ChunkAttnArgs a;

@@ -485,7 +485,8 @@ KVQ_API kvq_status kvq_prefill_attention_ex(const void* q, const void* k, const 
  * start[b + 1] > rows, n_b > max_chunk, seq_lens[b] < n_b or seq_lens[b]
  * beyond the cache's capacity reports KVQ_ERR_INVALID_ARG in dev_status and is
  * left out: nothing of it is read or written.
- * Rows that belong to no sequence (from start[B] on) are left as they are.
+ * Rows that belong to no sequence (from start[B] on) are left as they are.  A
+ * call with rows == 0 does nothing and needs no row buffers.
  */
 typedef struct kvq_chunk {
   const int32_t* start;      /* device int32 [B + 1], 4-byte aligned */

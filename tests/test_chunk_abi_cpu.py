@@ -60,6 +60,17 @@ def test_no_rows_is_nothing_to_do(L):
     assert L.kvq_chunk_attention(A, 1024, 128, P(ch), P(k), P(k), 8, 0.0, 0, 0, A, 0, A, 1 << 40, None, None) == 0
 
 
+def test_no_rows_need_no_row_buffers(L):
+    """An empty tensor has no address."""
+    k, ch = _cache(), _chunk(rows=0)
+    assert L.kvq_append_chunk(None, None, 256, 128, P(ch), P(k), P(k), None, None) == 0
+    assert L.kvq_dequantize(P(k), P(ch), None, 0, None, None) == 0
+    assert L.kvq_chunk_attention(None, 1024, 128, P(ch), P(k), P(k), 8, 0.0, 0, 0, None, 0, A, 1 << 40, None, None) == 0
+    pool, bt = _cache(B=9, Tcap=64), _table()
+    assert L.kvq_dequantize_paged(P(pool), P(ch), P(bt), None, 1, None, None) == 0
+    assert L.kvq_append_chunk(A, None, 256, 128, P(_chunk()), P(k), P(k), None, None) == 1
+
+
 def test_more_sequences_than_the_tables_hold(L):
     k, ch = _cache(B=4097), _chunk(B=4097)
     assert L.kvq_append_chunk(A, A, 256, 128, P(ch), P(k), P(k), None, None) == 2

@@ -789,6 +789,22 @@ def test_what_a_call_makes_for_itself_belongs_to_its_stream(op):
     b.ok()
 
 
+def test_a_step_without_new_rows():
+    """No sequence has a new token: empty tensors, nothing written, no error."""
+    kvq = _kvq()
+    b = Batch(92, 8, 2, 128, "84", [0, 0], [10, 70], False)
+    b.fill()
+    b.ok()
+    before = [(c.codes.clone(), c.sz.clone()) for c in (b.kc, b.vc)]
+    row = torch.empty((0, 2, 128), dtype=torch.bfloat16, device="cuda")
+    b.append(row, row, b.d_start, b.d_lens)
+    assert b.attend(torch.empty((0, 8, 128), dtype=torch.bfloat16, device="cuda")).shape == (0, 8, 128)
+    assert b.read("k", b.d_start, b.d_lens, 0).shape == (0, 2, 128)
+    b.ok()
+    for c, (codes, sz) in zip((b.kc, b.vc), before):
+        assert torch.equal(c.codes, codes) and torch.equal(c.sz, sz)
+
+
 def test_workspaces_and_status_words_elsewhere_are_refused():
     kvq = _kvq()
     b = Batch(91, 8, 2, 128, "84", [4, 1], [10, 20], True)
