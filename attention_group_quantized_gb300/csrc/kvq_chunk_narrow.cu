@@ -314,9 +314,12 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_narrow_kernel(const __grid_
   grid_dependency_wait();
   grid_launch_dependents();
   if (blockIdx.x == 0) chunk::check_sequences(p.c, threadIdx.x, kThreads, p.status);
+  const bool down = starts_descend(p, threadIdx.x, kThreads);
   count_units<NR>(p, pre, warp, lane, kThreads / 32);
-  __syncthreads();
-  if (warp == 1) {
+  const bool disorder = __syncthreads_or(down);   // (the units may be anything)
+  if (disorder) {
+    // nothing to do
+  } else if (warp == 1) {
     sum_units(p, pre, lane);
     start_walk<NR>(p, pre, walks[1], split.N, lane);
   } else if (warp == 2) {
@@ -328,8 +331,8 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_narrow_kernel(const __grid_
   tc::fence_after_sync();
   const uint32_t tmem = *tmem_slot;
   Walk& w = walks[warp];
-  const int from = split.parts<NR>(p) ? 2 : 1;   // the warp whose split it is
-  const int64_t total = walks[from].left;
+  const int from = !disorder && split.parts<NR>(p) ? 2 : 1;   // the warp whose split it is
+  const int64_t total = disorder ? 0 : walks[from].left;
   if (total <= 0) {   // the whole CTA: nothing was started
     if (warp == 0) tc::tmem_dealloc(tmem, kCols);
     return;

@@ -148,6 +148,15 @@ __device__ __forceinline__ int32_t sequence_units(const CParams& p, const chunk:
   return n;
 }
 
+// Whether the starts descend somewhere (each thread looks at some).  Sequences
+// that ascend share no row, so their rows are at most the call's; of others two
+// could write one row, and the units of all their rows could pass 32 bits.
+__device__ __forceinline__ bool starts_descend(const CParams& p, int tid, int nthr) {
+  bool down = false;
+  for (int b = tid; b < p.c.B; b += nthr) down |= p.c.start[b + 1] < p.c.start[b];
+  return down;
+}
+
 // pre[b + 1] = units of sequence b for one KV head: a warp per sequence.
 template <int ROWS>
 __device__ __forceinline__ void count_units(const CParams& p, int32_t* pre, int warp, int lane, int warps) {

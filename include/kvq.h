@@ -484,7 +484,9 @@ KVQ_API kvq_status kvq_prefill_attention_ex(const void* q, const void* k, const 
  * device.  A sequence with start[b] < 0, start[b + 1] < start[b],
  * start[b + 1] > rows, n_b > max_chunk, seq_lens[b] < n_b or seq_lens[b]
  * beyond the cache's capacity reports KVQ_ERR_INVALID_ARG in dev_status and is
- * left out: nothing of it is read or written.
+ * left out: nothing of it is read or written.  Where the starts descend, chunk
+ * attention leaves the whole call out, and the append and the read-back may
+ * leave out any of its sequences.
  * Rows that belong to no sequence (from start[B] on) are left as they are.  A
  * call with rows == 0 does nothing and needs no row buffers.
  */
