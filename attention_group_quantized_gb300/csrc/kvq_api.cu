@@ -759,12 +759,13 @@ static kvq_status chunk_attention_impl(const void* q, int64_t sq_row, int64_t sq
                                        const kvq_cache* k, const kvq_cache* v, const kvq_block_table* table,
                                        int32_t Hq, float softmax_scale, int32_t window, int32_t sinks, void* out,
                                        int32_t out_dtype, void* workspace, size_t workspace_bytes,
-                                       int32_t* dev_status, void* stream) {
+                                       int32_t* dev_status, void* stream, const kvq_policy* policy = nullptr) {
   if (!rows_ok(q, chunk) || k == nullptr || v == nullptr || !rows_ok(out, chunk) || !buffers_ok(*k) ||
       !buffers_ok(*v))
     return KVQ_ERR_INVALID_ARG;
   if (k->D > 0 && k->D != 64 && k->D != 128) return KVQ_ERR_UNSUPPORTED;
   ChunkAttnArgs a;
+  if (!resolve_policy(policy, &a.pol)) return KVQ_ERR_INVALID_ARG;
   if (!resolve_layout(*k, &a.layout) || !same_cache_shape(*k, *v)) return KVQ_ERR_INVALID_ARG;
   if (Hq <= 0 || Hq % k->Hkv || window < 0 || sinks < 0) return KVQ_ERR_INVALID_ARG;
   if (Hq / k->Hkv > 128) return KVQ_ERR_UNSUPPORTED;
@@ -844,6 +845,15 @@ kvq_status kvq_chunk_attention_paged(const void* q, int64_t sq_row, int64_t sq_h
   if (table == nullptr) return KVQ_ERR_INVALID_ARG;
   return chunk_attention_impl(q, sq_row, sq_head, chunk, k_pool, v_pool, table, Hq, softmax_scale, window, sinks, out,
                               out_dtype, workspace, workspace_bytes, dev_status, stream);
+}
+
+kvq_status kvq_chunk_attention_ex(const void* q, int64_t sq_row, int64_t sq_head, const kvq_chunk* chunk,
+                                  const kvq_cache* k, const kvq_cache* v, const kvq_block_table* table, int32_t Hq,
+                                  float softmax_scale, int32_t window, int32_t sinks, void* out, int32_t out_dtype,
+                                  void* workspace, size_t workspace_bytes, const kvq_policy* policy,
+                                  int32_t* dev_status, void* stream) {
+  return chunk_attention_impl(q, sq_row, sq_head, chunk, k, v, table, Hq, softmax_scale, window, sinks, out, out_dtype,
+                              workspace, workspace_bytes, dev_status, stream, policy);
 }
 
 kvq_status kvq_decode_attention_window(const void* q, const kvq_cache* k, const kvq_cache* v,

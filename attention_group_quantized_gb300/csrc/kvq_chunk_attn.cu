@@ -174,7 +174,7 @@ __device__ __forceinline__ bool fetch_queries(const CParams& p, uint32_t dst, ui
   constexpr int RPP = 128 / CPR;          // rows per pass
   const int ch = t % CPR, row = t / CPR;
   const int rows = w.t.rows - x * kT, end = rows > 0 ? kT : 0;   // the slot's
-  if (piece > 0 && !__all_sync(0xffffffffu, mbar_wait(empty, (piece - 1) & 1, p.status, kWaitNs))) return false;
+  if (piece > 0 && !__all_sync(0xffffffffu, mbar_wait(empty, (piece - 1) & 1, p.status, p.wait_ns))) return false;
   const uint16_t* base = p.q + static_cast<int64_t>(w.s.row0) * p.sq_row + w.kvh * p.rep * p.sq_head + ch * 8;
   const int R0 = w.rt * kRows + x * kT + row;   // token and head of this thread's row, stepped from pass to pass
   int tok = R0 / p.rep, hh = R0 - tok * p.rep;
@@ -234,13 +234,14 @@ __device__ __forceinline__ bool dequant_piece(const CParams& p, uint8_t* smem, u
   if (!fetch_queries<D>(p, smem_u32(smem + L::kOffQ), &bar[B_QEMPTY], w, x, t, piece)) return false;
   done(B_QREADY);
   for (int j = 0; j < w.n; ++j, ++jj) {
+    if (jj == p.issue_limit) return false;
     const uint32_t st = jj & 1, dst = kdst + st * L::kQBytes;
     load_v();
     const int t0 = cur.t0;
     next.check(p, bad);
     cur = next;
     next.look_up(p, w, min(j + 2, w.n - 1), x);
-    if (jj >= 2 && !__all_sync(0xffffffffu, mbar_wait(&bar[B_KVEMPTY0 + st], ((jj >> 1) - 1) & 1, p.status, kWaitNs)))
+    if (jj >= 2 && !__all_sync(0xffffffffu, mbar_wait(&bar[B_KVEMPTY0 + st], ((jj >> 1) - 1) & 1, p.status, p.wait_ns)))
       return false;
     store_half<D, BITS>(dst, k, x, row, c);
     done(B_KFULL0 + st);
@@ -414,7 +415,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_attention_kernel(const __gr
     if (warp == 0) {
       // The other roles finish in bounded time: each stops at its first wait
       // that runs out, and a role waits at most a few times per tile.
-      const uint64_t deadline = kWaitNs * static_cast<uint64_t>(8 * total + 16);
+      const uint64_t deadline = p.wait_ns * static_cast<uint64_t>(8 * min(total, int64_t(1) << 20) + 16) + 4 * kDrainNs;
       const uint64_t t0 = global_ns();
       uint32_t n = 0;
       while (!mbar_try_wait(&bar[B_EXIT], 0)) {
@@ -442,7 +443,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_attention_kernel(const __gr
           const int R = w.rt * kRows + r, tok = R / p.rep, hh = R - tok * p.rep;
           prefetch_l2_bulk(p.q + (w.s.row0 + tok) * p.sq_row + (w.kvh * p.rep + hh) * p.sq_head, D * 2);
         }
-        ok = __all_sync(0xffffffffu, mbar_wait(&bar[B_QREADY], piece & 1, p.status, kWaitNs));
+        ok = __all_sync(0xffffffffu, mbar_wait(&bar[B_QREADY], piece & 1, p.status, p.wait_ns));
         if (ok && lane == 0) mbar_arrive(&bar[B_QEMPTY]);
         ++piece;
       } while (ok && more);
@@ -458,7 +459,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_attention_kernel(const __gr
     const uint32_t v_base = smem_u32(smem + L::kOffV);
     const uint32_t d_s = tmem + h * 256, d_o = d_s + 128;
     auto wait_all = [&](int which, uint32_t parity) -> bool {
-      return __all_sync(0xffffffffu, mbar_wait(&bar[which], parity & 1, p.status, kWaitNs));
+      return __all_sync(0xffffffffu, mbar_wait(&bar[which], parity & 1, p.status, p.wait_ns));
     };
     auto issue_qk = [&](int st) {
       const uint32_t kh = k_base + st * L::kQBytes;
@@ -562,7 +563,8 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_attention_kernel(const __gr
     // pending arrives at once) before the warp reports that it is done
     if (tc::elect_one()) tc::commit(&bar[B_MMADONE]);
     __syncwarp();
-    wait_all(B_MMADONE, 0);
+    mbar_wait(&bar[B_MMADONE], 0, p.status, kDrainNs);
+    __syncwarp();
     tc::fence_before_sync();
     if (lane == 0) mbar_arrive(&bar[B_EXIT]);
     return;
@@ -600,7 +602,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_attention_kernel(const __gr
   auto group_sync = [&]() {
     __syncwarp();
     if (lane == 0) mbar_arrive(&bar[B_GROUP0 + h]);
-    ok = __all_sync(0xffffffffu, mbar_wait(&bar[B_GROUP0 + h], group & 1, p.status, kWaitNs)) && ok;
+    ok = __all_sync(0xffffffffu, mbar_wait(&bar[B_GROUP0 + h], group & 1, p.status, p.wait_ns)) && ok;
     ++group;
   };
   do {
@@ -619,7 +621,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_attention_kernel(const __gr
     for (int j = 0; j < w.n; ++j, ++sj) {
       const int t0 = w.t.tile(w.i + j) * kT;
       const bool masked = t0 > mask_from || (t0 < mask_below && t0 + kT > p.sinks);
-      ok = __all_sync(0xffffffffu, mbar_wait(&bar[B_SFULL0 + h], sj & 1, p.status, kWaitNs));
+      ok = __all_sync(0xffffffffu, mbar_wait(&bar[B_SFULL0 + h], sj & 1, p.status, p.wait_ns));
       if (!ok) break;
       tc::fence_after_sync();
       // the columns of 32-column chunk c that this row sees, one bit each:
@@ -678,7 +680,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_attention_kernel(const __gr
       }
       // rescale O (rare) before any P.V of this tile is issued
       if (__any_sync(0xffffffffu, alpha != 1.0f) && j > 0) {
-        ok = __all_sync(0xffffffffu, mbar_wait(&bar[B_ORDY0 + h], (sj - 1) & 1, p.status, kWaitNs));
+        ok = __all_sync(0xffffffffu, mbar_wait(&bar[B_ORDY0 + h], (sj - 1) & 1, p.status, p.wait_ns));
         if (!ok) break;
         tc::fence_after_sync();
 #pragma unroll
@@ -736,7 +738,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_attention_kernel(const __gr
     }
     if (!ok) break;
     // ---- end of the piece ----
-    ok = __all_sync(0xffffffffu, mbar_wait(&bar[B_ORDY0 + h], (sj - 1) & 1, p.status, kWaitNs));
+    ok = __all_sync(0xffffffffu, mbar_wait(&bar[B_ORDY0 + h], (sj - 1) & 1, p.status, p.wait_ns));
     if (!ok) break;
     tc::fence_after_sync();
     const float inv = l_run > 0.0f ? 1.0f / l_run : 0.0f;
@@ -877,6 +879,8 @@ kvq_status launch_chunk_attention(const ChunkAttnArgs& a, cudaStream_t stream) {
   p.status = a.status;
   p.out_dtype = a.out_dtype; p.Hq = a.Hq; p.Hkv = a.k->Hkv; p.rep = a.Hq / a.k->Hkv;
   p.window = a.window; p.sinks = a.sinks;
+  p.wait_ns = a.pol.wait_ns;
+  p.issue_limit = static_cast<uint32_t>(a.pol.issue_limit);   // (negative: more tiles than any call has)
   p.num_ctas = device_sm_count();
   p.slot_rows = slot_rows(a.chunk.rows, p.rep);
   // units of all sequences (one KV head) are counted in 32 bits

@@ -147,13 +147,13 @@ __device__ __forceinline__ bool dequant_piece(const CParams& p, uint8_t* smem, u
   for (int j = 0; j < w.n; ++j, ++jj) {
     const uint32_t st = jj & 1;
     if (jj >= 2 && !__all_sync(0xffffffffu, mbar_wait(&bar[B_EMPTY0 + 2 * which + st], ((jj >> 1) - 1) & 1, p.status,
-                                                      kWaitNs)))
+                                                      p.wait_ns)))
       return false;
     const uint32_t dst = smem_u32(smem + (which ? L::kOffV : L::kOffK) + st * L::kTile);
 #pragma unroll
     for (int s = 0; s < 2; ++s) {
       const int k = which * kRing + static_cast<int>(slot);
-      if (!__all_sync(0xffffffffu, mbar_wait(&bar[B_RAW0 + k], round & 1, p.status, kWaitNs))) return false;
+      if (!__all_sync(0xffffffffu, mbar_wait(&bar[B_RAW0 + k], round & 1, p.status, p.wait_ns))) return false;
       const bool mine = H > 1 || s == sub;
       const uint8_t* raw = smem + L::kOffRaw + k * L::kRawBytes;
       const uint4* codes = reinterpret_cast<const uint4*>(raw + row * F::R + c * 16);
@@ -340,8 +340,9 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_narrow_kernel(const __grid_
   if (warp != from) copy_walk(w, walks[from], lane);
   __syncthreads();   // (that warp's own walk goes on from here)
   auto wait_all = [&](int which, uint32_t parity) -> bool {
-    return __all_sync(0xffffffffu, mbar_wait(&bar[which], parity & 1, p.status, kWaitNs));
+    return __all_sync(0xffffffffu, mbar_wait(&bar[which], parity & 1, p.status, p.wait_ns));
   };
+  auto drain = [&](int which, uint32_t parity) { mbar_wait(&bar[which], parity & 1, p.status, kDrainNs); };
 
   // Registers: launched with 72 per thread (checked on the host); per
   // warpgroup 56 + 4 x 56 + 2 x 112 = 7 x 72.
@@ -381,10 +382,10 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_narrow_kernel(const __grid_
     } while (ok && next_piece<NR>(p, w, lane));
     if (tc::elect_one()) tc::commit(&bar[B_MMADONE0 + 1]);
     __syncwarp();
-    wait_all(B_MMADONE0 + 1, 0);
+    drain(B_MMADONE0 + 1, 0);
     // The other roles finish in bounded time: each stops at its first wait
     // that runs out, and a role waits at most a few times per tile.
-    const uint64_t deadline = kWaitNs * static_cast<uint64_t>(16 * total + 16);
+    const uint64_t deadline = p.wait_ns * static_cast<uint64_t>(16 * min(total, int64_t(1) << 20) + 16) + 4 * kDrainNs;
     const uint64_t t0 = global_ns();
     uint32_t n = 0;
     while (!mbar_try_wait(&bar[B_EXIT], 0)) {
@@ -435,7 +436,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_narrow_kernel(const __grid_
     // pending arrives at once) before the warp reports that it is done
     if (tc::elect_one()) tc::commit(&bar[B_MMADONE0]);
     __syncwarp();
-    wait_all(B_MMADONE0, 0);
+    drain(B_MMADONE0, 0);
     tc::fence_before_sync();
     if (lane == 0) mbar_arrive(&bar[B_EXIT]);
     return;
@@ -447,7 +448,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_narrow_kernel(const __grid_
     const int x = warp - 2;
     const int64_t blocks = static_cast<int64_t>(p.c.pB) * (p.c.pT / 64);
     const uint64_t pol = l2_evict_first_policy();
-    uint32_t slot = 0, round = 0;
+    uint32_t slot = 0, round = 0, tiles = 0;
     bool ok = true;
     do {
       const Seen seen(p, w);
@@ -457,6 +458,10 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_narrow_kernel(const __grid_
       const uint32_t* words = p.sz[x] + w.kvh * blocks * (64 * (D / 32));
       int half[2] = {0, 0};
       for (int j = 0; j < w.n && ok; ++j) {
+        if (tiles++ == p.issue_limit) {
+          ok = false;
+          break;
+        }
         if ((j & 31) == 0 && j + lane < w.n) {                     // 32 tiles' pages at a time, a lane each
           const int t0 = w.t.tile(w.i + j + lane) * kT;
 #pragma unroll
@@ -492,13 +497,11 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_narrow_kernel(const __grid_
         }
       }
     } while (ok && next_piece<NR>(p, w, lane));
-    // Every copy has landed before the CTA can exit: on the normal path the
-    // dequant warps have read them all; after a wait that ran out those in
-    // flight get a millisecond.
-    if (!ok) {
-      const uint64_t t0 = global_ns();
-      while (global_ns() - t0 < 1000000ull) {
-      }
+    // every copy has landed before the CTA can exit, whether or not the
+    // dequant warps got to read it: the last one into each slot
+    for (uint32_t k = 0; k < kRing; ++k) {
+      const uint32_t fills = round + (k < slot ? 1 : 0);
+      if (fills > 0) drain(B_RAW0 + x * kRing + static_cast<int>(k), fills - 1);
     }
     __syncwarp();
     if (lane == 0) mbar_arrive(&bar[B_EXIT]);

@@ -20,7 +20,9 @@ namespace chunk_walk {
 using tile::kT;
 
 constexpr float kRescaleThreshold = 8.0f;  // log2 units: the running max moves (and O is rescaled) beyond it
-constexpr uint64_t kWaitNs = kDefaultWaitLimitNs;
+// What a kernel waits for before it may end (its own products and copies in
+// flight) takes microseconds, and is given this long whatever the call's limit.
+constexpr uint64_t kDrainNs = kDefaultWaitLimitNs;
 
 struct CParams {
   chunk::View c;
@@ -36,6 +38,8 @@ struct CParams {
   int32_t out_dtype, Hq, Hkv, rep, window, sinks, num_ctas, slot_rows;
   float scale_log2;
   int64_t codes_bytes;              // size of each code buffer (the debug build's index checks)
+  uint64_t wait_ns;                 // bounded-wait limit
+  uint32_t issue_limit;             // test only: key tiles that a CTA makes ready before it stops
   int64_t plane_off[KVQ_MAX_HKV];
   int8_t bits[KVQ_MAX_HKV];
 };
@@ -442,7 +446,7 @@ __device__ __forceinline__ bool load_queries(const CParams& p, uint32_t dst, uin
         ++tok;
       }
     }
-    if (r0 == 0 && wait && !__all_sync(0xffffffffu, mbar_wait(empty, parity, p.status, kWaitNs))) return false;
+    if (r0 == 0 && wait && !__all_sync(0xffffffffu, mbar_wait(empty, parity, p.status, p.wait_ns))) return false;
 #pragma unroll
     for (int k = 0; k < NB; ++k) {
       const int r = r0 + k * RPP + t / CPR;

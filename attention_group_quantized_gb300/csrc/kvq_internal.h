@@ -26,7 +26,7 @@ struct Policy {
   int32_t ring = 4;               // decode: tiles in flight into shared memory (2 .. 4)
   int32_t l2_warm = 5;            // decode: tiles per CTA prefetched into L2 before the dependency wait
   uint64_t wait_ns = 2000000000ull;   // every bounded wait
-  int32_t issue_limit = -1;       // test only: tiles (decode) / Q loads (prefill) issued before stopping
+  int32_t issue_limit = -1;       // test only: tiles (decode, chunk) / Q loads (prefill) issued before stopping
 };
 
 struct QuantizeArgs {
@@ -119,6 +119,7 @@ struct ChunkAttnArgs {
   void* ws;
   size_t ws_bytes;
   int32_t* status;
+  Policy pol;
 };
 size_t chunk_workspace_bytes(int rows, int B, int Hq, int Hkv, int D);
 kvq_status launch_chunk_attention(const ChunkAttnArgs& a, cudaStream_t stream);

@@ -35,7 +35,7 @@ EXPORTS = ("kvq_cache_codes_bytes", "kvq_cache_sz_bytes", "kvq_cache_head_offset
            "kvq_build_tile_mask", "kvq_prefill_attention_varlen", "kvq_head_error_stats_workspace_bytes", "kvq_head_error_stats",
            "kvq_allocate_head_bits", "kvq_status_str", "kvq_policy_default", "kvq_decode_attention_ex",
            "kvq_prefill_attention_ex", "kvq_append_chunk", "kvq_append_chunk_paged", "kvq_dequantize",
-           "kvq_dequantize_paged", "kvq_chunk_workspace_bytes", "kvq_chunk_attention", "kvq_chunk_attention_paged",
+           "kvq_dequantize_paged", "kvq_chunk_workspace_bytes", "kvq_chunk_attention", "kvq_chunk_attention_paged", "kvq_chunk_attention_ex",
            "kvq_decode_attention_window", "kvq_decode_attention_window_paged")
 
 
@@ -137,6 +137,8 @@ def lib() -> ctypes.CDLL:
         L.kvq_chunk_attention.restype = I32
         L.kvq_chunk_attention_paged.argtypes = [P, I64, I64, P, CP, CP, P, I32, F32, I32, I32, P, I32, P, SZ, P, P]
         L.kvq_chunk_attention_paged.restype = I32
+        L.kvq_chunk_attention_ex.argtypes = [P, I64, I64, P, CP, CP, P, I32, F32, I32, I32, P, I32, P, SZ, PP, P, P]
+        L.kvq_chunk_attention_ex.restype = I32
         L.kvq_decode_attention_window.argtypes = [P, CP, CP, P, I32, F32, I32, I32, P, I32, P, SZ, P, P]
         L.kvq_decode_attention_window.restype = I32
         L.kvq_decode_attention_window_paged.argtypes = [P, CP, CP, P, P, I32, F32, I32, I32, P, I32, P, SZ, P, P]
@@ -726,7 +728,7 @@ def chunk_workspace(rows: int, B: int, Hq: int, Hkv: int, D: int, device="cuda")
 
 
 def _chunk_attention(q, k: QuantCache, v: QuantCache, block_table, start, seq_lens, softmax_scale, window, sinks, out,
-                     out_dtype, workspace, max_chunk, status, stream):
+                     out_dtype, workspace, max_chunk, status, stream, policy):
     if q.dim() != 3:
         _bad("q: bf16 [rows][Hq][D]")
     rows, Hq, D = q.shape
@@ -739,7 +741,15 @@ def _chunk_attention(q, k: QuantCache, v: QuantCache, block_table, start, seq_le
     ch = _chunk(start, seq_lens, rows, max_chunk)
     s_row, s_head, _ = q.stride()
     ws_n = workspace.numel() * workspace.element_size()
-    if bt is None:
+    if policy is not None:
+        if bt is not None:
+            _on_current_device(block_table)
+        st = lib().kvq_chunk_attention_ex(q.data_ptr(), s_row, s_head, ch, k.c_struct(), v.c_struct(), bt, Hq,
+                                          softmax_scale, window, sinks, out.data_ptr(), out_dtype,
+                                          workspace.data_ptr(), ws_n, ctypes.byref(policy), _status_on(status, dev),
+                                          _stream_on(stream, dev))
+        _check(st, "kvq_chunk_attention_ex")
+    elif bt is None:
         st = lib().kvq_chunk_attention(q.data_ptr(), s_row, s_head, ch, k.c_struct(), v.c_struct(), Hq, softmax_scale,
                                        window, sinks, out.data_ptr(), out_dtype, workspace.data_ptr(), ws_n,
                                        _status_on(status, dev), _stream_on(stream, dev))
@@ -756,21 +766,22 @@ def _chunk_attention(q, k: QuantCache, v: QuantCache, block_table, start, seq_le
 
 def chunk_attention(q, k: QuantCache, v: QuantCache, start, seq_lens, softmax_scale: float = 0.0, window: int = 0,
                     sinks: int = 0, out=None, out_dtype: int = OUT_F32, workspace=None,
-                    max_chunk: Optional[int] = None, status=None, stream=None):
+                    max_chunk: Optional[int] = None, status=None, stream=None, policy: Optional[CPolicy] = None):
     """Attention of packed new tokens q bf16 [rows][Hq][D] over caches that already hold them (append_chunk first);
     causal by cache position, optionally with a window of `window` tokens and the first `sinks` ones.
-    max_chunk: most rows of one sequence, if the caller knows it (chooses the kernel); returns [rows][Hq][D]."""
+    max_chunk: most rows of one sequence, if the caller knows it (chooses the kernel); returns [rows][Hq][D].
+    With a policy (see :func:`policy`) the call goes through kvq_chunk_attention_ex."""
     return _chunk_attention(q, k, v, None, start, seq_lens, softmax_scale, window, sinks, out, out_dtype, workspace,
-                            max_chunk, status, stream)
+                            max_chunk, status, stream, policy)
 
 
 def chunk_attention_paged(q, k_pool: QuantCache, v_pool: QuantCache, block_table, start, seq_lens,
                           softmax_scale: float = 0.0, window: int = 0, sinks: int = 0, out=None,
                           out_dtype: int = OUT_F32, workspace=None, max_chunk: Optional[int] = None, status=None,
-                          stream=None):
+                          stream=None, policy: Optional[CPolicy] = None):
     """chunk_attention over page pools through a block table."""
     return _chunk_attention(q, k_pool, v_pool, block_table, start, seq_lens, softmax_scale, window, sinks, out,
-                            out_dtype, workspace, max_chunk, status, stream)
+                            out_dtype, workspace, max_chunk, status, stream, policy)
 
 
 def _decode_window(q, k: QuantCache, v: QuantCache, block_table, seq_lens, window, sinks, softmax_scale, out,

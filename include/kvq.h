@@ -434,18 +434,20 @@ KVQ_API kvq_status kvq_decode_step_paged(const void* q, const void* k_new, const
  *   decode_l2_warm_tiles  tiles per CTA requested into L2 before the decode
  *                         waits for the previous kernel in the stream to
  *                         finish, 0 .. 16 (default 5).
- *   wait_limit_us         every bounded wait inside the decode and prefill
- *                         kernels gives up after this long and reports
- *                         KVQ_ERR_TIMEOUT in dev_status, 1 .. 60,000,000
- *                         (default 2,000,000 = 2 s).
+ *   wait_limit_us         every bounded wait inside the decode, prefill and
+ *                         chunk attention kernels gives up after this long
+ *                         and reports KVQ_ERR_TIMEOUT in dev_status,
+ *                         1 .. 60,000,000 (default 2,000,000 = 2 s).
  *   test_issue_limit      FOR TESTS OF THE TIMEOUT PATH ONLY; negative (the
  *                         default) = off.  Decode: each CTA's copy issuer
  *                         streams only its first test_issue_limit tiles, so
  *                         the waits for the rest run out.  Prefill: 0
  *                         withholds the query load, so every role's first
- *                         wait runs out (other values: no effect).  Nothing
- *                         is left in flight; the call reports KVQ_ERR_TIMEOUT
- *                         and its outputs are unspecified.
+ *                         wait runs out (other values: no effect).  Chunk
+ *                         attention: each CTA makes only its first
+ *                         test_issue_limit key tiles ready.  Nothing is left
+ *                         in flight; the call reports KVQ_ERR_TIMEOUT and its
+ *                         outputs are unspecified.
  * An out-of-range field returns KVQ_ERR_INVALID_ARG and launches nothing.
  */
 typedef struct kvq_policy {
@@ -578,6 +580,14 @@ KVQ_API kvq_status kvq_chunk_attention_paged(const void* q, int64_t sq_row, int6
                                              int32_t window, int32_t sinks, void* out, int32_t out_dtype,
                                              void* workspace, size_t workspace_bytes, int32_t* dev_status,
                                              void* stream);
+
+/* kvq_chunk_attention (table NULL) or kvq_chunk_attention_paged with a policy
+ * (NULL = kvq_policy_default; its decode fields have no effect here). */
+KVQ_API kvq_status kvq_chunk_attention_ex(const void* q, int64_t sq_row, int64_t sq_head, const kvq_chunk* chunk,
+                                          const kvq_cache* k, const kvq_cache* v, const kvq_block_table* table,
+                                          int32_t Hq, float softmax_scale, int32_t window, int32_t sinks, void* out,
+                                          int32_t out_dtype, void* workspace, size_t workspace_bytes,
+                                          const kvq_policy* policy, int32_t* dev_status, void* stream);
 
 /*
  * kvq_decode_attention_window -- kvq_decode_attention with a sliding window:
