@@ -26,13 +26,14 @@ struct View {
 // description is unusable, which `bad` tells), and its length.
 struct Seq {
   int32_t row0, n, len;
-  bool bad;
+  bool bad, down;   // down: it ends before it starts
 };
 __device__ __forceinline__ Seq sequence(const View& c, int b) {
   Seq s;
   s.row0 = c.start[b];
   const int32_t end = c.start[b + 1];
   s.len = c.seq_lens[b];
+  s.down = end < s.row0;
   s.bad = s.row0 < 0 || end < s.row0 || end > c.rows || s.len < 0 || s.len > c.cap;
   s.n = s.bad ? 0 : end - s.row0;
   if (s.n > s.len || s.n > c.max_chunk) {

@@ -222,19 +222,18 @@ __device__ __forceinline__ bool dequant_piece(const CParams& p, uint8_t* smem, u
   HalfRegs<D, BITS> k, v;
   auto load_k = [&]() { load_half<D, BITS>(p, k, p.codes[0] + coff, p.sz[0] + soff, cur.block); };
   auto load_v = [&]() { load_half<D, BITS>(p, v, p.codes[1] + coff, p.sz[1] + soff, cur.block); };
-  auto done = [&](int which) {
+  auto done = [&](int which, bool tell = true) {
     fence_proxy_async_smem();
     __syncwarp();
-    if (lane == 0) mbar_arrive(&bar[which]);
+    if (lane == 0 && tell) mbar_arrive(&bar[which]);
   };
   cur.look_up(p, w, 0, x);
   next.look_up(p, w, min(1, w.n - 1), x);
   cur.check(p, bad);
   load_k();
   if (!fetch_queries<D>(p, smem_u32(smem + L::kOffQ), &bar[B_QEMPTY], w, x, t, piece)) return false;
-  done(B_QREADY);
+  done(B_QREADY, piece < p.issue_limit);
   for (int j = 0; j < w.n; ++j, ++jj) {
-    if (jj == p.issue_limit) return false;
     const uint32_t st = jj & 1, dst = kdst + st * L::kQBytes;
     load_v();
     const int t0 = cur.t0;
@@ -379,9 +378,8 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_attention_kernel(const __gr
   grid_dependency_wait();
   grid_launch_dependents();
   if (blockIdx.x == 0) chunk::check_sequences(p.c, threadIdx.x, kThreads, p.status);
-  const bool down = starts_descend(p, threadIdx.x, kThreads);
-  count_units<kRows>(p, pre, warp, lane, kThreads / 32);
-  const bool disorder = __syncthreads_or(down);   // (the units may be anything)
+  // (starts that descend: the units may be anything)
+  const bool disorder = __syncthreads_or(count_units<kRows>(p, pre, warp, lane, kThreads / 32));
   if (disorder) {
     // nothing to do
   } else if (warp == 1) {
@@ -880,7 +878,7 @@ kvq_status launch_chunk_attention(const ChunkAttnArgs& a, cudaStream_t stream) {
   p.out_dtype = a.out_dtype; p.Hq = a.Hq; p.Hkv = a.k->Hkv; p.rep = a.Hq / a.k->Hkv;
   p.window = a.window; p.sinks = a.sinks;
   p.wait_ns = a.pol.wait_ns;
-  p.issue_limit = static_cast<uint32_t>(a.pol.issue_limit);   // (negative: more tiles than any call has)
+  p.issue_limit = static_cast<uint32_t>(a.pol.issue_limit);   // (negative: more pieces than any call has)
   p.num_ctas = device_sm_count();
   p.slot_rows = slot_rows(a.chunk.rows, p.rep);
   // units of all sequences (one KV head) are counted in 32 bits

@@ -314,9 +314,8 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_narrow_kernel(const __grid_
   grid_dependency_wait();
   grid_launch_dependents();
   if (blockIdx.x == 0) chunk::check_sequences(p.c, threadIdx.x, kThreads, p.status);
-  const bool down = starts_descend(p, threadIdx.x, kThreads);
-  count_units<NR>(p, pre, warp, lane, kThreads / 32);
-  const bool disorder = __syncthreads_or(down);   // (the units may be anything)
+  // (starts that descend: the units may be anything)
+  const bool disorder = __syncthreads_or(count_units<NR>(p, pre, warp, lane, kThreads / 32));
   if (disorder) {
     // nothing to do
   } else if (warp == 1) {
@@ -448,7 +447,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_narrow_kernel(const __grid_
     const int x = warp - 2;
     const int64_t blocks = static_cast<int64_t>(p.c.pB) * (p.c.pT / 64);
     const uint64_t pol = l2_evict_first_policy();
-    uint32_t slot = 0, round = 0, tiles = 0;
+    uint32_t slot = 0, round = 0;
     bool ok = true;
     do {
       const Seen seen(p, w);
@@ -458,10 +457,6 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_narrow_kernel(const __grid_
       const uint32_t* words = p.sz[x] + w.kvh * blocks * (64 * (D / 32));
       int half[2] = {0, 0};
       for (int j = 0; j < w.n && ok; ++j) {
-        if (tiles++ == p.issue_limit) {
-          ok = false;
-          break;
-        }
         if ((j & 31) == 0 && j + lane < w.n) {                     // 32 tiles' pages at a time, a lane each
           const int t0 = w.t.tile(w.i + j + lane) * kT;
 #pragma unroll
@@ -499,12 +494,15 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_narrow_kernel(const __grid_
     } while (ok && next_piece<NR>(p, w, lane));
     // every copy has landed before the CTA can exit, whether or not the
     // dequant warps got to read it: the last one into each slot
-    for (uint32_t k = 0; k < kRing; ++k) {
-      const uint32_t fills = round + (k < slot ? 1 : 0);
-      if (fills > 0) drain(B_RAW0 + x * kRing + static_cast<int>(k), fills - 1);
+    if (lane == 0) {
+#pragma unroll 1
+      for (uint32_t k = 0; k < kRing; ++k) {
+        const uint32_t fills = round + (k < slot ? 1 : 0);
+        if (fills > 0) drain(B_RAW0 + x * kRing + static_cast<int>(k), fills - 1);
+      }
+      mbar_arrive(&bar[B_EXIT]);
     }
     __syncwarp();
-    if (lane == 0) mbar_arrive(&bar[B_EXIT]);
     return;
   }
 
@@ -521,7 +519,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_narrow_kernel(const __grid_
         if (!ok) break;
         fence_proxy_async_smem();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&bar[B_QREADY]);
+        if (lane == 0 && piece < p.issue_limit) mbar_arrive(&bar[B_QREADY]);
       }
       ok = p.bits[w.kvh] == 4 ? dequant_piece<D, NR, 4>(p, smem, bar, w, which, sub, jj, slot, round, t, lane)
                               : dequant_piece<D, NR, 8>(p, smem, bar, w, which, sub, jj, slot, round, t, lane);

@@ -39,7 +39,7 @@ struct CParams {
   float scale_log2;
   int64_t codes_bytes;              // size of each code buffer (the debug build's index checks)
   uint64_t wait_ns;                 // bounded-wait limit
-  uint32_t issue_limit;             // test only: key tiles that a CTA makes ready before it stops
+  uint32_t issue_limit;             // test only: pieces whose queries a CTA makes ready
   int64_t plane_off[KVQ_MAX_HKV];
   int8_t bits[KVQ_MAX_HKV];
 };
@@ -152,22 +152,20 @@ __device__ __forceinline__ int32_t sequence_units(const CParams& p, const chunk:
   return n;
 }
 
-// Whether the starts descend somewhere (each thread looks at some).  Sequences
-// that ascend share no row, so their rows are at most the call's; of others two
-// could write one row, and the units of all their rows could pass 32 bits.
-__device__ __forceinline__ bool starts_descend(const CParams& p, int tid, int nthr) {
-  bool down = false;
-  for (int b = tid; b < p.c.B; b += nthr) down |= p.c.start[b + 1] < p.c.start[b];
-  return down;
-}
-
 // pre[b + 1] = units of sequence b for one KV head: a warp per sequence.
+// Returns whether the starts of this warp's sequences descend somewhere:
+// sequences that ascend share no row, so their rows are at most the call's; of
+// others two could write one row, and the units could pass 32 bits.
 template <int ROWS>
-__device__ __forceinline__ void count_units(const CParams& p, int32_t* pre, int warp, int lane, int warps) {
+__device__ __forceinline__ bool count_units(const CParams& p, int32_t* pre, int warp, int lane, int warps) {
+  bool down = false;
   for (int b = warp; b < p.c.B; b += warps) {
-    const int32_t n = sequence_units<ROWS>(p, chunk::sequence(p.c, b), lane);
+    const chunk::Seq s = chunk::sequence(p.c, b);
+    down |= s.down;
+    const int32_t n = sequence_units<ROWS>(p, s, lane);
     if (lane == 0) pre[b + 1] = n;
   }
+  return down;
 }
 
 // The counts' prefix sums in place: pre[b] = units of sequences 0 .. b - 1 (one warp).

@@ -444,10 +444,10 @@ KVQ_API kvq_status kvq_decode_step_paged(const void* q, const void* k_new, const
  *                         the waits for the rest run out.  Prefill: 0
  *                         withholds the query load, so every role's first
  *                         wait runs out (other values: no effect).  Chunk
- *                         attention: each CTA makes only its first
- *                         test_issue_limit key tiles ready.  Nothing is left
- *                         in flight; the call reports KVQ_ERR_TIMEOUT and its
- *                         outputs are unspecified.
+ *                         attention: each CTA makes only the queries of its
+ *                         first test_issue_limit pieces of work ready.
+ *                         Nothing is left in flight; the call reports
+ *                         KVQ_ERR_TIMEOUT and its outputs are unspecified.
  * An out-of-range field returns KVQ_ERR_INVALID_ARG and launches nothing.
  */
 typedef struct kvq_policy {
