@@ -153,6 +153,14 @@ __device__ __forceinline__ void store_half(uint32_t dst, const HalfRegs<D, BITS>
     dequant_chunk<BITS>(dst, F::RPI * (x * r.N + it) + row, c * F::VPC, r.c[it], r.w[it]);
 }
 
+template <int D, int BITS>
+__device__ __forceinline__ uint32_t max_word(const HalfRegs<D, BITS>& r) {
+  uint32_t m = r.w[0];
+#pragma unroll
+  for (int it = 1; it < r.N; ++it) m = __vmaxu2(m, r.w[it]);
+  return m;
+}
+
 // 16 bytes from global to shared memory without a register, zeros for n = 0.
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, uint32_t n) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
@@ -207,7 +215,8 @@ __device__ __forceinline__ bool fetch_queries(const CParams& p, uint32_t dst, ui
 // the CTA's tiles (stage jj & 1).  False after a wait that ran out.
 template <int D, int BITS, bool PAGED>
 __device__ __forceinline__ bool dequant_piece(const CParams& p, uint8_t* smem, uint64_t* bar, const Walk& w, int x,
-                                              uint32_t& jj, uint32_t piece, bool& bad, int t, int lane) {
+                                              uint32_t& jj, uint32_t piece, bool& bad, uint32_t& marks, int t,
+                                              int lane) {
   using L = CLayout<D>;
   using F = DqFmt<D, BITS>;
   constexpr int G = D / 32, N = HalfRegs<D, BITS>::N;
@@ -243,9 +252,12 @@ __device__ __forceinline__ bool dequant_piece(const CParams& p, uint8_t* smem, u
     if (jj >= 2 && !__all_sync(0xffffffffu, mbar_wait(&bar[B_KVEMPTY0 + st], ((jj >> 1) - 1) & 1, p.status, p.wait_ns)))
       return false;
     store_half<D, BITS>(dst, k, x, row, c);
+    uint32_t most = max_word<D, BITS>(k);   // (branch-free: a branch on a loaded word would wait for every load in flight)
     done(B_KFULL0 + st);
     if (j + 1 < w.n) load_k();
     store_half<D, BITS>(dst + kToV, v, x, row, c);
+    most = __vmaxu2(most, max_word<D, BITS>(v));
+    mark_big(marks, most, j);
     clear_unseen<D, BITS>(dst + kToV, p, w, t0, row, c, x * N, (x + 1) * N);
     done(B_VFULL0 + st);
   }
@@ -573,13 +585,16 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_attention_kernel(const __gr
     // ---------------- dequant warpgroups: half x of the tiles, slot x's queries ----------------
     const int x = (warp - 4) >> 2, t = threadIdx.x & 127;
     uint32_t jj = 0, piece = 0;
-    bool ok, bad = false;
+    bool ok, bad = false, big = false;
     do {
-      ok = p.bits[w.kvh] == 4 ? dequant_piece<D, 4, PAGED>(p, smem, bar, w, x, jj, piece, bad, t, lane)
-                              : dequant_piece<D, 8, PAGED>(p, smem, bar, w, x, jj, piece, bad, t, lane);
+      uint32_t marks = 0;
+      ok = p.bits[w.kvh] == 4 ? dequant_piece<D, 4, PAGED>(p, smem, bar, w, x, jj, piece, bad, marks, t, lane)
+                              : dequant_piece<D, 8, PAGED>(p, smem, bar, w, x, jj, piece, bad, marks, t, lane);
+      big |= marked_overflow<D>(p, w, marks, 0, 2, lane);
       ++piece;
     } while (ok && next_piece<kRows>(p, w, lane));
     if (bad) report(p.status, KVQ_ERR_INVALID_ARG);
+    if (big) report(p.status, KVQ_ERR_NONFINITE);
     __syncwarp();
     if (lane == 0) mbar_arrive(&bar[B_EXIT]);
     return;

@@ -136,7 +136,8 @@ __device__ __forceinline__ void sum_rows(float (&l)[NR], int lane, int32_t* dst)
 // iteration.
 template <int D, int NR, int BITS>
 __device__ __forceinline__ bool dequant_piece(const CParams& p, uint8_t* smem, uint64_t* bar, const Walk& w, int which,
-                                              int sub, uint32_t& jj, uint32_t& slot, uint32_t& round, int t, int lane) {
+                                              int sub, uint32_t& jj, uint32_t& slot, uint32_t& round, uint32_t& marks, int t,
+                                              int lane) {
   using L = NLayout<D, NR>;
   using F = DqFmt<D, BITS>;
   constexpr int H = F::NI / 2;              // iterations per slot, both warpgroups'
@@ -150,6 +151,7 @@ __device__ __forceinline__ bool dequant_piece(const CParams& p, uint8_t* smem, u
                                                       p.wait_ns)))
       return false;
     const uint32_t dst = smem_u32(smem + (which ? L::kOffV : L::kOffK) + st * L::kTile);
+    uint32_t most = 0;                      // the largest scale in the low half
 #pragma unroll
     for (int s = 0; s < 2; ++s) {
       const int k = which * kRing + static_cast<int>(slot);
@@ -175,6 +177,7 @@ __device__ __forceinline__ bool dequant_piece(const CParams& p, uint8_t* smem, u
         for (int i = 0; i < N; ++i) {
           const int it = s * H + (H > 1 ? 2 * i + sub : 0);
           dequant_chunk<BITS>(dst, F::RPI * it + row, c * F::VPC, v[i], word[i]);
+          most = __vmaxu2(most, word[i]);
         }
       }
       if (++slot == kRing) {
@@ -182,6 +185,7 @@ __device__ __forceinline__ bool dequant_piece(const CParams& p, uint8_t* smem, u
         ++round;
       }
     }
+    mark_big(marks, most, j);
     if (which) clear_unseen<D, BITS>(dst, p, w, w.t.tile(w.i + j) * kT, row, c, sub, F::NI, 2);
     fence_proxy_async_smem();
     __syncwarp();
@@ -512,7 +516,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_narrow_kernel(const __grid_
     const int wg = (warp - 4) >> 2, which = wg >> 1, sub = wg & 1;
     const int t = threadIdx.x & 127;
     uint32_t jj = 0, slot = 0, round = 0, piece = 0;
-    bool ok = true;
+    bool ok = true, big = false;
     do {
       if (wg == 0) {
         ok = load_queries<D, NR, NR>(p, smem_u32(smem + L::kOffQ), &bar[B_QEMPTY], w, t, (piece - 1) & 1, piece > 0);
@@ -521,10 +525,13 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_narrow_kernel(const __grid_
         __syncwarp();
         if (lane == 0 && piece < p.issue_limit) mbar_arrive(&bar[B_QREADY]);
       }
-      ok = p.bits[w.kvh] == 4 ? dequant_piece<D, NR, 4>(p, smem, bar, w, which, sub, jj, slot, round, t, lane)
-                              : dequant_piece<D, NR, 8>(p, smem, bar, w, which, sub, jj, slot, round, t, lane);
+      uint32_t marks = 0;
+      ok = p.bits[w.kvh] == 4 ? dequant_piece<D, NR, 4>(p, smem, bar, w, which, sub, jj, slot, round, marks, t, lane)
+                              : dequant_piece<D, NR, 8>(p, smem, bar, w, which, sub, jj, slot, round, marks, t, lane);
+      big |= marked_overflow<D>(p, w, marks, which, which + 1, lane);
       ++piece;
     } while (ok && next_piece<NR>(p, w, lane));
+    if (big) report(p.status, KVQ_ERR_NONFINITE);
     __syncwarp();
     if (lane == 0) mbar_arrive(&bar[B_EXIT]);
     return;

@@ -135,6 +135,16 @@ struct Seen {
       : end(w.t.pos_hi + 1), lo(p.window > 0 ? w.t.pos_lo - p.window + 1 : 0) {}
 };
 
+// The operands are fp16: a group whose scale and zero point can stand for a
+// value that rounds to infinity there (65520 and more) is reported if a query
+// sees it.  Smaller scales than kBigScale (as fp16 bits) never do.
+constexpr uint32_t kBigScale = 0x5C04u;   // 257: 8-bit codes; of 4-bit ones 4368 is the first
+__device__ __forceinline__ bool overflows(uint32_t word, int bits) {
+  const float qmax = static_cast<float>((1 << bits) - 1);
+  const float s = fabsf(half_lo(word)), z = half_hi(word);
+  return !(s * fmaxf(z, qmax - z) < 65520.0f);
+}
+
 // Output offset of packed row R of a sequence and KV head.
 __device__ __forceinline__ int64_t out_offset(const CParams& p, const Walk& w, int R, int D) {
   const int tok = R / p.rep, hh = R - tok * p.rep;
@@ -390,6 +400,37 @@ __device__ __forceinline__ void clear_unseen(uint32_t dst, const CParams& p, con
     const uint32_t rowp = dst + (ch0 >> 6) * (kT * 128) + r * 128;
     for (int i = 0; i < F::VPC / 8; ++i) tile::sts128(rowp + (((((ch0 & 63) >> 3) + i) ^ (r & 7)) << 4), 0u, 0u, 0u, 0u);
   }
+}
+
+// A dequant warp marks the tiles of its piece (bit j % 32 for tile j) in which
+// it met a scale of kBigScale or more, perhaps in rows that nothing sees; after
+// the piece it looks at the words of those tiles once more: whether one that is
+// seen overflows.  (By the whole warp; parts x0 .. x1 - 1 of K, V.)
+__device__ __forceinline__ void mark_big(uint32_t& marks, uint32_t most, int j) {
+  if ((most & 0xFFFFu) >= kBigScale) marks |= 1u << (j & 31);
+}
+template <int D>
+__device__ __forceinline__ bool marked_overflow(const CParams& p, const Walk& w, uint32_t marks, int x0, int x1, int lane) {
+  marks = __reduce_or_sync(0xffffffffu, marks);
+  if (marks == 0u || p.status == nullptr) return false;
+  const Seen s(p, w);
+  const int64_t storage = static_cast<int64_t>(p.c.pB) * p.c.pT;
+  bool big = false;
+#pragma unroll 1
+  for (int j = 0; j < w.n; ++j) {
+    if (!(marks >> (j & 31) & 1u)) continue;
+#pragma unroll 1
+    for (int tok = w.t.tile(w.i + j) * kT + lane, k = 0; k < kT / 32; tok += 32, ++k) {
+      if (tok >= s.end || (tok < s.lo && tok >= p.sinks)) continue;
+      const int64_t at = chunk::storage_row(p.c, w.b, tok);
+      if (at < 0) continue;   // (reported; page 0 stands in for it)
+#pragma unroll 1
+      for (int x = x0; x < x1; ++x)
+        for (int g = 0; g < D / 32; ++g)
+          big |= overflows(p.sz[x][(w.kvh * storage + at) * (D / 32) + g], p.bits[w.kvh]);
+    }
+  }
+  return big;
 }
 
 // Eight query channels, bf16 to fp16 (for a 4-bit head in the channel order of

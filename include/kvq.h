@@ -557,10 +557,13 @@ KVQ_API kvq_status kvq_dequantize_paged(const kvq_cache* pool, const kvq_chunk* 
  *   workspace serves chunk calls of every shape that fits it; it is not shared
  *   with other kinds of calls.
  * Cache tokens that no query of the call sees are not read into the result
- * (they may hold anything).  Of those that only some rows of a sequence see,
- * the values have to be finite in fp16, as the operands are (K_hat, V_hat and
- * the weights are rounded to fp16 as in kvq_prefill_attention; scores, sums and
- * outputs are fp32).  A call whose work list of 128-token tiles could reach
+ * (they may hold anything).  The values of the others have to be finite in
+ * fp16, as the operands are (K_hat, V_hat and the weights are rounded to fp16 as
+ * in kvq_prefill_attention; scores, sums and outputs are fp32): a token that some
+ * query sees, with a group whose scale s and zero point z can stand for 65520 or
+ * more (s * max(z, qmax - z)), reports KVQ_ERR_NONFINITE in dev_status, and the
+ * outputs of its sequence are then unspecified (kvq_decode_attention takes such
+ * values: its scales stay fp32).  A call whose work list of 128-token tiles could reach
  * 2^31 entries per KV head is KVQ_ERR_UNSUPPORTED.  The result depends on
  * neither the order of the CTAs nor the call's place in a program: equal calls
  * on equal devices give equal bits.  Errors and other arguments as
