@@ -711,6 +711,13 @@ static kvq_status chunk_desc(const kvq_chunk* c, const kvq_cache& storage, const
 // has no address).
 static bool rows_ok(const void* x, const kvq_chunk* c) { return x != nullptr || (c != nullptr && c->rows == 0); }
 
+// The type and the flag of an out_dtype that may carry KVQ_OUT_ZERO_REST.
+static bool split_out_dtype(int32_t in, int32_t* out_dtype, bool* zero_rest) {
+  *zero_rest = (in & KVQ_OUT_ZERO_REST) != 0;
+  *out_dtype = in & ~KVQ_OUT_ZERO_REST;
+  return *out_dtype == KVQ_OUT_F32 || *out_dtype == KVQ_OUT_BF16;
+}
+
 static bool buffers_ok(const kvq_cache& c) {
   return c.codes != nullptr && c.sz != nullptr && aligned16(c.codes) && aligned16(c.sz);
 }
@@ -744,13 +751,12 @@ static kvq_status dequantize_impl(const kvq_cache* src, const kvq_chunk* chunk, 
   if (src->D > 0 && src->D != 64 && src->D != 128) return KVQ_ERR_UNSUPPORTED;
   DequantizeArgs a;
   if (!resolve_layout(*src, &a.layout)) return KVQ_ERR_INVALID_ARG;
-  if (!aligned16(out) || (out_dtype != KVQ_OUT_F32 && out_dtype != KVQ_OUT_BF16)) return KVQ_ERR_INVALID_ARG;
+  if (!aligned16(out) || !split_out_dtype(out_dtype, &a.out_dtype, &a.zero_rest)) return KVQ_ERR_INVALID_ARG;
   const kvq_status s = chunk_desc(chunk, *src, table, &a.chunk);
   if (s != KVQ_OK) return s;
   if (chunk->rows == 0) return KVQ_OK;
   a.src = src;
   a.out = out;
-  a.out_dtype = out_dtype;
   a.status = dev_status;
   return launch_dequantize(a, static_cast<cudaStream_t>(stream)) == cudaSuccess ? KVQ_OK : KVQ_ERR_CUDA;
 }
@@ -769,7 +775,7 @@ static kvq_status chunk_attention_impl(const void* q, int64_t sq_row, int64_t sq
   if (!resolve_layout(*k, &a.layout) || !same_cache_shape(*k, *v)) return KVQ_ERR_INVALID_ARG;
   if (Hq <= 0 || Hq % k->Hkv || window < 0 || sinks < 0) return KVQ_ERR_INVALID_ARG;
   if (Hq / k->Hkv > 128) return KVQ_ERR_UNSUPPORTED;
-  if (out_dtype != KVQ_OUT_F32 && out_dtype != KVQ_OUT_BF16) return KVQ_ERR_INVALID_ARG;
+  if (!split_out_dtype(out_dtype, &a.out_dtype, &a.zero_rest)) return KVQ_ERR_INVALID_ARG;
   if (!aligned16(q) || !aligned16(out) || sq_row < 0 || sq_head < 0 || sq_row % 8 || sq_head % 8)
     return KVQ_ERR_INVALID_ARG;
   const kvq_status s = chunk_desc(chunk, *k, table, &a.chunk);
@@ -789,7 +795,6 @@ static kvq_status chunk_attention_impl(const void* q, int64_t sq_row, int64_t sq
   a.window = window;
   a.sinks = sinks;
   a.out = out;
-  a.out_dtype = out_dtype;
   a.ws = workspace;
   a.ws_bytes = workspace_bytes;
   a.status = dev_status;

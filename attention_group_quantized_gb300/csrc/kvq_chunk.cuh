@@ -81,6 +81,17 @@ __device__ __forceinline__ int storage_block(const View& c, int b, int i, int32_
   return 0;
 }
 
+// Whether packed row r0 + lane (of those below c.rows) is one that no usable
+// sequence has (the whole warp).
+__device__ __forceinline__ bool row_is_free(const View& c, int r0, int lane) {
+  int b = find_sequence(c.start, c.B, r0, lane);
+  const int r = r0 + lane;
+  if (r >= c.rows) return false;
+  while (b + 1 < c.B && c.start[b + 1] <= r) ++b;
+  const Seq s = sequence(c, b);
+  return r < s.row0 || r >= s.row0 + s.n;   // (n = 0 for one that is left out)
+}
+
 constexpr int64_t kNoRow = -1;     // belongs to no usable sequence
 constexpr int64_t kBadPage = -2;   // its page lies outside the pool
 

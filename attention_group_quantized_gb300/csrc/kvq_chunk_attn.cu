@@ -19,7 +19,8 @@
 // completes it merges them in a fixed order.
 //
 // One CTA (640 threads, one per SM):
-//   warp 0      allocates TMEM and frees it once every other role is done;
+//   warp 0      zeroes rows of no sequence, if asked to; allocates TMEM and
+//               frees it once every other role is done;
 //   warps 1, 2  issue slot h = warp - 1's tcgen05.mma (S_h = Q_h K^T from
 //               shared memory, O_h += P_h V with P from TMEM), taking turns so
 //               that one slot's softmax runs under the other's products;
@@ -411,6 +412,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_attention_kernel(const __gr
   const int64_t total = disorder ? 0 : walks[from].left;
   if (total <= 0) {   // the whole CTA: nothing was started
     if (warp == 0) tc::tmem_dealloc(tmem, kTmemCols);
+    if (warp == 1 && p.zero_rest) zero_rest_rows<D>(p, disorder, lane);
     return;
   }
   if (warp != from) copy_walk(w, walks[from], lane);
@@ -423,6 +425,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_attention_kernel(const __gr
   if (warp < 4) {
     tc::reg_dealloc<64>();
     if (warp == 0) {
+      if (p.zero_rest) zero_rest_rows<D>(p, false, lane);
       // The other roles finish in bounded time: each stops at its first wait
       // that runs out, and a role waits at most a few times per tile.
       const uint64_t deadline = p.wait_ns * static_cast<uint64_t>(8 * min(total, int64_t(1) << 20) + 16) + 4 * kDrainNs;
@@ -891,6 +894,7 @@ kvq_status launch_chunk_attention(const ChunkAttnArgs& a, cudaStream_t stream) {
   p.out = a.out;
   p.status = a.status;
   p.out_dtype = a.out_dtype; p.Hq = a.Hq; p.Hkv = a.k->Hkv; p.rep = a.Hq / a.k->Hkv;
+  p.zero_rest = a.zero_rest ? 1 : 0;
   p.window = a.window; p.sinks = a.sinks;
   p.wait_ns = a.pol.wait_ns;
   p.issue_limit = static_cast<uint32_t>(a.pol.issue_limit);   // (negative: more pieces than any call has)

@@ -338,6 +338,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_narrow_kernel(const __grid_
   const int64_t total = disorder ? 0 : walks[from].left;
   if (total <= 0) {   // the whole CTA: nothing was started
     if (warp == 0) tc::tmem_dealloc(tmem, kCols);
+    if (warp == 1 && p.zero_rest) zero_rest_rows<D>(p, disorder, lane);
     return;
   }
   if (warp != from) copy_walk(w, walks[from], lane);
@@ -538,6 +539,8 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_narrow_kernel(const __grid_
   }
 
   tc::reg_alloc<112>();
+  // (a warp whose first tile is the piece's second)
+  if (warp == kThreads / 32 - 1 && p.zero_rest) zero_rest_rows<D>(p, false, lane);
   // ---------------- softmax warpgroups: thread = key of the tile, then channel of O^T ----------------
   // Two states of the online softmax, each with its own maxima, sums and O^T:
   // warpgroup x takes the piece's tiles j with j % 2 == x, so that a tile's

@@ -35,7 +35,7 @@ struct CParams {
   float* ws_o;                      // [2 * CTAs][slot_rows * D], in the kernel's own order
   void* out;
   int32_t* status;
-  int32_t out_dtype, Hq, Hkv, rep, window, sinks, num_ctas, slot_rows;
+  int32_t out_dtype, zero_rest, Hq, Hkv, rep, window, sinks, num_ctas, slot_rows;
   float scale_log2;
   int64_t codes_bytes;              // size of each code buffer (the debug build's index checks)
   uint64_t wait_ns;                 // bounded-wait limit
@@ -149,6 +149,22 @@ __device__ __forceinline__ bool overflows(uint32_t word, int bits) {
 __device__ __forceinline__ int64_t out_offset(const CParams& p, const Walk& w, int R, int D) {
   const int tok = R / p.rep, hh = R - tok * p.rep;
   return ((static_cast<int64_t>(w.s.row0) + tok) * p.Hq + w.kvh * p.rep + hh) * D;
+}
+
+// The rows that no usable sequence has become zeros (zero_rest), by one warp of
+// each CTA, 32 rows in turn; all rows where the starts descend.
+template <int D>
+__device__ __forceinline__ void zero_rest_rows(const CParams& p, bool disorder, int lane) {
+  const int n = p.Hq * D / (p.out_dtype == KVQ_OUT_F32 ? 4 : 8);   // 16-byte stores of a row
+#pragma unroll 1
+  for (int64_t r0 = static_cast<int64_t>(blockIdx.x) * 32; r0 < p.c.rows; r0 += static_cast<int64_t>(p.num_ctas) * 32) {
+    const int first = static_cast<int>(r0);
+    const bool mine = disorder ? first + lane < p.c.rows : chunk::row_is_free(p.c, first, lane);
+    for (unsigned left = __ballot_sync(0xffffffffu, mine); left != 0u; left &= left - 1) {
+      uint4* row = static_cast<uint4*>(p.out) + (r0 + __ffs(left) - 1) * n;
+      for (int i = lane; i < n; i += 32) row[i] = make_uint4(0u, 0u, 0u, 0u);
+    }
+  }
 }
 
 // Units of a sequence for one KV head (the whole warp, a lane per row block).

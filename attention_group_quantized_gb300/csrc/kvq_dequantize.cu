@@ -26,6 +26,7 @@ struct DqParams {
   void* out;
   int32_t* status;
   int32_t Hkv, tiles;       // tiles: runs of a warp's rows
+  int32_t zero_rest;        // rows of no usable sequence become zeros
   int64_t codes_bytes;      // size of the code buffer (the debug build's index checks)
   int64_t plane_off[KVQ_MAX_HKV];
   int8_t bits[KVQ_MAX_HKV];
@@ -82,7 +83,7 @@ __global__ void __launch_bounds__(kWarps * 32) dequantize_kernel(const __grid_co
       for (int k = 0; k < NP; ++k) {
         pos[k] = __shfl_sync(0xffffffffu, mine, k * RPP + lane / LPR);
         c[k] = make_uint2(0u, 0u);
-        word[k] = 0u;                   // a page outside the pool reads as zeros
+        word[k] = 0u;                   // a page outside the pool (or, zero_rest, a row of no sequence) reads as zeros
         if (pos[k] < 0) continue;
         const int64_t off = p.plane_off[h] + pos[k] * (D * BITS / 8) + col * BITS;
         const int64_t si = (static_cast<int64_t>(h) * storage + pos[k]) * G + col / 4;
@@ -95,7 +96,7 @@ __global__ void __launch_bounds__(kWarps * 32) dequantize_kernel(const __grid_co
       }
 #pragma unroll
       for (int k = 0; k < NP; ++k) {
-        if (pos[k] == chunk::kNoRow) continue;
+        if (pos[k] == chunk::kNoRow && !(p.zero_rest && r0 + k * RPP + lane / LPR < p.c.rows)) continue;
         float x[8];
         values8<BITS>(x, c[k], word[k]);
         const int64_t o = (static_cast<int64_t>(r0 + k * RPP + lane / LPR) * p.Hkv + h) * D + col * 8;
@@ -134,6 +135,7 @@ cudaError_t launch_dequantize(const DequantizeArgs& a, cudaStream_t stream) {
   p.out = a.out;
   p.status = a.status;
   p.Hkv = s.Hkv;
+  p.zero_rest = a.zero_rest ? 1 : 0;
   p.codes_bytes = a.layout.off4 + static_cast<int64_t>(a.layout.n4) * s.B * s.Tcap * (s.D / 2);
   for (int h = 0; h < KVQ_MAX_HKV; ++h) {
     p.plane_off[h] = a.layout.plane_off[h];

@@ -99,6 +99,7 @@ struct DequantizeArgs {
   ChunkDesc chunk;
   void* out;
   int32_t out_dtype;
+  bool zero_rest;                   // rows of no usable sequence become zeros
   int32_t* status;
 };
 cudaError_t launch_dequantize(const DequantizeArgs& a, cudaStream_t stream);
@@ -116,6 +117,7 @@ struct ChunkAttnArgs {
   int32_t window, sinks;
   void* out;
   int32_t out_dtype;
+  bool zero_rest;                   // rows of no usable sequence become zeros
   void* ws;
   size_t ws_bytes;
   int32_t* status;

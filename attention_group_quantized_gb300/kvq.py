@@ -570,6 +570,7 @@ def prefill_attention(q, k, v, k_cache: QuantCache, v_cache: QuantCache, softmax
 
 _pack_chunk = struct.Struct("@PPiii4x").pack   # kvq_chunk
 _pack_table = struct.Struct("@Pii").pack       # kvq_block_table
+_ZERO_REST = 0x100                             # KVQ_OUT_ZERO_REST: asked for where a call makes its own output
 
 def _bad(what: str):
     raise KvqError(1, what)
@@ -690,16 +691,17 @@ def append_chunk_paged(k_new, v_new, k_pool: QuantCache, v_pool: QuantCache, blo
 def _dequantize(cache: QuantCache, block_table, start, seq_lens, rows: int, out, out_dtype, status, stream):
     bt = _block_table(block_table)
     dev = _on_current_device(cache.codes, start, seq_lens)
+    rest = _ZERO_REST if out is None else 0
     out = _out(out, (rows, cache.Hkv, cache.D), out_dtype, cache.codes, "dequantize", stream)
     ch = _chunk(start, seq_lens, rows, None)
     if bt is None:
-        st = lib().kvq_dequantize(cache.c_struct(), ch, out.data_ptr(), out_dtype, _status_on(status, dev),
+        st = lib().kvq_dequantize(cache.c_struct(), ch, out.data_ptr(), out_dtype | rest, _status_on(status, dev),
                                   _stream_on(stream, dev))
         _check(st, "kvq_dequantize")
     else:
         _on_current_device(block_table)
-        st = lib().kvq_dequantize_paged(cache.c_struct(), ch, bt, out.data_ptr(), out_dtype, _status_on(status, dev),
-                                        _stream_on(stream, dev))
+        st = lib().kvq_dequantize_paged(cache.c_struct(), ch, bt, out.data_ptr(), out_dtype | rest,
+                                        _status_on(status, dev), _stream_on(stream, dev))
         _check(st, "kvq_dequantize_paged")
     return out
 
@@ -707,7 +709,8 @@ def _dequantize(cache: QuantCache, block_table, start, seq_lens, rows: int, out,
 def dequantize(cache: QuantCache, start, seq_lens, rows: int, out=None, out_dtype: int = OUT_BF16, status=None,
                stream=None):
     """The stored values of ragged position ranges, [rows][Hkv][D]: row start[b] + i is sequence b's position
-    seq_lens[b] - n_b + i.  start = running sum of seq_lens reads whole sequences."""
+    seq_lens[b] - n_b + i.  start = running sum of seq_lens reads whole sequences.  Rows that no usable sequence has are
+    zeros, or with `out` given left as they are."""
     return _dequantize(cache, None, start, seq_lens, rows, out, out_dtype, status, stream)
 
 
@@ -735,7 +738,9 @@ def _chunk_attention(q, k: QuantCache, v: QuantCache, block_table, start, seq_le
     _packed(q, Hq, k.D, "q")
     bt = _block_table(block_table)
     dev = _on_current_device(q, k.codes, v.codes, start, seq_lens)
+    rest = _ZERO_REST if out is None else 0
     out = _out(out, (rows, Hq, D), out_dtype, q, "chunk_attention", stream)
+    out_dtype |= rest
     workspace = _workspace(workspace, dev, stream, chunk_workspace, rows, int(seq_lens.shape[0]), Hq, k.Hkv, D,
                            q.device)
     ch = _chunk(start, seq_lens, rows, max_chunk)
@@ -769,7 +774,9 @@ def chunk_attention(q, k: QuantCache, v: QuantCache, start, seq_lens, softmax_sc
                     max_chunk: Optional[int] = None, status=None, stream=None, policy: Optional[CPolicy] = None):
     """Attention of packed new tokens q bf16 [rows][Hq][D] over caches that already hold them (append_chunk first);
     causal by cache position, optionally with a window of `window` tokens and the first `sinks` ones.
-    max_chunk: most rows of one sequence, if the caller knows it (chooses the kernel); returns [rows][Hq][D].
+    max_chunk: most rows of one sequence, if the caller knows it (chooses the kernel; a sequence of more rows is left out
+    and reported in `status`); returns [rows][Hq][D].  Rows that no usable sequence has are zeros, or with `out` given left
+    as they are.
     With a policy (see :func:`policy`) the call goes through kvq_chunk_attention_ex."""
     return _chunk_attention(q, k, v, None, start, seq_lens, softmax_scale, window, sinks, out, out_dtype, workspace,
                             max_chunk, status, stream, policy)

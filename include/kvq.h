@@ -61,6 +61,7 @@ typedef enum kvq_status {
 #define KVQ_TILE_TOKENS 64    /* cache capacity granularity */
 #define KVQ_OUT_F32 0
 #define KVQ_OUT_BF16 1
+#define KVQ_OUT_ZERO_REST 0x100   /* or-ed to either by calls that say so (see kvq_chunk) */
 
 /*
  * A quantised KV cache (one for K, one for V).  Group quantisation of P4 §2.4:
@@ -489,8 +490,10 @@ KVQ_API kvq_status kvq_prefill_attention_ex(const void* q, const void* k, const 
  * left out: nothing of it is read or written.  Where the starts descend, chunk
  * attention leaves the whole call out, and the append and the read-back may
  * leave out any of its sequences.
- * Rows that belong to no sequence (from start[B] on) are left as they are.  A
- * call with rows == 0 does nothing and needs no row buffers.
+ * Rows that belong to no sequence (from start[B] on) or to one that is left out
+ * are left as they are; with KVQ_OUT_ZERO_REST or-ed to out_dtype the read-back
+ * and chunk attention write them as zeros.  A call with rows == 0 does nothing
+ * and needs no row buffers.
  */
 typedef struct kvq_chunk {
   const int32_t* start;      /* device int32 [B + 1], 4-byte aligned */
@@ -528,7 +531,8 @@ KVQ_API kvq_status kvq_append_chunk_paged(const void* k_new, const void* v_new, 
  * the stored values (c - z) * s of its cache position (the difference is
  * exact; one rounding, to out's type), for every KV head.  With start the
  * running sum of seq_lens it reads whole sequences.
- * out: device [rows][Hkv][D], contiguous, 16-byte aligned, fp32 or bf16.
+ * out: device [rows][Hkv][D], contiguous, 16-byte aligned, fp32 or bf16
+ *   (KVQ_OUT_ZERO_REST: see kvq_chunk).
  */
 KVQ_API kvq_status kvq_dequantize(const kvq_cache* src, const kvq_chunk* chunk, void* out, int32_t out_dtype,
                                   int32_t* dev_status, void* stream);
@@ -550,7 +554,8 @@ KVQ_API kvq_status kvq_dequantize_paged(const kvq_cache* pool, const kvq_chunk* 
  *   q[r * sq_row + h * sq_head + d] (element strides, multiples of 8; channels
  *   contiguous; 16-byte aligned base; |q| < 65504, as kvq_decode_attention).
  * Hq % Hkv == 0, Hq / Hkv <= 128.  window >= 0 (0: none), sinks >= 0.
- * out: device [rows][Hq][D], contiguous, 16-byte aligned, fp32 or bf16.
+ * out: device [rows][Hq][D], contiguous, 16-byte aligned, fp32 or bf16
+ *   (KVQ_OUT_ZERO_REST: see kvq_chunk).
  * workspace: device scratch of >= kvq_chunk_workspace_bytes(rows, B, Hq, Hkv,
  *   D) bytes, with kvq_decode_attention's rules (16-byte aligned, zero-filled
  *   once before its first use, calls that share it ordered on the GPU).  One

@@ -91,3 +91,75 @@ def test_values_beyond_fp16_that_nothing_sees_are_not(kernel, part):
     for tok, want in ((69, 6), (70, 0), (300, 0), (500, 0), (501, 6), (640, 6)):
         status, finite = _with_value(kernel, True, part, tok % 2, 0, tok, 1e5, **seen)
         assert status == want and (finite or want), tok
+
+
+# ---------------------------------------------------------------- rows that no usable sequence has, in a call's own output
+
+BAD = {   # what the second of three sequences [6, 5, 7] on [40, 130, 50] tokens becomes: starts, its length, max_chunk
+    "length_beyond_cap": ((0, 6, 11, 18), 10 ** 6, None),
+    "fewer_than_new": ((0, 6, 11, 18), 4, None),
+    "rows_past_the_buffer": ((0, 6, 11, 90), None, None),
+    "max_chunk_too_small": ((0, 6, 11, 18), None, 5),
+    "rows_before_the_first": ((2, 6, 11, 18), None, None),
+    "fewer_rows_than_the_buffer": ((0, 6, 11, 13), None, None),
+    "descending": ((0, 11, 6, 18), None, None),
+    "no_rows": ((0, 0, 0, 0), None, None),
+}
+
+
+def _used_again(shape, dtype):
+    """Memory that held something else is what the next call makes its output from."""
+    torch.cuda.synchronize()
+    junk = [torch.full(shape, float("nan"), dtype=dtype, device="cuda") for _ in range(3)]
+    del junk
+
+
+@pytest.mark.parametrize("bad", BAD)
+@pytest.mark.parametrize("Hq,bf16", [(2, True), (4, False), (8, True), (128, False)], ids=str)
+def test_rows_of_no_sequence_are_zeros_in_an_output_that_the_call_makes(bad, Hq, bf16):
+    kvq = _kvq()
+    start, length, max_chunk = BAD[bad]
+    b = Batch(121, Hq, 2, 64, "84", [6, 5, 7], [40, 130, 50], Hq == 4)
+    b.fill()
+    b.append_new()
+    b.ok()
+    b.d_start = _ints(*start)
+    if length is not None:
+        b.d_lens = _ints(b.lens[0], length, b.lens[2])
+    q, dt = U.to_dev_bf16(b.q), torch.bfloat16 if bf16 else torch.float32
+    kw = dict(max_chunk=max_chunk, out_dtype=kvq.OUT_BF16 if bf16 else kvq.OUT_F32)
+    kept = torch.full((18, Hq, 64), 7.0, dtype=dt, device="cuda")
+    b.attend(q, out=kept, **kw)                              # the caller's output: those rows stay as they were
+    free = (kept == 7.0).flatten(1).all(1)
+    assert bad == "no_rows" or free.any()
+    for status in (b.status, None):                          # whether or not anyone asks
+        _used_again((18, Hq, 64), dt)
+        got = b.attend(q, status=status, **kw)
+        assert (got[free] == 0).all() and torch.equal(got[~free], kept[~free])
+    rows = torch.full((18, 2, 64), 7.0, dtype=dt, device="cuda")
+    b.read("k", b.d_start, b.d_lens, 18, out=rows, out_dtype=kw["out_dtype"])
+    free = (rows == 7.0).flatten(1).all(1)
+    _used_again((18, 2, 64), dt)
+    got = b.read("k", b.d_start, b.d_lens, 18, out_dtype=kw["out_dtype"])
+    assert (got[free] == 0).all() and torch.equal(got[~free], rows[~free])
+
+
+def test_many_padding_rows_are_zeros_in_an_output_that_the_call_makes():
+    """More rows than the CTAs take in one turn, few of them a sequence's, with both kernels and by the read-back."""
+    kvq = _kvq()
+    b = Batch(122, 8, 2, 128, "84", [3, 1], [500, 40], True)
+    b.fill()
+    b.append_new()
+    ref, bound = b.reference()
+    q = torch.zeros((9001, 8, 128), dtype=torch.bfloat16, device="cuda")
+    q[:4] = U.to_dev_bf16(b.q)
+    for max_chunk in (3, None):
+        _used_again(q.shape, torch.float32)
+        got = b.attend(q, max_chunk=max_chunk)
+        b.ok()
+        check(got[:4], ref, bound, False)
+        assert (got[4:] == 0).all()
+    _used_again((9001, 2, 128), torch.bfloat16)
+    got = b.read("v", b.d_start, b.d_lens, 9001)
+    b.ok()
+    assert (got[4:] == 0).all() and (got[:4] != 0).any(2).all()
