@@ -595,14 +595,25 @@ def _stream_on(stream, device: int) -> int:
     return raw(device) if raw is not None else _TORCH.cuda.current_stream().cuda_stream
 
 
+_INT32_MAX = 0x7FFFFFFF
+
+
+def _tokens(n: int) -> int:
+    """A number of tokens as the C int that it becomes: no sequence is longer than the largest, and a negative one stays
+    negative (ctypes would take the low 32 bits, and 2 ** 32 for none)."""
+    return max(-1, min(n, _INT32_MAX))
+
+
 def _chunk(start, seq_lens, rows: int, max_chunk: Optional[int]) -> bytes:
     """start: device int32 [B + 1], seq_lens: device int32 [B]."""
+    if not 0 <= rows <= _INT32_MAX:
+        _bad("rows: 0 .. 2 ** 31 - 1")
     i32 = _torch().int32
     if (start.dtype != i32 or seq_lens.dtype != i32 or start.dim() != 1 or seq_lens.dim() != 1
             or start.shape[0] != seq_lens.shape[0] + 1 or not start.is_contiguous() or not seq_lens.is_contiguous()):
         _bad("chunk: start int32 [B + 1] and seq_lens int32 [B], contiguous")
     return _pack_chunk(start.data_ptr(), seq_lens.data_ptr(), seq_lens.shape[0], rows,
-                       0 if max_chunk is None else max_chunk)
+                       0 if max_chunk is None else _tokens(max_chunk))
 
 
 def _block_table(block_table):
@@ -691,9 +702,9 @@ def append_chunk_paged(k_new, v_new, k_pool: QuantCache, v_pool: QuantCache, blo
 def _dequantize(cache: QuantCache, block_table, start, seq_lens, rows: int, out, out_dtype, status, stream):
     bt = _block_table(block_table)
     dev = _on_current_device(cache.codes, start, seq_lens)
+    ch = _chunk(start, seq_lens, rows, None)
     rest = _ZERO_REST if out is None else 0
     out = _out(out, (rows, cache.Hkv, cache.D), out_dtype, cache.codes, "dequantize", stream)
-    ch = _chunk(start, seq_lens, rows, None)
     if bt is None:
         st = lib().kvq_dequantize(cache.c_struct(), ch, out.data_ptr(), out_dtype | rest, _status_on(status, dev),
                                   _stream_on(stream, dev))
@@ -746,6 +757,7 @@ def _chunk_attention(q, k: QuantCache, v: QuantCache, block_table, start, seq_le
     ch = _chunk(start, seq_lens, rows, max_chunk)
     s_row, s_head, _ = q.stride()
     ws_n = workspace.numel() * workspace.element_size()
+    window, sinks = _tokens(window), _tokens(sinks)
     if policy is not None:
         if bt is not None:
             _on_current_device(block_table)
@@ -805,6 +817,7 @@ def _decode_window(q, k: QuantCache, v: QuantCache, block_table, seq_lens, windo
     out = _out(out, (B, Hq, D), out_dtype, q, "decode_attention_window", stream)
     workspace = _workspace(workspace, dev, stream, decode_workspace, B, Hq, k.Hkv, D, q.device)
     ws_n = workspace.numel() * workspace.element_size()
+    window, sinks = _tokens(window), _tokens(sinks)
     if bt is None:
         st = lib().kvq_decode_attention_window(q.data_ptr(), k.c_struct(), v.c_struct(), seq_lens.data_ptr(), Hq,
                                                softmax_scale, window, sinks, out.data_ptr(), out_dtype,

@@ -163,3 +163,32 @@ def test_many_padding_rows_are_zeros_in_an_output_that_the_call_makes():
     got = b.read("v", b.d_start, b.d_lens, 9001)
     b.ok()
     assert (got[4:] == 0).all() and (got[:4] != 0).any(2).all()
+
+
+# ---------------------------------------------------------------- numbers of tokens beyond 32 bits
+
+@pytest.mark.parametrize("kernel", KERNELS, ids=[k[0] for k in KERNELS])
+def test_windows_wider_than_32_bits_hide_nothing(kernel):
+    kvq = _kvq()
+    _, Hq, n, _ = kernel
+    b = Batch(131, Hq, 2, 128, "84", [n, n - 1], [700, 300], True)
+    b.fill()
+    b.append_new()
+    q, last = U.to_dev_bf16(b.q), U.to_dev_bf16(b.q[b.start[1:] - 1])
+    want, want_last = b.attend(q, max_chunk=n), b.decode(last, 0, 0)
+    some = b.attend(q, max_chunk=n, window=9)
+    for big in (2 ** 31 - 1, 2 ** 31, 2 ** 32, 2 ** 32 + 5, 2 ** 63 - 1, 2 ** 64 + 9):
+        assert torch.equal(want, b.attend(q, max_chunk=n, window=big))
+        assert torch.equal(want, b.attend(q, max_chunk=n, window=9, sinks=big))
+        assert torch.equal(want, b.attend(q, max_chunk=big)) or n * Hq // 2 <= 32     # (the other kernel's bits)
+        assert torch.equal(want_last, b.decode(last, big, 0)) and torch.equal(want_last, b.decode(last, 9, big))
+    assert torch.equal(some, b.attend(q, max_chunk=n, window=9, sinks=0))
+    for bad in (dict(window=-1), dict(window=-2 ** 32), dict(sinks=-2 ** 32 + 4), dict(max_chunk=-2 ** 32 + 9)):
+        with pytest.raises(kvq.KvqError):
+            b.attend(q, **{"max_chunk": n, **bad})
+    with pytest.raises(kvq.KvqError):
+        b.decode(last, -2 ** 32 + 7, 0)
+    for rows in (-1, -2 ** 32 + 4, 2 ** 31, 2 ** 32 + 4):
+        with pytest.raises(kvq.KvqError):
+            b.read("k", b.d_start, b.d_lens, rows)
+    b.ok()
