@@ -499,7 +499,7 @@ typedef struct kvq_chunk {
   const int32_t* start;      /* device int32 [B + 1], 4-byte aligned */
   const int32_t* seq_lens;   /* device int32 [B], 4-byte aligned */
   int32_t B;                 /* sequences, 1 .. 4096; the cache's B, or the block table's */
-  int32_t rows;              /* rows of the caller's packed buffers */
+  int32_t rows;              /* rows of the caller's packed buffers; KVQ_ERR_UNSUPPORTED from 2^31 - 257 on */
   int32_t max_chunk;         /* most new tokens of one sequence; 0 = rows.  Chunk attention chooses its kernel by it. */
 } kvq_chunk;
 
