@@ -673,7 +673,7 @@ def _append_chunk(k_new, v_new, k: QuantCache, v: QuantCache, block_table, start
     if k_new.shape[0] != v_new.shape[0] or k_new.stride() != v_new.stride():
         _bad("k_new and v_new: the same rows and strides")
     bt = _block_table(block_table)
-    dev = _on_current_device(k_new, v_new, k.codes, v.codes, start, seq_lens)
+    dev = _on_current_device(k_new, v_new, k.codes, k.sz, v.codes, v.sz, start, seq_lens)
     ch = _chunk(start, seq_lens, k_new.shape[0], None)
     s_row, s_head, _ = k_new.stride()
     if bt is None:
@@ -701,7 +701,7 @@ def append_chunk_paged(k_new, v_new, k_pool: QuantCache, v_pool: QuantCache, blo
 
 def _dequantize(cache: QuantCache, block_table, start, seq_lens, rows: int, out, out_dtype, status, stream):
     bt = _block_table(block_table)
-    dev = _on_current_device(cache.codes, start, seq_lens)
+    dev = _on_current_device(cache.codes, cache.sz, start, seq_lens)
     ch = _chunk(start, seq_lens, rows, None)
     rest = _ZERO_REST if out is None else 0
     out = _out(out, (rows, cache.Hkv, cache.D), out_dtype, cache.codes, "dequantize", stream)
@@ -748,7 +748,7 @@ def _chunk_attention(q, k: QuantCache, v: QuantCache, block_table, start, seq_le
     rows, Hq, D = q.shape
     _packed(q, Hq, k.D, "q")
     bt = _block_table(block_table)
-    dev = _on_current_device(q, k.codes, v.codes, start, seq_lens)
+    dev = _on_current_device(q, k.codes, k.sz, v.codes, v.sz, start, seq_lens)
     rest = _ZERO_REST if out is None else 0
     out = _out(out, (rows, Hq, D), out_dtype, q, "chunk_attention", stream)
     out_dtype |= rest
@@ -813,7 +813,7 @@ def _decode_window(q, k: QuantCache, v: QuantCache, block_table, seq_lens, windo
     if (seq_lens.dtype != torch.int32 or seq_lens.dim() != 1 or seq_lens.shape[0] != B or not seq_lens.is_contiguous()
             or B != (k.B if bt is None else block_table.shape[0])):
         _bad("seq_lens: int32 [B]")
-    dev = _on_current_device(q, k.codes, v.codes, seq_lens)
+    dev = _on_current_device(q, k.codes, k.sz, v.codes, v.sz, seq_lens)
     out = _out(out, (B, Hq, D), out_dtype, q, "decode_attention_window", stream)
     workspace = _workspace(workspace, dev, stream, decode_workspace, B, Hq, k.Hkv, D, q.device)
     ws_n = workspace.numel() * workspace.element_size()

@@ -192,3 +192,22 @@ def test_windows_wider_than_32_bits_hide_nothing(kernel):
         with pytest.raises(kvq.KvqError):
             b.read("k", b.d_start, b.d_lens, rows)
     b.ok()
+
+
+def test_scale_words_elsewhere_are_refused():
+    """A cache whose codes lie on the GPU and whose words do not never reaches a kernel."""
+    kvq = _kvq()
+    b = Batch(141, 4, 2, 64, "84", [3, 1], [60, 20], False)
+    b.fill()
+    b.append_new()
+    q, rows = U.to_dev_bf16(b.q), U.to_dev_bf16(b.packed(b.k))
+    split = lambda c: kvq.QuantCache(c.codes, c.sz.cpu(), c.head_bits, c.B, c.Hkv, c.Tcap, c.D)
+    for k, v in ((split(b.kc), b.vc), (b.kc, split(b.vc))):
+        for call in (lambda: kvq.append_chunk(rows, rows, k, v, b.d_start, b.d_lens),
+                     lambda: kvq.chunk_attention(q, k, v, b.d_start, b.d_lens),
+                     lambda: kvq.decode_attention_window(q[:2], k, v, b.d_lens, 5)):
+            with pytest.raises(kvq.KvqError):
+                call()
+    with pytest.raises(kvq.KvqError):
+        kvq.dequantize(split(b.kc), b.d_start, b.d_lens, 4)
+    b.ok()
