@@ -7,6 +7,7 @@
 #include <cstdint>
 
 #include "kvq_device.cuh"
+#include "kvq_internal.h"
 
 namespace kvq {
 namespace chunk {
@@ -21,6 +22,16 @@ struct View {
   int32_t cap;               // tokens a sequence may have
   int32_t pB, pT;            // storage: pB sequences (or pages) of pT tokens
 };
+
+inline View view_of(const ChunkDesc& c, const kvq_cache& storage) {
+  View v;
+  v.start = c.start; v.seq_lens = c.seq_lens; v.bt = c.bt;
+  v.B = c.B; v.rows = c.rows; v.max_chunk = c.max_chunk;
+  v.bt_stride = c.bt_max_pages;
+  v.cap = c.cap;
+  v.pB = storage.B; v.pT = storage.Tcap;
+  return v;
+}
 
 // Sequence b's new tokens: its first row and their number (0 when the
 // description is unusable, which `bad` tells), and its length.

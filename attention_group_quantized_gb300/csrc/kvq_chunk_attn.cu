@@ -882,11 +882,7 @@ kvq_status launch_chunk_attention(const ChunkAttnArgs& a, cudaStream_t stream) {
   CParams p;
   memset(&p, 0, sizeof(p));
   const int D = a.k->D;
-  p.c.start = a.chunk.start; p.c.seq_lens = a.chunk.seq_lens; p.c.bt = a.chunk.bt;
-  p.c.B = a.chunk.B; p.c.rows = a.chunk.rows; p.c.max_chunk = a.chunk.max_chunk;
-  p.c.bt_stride = a.chunk.bt_max_pages;
-  p.c.cap = a.chunk.cap;
-  p.c.pB = a.k->B; p.c.pT = a.k->Tcap;
+  p.c = chunk::view_of(a.chunk, *a.k);
   p.q = a.q;
   p.sq_row = a.sq_row; p.sq_head = a.sq_head;
   p.codes[0] = a.k->codes; p.codes[1] = a.v->codes;

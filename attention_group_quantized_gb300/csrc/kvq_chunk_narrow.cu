@@ -520,7 +520,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_narrow_kernel(const __grid_
     bool ok = true, big = false;
     do {
       if (wg == 0) {
-        ok = load_queries<D, NR, NR>(p, smem_u32(smem + L::kOffQ), &bar[B_QEMPTY], w, t, (piece - 1) & 1, piece > 0);
+        ok = load_queries<D, NR>(p, smem_u32(smem + L::kOffQ), &bar[B_QEMPTY], w, t, (piece - 1) & 1, piece > 0);
         if (!ok) break;
         fence_proxy_async_smem();
         __syncwarp();

@@ -470,24 +470,24 @@ __device__ __forceinline__ void check_queries(const CParams& p, uint32_t big) {
 
 // The piece's query rows to fp16 in the swizzled layout (rows past the
 // segment's end zero); for a 4-bit head in the channel order of its K tiles.
-// dst: tiles of TILE rows ([D / 64 blocks][TILE rows][128 B] each), ROWS rows
-// a segment; empty: the barrier that says that the buffer is free.
-template <int D, int TILE, int ROWS>
+// dst: [D / 64 blocks][ROWS rows][128 B]; empty: the barrier that says that the
+// buffer is free.
+template <int D, int ROWS>
 __device__ __forceinline__ bool load_queries(const CParams& p, uint32_t dst, uint64_t* empty, const Walk& w, int t,
                                              uint32_t parity, bool wait) {
   constexpr int CPR = D / 8;              // 16-byte chunks per row
   constexpr int RPP = 128 / CPR;          // rows per pass
-  constexpr int NB = TILE / RPP < 8 ? TILE / RPP : 8;   // passes in flight
+  constexpr int NB = ROWS / RPP < 8 ? ROWS / RPP : 8;   // passes in flight
   const int ch = t % CPR;
   const bool four = p.bits[w.kvh] == 4;
   const uint16_t* base = p.q + static_cast<int64_t>(w.s.row0) * p.sq_row + w.kvh * p.rep * p.sq_head + ch * 8;
-  const int end = (w.t.rows + TILE - 1) / TILE * TILE, rows = w.t.rows;
+  const int rows = w.t.rows;
   // token and head of this thread's row, stepped from pass to pass
   const int R0 = w.rt * ROWS + t / CPR;
   int tok = R0 / p.rep, hh = R0 - tok * p.rep;
   const int dtok = RPP / p.rep, dhh = RPP - dtok * p.rep;
   uint32_t big = 0;
-  for (int r0 = 0; r0 < end; r0 += RPP * NB) {
+  for (int r0 = 0; r0 < ROWS; r0 += RPP * NB) {
     uint4 v[NB];
 #pragma unroll
     for (int k = 0; k < NB; ++k) {
@@ -506,7 +506,7 @@ __device__ __forceinline__ bool load_queries(const CParams& p, uint32_t dst, uin
     for (int k = 0; k < NB; ++k) {
       const int r = r0 + k * RPP + t / CPR;
       const uint4 x = query_chunk(v[k], four, big);
-      const uint32_t rowp = dst + (r / TILE) * (TILE * D * 2) + (ch >> 3) * (TILE * 128) + (r % TILE) * 128;
+      const uint32_t rowp = dst + (ch >> 3) * (ROWS * 128) + r * 128;
       tile::sts128(rowp + (((ch & 7) ^ (r & 7)) << 4), x.x, x.y, x.z, x.w);
     }
   }

@@ -125,11 +125,7 @@ __global__ void __launch_bounds__(kWarps * 32) dequantize_kernel(const __grid_co
 cudaError_t launch_dequantize(const DequantizeArgs& a, cudaStream_t stream) {
   DqParams p;
   const kvq_cache& s = *a.src;
-  p.c.start = a.chunk.start; p.c.seq_lens = a.chunk.seq_lens; p.c.bt = a.chunk.bt;
-  p.c.B = a.chunk.B; p.c.rows = a.chunk.rows; p.c.max_chunk = a.chunk.max_chunk;
-  p.c.bt_stride = a.chunk.bt_max_pages;
-  p.c.cap = a.chunk.cap;
-  p.c.pB = s.B; p.c.pT = s.Tcap;
+  p.c = chunk::view_of(a.chunk, s);
   p.codes = s.codes;
   p.sz = s.sz;
   p.out = a.out;

@@ -742,19 +742,9 @@ cudaError_t launch_append(const AppendArgs& a, cudaStream_t stream) {
   return cudaGetLastError();
 }
 
-static chunk::View chunk_view(const ChunkDesc& c, const kvq_cache& storage) {
-  chunk::View v;
-  v.start = c.start; v.seq_lens = c.seq_lens; v.bt = c.bt;
-  v.B = c.B; v.rows = c.rows; v.max_chunk = c.max_chunk;
-  v.bt_stride = c.bt_max_pages;
-  v.cap = c.cap;
-  v.pB = storage.B; v.pT = storage.Tcap;
-  return v;
-}
-
 cudaError_t launch_append_chunk(const AppendChunkArgs& a, cudaStream_t stream) {
   ACParams p;
-  p.c = chunk_view(a.chunk, *a.k);
+  p.c = chunk::view_of(a.chunk, *a.k);
   p.x[0] = a.k_new; p.x[1] = a.v_new;
   p.s_row = a.s_row; p.s_head = a.s_head;
   p.codes[0] = a.k->codes; p.codes[1] = a.v->codes;
