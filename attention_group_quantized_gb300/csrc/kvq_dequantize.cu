@@ -47,12 +47,19 @@ __device__ __forceinline__ void values8(float (&x)[8], uint2 c, uint32_t word) {
 }
 
 // NP: passes of 32 lanes whose loads are in flight together (NP x 256 / D rows
-// a warp).  Eight amortise the rows' look-up best when there are warps enough
-// (eight against four: 17.3 and 19.1 us for 79 MB); two spread a short call over
-// more of them (two against eight: 3.4 and 3.8 us for 5 MB).  Since 8-bit and
-// 4-bit heads have paths of their own (one path took both widths' shifts for
-// every value) it is 14.9 us for the 79 MB of mixed heads, 5.3 TB/s, 16.4 us for
-// 88 MB of 4-bit ones, 5.4 TB/s, and 3.2 us for the 5 MB.
+// a warp).  For bf16, eight amortise the rows' look-up best when there are warps
+// enough and two spread a short call over more of them; with fp32's twice as
+// many stores two are faster at every length.  Measured (us; two, eight passes):
+//   rows           1024        2048        3040        4096        8192       24576
+//   8 heads, D 128, INT8, bf16
+//             2.4   2.7   2.9   3.0   3.9   3.4   4.5   3.7   7.1   6.5  16.6  14.0
+//   4 heads, D 64, INT8, bf16 (a quarter of the warps of eight passes)
+//             2.1   2.7   2.2   2.7   2.2   2.7   2.4   2.7   2.9   3.0   5.9   5.8
+//   8 heads, D 128, INT4, fp32
+//             3.1   3.2   4.1   4.7   5.3   5.8   6.3   6.9   9.5  11.6  21.6  25.8
+// so eight from about eight warps an SM on.  In all: 14.9 us for 79 MB of mixed
+// heads, 5.3 TB/s, 18.0 us for 105 MB of 8-bit ones, 5.8 TB/s, 16.4 us for 88 MB
+// of 4-bit ones, 5.4 TB/s, 2.6 us for 5 MB.
 template <int D, bool F32, int NP>
 __global__ void __launch_bounds__(kWarps * 32) dequantize_kernel(const __grid_constant__ DqParams p) {
   constexpr int G = D / 32;
@@ -138,7 +145,8 @@ cudaError_t launch_dequantize(const DequantizeArgs& a, cudaStream_t stream) {
     p.bits[h] = a.layout.bits[h];
   }
   auto tiles_of = [&](int np) { return (a.chunk.rows + np * (256 / s.D) - 1) / (np * (256 / s.D)); };
-  const bool many = static_cast<int64_t>(tiles_of(8)) * p.Hkv >= 16 * device_sm_count();
+  const bool f32 = a.out_dtype == KVQ_OUT_F32;
+  const bool many = !f32 && static_cast<int64_t>(tiles_of(8)) * p.Hkv >= 8 * device_sm_count();
   p.tiles = tiles_of(many ? 8 : 2);
   const int64_t warps = static_cast<int64_t>(p.tiles) * p.Hkv;
   const int64_t blocks = std::min<int64_t>((warps + kWarps - 1) / kWarps, int64_t(1) << 30);
@@ -151,15 +159,14 @@ cudaError_t launch_dequantize(const DequantizeArgs& a, cudaStream_t stream) {
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  const bool f32 = a.out_dtype == KVQ_OUT_F32;
-  auto launch = [&](auto kernel2, auto kernel8) {
-    return many ? cudaLaunchKernelEx(&cfg, kernel8, p) : cudaLaunchKernelEx(&cfg, kernel2, p);
-  };
+  auto launch = [&](auto kernel) { return cudaLaunchKernelEx(&cfg, kernel, p); };
   if (s.D == 128)
-    return f32 ? launch(dequantize_kernel<128, true, 2>, dequantize_kernel<128, true, 8>)
-               : launch(dequantize_kernel<128, false, 2>, dequantize_kernel<128, false, 8>);
-  return f32 ? launch(dequantize_kernel<64, true, 2>, dequantize_kernel<64, true, 8>)
-             : launch(dequantize_kernel<64, false, 2>, dequantize_kernel<64, false, 8>);
+    return f32    ? launch(dequantize_kernel<128, true, 2>)
+           : many ? launch(dequantize_kernel<128, false, 8>)
+                  : launch(dequantize_kernel<128, false, 2>);
+  return f32    ? launch(dequantize_kernel<64, true, 2>)
+         : many ? launch(dequantize_kernel<64, false, 8>)
+                : launch(dequantize_kernel<64, false, 2>);
 }
 
 }  // namespace kvq
