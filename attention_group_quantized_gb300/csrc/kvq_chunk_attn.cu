@@ -36,7 +36,8 @@
 // 2^8; P is rounded to fp16, sums and O stay in fp32.
 //
 // Measured (32 query heads on 8, D = 128): 2048 tokens on 32K cached, INT8,
-// 864 us = 1312 TFLOP/s, 70 % of a bf16 GEMM's burst rate -- 1.87 us a tile of
+// 865 to 890 us (from GPU to GPU) = 1270 to 1310 TFLOP/s, 68 to 70 % of a bf16
+// GEMM's burst rate -- 1.87 us a tile of
 // 256 rows, of which the products take 1.37 at that rate and the softmax's 2^x
 // 1.1, next to them; what is left is the chain between them.  Shorter pieces
 // add about 10 us each (first queries and codes, partials, merge): 16 sequences

@@ -27,9 +27,9 @@
 // TMEM: S^T and O^T of each state, NR columns each.
 //
 // Measured: long contexts are bound by HBM's reads (eight sequences of 32K, 16
-// rows, INT8: 604 MB in 122 us, 4.8 TB/s over the call, 0.96 us per 36 KB tile an
+// rows, INT8: 590 MB in 118 us, 5.0 TB/s over the call, 0.95 us per 36 KB tile an
 // SM); a call of one tile takes 10 us, and a segment's cut about 9 us (eight
-// sequences of 8K: 41 us).  Fetching the codes into L2 further ahead was slower (54 us against 49 for
+// sequences of 8K: 42 us).  Fetching the codes into L2 further ahead was slower (54 us against 49 for
 // eight sequences of 8K), and so were slots of 32 tokens (more copies).
 #include <cmath>
 #include <mutex>
@@ -813,11 +813,16 @@ kvq_status launch_n(const CParams& p, cudaStream_t stream) {
 }  // namespace
 
 // At most 32 rows: with 64 columns a softmax thread's scores and sums do not fit
-// its registers.  Against the 256-row kernel (eight sequences, 8 KV heads, INT8):
-// 16 rows on 200, 2000, 8000, 32000 tokens 14, 27, 44, 122 us to its 15, 36, 67,
-// 187; 32 rows 19, 40, 59, 150 us to its 15, 35, 66, 186 (shorter than about 4K
-// it would be the faster one; the host does not know the lengths); 64 rows on
-// 8000 tokens 108 us to its 66.
+// its registers (even 32 spill some), and 64 rows on 8000 tokens took 108 us to
+// the 256-row kernel's 66.  Measured (us; this kernel, the 256-row one; eight
+// sequences, 8 KV heads, D = 128):
+//   tokens        200       1000       2000       4000       8000       32000
+//   INT8 16   11.0 12.5  16.6 21.8  20.1 27.1  27.7 40.6  41.8 65.5  118  189
+//        24   14.3 12.7  21.4 22.0  25.7 27.5  34.3 40.7  54.7 65.6  135  189
+//        32   14.7 12.6  21.8 22.0  26.8 27.2  35.3 40.9  55.9 65.0  137  188
+//   INT4 16   11.4 12.7  18.2 22.0  21.3 27.7  30.5 40.9  46.6 66.7  136  199
+//        32   14.7 12.5  22.6 22.1  27.6 27.8  36.7 40.9  59.3 66.5  150  198
+// (of 17 to 32 rows on a few hundred tokens the other would be 2 us faster)
 bool chunk_narrow_takes(int B, int64_t max_rows) { return B <= kMaxB && max_rows <= 32; }
 
 kvq_status launch_chunk_narrow(const CParams& p, int D, int64_t max_rows, cudaStream_t stream) {

@@ -837,7 +837,8 @@ def _decode_window(q, k: QuantCache, v: QuantCache, block_table, seq_lens, windo
 def decode_attention_window(q, k: QuantCache, v: QuantCache, seq_lens, window: int, sinks: int = 0,
                             softmax_scale: float = 0.0, out=None, out_dtype: int = OUT_F32, workspace=None,
                             status=None, stream=None):
-    """decode_attention over the last `window` tokens of each sequence and its first `sinks` ones (window 0: all)."""
+    """decode_attention over the last `window` tokens of each sequence and its first `sinks` ones (window 0: all).
+    Up to 8 query heads per KV head; with more, chunk_attention takes the B queries as B chunks of one row."""
     return _decode_window(q, k, v, None, seq_lens, window, sinks, softmax_scale, out, out_dtype, workspace, status,
                           stream)
 

@@ -603,7 +603,9 @@ KVQ_API kvq_status kvq_chunk_attention_ex(const void* q, int64_t sq_row, int64_t
  * window and j < min(sinks, len_b).  Only the 64-token tiles that hold such
  * tokens are read; tokens outside them may hold anything.  window == 0: every
  * token (kvq_decode_attention).  window, sinks >= 0.  Other arguments, the
- * workspace and errors as kvq_decode_attention.
+ * workspace and errors as kvq_decode_attention, Hq / Hkv <= 8 among them: with
+ * more query heads per KV head, kvq_chunk_attention computes the same from one
+ * row per sequence (start 0 .. B).
  */
 KVQ_API kvq_status kvq_decode_attention_window(const void* q, const kvq_cache* k, const kvq_cache* v,
                                                const int32_t* seq_lens, int32_t Hq, float softmax_scale,
