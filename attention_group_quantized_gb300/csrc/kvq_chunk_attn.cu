@@ -259,7 +259,7 @@ __device__ __forceinline__ bool dequant_piece(const CParams& p, uint8_t* smem, u
     if (j + 1 < w.n) load_k();
     store_half<D, BITS>(dst + kToV, v, x, row, c);
     most = __vmaxu2(most, max_word<D, BITS>(v));
-    mark_big(marks, most, j);
+    mark_big<BITS>(marks, most, j);
     clear_unseen<D, BITS>(dst + kToV, p, w, t0, row, c, x * N, (x + 1) * N);
     done(B_VFULL0 + st);
   }

@@ -185,7 +185,7 @@ __device__ __forceinline__ bool dequant_piece(const CParams& p, uint8_t* smem, u
         ++round;
       }
     }
-    mark_big(marks, most, j);
+    mark_big<BITS>(marks, most, j);
     if (which) clear_unseen<D, BITS>(dst, p, w, w.t.tile(w.i + j) * kT, row, c, sub, F::NI, 2);
     fence_proxy_async_smem();
     __syncwarp();

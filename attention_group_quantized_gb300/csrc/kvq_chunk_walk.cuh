@@ -138,7 +138,8 @@ struct Seen {
 // The operands are fp16: a group whose scale and zero point can stand for a
 // value that rounds to infinity there (65520 and more) is reported if a query
 // sees it.  Smaller scales than kBigScale (as fp16 bits) never do.
-constexpr uint32_t kBigScale = 0x5C04u;   // 257: 8-bit codes; of 4-bit ones 4368 is the first
+template <int BITS>
+constexpr uint32_t kBigScale = BITS == 8 ? 0x5C04u /* 257 */ : 0x6C44u /* 4368 */;
 __device__ __forceinline__ bool overflows(uint32_t word, int bits) {
   const float qmax = static_cast<float>((1 << bits) - 1);
   const float s = fabsf(half_lo(word)), z = half_hi(word);
@@ -422,8 +423,9 @@ __device__ __forceinline__ void clear_unseen(uint32_t dst, const CParams& p, con
 // it met a scale of kBigScale or more, perhaps in rows that nothing sees; after
 // the piece it looks at the words of those tiles once more: whether one that is
 // seen overflows.  (By the whole warp; parts x0 .. x1 - 1 of K, V.)
+template <int BITS>
 __device__ __forceinline__ void mark_big(uint32_t& marks, uint32_t most, int j) {
-  if ((most & 0xFFFFu) >= kBigScale) marks |= 1u << (j & 31);
+  if ((most & 0xFFFFu) >= kBigScale<BITS>) marks |= 1u << (j & 31);
 }
 template <int D>
 __device__ __forceinline__ bool marked_overflow(const CParams& p, const Walk& w, uint32_t marks, int x0, int x1, int lane) {

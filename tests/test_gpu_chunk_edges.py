@@ -211,3 +211,23 @@ def test_scale_words_elsewhere_are_refused():
     with pytest.raises(kvq.KvqError):
         kvq.dequantize(split(b.kc), b.d_start, b.d_lens, 4)
     b.ok()
+
+
+def test_large_scales_that_fit_are_taken():
+    """Every group's scale large (values of up to 30000 either way in 8 bits, 60000 in 4): nothing is reported, and the
+    outputs are right; words of unseen tokens hold a NaN."""
+    for kernel in KERNELS:
+        _, Hq, n, _ = kernel
+        b = Batch(112, Hq, 2, 128, "84", [n, n - 1], [700, 300], True)
+        rng = np.random.default_rng(7)
+        top = np.array([3e4, 6e4], np.float32)[None, :, None, None]
+        x = (rng.uniform(-1, 1, b.v.shape) * top).astype(np.float32)
+        x[..., ::32] = np.where(rng.random(x[..., ::32].shape) < 0.5, -top, top)
+        b.v = torch.from_numpy(x).bfloat16().view(torch.int16).numpy().view(np.uint16)
+        b.vp, _, _, b.vd = U.oracle_quantize(b.v, b.bits)
+        b.fill()
+        b.append_new()
+        ref, bound = b.reference()
+        out = b.attend(U.to_dev_bf16(b.q), max_chunk=n)
+        b.ok()
+        check(out, ref, bound, False, kernel[0])
