@@ -174,6 +174,9 @@ KVQ_API kvq_status kvq_decode_attention(const void* q, const kvq_cache* k, const
  *       nT * nT must stay below 2^31 (S up to 5,931,520), else
  *       KVQ_ERR_UNSUPPORTED.
  * out:  device [B][Hq][S][D], fp32 or bf16.
+ * The tensor-core operands are fp16: |q| < 65504, else KVQ_ERR_NONFINITE; K_hat,
+ * V_hat and the weights are rounded to it, and stored values of 65520 and more
+ * become infinities there, which is not reported.
  */
 KVQ_API kvq_status kvq_prefill_attention(const void* q, const void* k, const void* v,
                                  int32_t B, int32_t Hq, int32_t Hkv, int32_t S, int32_t D,
