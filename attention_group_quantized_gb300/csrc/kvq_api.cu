@@ -693,7 +693,8 @@ static kvq_status chunk_desc(const kvq_chunk* c, const kvq_cache& storage, const
   if (c->B <= 0 || c->rows < 0 || c->max_chunk < 0) return KVQ_ERR_INVALID_ARG;
   if (table != nullptr && !table_ok(table, storage)) return KVQ_ERR_INVALID_ARG;
   if (c->B != (table != nullptr ? table->B : storage.B)) return KVQ_ERR_INVALID_ARG;
-  if (c->B > 4096 || c->rows >= INT32_MAX - 256 || static_cast<int64_t>(c->rows) * storage.Hkv >= (int64_t(1) << 31) ||
+  const int32_t cap = table != nullptr ? table->max_pages * KVQ_TILE_TOKENS : storage.Tcap;
+  if (c->B > 4096 || c->rows >= INT32_MAX - 256 || cap > INT32_MAX - 256 || static_cast<int64_t>(c->rows) * storage.Hkv >= (int64_t(1) << 31) ||
       static_cast<int64_t>(storage.B) * (storage.Tcap / KVQ_TILE_TOKENS) >= (int64_t(1) << 31))
     return KVQ_ERR_UNSUPPORTED;
   out->start = c->start;
@@ -703,7 +704,7 @@ static kvq_status chunk_desc(const kvq_chunk* c, const kvq_cache& storage, const
   out->max_chunk = c->max_chunk == 0 ? c->rows : c->max_chunk;
   out->bt = table != nullptr ? table->pages : nullptr;
   out->bt_max_pages = table != nullptr ? table->max_pages : 0;
-  out->cap = table != nullptr ? table->max_pages * KVQ_TILE_TOKENS : storage.Tcap;
+  out->cap = cap;
   return KVQ_OK;
 }
 

@@ -496,7 +496,8 @@ KVQ_API kvq_status kvq_prefill_attention_ex(const void* q, const void* k, const 
  * Rows that belong to no sequence (from start[B] on) or to one that is left out
  * are left as they are; with KVQ_OUT_ZERO_REST or-ed to out_dtype the read-back
  * and chunk attention write them as zeros.  A call with rows == 0 does nothing
- * and needs no row buffers.
+ * and needs no row buffers.  Capacities of 2^31 - 256 tokens and more are
+ * KVQ_ERR_UNSUPPORTED.
  */
 typedef struct kvq_chunk {
   const int32_t* start;      /* device int32 [B + 1], 4-byte aligned */
