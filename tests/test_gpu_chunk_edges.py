@@ -231,3 +231,60 @@ def test_large_scales_that_fit_are_taken():
         out = b.attend(U.to_dev_bf16(b.q), max_chunk=n)
         b.ok()
         check(out, ref, bound, False, kernel[0])
+
+
+# ---------------------------------------------------------------- head layouts, shared pages
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("rep", [1, 2, 3, 5, 7, 11, 16, 31, 32, 33, 64, 100, 127, 128])
+def test_any_number_of_query_heads_per_kv_head(rep, D):
+    new = [1, 32 // rep if rep <= 32 else 1, 0, max(1, 300 // rep)]           # rows of a KV head up to about 300
+    b = Batch(151, rep, 1, D, "8" if rep % 2 else "4", new, [130, 400, 9, 70], rep % 3 == 0)
+    b.fill()
+    b.append_new()
+    for window, sinks in ((0, 0), (50, 3)):
+        ref, bound = b.reference(window, sinks)
+        check(b.attend(U.to_dev_bf16(b.q), window=window, sinks=sinks, max_chunk=max(new)), ref, bound, False)
+    if rep <= 32:                                                             # the kernel for few rows: single tokens
+        one = Batch(152, rep, 1, D, "4" if rep % 2 else "8", [1, 1, 1], [0, 127, 700], rep % 3 == 1)
+        one.fill()
+        one.append_new()
+        ref, bound = one.reference(90, 2)
+        check(one.attend(U.to_dev_bf16(one.q), window=90, sinks=2, max_chunk=1), ref, bound, False)
+        one.ok()
+    b.ok()
+
+
+@pytest.mark.parametrize("new", [(2, 1), (40, 3)], ids=["narrow", "wide"])
+def test_sixty_four_kv_heads(new):
+    kvq = _kvq()
+    bits = "84" * 20 + "4488" * 6
+    b = Batch(153, 128, 64, 64, bits, new, [300, 100], True)
+    b.fill()
+    b.append_new()
+    ref, bound = b.reference()
+    check(b.attend(U.to_dev_bf16(b.q), max_chunk=max(new)), ref, bound, False)
+    got = b.read("v", b.d_start, b.d_lens, b.rows, out_dtype=kvq.OUT_F32)
+    b.ok()
+    assert torch.equal(got.cpu(), torch.from_numpy(b.packed(b.vd)).float())
+
+
+@pytest.mark.parametrize("n", [3, 60], ids=["narrow", "wide"])
+def test_sequences_that_share_the_pages_of_a_prefix(n):
+    """Two sequences with one prefix of whole pages, stored once; each has tokens of its own behind it."""
+    kvq = _kvq()
+    b = Batch(154, 8, 2, 128, "84", [n, n], [448, 448], True)
+    for x in (b.k, b.v):
+        x[1, :, :384] = x[0, :, :384]
+    for name in "kv":
+        _, _, _, deq = U.oracle_quantize(getattr(b, name), b.bits)
+        setattr(b, name + "d", deq)
+    b.bt[1, :6] = b.bt[0, :6]
+    whole = torch.tensor([0, 384], dtype=torch.int32, device="cuda")
+    first = [U.to_dev_bf16(np.ascontiguousarray(x[0, :, :384].transpose(1, 0, 2))) for x in (b.k, b.v)]
+    kvq.append_chunk_paged(*first, b.kc, b.vc, b.bt[:1].contiguous(), whole, _ints(384), status=b.status)
+    tail = lambda x: U.to_dev_bf16(np.concatenate([x[s, :, 384:448 + n].transpose(1, 0, 2) for s in (0, 1)]))
+    b.append(tail(b.k), tail(b.v), _ints(0, 64 + n, 128 + 2 * n), b.d_lens)
+    ref, bound = b.reference()
+    check(b.attend(U.to_dev_bf16(b.q), max_chunk=n), ref, bound, False)
+    b.ok()
