@@ -231,8 +231,6 @@ __device__ __forceinline__ bool dequant_piece(const CParams& p, uint8_t* smem, u
   const int64_t soff = w.kvh * blocks * (64 * G) + row * G + c * F::VPC / 32;
   HalfTile<PAGED> cur, next;
   HalfRegs<D, BITS> k, v;
-  auto load_k = [&]() { load_half<D, BITS>(p, k, p.codes[0] + coff, p.sz[0] + soff, cur.block); };
-  auto load_v = [&]() { load_half<D, BITS>(p, v, p.codes[1] + coff, p.sz[1] + soff, cur.block); };
   auto done = [&](int which, bool tell = true) {
     fence_proxy_async_smem();
     __syncwarp();
@@ -241,6 +239,8 @@ __device__ __forceinline__ bool dequant_piece(const CParams& p, uint8_t* smem, u
   cur.look_up(p, w, 0, x);
   next.look_up(p, w, min(1, w.n - 1), x);
   cur.check(p, bad);
+  auto load_k = [&]() { load_half<D, BITS>(p, k, p.codes[0] + coff, p.sz[0] + soff, cur.block); };
+  auto load_v = [&]() { load_half<D, BITS>(p, v, p.codes[1] + coff, p.sz[1] + soff, cur.block); };
   load_k();
   if (!fetch_queries<D>(p, smem_u32(smem + L::kOffQ), &bar[B_QEMPTY], w, x, t, piece)) return false;
   done(B_QREADY, piece < p.issue_limit);
