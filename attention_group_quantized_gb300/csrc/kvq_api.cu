@@ -149,6 +149,7 @@ const char* kvq_status_str(kvq_status s) {
     case KVQ_ERR_TIMEOUT: return "device wait timed out";
     case KVQ_ERR_NONFINITE: return "non-finite input or fp16 overflow";
     case KVQ_ERR_BOUNDS: return "device index check failed (debug build)";
+    case KVQ_ERR_NO_PAGES: return "too few free pages";
   }
   return "unknown status";
 }
@@ -878,6 +879,374 @@ kvq_status kvq_decode_attention_window_paged(const void* q, const kvq_cache* k_p
   if (table == nullptr) return KVQ_ERR_INVALID_ARG;
   return decode_impl(q, k_pool, v_pool, table, seq_lens, Hq, softmax_scale, out, out_dtype, workspace,
                      workspace_bytes, dev_status, stream, nullptr, window, sinks);
+}
+
+}  // extern "C"
+
+// ---- rotated appends ----
+
+static kvq_status rotate_append_impl(const void* q, int64_t sq_row, int64_t sq_head, const void* k_new,
+                                     const void* v_new, int64_t s_row, int64_t s_head, const kvq_chunk* chunk,
+                                     const kvq_rotation* rotation, int32_t Hq, const kvq_cache* k, const kvq_cache* v,
+                                     const kvq_block_table* table, void* q_out, int32_t out_dtype,
+                                     int32_t* dev_status, void* stream) {
+  if (rotation == nullptr || k == nullptr || v == nullptr || !buffers_ok(*k) || !buffers_ok(*v) ||
+      !rows_ok(q, chunk) || !rows_ok(k_new, chunk) || !rows_ok(v_new, chunk) || !rows_ok(q_out, chunk))
+    return KVQ_ERR_INVALID_ARG;
+  if (k->D > 0 && k->D != 64 && k->D != 128) return KVQ_ERR_UNSUPPORTED;
+  RotateArgs a;
+  if (!resolve_layout(*k, &a.layout) || !same_cache_shape(*k, *v)) return KVQ_ERR_INVALID_ARG;
+  if (Hq <= 0 || !aligned16(q) || !aligned16(k_new) || !aligned16(v_new) || !aligned16(q_out) || sq_row < 0 ||
+      sq_head < 0 || s_row < 0 || s_head < 0 || sq_row % 8 || sq_head % 8 || s_row % 8 || s_head % 8)
+    return KVQ_ERR_INVALID_ARG;
+  const kvq_rotation& r = *rotation;
+  if (r.table != nullptr && (!aligned16(r.table) || r.positions <= 0 || r.rot_dim < 16 || r.rot_dim > k->D ||
+                             r.rot_dim % 16 || r.interleaved < 0 || r.interleaved > 1))
+    return KVQ_ERR_INVALID_ARG;
+  if (!aligned16(r.q_weight) || !aligned16(r.k_weight)) return KVQ_ERR_INVALID_ARG;
+  if ((r.q_weight != nullptr || r.k_weight != nullptr) && !(r.eps >= 1e-12f && r.eps <= 1.0f))
+    return KVQ_ERR_INVALID_ARG;
+  int32_t dtype;
+  if (!split_out_dtype(out_dtype, &dtype, &a.zero_rest)) return KVQ_ERR_INVALID_ARG;
+  if (dtype != KVQ_OUT_BF16) return KVQ_ERR_UNSUPPORTED;
+  const kvq_status s = chunk_desc(chunk, *k, table, &a.chunk);
+  if (s != KVQ_OK) return s;
+  if (static_cast<int64_t>(chunk->rows) * (static_cast<int64_t>(Hq) + 2 * k->Hkv) >= (int64_t(1) << 31))
+    return KVQ_ERR_UNSUPPORTED;
+  if (chunk->rows == 0) return KVQ_OK;
+  a.q = static_cast<const uint16_t*>(q);
+  a.sq_row = sq_row; a.sq_head = sq_head;
+  a.k_new = static_cast<const uint16_t*>(k_new);
+  a.v_new = static_cast<const uint16_t*>(v_new);
+  a.s_row = s_row; a.s_head = s_head;
+  a.rot = r;
+  a.Hq = Hq;
+  a.k = k; a.v = v;
+  a.q_out = static_cast<uint16_t*>(q_out);
+  a.status = dev_status;
+  return launch_rotate_append(a, static_cast<cudaStream_t>(stream)) == cudaSuccess ? KVQ_OK : KVQ_ERR_CUDA;
+}
+
+// ---- selected blocks ----
+
+static bool bounds_ok(const kvq_bounds* b) {
+  return b != nullptr && b->codes != nullptr && b->scales != nullptr && aligned16(b->codes) && aligned16(b->scales);
+}
+
+static int64_t storage_blocks(const kvq_cache& c) { return static_cast<int64_t>(c.B) * (c.Tcap / KVQ_TILE_TOKENS); }
+
+static kvq_status block_bounds_impl(const kvq_cache* k, const kvq_chunk* chunk, const kvq_block_table* table,
+                                    const kvq_bounds* bounds, int32_t* dev_status, void* stream) {
+  if (k == nullptr || !buffers_ok(*k) || !bounds_ok(bounds)) return KVQ_ERR_INVALID_ARG;
+  if (k->D > 0 && k->D != 64 && k->D != 128) return KVQ_ERR_UNSUPPORTED;
+  BoundsArgs a;
+  if (!resolve_layout(*k, &a.layout)) return KVQ_ERR_INVALID_ARG;
+  const kvq_status s = chunk_desc(chunk, *k, table, &a.chunk);
+  if (s != KVQ_OK) return s;
+  if (chunk->rows == 0) return KVQ_OK;
+  a.k = k;
+  a.bounds = *bounds;
+  a.status = dev_status;
+  return launch_block_bounds(a, static_cast<cudaStream_t>(stream)) == cudaSuccess ? KVQ_OK : KVQ_ERR_CUDA;
+}
+
+// What a selection and the attention over it check of their rows; *cap: the
+// tokens that a sequence may have.
+static kvq_status rows_desc(const kvq_cache& k, const kvq_block_table* table, const int32_t* blocks, int32_t n_select,
+                            const int32_t* row_seq, const int32_t* row_lens, int32_t rows, int32_t Hq, int32_t* cap) {
+  if (row_lens == nullptr || blocks == nullptr || (reinterpret_cast<uintptr_t>(row_lens) & 3u) ||
+      (reinterpret_cast<uintptr_t>(row_seq) & 3u) || (reinterpret_cast<uintptr_t>(blocks) & 3u))
+    return KVQ_ERR_INVALID_ARG;
+  if (table != nullptr && !table_ok(table, k)) return KVQ_ERR_INVALID_ARG;
+  if (rows < 0 || Hq <= 0 || Hq % k.Hkv || n_select < 1) return KVQ_ERR_INVALID_ARG;
+  if (row_seq == nullptr && rows > (table != nullptr ? table->B : k.B)) return KVQ_ERR_INVALID_ARG;
+  *cap = table != nullptr ? table->max_pages * KVQ_TILE_TOKENS : k.Tcap;
+  if (Hq / k.Hkv > 8 || rows > kMaxRows || n_select > kMaxSelect || *cap > (1 << 29) ||
+      static_cast<int64_t>(k.Hkv) * k.B * k.Tcap >= (int64_t(1) << 31))
+    return KVQ_ERR_UNSUPPORTED;
+  return KVQ_OK;
+}
+
+static kvq_status select_impl(const void* q, const kvq_cache* k, const kvq_bounds* bounds, const kvq_block_table* table,
+                              const int32_t* row_seq, const int32_t* row_lens, int32_t rows, int32_t Hq,
+                              int32_t n_select, int32_t first, int32_t last, int32_t* blocks, void* workspace,
+                              size_t workspace_bytes, int32_t* dev_status, void* stream) {
+  if (k == nullptr || !bounds_ok(bounds) || (rows != 0 && q == nullptr) || !aligned16(q)) return KVQ_ERR_INVALID_ARG;
+  if (k->D > 0 && k->D != 64 && k->D != 128) return KVQ_ERR_UNSUPPORTED;
+  if (!shape_ok(*k)) return KVQ_ERR_INVALID_ARG;
+  if (rows == 0) return KVQ_OK;
+  SelectArgs a;
+  const kvq_status s = rows_desc(*k, table, blocks, n_select, row_seq, row_lens, rows, Hq, &a.cap);
+  if (s != KVQ_OK) return s;
+  if (first < 0 || last < 0 || static_cast<int64_t>(first) + last > n_select) return KVQ_ERR_INVALID_ARG;
+  if (workspace == nullptr || !aligned16(workspace) || workspace_bytes < select_workspace_bytes(rows, k->Hkv, a.cap))
+    return KVQ_ERR_WORKSPACE;
+  a.q = static_cast<const uint16_t*>(q);
+  a.k = k;
+  a.bounds = *bounds;
+  a.seqs = k->B;
+  if (table != nullptr) {
+    a.bt = table->pages;
+    a.seqs = table->B;
+    a.bt_max_pages = table->max_pages;
+  }
+  a.row_seq = row_seq;
+  a.row_lens = row_lens;
+  a.rows = rows;
+  a.Hq = Hq;
+  a.n_select = n_select;
+  a.first = first;
+  a.last = last;
+  a.blocks = blocks;
+  a.ws = workspace;
+  a.status = dev_status;
+  return launch_select_blocks(a, static_cast<cudaStream_t>(stream)) == cudaSuccess ? KVQ_OK : KVQ_ERR_CUDA;
+}
+
+static kvq_status decode_blocks_impl(const void* q, const kvq_cache* k, const kvq_cache* v,
+                                     const kvq_block_table* table, const int32_t* blocks, int32_t n_select,
+                                     const int32_t* row_seq, const int32_t* row_lens, int32_t rows, int32_t Hq,
+                                     float softmax_scale, void* out, int32_t out_dtype, void* workspace,
+                                     size_t workspace_bytes, int32_t* dev_status, void* stream) {
+  if (k == nullptr || v == nullptr || !buffers_ok(*k) || !buffers_ok(*v) || !aligned16(q) || !aligned16(out) ||
+      (rows != 0 && (q == nullptr || out == nullptr)))
+    return KVQ_ERR_INVALID_ARG;
+  if (k->D > 0 && k->D != 64 && k->D != 128) return KVQ_ERR_UNSUPPORTED;
+  DecodeArgs a;
+  if (!resolve_layout(*k, &a.layout) || !same_cache_shape(*k, *v)) return KVQ_ERR_INVALID_ARG;
+  if (out_dtype != KVQ_OUT_F32 && out_dtype != KVQ_OUT_BF16) return KVQ_ERR_INVALID_ARG;
+  if (rows == 0) return KVQ_OK;
+  int32_t cap;
+  const kvq_status s = rows_desc(*k, table, blocks, n_select, row_seq, row_lens, rows, Hq, &cap);
+  if (s != KVQ_OK) return s;
+  if (workspace != nullptr && !aligned16(workspace)) return KVQ_ERR_INVALID_ARG;
+  a.q = static_cast<const uint16_t*>(q);
+  a.k = k;
+  a.v = v;
+  a.seq_lens = row_lens;
+  a.Hq = Hq;
+  a.softmax_scale = softmax_scale;
+  a.out = out;
+  a.out_dtype = out_dtype;
+  a.ws = workspace;
+  a.ws_bytes = workspace_bytes;
+  a.status = dev_status;
+  a.blocks = blocks;
+  a.row_seq = row_seq;
+  a.rows = rows;
+  a.n_select = n_select;
+  if (table != nullptr) {
+    a.bt = table->pages;
+    a.bt_B = table->B;
+    a.bt_max_pages = table->max_pages;
+  }
+  return launch_decode(a, static_cast<cudaStream_t>(stream));
+}
+
+// ---- pages ----
+
+static kvq_status page_table_ok(const kvq_page_table* t) {
+  if (t == nullptr || t->refs == nullptr || t->table == nullptr || t->seq_lens == nullptr ||
+      (reinterpret_cast<uintptr_t>(t->refs) & 3u) || (reinterpret_cast<uintptr_t>(t->table) & 3u) ||
+      (reinterpret_cast<uintptr_t>(t->seq_lens) & 3u) || t->n_pages <= 0 || t->slots <= 0 || t->max_pages <= 0)
+    return KVQ_ERR_INVALID_ARG;
+  if (t->n_pages > (1 << 24) || t->slots > 65536 ||
+      static_cast<int64_t>(t->max_pages) * KVQ_TILE_TOKENS >= (int64_t(1) << 31) ||
+      static_cast<int64_t>(t->max_pages) * t->slots >= (int64_t(1) << 31))
+    return KVQ_ERR_UNSUPPORTED;
+  return KVQ_OK;
+}
+
+static bool pages_workspace_ok(const kvq_page_table& t, const void* ws, size_t bytes) {
+  return ws != nullptr && aligned16(ws) && bytes >= pages_workspace_bytes(t.n_pages, t.slots);
+}
+
+// The pools (and bounds) that page data moves in.
+static kvq_status pools_ok(const kvq_cache* k, const kvq_cache* v, const kvq_bounds* bounds, PagesArgs* a) {
+  if (k == nullptr || v == nullptr || !buffers_ok(*k) || !buffers_ok(*v) || (bounds != nullptr && !bounds_ok(bounds)))
+    return KVQ_ERR_INVALID_ARG;
+  if (k->D > 0 && k->D != 64 && k->D != 128) return KVQ_ERR_UNSUPPORTED;
+  if (!resolve_layout(*k, &a->layout) || !same_cache_shape(*k, *v) || k->Tcap != KVQ_TILE_TOKENS)
+    return KVQ_ERR_INVALID_ARG;
+  a->k = k;
+  a->v = v;
+  if (bounds != nullptr) a->bounds = *bounds;
+  return KVQ_OK;
+}
+
+static bool list_ok(const int32_t* list, int32_t n) {
+  return n >= 0 && (n == 0 || (list != nullptr && (reinterpret_cast<uintptr_t>(list) & 3u) == 0));
+}
+
+extern "C" {
+
+kvq_status kvq_rotate_append(const void* q, int64_t sq_row, int64_t sq_head, const void* k_new, const void* v_new,
+                             int64_t s_row, int64_t s_head, const kvq_chunk* chunk, const kvq_rotation* rotation,
+                             int32_t Hq, const kvq_cache* k, const kvq_cache* v, void* q_out, int32_t out_dtype,
+                             int32_t* dev_status, void* stream) {
+  return rotate_append_impl(q, sq_row, sq_head, k_new, v_new, s_row, s_head, chunk, rotation, Hq, k, v, nullptr, q_out,
+                            out_dtype, dev_status, stream);
+}
+
+kvq_status kvq_rotate_append_paged(const void* q, int64_t sq_row, int64_t sq_head, const void* k_new, const void* v_new,
+                                   int64_t s_row, int64_t s_head, const kvq_chunk* chunk, const kvq_rotation* rotation,
+                                   int32_t Hq, const kvq_cache* k_pool, const kvq_cache* v_pool,
+                                   const kvq_block_table* table, void* q_out, int32_t out_dtype, int32_t* dev_status,
+                                   void* stream) {
+  if (table == nullptr) return KVQ_ERR_INVALID_ARG;
+  return rotate_append_impl(q, sq_row, sq_head, k_new, v_new, s_row, s_head, chunk, rotation, Hq, k_pool, v_pool, table,
+                            q_out, out_dtype, dev_status, stream);
+}
+
+int64_t kvq_bounds_bytes(const kvq_cache* k, int32_t which) {
+  if (k == nullptr || !shape_ok(*k) || which < 0 || which > 1) return -1;
+  const int64_t groups = storage_blocks(*k) * k->Hkv * (k->D / KVQ_GROUP);
+  return groups * (which == 0 ? 2 * KVQ_GROUP : 4);
+}
+
+kvq_status kvq_block_bounds(const kvq_cache* k, const kvq_chunk* chunk, const kvq_bounds* bounds, int32_t* dev_status,
+                            void* stream) {
+  return block_bounds_impl(k, chunk, nullptr, bounds, dev_status, stream);
+}
+
+kvq_status kvq_block_bounds_paged(const kvq_cache* k_pool, const kvq_chunk* chunk, const kvq_block_table* table,
+                                  const kvq_bounds* bounds, int32_t* dev_status, void* stream) {
+  if (table == nullptr) return KVQ_ERR_INVALID_ARG;
+  return block_bounds_impl(k_pool, chunk, table, bounds, dev_status, stream);
+}
+
+kvq_status kvq_bounds_values(const kvq_cache* k, const kvq_bounds* bounds, const int32_t* blocks, int32_t n, float* out,
+                             int32_t* dev_status, void* stream) {
+  if (k == nullptr || !shape_ok(*k) || !bounds_ok(bounds) || !list_ok(blocks, n) || !aligned16(out))
+    return KVQ_ERR_INVALID_ARG;
+  if (n == 0) return KVQ_OK;
+  if (out == nullptr) return KVQ_ERR_INVALID_ARG;
+  return launch_bounds_values(*k, *bounds, blocks, n, out, dev_status, static_cast<cudaStream_t>(stream)) == cudaSuccess
+             ? KVQ_OK : KVQ_ERR_CUDA;
+}
+
+size_t kvq_select_workspace_bytes(int32_t rows, int32_t Hkv, int32_t capacity) {
+  if (rows < 0 || rows > kMaxRows || Hkv <= 0 || Hkv > KVQ_MAX_HKV || capacity <= 0) return 0;
+  return select_workspace_bytes(rows, Hkv, capacity);
+}
+
+kvq_status kvq_select_blocks(const void* q, const kvq_cache* k, const kvq_bounds* bounds, const int32_t* row_seq,
+                             const int32_t* row_lens, int32_t rows, int32_t Hq, int32_t n_select, int32_t first,
+                             int32_t last, int32_t* blocks, void* workspace, size_t workspace_bytes,
+                             int32_t* dev_status, void* stream) {
+  return select_impl(q, k, bounds, nullptr, row_seq, row_lens, rows, Hq, n_select, first, last, blocks, workspace,
+                     workspace_bytes, dev_status, stream);
+}
+
+kvq_status kvq_select_blocks_paged(const void* q, const kvq_cache* k_pool, const kvq_bounds* bounds,
+                                   const kvq_block_table* table, const int32_t* row_seq, const int32_t* row_lens,
+                                   int32_t rows, int32_t Hq, int32_t n_select, int32_t first, int32_t last,
+                                   int32_t* blocks, void* workspace, size_t workspace_bytes, int32_t* dev_status,
+                                   void* stream) {
+  if (table == nullptr) return KVQ_ERR_INVALID_ARG;
+  return select_impl(q, k_pool, bounds, table, row_seq, row_lens, rows, Hq, n_select, first, last, blocks, workspace,
+                     workspace_bytes, dev_status, stream);
+}
+
+kvq_status kvq_decode_attention_blocks(const void* q, const kvq_cache* k, const kvq_cache* v, const int32_t* blocks,
+                                       int32_t n_select, const int32_t* row_seq, const int32_t* row_lens, int32_t rows,
+                                       int32_t Hq, float softmax_scale, void* out, int32_t out_dtype, void* workspace,
+                                       size_t workspace_bytes, int32_t* dev_status, void* stream) {
+  return decode_blocks_impl(q, k, v, nullptr, blocks, n_select, row_seq, row_lens, rows, Hq, softmax_scale, out,
+                            out_dtype, workspace, workspace_bytes, dev_status, stream);
+}
+
+kvq_status kvq_decode_attention_blocks_paged(const void* q, const kvq_cache* k_pool, const kvq_cache* v_pool,
+                                             const kvq_block_table* table, const int32_t* blocks, int32_t n_select,
+                                             const int32_t* row_seq, const int32_t* row_lens, int32_t rows, int32_t Hq,
+                                             float softmax_scale, void* out, int32_t out_dtype, void* workspace,
+                                             size_t workspace_bytes, int32_t* dev_status, void* stream) {
+  if (table == nullptr) return KVQ_ERR_INVALID_ARG;
+  return decode_blocks_impl(q, k_pool, v_pool, table, blocks, n_select, row_seq, row_lens, rows, Hq, softmax_scale, out,
+                            out_dtype, workspace, workspace_bytes, dev_status, stream);
+}
+
+size_t kvq_pages_workspace_bytes(int32_t n_pages, int32_t slots) {
+  if (n_pages <= 0 || n_pages > (1 << 24) || slots <= 0 || slots > 65536) return 0;
+  return pages_workspace_bytes(n_pages, slots);
+}
+
+kvq_status kvq_pages_reserve(const kvq_page_table* pages, const int32_t* add, void* workspace, size_t workspace_bytes,
+                             int32_t* dev_status, void* stream) {
+  const kvq_status s = page_table_ok(pages);
+  if (s != KVQ_OK) return s;
+  if (!list_ok(add, pages->slots)) return KVQ_ERR_INVALID_ARG;
+  if (!pages_workspace_ok(*pages, workspace, workspace_bytes)) return KVQ_ERR_WORKSPACE;
+  PagesArgs a;
+  a.t = *pages;
+  a.from = add;
+  a.ws = static_cast<int32_t*>(workspace);
+  a.status = dev_status;
+  return launch_pages_reserve(a, static_cast<cudaStream_t>(stream)) == cudaSuccess ? KVQ_OK : KVQ_ERR_CUDA;
+}
+
+kvq_status kvq_pages_fork(const kvq_page_table* pages, const kvq_cache* k_pool, const kvq_cache* v_pool,
+                          const kvq_bounds* bounds, const int32_t* from, const int32_t* to, int32_t n, void* workspace,
+                          size_t workspace_bytes, int32_t* dev_status, void* stream) {
+  PagesArgs a;
+  kvq_status s = page_table_ok(pages);
+  if (s == KVQ_OK) s = pools_ok(k_pool, v_pool, bounds, &a);
+  if (s != KVQ_OK) return s;
+  if (k_pool->B != pages->n_pages || !list_ok(from, n) || !list_ok(to, n) || n > pages->slots)
+    return KVQ_ERR_INVALID_ARG;
+  if (!pages_workspace_ok(*pages, workspace, workspace_bytes)) return KVQ_ERR_WORKSPACE;
+  if (n == 0) return KVQ_OK;
+  a.t = *pages;
+  a.from = from;
+  a.to = to;
+  a.n = n;
+  a.ws = static_cast<int32_t*>(workspace);
+  a.status = dev_status;
+  return launch_pages_fork(a, static_cast<cudaStream_t>(stream)) == cudaSuccess ? KVQ_OK : KVQ_ERR_CUDA;
+}
+
+kvq_status kvq_pages_free(const kvq_page_table* pages, const int32_t* which, int32_t n, int32_t* dev_status,
+                          void* stream) {
+  const kvq_status s = page_table_ok(pages);
+  if (s != KVQ_OK) return s;
+  if (!list_ok(which, n)) return KVQ_ERR_INVALID_ARG;
+  if (n == 0) return KVQ_OK;
+  PagesArgs a;
+  a.t = *pages;
+  a.from = which;
+  a.n = n;
+  a.status = dev_status;
+  return launch_pages_free(a, static_cast<cudaStream_t>(stream)) == cudaSuccess ? KVQ_OK : KVQ_ERR_CUDA;
+}
+
+kvq_status kvq_pages_compact(const kvq_page_table* pages, const kvq_cache* k_pool, const kvq_cache* v_pool,
+                             const kvq_bounds* bounds, int32_t* n_live, void* workspace, size_t workspace_bytes,
+                             int32_t* dev_status, void* stream) {
+  PagesArgs a;
+  kvq_status s = page_table_ok(pages);
+  if (s == KVQ_OK) s = pools_ok(k_pool, v_pool, bounds, &a);
+  if (s != KVQ_OK) return s;
+  if (k_pool->B != pages->n_pages || (reinterpret_cast<uintptr_t>(n_live) & 3u)) return KVQ_ERR_INVALID_ARG;
+  if (!pages_workspace_ok(*pages, workspace, workspace_bytes)) return KVQ_ERR_WORKSPACE;
+  a.t = *pages;
+  a.n_live = n_live;
+  a.ws = static_cast<int32_t*>(workspace);
+  a.status = dev_status;
+  return launch_pages_compact(a, static_cast<cudaStream_t>(stream)) == cudaSuccess ? KVQ_OK : KVQ_ERR_CUDA;
+}
+
+kvq_status kvq_copy_pages(const kvq_cache* k_pool, const kvq_cache* v_pool, const kvq_bounds* bounds,
+                          const int32_t* src, const int32_t* dst, int32_t n, int32_t* dev_status, void* stream) {
+  PagesArgs a = {};
+  const kvq_status s = pools_ok(k_pool, v_pool, bounds, &a);
+  if (s != KVQ_OK) return s;
+  if (!list_ok(src, n) || !list_ok(dst, n)) return KVQ_ERR_INVALID_ARG;
+  if (n == 0) return KVQ_OK;
+  a.from = src;
+  a.to = dst;
+  a.n = n;
+  a.status = dev_status;
+  return launch_copy_pages(a, static_cast<cudaStream_t>(stream)) == cudaSuccess ? KVQ_OK : KVQ_ERR_CUDA;
 }
 
 }  // extern "C"

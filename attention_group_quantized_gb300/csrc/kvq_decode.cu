@@ -105,9 +105,15 @@ struct DParams {
   // one, it is page bt[b * bt_stride + i] of a pool of pB pages of pT = 64
   const int32_t* bt;
   int32_t bt_stride, pB, pT;
-  // sliding window (WIN instantiations): a sequence's query sees its last
+  // sliding window (kWindow instantiations): a sequence's query sees its last
   // `window` tokens and its first `sinks`
   int32_t window, sinks;
+  // listed blocks (kListed instantiations): the B "sequences" are query rows,
+  // each with a sequence (null: its own index) among `seqs`, and sees its first
+  // seq_lens tokens that lie in the blocks blocks[row][KV head][n_select]
+  const int32_t* blocks;
+  const int32_t* row_seq;
+  int32_t n_select, seqs;
   float scale_log2;
   // per-call policy: tiles per CTA prefetched into L2 before the dependency
   // wait (0 .. kMaxL2Tiles), the bounded-wait limit, and the test-only issue
@@ -164,7 +170,8 @@ struct Smem {
   static constexpr int kOffBars = kOffEpi + ((static_cast<int>(sizeof(EpiBuf<D>)) + 15) / 16) * 16;
   static constexpr int kBars = (3 * kStages + 3) * 8;
   static constexpr int kFixed = kOffBars + kBars;
-  static size_t bytes(int B) { return 1024 + kFixed + static_cast<size_t>(B + 1) * 4 * 2; }
+  // (arrays of B + 1 words behind it: tile counts, lengths and, listed blocks, the rows' sequences)
+  static size_t bytes(int B, int arrays = 2) { return 1024 + kFixed + static_cast<size_t>(B + 1) * 4 * arrays; }
 };
 
 // tile flags (meta.z): tile index in bits 0-23, then
@@ -195,33 +202,44 @@ __device__ __forceinline__ void ffma2_b(float& d0, float& d1, float a, float b0,
       : "f"(a), "f"(b0), "f"(b1));
 }
 
+// What a query sees of its sequence: every token, a sliding window and sinks,
+// or the blocks of a list.
+enum { kAll = 0, kWindow = 1, kListed = 2 };
+
+// A listed block that is left out: past every length (capacities of listed
+// calls stay below it, and it fits the tile flags).
+constexpr int kNoTile = 0xFFFFFF;
+
 // The 64-token tiles of a sequence that its query sees, in order: without a
 // window all of them; with one, the sinks' tiles and then those from the
 // window's first token on.  Index i of that list is tile(i); the
-// work list, the split and the merge only ever see the indices.
+// work list, the split and the merge only ever see the indices.  With a list
+// they are as many as the list can have, the same for every KV head; which ones,
+// the issuer looks up (ListedTiles) and hands on with the copies.
 // (Eight 32K sequences, INT8, window 4096, four sinks: 75.7 MB in 20.7 us, 3.7
 // TB/s -- the pipeline of the call without a window on an eighth of the tiles,
 // so that its start and merge weigh more: 151 MB take 30.5 us, 4.95 TB/s.)
-template <bool WIN>
+template <int VIS>
 struct Visible {
   int n;               // tiles
-  int ns, skip;        // (WIN) index ns and later: tile i + skip
+  int ns, skip;        // (kWindow) index ns and later: tile i + skip
   __device__ __forceinline__ Visible(const DParams& p, int len) : ns(0), skip(0) {
     n = (len + kTile - 1) / kTile;
-    if constexpr (WIN) {
+    if constexpr (VIS == kListed) n = min(n, p.n_select);
+    if constexpr (VIS == kWindow) {
       const int fw = max(len - p.window, 0) / kTile;   // tile of the window's first token
       ns = min((min(p.sinks, len) + kTile - 1) / kTile, fw);
       skip = fw - ns;
       n -= skip;
     }
   }
-  __device__ __forceinline__ int tile(int i) const { return WIN && i >= ns ? i + skip : i; }
+  __device__ __forceinline__ int tile(int i) const { return VIS == kWindow && i >= ns ? i + skip : i; }
 };
 
 // Whether the query of a sequence of length len does not see token j < len.
-template <bool WIN>
+template <int VIS>
 __device__ __forceinline__ bool window_hides(const DParams& p, int len, int j) {
-  return WIN && j < len - p.window && j >= p.sinks;
+  return VIS == kWindow && j < len - p.window && j >= p.sinks;
 }
 
 using split::Cursor;
@@ -587,8 +605,8 @@ __device__ __forceinline__ void segment_end(const DParams& p, const EpiBuf<D>* e
 // the P.V products.  lim[u] = tokens of tile u inside the sequence.  The
 // running max m_run and the per-lane partial sums l_run are those of heads
 // 2t, 2t+1 -- the same heads as the lane's output accumulator columns.
-// WIN: rows from sk[u] to lo[u] - 1 of tile u lie before the window and are no sinks.
-template <int D, int BITS, int NT, bool WIN>
+// kWindow: rows from sk[u] to lo[u] - 1 of tile u lie before the window and are no sinks.
+template <int D, int BITS, int NT, int VIS>
 __device__ __forceinline__ void consume_tiles(const uint32_t (&st_s)[NT], const uint8_t* const (&st)[NT],
                                               const int (&lim)[NT], const int (&lo)[NT], const int (&sk)[NT], const uint32_t (&qa)[D / 16][2],
                                               const float (&qs)[D / 32][2], float (&O)[D / 16][4],
@@ -603,7 +621,7 @@ __device__ __forceinline__ void consume_tiles(const uint32_t (&st_s)[NT], const 
   for (int u = 0; u < NT; ++u) {
     if (r0 >= lim[u]) S[u][0] = S[u][1] = -INFINITY;
     if (r0 + 8 >= lim[u]) S[u][2] = S[u][3] = -INFINITY;
-    if constexpr (WIN) {
+    if constexpr (VIS == kWindow) {
       if (r0 < lo[u] && r0 >= sk[u]) S[u][0] = S[u][1] = -INFINITY;
       if (r0 + 8 < lo[u] && r0 + 8 >= sk[u]) S[u][2] = S[u][3] = -INFINITY;
     }
@@ -671,13 +689,13 @@ __device__ __forceinline__ void consume_tiles(const uint32_t (&st_s)[NT], const 
 // but they only choose which lines to prefetch (clamped into the cache), and
 // an L2 prefetch returns nothing to the program, so no result depends on
 // them.  Batches of more than 32 sequences skip the warm-up.
-template <int D, bool PAGED, bool WIN>
+template <int D, bool PAGED, int VIS>
 __device__ __forceinline__ void warm_l2(const DParams& p, int lane) {
   constexpr int G = D / 32;
   if (p.l2_warm <= 0 || p.B > 32) return;
   int len = lane < p.B ? p.seq_lens[lane] : 0;
   len = min(max(len, 0), p.Tcap);
-  const int n = Visible<WIN>(p, len).n;
+  const int n = Visible<VIS>(p, len).n;
   int incl = n;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
@@ -700,7 +718,7 @@ __device__ __forceinline__ void warm_l2(const DParams& p, int lane) {
   if (lane >= p.l2_warm || f >= f1 || b >= p.B || nb == 0) return;
   const int64_t off = f - static_cast<int64_t>(p.Hkv) * eb;
   const int kvh = static_cast<int>(off / nb);
-  const int i = Visible<WIN>(p, lb).tile(static_cast<int>(off % nb));
+  const int i = Visible<VIS>(p, lb).tile(static_cast<int>(off % nb));
   const int bits = p.bits[kvh];
   int pb = bs, pt = i * kTile;
   if constexpr (PAGED) {   // (a stale or bad page id only misdirects this prefetch)
@@ -717,12 +735,87 @@ __device__ __forceinline__ void warm_l2(const DParams& p, int lane) {
   prefetch_l2_bulk(p.v_sz + szoff * G, Smem<D>::kSzBytes);
 }
 
+// The copy issuer over listed blocks (one warp).  A tile's place takes two
+// dependent look-ups (the list's entry, then its page), so the lanes make them
+// for 32 tiles of the CTA's range at once; lane 0 then issues the copies.  The
+// tile index goes to the table warp with them, in the stage's meta word.
+template <int D, int RING>
+__device__ __forceinline__ void issue_listed(const DParams& p, uint8_t* smem, uint64_t* full, uint64_t* empty,
+                                             const int32_t* pre, const int32_t* lens, const int32_t* seqs, int64_t f0,
+                                             int ntiles, int lane) {
+  using L = Smem<D>;
+  constexpr int G = D / 32;
+  const int n_issue = p.issue_limit >= 0 && p.issue_limit < ntiles ? p.issue_limit : ntiles;   // (as in the kernel)
+  for (int k0 = 0; k0 < n_issue; k0 += 32) {
+    int store = 0, tile = kNoTile, bk = 0;   // the tile's block of the storage, its index, (row * Hkv + KV head, first)
+    bool starts = false;
+    if (k0 + lane < n_issue) {
+      const Cursor c = locate(f0 + k0 + lane, pre, p.B, p.Hkv);
+      const int len = lens[c.b], seq = seqs[c.b];
+      bk = c.b * p.Hkv + c.kvh;
+      starts = c.i == 0 || k0 + lane == 0;
+      const int32_t* list = p.blocks + static_cast<int64_t>(bk) * p.n_select;
+      if (KVQ_IN_RANGE(c.b < p.B && c.i < p.n_select, p.status)) {
+        const int t = list[c.i], before = c.i > 0 ? list[c.i - 1] : -1;
+        const int n = (len + kTile - 1) / kTile;
+        if (t >= 0 && t < n && (c.i == 0 || (before >= 0 && t > before))) tile = t;
+        else if (t != -1) report(p.status, KVQ_ERR_INVALID_ARG);
+      }
+      if (tile != kNoTile) {
+        store = seq * (p.pT / kTile) + tile;
+        if (p.bt != nullptr) {
+          store = KVQ_IN_RANGE(tile < p.bt_stride, p.status) ? p.bt[static_cast<int64_t>(seq) * p.bt_stride + tile] : 0;
+          if (store < 0 || store >= p.pB) {   // a page outside the pool: report, read page 0 instead
+            report(p.status, KVQ_ERR_INVALID_ARG);
+            store = 0;
+          }
+        }
+      }
+    }
+    const uint64_t pol = l2_evict_first_policy();
+    bool alive = true;
+    for (int j = 0; j < 32 && k0 + j < n_issue; ++j) {
+      const int k = k0 + j;
+      const int st_block = __shfl_sync(0xffffffffu, store, j), ti = __shfl_sync(0xffffffffu, tile, j);
+      const int seg = __shfl_sync(0xffffffffu, bk, j), first = __shfl_sync(0xffffffffu, starts ? 1 : 0, j);
+      int slot;
+      uint32_t par;
+      ring_pos<RING>(k, slot, par);
+      if (lane == 0 && k >= RING) alive = mbar_wait(&empty[slot], par ^ 1u, p.status, p.wait_ns);
+      if (__any_sync(0xffffffffu, !alive)) return;
+      if (lane != 0) continue;
+      uint8_t* st = smem + slot * L::kStageBytes;
+      const int row = seg / p.Hkv, kvh = seg - row * p.Hkv;
+      const int bits = p.bits[kvh];
+      const int Rb = D * bits / 8;
+      const int64_t per_head = static_cast<int64_t>(p.pB) * p.pT;
+      int32_t row0 = static_cast<int32_t>(p.plane[kvh] * per_head) + st_block * kTile;
+      int64_t szoff = kvh * per_head + static_cast<int64_t>(st_block) * kTile;
+      if (!KVQ_IN_RANGE(st_block >= 0 && (st_block + 1) * static_cast<int64_t>(kTile) <= per_head, p.status)) {
+        row0 = 0;
+        szoff = 0;
+      }
+      uint64_t* bar = &full[slot];
+      const uint32_t qbytes = first ? static_cast<uint32_t>(p.rep * D * 2) : 0u;
+      int64_t qoff = (static_cast<int64_t>(row) * p.Hq + kvh * p.rep) * D;
+      if (!KVQ_IN_RANGE(qoff >= 0 && qoff + p.rep * D <= static_cast<int64_t>(p.B) * p.Hq * D, p.status)) qoff = 0;
+      reinterpret_cast<int4*>(st + L::kOffMeta)->z = ti;   // (the table warp reads it once `full` completes)
+      mbar_arrive_expect_tx(bar, 2 * kTile * Rb + 2 * L::kSzBytes + qbytes);
+      if (first) bulk_g2s(st + L::kOffQ, p.q + qoff, qbytes, bar);
+      tma_2d_g2s_hint(st + L::kOffK, bits == 8 ? &p.tm_k8 : &p.tm_k4, 0, row0, bar, pol);
+      tma_2d_g2s_hint(st + L::kOffV, bits == 8 ? &p.tm_v8 : &p.tm_v4, 0, row0, bar, pol);
+      bulk_g2s_hint(st + L::kOffKsz, p.k_sz + szoff * G, L::kSzBytes, bar, pol);
+      bulk_g2s_hint(st + L::kOffVsz, p.v_sz + szoff * G, L::kSzBytes, bar, pol);
+    }
+  }
+}
+
 // PAGED: the tiles are pages of a pool found through p.bt (a separate
 // instantiation, so the contiguous kernel carries none of it).  RING: tiles
 // kept in flight into shared memory (the policy's ring depth, 2 or kStages).
-// WIN: only the tiles that a sliding window and its sinks leave visible (again
-// its own instantiation).
-template <int D, bool PAGED, int RING, bool WIN>
+// VIS: the tiles that a query sees (kWindow and kListed are their own
+// instantiations again; kListed finds its tiles' places whether paged or not).
+template <int D, bool PAGED, int RING, int VIS>
 __global__ void __launch_bounds__(kThreads, KVQ_DECODE_MIN_BLOCKS) decode_split_kernel(const __grid_constant__ DParams p) {
   using L = Smem<D>;
   constexpr int G = D / 32;
@@ -737,6 +830,7 @@ __global__ void __launch_bounds__(kThreads, KVQ_DECODE_MIN_BLOCKS) decode_split_
   uint64_t* gbar = epi_empty + 1;          // consumer-group barrier for the final piece
   int32_t* pre = reinterpret_cast<int32_t*>(smem + L::kFixed);
   int32_t* lens = pre + (p.B + 1);
+  int32_t* seqs = lens + (p.B + 1);        // (kListed)
 
   const int tid = threadIdx.x;
   const int w = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
@@ -759,7 +853,10 @@ __global__ void __launch_bounds__(kThreads, KVQ_DECODE_MIN_BLOCKS) decode_split_
     prefetch_tmap(&p.tm_k4);
     prefetch_tmap(&p.tm_v4);
   }
-  if (w == kWarps) warm_l2<D, PAGED, WIN>(p, lane);
+  // (the list of a kListed call is the kernel before's to write: nothing to warm)
+  if constexpr (VIS != kListed) {
+    if (w == kWarps) warm_l2<D, PAGED, VIS>(p, lane);
+  }
   // With programmatic dependent launch this kernel may start while the
   // previous kernel in the stream is finishing: wait for it (and its memory)
   // before the first global access whose data is used, then let the next one
@@ -774,6 +871,15 @@ __global__ void __launch_bounds__(kThreads, KVQ_DECODE_MIN_BLOCKS) decode_split_
     if (L0 < 0 || L0 > p.Tcap) {
       report(p.status, KVQ_ERR_INVALID_ARG);
       L0 = L0 < 0 ? 0 : p.Tcap;
+    }
+    if constexpr (VIS == kListed) {
+      const int seq = p.row_seq != nullptr ? p.row_seq[b] : b;
+      const bool ok = seq >= 0 && seq < p.seqs && p.seq_lens[b] <= p.Tcap;
+      if (!ok) {
+        report(p.status, KVQ_ERR_INVALID_ARG);
+        L0 = 0;
+      }
+      seqs[b] = ok ? seq : 0;
     }
     return L0;
   };
@@ -791,7 +897,7 @@ __global__ void __launch_bounds__(kThreads, KVQ_DECODE_MIN_BLOCKS) decode_split_
         len = small_b ? load_len(b) : lens[b];
         if (small_b) lens[b] = len;
       }
-      int n = Visible<WIN>(p, len).n;
+      int n = Visible<VIS>(p, len).n;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
         const int v = __shfl_up_sync(0xffffffffu, n, o);
@@ -832,6 +938,10 @@ __global__ void __launch_bounds__(kThreads, KVQ_DECODE_MIN_BLOCKS) decode_split_
     tc::reg_dealloc<kHelperRegs>();
     if (w == kWarps) {
       // ---------------- TMA issuer warp: lane 0 keeps RING tiles in flight ----------------
+      if constexpr (VIS == kListed) {
+        issue_listed<D, RING>(p, smem, full, empty, pre, lens, seqs, f0, ntiles, lane);
+        return;
+      }
       if (lane != 0) return;
       const uint64_t pol = l2_evict_first_policy();   // the cache is streamed once per call
       Cursor pc = locate(f0, pre, B, Hkv);
@@ -839,7 +949,7 @@ __global__ void __launch_bounds__(kThreads, KVQ_DECODE_MIN_BLOCKS) decode_split_
       // copies (a ring of registers), so the lookups overlap the stage waits
       Cursor pa = pc;
       auto page_id = [&](const Cursor& c) -> int {
-        const int i = Visible<WIN>(p, lens[c.b]).tile(c.i);
+        const int i = Visible<VIS>(p, lens[c.b]).tile(c.i);
         return KVQ_IN_RANGE(c.b < p.B && i < p.bt_stride, p.status)
                    ? p.bt[static_cast<int64_t>(c.b) * p.bt_stride + i] : 0;
       };
@@ -863,7 +973,7 @@ __global__ void __launch_bounds__(kThreads, KVQ_DECODE_MIN_BLOCKS) decode_split_
         uint8_t* st = smem + slot * L::kStageBytes;
         const int bits = p.bits[pc.kvh];
         const int Rb = D * bits / 8;
-        int pb = pc.b, pt = Visible<WIN>(p, lens[pc.b]).tile(pc.i) * kTile;
+        int pb = pc.b, pt = Visible<VIS>(p, lens[pc.b]).tile(pc.i) * kTile;
         if constexpr (PAGED) {
           pb = pg[0];
 #pragma unroll
@@ -919,7 +1029,8 @@ __global__ void __launch_bounds__(kThreads, KVQ_DECODE_MIN_BLOCKS) decode_split_
         const uint32_t* ksz = reinterpret_cast<const uint32_t*>(st + L::kOffKsz);
         const uint32_t* vsz = reinterpret_cast<const uint32_t*>(st + L::kOffVsz);
         const int len = lens[tc.b];
-        const int ti = Visible<WIN>(p, len).tile(tc.i);
+        const int ti = VIS == kListed ? reinterpret_cast<const int4*>(st + L::kOffMeta)->z
+                                      : Visible<VIS>(p, len).tile(tc.i);
         // Lane l takes tokens 2l and 2l+1 (all G groups of each: the raw words
         // are [token][group]) and writes their entries in the consumers'
         // fragment order: warp l/8; K table rows 2(l%4) and 2(l%4)+1, slot
@@ -936,7 +1047,7 @@ __global__ void __launch_bounds__(kThreads, KVQ_DECODE_MIN_BLOCKS) decode_split_
         load_words<G>(vw[1], vsz + (t0 + 1) * G);
 #pragma unroll
         for (int u = 0; u < 2; ++u)
-          if (ti * kTile + t0 + u >= len || window_hides<WIN>(p, len, ti * kTile + t0 + u)) {   // not seen: zero scales
+          if (ti * kTile + t0 + u >= len || window_hides<VIS>(p, len, ti * kTile + t0 + u)) {   // not seen: zero scales
 #pragma unroll
             for (int grp = 0; grp < G; ++grp) kw[u][grp] = vw[u][grp] = 0u;
           }
@@ -1039,16 +1150,16 @@ __global__ void __launch_bounds__(kThreads, KVQ_DECODE_MIN_BLOCKS) decode_split_
       const uint8_t* const sp[2] = {st0, st1};
       const int lim[2] = {tile_lim(meta.z), tile_lim(f1)};
       const int lo[2] = {tile_lo(meta.z), tile_lo(f1)}, sk[2] = {tile_sk(meta.z), tile_sk(f1)};
-      if (!four) consume_tiles<D, 8, 2, WIN>(ss, sp, lim, lo, sk, qa, qs, O, Z, m_run, l_run, la, w, g, t);
-      else consume_tiles<D, 4, 2, WIN>(ss, sp, lim, lo, sk, qa, qs, O, Z, m_run, l_run, la, w, g, t);
+      if (!four) consume_tiles<D, 8, 2, VIS>(ss, sp, lim, lo, sk, qa, qs, O, Z, m_run, l_run, la, w, g, t);
+      else consume_tiles<D, 4, 2, VIS>(ss, sp, lim, lo, sk, qa, qs, O, Z, m_run, l_run, la, w, g, t);
       fend = f1;
       nt = 2;
     } else {
       const uint32_t ss[1] = {smem_u32(st0)};
       const uint8_t* const sp[1] = {st0};
       const int lim[1] = {tile_lim(meta.z)}, lo[1] = {tile_lo(meta.z)}, sk[1] = {tile_sk(meta.z)};
-      if (!four) consume_tiles<D, 8, 1, WIN>(ss, sp, lim, lo, sk, qa, qs, O, Z, m_run, l_run, la, w, g, t);
-      else consume_tiles<D, 4, 1, WIN>(ss, sp, lim, lo, sk, qa, qs, O, Z, m_run, l_run, la, w, g, t);
+      if (!four) consume_tiles<D, 8, 1, VIS>(ss, sp, lim, lo, sk, qa, qs, O, Z, m_run, l_run, la, w, g, t);
+      else consume_tiles<D, 4, 1, VIS>(ss, sp, lim, lo, sk, qa, qs, O, Z, m_run, l_run, la, w, g, t);
       fend = meta.z;
       nt = 1;
     }
@@ -1128,12 +1239,15 @@ int ctas_per_sm() {
     int n = 0;
     const size_t sm = Smem<D>::bytes(64);
     const int lim = static_cast<int>(Smem<D>::bytes(4096));
-    cudaFuncSetAttribute(decode_split_kernel<D, PAGED, 2, false>, cudaFuncAttributeMaxDynamicSharedMemorySize, lim);
-    cudaFuncSetAttribute(decode_split_kernel<D, PAGED, kStages, false>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    cudaFuncSetAttribute(decode_split_kernel<D, PAGED, 2, kAll>, cudaFuncAttributeMaxDynamicSharedMemorySize, lim);
+    cudaFuncSetAttribute(decode_split_kernel<D, PAGED, kStages, kAll>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                          lim);
-    cudaFuncSetAttribute(decode_split_kernel<D, PAGED, kStages, true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    cudaFuncSetAttribute(decode_split_kernel<D, PAGED, kStages, kWindow>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                          lim);
-    if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, decode_split_kernel<D, PAGED, kStages, false>, kThreads,
+    if constexpr (!PAGED)
+      cudaFuncSetAttribute(decode_split_kernel<D, false, kStages, kListed>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                           static_cast<int>(Smem<D>::bytes(4096, 3)));
+    if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, decode_split_kernel<D, PAGED, kStages, kAll>, kThreads,
                                                       sm) !=
             cudaSuccess ||
         n < 1)
@@ -1153,10 +1267,10 @@ bool regs_ok() {
       cudaFuncAttributes fa;
       return cudaFuncGetAttributes(&fa, kernel) == cudaSuccess && fa.numRegs == 128;
     };
-    cached = (has128(decode_split_kernel<D, PAGED, 2, false>) && has128(decode_split_kernel<D, PAGED, kStages, false>) &&
-              has128(decode_split_kernel<D, PAGED, kStages, true>))
-                 ? 1
-                 : 0;
+    bool ok = has128(decode_split_kernel<D, PAGED, 2, kAll>) && has128(decode_split_kernel<D, PAGED, kStages, kAll>) &&
+              has128(decode_split_kernel<D, PAGED, kStages, kWindow>);
+    if constexpr (!PAGED) ok = ok && has128(decode_split_kernel<D, false, kStages, kListed>);
+    cached = ok ? 1 : 0;
   }
   return cached == 1;
 }
@@ -1169,17 +1283,20 @@ cudaError_t launch_split(const DParams& p, int C, int B, int ring, cudaStream_t 
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(C));
   cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = Smem<D>::bytes(B);
+  cfg.dynamicSmemBytes = Smem<D>::bytes(B, p.blocks != nullptr ? 3 : 2);
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  // (a windowed call takes the default ring depth: it has no policy argument)
-  if (p.window > 0) return cudaLaunchKernelEx(&cfg, decode_split_kernel<D, PAGED, kStages, true>, p);
-  return ring == 2 ? cudaLaunchKernelEx(&cfg, decode_split_kernel<D, PAGED, 2, false>, p)
-                   : cudaLaunchKernelEx(&cfg, decode_split_kernel<D, PAGED, kStages, false>, p);
+  // (windowed calls and those with a list take the default ring depth: they have no policy argument)
+  if constexpr (!PAGED) {
+    if (p.blocks != nullptr) return cudaLaunchKernelEx(&cfg, decode_split_kernel<D, false, kStages, kListed>, p);
+  }
+  if (p.window > 0) return cudaLaunchKernelEx(&cfg, decode_split_kernel<D, PAGED, kStages, kWindow>, p);
+  return ring == 2 ? cudaLaunchKernelEx(&cfg, decode_split_kernel<D, PAGED, 2, kAll>, p)
+                   : cudaLaunchKernelEx(&cfg, decode_split_kernel<D, PAGED, kStages, kAll>, p);
 }
 
 }  // namespace
@@ -1207,10 +1324,12 @@ kvq_status launch_decode(const DecodeArgs& a, cudaStream_t stream) {
   // K.B x K.Tcap is the storage (a page pool when a block table is given);
   // B x Tcap the sequences and their capacity
   const int D = K.D, Hkv = K.Hkv;
-  const int B = a.bt != nullptr ? a.bt_B : K.B;
+  const bool listed = a.blocks != nullptr;   // (B: the query rows then)
+  const int seqs = a.bt != nullptr ? a.bt_B : K.B;
+  const int B = listed ? a.rows : seqs;
   const int Tcap = a.bt != nullptr ? a.bt_max_pages * kTile : K.Tcap;
   if (B > 4096) return KVQ_ERR_UNSUPPORTED;  // dynamic shared memory was sized for B <= 4096
-  const bool paged = a.bt != nullptr;
+  const bool paged = a.bt != nullptr && !listed;
   const bool regs = D == 128 ? (paged ? regs_ok<128, true>() : regs_ok<128, false>())
                              : (paged ? regs_ok<64, true>() : regs_ok<64, false>());
   if (!regs) return KVQ_ERR_UNSUPPORTED;
@@ -1256,6 +1375,10 @@ kvq_status launch_decode(const DecodeArgs& a, cudaStream_t stream) {
   p.pT = K.Tcap;
   p.window = a.window;
   p.sinks = a.sinks;
+  p.blocks = a.blocks;
+  p.row_seq = a.row_seq;
+  p.n_select = a.n_select;
+  p.seqs = seqs;
   const float scale = a.softmax_scale > 0.0f ? a.softmax_scale : 1.0f / sqrtf(static_cast<float>(D));
   p.scale_log2 = scale * 1.4426950408889634f;
   for (int h = 0; h < KVQ_MAX_HKV; ++h) {

@@ -92,6 +92,25 @@ struct AppendChunkArgs {
 };
 cudaError_t launch_append_chunk(const AppendChunkArgs& a, cudaStream_t stream);
 
+// The chunk's queries normed and rotated, its keys and values into the caches.
+struct RotateArgs {
+  const uint16_t* q;
+  int64_t sq_row, sq_head;
+  const uint16_t* k_new;
+  const uint16_t* v_new;
+  int64_t s_row, s_head;
+  ChunkDesc chunk;
+  kvq_rotation rot;
+  int32_t Hq;
+  const kvq_cache* k;
+  const kvq_cache* v;
+  HeadLayout layout;                // shared by K and V
+  uint16_t* q_out;
+  bool zero_rest;                   // query rows of no usable sequence become zeros
+  int32_t* status;
+};
+cudaError_t launch_rotate_append(const RotateArgs& a, cudaStream_t stream);
+
 // The chunk's positions of one cache as values.
 struct DequantizeArgs {
   const kvq_cache* src;
@@ -126,6 +145,37 @@ struct ChunkAttnArgs {
 size_t chunk_workspace_bytes(int rows, int B, int Hq, int Hkv, int D);
 kvq_status launch_chunk_attention(const ChunkAttnArgs& a, cudaStream_t stream);
 
+// The bounds of the blocks that hold a chunk's positions.
+struct BoundsArgs {
+  const kvq_cache* k;
+  HeadLayout layout;
+  ChunkDesc chunk;
+  kvq_bounds bounds;
+  int32_t* status;
+};
+cudaError_t launch_block_bounds(const BoundsArgs& a, cudaStream_t stream);
+cudaError_t launch_bounds_values(const kvq_cache& k, const kvq_bounds& bounds, const int32_t* blocks, int32_t n,
+                                 float* out, int32_t* status, cudaStream_t stream);
+
+constexpr int kMaxRows = 4096;      // query rows of a selection and of the attention over it
+constexpr int kMaxSelect = 65536;   // blocks of one row
+// Blocks for each row and KV head.
+struct SelectArgs {
+  const uint16_t* q;
+  const kvq_cache* k;
+  kvq_bounds bounds;
+  const int32_t* bt = nullptr;      // optional block table
+  int32_t seqs, bt_max_pages = 0, cap;
+  const int32_t* row_seq;           // null: row r is sequence r
+  const int32_t* row_lens;
+  int32_t rows, Hq, n_select, first, last;
+  int32_t* blocks;
+  void* ws;
+  int32_t* status;
+};
+size_t select_workspace_bytes(int rows, int Hkv, int64_t cap);
+cudaError_t launch_select_blocks(const SelectArgs& a, cudaStream_t stream);
+
 struct DecodeArgs {
   const uint16_t* q;
   const kvq_cache* k;
@@ -144,6 +194,11 @@ struct DecodeArgs {
   int32_t bt_B = 0, bt_max_pages = 0;
   // sliding window (0: none) and leading tokens that stay visible with it
   int32_t window = 0, sinks = 0;
+  // listed blocks [rows][Hkv][n_select] (null: every token): seq_lens is then
+  // the rows' lengths, row_seq their sequences (null: row r is sequence r)
+  const int32_t* blocks = nullptr;
+  const int32_t* row_seq = nullptr;
+  int32_t rows = 0, n_select = 0;
   Policy pol;
 };
 // Number of persistent split CTAs on the current device for head dim D.
@@ -169,6 +224,27 @@ struct PrefillArgs {
   Policy pol;
 };
 kvq_status launch_prefill(const PrefillArgs& a, cudaStream_t stream);
+
+// Page tables (kvq_page_table) and their pools.
+struct PagesArgs {
+  kvq_page_table t;
+  const kvq_cache* k = nullptr;
+  const kvq_cache* v = nullptr;
+  HeadLayout layout;                // shared by K and V
+  kvq_bounds bounds = {nullptr, nullptr};
+  const int32_t* from = nullptr;    // fork: from, to; free: which; reserve: add; copy: src, dst
+  const int32_t* to = nullptr;
+  int32_t n = 0;
+  int32_t* n_live = nullptr;
+  int32_t* ws = nullptr;
+  int32_t* status = nullptr;
+};
+size_t pages_workspace_bytes(int n_pages, int slots);
+cudaError_t launch_pages_reserve(const PagesArgs& a, cudaStream_t stream);
+cudaError_t launch_pages_fork(const PagesArgs& a, cudaStream_t stream);
+cudaError_t launch_pages_free(const PagesArgs& a, cudaStream_t stream);
+cudaError_t launch_pages_compact(const PagesArgs& a, cudaStream_t stream);
+cudaError_t launch_copy_pages(const PagesArgs& a, cudaStream_t stream);
 
 cudaError_t launch_tile_mask(uint8_t* mask, int nT, int num, int den, uint64_t seed, cudaStream_t stream);
 

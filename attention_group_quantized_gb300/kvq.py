@@ -21,7 +21,8 @@ DEBUG_LIB_PATH = os.path.join(HERE, "libkvq_debug.so")
 
 KVQ_OK = 0
 STATUS_NAMES = {0: "ok", 1: "invalid argument", 2: "unsupported", 3: "CUDA error",
-                4: "workspace", 5: "timeout", 6: "non-finite", 7: "index check (debug build)"}
+                4: "workspace", 5: "timeout", 6: "non-finite", 7: "index check (debug build)",
+                8: "too few free pages"}
 OUT_F32 = 0
 OUT_BF16 = 1
 GROUP = 32
@@ -36,7 +37,11 @@ EXPORTS = ("kvq_cache_codes_bytes", "kvq_cache_sz_bytes", "kvq_cache_head_offset
            "kvq_allocate_head_bits", "kvq_status_str", "kvq_policy_default", "kvq_decode_attention_ex",
            "kvq_prefill_attention_ex", "kvq_append_chunk", "kvq_append_chunk_paged", "kvq_dequantize",
            "kvq_dequantize_paged", "kvq_chunk_workspace_bytes", "kvq_chunk_attention", "kvq_chunk_attention_paged", "kvq_chunk_attention_ex",
-           "kvq_decode_attention_window", "kvq_decode_attention_window_paged")
+           "kvq_decode_attention_window", "kvq_decode_attention_window_paged", "kvq_rotate_append",
+           "kvq_rotate_append_paged", "kvq_bounds_bytes", "kvq_block_bounds", "kvq_block_bounds_paged",
+           "kvq_bounds_values", "kvq_select_workspace_bytes", "kvq_select_blocks", "kvq_select_blocks_paged",
+           "kvq_decode_attention_blocks", "kvq_decode_attention_blocks_paged", "kvq_pages_workspace_bytes",
+           "kvq_pages_reserve", "kvq_pages_fork", "kvq_pages_free", "kvq_pages_compact", "kvq_copy_pages")
 
 
 class CBlockTable(ctypes.Structure):
@@ -143,6 +148,28 @@ def lib() -> ctypes.CDLL:
         L.kvq_decode_attention_window.restype = I32
         L.kvq_decode_attention_window_paged.argtypes = [P, CP, CP, P, P, I32, F32, I32, I32, P, I32, P, SZ, P, P]
         L.kvq_decode_attention_window_paged.restype = I32
+        # (rotations, bounds and page tables too: their bytes)
+        L.kvq_rotate_append.argtypes = [P, I64, I64, P, P, I64, I64, P, P, I32, CP, CP, P, I32, P, P]
+        L.kvq_rotate_append_paged.argtypes = [P, I64, I64, P, P, I64, I64, P, P, I32, CP, CP, P, P, I32, P, P]
+        L.kvq_bounds_bytes.argtypes = [CP, I32]; L.kvq_bounds_bytes.restype = I64
+        L.kvq_block_bounds.argtypes = [CP, P, P, P, P]
+        L.kvq_block_bounds_paged.argtypes = [CP, P, P, P, P, P]
+        L.kvq_bounds_values.argtypes = [CP, P, P, I32, P, P, P]
+        L.kvq_select_workspace_bytes.argtypes = [I32, I32, I32]; L.kvq_select_workspace_bytes.restype = SZ
+        L.kvq_select_blocks.argtypes = [P, CP, P, P, P, I32, I32, I32, I32, I32, P, P, SZ, P, P]
+        L.kvq_select_blocks_paged.argtypes = [P, CP, P, P, P, P, I32, I32, I32, I32, I32, P, P, SZ, P, P]
+        L.kvq_decode_attention_blocks.argtypes = [P, CP, CP, P, I32, P, P, I32, I32, F32, P, I32, P, SZ, P, P]
+        L.kvq_decode_attention_blocks_paged.argtypes = [P, CP, CP, P, P, I32, P, P, I32, I32, F32, P, I32, P, SZ, P, P]
+        L.kvq_pages_workspace_bytes.argtypes = [I32, I32]; L.kvq_pages_workspace_bytes.restype = SZ
+        L.kvq_pages_reserve.argtypes = [P, P, P, SZ, P, P]
+        L.kvq_pages_fork.argtypes = [P, CP, CP, P, P, P, I32, P, SZ, P, P]
+        L.kvq_pages_free.argtypes = [P, P, I32, P, P]
+        L.kvq_pages_compact.argtypes = [P, CP, CP, P, P, P, SZ, P, P]
+        L.kvq_copy_pages.argtypes = [CP, CP, P, P, P, I32, P, P]
+        for name in ("rotate_append", "rotate_append_paged", "block_bounds", "block_bounds_paged", "bounds_values",
+                     "select_blocks", "select_blocks_paged", "decode_attention_blocks", "decode_attention_blocks_paged",
+                     "pages_reserve", "pages_fork", "pages_free", "pages_compact", "copy_pages"):
+            getattr(L, "kvq_" + name).restype = I32
         _LIB = L
     return _LIB
 
@@ -849,3 +876,395 @@ def decode_attention_window_paged(q, k_pool: QuantCache, v_pool: QuantCache, blo
     """decode_attention_window over page pools through a block table."""
     return _decode_window(q, k_pool, v_pool, block_table, seq_lens, window, sinks, softmax_scale, out, out_dtype,
                           workspace, status, stream)
+
+
+# ---------------------------------------------------------------------------
+# from projections to the cache: norms, rotation, append
+# ---------------------------------------------------------------------------
+
+_pack_rotation = struct.Struct("@PPPiiif").pack   # kvq_rotation
+
+
+def _same_device(device: int, *tensors):
+    for t in tensors:
+        if t is not None and t.get_device() != device:
+            _bad("tensors on different devices")
+
+
+def _rotation(rotary, q_weight, k_weight, eps: float, interleaved: bool, D: int, device: int) -> bytes:
+    torch = _torch()
+    for w in (q_weight, k_weight):
+        if w is not None and (w.dtype != torch.bfloat16 or tuple(w.shape) != (D,) or not w.is_contiguous()):
+            _bad("norm weights: bf16 [D], contiguous")
+    if rotary is not None and (rotary.dtype != torch.float32 or rotary.dim() != 2 or not rotary.is_contiguous()):
+        _bad("rotary: fp32 [positions][rot_dim], contiguous")
+    _same_device(device, rotary, q_weight, k_weight)
+    ptr = lambda t: 0 if t is None else t.data_ptr()
+    positions, rot = (0, 0) if rotary is None else rotary.shape
+    return _pack_rotation(ptr(rotary), ptr(q_weight), ptr(k_weight), _tokens(positions), _tokens(rot),
+                          1 if interleaved else 0, eps)
+
+
+def _rotate_append(q, k_new, v_new, k: QuantCache, v: QuantCache, block_table, start, seq_lens, rotary, q_weight, k_weight,
+                   eps, interleaved, out, status, stream):
+    if q.dim() != 3:
+        _bad("q: bf16 [rows][Hq][D]")
+    rows, Hq, D = q.shape
+    _packed(q, Hq, k.D, "q")
+    _packed(k_new, k.Hkv, k.D, "k_new")
+    _packed(v_new, k.Hkv, k.D, "v_new")
+    if k_new.shape[0] != rows or v_new.shape[0] != rows or k_new.stride() != v_new.stride():
+        _bad("q, k_new and v_new: the same rows; k_new and v_new: the same strides")
+    bt = _block_table(block_table)
+    dev = _on_current_device(q, k_new, v_new, k.codes, k.sz, v.codes, v.sz, start, seq_lens)
+    rot = _rotation(rotary, q_weight, k_weight, eps, interleaved, D, dev)
+    rest = _ZERO_REST if out is None else 0
+    out = _out(out, (rows, Hq, D), OUT_BF16, q, "rotate_append", stream)
+    ch = _chunk(start, seq_lens, rows, None)
+    sq_row, sq_head, _ = q.stride()
+    s_row, s_head, _ = k_new.stride()
+    if bt is None:
+        st = lib().kvq_rotate_append(q.data_ptr(), sq_row, sq_head, k_new.data_ptr(), v_new.data_ptr(), s_row, s_head, ch,
+                                     rot, Hq, k.c_struct(), v.c_struct(), out.data_ptr(), OUT_BF16 | rest,
+                                     _status_on(status, dev), _stream_on(stream, dev))
+        _check(st, "kvq_rotate_append")
+    else:
+        _on_current_device(block_table)
+        st = lib().kvq_rotate_append_paged(q.data_ptr(), sq_row, sq_head, k_new.data_ptr(), v_new.data_ptr(), s_row, s_head,
+                                           ch, rot, Hq, k.c_struct(), v.c_struct(), bt, out.data_ptr(), OUT_BF16 | rest,
+                                           _status_on(status, dev), _stream_on(stream, dev))
+        _check(st, "kvq_rotate_append_paged")
+    return out
+
+
+def rotate_append(q, k_new, v_new, k: QuantCache, v: QuantCache, start, seq_lens, rotary=None, q_weight=None,
+                  k_weight=None, eps: float = 1e-6, interleaved: bool = False, out=None, status=None, stream=None):
+    """Packed projected rows q bf16 [rows][Hq][D] and k_new/v_new bf16 [rows][Hkv][D] (row and head strides free: slices
+    of a fused projection's output) on their way to attention, in one pass: queries and keys normed per head (with
+    q_weight / k_weight bf16 [D]) and rotated by their positions (rotary fp32 [positions][rot_dim]: the cosines, then the
+    sines, of each), queries returned [rows][Hq][D], keys and values appended as append_chunk does it.
+    interleaved: a pair is channels 2i and 2i + 1, else i and i + rot_dim / 2.  Rows that no usable sequence has are
+    zeros, or with `out` given (which may be q itself, where it is contiguous) left as they are."""
+    return _rotate_append(q, k_new, v_new, k, v, None, start, seq_lens, rotary, q_weight, k_weight, eps, interleaved, out,
+                          status, stream)
+
+
+def rotate_append_paged(q, k_new, v_new, k_pool: QuantCache, v_pool: QuantCache, block_table, start, seq_lens, rotary=None,
+                        q_weight=None, k_weight=None, eps: float = 1e-6, interleaved: bool = False, out=None, status=None,
+                        stream=None):
+    """rotate_append into page pools through a block table."""
+    return _rotate_append(q, k_new, v_new, k_pool, v_pool, block_table, start, seq_lens, rotary, q_weight, k_weight, eps,
+                          interleaved, out, status, stream)
+
+
+# ---------------------------------------------------------------------------
+# attention over selected blocks
+# ---------------------------------------------------------------------------
+
+@dataclass
+class BlockBounds:
+    """Channel bounds of a K cache's 64-token blocks (see kvq_bounds), backed by torch tensors."""
+    codes: "object"           # torch.int8 [Hkv][blocks][D / 32][2][32]
+    scales: "object"          # torch.float32 [Hkv][blocks][D / 32]
+
+
+_pack_bounds = struct.Struct("@PP").pack   # kvq_bounds
+
+
+def empty_bounds(k: QuantCache) -> BlockBounds:
+    """Bounds for every block of a K cache (or page pool), zero-filled."""
+    torch = _torch()
+    blocks, G = k.B * (k.Tcap // TILE_TOKENS), k.D // GROUP
+    return BlockBounds(torch.zeros((k.Hkv, blocks, G, 2, GROUP), dtype=torch.int8, device=k.codes.device),
+                       torch.zeros((k.Hkv, blocks, G), dtype=torch.float32, device=k.codes.device))
+
+
+def _bounds(bounds, k: QuantCache, device: int):
+    if bounds is None:
+        return None
+    torch = _torch()
+    G = k.D // GROUP
+    blocks = k.B * (k.Tcap // TILE_TOKENS)
+    c, s = bounds.codes, bounds.scales
+    if (c.dtype != torch.int8 or tuple(c.shape) != (k.Hkv, blocks, G, 2, GROUP) or not c.is_contiguous()
+            or s.dtype != torch.float32 or tuple(s.shape) != (k.Hkv, blocks, G) or not s.is_contiguous()):
+        _bad("bounds: those of this cache's shape (empty_bounds)")
+    _same_device(device, c, s)
+    return _pack_bounds(c.data_ptr(), s.data_ptr())
+
+
+def _block_bounds(k: QuantCache, bounds: BlockBounds, block_table, start, seq_lens, rows: int, status, stream):
+    bt = _block_table(block_table)
+    dev = _on_current_device(k.codes, k.sz, start, seq_lens)
+    bb = _bounds(bounds, k, dev)
+    ch = _chunk(start, seq_lens, rows, None)
+    if bt is None:
+        st = lib().kvq_block_bounds(k.c_struct(), ch, bb, _status_on(status, dev), _stream_on(stream, dev))
+        _check(st, "kvq_block_bounds")
+    else:
+        _on_current_device(block_table)
+        st = lib().kvq_block_bounds_paged(k.c_struct(), ch, bt, bb, _status_on(status, dev), _stream_on(stream, dev))
+        _check(st, "kvq_block_bounds_paged")
+
+
+def block_bounds(k: QuantCache, bounds: BlockBounds, start, seq_lens, rows: int, status=None, stream=None):
+    """Recompute the bounds of the blocks that a chunk's new tokens lie in (call it after the append); start the running
+    sum of seq_lens does whole sequences.  rows: the chunk's packed rows."""
+    _block_bounds(k, bounds, None, start, seq_lens, rows, status, stream)
+
+
+def block_bounds_paged(k_pool: QuantCache, bounds: BlockBounds, block_table, start, seq_lens, rows: int, status=None,
+                       stream=None):
+    """block_bounds over a page pool through a block table."""
+    _block_bounds(k_pool, bounds, block_table, start, seq_lens, rows, status, stream)
+
+
+def bounds_values(bounds: BlockBounds, blocks, out=None, status=None, stream=None):
+    """The greatest and least values that listed storage blocks' bounds stand for: fp32 [Hkv][n][2][D] of blocks
+    int32 [n] (a pool's page ids, or b * Tcap / 64 + i)."""
+    torch = _torch()
+    Hkv, n_blocks, G = bounds.scales.shape
+    if blocks.dtype != torch.int32 or blocks.dim() != 1 or not blocks.is_contiguous():
+        _bad("blocks: int32 [n], contiguous")
+    n = blocks.shape[0]
+    dev = _on_current_device(bounds.codes, bounds.scales, blocks)
+    shape = QuantCache(bounds.codes, bounds.scales, np.full(Hkv, 8, np.int8), n_blocks, Hkv, TILE_TOKENS, G * GROUP)
+    bb = _bounds(bounds, shape, dev)
+    out = _out(out, (Hkv, n, 2, G * GROUP), OUT_F32, bounds.codes, "bounds_values", stream)
+    st = lib().kvq_bounds_values(shape.c_struct(), bb, blocks.data_ptr(), n, out.data_ptr(), _status_on(status, dev),
+                                 _stream_on(stream, dev))
+    _check(st, "kvq_bounds_values")
+    return out
+
+
+def select_workspace(rows: int, Hkv: int, capacity: int, device="cuda"):
+    """A zero-filled workspace for select_blocks: up to `rows` query rows over sequences of up to `capacity` tokens (the
+    cache's Tcap, or 64 times the block table's pages)."""
+    import torch
+    n = int(lib().kvq_select_workspace_bytes(rows, Hkv, _tokens(capacity)))
+    if n == 0:
+        raise KvqError(1, "kvq_select_workspace_bytes: invalid shape")
+    return torch.zeros(n, dtype=torch.uint8, device=device)
+
+
+def _query_rows(q, k: QuantCache, row_lens, row_seq):
+    torch = _torch()
+    if q.dim() != 3 or q.dtype != torch.bfloat16 or not q.is_contiguous() or q.shape[2] != k.D:
+        _bad("q: contiguous bf16 [rows][Hq][D]")
+    for x in (row_lens, row_seq):
+        if x is not None and (x.dtype != torch.int32 or x.dim() != 1 or x.shape[0] != q.shape[0] or not x.is_contiguous()):
+            _bad("row_lens, row_seq: int32 [rows], contiguous")
+    return q.shape
+
+
+def _select_blocks(q, k: QuantCache, bounds: BlockBounds, block_table, row_lens, n_select, first, last, row_seq, out,
+                   workspace, status, stream):
+    torch = _torch()
+    rows, Hq, D = _query_rows(q, k, row_lens, row_seq)
+    bt = _block_table(block_table)
+    dev = _on_current_device(q, k.codes, row_lens)
+    _same_device(dev, row_seq, block_table)
+    bb = _bounds(bounds, k, dev)
+    shape = (rows, k.Hkv, n_select)
+    if out is None:
+        if not 1 <= n_select <= 65536:
+            _bad("n_select: 1 .. 65536")
+        out = _made_on(stream, lambda: torch.empty(shape, dtype=torch.int32, device=q.device))
+    elif tuple(out.shape) != shape or out.dtype != torch.int32 or not out.is_contiguous() or out.get_device() != dev:
+        _bad("select_blocks: out int32 [rows][Hkv][n_select], contiguous, on the inputs' device")
+    cap = k.Tcap if bt is None else TILE_TOKENS * block_table.shape[1]
+    workspace = _workspace(workspace, dev, stream, select_workspace, rows, k.Hkv, cap, q.device)
+    ws_n = workspace.numel() * workspace.element_size()
+    first, last = _tokens(first), _tokens(last)
+    seq_p = None if row_seq is None else row_seq.data_ptr()
+    if bt is None:
+        st = lib().kvq_select_blocks(q.data_ptr(), k.c_struct(), bb, seq_p, row_lens.data_ptr(), rows, Hq, n_select, first,
+                                     last, out.data_ptr(), workspace.data_ptr(), ws_n, _status_on(status, dev),
+                                     _stream_on(stream, dev))
+        _check(st, "kvq_select_blocks")
+    else:
+        st = lib().kvq_select_blocks_paged(q.data_ptr(), k.c_struct(), bb, bt, seq_p, row_lens.data_ptr(), rows, Hq,
+                                           n_select, first, last, out.data_ptr(), workspace.data_ptr(), ws_n,
+                                           _status_on(status, dev), _stream_on(stream, dev))
+        _check(st, "kvq_select_blocks_paged")
+    return out
+
+
+def select_blocks(q, k: QuantCache, bounds: BlockBounds, row_lens, n_select: int, first: int = 1, last: int = 1,
+                  row_seq=None, out=None, workspace=None, status=None, stream=None):
+    """For each query row q bf16 [rows][Hq][D] and KV head, the n_select 64-token blocks of the row's sequence with the
+    highest scores from their bounds, the first `first` and last `last` ones always among them: int32
+    [rows][Hkv][n_select], ascending, -1 where there are fewer.  row_lens int32 [rows]: the tokens that each row sees;
+    row_seq int32 [rows]: its sequence (None: row r is sequence r).  Up to 8 query heads per KV head."""
+    return _select_blocks(q, k, bounds, None, row_lens, n_select, first, last, row_seq, out, workspace, status, stream)
+
+
+def select_blocks_paged(q, k_pool: QuantCache, bounds: BlockBounds, block_table, row_lens, n_select: int, first: int = 1,
+                        last: int = 1, row_seq=None, out=None, workspace=None, status=None, stream=None):
+    """select_blocks over a page pool through a block table."""
+    return _select_blocks(q, k_pool, bounds, block_table, row_lens, n_select, first, last, row_seq, out, workspace, status,
+                          stream)
+
+
+def _decode_blocks(q, k: QuantCache, v: QuantCache, block_table, blocks, row_lens, row_seq, softmax_scale, out, out_dtype,
+                   workspace, status, stream):
+    torch = _torch()
+    rows, Hq, D = _query_rows(q, k, row_lens, row_seq)
+    if (blocks.dtype != torch.int32 or blocks.dim() != 3 or blocks.shape[0] != rows or blocks.shape[1] != k.Hkv
+            or not blocks.is_contiguous()):
+        _bad("blocks: int32 [rows][Hkv][n_select], contiguous")
+    bt = _block_table(block_table)
+    dev = _on_current_device(q, k.codes, k.sz, v.codes, v.sz, blocks, row_lens)
+    _same_device(dev, row_seq, block_table)
+    out = _out(out, (rows, Hq, D), out_dtype, q, "decode_attention_blocks", stream)
+    workspace = _workspace(workspace, dev, stream, decode_workspace, rows, Hq, k.Hkv, D, q.device)
+    ws_n = workspace.numel() * workspace.element_size()
+    seq_p = None if row_seq is None else row_seq.data_ptr()
+    n_select = blocks.shape[2]
+    if bt is None:
+        st = lib().kvq_decode_attention_blocks(q.data_ptr(), k.c_struct(), v.c_struct(), blocks.data_ptr(), n_select,
+                                               seq_p, row_lens.data_ptr(), rows, Hq, softmax_scale, out.data_ptr(),
+                                               out_dtype, workspace.data_ptr(), ws_n, _status_on(status, dev),
+                                               _stream_on(stream, dev))
+        _check(st, "kvq_decode_attention_blocks")
+    else:
+        st = lib().kvq_decode_attention_blocks_paged(q.data_ptr(), k.c_struct(), v.c_struct(), bt, blocks.data_ptr(),
+                                                     n_select, seq_p, row_lens.data_ptr(), rows, Hq, softmax_scale,
+                                                     out.data_ptr(), out_dtype, workspace.data_ptr(), ws_n,
+                                                     _status_on(status, dev), _stream_on(stream, dev))
+        _check(st, "kvq_decode_attention_blocks_paged")
+    return out
+
+
+def decode_attention_blocks(q, k: QuantCache, v: QuantCache, blocks, row_lens, row_seq=None, softmax_scale: float = 0.0,
+                            out=None, out_dtype: int = OUT_F32, workspace=None, status=None, stream=None):
+    """decode_attention over listed blocks: row r of q bf16 [rows][Hq][D] attends the first row_lens[r] tokens of its
+    sequence (row_seq[r], None: r) that lie in the blocks blocks[r][KV head] (select_blocks's result).  workspace: a
+    decode_workspace of `rows` sequences.  Returns [rows][Hq][D]."""
+    return _decode_blocks(q, k, v, None, blocks, row_lens, row_seq, softmax_scale, out, out_dtype, workspace, status,
+                          stream)
+
+
+def decode_attention_blocks_paged(q, k_pool: QuantCache, v_pool: QuantCache, block_table, blocks, row_lens, row_seq=None,
+                                  softmax_scale: float = 0.0, out=None, out_dtype: int = OUT_F32, workspace=None,
+                                  status=None, stream=None):
+    """decode_attention_blocks over page pools through a block table."""
+    return _decode_blocks(q, k_pool, v_pool, block_table, blocks, row_lens, row_seq, softmax_scale, out, out_dtype,
+                          workspace, status, stream)
+
+
+# ---------------------------------------------------------------------------
+# pages: who has them
+# ---------------------------------------------------------------------------
+
+@dataclass
+class PageTable:
+    """The pages of a pool and the slots that have them (see kvq_page_table), kept on the device.  `table` is what the
+    paged calls take as a block table, `seq_lens` their lengths."""
+    refs: "object"            # torch.int32 [n_pages]: entries that are this page; 0: free
+    table: "object"           # torch.int32 [slots][max_pages]
+    seq_lens: "object"        # torch.int32 [slots]
+
+
+_pack_page_table = struct.Struct("@PPPiii4x").pack   # kvq_page_table
+
+
+def empty_page_table(n_pages: int, slots: int, max_pages: int, device="cuda") -> PageTable:
+    """A page table with every page free and every slot empty."""
+    import torch
+    return PageTable(torch.zeros(n_pages, dtype=torch.int32, device=device),
+                     torch.zeros((slots, max_pages), dtype=torch.int32, device=device),
+                     torch.zeros(slots, dtype=torch.int32, device=device))
+
+
+def pages_workspace(n_pages: int, slots: int, device="cuda"):
+    """Scratch for the page calls."""
+    import torch
+    n = int(lib().kvq_pages_workspace_bytes(n_pages, slots))
+    if n == 0:
+        raise KvqError(1, "kvq_pages_workspace_bytes: invalid sizes")
+    return torch.empty(n, dtype=torch.uint8, device=device)
+
+
+def _page_table(pages: PageTable):
+    i32 = _torch().int32
+    r, t, s = pages.refs, pages.table, pages.seq_lens
+    if (r.dtype != i32 or t.dtype != i32 or s.dtype != i32 or r.dim() != 1 or t.dim() != 2 or s.dim() != 1
+            or t.shape[0] != s.shape[0] or not r.is_contiguous() or not t.is_contiguous() or not s.is_contiguous()):
+        _bad("page table: int32 refs [n_pages], table [slots][max_pages], seq_lens [slots], contiguous")
+    dev = _on_current_device(r, t, s)
+    return dev, _pack_page_table(r.data_ptr(), t.data_ptr(), s.data_ptr(), r.shape[0], t.shape[0], t.shape[1])
+
+
+def _ids(x, device: int, what: str) -> int:
+    if x.dtype != _torch().int32 or x.dim() != 1 or not x.is_contiguous() or x.get_device() != device:
+        _bad(f"{what}: int32 [n], contiguous, on the page table's device")
+    return x.shape[0]
+
+
+def _pages_ws(workspace, pages: PageTable, device: int, stream):
+    return _workspace(workspace, device, stream, pages_workspace, pages.refs.shape[0], pages.table.shape[0],
+                      pages.refs.device)
+
+
+def pages_reserve(pages: PageTable, add, workspace=None, status=None, stream=None):
+    """Room for add[s] more tokens (int32 [slots]) in every slot: new pages where its length needs them, and the length
+    itself.  A pool that runs out is reported in `status` (KVQ_ERR_NO_PAGES); the slots that got none keep their length."""
+    dev, pt = _page_table(pages)
+    if _ids(add, dev, "add") != pages.table.shape[0]:
+        _bad("add: int32 [slots]")
+    ws = _pages_ws(workspace, pages, dev, stream)
+    st = lib().kvq_pages_reserve(pt, add.data_ptr(), ws.data_ptr(), ws.numel() * ws.element_size(),
+                                 _status_on(status, dev), _stream_on(stream, dev))
+    _check(st, "kvq_pages_reserve")
+
+
+def pages_fork(pages: PageTable, k_pool: QuantCache, v_pool: QuantCache, from_slots, to_slots,
+               bounds: Optional[BlockBounds] = None, workspace=None, status=None, stream=None):
+    """Slots to_slots (int32 [n], empty) become copies of from_slots: full pages shared, a partly filled last page
+    copied (in both pools and the bounds)."""
+    dev, pt = _page_table(pages)
+    n = _ids(from_slots, dev, "from_slots")
+    if _ids(to_slots, dev, "to_slots") != n:
+        _bad("from_slots and to_slots: one length")
+    _on_current_device(k_pool.codes, k_pool.sz, v_pool.codes, v_pool.sz)
+    ws = _pages_ws(workspace, pages, dev, stream)
+    st = lib().kvq_pages_fork(pt, k_pool.c_struct(), v_pool.c_struct(), _bounds(bounds, k_pool, dev),
+                              from_slots.data_ptr(), to_slots.data_ptr(), n, ws.data_ptr(),
+                              ws.numel() * ws.element_size(), _status_on(status, dev), _stream_on(stream, dev))
+    _check(st, "kvq_pages_fork")
+
+
+def pages_free(pages: PageTable, slots, status=None, stream=None):
+    """Slots (int32 [n]) let their pages go and are empty."""
+    dev, pt = _page_table(pages)
+    n = _ids(slots, dev, "slots")
+    st = lib().kvq_pages_free(pt, slots.data_ptr(), n, _status_on(status, dev), _stream_on(stream, dev))
+    _check(st, "kvq_pages_free")
+
+
+def pages_compact(pages: PageTable, k_pool: QuantCache, v_pool: QuantCache, bounds: Optional[BlockBounds] = None,
+                  n_live=None, workspace=None, status=None, stream=None):
+    """The live pages become pages 0 .. n_live - 1, their data (in both pools and the bounds), counts and table entries
+    with them.  n_live: int32 [1], gets their number."""
+    dev, pt = _page_table(pages)
+    _on_current_device(k_pool.codes, k_pool.sz, v_pool.codes, v_pool.sz)
+    if n_live is not None and _ids(n_live, dev, "n_live") < 1:
+        _bad("n_live: int32 [1]")
+    ws = _pages_ws(workspace, pages, dev, stream)
+    st = lib().kvq_pages_compact(pt, k_pool.c_struct(), v_pool.c_struct(), _bounds(bounds, k_pool, dev),
+                                 None if n_live is None else n_live.data_ptr(), ws.data_ptr(),
+                                 ws.numel() * ws.element_size(), _status_on(status, dev), _stream_on(stream, dev))
+    _check(st, "kvq_pages_compact")
+
+
+def copy_pages(k_pool: QuantCache, v_pool: QuantCache, src, dst, bounds: Optional[BlockBounds] = None, status=None,
+               stream=None):
+    """Pages dst (int32 [n]) of both pools (and the bounds) become copies of pages src; a pair with -1 is skipped."""
+    dev = _on_current_device(k_pool.codes, k_pool.sz, v_pool.codes, v_pool.sz)
+    n = _ids(src, dev, "src")
+    if _ids(dst, dev, "dst") != n:
+        _bad("src and dst: one length")
+    st = lib().kvq_copy_pages(k_pool.c_struct(), v_pool.c_struct(), _bounds(bounds, k_pool, dev), src.data_ptr(),
+                              dst.data_ptr(), n, _status_on(status, dev), _stream_on(stream, dev))
+    _check(st, "kvq_copy_pages")

@@ -53,7 +53,8 @@ typedef enum kvq_status {
   KVQ_ERR_WORKSPACE = 4,     /* workspace missing or too small */
   KVQ_ERR_TIMEOUT = 5,       /* (device) a bounded wait gave up */
   KVQ_ERR_NONFINITE = 6,     /* (device) non-finite input or fp16 overflow */
-  KVQ_ERR_BOUNDS = 7         /* (device, libkvq_debug.so only) an index check failed; the access was skipped */
+  KVQ_ERR_BOUNDS = 7,        /* (device, libkvq_debug.so only) an index check failed; the access was skipped */
+  KVQ_ERR_NO_PAGES = 8       /* (device) a page pool has too few free pages */
 } kvq_status;
 
 #define KVQ_GROUP 32          /* channels per quantisation group (P4 §3.2) */
@@ -623,6 +624,272 @@ KVQ_API kvq_status kvq_decode_attention_window_paged(const void* q, const kvq_ca
                                                      int32_t Hq, float softmax_scale, int32_t window, int32_t sinks,
                                                      void* out, int32_t out_dtype, void* workspace,
                                                      size_t workspace_bytes, int32_t* dev_status, void* stream);
+
+/*
+ * kvq_rotation -- what a model does to the projected queries and keys of every
+ * head before they meet: a root-mean-square norm with weights, and a rotation
+ * of channel pairs by the row's cache position.
+ */
+typedef struct kvq_rotation {
+  const float* table;       /* device fp32 [positions][rot_dim], 16-byte aligned: row p holds position p's rot_dim / 2
+                               cosines, then as many sines.  NULL: no rotation. */
+  const void* q_weight;     /* device bf16 [D], 16-byte aligned; NULL: queries are not normed */
+  const void* k_weight;     /* the same for keys */
+  int32_t positions;        /* rows of the table */
+  int32_t rot_dim;          /* channels 0 .. rot_dim - 1 turn, the others stay: a multiple of 16, 16 .. D */
+  int32_t interleaved;      /* pair i is channels 2i and 2i + 1 (1), or i and i + rot_dim / 2 (0) */
+  float eps;                /* 1e-12 .. 1, looked at where a weight is given */
+} kvq_rotation;
+
+/*
+ * kvq_rotate_append -- from the projections' rows to the cache in one pass:
+ * queries normed and rotated into q_out, keys normed, rotated and quantised
+ * into k's cache, values quantised into v's (positions as kvq_append_chunk).
+ *
+ * For a row x[D] of a head, all arithmetic IEEE fp32 with one rounding an
+ * operation unless said otherwise:
+ *   with a weight w:  m = the exact mean of x^2, rounded once;
+ *                     r = 1 / sqrt(m + eps);  y = (x * r) * w     (else y = x)
+ *   with a table:     pair (a, b) -> (a * cos - b * sin, b * cos + a * sin)
+ * then rounded to bf16.  Keys are quantised from that bf16 value exactly as
+ * kvq_quantize does it, so the codes are a function of the inputs.  (m is
+ * exact to 2^-40 before its rounding.)
+ *
+ * q: device bf16, channel d of (row r, query head h) at
+ *   q[r * sq_row + h * sq_head + d]; k_new, v_new as kvq_append_chunk (the
+ *   same strides for both); element strides, multiples of 8; 16-byte aligned.
+ * q_out: device bf16 [rows][Hq][D], contiguous, 16-byte aligned; it may be q
+ *   itself where q is laid out so, and overlaps no other input.
+ * out_dtype: KVQ_OUT_BF16 (KVQ_OUT_ZERO_REST: see kvq_chunk).
+ * Hq >= 1; rows * (Hq + 2 Hkv) below 2^31.  A row whose position is not below
+ * `positions` (with a table) reports KVQ_ERR_INVALID_ARG and is left out like
+ * the rows of an unusable sequence.  Non-finite keys and values as in
+ * kvq_quantize (a key that the norm makes non-finite among them); non-finite
+ * queries are not reported.
+ */
+KVQ_API kvq_status kvq_rotate_append(const void* q, int64_t sq_row, int64_t sq_head, const void* k_new,
+                                     const void* v_new, int64_t s_row, int64_t s_head, const kvq_chunk* chunk,
+                                     const kvq_rotation* rotation, int32_t Hq, const kvq_cache* k, const kvq_cache* v,
+                                     void* q_out, int32_t out_dtype, int32_t* dev_status, void* stream);
+/* The same into page pools; a row whose page id lies outside the pool reports
+ * KVQ_ERR_INVALID_ARG, its key and value are not written, its query is. */
+KVQ_API kvq_status kvq_rotate_append_paged(const void* q, int64_t sq_row, int64_t sq_head, const void* k_new,
+                                           const void* v_new, int64_t s_row, int64_t s_head, const kvq_chunk* chunk,
+                                           const kvq_rotation* rotation, int32_t Hq, const kvq_cache* k_pool,
+                                           const kvq_cache* v_pool, const kvq_block_table* table, void* q_out,
+                                           int32_t out_dtype, int32_t* dev_status, void* stream);
+
+/*
+ * Attention over selected blocks: a cache's tokens are looked at in blocks of
+ * 64 (its tiles; a pool's pages).  Beside K's cache a caller keeps each
+ * block's bounds -- per channel the least and greatest stored value -- in 8
+ * bits, from which a cheap score tells which blocks a query needs.
+ *
+ * kvq_bounds -- bounds of every storage block of a K cache (block index
+ * b * Tcap / 64 + i of sequence b's tokens 64 i .. 64 i + 63, or a pool's page
+ * id), NB = B * Tcap / 64 of them:
+ *   codes:  int8 [Hkv][NB][D / 32][2][32]: of each group of 32 channels the
+ *           greatest values' codes, then the least values'.  16-byte aligned.
+ *   scales: fp32 [Hkv][NB][D / 32].  16-byte aligned.
+ * A code c stands for c * scale.  Per block and group, in IEEE fp32, over the
+ * block's tokens below its sequence's length:
+ *   a = max |stored value|, s = a / 127, codes ceil(greatest / s) and
+ *   floor(least / s), clamped to +-127; a == 0: s = 0, codes 0
+ * so that (to the rounding of s) no stored value lies outside.
+ */
+typedef struct kvq_bounds {
+  int8_t* codes;
+  float* scales;
+} kvq_bounds;
+
+/* Bytes of a cache's bounds: the codes (0) or the scales (1); -1 on invalid shape. */
+KVQ_API int64_t kvq_bounds_bytes(const kvq_cache* k, int32_t which);
+
+/*
+ * kvq_block_bounds -- (re)computes the bounds of the blocks that hold a
+ * chunk's positions, from the stored codes: call it after the append, on the
+ * same stream.  With start the running sum of seq_lens it does whole
+ * sequences.  Other blocks' bounds keep their contents.  A block with a
+ * non-finite stored value reports KVQ_ERR_NONFINITE; its bounds are then
+ * unspecified.
+ */
+KVQ_API kvq_status kvq_block_bounds(const kvq_cache* k, const kvq_chunk* chunk, const kvq_bounds* bounds,
+                                    int32_t* dev_status, void* stream);
+/* The same from a page pool; a page id outside the pool reports
+ * KVQ_ERR_INVALID_ARG and is skipped. */
+KVQ_API kvq_status kvq_block_bounds_paged(const kvq_cache* k_pool, const kvq_chunk* chunk,
+                                          const kvq_block_table* table, const kvq_bounds* bounds, int32_t* dev_status,
+                                          void* stream);
+
+/*
+ * kvq_bounds_values -- the bounds of n listed storage blocks as values:
+ * out fp32 [Hkv][n][2][D] (greatest, then least), 16-byte aligned; blocks:
+ * device int32 [n].  An index outside [0, NB) reports KVQ_ERR_INVALID_ARG and
+ * gives zeros.  n == 0 does nothing.
+ */
+KVQ_API kvq_status kvq_bounds_values(const kvq_cache* k, const kvq_bounds* bounds, const int32_t* blocks, int32_t n,
+                                     float* out, int32_t* dev_status, void* stream);
+
+/*
+ * kvq_select_blocks -- for each query row and KV head, the blocks of its
+ * sequence that its queries (all of the head's group) need most.
+ *
+ * q: device bf16 [rows][Hq][D], contiguous, 16-byte aligned; Hq % Hkv == 0,
+ *   Hq / Hkv <= 8.
+ * row_seq: device int32 [rows], the sequence of each row, or NULL: row r is
+ *   sequence r.  row_lens: device int32 [rows], the tokens that the row sees
+ *   (a decode step's seq_lens; for drafted tokens, each one's position + 1).
+ *   A row with a sequence outside the cache's (or the table's), or a length
+ *   outside [0, capacity], reports KVQ_ERR_INVALID_ARG and counts as length 0.
+ * The score of a block, all in IEEE fp32, one rounding an operation, per group
+ * g of 32 channels with qp[d], qn[d] = the sums of max(q, 0) and of min(q, 0)
+ * over the group's query heads in order:
+ *   u = max(qp, -qn over g) / 127, cp = rne(qp / u), cn = rne(qn / u) (u == 0:
+ *   0); n = sum of cp * greatest code + cn * least code, a whole number;
+ *   t_g = (u * scale_g) * n; the score is ((t_0 + t_1) + t_2) + t_3
+ * -- an upper bound of the summed q.k of any of the block's tokens, but for
+ * the rounding of q to 8 bits.
+ * Of a row's ceil(len / 64) blocks the first `first` and the last `last` are
+ * always taken (first, last >= 0, first + last <= n_select); the rest are
+ * those of the highest scores, ties to the lower index.  NaN scores (a
+ * non-finite query reports KVQ_ERR_NONFINITE) select blocks of the sequence,
+ * unspecified which.
+ * blocks: device int32 [rows][Hkv][n_select], ascending, then -1 where the
+ *   sequence has fewer.  1 <= n_select <= 65536.
+ * workspace: device, >= kvq_select_workspace_bytes(rows, Hkv, capacity) bytes
+ *   (capacity: tokens a sequence may have: Tcap, or 64 * max_pages), with
+ *   kvq_decode_attention's rules (16-byte aligned, zero-filled once before its
+ *   first use, calls that share it ordered on the GPU).  One workspace serves
+ *   selections of every shape that fits it, and nothing else.
+ * rows <= 4096; capacities above 2^29 tokens are KVQ_ERR_UNSUPPORTED.
+ */
+KVQ_API size_t kvq_select_workspace_bytes(int32_t rows, int32_t Hkv, int32_t capacity);
+KVQ_API kvq_status kvq_select_blocks(const void* q, const kvq_cache* k, const kvq_bounds* bounds,
+                                     const int32_t* row_seq, const int32_t* row_lens, int32_t rows, int32_t Hq,
+                                     int32_t n_select, int32_t first, int32_t last, int32_t* blocks, void* workspace,
+                                     size_t workspace_bytes, int32_t* dev_status, void* stream);
+/* The same over a page pool; a block whose page id lies outside the pool
+ * reports KVQ_ERR_INVALID_ARG and scores as page 0. */
+KVQ_API kvq_status kvq_select_blocks_paged(const void* q, const kvq_cache* k_pool, const kvq_bounds* bounds,
+                                           const kvq_block_table* table, const int32_t* row_seq,
+                                           const int32_t* row_lens, int32_t rows, int32_t Hq, int32_t n_select,
+                                           int32_t first, int32_t last, int32_t* blocks, void* workspace,
+                                           size_t workspace_bytes, int32_t* dev_status, void* stream);
+
+/*
+ * kvq_decode_attention_blocks -- kvq_decode_attention over listed blocks: the
+ * query of row r and KV head h attends the tokens below row_lens[r] of its
+ * sequence's blocks blocks[r][h][0 .. n - 1], n = min(n_select, ceil(len /
+ * 64)), each KV head its own.  rows, row_seq, row_lens as kvq_select_blocks;
+ * the list ascends, -1 (at its end) stands for no block.  An entry that does
+ * not ascend, or lies outside the sequence, reports KVQ_ERR_INVALID_ARG and is
+ * left out (the entry after it is compared with it all the same).  A row
+ * without a token gives zeros.  Blocks that are not listed may hold anything.
+ * q, out: [rows][Hq][D]; workspace: kvq_decode_workspace_bytes(rows, Hq, Hkv,
+ * D) bytes.  Other arguments and errors as kvq_decode_attention.
+ */
+KVQ_API kvq_status kvq_decode_attention_blocks(const void* q, const kvq_cache* k, const kvq_cache* v,
+                                               const int32_t* blocks, int32_t n_select, const int32_t* row_seq,
+                                               const int32_t* row_lens, int32_t rows, int32_t Hq, float softmax_scale,
+                                               void* out, int32_t out_dtype, void* workspace, size_t workspace_bytes,
+                                               int32_t* dev_status, void* stream);
+/* The same over page pools (page ids as kvq_decode_attention_paged). */
+KVQ_API kvq_status kvq_decode_attention_blocks_paged(const void* q, const kvq_cache* k_pool, const kvq_cache* v_pool,
+                                                     const kvq_block_table* table, const int32_t* blocks,
+                                                     int32_t n_select, const int32_t* row_seq,
+                                                     const int32_t* row_lens, int32_t rows, int32_t Hq,
+                                                     float softmax_scale, void* out, int32_t out_dtype,
+                                                     void* workspace, size_t workspace_bytes, int32_t* dev_status,
+                                                     void* stream);
+
+/*
+ * kvq_page_table -- the pages of a pool and who has them, kept on the device:
+ * every call below changes it in place, in the order of the stream, so that a
+ * scheduler's loop needs no copies to the host.  Slot s is a sequence of
+ * seq_lens[s] tokens in pages table[s][0 .. ceil(len / 64) - 1] (later entries
+ * mean nothing and keep their contents); refs[p] counts the entries that are
+ * page p, 0: free.  (table and seq_lens are what the block table and the chunk
+ * of the other calls take.)  Pages are handed out lowest free page first.
+ */
+typedef struct kvq_page_table {
+  int32_t* refs;       /* device int32 [n_pages] */
+  int32_t* table;      /* device int32 [slots][max_pages] */
+  int32_t* seq_lens;   /* device int32 [slots] */
+  int32_t n_pages;     /* 1 .. 2^24 */
+  int32_t slots;       /* 1 .. 65536 */
+  int32_t max_pages;   /* pages a slot may have; slots * max_pages and 64 * max_pages below 2^31 */
+} kvq_page_table;
+
+/* Device scratch of the calls that take a workspace (16-byte aligned, no
+ * initial contents; calls that share it ordered on the GPU). 0 on invalid sizes. */
+KVQ_API size_t kvq_pages_workspace_bytes(int32_t n_pages, int32_t slots);
+
+/*
+ * kvq_pages_reserve -- room for add[s] >= 0 more tokens in every slot: the
+ * pages that the new length needs beyond those it has, handed out in the order
+ * of the slots, and the length itself (the new tokens' rows can then be
+ * appended).  Where the pages run out, the slots from the first one that they
+ * do not suffice for get none: their lengths stay, KVQ_ERR_NO_PAGES is
+ * reported (slots that need no new page are served all the same).  A negative
+ * add, a length outside [0, 64 * max_pages] or one that would pass it reports
+ * KVQ_ERR_INVALID_ARG and leaves the slot alone.
+ * add: device int32 [slots].
+ */
+KVQ_API kvq_status kvq_pages_reserve(const kvq_page_table* pages, const int32_t* add, void* workspace,
+                                     size_t workspace_bytes, int32_t* dev_status, void* stream);
+
+/*
+ * kvq_pages_fork -- slot to[i] becomes a copy of slot from[i], i < n: it
+ * shares the full pages (their counts rise) and gets its own copy of a last
+ * page that is partly filled, in both pools and in `bounds` (NULL: none kept).
+ * A slot may be forked into several.  to[i] has to be empty (length 0) and no
+ * other pair's to; a pair that breaks this, names a slot outside [0, slots) or
+ * whose from has a length outside [0, 64 * max_pages], reports
+ * KVQ_ERR_INVALID_ARG and does nothing (of pairs with the same to, the first
+ * is served).  Lengths are those before the call.  A pair that finds no page
+ * for its copy, and those after it that need one, report KVQ_ERR_NO_PAGES and
+ * do nothing.  A page id outside the pool in a used entry is copied as it
+ * stands and reported as KVQ_ERR_INVALID_ARG.
+ * k_pool, v_pool: the pools, B = n_pages, Tcap = 64, of equal shape and bits.
+ * from, to: device int32 [n]; n <= slots, n == 0 does nothing.
+ */
+KVQ_API kvq_status kvq_pages_fork(const kvq_page_table* pages, const kvq_cache* k_pool, const kvq_cache* v_pool,
+                                  const kvq_bounds* bounds, const int32_t* from, const int32_t* to, int32_t n,
+                                  void* workspace, size_t workspace_bytes, int32_t* dev_status, void* stream);
+
+/*
+ * kvq_pages_free -- slots which[i], i < n, let their pages go (the counts
+ * fall) and are empty.  A slot outside [0, slots), a length outside [0, 64 *
+ * max_pages] or a page that is outside the pool or free already reports
+ * KVQ_ERR_INVALID_ARG and is passed over (such a length becomes 0); a slot
+ * listed twice is let go once.  n == 0 does nothing.
+ */
+KVQ_API kvq_status kvq_pages_free(const kvq_page_table* pages, const int32_t* which, int32_t n, int32_t* dev_status,
+                                  void* stream);
+
+/*
+ * kvq_pages_compact -- the live pages (refs > 0) become pages 0 .. n_live - 1:
+ * the live ones from n_live on move, in order, into the free ones before it,
+ * in order; their data in both pools and `bounds` (NULL: none kept), their
+ * counts and every table entry in use follow.  n_live (device int32 [1], NULL:
+ * not wanted) gets the number of live pages.  Pages that became free keep
+ * their data.
+ */
+KVQ_API kvq_status kvq_pages_compact(const kvq_page_table* pages, const kvq_cache* k_pool, const kvq_cache* v_pool,
+                                     const kvq_bounds* bounds, int32_t* n_live, void* workspace,
+                                     size_t workspace_bytes, int32_t* dev_status, void* stream);
+
+/*
+ * kvq_copy_pages -- page dst[i] of both pools (and `bounds`, NULL: none kept)
+ * becomes a copy of page src[i], i < n.  A pair with a negative index is
+ * skipped; one beyond the pool reports KVQ_ERR_INVALID_ARG and is skipped.  A
+ * page may be the source of several pairs, but a destination is no other
+ * pair's source or destination.  src, dst: device int32 [n]; n == 0 does
+ * nothing.
+ */
+KVQ_API kvq_status kvq_copy_pages(const kvq_cache* k_pool, const kvq_cache* v_pool, const kvq_bounds* bounds,
+                                  const int32_t* src, const int32_t* dst, int32_t n, int32_t* dev_status,
+                                  void* stream);
 
 /* Static, human-readable name of a status code. */
 KVQ_API const char* kvq_status_str(kvq_status status);
