@@ -150,6 +150,15 @@ def test_rotate_append(kvq, case):
     c.check(out)
 
 
+@pytest.mark.parametrize("interleaved", [False, True])
+def test_a_few_million_queries_bit_for_bit(kvq, interleaved):
+    """A product fused into a sum, or a mean that is not the exact one rounded, changes about one bf16 value in 2^15."""
+    c = Case(kvq, 12, [6000], [0], 4, 1, 128, "8", 128, interleaved=interleaved)
+    out = c.run()
+    want = c.expect()[0][0]
+    assert np.array_equal(out.cpu().view(torch.int16).numpy().view(np.uint16), want)
+
+
 def test_equal_calls_give_equal_bits_and_zero_rows_do_nothing(kvq):
     c = Case(kvq, 3, [50, 1], [4, 80], 8, 2, 128, "mixed", 128)
     a, b = c.run(), c.run()
