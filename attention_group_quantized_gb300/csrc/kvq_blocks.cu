@@ -25,6 +25,7 @@ namespace {
 // ---------------------------------------------------------------------------
 
 constexpr int kBoundsWarps = 4;
+constexpr int kBoundsBlocks = 8;    // an SM (four prompts of 32K: 8 38.5 us, 6 40.0, 5 44.0)
 
 struct BParams {
   chunk::View c;
@@ -105,21 +106,39 @@ __device__ __forceinline__ void block_of(const BParams& p, int h, int sb, int n,
     lo[i] = INFINITY;
     hi[i] = -INFINITY;
   }
+  // the lane's rows at fixed distances from two pointers; of a block that is
+  // cut, whole rows are read (they are the storage's) and those past its end
+  // replaced by the lane's first
+  const uint8_t* src = p.codes + off0 + part * (D * BITS / 8);
+  const uint32_t* sw = p.sz + si0 + part * G;
+  uint2 c0 = make_uint2(0u, 0u);
+  uint32_t word0 = 0u;
+  if (n < KVQ_TILE_TOKENS) {          // (token 0 for lanes whose first one is past the end)
+    const int back = part < n ? 0 : part;
+    if constexpr (BITS == 8) c0 = *reinterpret_cast<const uint2*>(src - back * (D * BITS / 8));
+    else c0.x = *reinterpret_cast<const uint32_t*>(src - back * (D * BITS / 8));
+    word0 = *(sw - back * G);
+  }
 #pragma unroll 1
   for (int t0 = 0; t0 < n; t0 += RPP * U) {
     uint2 c[U];
     uint32_t word[U];
-    // (a token past the end stands in for the lane's first one of the block,
-    // or the block's first)
 #pragma unroll
     for (int j = 0; j < U; ++j) {
-      int t = t0 + j * RPP + part;
-      t = t < n ? t : 0;
-      const uint8_t* src = p.codes + off0 + t * (D * BITS / 8);
       c[j] = make_uint2(0u, 0u);
-      if constexpr (BITS == 8) c[j] = *reinterpret_cast<const uint2*>(src);
-      else c[j].x = *reinterpret_cast<const uint32_t*>(src);
-      word[j] = p.sz[si0 + static_cast<int64_t>(t) * G];
+      if constexpr (BITS == 8) c[j] = *reinterpret_cast<const uint2*>(src + j * RPP * (D * BITS / 8));
+      else c[j].x = *reinterpret_cast<const uint32_t*>(src + j * RPP * (D * BITS / 8));
+      word[j] = sw[j * RPP * G];
+    }
+    src += RPP * U * (D * BITS / 8);
+    sw += RPP * U * G;
+    if (n < KVQ_TILE_TOKENS) {
+#pragma unroll
+      for (int j = 0; j < U; ++j)
+        if (t0 + j * RPP + part >= n) {
+          c[j] = c0;
+          word[j] = word0;
+        }
     }
 #pragma unroll
     for (int j = 0; j < U; j += 2) {
@@ -168,10 +187,10 @@ __device__ __forceinline__ void block_of(const BParams& p, int h, int sb, int n,
 
 // A block is the work of the row that holds its first new token: a sequence's
 // first new row, or one at the start of a block.  A warp looks at R rows for
-// one head: one at a time while the rows are few (each may own a block), 32
-// once they are many (mostly prompts, one owner in 64).
+// one head: one while the rows are few (each may own a block), 64 once they are
+// many (mostly prompts, one owner in 64).
 template <int D, int R>
-__global__ void __launch_bounds__(kBoundsWarps * 32) block_bounds_kernel(const __grid_constant__ BParams p) {
+__global__ void __launch_bounds__(kBoundsWarps * 32, kBoundsBlocks) block_bounds_kernel(const __grid_constant__ BParams p) {
   grid_dependency_wait();
   grid_launch_dependents();
   const int lane = threadIdx.x & 31;
@@ -181,57 +200,61 @@ __global__ void __launch_bounds__(kBoundsWarps * 32) block_bounds_kernel(const _
        u += static_cast<int64_t>(gridDim.x) * kBoundsWarps) {
     const int tile = static_cast<int>(static_cast<uint32_t>(u) / static_cast<uint32_t>(p.Hkv));
     const int h = static_cast<int>(static_cast<uint32_t>(u) - static_cast<uint32_t>(tile) * p.Hkv);
-    const int r0 = tile * R;
-    int b = chunk::find_sequence(p.c.start, p.c.B, r0, lane);
-    const int r = r0 + lane;
-    int sb = -1, n = 0;
-    if (lane < R && r < p.c.rows) {
-      while (b + 1 < p.c.B && p.c.start[b + 1] <= r) ++b;
-      const chunk::Seq s = chunk::sequence(p.c, b);
-      const int pos = s.len - s.n + (r - s.row0);
-      if (!s.bad && r >= s.row0 && r < s.row0 + s.n && (r == s.row0 || pos % KVQ_TILE_TOKENS == 0)) {
-        const int i = pos / KVQ_TILE_TOKENS;
-        const int64_t row = chunk::storage_row(p.c, b, i * KVQ_TILE_TOKENS);
-        if (row >= 0) sb = static_cast<int>(row / KVQ_TILE_TOKENS);
-        else if (h == 0) report(p.status, KVQ_ERR_INVALID_ARG);
-        n = min(KVQ_TILE_TOKENS, s.len - i * KVQ_TILE_TOKENS);
+#pragma unroll 1
+    for (int r0 = tile * R; r0 < min((tile + 1) * R, p.c.rows); r0 += 32) {
+      int b = chunk::find_sequence(p.c.start, p.c.B, r0, lane);
+      const int r = r0 + lane;
+      int sb = -1, n = 0;
+      if (lane < R && r < p.c.rows) {
+        while (b + 1 < p.c.B && p.c.start[b + 1] <= r) ++b;
+        const chunk::Seq s = chunk::sequence(p.c, b);
+        const int pos = s.len - s.n + (r - s.row0);
+        if (!s.bad && r >= s.row0 && r < s.row0 + s.n && (r == s.row0 || pos % KVQ_TILE_TOKENS == 0)) {
+          const int i = pos / KVQ_TILE_TOKENS;
+          const int64_t row = chunk::storage_row(p.c, b, i * KVQ_TILE_TOKENS);
+          if (row >= 0) sb = static_cast<int>(row / KVQ_TILE_TOKENS);
+          else if (h == 0) report(p.status, KVQ_ERR_INVALID_ARG);
+          n = min(KVQ_TILE_TOKENS, s.len - i * KVQ_TILE_TOKENS);
+        }
       }
-    }
-    for (unsigned m = __ballot_sync(0xffffffffu, sb >= 0); m != 0; m &= m - 1) {
-      const int src = __ffs(m) - 1;
-      const int block = __shfl_sync(0xffffffffu, sb, src), count = __shfl_sync(0xffffffffu, n, src);
-      if (p.bits[h] == 8) block_of<D, 8>(p, h, block, count, lane);
-      else block_of<D, 4>(p, h, block, count, lane);
-      __syncwarp();
+      for (unsigned m = __ballot_sync(0xffffffffu, sb >= 0); m != 0; m &= m - 1) {
+        const int src = __ffs(m) - 1;
+        const int block = __shfl_sync(0xffffffffu, sb, src), count = __shfl_sync(0xffffffffu, n, src);
+        if (p.bits[h] == 8) block_of<D, 8>(p, h, block, count, lane);
+        else block_of<D, 4>(p, h, block, count, lane);
+        __syncwarp();
+      }
     }
   }
 }
 
-// Listed blocks' bounds as values, a thread per 4 channels.
-__global__ void __launch_bounds__(256) bounds_values_kernel(const int8_t* codes, const float* scales, const int32_t* ids,
-                                                            int n, int Hkv, int64_t NB, int D, float* out,
-                                                            int32_t* status) {
+// Listed blocks' bounds as values: a warp per (KV head, block), 4 channels a lane
+// at a time (16 bytes out, 4 of codes in).
+__global__ void __launch_bounds__(kBoundsWarps * 32) bounds_values_kernel(const int8_t* codes, const float* scales,
+                                                                          const int32_t* ids, int n, int Hkv, int64_t NB,
+                                                                          int D, float* out, int32_t* status) {
   grid_dependency_wait();
   grid_launch_dependents();
-  const int quads = D / 2;                                 // 4-channel runs of one block's two rows
-  const int64_t total = static_cast<int64_t>(Hkv) * n * quads;
-  for (int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; i < total;
-       i += static_cast<int64_t>(gridDim.x) * 256) {
-    const int64_t hb = i / quads;
-    const int e = static_cast<int>(i - hb * quads) * 4;    // in [0, 2 D): row e / D, channel e % D
-    const int h = static_cast<int>(hb / n), d = e % D;
-    const int id = ids[hb - static_cast<int64_t>(h) * n];
-    float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-    if (id < 0 || id >= NB) {
-      if (e == 0 && h == 0) report(status, KVQ_ERR_INVALID_ARG);
-    } else {
-      const int64_t g = (h * NB + id) * (D / 32) + d / 32;
-      const char4 c = *reinterpret_cast<const char4*>(codes + g * 64 + (e / D) * 32 + d % 32);
-      const float s = scales[g];
-      v = make_float4(static_cast<signed char>(c.x) * s, static_cast<signed char>(c.y) * s,
-                      static_cast<signed char>(c.z) * s, static_cast<signed char>(c.w) * s);
+  const int lane = threadIdx.x & 31;
+  const int64_t total = static_cast<int64_t>(Hkv) * n;
+  for (int64_t u = static_cast<int64_t>(blockIdx.x) * kBoundsWarps + (threadIdx.x >> 5); u < total;
+       u += static_cast<int64_t>(gridDim.x) * kBoundsWarps) {
+    const int64_t h = u / n;
+    const int id = ids[u - h * n];
+    const bool ok = id >= 0 && id < NB;
+    if (!ok && h == 0 && lane == 0) report(status, KVQ_ERR_INVALID_ARG);
+    const int64_t g0 = ok ? (h * NB + id) * (D / 32) : 0;
+    for (int e = lane * 4; e < 2 * D; e += 128) {          // row e / D (greatest, least), channel e % D
+      const int d = e % D;
+      float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+      if (ok) {
+        const char4 c = *reinterpret_cast<const char4*>(codes + (g0 + d / 32) * 64 + (e / D) * 32 + d % 32);
+        const float s = scales[g0 + d / 32];
+        v = make_float4(static_cast<signed char>(c.x) * s, static_cast<signed char>(c.y) * s,
+                        static_cast<signed char>(c.z) * s, static_cast<signed char>(c.w) * s);
+      }
+      *reinterpret_cast<float4*>(out + u * 2 * D + e) = v;
     }
-    *reinterpret_cast<float4*>(out + i * 4) = v;
   }
 }
 
@@ -240,6 +263,7 @@ __global__ void __launch_bounds__(256) bounds_values_kernel(const int8_t* codes,
 // ---------------------------------------------------------------------------
 
 constexpr int kSelThreads = 256;
+constexpr int kSelectPer = 128;     // blocks of a CTA at least
 constexpr int kSelWarps = kSelThreads / 32;
 constexpr int kSmemKeys = 8192;     // keys selected from in shared memory (sequences up to 524,288 tokens)
 constexpr int kMaxChunks = 64;      // CTAs of one (row, KV head)
@@ -267,90 +291,130 @@ __device__ __forceinline__ uint32_t key_of(float score) {
   return u ^ ((u >> 31) != 0u ? 0xFFFFFFFFu : 0x80000000u);
 }
 
-// Exclusive prefix sum of v over the CTA's threads.
-__device__ __forceinline__ int scan_exclusive(int v, int* warp_sums) {
-  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
-  int x = v;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int y = __shfl_up_sync(0xffffffffu, x, o);
-    if (lane >= o) x += y;
-  }
-  if (lane == 31) warp_sums[w] = x;
-  __syncthreads();
-  int before = 0;
-#pragma unroll
-  for (int i = 0; i < kSelWarps; ++i) before += i < w ? warp_sums[i] : 0;
-  __syncthreads();
-  return before + x - v;
-}
+// Shared memory of a selection's last part.
+struct SelectSmem {
+  int hist[2][256];
+  uint32_t lo[kSelWarps], hi[kSelWarps];   // each warp's least and greatest key
+  int2 sums[kSelWarps];
+  int digit, above, count;
+};
 
-// The indices of the `want` largest of n keys (0 < want < n), ascending, ties
-// to the lower index: the key of rank `want` found digit by digit (8 bits,
-// from the top, a histogram of those that agree so far), then one ordered pass.
+// The indices (plus `base`) of the `want` largest of n keys (0 < want < n),
+// ascending, ties to the lower index.  The key of rank `want` is found digit by
+// digit, 8 bits at a time from the highest bit in which any two keys differ
+// (scores of one row share sign and most of their exponents), with a histogram
+// of the keys that agree so far; it ends early where all keys of the rank's
+// digit are wanted.  Then one ordered pass.  mn, mx: this thread's least and
+// greatest key.
 template <class Load>
-__device__ __forceinline__ void select_largest(Load key, int n, int want, int32_t* out, int* hist, int* warp_sums,
-                                               int* found) {
-  const int tid = threadIdx.x;
-  uint32_t prefix = 0u;
-  int left = want;                    // rank among the keys that agree with the prefix
-#pragma unroll 1
-  for (int shift = 24; shift >= 0; shift -= 8) {
-    hist[tid] = 0;
-    __syncthreads();
-    const uint32_t mask = shift == 24 ? 0u : 0xFFFFFFFFu << (shift + 8);
-    for (int i0 = 0; i0 < n; i0 += kSelThreads) {
-      const int i = i0 + tid;
-      const uint32_t k = i < n ? key(i) : 0u;
-      const bool in = i < n && (k & mask) == prefix;
-      // lanes with the same digit count once for all (scores share their top
-      // bits: one counter would be added to by every lane)
-      const uint32_t digit = in ? (k >> shift) & 255u : 256u;
-      const unsigned same = __match_any_sync(0xffffffffu, digit);
-      if (in && (threadIdx.x & 31) == __ffs(same) - 1) atomicAdd(&hist[digit], __popc(same));
-    }
-    __syncthreads();
-    const int d = 255 - tid;          // thread t: the digit with t larger ones
-    const int mine = hist[d];
-    const int before = scan_exclusive(mine, warp_sums);
-    if (before < left && before + mine >= left) {
-      found[0] = d;
-      found[1] = before;
-    }
-    __syncthreads();
-    prefix |= static_cast<uint32_t>(found[0]) << shift;
-    left -= found[1];
-    __syncthreads();
+__device__ __forceinline__ void select_largest(Load key, int n, int want, int base, int32_t* out, uint32_t mn, uint32_t mx,
+                                               SelectSmem& sm) {
+  const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
+  mn = __reduce_min_sync(0xffffffffu, mn);
+  mx = __reduce_max_sync(0xffffffffu, mx);
+  if (lane == 0) {
+    sm.lo[w] = mn;
+    sm.hi[w] = mx;
   }
-  // keys above the threshold, and the first `left` of those equal to it
+  if (tid < 256) sm.hist[0][tid] = 0;
+  __syncthreads();
+  mn = __reduce_min_sync(0xffffffffu, sm.lo[lane % kSelWarps]);
+  mx = __reduce_max_sync(0xffffffffu, sm.hi[lane % kSelWarps]);
+  int shift = mn == mx ? 0 : max(24 - __clz(mn ^ mx), 0);      // the first digit's lowest bit
+  uint32_t mask = shift >= 24 ? 0u : 0xFFFFFFFFu << (shift + 8);   // bits that all keys looked at agree in
+  uint32_t prefix = mx & mask;
+  int left = want;                    // rank among the keys that agree with the prefix
+  bool whole = mn == mx;              // every key from the prefix on is wanted (mn == mx: ties, by index below)
+  if (whole) {
+    mask = 0xFFFFFFFFu;
+    prefix = mx;
+  }
+  for (int pass = 0; !whole; ++pass) {
+    int* hist = sm.hist[pass & 1];
+    for (int i = tid; i < n; i += kSelThreads) {
+      const uint32_t k = key(i);
+      if ((k & mask) == prefix) atomicAdd(&hist[(k >> shift) & 255u], 1);
+    }
+    if (tid < 256) sm.hist[(pass & 1) ^ 1][tid] = 0;
+    __syncthreads();
+    if (w == 0) {                     // lane l: digits 255 - 8 l .. 248 - 8 l
+      int c[8], sum = 0;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) sum += c[j] = hist[255 - 8 * lane - j];
+      int before = sum;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, before, o);
+        if (lane >= o) before += y;
+      }
+      before -= sum;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        if (before < left && before + c[j] >= left) {
+          sm.digit = 255 - 8 * lane - j;
+          sm.above = before;
+          sm.count = c[j];
+        }
+        before += c[j];
+      }
+    }
+    __syncthreads();
+    prefix |= static_cast<uint32_t>(sm.digit) << shift;
+    mask |= 255u << shift;
+    left -= sm.above;
+    whole = left == sm.count || shift == 0;
+    shift = max(shift - 8, 0);
+    // (a last digit of fewer than 8 new bits overlaps the one before: those bits agree)
+  }
+  // keys whose known digits are above the prefix, and the first `left` of those equal to it
   const int per = (n + kSelThreads - 1) / kSelThreads;
   const int i0 = min(tid * per, n), i1 = min(i0 + per, n);
-  int above = 0, equal = 0;
+  int2 mine = make_int2(0, 0);
   for (int i = i0; i < i1; ++i) {
-    const uint32_t k = key(i);
-    above += k > prefix;
-    equal += k == prefix;
+    const uint32_t k = key(i) & mask;
+    mine.x += k > prefix;
+    mine.y += k == prefix;
   }
-  const int above0 = scan_exclusive(above, warp_sums);
-  int equal0 = scan_exclusive(equal, warp_sums);
-  int at = above0 + min(equal0, left);
+  int2 x = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int y0 = __shfl_up_sync(0xffffffffu, x.x, o), y1 = __shfl_up_sync(0xffffffffu, x.y, o);
+    if (lane >= o) {
+      x.x += y0;
+      x.y += y1;
+    }
+  }
+  if (lane == 31) sm.sums[w] = x;
+  __syncthreads();
+  int above = x.x - mine.x, equal = x.y - mine.y;
+#pragma unroll
+  for (int i = 0; i < kSelWarps; ++i)
+    if (i < w) {
+      above += sm.sums[i].x;
+      equal += sm.sums[i].y;
+    }
+  int at = above + min(equal, left);
   for (int i = i0; i < i1; ++i) {
-    const uint32_t k = key(i);
-    if (k > prefix || (k == prefix && equal0++ < left)) out[at++] = i;
+    const uint32_t k = key(i) & mask;
+    if (k > prefix || (k == prefix && equal++ < left)) out[at++] = base + i;
   }
 }
 
 // One CTA scores per_chunk blocks of a (row, KV head), its threads G lanes a
 // block (one per group, 64 bytes of bounds each); where there are several
-// CTAs, the last to arrive selects from all the keys.
+// CTAs, the last to arrive selects from all the keys.  The blocks that are
+// always taken are left out of all this: the others are `first` .. nblk -
+// `last` - 1, candidate i being block first + i.
 template <int D>
 __global__ void __launch_bounds__(kSelThreads) select_blocks_kernel(const __grid_constant__ SParams p) {
   constexpr int G = D / 32;
   constexpr int U = 2;                // blocks of a lane whose loads are in flight together
+  constexpr int kRound = U * kSelThreads / G;
   __shared__ __align__(16) uint32_t s_q[G][16];   // the group's 32 greatest-side codes, then the least-side ones
   __shared__ float s_u[G];
   __shared__ uint32_t s_keys[kSmemKeys];
-  __shared__ int s_hist[256], s_sums[kSelWarps], s_found[2], s_last;
+  __shared__ SelectSmem sm;
+  __shared__ int s_last;
   grid_dependency_wait();
   grid_launch_dependents();
   const int tid = threadIdx.x, lane = tid & 31;
@@ -359,6 +423,12 @@ __global__ void __launch_bounds__(kSelThreads) select_blocks_kernel(const __grid
   const int row = seg / p.Hkv, kvh = seg - row * p.Hkv;
   int len = p.row_lens[row];
   const int seq = p.row_seq != nullptr ? p.row_seq[row] : row;
+  uint32_t qv[8];                     // the lane's channel of the group's queries
+  if (tid < D) {
+    const uint16_t* src = p.q + (static_cast<int64_t>(row) * p.Hq + kvh * p.rep) * D + tid;
+#pragma unroll
+    for (int r = 0; r < 8; ++r) qv[r] = r < p.rep ? src[r * D] : 0u;
+  }
   if (len < 0 || len > p.cap || seq < 0 || seq >= p.seqs) {
     if (tid == 0) report(p.status, KVQ_ERR_INVALID_ARG);
     len = 0;
@@ -370,50 +440,22 @@ __global__ void __launch_bounds__(kSelThreads) select_blocks_kernel(const __grid
       for (int i = tid; i < p.n_select; i += kSelThreads) out[i] = i < nblk ? i : -1;
     return;
   }
-  const int c0 = chunk * p.per_chunk, c1 = min(c0 + p.per_chunk, nblk);
-  if (c0 >= nblk) return;
-  const int used = (nblk + p.per_chunk - 1) / p.per_chunk;   // CTAs with blocks to score
+  const int n = nblk - p.first - p.last, want = p.n_select - p.first - p.last;   // (n > want >= 0)
+  if (chunk == 0) {
+    for (int i = tid; i < p.first; i += kSelThreads) out[i] = i;
+    for (int i = tid; i < p.last; i += kSelThreads) out[p.n_select - p.last + i] = nblk - p.last + i;
+  }
+  const int c0 = chunk * p.per_chunk, c1 = min(c0 + p.per_chunk, n);
+  if (want == 0 || c0 >= n) return;
+  const int used = (n + p.per_chunk - 1) / p.per_chunk;   // CTAs with blocks to score
 
-  // the query in 8 bits: warp g has group g, lane l its channel l
-  if (tid < D) {
-    const uint16_t* src = p.q + (static_cast<int64_t>(row) * p.Hq + kvh * p.rep) * D + tid;
-    float up = 0.0f, down = 0.0f;
-    bool finite = true;
-    for (int r = 0; r < p.rep; ++r) {
-      const float v = __uint_as_float(static_cast<uint32_t>(src[r * D]) << 16);
-      finite &= fabsf(v) < INFINITY;
-      up = __fadd_rn(up, fmaxf(v, 0.0f));
-      down = __fadd_rn(down, fminf(v, 0.0f));
-    }
-    if (!finite) report(p.status, KVQ_ERR_NONFINITE);
-    float a = fmaxf(up, -down);
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, o));
-    const float u = __fdiv_rn(a, 127.0f);
-    const float cp = u > 0.0f ? rintf(__fdiv_rn(up, u)) : 0.0f, cn = u > 0.0f ? rintf(__fdiv_rn(down, u)) : 0.0f;
-    int8_t* dst = reinterpret_cast<int8_t*>(s_q[tid / 32]);
-    dst[lane] = static_cast<int8_t>(static_cast<int>(fminf(fmaxf(cp, -127.0f), 127.0f)));
-    dst[32 + lane] = static_cast<int8_t>(static_cast<int>(fminf(fmaxf(cn, -127.0f), 127.0f)));
-    if (lane == 0) s_u[tid / 32] = u;
-  }
-  __syncthreads();
   const int g = lane % G;
-  uint32_t qc[16];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const uint4 v = *reinterpret_cast<const uint4*>(&s_q[g][4 * i]);
-    qc[4 * i] = v.x; qc[4 * i + 1] = v.y; qc[4 * i + 2] = v.z; qc[4 * i + 3] = v.w;
-  }
-  const float u = s_u[g];
-  const bool in_smem = nblk <= kSmemKeys;
-  const bool alone = used == 1;
-  uint32_t* gkeys = p.keys + static_cast<int64_t>(seg) * p.key_stride;
-  for (int i0 = c0; i0 < c1; i0 += U * kSelThreads / G) {
-    uint4 w[U][4];
-    float sc[U];
+  uint4 w[U][4];
+  float sc[U];
+  auto fetch = [&](int i0) {
 #pragma unroll
     for (int j = 0; j < U; ++j) {
-      const int i = min(i0 + (j * kSelThreads + tid) / G, c1 - 1);   // (past the end: the last block again)
+      const int i = p.first + min(i0 + (j * kSelThreads + tid) / G, c1 - 1);   // (past the end: the last block again)
       int64_t sb = static_cast<int64_t>(seq) * (p.cap / KVQ_TILE_TOKENS) + i;
       if (p.bt != nullptr) {
         int page = KVQ_IN_RANGE(i < p.bt_stride, p.status) ? p.bt[static_cast<int64_t>(seq) * p.bt_stride + i] : 0;
@@ -430,23 +472,63 @@ __global__ void __launch_bounds__(kSelThreads) select_blocks_kernel(const __grid
       for (int v = 0; v < 4; ++v) w[j][v] = src[v];
       sc[j] = p.b_scales[at];
     }
+  };
+  fetch(c0);
+  // the query in 8 bits: warp g has group g, lane l its channel l
+  if (tid < D) {
+    float up = 0.0f, down = 0.0f;
+    bool finite = true;
+#pragma unroll
+    for (int r = 0; r < 8; ++r) {     // (heads past the group's add nothing)
+      const float v = __uint_as_float(qv[r] << 16);
+      finite &= fabsf(v) < INFINITY;
+      up = __fadd_rn(up, fmaxf(v, 0.0f));
+      down = __fadd_rn(down, fminf(v, 0.0f));
+    }
+    if (!finite) report(p.status, KVQ_ERR_NONFINITE);
+    float a = fmaxf(up, -down);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, o));
+    const float u = __fdiv_rn(a, 127.0f);
+    const float cp = u > 0.0f ? rintf(__fdiv_rn(up, u)) : 0.0f, cn = u > 0.0f ? rintf(__fdiv_rn(down, u)) : 0.0f;
+    int8_t* dst = reinterpret_cast<int8_t*>(s_q[tid / 32]);
+    dst[lane] = static_cast<int8_t>(static_cast<int>(fminf(fmaxf(cp, -127.0f), 127.0f)));
+    dst[32 + lane] = static_cast<int8_t>(static_cast<int>(fminf(fmaxf(cn, -127.0f), 127.0f)));
+    if (lane == 0) s_u[tid / 32] = u;
+  }
+  __syncthreads();
+  uint32_t qc[16];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const uint4 v = *reinterpret_cast<const uint4*>(&s_q[g][4 * i]);
+    qc[4 * i] = v.x; qc[4 * i + 1] = v.y; qc[4 * i + 2] = v.z; qc[4 * i + 3] = v.w;
+  }
+  const float u = s_u[g];
+  const bool in_smem = n <= kSmemKeys;
+  const bool alone = used == 1;
+  uint32_t* gkeys = p.keys + static_cast<int64_t>(seg) * p.key_stride;
+  uint32_t mn = 0xFFFFFFFFu, mx = 0u;
+  for (int i0 = c0; i0 < c1; i0 += kRound) {
+    if (i0 != c0) fetch(i0);
 #pragma unroll
     for (int j = 0; j < U; ++j) {
-      int n = 0;
+      int dots = 0;
 #pragma unroll
       for (int v = 0; v < 4; ++v) {
-        n = __dp4a(static_cast<int>(w[j][v].x), static_cast<int>(qc[4 * v]), n);
-        n = __dp4a(static_cast<int>(w[j][v].y), static_cast<int>(qc[4 * v + 1]), n);
-        n = __dp4a(static_cast<int>(w[j][v].z), static_cast<int>(qc[4 * v + 2]), n);
-        n = __dp4a(static_cast<int>(w[j][v].w), static_cast<int>(qc[4 * v + 3]), n);
+        dots = __dp4a(static_cast<int>(w[j][v].x), static_cast<int>(qc[4 * v]), dots);
+        dots = __dp4a(static_cast<int>(w[j][v].y), static_cast<int>(qc[4 * v + 1]), dots);
+        dots = __dp4a(static_cast<int>(w[j][v].z), static_cast<int>(qc[4 * v + 2]), dots);
+        dots = __dp4a(static_cast<int>(w[j][v].w), static_cast<int>(qc[4 * v + 3]), dots);
       }
-      const float t = __fmul_rn(__fmul_rn(u, sc[j]), static_cast<float>(n));
+      const float t = __fmul_rn(__fmul_rn(u, sc[j]), static_cast<float>(dots));
       float score = __shfl_sync(0xffffffffu, t, lane - g);
 #pragma unroll
       for (int k = 1; k < G; ++k) score = __fadd_rn(score, __shfl_sync(0xffffffffu, t, lane - g + k));
       const int i = i0 + (j * kSelThreads + tid) / G;
       if (g == 0 && i < c1) {
-        const uint32_t key = i < p.first || i >= nblk - p.last ? 0xFFFFFFFFu : key_of(score);
+        const uint32_t key = key_of(score);
+        mn = min(mn, key);
+        mx = max(mx, key);
         if (alone && in_smem) s_keys[i] = key;
         else if (KVQ_IN_RANGE(i < p.key_stride, p.status)) gkeys[i] = key;
       }
@@ -461,13 +543,17 @@ __global__ void __launch_bounds__(kSelThreads) select_blocks_kernel(const __grid
     __syncthreads();
     if (!s_last) return;
     if (tid == 0) p.cnt[seg] = 0;     // ready for the next call
-    if (in_smem) {
-      for (int i = tid; i < nblk; i += kSelThreads) s_keys[i] = __ldcg(gkeys + i);
-      __syncthreads();
+    for (int i = tid; i < n; i += kSelThreads) {
+      const uint32_t key = __ldcg(gkeys + i);
+      mn = min(mn, key);
+      mx = max(mx, key);
+      if (in_smem) s_keys[i] = key;
     }
+    // (select_largest's first barrier orders these before its reads)
   }
-  if (in_smem) select_largest([&](int i) { return s_keys[i]; }, nblk, p.n_select, out, s_hist, s_sums, s_found);
-  else select_largest([&](int i) { return __ldcg(gkeys + i); }, nblk, p.n_select, out, s_hist, s_sums, s_found);
+  out += p.first;
+  if (in_smem) select_largest([&](int i) { return s_keys[i]; }, n, want, p.first, out, mn, mx, sm);
+  else select_largest([&](int i) { return __ldcg(gkeys + i); }, n, want, p.first, out, mn, mx, sm);
 }
 
 cudaLaunchConfig_t config(int64_t blocks, int threads, cudaStream_t stream, cudaLaunchAttribute* attr) {
@@ -500,19 +586,19 @@ cudaError_t launch_block_bounds(const BoundsArgs& a, cudaStream_t stream) {
     p.bits[h] = a.layout.bits[h];
   }
   const bool few = a.chunk.rows <= 4096;
-  p.tiles = few ? a.chunk.rows : (static_cast<int64_t>(a.chunk.rows) + 31) / 32;
+  p.tiles = few ? a.chunk.rows : (static_cast<int64_t>(a.chunk.rows) + 63) / 64;
   cudaLaunchAttribute attr;
   const cudaLaunchConfig_t cfg = config((p.tiles * p.Hkv + kBoundsWarps - 1) / kBoundsWarps, kBoundsWarps * 32, stream, &attr);
   auto launch = [&](auto kernel) { return cudaLaunchKernelEx(&cfg, kernel, p); };
-  if (k.D == 128) return few ? launch(block_bounds_kernel<128, 1>) : launch(block_bounds_kernel<128, 32>);
-  return few ? launch(block_bounds_kernel<64, 1>) : launch(block_bounds_kernel<64, 32>);
+  if (k.D == 128) return few ? launch(block_bounds_kernel<128, 1>) : launch(block_bounds_kernel<128, 64>);
+  return few ? launch(block_bounds_kernel<64, 1>) : launch(block_bounds_kernel<64, 64>);
 }
 
 cudaError_t launch_bounds_values(const kvq_cache& k, const kvq_bounds& bounds, const int32_t* blocks, int32_t n,
                                  float* out, int32_t* status, cudaStream_t stream) {
-  const int64_t threads = static_cast<int64_t>(k.Hkv) * n * (k.D / 2);
+  const int64_t warps = static_cast<int64_t>(k.Hkv) * n;
   cudaLaunchAttribute attr;
-  const cudaLaunchConfig_t cfg = config((threads + 255) / 256, 256, stream, &attr);
+  const cudaLaunchConfig_t cfg = config((warps + kBoundsWarps - 1) / kBoundsWarps, kBoundsWarps * 32, stream, &attr);
   return cudaLaunchKernelEx(&cfg, bounds_values_kernel, static_cast<const int8_t*>(bounds.codes),
                             static_cast<const float*>(bounds.scales), blocks, static_cast<int>(n),
                             static_cast<int>(k.Hkv), static_cast<int64_t>(k.B) * (k.Tcap / KVQ_TILE_TOKENS),
@@ -559,7 +645,7 @@ cudaError_t launch_select_blocks(const SelectArgs& a, cudaStream_t stream) {
   const int64_t segs = static_cast<int64_t>(a.rows) * k.Hkv;
   int64_t per = (segs * nb + 4 * device_sm_count() - 1) / (4 * device_sm_count());
   per = std::max<int64_t>(per, (nb + kMaxChunks - 1) / kMaxChunks);
-  per = std::max<int64_t>((per + 127) / 128 * 128, 128);
+  per = std::max<int64_t>((per + 127) / 128 * 128, kSelectPer);
   p.per_chunk = static_cast<int32_t>(per);
   p.chunks = static_cast<int32_t>(std::max<int64_t>((nb + per - 1) / per, 1));
   cudaLaunchAttribute attr;

@@ -202,20 +202,6 @@ __global__ void __launch_bounds__(kPlanThreads) fork_kernel(const __grid_constan
     }
     p.t.seq_lens[t] = size;
   }
-  __syncthreads();
-  // full pages: a warp per pair
-  for (int i = tid / 32; i < p.n; i += kPlanWarps) {
-    const int full = p.s.size[i] / KVQ_TILE_TOKENS;   // (-1: 0)
-    if (full == 0) continue;
-    const int32_t* row = p.t.table + static_cast<int64_t>(p.from[i]) * p.t.max_pages;
-    int32_t* out = p.t.table + static_cast<int64_t>(p.to[i]) * p.t.max_pages;
-    for (int j = tid & 31; j < full; j += 32) {
-      const int page = row[j];
-      out[j] = page;
-      if (page >= 0 && page < p.t.n_pages) atomicAdd(&p.t.refs[page], 1);
-      else report(p.status, KVQ_ERR_INVALID_ARG);
-    }
-  }
 }
 
 // A warp per listed slot.
@@ -287,8 +273,11 @@ __global__ void __launch_bounds__(kPlanThreads) compact_kernel(const __grid_cons
 }
 
 // Page pairs copied: a warp per (pair, KV head, K or V), whole rows of 16-byte
-// words.  After a plan the pairs are in the workspace; `entries` rows of the
-// page table then get their pages' new places by the same launch.
+// words.  After a plan the pairs are in the workspace, and the same launch does
+// what else takes more than one CTA: the entries of the full pages that a fork
+// shares, a warp per pair (in the planning CTA they took most of its time: 128
+// forks of up to 125 pages with what goes with them 24.3 us, 18.9 us here), or the page table's
+// entries renamed after a compaction, a warp per slot.
 struct CParams {
   const int32_t* pairs;     // number of pairs, null: n
   const int32_t* src;
@@ -298,6 +287,9 @@ struct CParams {
   int8_t* b_codes;
   float* b_scales;
   const int32_t* remap;     // compact: where a page goes, null: nothing to rename
+  const int32_t* from;      // fork: the pairs' slots and lengths (-1: not forked), null: none
+  const int32_t* to;
+  const int32_t* size;
   kvq_page_table t;
   int32_t* status;
   int32_t n, n_pages, Hkv, D;
@@ -353,6 +345,21 @@ __global__ void __launch_bounds__(kCopyWarps * 32) copy_pages_kernel(const __gri
       if (lane < G) p.b_scales[hd * G + lane] = p.b_scales[hs * G + lane];
     }
   }
+  if (p.size != nullptr) {
+    // (from the last warp down: the first ones copy)
+    for (int64_t i = nw - 1 - w0; i < n; i += nw) {
+      const int full = p.size[i] / KVQ_TILE_TOKENS;   // (-1: 0)
+      const int32_t* row = p.t.table + static_cast<int64_t>(p.from[i]) * p.t.max_pages;
+      int32_t* out = p.t.table + static_cast<int64_t>(p.to[i]) * p.t.max_pages;
+#pragma unroll 4
+      for (int j = lane; j < full; j += 32) {
+        const int page = row[j];
+        out[j] = page;
+        if (page >= 0 && page < p.n_pages) atomicAdd(&p.t.refs[page], 1);
+        else report(p.status, KVQ_ERR_INVALID_ARG);
+      }
+    }
+  }
   if (p.remap == nullptr) return;
   for (int64_t s = w0; s < p.t.slots; s += nw) {
     const int len = p.t.seq_lens[s];
@@ -395,9 +402,9 @@ PParams plan_params(const PagesArgs& a) {
   return p;
 }
 
-// most: pairs that the list can have; renames: rows of the page table to rename
+// most: pairs that the list can have
 cudaError_t launch_copy(const PagesArgs& a, const int32_t* pairs, const int32_t* src, const int32_t* dst, int64_t most,
-                        const int32_t* remap, cudaStream_t stream) {
+                        const int32_t* remap, const int32_t* size, cudaStream_t stream) {
   CParams p;
   const kvq_cache& k = *a.k;
   p.pairs = pairs;
@@ -408,6 +415,9 @@ cudaError_t launch_copy(const PagesArgs& a, const int32_t* pairs, const int32_t*
   p.b_codes = a.bounds.codes;
   p.b_scales = a.bounds.scales;
   p.remap = remap;
+  p.from = a.from;
+  p.to = a.to;
+  p.size = size;
   p.t = a.t;
   p.status = a.status;
   p.n = a.n;
@@ -421,6 +431,7 @@ cudaError_t launch_copy(const PagesArgs& a, const int32_t* pairs, const int32_t*
   }
   int64_t warps = most * k.Hkv * 2;
   if (remap != nullptr) warps = std::max<int64_t>(warps, a.t.slots);
+  if (size != nullptr) warps += a.n;
   const int64_t blocks = std::min<int64_t>((warps + kCopyWarps - 1) / kCopyWarps, int64_t(32) * device_sm_count());
   return launch(copy_pages_kernel, p, std::max<int64_t>(blocks, 1), kCopyWarps * 32, stream);
 }
@@ -439,7 +450,7 @@ cudaError_t launch_pages_fork(const PagesArgs& a, cudaStream_t stream) {
   const PParams p = plan_params(a);
   const cudaError_t e = launch(fork_kernel, p, 1, kPlanThreads, stream);
   if (e != cudaSuccess) return e;
-  return launch_copy(a, p.s.pairs, p.s.src, p.s.dst, a.n, nullptr, stream);
+  return launch_copy(a, p.s.pairs, p.s.src, p.s.dst, a.n, nullptr, p.s.size, stream);
 }
 
 cudaError_t launch_pages_free(const PagesArgs& a, cudaStream_t stream) {
@@ -455,11 +466,11 @@ cudaError_t launch_pages_compact(const PagesArgs& a, cudaStream_t stream) {
   const PParams p = plan_params(a);
   const cudaError_t e = launch(compact_kernel, p, 1, kPlanThreads, stream);
   if (e != cudaSuccess) return e;
-  return launch_copy(a, p.s.pairs, p.s.src, p.s.dst, a.t.n_pages / 2, p.s.list, stream);
+  return launch_copy(a, p.s.pairs, p.s.src, p.s.dst, a.t.n_pages / 2, p.s.list, nullptr, stream);
 }
 
 cudaError_t launch_copy_pages(const PagesArgs& a, cudaStream_t stream) {
-  return launch_copy(a, nullptr, a.from, a.to, a.n, nullptr, stream);
+  return launch_copy(a, nullptr, a.from, a.to, a.n, nullptr, nullptr, stream);
 }
 
 }  // namespace kvq

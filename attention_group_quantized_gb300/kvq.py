@@ -179,14 +179,19 @@ def _check(status: int, what: str):
         raise KvqError(status, what)
 
 
-_TORCH = None
+_TORCH = _I32 = _BF16 = _F32 = _EMPTY = _DEVICE = _RAW_STREAM = None
 
 
 def _torch():
-    """torch, imported on first use (an import statement in every call costs more than this)."""
-    global _TORCH
+    """torch, imported on first use (an import statement in every call costs more than this), and the names of it that
+    every call looks up."""
+    global _TORCH, _I32, _BF16, _F32, _EMPTY, _DEVICE, _RAW_STREAM
     if _TORCH is None:
         import torch
+        _I32, _BF16, _F32, _EMPTY = torch.int32, torch.bfloat16, torch.float32, torch.empty
+        # the current device and a device's current stream without the objects that torch.cuda wraps around them
+        _DEVICE = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+        _RAW_STREAM = getattr(torch._C, "_cuda_getCurrentRawStream", lambda d: torch.cuda.current_stream(d).cuda_stream)
         _TORCH = torch
     return _TORCH
 
@@ -213,10 +218,12 @@ class QuantCache:
 
     def c_struct(self) -> CCache:
         """The C view of the cache, rebuilt only when a backing buffer changed."""
-        key = (self.codes.data_ptr(), self.sz.data_ptr(), id(self.head_bits), self.B, self.Hkv, self.Tcap, self.D)
         cached = self.__dict__.get("_c_view")
-        if cached is not None and cached[0] == key:
-            return cached[1]
+        if cached is not None:
+            codes, sz, bits, B, Hkv, Tcap, D = cached[0]
+            if (codes == self.codes.data_ptr() and sz == self.sz.data_ptr() and bits == id(self.head_bits) and B == self.B
+                    and Hkv == self.Hkv and Tcap == self.Tcap and D == self.D):
+                return cached[1]
         hb = np.ascontiguousarray(self.head_bits, dtype=np.int8)
         self.head_bits = hb
         cs = CCache(self.codes.data_ptr(), self.sz.data_ptr(), hb.ctypes.data, self.B, self.Hkv, self.Tcap, self.D)
@@ -606,7 +613,7 @@ def _bad(what: str):
 def _on_current_device(x, *others) -> int:
     """The kernels launch on the current device: every tensor must live there.  Returns its index."""
     i = x.get_device()
-    if i < 0 or i != _torch().cuda.current_device():
+    if i < 0 or i != (_DEVICE or (_torch() and _DEVICE))():
         _bad("tensors that are not on the current CUDA device")
     for o in others:
         if o.get_device() != i:
@@ -618,8 +625,7 @@ def _stream_on(stream, device: int) -> int:
     """The stream to launch on: the caller's, or the device's current one."""
     if stream is not None:
         return stream.cuda_stream
-    raw = getattr(_TORCH._C, "_cuda_getCurrentRawStream", None)
-    return raw(device) if raw is not None else _TORCH.cuda.current_stream().cuda_stream
+    return _RAW_STREAM(device)
 
 
 _INT32_MAX = 0x7FFFFFFF
@@ -635,11 +641,13 @@ def _chunk(start, seq_lens, rows: int, max_chunk: Optional[int]) -> bytes:
     """start: device int32 [B + 1], seq_lens: device int32 [B]."""
     if not 0 <= rows <= _INT32_MAX:
         _bad("rows: 0 .. 2 ** 31 - 1")
-    i32 = _torch().int32
-    if (start.dtype != i32 or seq_lens.dtype != i32 or start.dim() != 1 or seq_lens.dim() != 1
-            or start.shape[0] != seq_lens.shape[0] + 1 or not start.is_contiguous() or not seq_lens.is_contiguous()):
+    if _I32 is None:
+        _torch()
+    B = seq_lens.numel()
+    if (start.dtype is not _I32 or seq_lens.dtype is not _I32 or start.dim() != 1 or seq_lens.dim() != 1
+            or start.numel() != B + 1 or not start.is_contiguous() or not seq_lens.is_contiguous()):
         _bad("chunk: start int32 [B + 1] and seq_lens int32 [B], contiguous")
-    return _pack_chunk(start.data_ptr(), seq_lens.data_ptr(), seq_lens.shape[0], rows,
+    return _pack_chunk(start.data_ptr(), seq_lens.data_ptr(), B, rows,
                        0 if max_chunk is None else _tokens(max_chunk))
 
 
@@ -647,13 +655,18 @@ def _block_table(block_table):
     """The C view of a block table (device int32 [B][max_pages], contiguous), None for None."""
     if block_table is None:
         return None
-    if block_table.dtype != _torch().int32 or block_table.dim() != 2 or not block_table.is_contiguous():
+    if _I32 is None:
+        _torch()
+    if block_table.dtype is not _I32 or block_table.dim() != 2 or not block_table.is_contiguous():
         _bad("block_table: int32 [B][max_pages], contiguous")
-    return _pack_table(block_table.data_ptr(), block_table.shape[0], block_table.shape[1])
+    B, most = block_table.shape
+    return _pack_table(block_table.data_ptr(), B, most)
 
 
 def _packed(x, heads: int, D: int, what: str):
-    if x.dtype != _torch().bfloat16 or x.dim() != 3 or x.shape[1] != heads or x.shape[2] != D or x.stride(2) != 1:
+    if _BF16 is None:
+        _torch()
+    if x.dtype is not _BF16 or x.dim() != 3 or x.shape[1:] != (heads, D) or x.stride(2) != 1:
         _bad(f"{what}: bf16 [rows][{heads}][{D}], channels contiguous")
 
 
@@ -683,13 +696,16 @@ def _workspace(workspace, device: int, stream, make, *args):
 
 
 def _out(out, shape, out_dtype: int, like, what: str, stream):
-    torch = _torch()
+    if _EMPTY is None:
+        _torch()
     if out_dtype != OUT_F32 and out_dtype != OUT_BF16:
         _bad(f"{what}: out_dtype")
-    dt = torch.float32 if out_dtype == OUT_F32 else torch.bfloat16
+    dt = _F32 if out_dtype == OUT_F32 else _BF16
     if out is None:
-        return _made_on(stream, lambda: torch.empty(shape, dtype=dt, device=like.device))
-    if tuple(out.shape) != shape or out.dtype != dt or not out.is_contiguous() or out.get_device() != like.get_device():
+        if stream is None:
+            return _EMPTY(shape, dtype=dt, device=like.device)
+        return _made_on(stream, lambda: _EMPTY(shape, dtype=dt, device=like.device))
+    if out.shape != shape or out.dtype is not dt or not out.is_contiguous() or out.get_device() != like.get_device():
         _bad(f"{what}: out must be contiguous {dt} {shape} on the inputs' device")
     return out
 
@@ -891,18 +907,27 @@ def _same_device(device: int, *tensors):
             _bad("tensors on different devices")
 
 
+def _weight(w, D: int, device: int) -> int:
+    if w is None:
+        return 0
+    if w.dtype is not _BF16 or w.shape != (D,) or w.stride(0) != 1:
+        _bad("norm weights: bf16 [D], contiguous")
+    if w.get_device() != device:
+        _bad("tensors on different devices")
+    return w.data_ptr()
+
+
 def _rotation(rotary, q_weight, k_weight, eps: float, interleaved: bool, D: int, device: int) -> bytes:
-    torch = _torch()
-    for w in (q_weight, k_weight):
-        if w is not None and (w.dtype != torch.bfloat16 or tuple(w.shape) != (D,) or not w.is_contiguous()):
-            _bad("norm weights: bf16 [D], contiguous")
-    if rotary is not None and (rotary.dtype != torch.float32 or rotary.dim() != 2 or not rotary.is_contiguous()):
-        _bad("rotary: fp32 [positions][rot_dim], contiguous")
-    _same_device(device, rotary, q_weight, k_weight)
-    ptr = lambda t: 0 if t is None else t.data_ptr()
-    positions, rot = (0, 0) if rotary is None else rotary.shape
-    return _pack_rotation(ptr(rotary), ptr(q_weight), ptr(k_weight), _tokens(positions), _tokens(rot),
-                          1 if interleaved else 0, eps)
+    at = positions = rot = 0
+    if rotary is not None:
+        if rotary.dtype is not _F32 or rotary.dim() != 2 or not rotary.is_contiguous():
+            _bad("rotary: fp32 [positions][rot_dim], contiguous")
+        if rotary.get_device() != device:
+            _bad("tensors on different devices")
+        at = rotary.data_ptr()
+        positions, rot = rotary.shape
+    return _pack_rotation(at, _weight(q_weight, D, device), _weight(k_weight, D, device), _tokens(positions),
+                          _tokens(rot), 1 if interleaved else 0, eps)
 
 
 def _rotate_append(q, k_new, v_new, k: QuantCache, v: QuantCache, block_table, start, seq_lens, rotary, q_weight, k_weight,
@@ -911,9 +936,9 @@ def _rotate_append(q, k_new, v_new, k: QuantCache, v: QuantCache, block_table, s
         _bad("q: bf16 [rows][Hq][D]")
     rows, Hq, D = q.shape
     _packed(q, Hq, k.D, "q")
-    _packed(k_new, k.Hkv, k.D, "k_new")
-    _packed(v_new, k.Hkv, k.D, "v_new")
-    if k_new.shape[0] != rows or v_new.shape[0] != rows or k_new.stride() != v_new.stride():
+    _packed(k_new, k.Hkv, D, "k_new")
+    strides = k_new.stride()
+    if k_new.shape[0] != rows or v_new.shape != k_new.shape or v_new.dtype is not _BF16 or v_new.stride() != strides:
         _bad("q, k_new and v_new: the same rows; k_new and v_new: the same strides")
     bt = _block_table(block_table)
     dev = _on_current_device(q, k_new, v_new, k.codes, k.sz, v.codes, v.sz, start, seq_lens)
@@ -922,7 +947,7 @@ def _rotate_append(q, k_new, v_new, k: QuantCache, v: QuantCache, block_table, s
     out = _out(out, (rows, Hq, D), OUT_BF16, q, "rotate_append", stream)
     ch = _chunk(start, seq_lens, rows, None)
     sq_row, sq_head, _ = q.stride()
-    s_row, s_head, _ = k_new.stride()
+    s_row, s_head, _ = strides
     if bt is None:
         st = lib().kvq_rotate_append(q.data_ptr(), sq_row, sq_head, k_new.data_ptr(), v_new.data_ptr(), s_row, s_head, ch,
                                      rot, Hq, k.c_struct(), v.c_struct(), out.data_ptr(), OUT_BF16 | rest,
@@ -969,6 +994,8 @@ class BlockBounds:
 
 
 _pack_bounds = struct.Struct("@PP").pack   # kvq_bounds
+_EIGHT_BITS = np.full(64, 8, np.int8)
+_EIGHTS = _EIGHT_BITS.ctypes.data
 
 
 def empty_bounds(k: QuantCache) -> BlockBounds:
@@ -982,14 +1009,13 @@ def empty_bounds(k: QuantCache) -> BlockBounds:
 def _bounds(bounds, k: QuantCache, device: int):
     if bounds is None:
         return None
-    torch = _torch()
-    G = k.D // GROUP
-    blocks = k.B * (k.Tcap // TILE_TOKENS)
     c, s = bounds.codes, bounds.scales
-    if (c.dtype != torch.int8 or tuple(c.shape) != (k.Hkv, blocks, G, 2, GROUP) or not c.is_contiguous()
-            or s.dtype != torch.float32 or tuple(s.shape) != (k.Hkv, blocks, G) or not s.is_contiguous()):
+    shape = (k.Hkv, k.B * (k.Tcap // TILE_TOKENS), k.D // GROUP)
+    if (c.dtype is not _TORCH.int8 or c.shape != shape + (2, GROUP) or not c.is_contiguous() or s.dtype is not _F32
+            or s.shape != shape or not s.is_contiguous()):
         _bad("bounds: those of this cache's shape (empty_bounds)")
-    _same_device(device, c, s)
+    if c.get_device() != device or s.get_device() != device:
+        _bad("tensors on different devices")
     return _pack_bounds(c.data_ptr(), s.data_ptr())
 
 
@@ -1022,17 +1048,22 @@ def block_bounds_paged(k_pool: QuantCache, bounds: BlockBounds, block_table, sta
 def bounds_values(bounds: BlockBounds, blocks, out=None, status=None, stream=None):
     """The greatest and least values that listed storage blocks' bounds stand for: fp32 [Hkv][n][2][D] of blocks
     int32 [n] (a pool's page ids, or b * Tcap / 64 + i)."""
-    torch = _torch()
-    Hkv, n_blocks, G = bounds.scales.shape
-    if blocks.dtype != torch.int32 or blocks.dim() != 1 or not blocks.is_contiguous():
+    if _TORCH is None:
+        _torch()
+    codes, scales = bounds.codes, bounds.scales
+    if blocks.dtype is not _I32 or blocks.dim() != 1 or not blocks.is_contiguous():
         _bad("blocks: int32 [n], contiguous")
-    n = blocks.shape[0]
-    dev = _on_current_device(bounds.codes, bounds.scales, blocks)
-    shape = QuantCache(bounds.codes, bounds.scales, np.full(Hkv, 8, np.int8), n_blocks, Hkv, TILE_TOKENS, G * GROUP)
-    bb = _bounds(bounds, shape, dev)
-    out = _out(out, (Hkv, n, 2, G * GROUP), OUT_F32, bounds.codes, "bounds_values", stream)
-    st = lib().kvq_bounds_values(shape.c_struct(), bb, blocks.data_ptr(), n, out.data_ptr(), _status_on(status, dev),
-                                 _stream_on(stream, dev))
+    if (scales.dim() != 3 or scales.dtype is not _F32 or codes.dtype is not _TORCH.int8 or not scales.is_contiguous()
+            or codes.shape != scales.shape + (2, GROUP) or not codes.is_contiguous()):
+        _bad("bounds: codes int8 [Hkv][blocks][D / 32][2][32], scales fp32 [Hkv][blocks][D / 32], contiguous")
+    Hkv, n_blocks, G = scales.shape
+    n = blocks.numel()
+    dev = _on_current_device(codes, scales, blocks)
+    # (the call asks a cache for its shape alone: as many pages of any width)
+    view = CCache(None, None, _EIGHTS, _tokens(n_blocks), _tokens(Hkv), TILE_TOKENS, G * GROUP)
+    out = _out(out, (Hkv, n, 2, G * GROUP), OUT_F32, codes, "bounds_values", stream)
+    st = lib().kvq_bounds_values(view, _pack_bounds(codes.data_ptr(), scales.data_ptr()), blocks.data_ptr(), n,
+                                 out.data_ptr(), _status_on(status, dev), _stream_on(stream, dev))
     _check(st, "kvq_bounds_values")
     return out
 
@@ -1048,43 +1079,46 @@ def select_workspace(rows: int, Hkv: int, capacity: int, device="cuda"):
 
 
 def _query_rows(q, k: QuantCache, row_lens, row_seq):
-    torch = _torch()
-    if q.dim() != 3 or q.dtype != torch.bfloat16 or not q.is_contiguous() or q.shape[2] != k.D:
+    if _TORCH is None:
+        _torch()
+    if q.dim() != 3 or q.dtype is not _BF16 or not q.is_contiguous() or q.shape[2] != k.D:
         _bad("q: contiguous bf16 [rows][Hq][D]")
-    for x in (row_lens, row_seq):
-        if x is not None and (x.dtype != torch.int32 or x.dim() != 1 or x.shape[0] != q.shape[0] or not x.is_contiguous()):
-            _bad("row_lens, row_seq: int32 [rows], contiguous")
-    return q.shape
+    shape = q.shape
+    n = shape[:1]
+    if (row_lens.dtype is not _I32 or row_lens.shape != n or not row_lens.is_contiguous() or row_seq is not None
+            and (row_seq.dtype is not _I32 or row_seq.shape != n or not row_seq.is_contiguous())):
+        _bad("row_lens, row_seq: int32 [rows], contiguous")
+    return shape
 
 
 def _select_blocks(q, k: QuantCache, bounds: BlockBounds, block_table, row_lens, n_select, first, last, row_seq, out,
                    workspace, status, stream):
-    torch = _torch()
     rows, Hq, D = _query_rows(q, k, row_lens, row_seq)
-    bt = _block_table(block_table)
     dev = _on_current_device(q, k.codes, row_lens)
-    _same_device(dev, row_seq, block_table)
-    bb = _bounds(bounds, k, dev)
+    if row_seq is not None and row_seq.get_device() != dev or block_table is not None and block_table.get_device() != dev:
+        _bad("tensors on different devices")
     shape = (rows, k.Hkv, n_select)
     if out is None:
         if not 1 <= n_select <= 65536:
             _bad("n_select: 1 .. 65536")
-        out = _made_on(stream, lambda: torch.empty(shape, dtype=torch.int32, device=q.device))
-    elif tuple(out.shape) != shape or out.dtype != torch.int32 or not out.is_contiguous() or out.get_device() != dev:
+        if stream is None:
+            out = _EMPTY(shape, dtype=_I32, device=q.device)
+        else:
+            out = _made_on(stream, lambda: _EMPTY(shape, dtype=_I32, device=q.device))
+    elif out.shape != shape or out.dtype is not _I32 or not out.is_contiguous() or out.get_device() != dev:
         _bad("select_blocks: out int32 [rows][Hkv][n_select], contiguous, on the inputs' device")
-    cap = k.Tcap if bt is None else TILE_TOKENS * block_table.shape[1]
-    workspace = _workspace(workspace, dev, stream, select_workspace, rows, k.Hkv, cap, q.device)
-    ws_n = workspace.numel() * workspace.element_size()
-    first, last = _tokens(first), _tokens(last)
+    workspace = _workspace(workspace, dev, stream, select_workspace, rows, k.Hkv,
+                           k.Tcap if block_table is None else TILE_TOKENS * block_table.shape[-1], q.device)
     seq_p = None if row_seq is None else row_seq.data_ptr()
-    if bt is None:
-        st = lib().kvq_select_blocks(q.data_ptr(), k.c_struct(), bb, seq_p, row_lens.data_ptr(), rows, Hq, n_select, first,
-                                     last, out.data_ptr(), workspace.data_ptr(), ws_n, _status_on(status, dev),
-                                     _stream_on(stream, dev))
+    if block_table is None:
+        st = lib().kvq_select_blocks(q.data_ptr(), k.c_struct(), _bounds(bounds, k, dev), seq_p, row_lens.data_ptr(), rows,
+                                     Hq, n_select, _tokens(first), _tokens(last), out.data_ptr(), workspace.data_ptr(),
+                                     workspace.nbytes, _status_on(status, dev), _stream_on(stream, dev))
         _check(st, "kvq_select_blocks")
     else:
-        st = lib().kvq_select_blocks_paged(q.data_ptr(), k.c_struct(), bb, bt, seq_p, row_lens.data_ptr(), rows, Hq,
-                                           n_select, first, last, out.data_ptr(), workspace.data_ptr(), ws_n,
+        st = lib().kvq_select_blocks_paged(q.data_ptr(), k.c_struct(), _bounds(bounds, k, dev), _block_table(block_table),
+                                           seq_p, row_lens.data_ptr(), rows, Hq, n_select, _tokens(first), _tokens(last),
+                                           out.data_ptr(), workspace.data_ptr(), workspace.nbytes,
                                            _status_on(status, dev), _stream_on(stream, dev))
         _check(st, "kvq_select_blocks_paged")
     return out
@@ -1108,30 +1142,26 @@ def select_blocks_paged(q, k_pool: QuantCache, bounds: BlockBounds, block_table,
 
 def _decode_blocks(q, k: QuantCache, v: QuantCache, block_table, blocks, row_lens, row_seq, softmax_scale, out, out_dtype,
                    workspace, status, stream):
-    torch = _torch()
-    rows, Hq, D = _query_rows(q, k, row_lens, row_seq)
-    if (blocks.dtype != torch.int32 or blocks.dim() != 3 or blocks.shape[0] != rows or blocks.shape[1] != k.Hkv
-            or not blocks.is_contiguous()):
+    rows, Hq, D = shape = _query_rows(q, k, row_lens, row_seq)
+    if blocks.dtype is not _I32 or blocks.dim() != 3 or blocks.shape[:2] != (rows, k.Hkv) or not blocks.is_contiguous():
         _bad("blocks: int32 [rows][Hkv][n_select], contiguous")
-    bt = _block_table(block_table)
     dev = _on_current_device(q, k.codes, k.sz, v.codes, v.sz, blocks, row_lens)
-    _same_device(dev, row_seq, block_table)
-    out = _out(out, (rows, Hq, D), out_dtype, q, "decode_attention_blocks", stream)
+    if row_seq is not None and row_seq.get_device() != dev or block_table is not None and block_table.get_device() != dev:
+        _bad("tensors on different devices")
+    out = _out(out, shape, out_dtype, q, "decode_attention_blocks", stream)
     workspace = _workspace(workspace, dev, stream, decode_workspace, rows, Hq, k.Hkv, D, q.device)
-    ws_n = workspace.numel() * workspace.element_size()
     seq_p = None if row_seq is None else row_seq.data_ptr()
-    n_select = blocks.shape[2]
-    if bt is None:
-        st = lib().kvq_decode_attention_blocks(q.data_ptr(), k.c_struct(), v.c_struct(), blocks.data_ptr(), n_select,
-                                               seq_p, row_lens.data_ptr(), rows, Hq, softmax_scale, out.data_ptr(),
-                                               out_dtype, workspace.data_ptr(), ws_n, _status_on(status, dev),
-                                               _stream_on(stream, dev))
+    if block_table is None:
+        st = lib().kvq_decode_attention_blocks(q.data_ptr(), k.c_struct(), v.c_struct(), blocks.data_ptr(),
+                                               blocks.shape[2], seq_p, row_lens.data_ptr(), rows, Hq, softmax_scale,
+                                               out.data_ptr(), out_dtype, workspace.data_ptr(), workspace.nbytes,
+                                               _status_on(status, dev), _stream_on(stream, dev))
         _check(st, "kvq_decode_attention_blocks")
     else:
-        st = lib().kvq_decode_attention_blocks_paged(q.data_ptr(), k.c_struct(), v.c_struct(), bt, blocks.data_ptr(),
-                                                     n_select, seq_p, row_lens.data_ptr(), rows, Hq, softmax_scale,
-                                                     out.data_ptr(), out_dtype, workspace.data_ptr(), ws_n,
-                                                     _status_on(status, dev), _stream_on(stream, dev))
+        st = lib().kvq_decode_attention_blocks_paged(q.data_ptr(), k.c_struct(), v.c_struct(), _block_table(block_table),
+                                                     blocks.data_ptr(), blocks.shape[2], seq_p, row_lens.data_ptr(), rows,
+                                                     Hq, softmax_scale, out.data_ptr(), out_dtype, workspace.data_ptr(),
+                                                     workspace.nbytes, _status_on(status, dev), _stream_on(stream, dev))
         _check(st, "kvq_decode_attention_blocks_paged")
     return out
 
@@ -1187,19 +1217,21 @@ def pages_workspace(n_pages: int, slots: int, device="cuda"):
 
 
 def _page_table(pages: PageTable):
-    i32 = _torch().int32
+    if _I32 is None:
+        _torch()
     r, t, s = pages.refs, pages.table, pages.seq_lens
-    if (r.dtype != i32 or t.dtype != i32 or s.dtype != i32 or r.dim() != 1 or t.dim() != 2 or s.dim() != 1
-            or t.shape[0] != s.shape[0] or not r.is_contiguous() or not t.is_contiguous() or not s.is_contiguous()):
+    if (r.dtype is not _I32 or t.dtype is not _I32 or s.dtype is not _I32 or r.dim() != 1 or t.dim() != 2
+            or t.shape[:1] != s.shape or not r.is_contiguous() or not t.is_contiguous() or not s.is_contiguous()):
         _bad("page table: int32 refs [n_pages], table [slots][max_pages], seq_lens [slots], contiguous")
     dev = _on_current_device(r, t, s)
-    return dev, _pack_page_table(r.data_ptr(), t.data_ptr(), s.data_ptr(), r.shape[0], t.shape[0], t.shape[1])
+    slots, most = t.shape
+    return dev, _pack_page_table(r.data_ptr(), t.data_ptr(), s.data_ptr(), r.numel(), slots, most)
 
 
 def _ids(x, device: int, what: str) -> int:
-    if x.dtype != _torch().int32 or x.dim() != 1 or not x.is_contiguous() or x.get_device() != device:
+    if x.dtype is not _I32 or x.dim() != 1 or not x.is_contiguous() or x.get_device() != device:
         _bad(f"{what}: int32 [n], contiguous, on the page table's device")
-    return x.shape[0]
+    return x.numel()
 
 
 def _pages_ws(workspace, pages: PageTable, device: int, stream):
@@ -1214,7 +1246,7 @@ def pages_reserve(pages: PageTable, add, workspace=None, status=None, stream=Non
     if _ids(add, dev, "add") != pages.table.shape[0]:
         _bad("add: int32 [slots]")
     ws = _pages_ws(workspace, pages, dev, stream)
-    st = lib().kvq_pages_reserve(pt, add.data_ptr(), ws.data_ptr(), ws.numel() * ws.element_size(),
+    st = lib().kvq_pages_reserve(pt, add.data_ptr(), ws.data_ptr(), ws.nbytes,
                                  _status_on(status, dev), _stream_on(stream, dev))
     _check(st, "kvq_pages_reserve")
 
@@ -1231,7 +1263,7 @@ def pages_fork(pages: PageTable, k_pool: QuantCache, v_pool: QuantCache, from_sl
     ws = _pages_ws(workspace, pages, dev, stream)
     st = lib().kvq_pages_fork(pt, k_pool.c_struct(), v_pool.c_struct(), _bounds(bounds, k_pool, dev),
                               from_slots.data_ptr(), to_slots.data_ptr(), n, ws.data_ptr(),
-                              ws.numel() * ws.element_size(), _status_on(status, dev), _stream_on(stream, dev))
+                              ws.nbytes, _status_on(status, dev), _stream_on(stream, dev))
     _check(st, "kvq_pages_fork")
 
 
@@ -1254,7 +1286,7 @@ def pages_compact(pages: PageTable, k_pool: QuantCache, v_pool: QuantCache, boun
     ws = _pages_ws(workspace, pages, dev, stream)
     st = lib().kvq_pages_compact(pt, k_pool.c_struct(), v_pool.c_struct(), _bounds(bounds, k_pool, dev),
                                  None if n_live is None else n_live.data_ptr(), ws.data_ptr(),
-                                 ws.numel() * ws.element_size(), _status_on(status, dev), _stream_on(stream, dev))
+                                 ws.nbytes, _status_on(status, dev), _stream_on(stream, dev))
     _check(st, "kvq_pages_compact")
 
 
@@ -1262,6 +1294,8 @@ def copy_pages(k_pool: QuantCache, v_pool: QuantCache, src, dst, bounds: Optiona
                stream=None):
     """Pages dst (int32 [n]) of both pools (and the bounds) become copies of pages src; a pair with -1 is skipped."""
     dev = _on_current_device(k_pool.codes, k_pool.sz, v_pool.codes, v_pool.sz)
+    if _I32 is None:
+        _torch()
     n = _ids(src, dev, "src")
     if _ids(dst, dev, "dst") != n:
         _bad("src and dst: one length")
