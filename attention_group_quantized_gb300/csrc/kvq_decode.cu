@@ -215,7 +215,10 @@ constexpr int kNoTile = 0xFFFFFF;
 // window's first token on.  Index i of that list is tile(i); the
 // work list, the split and the merge only ever see the indices.  With a list
 // they are as many as the list can have, the same for every KV head; which ones,
-// the issuer looks up (ListedTiles) and hands on with the copies.
+// the issuer looks up (issue_listed) and hands on with the copies.  (32 listed
+// tiles of eight 32K sequences, 8 KV heads, INT8: 37.7 MB in 17.8 us, against
+// 14.9 us for the first 32 tiles without a list: the look-up, which the first
+// copies wait for, and no tiles warmed into L2 before it.)
 // (Eight 32K sequences, INT8, window 4096, four sinks: 75.7 MB in 20.7 us, 3.7
 // TB/s -- the pipeline of the call without a window on an eighth of the tiles,
 // so that its start and merge weigh more: 151 MB take 30.5 us, 4.95 TB/s.)

@@ -21,6 +21,11 @@
 // rot_dim / 16 away (or, interleaved, in the lane itself); a quantisation group
 // is four lanes, which exchange quarters so that each has a head's whole group
 // and works out its scale once.
+//
+// Measured: 32K rows of 32 + 8 + 8 heads, half of the channels turned, INT4, 722
+// MB, 203 us, 3.6 TB/s (its floor is 107 us at 6.78 TB/s): bound by issue slots,
+// 211 instructions a warp and head, of which the norm has about 90, the rotation
+// 45, a key's or value's quantisation 90.
 #include <algorithm>
 #include <type_traits>
 
