@@ -1170,7 +1170,7 @@ def decode_attention_blocks(q, k: QuantCache, v: QuantCache, blocks, row_lens, r
                             out=None, out_dtype: int = OUT_F32, workspace=None, status=None, stream=None):
     """decode_attention over listed blocks: row r of q bf16 [rows][Hq][D] attends the first row_lens[r] tokens of its
     sequence (row_seq[r], None: r) that lie in the blocks blocks[r][KV head] (select_blocks's result).  workspace: a
-    decode_workspace of `rows` sequences.  Returns [rows][Hq][D]."""
+    decode_workspace of `rows` sequences, for calls of this shape alone.  Returns [rows][Hq][D]."""
     return _decode_blocks(q, k, v, None, blocks, row_lens, row_seq, softmax_scale, out, out_dtype, workspace, status,
                           stream)
 

@@ -786,7 +786,9 @@ KVQ_API kvq_status kvq_select_blocks_paged(const void* q, const kvq_cache* k_poo
  * left out (the entry after it is compared with it all the same).  A row
  * without a token gives zeros.  Blocks that are not listed may hold anything.
  * q, out: [rows][Hq][D]; workspace: kvq_decode_workspace_bytes(rows, Hq, Hkv,
- * D) bytes.  Other arguments and errors as kvq_decode_attention.
+ * D) bytes, for calls of one rows, Hq, Hkv and D (its counters' place depends on
+ * them: zero-fill it again before calls of another shape).  Other arguments and
+ * errors as kvq_decode_attention.
  */
 KVQ_API kvq_status kvq_decode_attention_blocks(const void* q, const kvq_cache* k, const kvq_cache* v,
                                                const int32_t* blocks, int32_t n_select, const int32_t* row_seq,
