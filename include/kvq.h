@@ -653,7 +653,7 @@ typedef struct kvq_rotation {
  *   with a table:     pair (a, b) -> (a * cos - b * sin, b * cos + a * sin)
  * then rounded to bf16.  Keys are quantised from that bf16 value exactly as
  * kvq_quantize does it, so the codes are a function of the inputs.  (m is
- * exact to 2^-40 before its rounding.)
+ * within 2^-38 of the exact mean before its rounding.)
  *
  * q: device bf16, channel d of (row r, query head h) at
  *   q[r * sq_row + h * sq_head + d]; k_new, v_new as kvq_append_chunk (the
