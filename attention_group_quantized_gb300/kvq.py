@@ -930,6 +930,12 @@ def _rotation(rotary, q_weight, k_weight, eps: float, interleaved: bool, D: int,
                           _tokens(rot), 1 if interleaved else 0, eps)
 
 
+def _strides(x):
+    """Row and head strides of packed rows, 0 where there is one row or head (torch leaves those anything)."""
+    (rows, heads, _), (s_row, s_head, _) = x.shape, x.stride()
+    return (s_row if rows > 1 else 0), (s_head if heads > 1 else 0)
+
+
 def _rotate_append(q, k_new, v_new, k: QuantCache, v: QuantCache, block_table, start, seq_lens, rotary, q_weight, k_weight,
                    eps, interleaved, out, status, stream):
     if q.dim() != 3:
@@ -937,8 +943,8 @@ def _rotate_append(q, k_new, v_new, k: QuantCache, v: QuantCache, block_table, s
     rows, Hq, D = q.shape
     _packed(q, Hq, k.D, "q")
     _packed(k_new, k.Hkv, D, "k_new")
-    strides = k_new.stride()
-    if k_new.shape[0] != rows or v_new.shape != k_new.shape or v_new.dtype is not _BF16 or v_new.stride() != strides:
+    if (k_new.shape[0] != rows or v_new.shape != k_new.shape or v_new.dtype is not _BF16 or v_new.stride(2) != 1
+            or _strides(v_new) != _strides(k_new)):
         _bad("q, k_new and v_new: the same rows; k_new and v_new: the same strides")
     bt = _block_table(block_table)
     dev = _on_current_device(q, k_new, v_new, k.codes, k.sz, v.codes, v.sz, start, seq_lens)
@@ -946,8 +952,8 @@ def _rotate_append(q, k_new, v_new, k: QuantCache, v: QuantCache, block_table, s
     rest = _ZERO_REST if out is None else 0
     out = _out(out, (rows, Hq, D), OUT_BF16, q, "rotate_append", stream)
     ch = _chunk(start, seq_lens, rows, None)
-    sq_row, sq_head, _ = q.stride()
-    s_row, s_head, _ = strides
+    sq_row, sq_head = _strides(q)
+    s_row, s_head = _strides(k_new)
     if bt is None:
         st = lib().kvq_rotate_append(q.data_ptr(), sq_row, sq_head, k_new.data_ptr(), v_new.data_ptr(), s_row, s_head, ch,
                                      rot, Hq, k.c_struct(), v.c_struct(), out.data_ptr(), OUT_BF16 | rest,

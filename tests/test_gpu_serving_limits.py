@@ -241,3 +241,91 @@ def test_the_debug_build_finds_no_index_out_of_range(kvq, D, Hq, Hkv, paged, row
             results.append([t.clone() for t in outs])
     for a, c in zip(*results):
         assert torch.equal(a.view(torch.uint8), c.view(torch.uint8))
+
+
+def test_two_graphs_of_different_shapes_share_a_workspace(kvq):
+    """Captured selections that share a workspace, replayed in turn: each leaves it as the other needs it."""
+    ws = kvq.select_workspace(8, 2, 64 * 3000)
+    gen = torch.Generator(device="cuda").manual_seed(6)
+    parts = []
+    for B, Hkv, blocks, n in ((1, 2, 3000, 50), (8, 1, 900, 7)):
+        k = kvq.empty_cache([4] * Hkv, B, blocks * 64, 128)
+        b = kvq.empty_bounds(k)
+        b.codes.copy_(torch.randint(-127, 128, b.codes.shape, generator=gen, device="cuda", dtype=torch.int8))
+        b.scales.copy_(torch.rand(b.scales.shape, generator=gen, device="cuda"))
+        q = torch.randn((B, 4 * Hkv, 128), generator=gen, device="cuda").bfloat16()
+        lens = _dev([blocks * 64] * B)
+        out = torch.empty((B, Hkv, n), dtype=torch.int32, device="cuda")
+        want = kvq.select_blocks(q, k, b, lens, n)
+        kvq.select_blocks(q, k, b, lens, n, out=out, workspace=ws)
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            kvq.select_blocks(q, k, b, lens, n, out=out, workspace=ws)
+        parts.append((graph, out, want, (k, b, q, lens)))
+    for _ in range(3):
+        for graph, out, want, _ in parts:
+            out.fill_(-7)
+            graph.replay()
+            torch.cuda.synchronize()
+            assert torch.equal(out, want)
+
+
+def test_strides_of_single_rows_and_heads_do_not_matter(kvq):
+    """A stride that no index uses may be anything: one KV head, or one row, from tensors laid out differently."""
+    gen = torch.Generator(device="cuda").manual_seed(8)
+    for rows, Hkv in ((5, 1), (1, 2), (1, 1)):
+        k, v = (kvq.empty_cache([8] * Hkv, 1, 64, 64) for _ in range(2))
+        start, lens = _dev([0, rows]), _dev([rows])
+        x = torch.randn((rows, 4 * Hkv, 64), generator=gen, device="cuda").bfloat16()
+        q, kn, vn = x[:, :2 * Hkv], x[:, 2 * Hkv:3 * Hkv], x[:, 3 * Hkv:]
+        if rows > 1:                                                # the same row stride, another head stride
+            vn = vn.as_strided(vn.shape, (vn.stride(0), 3, 1), vn.storage_offset())
+        else:
+            vn = vn.as_strided(vn.shape, (7, vn.stride(1) if Hkv > 1 else 5, 1), vn.storage_offset())
+        got = kvq.rotate_append(q, kn, vn, k, v, start, lens)
+        assert torch.equal(got, q)
+        k2, v2 = (kvq.empty_cache([8] * Hkv, 1, 64, 64) for _ in range(2))
+        kvq.append_chunk(x[:, 2 * Hkv:3 * Hkv], x[:, 3 * Hkv:], k2, v2, start, lens)
+        assert torch.equal(kvq.dequantize(v, start, lens, rows), kvq.dequantize(v2, start, lens, rows))
+        assert torch.equal(kvq.dequantize(k, start, lens, rows), kvq.dequantize(k2, start, lens, rows))
+
+
+@pytest.mark.parametrize("case", range(12))
+def test_random_rotated_appends_against_the_append(kvq, case):
+    """Without norm and rotation the call is the append; with them, the append of the turned keys: equal caches, byte for
+    byte, over random shapes."""
+    rng = np.random.default_rng(100 + case)
+    B, D, Hkv = int(rng.integers(1, 9)), int(rng.choice([64, 128])), int(rng.choice([1, 2, 3, 5, 8]))
+    Hq = Hkv * int(rng.choice([1, 2, 4, 7]))
+    bits = [int(x) for x in rng.choice([4, 8], Hkv)]
+    new = [int(x) for x in rng.integers(0, int(rng.choice([3, 40, 400])), B)]
+    lens = [n + int(rng.integers(0, 200)) for n in new]
+    T, cap = sum(new), -(-max(max(lens), 1) // 64) * 64
+    x = R.bf16_bits(rng.standard_normal((T, Hq + 2 * Hkv, D)).astype(np.float32))
+    rot = int(rng.choice([0, 16, D // 2, D]))
+    inter, eps = bool(rng.random() < 0.5), 1e-5
+    table = rng.uniform(-1, 1, (cap, rot)).astype(np.float32) if rot else None
+    w = R.bf16_bits(rng.uniform(0.5, 2, D).astype(np.float32)) if rng.random() < 0.7 else None
+    start = np.concatenate([[0], np.cumsum(new)])
+    pos = np.concatenate([np.arange(L - n, L) for n, L in zip(new, lens)] or [[]]).astype(int)
+    made = [[kvq.empty_cache(bits, B, cap, D) for _ in range(2)] for _ in range(2)]
+    for pair in made:
+        for c in pair:
+            c.codes.fill_(1)
+            c.sz.fill_(2)
+    rows = U.to_dev_bf16(x)
+    st = _status()
+    dev_w = None if w is None else U.to_dev_bf16(w)
+    q = kvq.rotate_append(rows[:, :Hq], rows[:, Hq:Hq + Hkv], rows[:, Hq + Hkv:], *made[0], _dev(start), _dev(lens),
+                          rotary=None if table is None else _dev(table, np.float32), q_weight=dev_w, k_weight=dev_w,
+                          eps=eps, interleaved=inter, status=st)
+    if T:
+        assert np.array_equal(q.cpu().view(torch.int16).numpy().view(np.uint16),
+                              R.turn(x[:, :Hq], w, table, pos, eps, inter)[0])
+        turned = U.to_dev_bf16(R.turn(x[:, Hq:Hq + Hkv], w, table, pos, eps, inter)[0])
+        kv = torch.stack([turned, rows[:, Hq + Hkv:]])
+        kvq.append_chunk(kv[0], kv[1], *made[1], _dev(start), _dev(lens), status=st)
+    assert int(st) == 0
+    for a, b in zip(*made):
+        assert torch.equal(a.codes, b.codes) and torch.equal(a.sz, b.sz)
