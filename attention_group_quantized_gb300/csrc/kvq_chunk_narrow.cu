@@ -27,9 +27,9 @@
 // TMEM: S^T and O^T of each state, NR columns each.
 //
 // Measured: long contexts are bound by HBM's reads (eight sequences of 32K, 16
-// rows, INT8: 590 MB in 118 us, 5.0 TB/s over the call, 0.95 us per 36 KB tile an
+// rows, INT8: 590 MB in 123 us, 4.8 TB/s over the call, 1 us per 36 KB tile an
 // SM); a call of one tile takes 10 us, and a segment's cut about 9 us (eight
-// sequences of 8K: 42 us).  Fetching the codes into L2 further ahead was slower (54 us against 49 for
+// sequences of 8K: 43 us).  Fetching the codes into L2 further ahead was slower (54 us against 49 for
 // eight sequences of 8K), and so were slots of 32 tokens (more copies).
 #include <cmath>
 #include <mutex>
@@ -170,8 +170,6 @@ __device__ __forceinline__ bool dequant_piece(const CParams& p, uint8_t* smem, u
           word[i] = words[it * F::RPI * (D / 32)];
         }
       }
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&bar[B_RFREE0 + k]);
       if (mine) {
 #pragma unroll
         for (int i = 0; i < N; ++i) {
@@ -180,6 +178,16 @@ __device__ __forceinline__ bool dequant_piece(const CParams& p, uint8_t* smem, u
           most = __vmaxu2(most, word[i]);
         }
       }
+      // The slot is free once its values have been used, not once their loads
+      // are issued: the copy that refills it writes through the async proxy,
+      // which an arrival after loads in flight does not hold back (released
+      // there, about one call in a hundred of long 4-bit sequences had a wrong
+      // segment, none of 8000 since; all had a last tile whose half stands for
+      // the other, a copy that comes early, from L2).  8-bit heads pay 4 % on
+      // long contexts, 118 -> 123 us, 4-bit ones gain 9, 136 -> 124; an arrival
+      // that hangs on the loaded values before the conversion: 122 and 138 us.
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bar[B_RFREE0 + k]);
       if (++slot == kRing) {
         slot = 0;
         ++round;
@@ -817,11 +825,11 @@ kvq_status launch_n(const CParams& p, cudaStream_t stream) {
 // the 256-row kernel's 66.  Measured (us; this kernel, the 256-row one; eight
 // sequences, 8 KV heads, D = 128):
 //   tokens        200       1000       2000       4000       8000       32000
-//   INT8 16   11.0 12.5  16.6 21.8  20.1 27.1  27.7 40.6  41.8 65.5  118  189
-//        24   14.3 12.7  21.4 22.0  25.7 27.5  34.3 40.7  54.7 65.6  135  189
-//        32   14.7 12.6  21.8 22.0  26.8 27.2  35.3 40.9  55.9 65.0  137  188
-//   INT4 16   11.4 12.7  18.2 22.0  21.3 27.7  30.5 40.9  46.6 66.7  136  199
-//        32   14.7 12.5  22.6 22.1  27.6 27.8  36.7 40.9  59.3 66.5  150  198
+//   INT8 16   11.5 12.5  17.2 21.8  20.9 27.1  28.7 40.6  43.2 65.5  123  189
+//        24   14.6 12.7  21.9 22.0  26.1 27.5  34.3 40.7  56.3 65.6  138  189
+//        32   14.9 12.6  22.0 22.0  27.2 27.2  35.5 40.9  58.1 65.0  139  188
+//   INT4 16   11.3 12.7  17.4 22.0  20.7 27.7  28.7 40.9  43.5 66.7  124  199
+//        32   14.9 12.5  22.5 22.1  27.5 27.8  36.6 40.9  60.8 66.5  148  198
 // (of 17 to 32 rows on a few hundred tokens the other would be 2 us faster)
 bool chunk_narrow_takes(int B, int64_t max_rows) { return B <= kMaxB && max_rows <= 32; }
 
