@@ -72,11 +72,12 @@ __device__ __forceinline__ void add_exact(float& s, float& e, float v) {
   s = t;
 }
 
-// The sum of a lane's eight squares as s + e, exact likewise.  Added to a
-// power of two M above the sum, a square is cut at M's last place: what the
-// sum grew by is exact, what was cut off as well (both fused, so the square
-// itself is never rounded), and the sums of the former stay exact.  Four
-// two-wide instructions a pair of values.
+// The sum of a lane's eight squares over 2 D as s + e, exact likewise: half of
+// what the lane adds to the mean, so that no sum across lanes passes fp32
+// unless the mean does.  Added to a power of two M above the sum, a square is
+// cut at M's last place: what the sum grew by is exact, what was cut off as
+// well (both fused, so the square itself is never rounded), and the sums of
+// the former stay exact.  Four two-wide instructions a pair of values.
 __device__ __forceinline__ int top_exponent(const uint4& raw) {   // |x| < 2^(top - 126) for the lane's values
   const __nv_bfloat162 a = __habs2(*reinterpret_cast<const __nv_bfloat162*>(&raw.x)), b = __habs2(*reinterpret_cast<const __nv_bfloat162*>(&raw.y));
   const __nv_bfloat162 c = __habs2(*reinterpret_cast<const __nv_bfloat162*>(&raw.z)), d = __habs2(*reinterpret_cast<const __nv_bfloat162*>(&raw.w));
@@ -84,6 +85,7 @@ __device__ __forceinline__ int top_exponent(const uint4& raw) {   // |x| < 2^(to
   const uint32_t m = *reinterpret_cast<const uint32_t*>(&m2);
   return static_cast<int>(max(m >> 16, m & 0xFFFFu) >> 7);
 }
+template <int D>
 __device__ __forceinline__ void square_sum(float& s, float& e, int top, float2 (&f)[4]) {
   const bool large = top > 180;       // squares that near fp32's end or pass it: summed 2^-200 times as large
   if (large) {
@@ -105,10 +107,15 @@ __device__ __forceinline__ void square_sum(float& s, float& e, int top, float2 (
   }
   s = __fadd_rn(__fsub_rn(S.x, M), __fsub_rn(S.y, M));
   e = __fadd_rn(E.x, E.y);
-  if (large) {
-    s = __fmul_rn(__fmul_rn(s, 0x1p100f), 0x1p100f);
-    e = __fmul_rn(__fmul_rn(e, 0x1p100f), 0x1p100f);
+  float up = 0.5f / D;
+  if (large) {                        // (the first 2^100 passes fp32 only where the lane's part of the mean does)
+    s = __fmul_rn(s, 0x1p100f);
+    e = __fmul_rn(e, 0x1p100f);
+    up *= 0x1p100f;
   }
+  const float2 se = __fmul2_rn(make_float2(s, e), make_float2(up, up));
+  s = se.x;
+  e = se.y;
 }
 
 // What a lane needs of its row: its position and where the cache keeps it.
@@ -162,12 +169,11 @@ __device__ __forceinline__ uint4 round8(const float2 (&f)[4]) {
   return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-// 1 / sqrt(mean + eps) of the squares that LPR lanes hold as s + e.
-template <int D>
+// 1 / sqrt(mean + eps) of half a mean s + e.
 __device__ __forceinline__ float inverse_root(float s, float e, float eps) {
-  // (a sum past fp32 is infinite; its error term is then no number)
-  const float sum = isinf(s) ? s : __fadd_rn(s, e);
-  const float mean = __fmul_rn(sum, 1.0f / D);   // exact: a power of two
+  // (a half past fp32 is infinite; its error term is then no number)
+  const float half = isinf(s) ? s : __fadd_rn(s, e);
+  const float mean = __fmul_rn(half, 2.0f);   // exact, and infinite where the mean rounds to that
   return __frcp_rn(__fsqrt_rn(__fadd_rn(mean, eps)));
 }
 
@@ -189,7 +195,7 @@ __device__ __forceinline__ void norm_factors(float (&r)[NH], const uint4 (&raw)[
   for (int j = 0; j < NH; ++j) {
     float2 f[4];
     widen8(f, raw[j]);
-    square_sum(s[j], e[j], top_exponent(raw[j]), f);
+    square_sum<D>(s[j], e[j], top_exponent(raw[j]), f);
   }
   if constexpr (NH == 4) {
     const bool up = lane & (LPR / 2), right = lane & (LPR / 4);
@@ -209,7 +215,7 @@ __device__ __forceinline__ void norm_factors(float (&r)[NH], const uint4 (&raw)[
     et = __fadd_rn(et, e2);
 #pragma unroll
     for (int o = LPR / 8; o > 0; o >>= 1) add_across(st, et, o);
-    const float mine = inverse_root<D>(st, et, eps);
+    const float mine = inverse_root(st, et, eps);
 #pragma unroll
     for (int j = 0; j < 4; ++j)
       r[j] = __shfl_sync(0xffffffffu, mine, (lane & ~(LPR - 1)) + (j >> 1) * (LPR / 2) + (j & 1) * (LPR / 4));
@@ -218,7 +224,7 @@ __device__ __forceinline__ void norm_factors(float (&r)[NH], const uint4 (&raw)[
     for (int j = 0; j < NH; ++j) {
 #pragma unroll
       for (int o = 1; o < LPR; o <<= 1) add_across(s[j], e[j], o);
-      r[j] = inverse_root<D>(s[j], e[j], eps);
+      r[j] = inverse_root(s[j], e[j], eps);
     }
   }
 }
