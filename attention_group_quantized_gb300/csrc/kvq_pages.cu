@@ -149,21 +149,27 @@ __global__ void __launch_bounds__(kPlanThreads) fork_kernel(const __grid_constan
   const int64_t cap = static_cast<int64_t>(p.t.max_pages) * KVQ_TILE_TOKENS;
   for (int s = tid; s < slots; s += kPlanThreads) p.s.mark[s] = INT32_MAX;
   __syncthreads();
-  // pairs that hold: size[i] = the length to copy, else -1 (the lengths are
+  // pairs that hold: size[i] = the length to copy, else -1, and src[i] the
+  // partly filled last page, -1 where there is none in the pool (lengths are
   // read before any is written)
   for (int i = tid; i < p.n; i += kPlanThreads) {
     const int f = p.from[i], t = p.to[i];
-    int size = -1;
+    int size = -1, last = -1;
     if (f >= 0 && f < slots && t >= 0 && t < slots && p.t.seq_lens[t] == 0) {
       const int len = p.t.seq_lens[f];
       if (len >= 0 && len <= cap) {
         size = len;
         atomicMin(&p.s.mark[t], i);
+        if (len % KVQ_TILE_TOKENS != 0) {
+          last = p.t.table[static_cast<int64_t>(f) * p.t.max_pages + len / KVQ_TILE_TOKENS];
+          if (last < 0 || last >= p.t.n_pages) last = -1;
+        }
       }
     }
     if (size < 0) report(p.status, KVQ_ERR_INVALID_ARG);
     p.s.size[i] = size;
-    p.s.src[i] = p.s.dst[i] = -1;
+    p.s.src[i] = last;
+    p.s.dst[i] = -1;
   }
   if (tid == 0) *p.s.pairs = p.n;
   __syncthreads();
@@ -172,33 +178,31 @@ __global__ void __launch_bounds__(kPlanThreads) fork_kernel(const __grid_constan
   for (int i = i0; i < i1; ++i) {
     if (p.s.size[i] >= 0 && p.s.mark[p.to[i]] != i) {   // another pair's to
       report(p.status, KVQ_ERR_INVALID_ARG);
-      p.s.size[i] = -1;
+      p.s.size[i] = p.s.src[i] = -1;
     }
-    n += p.s.size[i] > 0 && p.s.size[i] % KVQ_TILE_TOKENS != 0;
+    n += p.s.src[i] >= 0;
   }
   int at = scan_cta(n, sums, &need_all);
   const int have = list_free(p, need_all, sums);
   for (int i = i0; i < i1; ++i) {
     const int size = p.s.size[i];
     if (size < 0) continue;
-    const int f = p.from[i], t = p.to[i];
-    if (size % KVQ_TILE_TOKENS != 0) {
+    const int f = p.from[i], t = p.to[i], last = size / KVQ_TILE_TOKENS;
+    if (p.s.src[i] >= 0) {
       if (at >= have) {
         report(p.status, KVQ_ERR_NO_PAGES);
-        p.s.size[i] = -1;
+        p.s.size[i] = p.s.src[i] = -1;
         ++at;
         continue;
       }
-      const int last = size / KVQ_TILE_TOKENS, page = p.s.list[at++];
-      const int old = p.t.table[static_cast<int64_t>(f) * p.t.max_pages + last];
-      if (old >= 0 && old < p.t.n_pages) {
-        p.s.src[i] = old;
-        p.s.dst[i] = page;
-      } else {
-        report(p.status, KVQ_ERR_INVALID_ARG);
-      }
+      const int page = p.s.list[at++];
+      p.s.dst[i] = page;
       p.t.table[static_cast<int64_t>(t) * p.t.max_pages + last] = page;
       p.t.refs[page] = 1;
+    } else if (size % KVQ_TILE_TOKENS != 0) {            // outside the pool: copied as it stands
+      report(p.status, KVQ_ERR_INVALID_ARG);
+      p.t.table[static_cast<int64_t>(t) * p.t.max_pages + last] =
+          p.t.table[static_cast<int64_t>(f) * p.t.max_pages + last];
     }
     p.t.seq_lens[t] = size;
   }

@@ -851,7 +851,8 @@ KVQ_API kvq_status kvq_pages_reserve(const kvq_page_table* pages, const int32_t*
  * is served).  Lengths are those before the call.  A pair that finds no page
  * for its copy, and those after it that need one, report KVQ_ERR_NO_PAGES and
  * do nothing.  A page id outside the pool in a used entry is copied as it
- * stands and reported as KVQ_ERR_INVALID_ARG.
+ * stands and reported as KVQ_ERR_INVALID_ARG; a partly filled last page with
+ * such an id takes no page for to[i].
  * k_pool, v_pool: the pools, B = n_pages, Tcap = 64, of equal shape and bits.
  * from, to: device int32 [n]; n <= slots, n == 0 does nothing.
  */
