@@ -920,8 +920,8 @@ def _weight(w, D: int, device: int) -> int:
 def _rotation(rotary, q_weight, k_weight, eps: float, interleaved: bool, D: int, device: int) -> bytes:
     at = positions = rot = 0
     if rotary is not None:
-        if rotary.dtype is not _F32 or rotary.dim() != 2 or not rotary.is_contiguous():
-            _bad("rotary: fp32 [positions][rot_dim], contiguous")
+        if rotary.dtype is not _F32 or rotary.dim() != 2 or not rotary.is_contiguous() or not rotary.numel():
+            _bad("rotary: fp32 [positions][rot_dim], contiguous, not empty")   # (an empty tensor has no address: no table)
         if rotary.get_device() != device:
             _bad("tensors on different devices")
         at = rotary.data_ptr()
