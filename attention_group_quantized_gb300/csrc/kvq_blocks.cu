@@ -193,8 +193,8 @@ __device__ __forceinline__ void block_of(const BParams& p, int h, int sb, int n,
 //
 // A block is the work of the row that holds its first new token: a sequence's
 // first new row, or one at the start of a block.  A warp looks at R rows for
-// one head: one while the rows are few (each may own a block), 64 once they are
-// many (mostly prompts, one owner in 64).
+// one head: one while the rows are few or mostly sequences' first (each may own
+// a block), 64 once they are many (mostly prompts, one owner in 64).
 template <int D, int R>
 __global__ void __launch_bounds__(kBoundsWarps * 32, kBoundsBlocks) block_bounds_kernel(const __grid_constant__ BParams p) {
   grid_dependency_wait();
@@ -595,7 +595,14 @@ cudaError_t launch_block_bounds(const BoundsArgs& a, cudaStream_t stream) {
     p.plane_off[h] = a.layout.plane_off[h];
     p.bits[h] = a.layout.bits[h];
   }
-  const bool few = a.chunk.rows <= 4096;
+  // A row a warp costs by rows, 64 by the first new rows that lie in one run of
+  // 64.  Up to 4096 rows (8 heads, INT8, one against 64): a prompt of 512 5.0
+  // and 4.8 us, of 2048 8.3 and 5.1, of 4096 12.3 and 5.1, at worst 7 us lost;
+  // but 256 sequences of one row 7.6 and 170, of four 10.4 and 46.  Above: a
+  // prompt of 8192 20.5 and 5.8, 1000 sequences of sixteen 57 and 28, unless
+  // most rows are a sequence's first: 3000 sequences of two 58 and 148, of
+  // four 73 and 86, of sixteen 166 and 66.
+  const bool few = a.chunk.rows <= std::max<int64_t>(4096, int64_t(4) * a.chunk.B);
   p.tiles = few ? a.chunk.rows : (static_cast<int64_t>(a.chunk.rows) + 63) / 64;
   cudaLaunchAttribute attr;
   const cudaLaunchConfig_t cfg = config((p.tiles * p.Hkv + kBoundsWarps - 1) / kBoundsWarps, kBoundsWarps * 32, stream, &attr);
