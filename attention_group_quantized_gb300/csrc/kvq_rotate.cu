@@ -38,10 +38,16 @@ namespace {
 
 constexpr int kWarps = 4;
 constexpr int kBlocksPerSM = 4;   // (five or six, on fewer registers: the same)
-// Warps an SM that a call should have before a warp takes four heads, and then
-// several runs of rows (16: 9.0 us for 1,030 rows of 48 heads, 32: 14.0 us)
-constexpr int kWarpsPerSM = 16;
-constexpr int kMaxPasses = 8;     // (32K rows of 48 heads: 1 pass 270 us, 2 228, 4 209, 8 203)
+// Warps an SM that are left where a warp takes four heads (one against four of
+// them: 100 rows of 32 + 8 + 8 heads 4.6 and 4.9 us, 128 6.2 and 5.1, 400 11.6
+// and 6.1; 512 rows of 4 + 1 + 1 heads 4.3 and 4.7, 1024 6.1 and 5.5) ...
+constexpr int kWarpsPerSM = 4;
+// ... and where it takes twice as many runs of rows: one, two, four and eight of
+// them take, 48 heads, 560 rows: 9.1, 9.6, 13.3 and 20.9 us, 2048: 20.8, 19.8,
+// 21.6 and 28.0, 4096: 38.3, 34.7, 35.0 and 40.3, 8192: 76.7, 66.6, 64.1 and
+// 67.0, 32K: 270, 228, 210 and 205.
+constexpr int kPassWarpsPerSM = 32;
+constexpr int kMaxPasses = 8;
 
 struct RParams {
   chunk::View c;
@@ -385,7 +391,7 @@ __device__ __forceinline__ void unit_of(const RParams& p, int kind, int r0, int 
           if (j < count) *reinterpret_cast<uint4*>(dst + j * D) = pos >= 0 ? y[j] : make_uint4(0u, 0u, 0u, 0u);
       }
     } else {
-uint32_t v[16];
+      uint32_t v[16];
       own_group(v, y, lane);
       const int j = NH == 1 ? 0 : lane & 3, h = h0 + j;
       if (j < count && store >= 0 && (NH > 1 || (lane & 3) == 0)) {
@@ -457,7 +463,7 @@ cudaError_t launch_rotate_append(const RotateArgs& a, cudaStream_t stream) {
   const bool many = runs * fours >= want;
   const int64_t heads = many ? fours : a.Hq + 2 * k.Hkv;
   p.passes = 1;
-  while (p.passes < kMaxPasses && runs * heads >= 2 * want * p.passes) p.passes *= 2;
+  while (p.passes < kMaxPasses && runs * heads >= int64_t(2 * kPassWarpsPerSM) * device_sm_count() * p.passes) p.passes *= 2;
   p.tiles = (runs + p.passes - 1) / p.passes;
   const int64_t warps = p.tiles * heads;
   cudaLaunchConfig_t cfg = {};
