@@ -682,6 +682,7 @@ def _own_compact(state, kvq):
     keep = _kept(state, kvq)
     state["table"].copy_(state["table0"])                                    # what the last pass began with
     state["refs"].copy_(state["refs0"])
+    state["lens"].copy_(state["lens0"])
     kvq.pages_compact(keep["pages"], keep["k"], keep["v"], bounds=keep.get("bounds"), workspace=keep["ws"])
     return _pool(state)
 
