@@ -5,7 +5,8 @@
 // 《分块稀疏注意力与KV Cache量化：长文本推理显存优化实践》 §1.3, §2.3; this is a
 // judgement made at decode time, per query.)
 //
-// The score bounds the best product that any token of the block can give:
+// The score bounds the best product that any token of the block can give, but
+// for the rounding of the query to 8 bits:
 //   sum_h q_h . k <= sum_d qp_d max_d + qn_d min_d,
 //   qp = sum_h max(q_h, 0), qn = sum_h min(q_h, 0)
 // over the query heads h of a KV head, so a group of heads costs no more than

@@ -180,10 +180,11 @@ __device__ __forceinline__ bool dequant_piece(const CParams& p, uint8_t* smem, u
       }
       // The slot is free once its values have been used, not once their loads
       // are issued: the copy that refills it writes through the async proxy,
-      // which an arrival after loads in flight does not hold back (released
+      // which an arrival after loads in flight does not hold back.  (Released
       // there, about one call in a hundred of long 4-bit sequences had a wrong
       // segment, none of 8000 since; all had a last tile whose half stands for
-      // the other, a copy that comes early, from L2).  8-bit heads pay 4 % on
+      // the other, a copy that comes early, from L2.  That the early copy was
+      // the cause is inferred from this, not observed.)  8-bit heads pay 4 % on
       // long contexts, 118 -> 123 us, 4-bit ones gain 9, 136 -> 124; an arrival
       // that hangs on the loaded values before the conversion: 122 and 138 us.
       __syncwarp();

@@ -280,7 +280,7 @@ __global__ void __launch_bounds__(kPlanThreads) compact_kernel(const __grid_cons
 // words.  After a plan the pairs are in the workspace, and the same launch does
 // what else takes more than one CTA: the entries of the full pages that a fork
 // shares, a warp per pair (in the planning CTA they took most of its time: 128
-// forks of up to 125 pages with what goes with them 24.3 us, 18.9 us here), or the page table's
+// forks of up to 125 pages with what goes with them 24.3 us, 18.5 us here), or the page table's
 // entries renamed after a compaction, a warp per slot.
 struct CParams {
   const int32_t* pairs;     // number of pairs, null: n

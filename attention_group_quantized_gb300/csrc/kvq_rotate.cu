@@ -23,9 +23,10 @@
 // and works out its scale once.
 //
 // Measured: 32K rows of 32 + 8 + 8 heads, half of the channels turned, INT4, 722
-// MB, 203 us, 3.6 TB/s (its floor is 107 us at 6.78 TB/s): bound by issue slots,
-// 211 instructions a warp and head, of which the norm has about 90, the rotation
-// 45, a key's or value's quantisation 90.
+// MB, 205 us, 3.5 TB/s (its floor is 107 us at 6.78 TB/s).  Neither HBM nor issue
+// is full: 212 instructions a warp and head (the norm about 90, the rotation 45,
+// a key's or value's quantisation 90) in chains, and 14 warps an SM (of the 16
+// that 128 registers allow) that fill 60 % of its issue slots.
 #include <algorithm>
 #include <type_traits>
 

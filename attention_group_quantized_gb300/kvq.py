@@ -901,12 +901,6 @@ def decode_attention_window_paged(q, k_pool: QuantCache, v_pool: QuantCache, blo
 _pack_rotation = struct.Struct("@PPPiiif").pack   # kvq_rotation
 
 
-def _same_device(device: int, *tensors):
-    for t in tensors:
-        if t is not None and t.get_device() != device:
-            _bad("tensors on different devices")
-
-
 def _weight(w, D: int, device: int) -> int:
     if w is None:
         return 0

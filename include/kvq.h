@@ -812,6 +812,13 @@ KVQ_API kvq_status kvq_decode_attention_blocks_paged(const void* q, const kvq_ca
  * mean nothing and keep their contents); refs[p] counts the entries that are
  * page p, 0: free.  (table and seq_lens are what the block table and the chunk
  * of the other calls take.)  Pages are handed out lowest free page first.
+ * No call shortens a sequence.  A program may lower a length itself (drafted
+ * tokens that were rejected), within the last page, length > 64 * (pages - 1),
+ * and where that page's count is 1: new tokens go into it, and a page that a
+ * fork shares would change for the others too.  Lowered further, the pages past
+ * the new end are in no used entry, but their counts stay: the program has to
+ * lower those as well (refs[p] by one for each entry given up), or the pages
+ * are lost until the table is made anew.
  */
 typedef struct kvq_page_table {
   int32_t* refs;       /* device int32 [n_pages] */
