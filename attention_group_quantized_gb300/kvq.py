@@ -666,7 +666,8 @@ def _block_table(block_table):
 def _packed(x, heads: int, D: int, what: str):
     if _BF16 is None:
         _torch()
-    if x.dtype is not _BF16 or x.dim() != 3 or x.shape[1:] != (heads, D) or x.stride(2) != 1:
+    if x.dtype is not _BF16 or x.dim() != 3 or x.shape[1:] != (heads, D) or x.stride(2) != 1 and x.shape[0]:
+        # (the strides of no rows may be anything: an empty array's are 0)
         _bad(f"{what}: bf16 [rows][{heads}][{D}], channels contiguous")
 
 
@@ -927,7 +928,7 @@ def _rotation(rotary, q_weight, k_weight, eps: float, interleaved: bool, D: int,
 def _strides(x):
     """Row and head strides of packed rows, 0 where there is one row or head (torch leaves those anything)."""
     (rows, heads, _), (s_row, s_head, _) = x.shape, x.stride()
-    return (s_row if rows > 1 else 0), (s_head if heads > 1 else 0)
+    return (s_row if rows > 1 else 0), (s_head if heads > 1 and rows else 0)
 
 
 def _rotate_append(q, k_new, v_new, k: QuantCache, v: QuantCache, block_table, start, seq_lens, rotary, q_weight, k_weight,
@@ -937,8 +938,8 @@ def _rotate_append(q, k_new, v_new, k: QuantCache, v: QuantCache, block_table, s
     rows, Hq, D = q.shape
     _packed(q, Hq, k.D, "q")
     _packed(k_new, k.Hkv, D, "k_new")
-    if (k_new.shape[0] != rows or v_new.shape != k_new.shape or v_new.dtype is not _BF16 or v_new.stride(2) != 1
-            or _strides(v_new) != _strides(k_new)):
+    if (k_new.shape[0] != rows or v_new.shape != k_new.shape or v_new.dtype is not _BF16
+            or v_new.stride(2) != 1 and rows or _strides(v_new) != _strides(k_new)):
         _bad("q, k_new and v_new: the same rows; k_new and v_new: the same strides")
     bt = _block_table(block_table)
     dev = _on_current_device(q, k_new, v_new, k.codes, k.sz, v.codes, v.sz, start, seq_lens)
